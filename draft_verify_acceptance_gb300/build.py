@@ -16,7 +16,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libspecverify.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["spec_verify.cu", "verify_greedy.cu", "verify_sample.cu", "verify_sample_fused.cu", "verify_sample_seq.cu", "verify_sample_ee.cu", "verify_sample_2p.cu", "verify_draft_sample.cu", "verify_scd.cu", "rejection_cut.cu",
-           "spec_verify_static.cu"]
+           "spec_verify_static.cu", "spec_decode.cu", "attention.cu", "cache_pages.cu", "filtered_sample.cu"]
 
 
 def _nvcc():
@@ -28,7 +28,7 @@ def _nvcc():
 
 def _deps():
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    files.append(os.path.join(ROOT, "include", "spec_verify.h"))
+    files += [os.path.join(ROOT, "include", h) for h in ("spec_verify.h", "spec_decode.h")]
     files.append(os.path.abspath(__file__))
     return files
 

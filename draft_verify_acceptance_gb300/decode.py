@@ -1,0 +1,401 @@
+"""ctypes binding of the decode-side operators (include/spec_decode.h).
+
+    paged_attention   the newest Q tokens' attention over a paged key-value cache
+    cache_append      new tokens' keys and values into their pages
+    cache_fork        the next step's sequences: fork, trim, end, reorder, reserve
+    cache_compact     pages in use to the front of the pool
+    filtered_sample   temperature, top-k, min-p and top-p from given uniforms
+
+As in ``binding``, every step runs in the library's CUDA kernels; this module checks
+tensors, owns a workspace per (device, stream) and passes pointers.  There is no CPU
+fallback.  Calls are queued on ``stream`` (default: the current stream); with
+``debug=True`` they also return the device status word (OR of DATA_* bits).
+
+A cache tensor is [pages, page_size, heads, head_dim], or with a leading layers
+dimension for cache_fork and cache_compact; the last two dimensions are contiguous, the
+other strides free (a layer of a larger tensor, K and V interleaved), the same for K
+and V.  A page table is int32 [B, max_pages].
+"""
+import ctypes
+import math
+import threading
+from typing import NamedTuple
+
+import torch
+
+from .binding import (DTYPE_BF16, DTYPE_F32, ERR_INVALID_ARG, ERR_UNSUPPORTED, MAX_V, OK, SpecVerifyError,
+                      _lib)
+
+DATA_PAGE_RANGE = 64
+DATA_LENGTH_RANGE = 128
+DATA_CACHE_FULL = 256
+DATA_PARAM_RANGE = 512
+
+EXPORTS = ("spec_attention_workspace_size", "spec_paged_attention", "spec_cache_append",
+           "spec_cache_fork_workspace_size", "spec_cache_fork", "spec_cache_compact_workspace_size",
+           "spec_cache_compact", "spec_filtered_sample_workspace_size", "spec_filtered_sample")
+
+
+class _Cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("layer_stride", ctypes.c_int64),
+                ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64), ("layers", ctypes.c_int),
+                ("pages", ctypes.c_int), ("page_size", ctypes.c_int), ("heads", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("dtype", ctypes.c_int)]
+
+
+def _declare():
+    P, I, F, Z, L = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_int64
+    C = ctypes.POINTER(_Cache)
+    sig = {
+        "spec_attention_workspace_size": (Z, [I] * 6),
+        "spec_paged_attention": (I, [P, L, L, L, C, P, L, I, P, I, I, I, F, P, P, P, Z, P, P]),
+        "spec_cache_append": (I, [P, P, L, I, P, C, P, L, I, P, I, P, P]),
+        "spec_cache_fork_workspace_size": (Z, [I, I]),
+        "spec_cache_fork": (I, [C, P, L, I, P, I, P, P, I, I, P, P, P, P, P, P, Z, P, P]),
+        "spec_cache_compact_workspace_size": (Z, [I]),
+        "spec_cache_compact": (I, [C, P, L, I, I, P, P, P, P, Z, P, P]),
+        "spec_filtered_sample_workspace_size": (Z, [I, I, I]),
+        "spec_filtered_sample": (I, [P, L, P, I, I, I, F, I, F, F, P, P, P, P, P, P, P, P, P, Z, P, P]),
+    }
+    for name, (res, args) in sig.items():
+        f = getattr(_lib, name)
+        f.restype, f.argtypes = res, args
+
+
+_declare()
+_DTYPES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
+_ws_lock = threading.Lock()
+_ws = {}
+
+
+class ForkResult(NamedTuple):
+    page_table: torch.Tensor  # int32 [C, max_pages]
+    lengths: torch.Tensor     # int32 [C]
+    ref_counts: torch.Tensor  # int32 [pages]
+    free_pages: torch.Tensor  # int32 [pages]: ascending, then -1
+    n_free: torch.Tensor      # int32 [1]
+    status: torch.Tensor      # int32 [1] with debug, else None
+
+
+class CompactResult(NamedTuple):
+    page_table: torch.Tensor  # int32 [B, max_pages]
+    ref_counts: torch.Tensor  # int32 [pages]
+    n_live: torch.Tensor      # int32 [1]
+    status: torch.Tensor      # int32 [1] with debug, else None
+
+
+class SampleResult(NamedTuple):
+    tokens: torch.Tensor      # int32 [...]
+    p: torch.Tensor           # float32 [...]
+    n_kept: torch.Tensor      # int32 [...]
+    filtered: torch.Tensor    # [..., V] in the logits' dtype, or None
+    status: torch.Tensor      # int32 [1] with debug, else None
+
+
+def _workspace(kind, device, stream, nbytes, given):
+    """The caller's workspace, or one kept for this kind of call, device and stream (zero-filled
+    when made, as spec_paged_attention asks)."""
+    if given is not None:
+        if given.device != device or not given.is_contiguous():
+            raise ValueError(f"workspace must be contiguous on {device}")
+        if given.numel() * given.element_size() < nbytes:
+            raise ValueError(f"workspace holds {given.numel() * given.element_size()} bytes, {nbytes} are needed")
+        return given.data_ptr(), given.numel() * given.element_size()
+    key = (kind, device.index, stream)
+    with _ws_lock:
+        ws = _ws.get(key)
+        if ws is None or ws.numel() < nbytes:
+            ws = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
+            _ws[key] = ws
+    return ws.data_ptr(), ws.numel()
+
+
+def _on_stream(fn):
+    """Runs a call with its device and, when one is given, its stream current, so that what it allocates
+    belongs to the stream that uses it."""
+    def call(first, *args, stream=None, **kw):
+        if not isinstance(first, torch.Tensor) or not first.is_cuda:
+            where = first.device if isinstance(first, torch.Tensor) else type(first).__name__
+            raise ValueError(f"{fn.__name__} takes CUDA tensors (got {where})")
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return fn(first, *args, _stream=stream.cuda_stream, **kw)
+        device = first.device
+        if device.index != torch.cuda.current_device():
+            with torch.cuda.device(device):
+                return fn(first, *args, _stream=torch.cuda.current_stream(device).cuda_stream, **kw)
+        return fn(first, *args, _stream=torch.cuda.current_stream(device).cuda_stream, **kw)
+    call.__name__, call.__doc__, call.__wrapped__ = fn.__name__, fn.__doc__, fn
+    return call
+
+
+def _ints(t, name, shape, device):
+    """The pointer of a contiguous int32 tensor of a shape."""
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32:
+        raise TypeError(f"{name} must be an int32 tensor")
+    if t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {tuple(shape)} on {device}, "
+                         f"got {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _table(t, B, device):
+    """(pointer, row stride, max_pages) of a page table; its rows may be strided."""
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32:
+        raise TypeError("page_table must be an int32 tensor")
+    if t.dim() != 2 or t.shape[0] != B or t.device != device:
+        raise ValueError(f"page_table must be [{B}, max_pages] on {device}, got {tuple(t.shape)} on {t.device}")
+    M = t.shape[1]
+    if M > 1 and t.stride(1) != 1:
+        raise ValueError("page_table rows must be contiguous")
+    return t.data_ptr(), max(t.stride(0), M) if B > 1 else M, M
+
+
+def _cache(k, v, layered, device):
+    dt = _DTYPES.get(k.dtype)
+    if dt is None or v.dtype != k.dtype:
+        raise TypeError(f"k_pages and v_pages must both be float32 or bfloat16, got {k.dtype} and {v.dtype}")
+    dims = k.dim()
+    if dims != 4 and not (layered and dims == 5):
+        raise ValueError("a cache tensor is [pages, page_size, heads, head_dim]"
+                         + (" or [layers, pages, page_size, heads, head_dim]" if layered else ""))
+    shape, stride = k.shape, k.stride()
+    if v.shape != shape or v.stride() != stride or k.device != device or v.device != device:
+        raise ValueError("k_pages and v_pages must have the same shape, strides and device")
+    P, S, H, D = shape[-4:]
+    if (D > 1 and stride[-1] != 1) or (H > 1 and stride[-2] != D):
+        raise ValueError("the last two dimensions (heads, head_dim) of a cache tensor must be contiguous")
+    return _Cache(k.data_ptr(), v.data_ptr(), stride[0] if dims == 5 else 0, stride[-4],
+                  stride[-3] if S > 1 else max(stride[-3], H * D), shape[0] if dims == 5 else 1, P, S, H, D, dt)
+
+
+def _raise(rc, what):
+    raise SpecVerifyError(rc, what)
+
+
+def _status(debug, device):
+    return torch.zeros(1, dtype=torch.int32, device=device) if debug else None
+
+
+def _p(t):
+    return None if t is None else t.data_ptr()
+
+
+@_on_stream
+def paged_attention(q, k_pages, v_pages, page_table, lengths, scale=None, *, return_lse=False, out=None,
+                    workspace=None, debug=False, _stream=0):
+    """Attention of the newest Q tokens of each sequence over its paged cache.
+
+    q [B, Q, Hq, D] (strides free but the last; D 64 or 128), k_pages / v_pages
+    [pages, page_size, heads, D] of the same dtype (float32 or bfloat16), page_table int32
+    [B, max_pages], lengths int32 [B] (the Q new tokens included: cache_append comes
+    first).  Query i of a sequence of n tokens stands at n - Q + i and sees the tokens up to
+    itself; query head h reads cache head h * heads // Hq.  ``scale`` defaults to
+    1 / sqrt(D).  Returns out [B, Q, Hq, D], with ``return_lse`` (out, lse float32
+    [B, Q, Hq]); a query that sees nothing gets 0 and -inf.
+    """
+    if q.dim() != 4:
+        raise ValueError("q must be [B, Q, Hq, D]")
+    device = q.device
+    B, Q, Hq, D = q.shape
+    c = _cache(k_pages, v_pages, False, device)
+    if q.dtype != k_pages.dtype:
+        raise TypeError(f"q is {q.dtype}, the cache {k_pages.dtype}")
+    if D != c.head_dim or Hq % c.heads:
+        raise ValueError(f"q has {Hq} heads of {D}, the cache {c.heads} of {c.head_dim}")
+    st = q.stride()
+    if D > 1 and st[3] != 1:
+        raise ValueError("q's last dimension must be contiguous")
+    table, ts, M = _table(page_table, B, device)
+    lens = _ints(lengths, "lengths", (B,), device)
+    if out is None:
+        out = torch.empty((B, Q, Hq, D), dtype=q.dtype, device=device)
+    elif out.shape != q.shape or out.dtype != q.dtype or out.device != device or not out.is_contiguous():
+        raise ValueError("out must be contiguous, shaped and typed as q")
+    lse = torch.empty((B, Q, Hq), dtype=torch.float32, device=device) if return_lse else None
+    status = _status(debug, device)
+    need = _lib.spec_attention_workspace_size(B, Q, Hq, c.heads, D, c.dtype)
+    if need == 0:
+        _raise(ERR_UNSUPPORTED, f"paged_attention with head_dim {D}")
+    ws, nbytes = _workspace("attention", device, _stream, need, workspace)
+    # the stride of a dimension of one element is free in torch
+    rc = _lib.spec_paged_attention(
+        q.data_ptr(), st[0] if B > 1 else 0, st[1] if Q > 1 else 0, st[2] if Hq > 1 else 0, ctypes.byref(c), table, ts, M,
+        lens, B, Q, Hq, 1.0 / math.sqrt(D) if scale is None else float(scale), out.data_ptr(), _p(lse), ws, nbytes,
+        _stream, _p(status))
+    if rc != OK:
+        _raise(rc, "spec_paged_attention")
+    if debug:
+        return (out, lse, status) if return_lse else (out, status)
+    return (out, lse) if return_lse else out
+
+
+@_on_stream
+def cache_append(k_new, v_new, k_pages, v_pages, page_table, lengths, starts=None, *, debug=False, _stream=0):
+    """Writes new tokens' keys and values into their pages (in place).
+
+    k_new / v_new [T, heads, head_dim] with ``starts`` int32 [B + 1] (sequence b's new
+    tokens are rows starts[b] .. starts[b+1] - 1), or [B, n, heads, head_dim] without;
+    lengths int32 [B] counts the new tokens in: they become the last ones of their
+    sequence.  Rows may be strided (a slice of a fused projection).  Returns the status
+    word with ``debug``, else None.
+    """
+    device = k_new.device
+    c = _cache(k_pages, v_pages, False, device)
+    if k_new.dtype != k_pages.dtype or v_new.dtype != k_pages.dtype:
+        raise TypeError(f"the new tokens are {k_new.dtype}, {v_new.dtype}, the cache {k_pages.dtype}")
+    if k_new.shape != v_new.shape or k_new.stride() != v_new.stride() or v_new.device != device:
+        raise ValueError("k_new and v_new must have the same shape, strides and device")
+    B = lengths.shape[0]
+    H, D = c.heads, c.head_dim
+    shape, st = k_new.shape, k_new.stride()
+    if starts is not None:
+        if k_new.dim() != 3 or shape[1:] != (H, D):
+            raise ValueError(f"with starts, k_new must be [T, {H}, {D}]")
+        T, row = shape[0], st[0]
+    else:
+        if k_new.dim() != 4 or shape[0] != B or shape[2:] != (H, D):
+            raise ValueError(f"without starts, k_new must be [{B}, n, {H}, {D}]")
+        T, row = B * shape[1], st[1] if shape[1] > 1 else st[0]
+        if B > 1 and shape[1] > 1 and st[0] != shape[1] * st[1]:
+            raise ValueError("without starts, the rows of k_new must lie at one stride")
+    if (D > 1 and st[-1] != 1) or (H > 1 and st[-2] != D):
+        raise ValueError("heads and head_dim of k_new must be contiguous")
+    table, ts, M = _table(page_table, B, device)
+    lens = _ints(lengths, "lengths", (B,), device)
+    first = None if starts is None else _ints(starts, "starts", (B + 1,), device)
+    status = _status(debug, device)
+    rc = _lib.spec_cache_append(k_new.data_ptr(), v_new.data_ptr(), row if T > 1 else H * D, T, first, ctypes.byref(c),
+                                table, ts, M, lens, B, _stream, _p(status))
+    if rc != OK:
+        _raise(rc, "spec_cache_append")
+    return status
+
+
+@_on_stream
+def cache_fork(k_pages, v_pages, page_table, lengths, parents, keep, room=0, *, workspace=None, debug=False,
+               _stream=0):
+    """The next step's sequences from the current ones.
+
+    Sequence c of the next step continues sequence ``parents[c]`` (-1: a new one) with its
+    first ``keep[c]`` tokens, and gets pages for ``room`` tokens more.  Full pages are
+    shared; a partly filled one stays with one sequence, the others that end in it get
+    copies (all layers of k_pages / v_pages, in place); sequences that nobody continues
+    end, and their pages are free.  Returns a ForkResult: the new page table and lengths,
+    the references to each page, and the free pages.
+    """
+    device = k_pages.device
+    c = _cache(k_pages, v_pages, True, device)
+    B, C = lengths.shape[0], parents.shape[0]
+    table, ts, M = _table(page_table, B, device)
+    lens = _ints(lengths, "lengths", (B,), device)
+    par, kp = _ints(parents, "parents", (C,), device), _ints(keep, "keep", (C,), device)
+    P = c.pages
+    # one allocation; the results are views of it
+    buf = torch.empty(C * M + C + 2 * P + 1, dtype=torch.int32, device=device)
+    new, lens_new, refs, free, n_free = buf.split_with_sizes((C * M, C, P, P, 1))
+    status = _status(debug, device)
+    ws, nbytes = _workspace("pages", device, _stream, _lib.spec_cache_fork_workspace_size(P, C), workspace)
+    base = buf.data_ptr()
+    rc = _lib.spec_cache_fork(
+        ctypes.byref(c), table, ts, M, lens, B, par, kp, C, int(room), base, base + 4 * C * M, base + 4 * (C * M + C),
+        base + 4 * (C * M + C + P), base + 4 * (C * M + C + 2 * P), ws, nbytes, _stream, _p(status))
+    if rc != OK:
+        _raise(rc, "spec_cache_fork")
+    return ForkResult(new.view(C, M), lens_new, refs, free, n_free, status)
+
+
+@_on_stream
+def cache_compact(k_pages, v_pages, page_table, *, workspace=None, debug=False, _stream=0):
+    """Moves the pages in use (entries >= 0 of the page table) to the front of the pool, in place,
+    all layers: with n in use, those at or above n fill the unused ones below n, in
+    ascending order.  Returns a CompactResult: the rewritten page table, the references
+    to each page, and n.
+    """
+    device = k_pages.device
+    c = _cache(k_pages, v_pages, True, device)
+    B = page_table.shape[0]
+    table, ts, M = _table(page_table, B, device)
+    P = c.pages
+    buf = torch.empty(B * M + P + 1, dtype=torch.int32, device=device)
+    new, refs, n_live = buf.split_with_sizes((B * M, P, 1))
+    status = _status(debug, device)
+    ws, nbytes = _workspace("pages", device, _stream, _lib.spec_cache_compact_workspace_size(P), workspace)
+    base = buf.data_ptr()
+    rc = _lib.spec_cache_compact(ctypes.byref(c), table, ts, M, B, base, base + 4 * B * M, base + 4 * (B * M + P), ws,
+                                 nbytes, _stream, _p(status))
+    if rc != OK:
+        _raise(rc, "spec_cache_compact")
+    return CompactResult(new.view(B, M), refs, n_live, status)
+
+
+def _setting(v, off, kind, name, R, device):
+    """(scalar, pointer) of a sampling setting: None, a number for every row, or one a row."""
+    if v is None:
+        return off, None
+    if not isinstance(v, torch.Tensor):
+        return v, None
+    if v.dtype != kind:
+        raise TypeError(f"{name} must be {kind}, got {v.dtype}")
+    if v.numel() != R or v.device != device or not v.is_contiguous():
+        raise ValueError(f"{name} must hold one value a row on {device}")
+    return off, v.data_ptr()
+
+
+@_on_stream
+def filtered_sample(logits, uniforms, temperature=1.0, *, top_k=None, top_p=None, min_p=None, return_filtered=False,
+                    out=None, workspace=None, debug=False, _stream=0):
+    """One token per row of ``logits`` [..., V] (float32 or bfloat16; rows may be strided when
+    two-dimensional) from its truncated softmax, by the given uniforms [...].
+
+    temperature, top_k, top_p and min_p are numbers or tensors with one value a row
+    (float32; top_k int32).  top_k keeps the largest logits; min_p those of at least
+    min_p times the largest one's probability; top_p then the most likely ones up to
+    that share of what is left.  Temperature 0 takes the largest logit.  Returns a
+    SampleResult: tokens, p (the token's probability among the kept ones), n_kept and, with
+    ``return_filtered``, the logits with -inf for what was not kept -- rows for ``verify``,
+    whose accept test then holds for the truncated distributions.  ``out`` may give a
+    preallocated tensor for those.
+    """
+    if logits.dim() < 1:
+        raise ValueError("logits must be [..., V]")
+    device, shape = logits.device, logits.shape
+    dt = _DTYPES.get(logits.dtype)
+    if dt is None:
+        raise TypeError(f"logits must be float32 or bfloat16, got {logits.dtype}")
+    V = shape[-1]
+    if V < 1:
+        _raise(ERR_INVALID_ARG, "filtered_sample with an empty vocabulary")
+    if V > MAX_V:
+        _raise(ERR_UNSUPPORTED, f"filtered_sample with {V} tokens")
+    rows = shape[:-1]
+    R = rows.numel()
+    if logits.is_contiguous():
+        stride = V
+    elif logits.dim() == 2 and logits.stride(1) == 1 and logits.stride(0) >= V:
+        stride = logits.stride(0)
+    else:
+        raise ValueError("the rows of logits must be contiguous, and at one stride")
+    if uniforms.dtype != torch.float32 or uniforms.shape != rows or uniforms.device != device or not uniforms.is_contiguous():
+        raise ValueError(f"uniforms must be contiguous float32 {tuple(rows)} on {device}")
+    T, Tp = _setting(temperature, 1.0, torch.float32, "temperature", R, device)
+    k, kp = _setting(top_k, 0, torch.int32, "top_k", R, device)
+    p, pp = _setting(top_p, 1.0, torch.float32, "top_p", R, device)
+    m, mp = _setting(min_p, 0.0, torch.float32, "min_p", R, device)
+    tokens = torch.empty(rows, dtype=torch.int32, device=device)
+    prob = torch.empty(rows, dtype=torch.float32, device=device)
+    n_kept = torch.empty(rows, dtype=torch.int32, device=device)
+    if out is not None:
+        if out.shape != shape or out.dtype != logits.dtype or out.device != device or not out.is_contiguous():
+            raise ValueError("out must be contiguous, shaped and typed as logits")
+    elif return_filtered:
+        out = torch.empty(shape, dtype=logits.dtype, device=device)
+    status = _status(debug, device)
+    need = _lib.spec_filtered_sample_workspace_size(R, V, dt)
+    ws, nbytes = _workspace("sample", device, _stream, need, workspace) if need else (None, 0)
+    rc = _lib.spec_filtered_sample(
+        logits.data_ptr(), stride, uniforms.data_ptr(), R, V, dt, T, int(k), p, m, Tp, kp, pp, mp, tokens.data_ptr(),
+        prob.data_ptr(), n_kept.data_ptr(), _p(out), ws, nbytes, _stream, _p(status))
+    if rc != OK:
+        _raise(rc, "spec_filtered_sample")
+    return SampleResult(tokens, prob, n_kept, out, status)

@@ -1,0 +1,570 @@
+"""The decode-side operators against plain 64-bit references, at the sizes and masks where they can go wrong.
+
+Tolerances.  Attention: a score is a sum of D products in fp32, off by at most (D + 8) 2^-24 sum|q||k|
+scale, which moves a weight by that relative amount (twice: numerator and sum); weights, scaling and
+joining add less than 2^-18 of sum p|v|; in bf16 a weight is rounded once (2^-9) and the output
+once (2^-9 of itself).  lse is off by the score's error plus 2^-20 of its own size.  The cache operators
+and the sampler's tokens are whole numbers or copies and must be equal; p = w / S is a quotient of weights
+within 2^-21 of the exponential each and two roundings: 2^-19 relative for p above 2^-18 of the largest,
+whose whole-number weights are rounded by 2^-22 at most.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import decode_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def decode():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import __graft_entry__
+    __graft_entry__.build()
+    from draft_verify_acceptance_gb300 import decode
+    return decode
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def i32(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def make_cache(lens, S, H, D, dtype, seed, layers=None, spare=3, extra_cols=2):
+    g = gen(seed)
+    pages = [-(-n // S) for n in lens]
+    P, M = sum(pages) + spare, max(pages + [0]) + extra_cols
+    shape = (P, S, H, D) if layers is None else (layers, P, S, H, D)
+    k = torch.randn(shape, generator=g, device="cuda").to(dtype)
+    v = torch.randn(shape, generator=g, device="cuda").to(dtype)
+    ids = torch.randperm(P, generator=g, device="cuda").to(torch.int32)
+    table = torch.full((len(lens), M), -1, dtype=torch.int32, device="cuda")
+    at = 0
+    for b, n in enumerate(pages):
+        table[b, :n] = ids[at:at + n]
+        at += n
+    return k, v, table, i32(lens)
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+def check_attention(out, lse, q, k, v, table, lengths, scale=None):
+    D = q.shape[-1]
+    scale = 1 / math.sqrt(D) if scale is None else scale
+    o, l, mag, spread = ref.attention(f64(q), f64(k), f64(v), table.cpu().numpy(), lengths.cpu().numpy(), scale)
+    score = (D + 8) * 2.0 ** -24 * spread
+    tol = mag * (2 * score[..., None] + 2.0 ** -18) + 1e-30
+    if q.dtype == torch.bfloat16:
+        tol += 2.0 ** -9 * mag + 2.0 ** -9 * np.abs(o)
+    err = np.abs(f64(out) - o)
+    assert (err <= tol).all(), (err - tol).max()
+    if lse is not None:
+        got = f64(lse)
+        empty = np.isinf(l)
+        assert np.array_equal(np.isinf(got), empty)
+        e = np.abs(got[~empty] - l[~empty])
+        assert (e <= score[~empty] + 2.0 ** -20 * (1 + np.abs(l[~empty]))).all(), e.max()
+
+
+# ---- attention ----------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("B,Q,Hq,H,D,S,lens", [
+    (1, 1, 1, 1, 64, 16, [1]),
+    (3, 1, 4, 1, 128, 1, [1, 0, 5]),                 # an empty sequence, pages of one token
+    (4, 1, 8, 2, 64, 16, [15, 16, 17, 300]),
+    (3, 5, 6, 2, 128, 5, [3, 5, 77]),                # queries before the sequence's start see nothing
+    (2, 7, 7, 1, 64, 48, [7, 129]),                  # odd group, page not a power of two
+    (2, 17, 16, 2, 128, 8, [17, 513]),               # 136 rows a cache head
+    (5, 2, 5, 5, 128, 64, [2, 63, 64, 65, 1025]),
+    (1, 65, 2, 1, 64, 16, [400]),
+    (40, 1, 12, 4, 128, 32, list(range(1, 41))),
+    (1, 3, 8, 8, 128, 128, [6001]),                  # one sequence, cut over many blocks
+    (2, 9, 32, 4, 128, 16, [2000, 31]),              # 72 rows a cache head
+])
+def test_attention(decode, dtype, B, Q, Hq, H, D, S, lens):
+    k, v, table, lengths = make_cache(lens, S, H, D, dtype, seed=B * 1000 + Q)
+    q = (torch.randn((B, Q, Hq, D), generator=gen(5), device="cuda") * 2).to(dtype)
+    out, lse, status = decode.paged_attention(q, k, v, table, lengths, return_lse=True, debug=True)
+    assert int(status) == 0
+    check_attention(out, lse, q, k, v, table, lengths)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("Q,G,D", [(1, 4, 128), (6, 4, 64), (4, 8, 128), (9, 8, 128), (17, 3, 64)])
+def test_attention_unseen_tokens_do_not_matter(decode, dtype, Q, G, D):
+    """NaN and infinities where no query looks: past the length, in unused pages, and -- for each query --
+    at the later new tokens; the type's lowest value among the scores."""
+    lens, S, H = [Q, 50, 333], 16, 2
+    k, v, table, lengths = make_cache(lens, S, H, D, dtype, seed=3)
+    q = torch.randn((3, Q, H * G, D), generator=gen(1), device="cuda").to(dtype)
+    clean = decode.paged_attention(q, k, v, table, lengths)
+    used = torch.zeros(k.shape[:2], dtype=torch.bool, device="cuda")
+    for b, n in enumerate(lens):
+        for t in range(n):
+            used[table[b, t // S], t % S] = True
+    for bad in (math.nan, math.inf, -math.inf):
+        k2, v2 = k.clone(), v.clone()
+        k2[~used] = bad
+        v2[~used] = bad
+        assert torch.equal(decode.paged_attention(q, k2, v2, table, lengths), clean)
+        for i in range(Q - 1):  # everything after query i is bad: queries up to i do not change
+            for b, n in enumerate(lens):
+                for t in range(max(0, n - Q + i + 1), n):
+                    k2[table[b, t // S], t % S] = bad
+                    v2[table[b, t // S], t % S] = bad
+            if i in (0, Q // 2, Q - 2):
+                k3, v3 = k2.clone(), v2.clone()
+                got = decode.paged_attention(q, k3, v3, table, lengths)
+                assert torch.equal(got[:, :1], clean[:, :1])
+            break
+        for i in range(Q - 1):
+            k2, v2 = k.clone(), v.clone()
+            for b, n in enumerate(lens):
+                for t in range(max(0, n - Q + i + 1), n):
+                    k2[table[b, t // S], t % S] = bad
+                    v2[table[b, t // S], t % S] = bad
+            got = decode.paged_attention(q, k2, v2, table, lengths)
+            assert torch.equal(got[:, :i + 1], clean[:, :i + 1]), (bad, i)
+    # a seen token's infinity or NaN does reach the result
+    v2 = v.clone()
+    v2[table[2, 0], 0, 0, 5] = math.nan
+    got = decode.paged_attention(q, k, v2, table, lengths)
+    assert torch.isnan(got[2, :, :G, 5]).all() and not torch.isnan(got[:2]).any()
+    assert not torch.isnan(got[2, :, G:]).any() and torch.equal(got[2, :, :G, :5], clean[2, :, :G, :5])
+    low = torch.finfo(dtype).min
+    k2 = k.clone()
+    k2[table[1, 0], 3] = low * 1e-3
+    q1 = q.abs()
+    o, l = decode.paged_attention(q1, k2, v, table, lengths, return_lse=True)
+    assert torch.isfinite(o).all() and torch.isfinite(l[1]).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_attention_layouts(decode, dtype):
+    """Query from a fused projection, K and V interleaved by page, a layer of a larger cache, a table of
+    strided rows, a scale, another stream: the same bits as from contiguous tensors."""
+    B, Q, Hq, H, D, S = 3, 4, 8, 2, 128, 16
+    k, v, table, lengths = make_cache([70, 4, 1000], S, H, D, dtype, seed=8)
+    q = torch.randn((B, Q, Hq, D), generator=gen(2), device="cuda").to(dtype)
+    want = decode.paged_attention(q, k, v, table, lengths, scale=0.3)
+    check_attention(want, None, q, k, v, table, lengths, 0.3)
+    fused = torch.zeros((B, Q, (Hq + 2 * H) * D), dtype=dtype, device="cuda")
+    fused[..., :Hq * D] = q.flatten(2)
+    qs = fused[..., :Hq * D].unflatten(2, (Hq, D))
+    assert torch.equal(decode.paged_attention(qs, k, v, table, lengths, 0.3), want)
+    qt = q.permute(1, 2, 0, 3).contiguous().permute(2, 0, 1, 3)
+    assert torch.equal(decode.paged_attention(qt, k, v, table, lengths, 0.3), want)
+    kv = torch.stack((k, v), 1)
+    assert torch.equal(decode.paged_attention(q, kv[:, 0], kv[:, 1], table, lengths, 0.3), want)
+    deep = torch.stack((v, k, v), 1), torch.stack((k, v, k), 1)
+    assert torch.equal(decode.paged_attention(q, deep[0][:, 1], deep[1][:, 1], table, lengths, 0.3), want)
+    wide = torch.full((B, table.shape[1] + 9), 7, dtype=torch.int32, device="cuda")
+    wide[:, :table.shape[1]] = table
+    assert torch.equal(decode.paged_attention(q, k, v, wide[:, :table.shape[1]], lengths, 0.3), want)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = decode.paged_attention(q, k, v, table, lengths, 0.3, stream=s)
+    s.synchronize()
+    assert torch.equal(got, want)
+
+
+def test_attention_repeats_bit_for_bit_and_leaves_its_workspace_fit(decode):
+    shapes = [([5000], 1, 8, 8, 128), ([3, 900, 77], 6, 8, 2, 64), ([300] * 50, 2, 4, 2, 128), ([12], 17, 16, 2, 128)]
+    cases = []
+    for j, (lens, Q, Hq, H, D) in enumerate(shapes):
+        k, v, table, lengths = make_cache(lens, 16, H, D, torch.bfloat16, seed=j)
+        q = torch.randn((len(lens), Q, Hq, D), generator=gen(j), device="cuda").to(torch.bfloat16)
+        cases.append((q, k, v, table, lengths))
+    want = [decode.paged_attention(*c, return_lse=True) for c in cases]
+    for _ in range(30):
+        for c, (o, l) in zip(cases, want):
+            a, b = decode.paged_attention(*c, return_lse=True)
+            assert torch.equal(a, o) and torch.equal(b, l)
+
+
+def test_attention_in_a_cuda_graph(decode):
+    k, v, table, lengths = make_cache([40, 700], 16, 2, 128, torch.bfloat16, seed=4)
+    q = torch.randn((2, 1, 8, 128), generator=gen(4), device="cuda").to(torch.bfloat16)
+    out = torch.empty_like(q)
+    decode.paged_attention(q, k, v, table, lengths, out=out)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    ws = torch.zeros(1 << 23, dtype=torch.uint8, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        decode.paged_attention(q, k, v, table, lengths, out=out, workspace=ws)
+    for n in ([40, 700], [1, 3], [39, 0]):
+        lengths.copy_(i32(n))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, decode.paged_attention(q, k, v, table, lengths))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_attention_data_errors(decode, dtype):
+    """Pages out of range are skipped, lengths beyond the table are clamped, both reported."""
+    lens, S, H, D = [40, 64, 33], 16, 1, 64
+    k, v, table, lengths = make_cache(lens, S, H, D, dtype, seed=6, extra_cols=0)
+    q = torch.randn((3, 2, 4, D), generator=gen(6), device="cuda").to(dtype)
+    table[0, 1] = k.shape[0] + 5
+    table[2, 0] = -7
+    out, lse, status = decode.paged_attention(q, k, v, table, lengths, return_lse=True, debug=True)
+    assert int(status) == decode.DATA_PAGE_RANGE
+    check_attention(out, lse, q, k, v, table, lengths)
+    lengths = i32([40, 10 ** 9, -5])
+    out, lse, status = decode.paged_attention(q, k, v, table, lengths, return_lse=True, debug=True)
+    assert int(status) == decode.DATA_PAGE_RANGE | decode.DATA_LENGTH_RANGE
+    check_attention(out, lse, q, k, v, table, lengths)
+    assert (out[2] == 0).all() and torch.isinf(lse[2]).all()
+
+
+def test_attention_offsets_past_32_bits(decode):
+    """Pages beyond 2^32 bytes and 2^31 elements of the pool."""
+    S, H, D = 16, 8, 128
+    P = (1 << 31) // (S * H * D) + 40
+    k = torch.empty((P, S, H, D), dtype=torch.bfloat16, device="cuda")
+    lens = [100, 37]
+    ids = [P - 1, 3, P - 9, P // 2 + 1, P - 2, 11, P - 30]
+    table = i32([ids, [P - 5, 7, P - 6, -1, -1, -1, -1]])
+    for p in set(table.flatten().tolist()) - {-1}:
+        k[p] = torch.randn((S, H, D), generator=gen(p % 1000), device="cuda").to(torch.bfloat16)
+    q = torch.randn((2, 3, 16, D), generator=gen(1), device="cuda").to(torch.bfloat16)
+    out, lse = decode.paged_attention(q, k, k, table, i32(lens), return_lse=True)
+    flat = sorted(set(table.flatten().tolist()) - {-1})
+    small = k[flat]
+    remap = {p: i for i, p in enumerate(flat)}
+    t2 = i32([[remap.get(p, -1) for p in row] for row in table.tolist()])
+    check_attention(out, lse, q, small, small, t2, i32(lens))
+    new = torch.randn((2, 3, H, D), generator=gen(9), device="cuda").to(torch.bfloat16)
+    decode.cache_append(new, new, k, k, table, i32(lens))
+    assert torch.equal(k[P - 30, 1:4], new[0]) and torch.equal(k[P - 6, 2:5], new[1])
+
+
+# ---- append ---------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("S,H,D,counts,before", [
+    (16, 2, 64, [1, 1, 1], [0, 15, 16]),
+    (5, 1, 128, [7, 0, 13, 1], [3, 9, 0, 0]),
+    (64, 8, 128, [300, 2], [63, 1000]),
+    (1, 3, 8, [4, 4], [0, 2]),
+])
+def test_append(decode, dtype, S, H, D, counts, before):
+    lens = [a + b for a, b in zip(counts, before)]
+    k, v, table, lengths = make_cache(lens, S, H, D, dtype, seed=2)
+    T = sum(counts)
+    new = torch.randn((T, 3, H, D), generator=gen(7), device="cuda").to(dtype)  # rows strided
+    starts = i32([sum(counts[:i]) for i in range(len(counts) + 1)])
+    want_k, want_v, row = k.clone(), v.clone(), 0
+    for b, c in enumerate(counts):
+        for i in range(c):
+            t = lens[b] - c + i
+            want_k[table[b, t // S], t % S] = new[row, 0]
+            want_v[table[b, t // S], t % S] = new[row, 2]
+            row += 1
+    status = decode.cache_append(new[:, 0], new[:, 2], k, v, table, lengths, starts, debug=True)
+    assert int(status) == 0 and torch.equal(k, want_k) and torch.equal(v, want_v)
+    if len(set(counts)) == 1:
+        k.zero_(), v.zero_()
+        n = counts[0]
+        decode.cache_append(new[:, 0].unflatten(0, (-1, n)), new[:, 2].unflatten(0, (-1, n)), k, v, table, lengths)
+        at = [(b, lens[b] - n + i) for b in range(len(counts)) for i in range(n)]
+        for r, (b, t) in enumerate(at):
+            assert torch.equal(k[table[b, t // S], t % S], new[r, 0])
+
+
+def test_append_data_errors(decode):
+    """Rows without a sequence, position or page are skipped and reported; nothing else is written."""
+    k, v, table, lengths = make_cache([20, 5], 16, 1, 64, torch.float32, seed=1, extra_cols=0)
+    new = torch.randn((6, 1, 64), generator=gen(7), device="cuda")
+    before = k.clone()
+    lengths2 = i32([2, 5])  # sequence 0 gets four rows but has two positions
+    status = decode.cache_append(new, new, k, v, table, lengths2, i32([0, 4, 6]), debug=True)
+    assert int(status) == decode.DATA_LENGTH_RANGE
+    want = before.clone()
+    want[table[0, 0], 0:2] = new[2:4]
+    want[table[1, 0], 3:5] = new[4:6]
+    assert torch.equal(k, want)
+    k.copy_(before)
+    bad = table.clone()
+    bad[0, 1] = k.shape[0]
+    status = decode.cache_append(new, new, k, v, bad, i32([18, 5]), i32([1, 5, 6]), debug=True)
+    assert int(status) == decode.DATA_PAGE_RANGE | decode.DATA_LENGTH_RANGE  # row 0 is nobody's
+    want = before.clone()
+    want[table[0, 0], 14:16] = new[1:3]
+    want[table[1, 0], 4] = new[5]
+    assert torch.equal(k, want)
+
+
+# ---- fork and compact ----------------------------------------------------------------------------
+
+def check_fork(decode, k, v, table, lengths, parents, keep, room, expect=0):
+    S, P = k.shape[-3], k.shape[-4]
+    k0, v0 = k.clone(), v.clone()
+    new, lens, refs, free, copies = ref.fork(table.cpu().numpy(), lengths.cpu().numpy(), parents, keep, room, P, S)
+    for _ in range(2):  # twice: the call can be repeated
+        r = decode.cache_fork(k, v, table, lengths, i32(parents), i32(keep), room, debug=True)
+        assert int(r.status) == expect
+        assert r.page_table.tolist() == new.tolist()
+        assert r.lengths.tolist() == lens.tolist()
+        assert r.ref_counts.tolist() == refs.tolist()
+        assert int(r.n_free) == len(free)
+        assert r.free_pages.tolist() == free + [-1] * (P - len(free))
+        for x, x0 in ((k, k0), (v, v0)):
+            want = x0.clone()
+            for a, b, n in copies:
+                want[..., b, :n, :, :] = x0[..., a, :n, :, :]
+            assert torch.equal(x, want)
+    return r
+
+
+@pytest.mark.parametrize("S,H,D,dtype,layers", [(16, 2, 64, torch.bfloat16, 3), (5, 1, 8, torch.float32, None),
+                                                (1, 1, 8, torch.float32, 2), (32, 8, 128, torch.bfloat16, 1)])
+def test_fork(decode, S, H, D, dtype, layers):
+    lens = [3 * S + 2, 2 * S, 1, 0, 7 * S - 1]
+    k, v, table, lengths = make_cache(lens, S, H, D, dtype, seed=S, layers=layers, spare=40, extra_cols=4)
+    same = list(range(5))
+    check_fork(decode, k, v, table, lengths, same, lens, 0)                          # nothing happens
+    check_fork(decode, k, v, table, lengths, same, [max(0, n - 3) for n in lens], 4)  # rejected tokens leave
+    check_fork(decode, k, v, table, lengths, [0, 0, 0, 4, 4, 1, 1, 3, -1],
+               [lens[0], lens[0] - 1, S, lens[4], lens[4] - S, lens[1], 0, 0, 0], 3)  # forks, trims, an end, a start
+    check_fork(decode, k, v, table, lengths, [], [], 9)                               # all end
+    r = check_fork(decode, k, v, table, lengths, [4, 0, 4], [lens[4] - 1, 1, lens[4] - 1], 1)
+    # and once more on its results
+    check_fork(decode, k, v, r.page_table, r.lengths, [2, 0, 1, 0], [lens[4] - 1, S, 1, lens[4] - 1], 2 * S)
+
+
+def test_fork_random(decode):
+    rng = np.random.RandomState(3)
+    for trial in range(25):
+        S = int(rng.randint(1, 20))
+        lens = [int(n) for n in rng.randint(0, 9 * S, rng.randint(1, 9))]
+        k, v, table, lengths = make_cache(lens, S, 1, 8, torch.float32, seed=trial, spare=int(rng.randint(20, 90)),
+                                          extra_cols=3)
+        for _ in range(2):
+            C = int(rng.randint(0, 12))
+            have = lengths.tolist()
+            parents = rng.randint(0, len(have), C).tolist()
+            keep = [int(rng.randint(0, have[p] + 1)) if rng.rand() < 0.7 else have[p] for p in parents]
+            # pages enough for every outcome, or an expected shortage
+            new, lens2, refs, free, _ = ref.fork(table.cpu().numpy(), np.array(have), parents, keep, 2, k.shape[0], S)
+            short = any((new[c] >= 0).sum() < min(table.shape[1], -(-(lens2[c] + 2) // S)) for c in range(C))
+            full = any(-(-(int(n) + 2) // S) > table.shape[1] for n in lens2)
+            r = check_fork(decode, k, v, table, lengths, parents, keep, 2,
+                           (decode.DATA_CACHE_FULL if short else 0) | (decode.DATA_LENGTH_RANGE if full else 0))
+            if C == 0 or short or full:
+                break
+            table, lengths = r.page_table, r.lengths
+
+
+def test_fork_many_pages(decode):
+    """More pages and sequences than one block has threads."""
+    rng = np.random.RandomState(5)
+    lens = rng.randint(1, 60, 700).tolist()
+    k, v, table, lengths = make_cache(lens, 4, 1, 8, torch.float32, seed=1, spare=9000, extra_cols=3)
+    parents = rng.randint(0, 700, 2500).tolist()
+    keep = [int(rng.randint(0, lens[p] + 1)) for p in parents]
+    check_fork(decode, k, v, table, lengths, parents, keep, 5)
+
+
+def test_fork_data_errors(decode):
+    k, v, table, lengths = make_cache([20, 33], 16, 1, 64, torch.float32, seed=1, spare=2, extra_cols=0)
+    check_fork(decode, k, v, table, lengths, [0, 5, -2, 1, -1], [21, 1, 0, 33, 3], 0, decode.DATA_LENGTH_RANGE)
+    check_fork(decode, k, v, table, lengths, [1, 1, 1], [33, 33, 33], 0, 0)
+    check_fork(decode, k, v, table, lengths, [1, 1, 1, 0, 0, 0], [33] * 3 + [20] * 3, 0, decode.DATA_CACHE_FULL)
+    check_fork(decode, k, v, table, lengths, [1], [33], 100, decode.DATA_LENGTH_RANGE | decode.DATA_CACHE_FULL
+               if k.shape[0] < 3 else decode.DATA_LENGTH_RANGE)
+    table[1, 1] = 99
+    check_fork(decode, k, v, table, lengths, [1, 0], [33, 20], 0, decode.DATA_PAGE_RANGE)
+
+
+@pytest.mark.parametrize("P,M,B,live,layers", [(1, 1, 1, 1, None), (40, 9, 5, 17, 2), (40, 9, 5, 0, 1), (64, 70, 3, 64, None),
+                                               (5000, 300, 40, 2300, 1)])
+def test_compact(decode, P, M, B, live, layers):
+    g = gen(P)
+    shape = (P, 4, 1, 8) if layers is None else (layers, P, 4, 1, 8)
+    k, v = (torch.randn(shape, generator=g, device="cuda") for _ in range(2))
+    ids = torch.randperm(P, generator=g, device="cuda")[:live].to(torch.int32)
+    table = torch.full((B * M,), -1, dtype=torch.int32, device="cuda")
+    at = torch.randperm(B * M, generator=g, device="cuda")[:min(live, B * M)]
+    table[at] = ids[:len(at)]
+    if live > 5:  # shared pages
+        table[at[0]] = table[at[1]]
+    table = table.view(B, M)
+    k0, v0 = k.clone(), v.clone()
+    new, refs, n, moves = ref.compact(table.cpu().numpy(), P)
+    for _ in range(2):
+        r = decode.cache_compact(k, v, table, debug=True)
+        assert int(r.status) == 0 and int(r.n_live) == n
+        assert r.page_table.tolist() == new.tolist() and r.ref_counts.tolist() == refs.tolist()
+        for x, x0 in ((k, k0), (v, v0)):
+            want = x0.clone()
+            for a, b in moves.items():
+                want[..., b, :, :, :] = x0[..., a, :, :, :]
+            assert torch.equal(x, want)
+
+
+def test_compact_strided_and_errors(decode):
+    kv = torch.randn((30, 2, 4, 2, 64), generator=gen(2), device="cuda").to(torch.bfloat16)
+    k0 = kv.clone()
+    table = i32([[29, 3, -1], [500, 7, -9]])
+    r = decode.cache_compact(kv[:, 0], kv[:, 1], table, debug=True)
+    assert int(r.status) == decode.DATA_PAGE_RANGE and int(r.n_live) == 3
+    assert r.page_table.tolist() == [[1, 0, -1], [-1, 2, -1]] or r.page_table.tolist() == [[2, 0, -1], [-1, 1, -1]]
+    for a, b in zip([3, 7, 29], [0, 1, 2]):
+        assert torch.equal(kv[b], k0[a])
+
+
+# ---- sampling ---------------------------------------------------------------------------------------
+
+def check_sample(decode, x, u, settings, filtered=True, bits=0):
+    """x [R, V] on the GPU, settings one (T, k, p, m) a row."""
+    R, V = x.shape
+    T, k, p, m = (list(c) for c in zip(*settings))
+    f = lambda c: torch.tensor(c, dtype=torch.float32, device="cuda")  # noqa: E731
+    r = decode.filtered_sample(x, u, f(T), top_k=i32(k), top_p=f(p), min_p=f(m), return_filtered=filtered, debug=True)
+    assert int(r.status) == bits
+    xs, us = x.float().cpu().numpy(), u.cpu().numpy()
+    tok, ps, cnt = r.tokens.tolist(), r.p.tolist(), r.n_kept.tolist()
+    fl = r.filtered.float().cpu().numpy() if filtered else None
+    for i in range(R):
+        j, want, kept = ref.sample_row(xs[i], us[i], T[i], k[i], p[i], m[i])
+        assert (tok[i], cnt[i]) == (j, len(kept)), (i, settings[i])
+        assert abs(ps[i] - want) <= 2.0 ** -19 * want + 2.0 ** -40, (i, ps[i], want)
+        if filtered:
+            w = np.full(V, -np.inf, np.float32)
+            w[kept] = xs[i][kept]
+            assert np.array_equal(fl[i], w), (i, settings[i])
+    return r
+
+
+MIX = [(1.0, 0, 1.0, 0.0), (0.7, 50, 0.95, 0.0), (0.8, 0, 0.9, 0.0), (1.0, 0, 1.0, 0.05), (0.6, 20, 0.8, 0.02),
+       (0.0, 0, 1.0, 0.0), (1.2, 400, 1.0, 0.0), (0.9, 0, 0.6, 0.01), (1.5, 0, 0.99, 0.0), (1.0, 1, 1.0, 0.0),
+       (2.0, 700, 0.9999, 1e-6), (0.05, 0, 0.5, 0.0), (1.0, 0, 0.0, 0.0), (1.0, 0, 1.0, 1.0), (30.0, 0, 0.7, 0.0),
+       (1.0, 5000, 0.3, 0.0), (0.3, -4, 2.0, -1.0)]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [1, 2, 7, 33, 1000, 4096, 12001, 32000, 128256, 152064, 300001])
+def test_sample_settings(decode, dtype, V):
+    R = len(MIX)
+    for std in (3.0, 0.3):
+        x = (torch.randn((R, V), generator=gen(V), device="cuda") * std).to(dtype)
+        u = torch.rand(R, generator=gen(V + 1), device="cuda")
+        check_sample(decode, x, u, MIX)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_sample_ties_and_masks(decode, dtype):
+    """Rows of equal logits, of two values, mostly -inf, signed zeros, the type's lowest value; uniforms at both ends."""
+    for V in (5, 2048, 40008, 70001):
+        base = torch.zeros((6, V), device="cuda")
+        base[1] = torch.randint(0, 2, (V,), generator=gen(1), device="cuda") * 1.5
+        base[2] = -math.inf
+        base[2, V // 3], base[2, V - 1] = 2.0, 1.5
+        base[3] = torch.where(torch.rand(V, generator=gen(2), device="cuda") < 0.5, 0.0, -0.0)
+        base[4] = torch.finfo(dtype).min
+        base[4, V // 2] = -3.0
+        base[5] = torch.randint(0, 4, (V,), generator=gen(3), device="cuda").float()
+        x = base.to(dtype)
+        for u in (0.0, 0.5, 1 - 2.0 ** -24):
+            for s in ((1.0, 0, 1.0, 0.0), (1.0, 3, 1.0, 0.0), (1.0, 0, 0.37, 0.0), (0.0, 0, 1.0, 0.0),
+                      (0.5, V // 2, 0.9, 0.2), (3.0, 1500, 0.5, 0.0)):
+                check_sample(decode, x, torch.full((6,), u, device="cuda"), [s] * 6)
+
+
+def test_sample_sorted_rows_and_many_rows(decode):
+    V = 32000
+    x = torch.sort(torch.randn((40, V), generator=gen(4), device="cuda") * 3, dim=1).values
+    x[::2] = x[::2].flip(1)
+    u = torch.rand(40, generator=gen(5), device="cuda")
+    check_sample(decode, x.to(torch.bfloat16), u, [MIX[i % len(MIX)] for i in range(40)])
+    check_sample(decode, x, u, [MIX[i % len(MIX)] for i in range(40)], filtered=False)
+    R = 1500
+    x = (torch.randn((R, 700), generator=gen(6), device="cuda") * 4).to(torch.bfloat16)
+    check_sample(decode, x, torch.rand(R, generator=gen(7), device="cuda"), [MIX[i % len(MIX)] for i in range(R)])
+
+
+def test_sample_scalars_strides_and_streams(decode):
+    big = (torch.randn((9, 5000), generator=gen(1), device="cuda") * 3).to(torch.bfloat16)
+    u = torch.rand(9, generator=gen(2), device="cuda")
+    for cols in (slice(0, 4000), slice(3, 4004), slice(8, 4009)):
+        x = big[:, cols]
+        want = decode.filtered_sample(x.contiguous(), u, 0.7, top_k=40, top_p=0.9, return_filtered=True)
+        got = decode.filtered_sample(x, u, torch.full((9,), 0.7, device="cuda"), top_k=i32([40] * 9), top_p=0.9,
+                                     return_filtered=True)
+        assert all(torch.equal(a, b) for a, b in zip(got[:4], want[:4]))
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        other = decode.filtered_sample(x, u, 0.7, top_k=40, top_p=0.9, return_filtered=True, stream=s)
+        s.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(other[:4], want[:4]))
+    x3 = big[:, :4000].contiguous().view(3, 3, 4000)
+    r = decode.filtered_sample(x3, u.view(3, 3), 0.7, top_k=40, top_p=0.9)
+    assert r.tokens.shape == (3, 3) and r.filtered is None
+    for j in range(9):
+        assert int(r.tokens.flatten()[j]) == ref.sample_row(x3.view(9, -1)[j].float().cpu().numpy(), float(u[j]), 0.7, 40, 0.9)[0]
+
+
+@pytest.mark.parametrize("V", [100, 40000, 300001])
+def test_sample_data_errors(decode, V):
+    x = torch.randn((6, V), generator=gen(1), device="cuda")
+    x[1, V // 2] = math.nan
+    x[2, V - 1] = math.inf
+    x[3] = -math.inf
+    u = torch.full((6,), 0.5, device="cuda")
+    for kw in ({}, {"top_k": 5}, {"top_p": 0.5}):
+        r = decode.filtered_sample(x, u, 1.0, return_filtered=True, debug=True, **kw)
+        assert int(r.status) == 2  # SPEC_DATA_NONFINITE_LOGIT
+        for i in (1, 2, 3):
+            assert (int(r.tokens[i]), float(r.p[i]), int(r.n_kept[i])) == (0, 0.0, 0)
+            assert (r.filtered[i] == -math.inf).all()
+        good = decode.filtered_sample(x[[0, 4, 5]].contiguous(), u[:3], 1.0, return_filtered=True, **kw)
+        for a, b in zip(r[:4], good[:4]):
+            assert torch.equal(a[[0, 4, 5]], b)
+    y = x[[0, 4, 5]].contiguous()
+    r = decode.filtered_sample(y, torch.tensor([0.5, 1.0, -0.1], device="cuda"), 1.0, debug=True)
+    assert int(r.status) == 4 and (r.tokens >= 0).all() and (r.tokens < V).all()
+    T = torch.tensor([math.nan, -1.0, 0.5], device="cuda")
+    r = decode.filtered_sample(y, u[:3], T, debug=True)
+    assert int(r.status) == decode.DATA_PARAM_RANGE
+    for i, t in enumerate((1.0, 1.0, 0.5)):
+        assert int(r.tokens[i]) == ref.sample_row(y[i].cpu().numpy(), 0.5, t)[0]
+
+
+def test_filtered_rows_feed_the_verifier(decode):
+    """Truncated target and drafter rows: the verifier's outputs equal the oracle's on the rows that the
+    definition gives, and no token outside the kept sets is ever emitted."""
+    import oracle
+    from draft_verify_acceptance_gb300 import binding
+    B, K, V, T = 24, 4, 5003 // 8 * 8, 0.9
+    t = (torch.randn((B, K + 1, V), generator=gen(1), device="cuda") * 3).to(torch.bfloat16)
+    d = (t[:, :K].float() + 0.5 * torch.randn((B, K, V), generator=gen(2), device="cuda")).to(torch.bfloat16)
+    u = torch.rand((B, K + 1), generator=gen(3), device="cuda")
+    draft = decode.filtered_sample(d, torch.rand((B, K), generator=gen(4), device="cuda"), T, top_k=40, top_p=0.95,
+                                   return_filtered=True)
+    target = decode.filtered_sample(t, u, T, top_k=40, top_p=0.95, return_filtered=True).filtered
+    res = binding.verify_ex(target, draft.filtered, draft.tokens, u, T)
+    assert int(res["status"]) == 0
+    raw = lambda x: x.cpu().view(torch.int16).numpy().view(np.uint16)  # noqa: E731
+    want = oracle.verify_ref(raw(target), raw(draft.filtered), draft.tokens.cpu().numpy(), u.cpu().numpy(), T, 0,
+                             want_debug=True)
+    ok = want["flags"] == 0
+    assert ok.sum() > B // 2
+    assert np.array_equal(res["accepted_len"].cpu().numpy()[ok], want["accepted_len"][ok])
+    assert np.array_equal(res["out_tokens"].cpu().numpy()[ok], want["out_tokens"][ok])
+    n, out = res["accepted_len"].tolist(), res["out_tokens"].tolist()
+    for b in range(B):
+        for i in range(n[b] + 1):
+            assert float(target[b, i, out[b][i]]) > -math.inf
