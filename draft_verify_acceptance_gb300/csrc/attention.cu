@@ -5,6 +5,7 @@
 //   l_r = sum_t e^(s_rt - m_r),  m_r a running maximum,
 // for the tokens t <= n - Q + i that query i of a sequence of n tokens sees.
 #include "attention_common.cuh"
+#include "attention_mma.cuh"
 
 namespace specv {
 namespace {
@@ -202,22 +203,44 @@ __global__ void __launch_bounds__(kThreadsF) attention_kernel(const AttnArgs a) 
 
 }  // namespace
 
+constexpr int kMaxBlocks = 4;  // blocks of 8 rows an item of the tensor-core kernel holds at most
+
 size_t attention_workspace(int D, bool bf16) {
-  (void)bf16;
+  const size_t rows = bf16 ? 8 * kMaxBlocks : kRowsF;
   return (static_cast<size_t>(kAttnMaxCtas) * 4 +
-          static_cast<size_t>(kAttnMaxCtas) * 2 * kRowsF * (D + 2) * 4 + 255) & ~static_cast<size_t>(255);
+          static_cast<size_t>(kAttnMaxCtas) * 2 * rows * (D + 2) * 4 + 255) & ~static_cast<size_t>(255);
 }
 
-cudaError_t attention_prepare() { return cudaSuccess; }
+cudaError_t attention_prepare() {
+  cudaError_t e[] = {mma::prepare<64, 1>(), mma::prepare<64, 2>(), mma::prepare<64, 3>(), mma::prepare<64, 4>(),
+                     mma::prepare<128, 1>(), mma::prepare<128, 2>(), mma::prepare<128, 3>(), mma::prepare<128, 4>()};
+  for (cudaError_t x : e)
+    if (x != cudaSuccess) return x;
+  return cudaSuccess;
+}
 
 cudaError_t launch_attention(const AttnArgs& a, int sm_count, cudaStream_t stream) {
-  const int grid = sm_count * 3 < kAttnMaxCtas ? sm_count * 3 : kAttnMaxCtas;
-  if (a.cache.head_dim == 64) {
-    if (a.cache.bf16) attention_kernel<BF16, 64><<<grid, kThreadsF, 0, stream>>>(a);
+  const bool wide = a.cache.head_dim == 128;
+  if (!a.cache.bf16) {
+    const int grid = sm_count * 3 < kAttnMaxCtas ? sm_count * 3 : kAttnMaxCtas;
+    if (wide) attention_kernel<F32, 128><<<grid, kThreadsF, 0, stream>>>(a);
     else attention_kernel<F32, 64><<<grid, kThreadsF, 0, stream>>>(a);
-  } else {
-    if (a.cache.bf16) attention_kernel<BF16, 128><<<grid, kThreadsF, 0, stream>>>(a);
-    else attention_kernel<F32, 128><<<grid, kThreadsF, 0, stream>>>(a);
+    return cudaGetLastError();
+  }
+  // Rows in tiles of equal size, at most 32.
+  const int R = a.Q * (a.Hq / a.cache.heads), most = 8 * kMaxBlocks;
+  const int tiles = (R + most - 1) / most;
+  const int nb = ((R + tiles - 1) / tiles + 7) / 8;
+  const int grid = sm_count * 2 < kAttnMaxCtas ? sm_count * 2 : kAttnMaxCtas;
+  switch (nb + (wide ? 4 : 0)) {
+    case 1: mma::launch<64, 1>(a, grid, stream); break;
+    case 2: mma::launch<64, 2>(a, grid, stream); break;
+    case 3: mma::launch<64, 3>(a, grid, stream); break;
+    case 4: mma::launch<64, 4>(a, grid, stream); break;
+    case 5: mma::launch<128, 1>(a, grid, stream); break;
+    case 6: mma::launch<128, 2>(a, grid, stream); break;
+    case 7: mma::launch<128, 3>(a, grid, stream); break;
+    default: mma::launch<128, 4>(a, grid, stream); break;
   }
   return cudaGetLastError();
 }

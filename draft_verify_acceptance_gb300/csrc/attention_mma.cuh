@@ -1,0 +1,434 @@
+// attention_mma.cuh -- bf16 paged attention on the tensor cores (sm_103a).
+//
+// Decode attention reads every cached byte for a handful of rows, so HBM is
+// the bound and the tensor cores only have to keep out of its way.  The
+// products are taken transposed,
+//     S^T [tokens x rows] = K Q^T,   O^T [D x rows] += V^T P^T,
+// which puts the long dimensions (tokens, D) on the 16-row side of
+// mma.m16n8k16 and the few rows on its 8-column side: 4 rows cost one column
+// block and 24 cost three, where rows on the 16-row side would cost two and
+// four.  It also leaves a row's running maximum, its sum and its column of
+// O^T in the same threads.  P^T changes from accumulator to operand layout
+// by one 8 x 8 transpose (movmatrix) per 8 tokens.  A weight enters the second
+// product as the sum of two bf16 values (16 significant bits): one bf16 weight
+// would lose up to 2^-8 of each term, as much as rounding the output does, and
+// the extra product is hidden behind HBM.
+//
+// Every warp streams tokens of its own: 16 a step through a private ring of
+// kStages steps in shared memory (cp.async, 16-byte pieces, XOR-swizzled
+// rows), so warps wait for their own loads alone and the block meets only at
+// the end of an item.  A row's reference maximum moves only when a score
+// passes it by 2^8 (the weights then stay below 2^8, which fp32 sums carry
+// without loss), so most steps need no reduction across
+// lanes and no rescaling.
+#pragma once
+
+#include "attention_common.cuh"
+
+namespace specv {
+namespace mma {
+
+constexpr int kWarpsM = 4;
+constexpr int kThreadsM = kWarpsM * 32;
+constexpr int kTokens = 16;                  // a warp's step
+constexpr int kStepM = kWarpsM * kTokens;    // a block's step
+constexpr float kSlack = 8.f;                // how far (log2) a score may pass the reference
+
+template <int D>
+struct Ring {
+  static constexpr int kStages = D == 128 ? 3 : 6;
+  static constexpr int kRow = D * 2;                     // bytes of a token's K or V
+  static constexpr int kHalf = kTokens * kRow;           // K of a step; V follows
+  static constexpr int kStage = 2 * kHalf;
+  static constexpr int kBytes = kWarpsM * kStages * kStage;
+};
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+__device__ __forceinline__ bool nonfinite2(uint32_t w) {
+  return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+}
+
+// NB blocks of 8 rows an item.
+template <int D, int NB>
+__global__ void __launch_bounds__(kThreadsM, 2) attention_mma_kernel(const AttnArgs a, DivU64 by_page) {
+  constexpr int kRows = 8 * NB, KS = D / 16, kStages = Ring<D>::kStages;
+  constexpr int kRow = Ring<D>::kRow, kHalf = Ring<D>::kHalf, kStage = Ring<D>::kStage;
+  constexpr int kChunks = D / 8;               // 16-byte pieces of a row
+  constexpr int kRowsPer = 32 / kChunks;       // rows a warp's copy instruction covers
+  constexpr int kPitch = D + 4;                // of the warps' O in shared memory, floats
+  static_assert(kWarpsM * kRows * kPitch * 4 <= Ring<D>::kBytes, "the warps' parts fit the ring");
+  extern __shared__ __align__(128) char ring[];
+  __shared__ uint32_t s_valid[kWarpsM][kStages];  // which tokens of a step exist
+  __shared__ float s_m[kWarpsM][kRows], s_l[kWarpsM][kRows];
+  __shared__ long long s_plan[2 * kWarpsM + 4];
+  __shared__ int s_flag;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, t4 = lane & 3;
+  const int H = a.cache.heads, G = a.Hq / H, R = a.Q * G;
+  const int RT = (R + kRows - 1) / kRows;
+  const int S = a.cache.page_size;
+  const bool page_steps = S % kTokens == 0;    // a step lies in one page
+  char* mine = ring + warp * (kStages * kStage);
+  const uint32_t mine_at = smem_addr(mine);
+
+  AttnPlan plan = attn_plan<kStepM, kThreadsM>(a, H * RT, 4, s_plan);
+  long long w = plan.per * blockIdx.x;
+  const long long end = min(plan.total, w + plan.per);
+  int b = plan.b;
+  long long base = plan.base;
+  while (w < end) {
+    int n = attn_length(a, b), tiles = attn_tiles<kStepM>(n);
+    while (w >= base + static_cast<long long>(tiles) * H * RT) {
+      base += static_cast<long long>(tiles) * H * RT;
+      n = attn_length(a, ++b);
+      tiles = attn_tiles<kStepM>(n);
+    }
+    const int item = static_cast<int>((w - base) / tiles);
+    const int tile0 = static_cast<int>((w - base) - static_cast<long long>(item) * tiles);
+    const int tile1 = static_cast<int>(min(static_cast<long long>(tiles), tile0 + (end - w)));
+    const int rt = item / H, h = item - rt * H;
+    const int row0 = rt * kRows, rows = min(kRows, R - row0);
+    const int32_t* table = a.table.ids + b * a.table.stride;
+
+    // The warp's steps: tokens [kStepM * tile + 16 * warp, + 16) of each tile.
+    const int first = tile0 * kStepM + warp * kTokens;
+    const int last = min(tile1 * kStepM, n);   // tokens of this part end here
+    const int steps = first < last ? (last - first + kStepM - 1) / kStepM : 0;
+
+    // Lane l looks up the page of the step's token l % 16.
+    auto page_of = [&](int j) -> int {
+      const int t = first + j * kStepM + (lane & (kTokens - 1));
+      return t < last ? table[static_cast<int>(by_page(static_cast<unsigned long long>(t)))] : 0;
+    };
+    auto issue = [&](int j, int page) {
+      const int t0 = first + j * kStepM;
+      const int t = t0 + (lane & (kTokens - 1));
+      const bool known = page >= 0 && page < a.cache.pages;
+      const bool ok = t < last && known;
+      if (t < last && !known && a.status) atomicOr(a.status, kDataPageRange);
+      const uint32_t valid = __ballot_sync(0xffffffffu, ok) & 0xffffu;
+      const int stage = j % kStages;
+      if (lane == 0) s_valid[warp][stage] = valid;
+      const int slot = static_cast<int>(by_page(static_cast<unsigned long long>(t)));
+      const long long off = (ok ? page * a.cache.page_stride + (t - slot * S) * a.cache.token_stride : 0ll) +
+                            h * (D * 2);
+      const int chunk = lane % kChunks, r0 = lane / kChunks;
+      const uint32_t dst = mine_at + stage * kStage;
+      const char* kp = a.cache.k + chunk * 16;
+      const char* vp = a.cache.v + chunk * 16;
+      if (page_steps && valid == 0xffffu) {
+        const long long o0 = __shfl_sync(0xffffffffu, off, 0) + r0 * a.cache.token_stride;
+        kp += o0;
+        vp += o0;
+#pragma unroll
+        for (int i = 0; i < kTokens / kRowsPer; ++i) {
+          const int r = r0 + i * kRowsPer;
+          const uint32_t d = dst + r * kRow + ((chunk ^ (r & 7)) << 4);
+          cp16(d, kp, 16);
+          cp16(d + kHalf, vp, 16);
+          kp += kRowsPer * a.cache.token_stride;
+          vp += kRowsPer * a.cache.token_stride;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kTokens / kRowsPer; ++i) {
+          const int r = r0 + i * kRowsPer;
+          const long long o = __shfl_sync(0xffffffffu, off, r);
+          const uint32_t bytes = (valid >> r) & 1 ? 16 : 0;  // 0: the piece is zero-filled
+          const uint32_t d = dst + r * kRow + ((chunk ^ (r & 7)) << 4);
+          cp16(d, kp + o, bytes);
+          cp16(d + kHalf, vp + o, bytes);
+        }
+      }
+    };
+
+    __syncthreads();  // the ring is free again
+    int page = page_of(0);
+#pragma unroll
+    for (int j = 0; j < kStages - 1; ++j) {
+      const int next = page_of(j + 1);
+      if (j < steps) issue(j, page);
+      cp_commit();
+      page = next;
+    }
+
+    // Queries as operand fragments (rows past the last are zero), and the
+    // last token that each of the thread's rows sees.
+    uint32_t qf[NB][KS][2];
+    int limit[NB][2];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      const int r = nb * 8 + g;
+      const AttnRow ar = attn_row(a, row0 + min(r, rows - 1), h);
+      const char* qp = a.q + b * a.q_batch + ar.i * a.q_token + ar.hq * a.q_head + t4 * 4;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        qf[nb][ks][0] = r < rows ? __ldg(reinterpret_cast<const uint32_t*>(qp + ks * 32)) : 0u;
+        qf[nb][ks][1] = r < rows ? __ldg(reinterpret_cast<const uint32_t*>(qp + ks * 32 + 16)) : 0u;
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) limit[nb][x] = n - a.Q + (row0 + nb * 8 + t4 * 2 + x) / G;
+    }
+
+    float o[KS][NB][4], m[NB][2], l[NB][2];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      m[nb][0] = m[nb][1] = -INFINITY;
+      l[nb][0] = l[nb][1] = 0.f;
+#pragma unroll
+      for (int mt = 0; mt < KS; ++mt)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) o[mt][nb][x] = 0.f;
+    }
+
+    for (int j = 0; j < steps; ++j) {
+      const int next = page_of(j + kStages);
+      cp_wait<kStages - 2>();
+      __syncwarp();  // this step has landed, and every lane is done with the one before
+      if (j + kStages - 1 < steps) issue(j + kStages - 1, page);
+      cp_commit();
+      page = next;
+      const int t0 = first + j * kStepM;
+      const int stage = j % kStages;
+      const uint32_t kat = mine_at + stage * kStage, vat = kat + kHalf;
+      const uint32_t valid = s_valid[warp][stage];
+
+      // S^T = K Q^T
+      float s[NB][4];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) s[nb][x] = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        const int r = lane & 15, c = ks * 2 + (lane >> 4);
+        uint32_t kf[4];
+        ldsm4(kf, kat + r * kRow + ((c ^ (r & 7)) << 4));
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) mma16816(s[nb], kf, qf[nb][ks][0], qf[nb][ks][1]);
+      }
+      // a step whose 16 tokens exist and are seen by every row needs no mask
+      const bool masked = valid != 0xffffu || t0 + kTokens - 1 > n - a.Q;
+      bool grow = false;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          s[nb][x] *= a.scale_log2;
+          if (masked) {
+            const int r = g + (x >> 1) * 8;
+            if (!((valid >> r) & 1) || t0 + r > limit[nb][x & 1]) s[nb][x] = -INFINITY;
+          }
+          grow |= s[nb][x] > m[nb][x & 1] + kSlack;
+        }
+      if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            float mx = fmaxf(s[nb][x], s[nb][x + 2]);
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            mx = fmaxf(mx, m[nb][x]);
+            const float c = m[nb][x] == -INFINITY ? 0.f : ex2(m[nb][x] - mx);
+            m[nb][x] = mx;
+            l[nb][x] *= c;
+#pragma unroll
+            for (int mt = 0; mt < KS; ++mt) {
+              o[mt][nb][x] *= c;
+              o[mt][nb][x + 2] *= c;
+            }
+          }
+      }
+      // weights, their sums, and P^T as operand fragments
+      uint32_t pf[NB][4];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const float ref = m[nb][x & 1] == -INFINITY ? 0.f : m[nb][x & 1];
+          s[nb][x] = ex2(s[nb][x] - ref);
+          l[nb][x & 1] += s[nb][x];
+        }
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const uint32_t hi = pack2(s[nb][y * 2], s[nb][y * 2 + 1]);
+          const uint32_t lo = pack2(s[nb][y * 2] - bf16_lo(hi), s[nb][y * 2 + 1] - bf16_hi(hi));
+          pf[nb][y] = transpose8(hi);
+          pf[nb][y + 2] = transpose8(lo);
+        }
+      }
+      if (masked) {
+        // A value that is not finite would reach rows that do not see its
+        // token as 0 * inf.  Such values are added to the rows that do see
+        // them one by one, and are zero in the product.
+        bool odd = false;
+        for (int e = lane; e < kTokens * kChunks; e += 32) {
+          uint32_t x[4];
+          asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(vat + e * 16) : "memory");
+          odd |= nonfinite2(x[0]) || nonfinite2(x[1]) || nonfinite2(x[2]) || nonfinite2(x[3]);
+        }
+        if (__any_sync(0xffffffffu, odd)) {
+          const uint16_t* vs = reinterpret_cast<const uint16_t*>(mine + stage * kStage + kHalf);
+          for (int t = 0; t < kTokens; ++t) {
+            const int from = (t & 7) * 4 + t4;
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+              float p[2];
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                const float lo = __shfl_sync(0xffffffffu, s[nb][x], from);
+                const float hi = __shfl_sync(0xffffffffu, s[nb][x + 2], from);
+                p[x] = t < 8 ? lo : hi;
+              }
+#pragma unroll
+              for (int mt = 0; mt < KS; ++mt)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                  const int d = mt * 16 + g + y * 8;
+                  const float v = __uint_as_float(
+                      static_cast<uint32_t>(vs[t * D + (((d >> 3) ^ (t & 7)) << 3) + (d & 7)]) << 16);
+                  if (!isfinite(v)) {
+                    if (p[0] != 0.f) o[mt][nb][y * 2] += p[0] * v;
+                    if (p[1] != 0.f) o[mt][nb][y * 2 + 1] += p[1] * v;
+                  }
+                }
+            }
+          }
+          __syncwarp();
+          for (int e = lane; e < kTokens * D / 2; e += 32) {
+            uint32_t* x = reinterpret_cast<uint32_t*>(mine + stage * kStage + kHalf) + e;
+            uint32_t v = *x;
+            if ((v & 0x7f80u) == 0x7f80u) v &= 0xffff0000u;
+            if ((v & 0x7f800000u) == 0x7f800000u) v &= 0xffffu;
+            *x = v;
+          }
+          __syncwarp();
+        }
+      }
+      // O^T += V^T P^T
+#pragma unroll
+      for (int mt = 0; mt < KS; ++mt) {
+        const int r = (lane & 7) + ((lane >> 4) << 3), c = mt * 2 + ((lane >> 3) & 1);
+        uint32_t vf[4];
+        ldsm4t(vf, vat + r * kRow + ((c ^ (r & 7)) << 4));
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          mma16816(o[mt][nb], vf, pf[nb][0], pf[nb][1]);
+          mma16816(o[mt][nb], vf, pf[nb][2], pf[nb][3]);
+        }
+      }
+    }
+    cp_wait<0>();
+
+    // ---- the warps' parts, then the item's ----
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        l[nb][x] += __shfl_xor_sync(0xffffffffu, l[nb][x], 4);
+        l[nb][x] += __shfl_xor_sync(0xffffffffu, l[nb][x], 8);
+        l[nb][x] += __shfl_xor_sync(0xffffffffu, l[nb][x], 16);
+        if (g == 0) {
+          s_m[warp][nb * 8 + t4 * 2 + x] = m[nb][x];
+          s_l[warp][nb * 8 + t4 * 2 + x] = l[nb][x];
+        }
+      }
+    __syncthreads();  // every warp has left its ring
+    float* parts = reinterpret_cast<float*>(ring);
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int mt = 0; mt < KS; ++mt)
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          parts[(warp * kRows + nb * 8 + t4 * 2 + (x & 1)) * kPitch + mt * 16 + g + (x >> 1) * 8] = o[mt][nb][x];
+    __syncthreads();
+    const bool whole = tile0 == 0 && tile1 == tiles;
+    float* slot = attn_slot<kRows, D>(a, blockIdx.x, tile0 == 0);
+    for (int e = tid; e < rows * (D / 4); e += kThreadsM) {
+      const int r = e / (D / 4), d = (e - r * (D / 4)) * 4;
+      float mm = -INFINITY, ll = 0.f;
+      float4 oo = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int x = 0; x < kWarpsM; ++x) mm = fmaxf(mm, s_m[x][r]);
+#pragma unroll
+      for (int x = 0; x < kWarpsM; ++x) {
+        const float c = s_m[x][r] == -INFINITY ? 0.f : ex2(s_m[x][r] - mm);
+        const float4 v = *reinterpret_cast<const float4*>(parts + (x * kRows + r) * kPitch + d);
+        ll = fmaf(c, s_l[x][r], ll);
+        oo.x = fmaf(c, v.x, oo.x);
+        oo.y = fmaf(c, v.y, oo.y);
+        oo.z = fmaf(c, v.z, oo.z);
+        oo.w = fmaf(c, v.w, oo.w);
+      }
+      if (whole) {
+        attn_write<D>(a, b, h, row0 + r, d, mm, ll, oo);
+      } else {
+        *reinterpret_cast<float4*>(slot + r * D + d) = oo;
+        if (d == 0) {
+          slot[kRows * D + r] = mm;
+          slot[kRows * D + kRows + r] = ll;
+        }
+      }
+    }
+    if (!whole) {
+      const long long first_step = base + static_cast<long long>(item) * tiles;
+      if (attn_arrive(a, first_step, tiles, plan.per, &s_flag))
+        attn_join<kRows, D, kThreadsM>(a, b, h, row0, rows, first_step, tiles, plan.per);
+    }
+    w += tile1 - tile0;
+  }
+}
+
+template <int D, int NB>
+cudaError_t prepare() {
+  return cudaFuncSetAttribute(attention_mma_kernel<D, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              Ring<D>::kBytes);
+}
+template <int D, int NB>
+void launch(const AttnArgs& a, int grid, cudaStream_t stream) {
+  attention_mma_kernel<D, NB><<<grid, kThreadsM, Ring<D>::kBytes, stream>>>(
+      a, DivU64::make(static_cast<unsigned long long>(a.cache.page_size)));
+}
+
+}  // namespace mma
+}  // namespace specv

@@ -181,6 +181,12 @@ def _p(t):
     return None if t is None else t.data_ptr()
 
 
+def attention_workspace_size(B, Q, Hq, heads, head_dim, dtype):
+    """Bytes of workspace that a paged_attention call with these sizes needs (0: not supported).  A call
+    inside a CUDA graph brings its own: zero-filled once, used by one call at a time."""
+    return int(_lib.spec_attention_workspace_size(B, Q, Hq, heads, head_dim, _DTYPES[dtype]))
+
+
 @_on_stream
 def paged_attention(q, k_pages, v_pages, page_table, lengths, scale=None, *, return_lse=False, out=None,
                     workspace=None, debug=False, _stream=0):

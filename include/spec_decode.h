@@ -66,7 +66,8 @@ typedef struct {
  *            every call leaves it fit for the next.  One call at a time.
  *
  * Scores, softmax and sums are fp32 (bf16: products of bf16 pairs summed in
- * fp32; the weights exp(...) are rounded to bf16 for the product with v).
+ * fp32; a weight exp(...) multiplies v as the sum of two bf16 values), and
+ * the output is rounded once.
  * The result does not depend on the schedule's timing: partial results are
  * joined in a fixed order.
  */

@@ -2,8 +2,8 @@
 
 Tolerances.  Attention: a score is a sum of D products in fp32, off by at most (D + 8) 2^-24 sum|q||k|
 scale, which moves a weight by that relative amount (twice: numerator and sum); weights, scaling and
-joining add less than 2^-18 of sum p|v|; in bf16 a weight is rounded once (2^-9) and the output
-once (2^-9 of itself).  lse is off by the score's error plus 2^-20 of its own size.  The cache operators
+joining add less than 2^-18 of sum p|v|; a bf16 output is rounded once, by at most 2^-8 of itself, which
+is at most 2^-9 (sum p|v| + |out|).  lse is off by the score's error plus 2^-20 of its own size.  The cache operators
 and the sampler's tokens are whole numbers or copies and must be equal; p = w / S is a quotient of weights
 within 2^-21 of the exponential each and two roundings: 2^-19 relative for p above 2^-18 of the largest,
 whose whole-number weights are rounded by 2^-22 at most.
@@ -200,7 +200,7 @@ def test_attention_in_a_cuda_graph(decode):
     torch.cuda.synchronize()
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
-    ws = torch.zeros(1 << 23, dtype=torch.uint8, device="cuda")
+    ws = torch.zeros(decode.attention_workspace_size(2, 1, 8, 2, 128, q.dtype), dtype=torch.uint8, device="cuda")
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph, stream=s):
         decode.paged_attention(q, k, v, table, lengths, out=out, workspace=ws)
