@@ -496,6 +496,24 @@ def test_sample_sorted_rows_and_many_rows(decode):
     check_sample(decode, x, torch.rand(R, generator=gen(7), device="cuda"), [MIX[i % len(MIX)] for i in range(R)])
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [1000, 32000, 40000, 128256, 500003])
+def test_sample_sums_are_the_definition_s(decode, dtype, V):
+    """p is fp32(w) / fp32(S) of the whole-number weights to the bit, so a sum that is off by little shows; the
+    largest uniform draws the last token of any weight."""
+    x = (torch.randn((12, V), generator=gen(V + 9), device="cuda") * 2.5).to(dtype)
+    u = torch.rand(12, generator=gen(V), device="cuda")
+    u[::4] = 1 - 2.0 ** -24
+    for top_p in (1.0, 0.9, 0.3):
+        r = decode.filtered_sample(x, u, 0.8, top_p=top_p)
+        for i in range(12):
+            row = x[i].float().cpu().numpy()
+            j, _, kept = ref.sample_row(row, float(u[i]), 0.8, 0, top_p)
+            w = ref.weights(row, 0.8)
+            assert int(r.tokens[i]) == j and int(r.n_kept[i]) == len(kept)
+            assert float(r.p[i]) == float(np.float32(w[j]) / np.float32(w[kept].sum()))
+
+
 def test_sample_scalars_strides_and_streams(decode):
     big = (torch.randn((9, 5000), generator=gen(1), device="cuda") * 3).to(torch.bfloat16)
     u = torch.rand(9, generator=gen(2), device="cuda")
