@@ -38,17 +38,18 @@ namespace cg = cooperative_groups;
 namespace specv {
 namespace {
 
-constexpr int kThreadsS = 256;
+constexpr int kThreadsS = 512;
 constexpr int kWarpsS = kThreadsS / 32;
 constexpr int kMaxCS = 8;               // blocks of a cluster
 constexpr int kDepth = 12;              // listed logits a thread holds
 constexpr int kList = 1024;             // listed logits of a row
 constexpr int kPerThread = kList / kThreadsS;
-constexpr int kGroups = kList / kWarpsS;  // groups of vectors with sums of their own (they share the list's memory)
-constexpr long long kSliceBytesS = 65024;
+constexpr int kGroups = kList / kWarpsS;  // rounds with group sums of their own (they share the list's memory)
+constexpr long long kSliceBytesS = 65024;     // a slice, while more blocks can share the row
+constexpr long long kMaxSliceS = 128 * 1024;  // a slice of the largest cluster (65536 bf16: 16-bit places)
 constexpr int kChunkS = 1024;           // vectors per bulk copy
-constexpr int kMaxChunksS = 4;
-static_assert(kSliceBytesS / 16 <= kChunkS * kMaxChunksS, "bulk copies of a slice");
+constexpr int kMaxChunksS = 8;
+static_assert(kMaxSliceS / 16 <= kChunkS * kMaxChunksS, "bulk copies of a slice");
 
 // 2^f on [-1/2, 1/2] times 2^40: 1 + f (c1 + f (c2 + ...)), a minimax fit of
 // the relative error (9.2e-8; 1.9e-7 with the roundings of every operation).
@@ -219,10 +220,57 @@ __device__ __forceinline__ float element(const uint4& w, int k) {
   return (k & 1) ? bf16_hi(u[k >> 1]) : bf16_lo(u[k >> 1]);
 }
 
+// A running maximum of 16-byte vectors that keeps a NaN.
+template <typename E>
+struct Peak;
+template <>
+struct Peak<BF16> {
+  uint32_t m = 0xff80ff80u;  // (-inf, -inf)
+  static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+  }
+  __device__ __forceinline__ void take(const uint4& w) { m = max2(m, max2(max2(w.x, w.y), max2(w.z, w.w))); }
+  __device__ __forceinline__ float value() const {
+    const uint32_t x = max2(m, __byte_perm(m, 0, 0x1032));
+    return bf16_lo(x);
+  }
+};
+template <>
+struct Peak<F32> {
+  float m = -INFINITY;
+  static __device__ __forceinline__ float max2(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+  }
+  __device__ __forceinline__ void take(const uint4& w) {
+    m = max2(m, max2(max2(__uint_as_float(w.x), __uint_as_float(w.y)), max2(__uint_as_float(w.z), __uint_as_float(w.w))));
+  }
+  __device__ __forceinline__ float value() const { return m; }
+};
+
+// Which elements of a vector are at least `from`: bit k for element k.
+template <typename E>
+__device__ __forceinline__ uint32_t at_least(const uint4& w, float from) {
+  uint32_t hit = 0;
+#pragma unroll
+  for (int k = 0; k < Staged<E>::kVec; ++k) hit |= (element<E>(w, k) >= from ? 1u : 0u) << k;
+  return hit;
+}
+
+// The logit of a cut key; the lowest finite one for "no cut".
+__device__ __forceinline__ float logit_of(unsigned long long cut) {
+  if (cut == ~0ull) return -FLT_MAX;
+  const unsigned int o = ~static_cast<unsigned int>(cut >> 22);
+  return __uint_as_float((o >> 31) ? o & 0x7fffffffu : ~o);
+}
+
 // What every rank of a cluster publishes to all.
 struct Exchange {
-  float max[kMaxCS], tau[kMaxCS];
-  int odd[kMaxCS], listed[kMaxCS];                          // listed: -1 when the list overflowed
+  float max[kMaxCS], tau[kMaxCS];  // tau: sum of the warps' order statistics, taus of them
+  int taus[kMaxCS], listed[kMaxCS];                         // listed: -1 when a thread's list overflowed
   unsigned long long sum[kMaxCS], listed_sum[kMaxCS];
   unsigned long long mass[kMaxCS], count[kMaxCS];
 };
@@ -239,11 +287,36 @@ struct Shared {
   int sel[4];
 };
 
+// 256 bins of weights, kept as 32-bit parts so that shared memory adds them
+// without a loop, and of counts.
+struct Bins {
+  unsigned int part[4][256], count[256];
+  unsigned long long sum[256];  // of the cluster
+  unsigned int all[256];
+};
+template <int kParts>  // parts of 20 bits (a list) or of 11 (a slice)
+__device__ __forceinline__ void bin_add(Bins* h, unsigned int at, unsigned long long w) {
+  constexpr int kBits = kParts == 2 ? 20 : 11;
+#pragma unroll
+  for (int i = 0; i < kParts; ++i) {
+    const unsigned int x = static_cast<unsigned int>(w >> (i * kBits)) & (i == kParts - 1 ? ~0u : (1u << kBits) - 1u);
+    if (x) atomicAdd(&h->part[i][at], x);
+  }
+  atomicAdd(&h->count[at], 1u);
+}
+template <int kParts>
+__device__ __forceinline__ unsigned long long bin_value(const Bins* h, unsigned int at) {
+  constexpr int kBits = kParts == 2 ? 20 : 11;
+  unsigned long long v = 0;
+#pragma unroll
+  for (int i = 0; i < kParts; ++i) v += static_cast<unsigned long long>(h->part[i][at]) << (i * kBits);
+  return v;
+}
+
 struct Ctx {
   Shared* sh;
-  unsigned long long* hist;  // [256] weights, then 256 counts (32-bit)
+  Bins* bins;
   int C, rank;
-  __device__ __forceinline__ unsigned int* counts() const { return reinterpret_cast<unsigned int*>(hist + 256); }
   __device__ __forceinline__ void sync() const {
     if (C == 1) {
       __syncthreads();
@@ -255,6 +328,11 @@ struct Ctx {
   template <typename T>
   __device__ __forceinline__ T* at(T* p, int r) const {
     return C == 1 ? p : cg::this_cluster().map_shared_rank(p, r);
+  }
+  __device__ __forceinline__ void clear() const {
+    unsigned int* x = &bins->part[0][0];
+    for (int i = threadIdx.x; i < 5 * 256; i += kThreadsS) x[i] = 0;
+    if (threadIdx.x == 0) sh->n_few = 0;
   }
 };
 
@@ -269,14 +347,34 @@ __device__ __forceinline__ unsigned long long block_sum(unsigned long long v, un
   return t;
 }
 
-// One warp: the first of 256 bins (by the running sum of hist) to pass rem.
-// Leaves the bin, what is left of rem inside it and its count in `sh`.
-__device__ __forceinline__ void crossing_bin(const Ctx& c, unsigned long long rem) {
+// Two sums at once.
+__device__ __forceinline__ void block_sum2(unsigned long long a, unsigned long long b, Shared& sh,
+                                           unsigned long long* sa, unsigned long long* sb) {
+  a = warp_sum_u64(a);
+  b = warp_sum_u64(b);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) {
+    sh.part[threadIdx.x >> 5] = a;
+    sh.part2[threadIdx.x >> 5] = b;
+  }
+  __syncthreads();
+  *sa = *sb = 0;
+#pragma unroll
+  for (int w = 0; w < kWarpsS; ++w) {
+    *sa += sh.part[w];
+    *sb += sh.part2[w];
+  }
+}
+
+// One warp: the first of 256 bins (by the running sum of value(bin)) to pass
+// rem.  Leaves the bin, what is left of rem inside it and its count in `sh`.
+template <typename F>
+__device__ __forceinline__ void crossing_bin(const Ctx& c, unsigned long long rem, F value) {
   const int lane = threadIdx.x & 31;
   unsigned long long h[8], mine = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    h[i] = c.hist[lane * 8 + i];
+    h[i] = value(lane * 8 + i);
     mine += h[i];
   }
   unsigned long long before = warp_scan_u64(mine, lane) - mine;
@@ -284,10 +382,15 @@ __device__ __forceinline__ void crossing_bin(const Ctx& c, unsigned long long re
   const int owner = hit ? __ffs(hit) - 1 : 31;
   if (lane == owner) {
     int b = 0;
-    while (b < 7 && before + h[b] <= rem) before += h[b++];
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+      if (b == i && before + h[i] <= rem) {
+        before += h[i];
+        b = i + 1;
+      }
     c.sh->sel[0] = lane * 8 + b;
     c.sh->rem = rem >= before ? rem - before : 0;
-    c.sh->bin_count = c.counts()[lane * 8 + b];
+    c.sh->bin_count = c.bins->count[lane * 8 + b];
   }
 }
 
@@ -316,26 +419,29 @@ __device__ __forceinline__ int bin_shift(unsigned long long span) {
 
 // The crossing key over the listed elements, which the block's threads hold
 // (key, and weight 0 for those outside the set).  Keys lie in [lo, hi].
+// kCount: every weight is 1.
+template <bool kCount>
 __device__ unsigned long long list_crossing(const Ctx& c, const unsigned long long (&key)[kPerThread],
                                             const unsigned long long (&w)[kPerThread], unsigned long long lo,
                                             unsigned long long hi, unsigned long long rem) {
   int shift = bin_shift(hi - lo);
   for (;;) {
     __syncthreads();
-    c.hist[threadIdx.x] = 0;
-    c.counts()[threadIdx.x] = 0;
-    if (threadIdx.x == 0) c.sh->n_few = 0;
+    c.clear();
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kPerThread; ++i) {
       const unsigned long long at = (key[i] - lo) >> shift;
       if (w[i] && key[i] >= lo && at < 256) {
-        atomicAdd(&c.hist[at], w[i]);
-        atomicAdd(&c.counts()[at], 1u);
+        if (kCount) atomicAdd(&c.bins->count[at], 1u);
+        else bin_add<2>(c.bins, static_cast<unsigned int>(at), w[i]);
       }
     }
     __syncthreads();
-    if (threadIdx.x < 32) crossing_bin(c, rem);
+    if (threadIdx.x < 32)
+      crossing_bin(c, rem, [&](int b) -> unsigned long long {
+        return kCount ? c.bins->count[b] : bin_value<2>(c.bins, b);
+      });
     __syncthreads();
     rem = c.sh->rem;
     lo += static_cast<unsigned long long>(c.sh->sel[0]) << shift;
@@ -361,13 +467,17 @@ __device__ unsigned long long list_crossing(const Ctx& c, const unsigned long lo
   return c.sh->lo;
 }
 
-// The same over the cluster's slices; measure(index, x) is an element's
-// weight.  Every rank gets the key.
-template <typename E, bool kStaged, typename F>
-__device__ unsigned long long slice_crossing(const Ctx& c, const Slice<E, kStaged>& sl, unsigned long long lo,
-                                             unsigned long long hi, unsigned long long rem, F measure) {
+// The crossing cut key over the cluster's slices, for rows whose kept set
+// does not lie in the list; measure(index, x) is an element's weight.  The
+// first bins are sixths of t, which spreads a row's elements over them; the
+// following ones divide the crossing bin's keys.  Every rank gets the key.
+template <typename E, bool kStaged, bool kCount, typename F>
+__device__ unsigned long long slice_crossing(const Ctx& c, const Slice<E, kStaged>& sl, float M, float s,
+                                             unsigned long long rem, F measure) {
   constexpr int VEC = Staged<E>::kVec;
-  auto sweep = [&](auto use) {
+  auto bin_of = [&](float x) { return min(255, static_cast<int>(fmaxf((x - M) * s, -64.f) * -6.f)); };
+  // use(index, x) of every element in [from, to]
+  auto sweep = [&](float from, float to, auto use) {
     for (int r = 0; r < sl.rounds(); ++r)
       for (int i = 0; i < sl.width; ++i) {
         const int v = sl.vec(r, i);
@@ -376,52 +486,75 @@ __device__ unsigned long long slice_crossing(const Ctx& c, const Slice<E, kStage
 #pragma unroll
         for (int k = 0; k < VEC; ++k) {
           const float x = element<E>(w, k);
-          use(sl.first + v * VEC + k, x);
+          if (x >= from && x <= to) use(sl.first + v * VEC + k, x);
         }
       }
   };
-  int shift = bin_shift(hi - lo);
+  int shift = -1, bin = 0;  // -1: bins of t
+  unsigned long long lo = 0;
+  float from = -INFINITY, to = INFINITY;
   for (;;) {
-    c.sync();  // the bins that other ranks read are free
-    c.hist[threadIdx.x] = 0;
-    c.counts()[threadIdx.x] = 0;
-    if (threadIdx.x == 0) c.sh->n_few = 0;
+    c.sync();  // what other ranks read is free
+    c.clear();
     __syncthreads();
-    sweep([&](unsigned int j, float x) {
-      const unsigned long long key = cut_key(x, j);
-      const unsigned long long at = (key - lo) >> shift;
-      if (key >= lo && at < 256) {
+    sweep(from, to, [&](unsigned int j, float x) {
+      unsigned int at = bin_of(x);
+      if (shift >= 0) {
+        const unsigned long long key = cut_key(x, j), d = (key - lo) >> shift;
+        if (static_cast<int>(at) != bin || key < lo || d > 255) return;
+        at = static_cast<unsigned int>(d);
+      }
+      if (kCount) {
+        atomicAdd(&c.bins->count[at], 1u);
+      } else {
         const unsigned long long w = measure(j, x);
-        if (w) {
-          atomicAdd(&c.hist[at], w);
-          atomicAdd(&c.counts()[at], 1u);
-        }
+        if (w) bin_add<4>(c.bins, at, w);
       }
     });
     c.sync();
-    unsigned long long w = 0;
-    unsigned int n = 0;
-    for (int r = 0; r < c.C; ++r) {
-      w += c.at(c.hist, r)[threadIdx.x];
-      n += c.at(c.counts(), r)[threadIdx.x];
+    if (threadIdx.x < 256) {
+      unsigned long long w = 0;
+      unsigned int n = 0;
+      for (int r = 0; r < c.C; ++r) {
+        const Bins* h = c.at(c.bins, r);
+        n += h->count[threadIdx.x];
+        if (!kCount) w += bin_value<4>(h, threadIdx.x);
+      }
+      c.bins->sum[threadIdx.x] = kCount ? n : w;
+      c.bins->all[threadIdx.x] = n;
     }
-    c.sync();  // every rank has read every rank's bins
-    c.hist[threadIdx.x] = w;
-    c.counts()[threadIdx.x] = n;
     __syncthreads();
-    if (threadIdx.x < 32) crossing_bin(c, rem);
+    if (threadIdx.x < 32) crossing_bin(c, rem, [&](int b) { return c.bins->sum[b]; });
     __syncthreads();
     rem = c.sh->rem;
-    lo += static_cast<unsigned long long>(c.sh->sel[0]) << shift;
+    const int b = c.sh->sel[0];
+    const bool few = c.bins->all[b] <= 32;
+    if (shift < 0) {
+      // the bin's logits, with room for the roundings of t and of these bounds
+      bin = b;
+      const float unit = __fdiv_rn(1.f, 6.f * s);
+      to = fminf(M, M - (b - 0.01f) * unit);
+      to = fminf(M, to + fabsf(to) * 4.8e-7f);
+      from = b == 255 ? -INFINITY : M - (b + 1.01f) * unit;
+      from -= b == 255 ? 0.f : fabsf(from) * 4.8e-7f;
+      lo = cut_key(to, 0);
+      shift = bin_shift(cut_key(from, 0x3fffff) - lo);
+      if (few) {
+        shift = 54;  // all keys of the bin at once
+        break;
+      }
+      continue;
+    }
+    lo += static_cast<unsigned long long>(b) << shift;
     if (shift == 0) return lo;
-    if (c.sh->bin_count <= 32) break;
+    if (few) break;
     shift = shift > 8 ? shift - 8 : 0;
   }
   Shared* zero = c.at(c.sh, 0);
-  sweep([&](unsigned int j, float x) {
+  sweep(from, to, [&](unsigned int j, float x) {
     const unsigned long long key = cut_key(x, j);
-    if (key >= lo && (key - lo) >> shift == 0) {
-      const unsigned long long w = measure(j, x);
+    if (bin_of(x) == bin && key >= lo && (key - lo) >> shift == 0) {
+      const unsigned long long w = kCount ? 1ull : measure(j, x);
       if (w) {
         const unsigned int at = atomicAdd(&zero->n_few, 1u);
         if (at < 32) {
@@ -461,7 +594,8 @@ __device__ void group_sums(const Ctx& c, const Slice<E, kStaged>& sl, unsigned l
     g = warp_sum_u64(g);
     if (lane == 0) groups[r * kWarpsS + warp] = g;
   }
-  const unsigned long long t = block_sum(mine, c.sh->part), k = block_sum(n, c.sh->part2);
+  unsigned long long t, k;
+  block_sum2(mine, n, *c.sh, &t, &k);
   if (threadIdx.x < c.C) {
     *c.at(&c.sh->x.mass[c.rank], threadIdx.x) = t;
     *c.at(&c.sh->x.count[c.rank], threadIdx.x) = k;
@@ -562,10 +696,16 @@ __device__ __forceinline__ float warp_sort(float x, int lane) {
   return x;
 }
 
-// Which of a warp's 32 sorted maxima bounds the list, by cluster size: about
-// 300 to 900 logits of a row lie above the largest warp's (counted on normal
-// and Zipf-shifted rows; a list of 1024 overflows on none of them).
-__device__ __forceinline__ int tau_lane(int C) { return C == 1 ? 1 : C == 2 ? 4 : C == 4 ? 8 : 16; }
+// How many logits the list should hold, and which of a warp's 32 sorted
+// maxima says so: with m logits listed among T threads a thread holds none
+// with probability e^(-m/T), so the threshold is that quantile of the
+// maxima.  Averaged over the row's warps it lists m within a tenth on normal
+// rows, up to 1.5 m on Zipf-shifted ones (counted).
+__device__ __forceinline__ int tau_lane(const Settings& set, int V, int C) {
+  const float m = set.k < V ? fminf(1.25f * set.k + 64.f, 700.f) : 640.f;
+  const float below = ex2(-1.44269504f * m / (kThreadsS * C));
+  return min(31, max(0, static_cast<int>(32.f * below)));
+}
 
 // A vector of the filtered row.  Most elements fail the comparison with the
 // cut's logit; the others are tested exactly.
@@ -596,7 +736,7 @@ __device__ __forceinline__ void write_kept(const SampleArgs& a, int row, int fir
 }
 
 template <typename E, bool kStaged>
-__global__ void __launch_bounds__(kThreadsS, 3)
+__global__ void __launch_bounds__(kThreadsS, 2)
 filtered_sample_kernel(const SampleArgs a, int nvec, int nvs, bool aligned_in, bool aligned_out, float mz) {
   constexpr int VEC = Staged<E>::kVec;
   using raw = typename E::raw;
@@ -612,7 +752,7 @@ filtered_sample_kernel(const SampleArgs a, int nvec, int nvs, bool aligned_in, b
   uint2* list = reinterpret_cast<uint2*>(dyn + (kStaged ? nvs : 0));          // (x, index)
   unsigned long long* groups = reinterpret_cast<unsigned long long*>(list);   // shares the list's memory
   uint16_t* deep = reinterpret_cast<uint16_t*>(list + kList);                 // [kDepth][threads]
-  c.hist = reinterpret_cast<unsigned long long*>(list + kList);               // shares it
+  c.bins = reinterpret_cast<Bins*>(list + kList);                             // shares it
   const int lgC = __ffs(c.C) - 1;
   const int row = static_cast<int>(blockIdx.x >> lgC);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -656,22 +796,7 @@ filtered_sample_kernel(const SampleArgs a, int nvec, int nvs, bool aligned_in, b
 
   // ---- 1. the row's maximum and the list's threshold ----------------------
   bool landed = true;
-  float mine = -INFINITY;
-  bool odd = false;
-  auto take = [&](const uint4& w) {
-#pragma unroll
-    for (int k = 0; k < VEC / 2; ++k) {
-      if constexpr (VEC == 8) {
-        const uint32_t p = k == 0 ? w.x : k == 1 ? w.y : k == 2 ? w.z : w.w;
-        mine = fmaxf(mine, fmaxf(bf16_lo(p), bf16_hi(p)));
-        odd |= isnan(bf16_lo(p)) || isnan(bf16_hi(p));
-      } else {
-        const float x = element<E>(w, 2 * k), y = element<E>(w, 2 * k + 1);
-        mine = fmaxf(mine, fmaxf(x, y));
-        odd |= isnan(x) || isnan(y);
-      }
-    }
-  };
+  Peak<E> peak;
   if (bulk) {
     for (int k = 0; k < nch; ++k) {
       if (!mbar_wait_sleep(&bars[k], 0u)) {
@@ -679,33 +804,46 @@ filtered_sample_kernel(const SampleArgs a, int nvec, int nvs, bool aligned_in, b
         break;
       }
       const int stop = min((k + 1) * kChunkS, sl.nv);
-      for (int v = k * kChunkS + tid; v < stop; v += kThreadsS) take(slice[v]);
+#pragma unroll 2
+      for (int v = k * kChunkS + tid; v < stop; v += kThreadsS) peak.take(slice[v]);
     }
   } else {
-    for (int v = tid; v < sl.nv; v += kThreadsS) take(sl.at(v));
+    for (int v = tid; v < sl.nv; v += kThreadsS) peak.take(sl.at(v));
   }
+  const float mine = peak.value();
+  const bool odd = __any_sync(0xffffffffu, isnan(mine));
   const float sorted = warp_sort(mine, lane);
-  const bool any_odd = __any_sync(0xffffffffu, odd);
-  if (lane == 31) sh.wmax[warp] = any_odd ? INFINITY : sorted;
-  if (lane == tau_lane(c.C)) sh.wtau[warp] = sorted;
+  const float order = __shfl_sync(0xffffffffu, sorted, tau_lane(set, a.V, c.C));
+  if (lane == 31) {
+    sh.wmax[warp] = odd ? INFINITY : sorted;
+    sh.wtau[warp] = order;
+  }
   const int timeout = __syncthreads_or(!landed);
   if (c.C > 1) cluster_wait();  // every block of the cluster has started
   if (tid < c.C) {
-    float m = -INFINITY, t = -INFINITY;
+    float m = -INFINITY, t = 0.f;
+    int n = 0;
 #pragma unroll
     for (int w = 0; w < kWarpsS; ++w) {
       m = fmaxf(m, sh.wmax[w]);
-      t = fmaxf(t, sh.wtau[w]);
+      if (sh.wtau[w] > -INFINITY) {
+        t += sh.wtau[w];
+        ++n;
+      }
     }
     *c.at(&sh.x.max[c.rank], tid) = m;
     *c.at(&sh.x.tau[c.rank], tid) = t;
+    *c.at(&sh.x.taus[c.rank], tid) = n;
   }
   c.sync();
-  float M = -INFINITY, tau = -INFINITY;
+  float M = -INFINITY, tau = 0.f;
+  int taus = 0;
   for (int r = 0; r < c.C; ++r) {
     M = fmaxf(M, sh.x.max[r]);
-    tau = fmaxf(tau, sh.x.tau[r]);
+    tau += sh.x.tau[r];
+    taus += sh.x.taus[r];
   }
+  tau = taus ? fminf(tau / taus, M) : -INFINITY;
   M += 0.f;
   const bool good = M > -INFINITY && M < INFINITY;
   Kept kept;
@@ -715,10 +853,10 @@ filtered_sample_kernel(const SampleArgs a, int nvec, int nvs, bool aligned_in, b
   const float p_clamped = fminf(fmaxf(set.top_p, 0.f), 0.99999994f);
   unsigned long long S = 0, count = 0;
   int token = -1;  // on the rank that finds it
-  float x_token = 0.f;
 
+  float edge = -FLT_MAX;  // the cut's logit
   auto weigh = [&](unsigned int j, float x) -> unsigned long long {
-    if (cut_key(x, j) > kept.cut) return 0ull;
+    if (!(x >= edge) || cut_key(x, j) > kept.cut) return 0ull;
     const unsigned long long w = weight(x, M, s);
     return w >= kept.least ? w : 0ull;
   };
@@ -736,12 +874,9 @@ filtered_sample_kernel(const SampleArgs a, int nvec, int nvs, bool aligned_in, b
       int n = 0;
       unsigned int vectors = 0;
       auto put = [&](const uint4& w, int v) {
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) {
-          if (element<E>(w, k) >= from) {
-            if (n < kDepth) deep[n * kThreadsS + tid] = static_cast<uint16_t>(v * VEC + k);
-            ++n;
-          }
+        for (uint32_t hit = at_least<E>(w, from); hit; hit &= hit - 1) {
+          if (n < kDepth) deep[n * kThreadsS + tid] = static_cast<uint16_t>(v * VEC + __ffs(hit) - 1);
+          ++n;
         }
       };
       const bool lists = kStaged && !timeout;
@@ -784,14 +919,13 @@ filtered_sample_kernel(const SampleArgs a, int nvec, int nvs, bool aligned_in, b
         for (int i = 0; i < n; ++i) {
           const int e = deep[i * kThreadsS + tid];
           const float x = staged_elem<E>(slice, e);
-          const unsigned long long w = weight(x, M, s);
-          lw += w >= kept.least ? w : 0ull;
+          if (whole) lw += weight(x, M, s);  // the sum decides whether the list covers top-p
           if (base + before + i < kList)
             to[base + before + i] = make_uint2(__float_as_uint(x), static_cast<unsigned int>(sl.first + e));
         }
       }
-      const unsigned long long zs = block_sum(value_of(z, vectors * VEC), sh.part);
-      lw = block_sum(lw, sh.part2);
+      unsigned long long zs = 0;
+      if (whole) block_sum2(value_of(z, vectors * VEC), lw, sh, &zs, &lw);
       if (tid < c.C) {
         *c.at(&sh.x.sum[c.rank], tid) = zs;
         *c.at(&sh.x.listed_sum[c.rank], tid) = lw;
@@ -839,7 +973,7 @@ filtered_sample_kernel(const SampleArgs a, int nvec, int nvs, bool aligned_in, b
           }
           const unsigned long long klo = cut_key(M, 0), khi = cut_key(from, 0x3fffff);
           if (has_k && set.k < listed) {
-            kept.cut = list_crossing(c, key, one, klo, khi, set.k - 1);
+            kept.cut = list_crossing<true>(c, key, one, klo, khi, set.k - 1);
 #pragma unroll
             for (int i = 0; i < kPerThread; ++i)
               if (key[i] > kept.cut) w[i] = 0;
@@ -849,7 +983,7 @@ filtered_sample_kernel(const SampleArgs a, int nvec, int nvs, bool aligned_in, b
 #pragma unroll
             for (int i = 0; i < kPerThread; ++i) total += w[i];
             total = whole ? Z : block_sum(total, sh.part);
-            kept.cut = list_crossing(c, key, w, klo, khi, max(1ull, draw_threshold(p_clamped, total)) - 1);
+            kept.cut = list_crossing<false>(c, key, w, klo, khi, max(1ull, draw_threshold(p_clamped, total)) - 1);
 #pragma unroll
             for (int i = 0; i < kPerThread; ++i)
               if (key[i] > kept.cut) w[i] = 0;
@@ -861,8 +995,7 @@ filtered_sample_kernel(const SampleArgs a, int nvec, int nvs, bool aligned_in, b
             n_kept += w[i] > 0;
             if (w[i] && key[i] > top) top = key[i];
           }
-          S = block_sum(t, sh.part);
-          count = block_sum(n_kept, sh.part2);
+          block_sum2(t, n_kept, sh, &S, &count);
           if (a.filtered) {  // the largest key kept: a bound for rows cut by min-p alone
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -873,7 +1006,7 @@ filtered_sample_kernel(const SampleArgs a, int nvec, int nvs, bool aligned_in, b
             for (int x = 0; x < kWarpsS; ++x) top = max(top, sh.part[x]);
             kept.cut = top;
           }
-          token = static_cast<int>(list_crossing(c, id, w, 0, a.V - 1, draw_threshold(u, S)));
+          token = static_cast<int>(list_crossing<false>(c, id, w, 0, a.V - 1, draw_threshold(u, S)));
 #pragma unroll
           for (int i = 0; i < kPerThread; ++i)
             if (w[i] && id[i] == static_cast<unsigned long long>(token)) sh.part2[0] = w[i];
@@ -891,10 +1024,12 @@ filtered_sample_kernel(const SampleArgs a, int nvec, int nvs, bool aligned_in, b
         }
       } else {
         // ---- the cuts over the slices ----
-        const unsigned long long klo = cut_key(M, 0), kall = (0xffffffffull << 22) | 0x3fffff;
-        const unsigned long long khi = cut_key(floor, 0x3fffff);
+        auto cut_at = [&](unsigned long long key) {
+          kept.cut = key;
+          edge = logit_of(key);
+        };
         if (has_k)
-          kept.cut = slice_crossing<E, kStaged>(c, sl, klo, kall, set.k - 1, [](unsigned int, float) { return 1ull; });
+          cut_at(slice_crossing<E, kStaged, true>(c, sl, M, s, set.k - 1, weigh));
         if (has_p) {
           unsigned long long total = Z;
           if (!(whole && lists)) {
@@ -907,7 +1042,7 @@ filtered_sample_kernel(const SampleArgs a, int nvec, int nvs, bool aligned_in, b
               return t;
             }, &total, &count);
           }
-          kept.cut = slice_crossing<E, kStaged>(c, sl, klo, khi, max(1ull, draw_threshold(p_clamped, total)) - 1, weigh);
+          cut_at(slice_crossing<E, kStaged, false>(c, sl, M, s, max(1ull, draw_threshold(p_clamped, total)) - 1, weigh));
         }
       }
     }
@@ -939,7 +1074,7 @@ filtered_sample_kernel(const SampleArgs a, int nvec, int nvs, bool aligned_in, b
       }, &S, &count);
       token = group_draw<E, kStaged>(c, sl, groups, draw_threshold(u, S), weigh);
       if (token >= 0) {  // on the rank that holds it
-        x_token = kStaged ? staged_elem<E>(slice, token - sl.first) : load_one<E>(sl.global, token - sl.first);
+        const float x_token = kStaged ? staged_elem<E>(slice, token - sl.first) : load_one<E>(sl.global, token - sl.first);
         if (tid == 0) {
           a.tokens[row] = token;
           if (a.p) a.p[row] = __fdiv_rn(__ull2float_rn(weight(x_token, M, s)), __ull2float_rn(S));
@@ -955,10 +1090,8 @@ filtered_sample_kernel(const SampleArgs a, int nvec, int nvs, bool aligned_in, b
 
   // ---- the filtered row ----
   if (a.filtered) {
-    const unsigned int theta = ~static_cast<unsigned int>(kept.cut >> 22);  // as falling() orders
-    float edge = __uint_as_float((theta >> 31) ? theta & 0x7fffffffu : ~theta);
-    if (kept.cut == ~0ull) edge = -FLT_MAX;
-    if (!good) edge = INFINITY, kept.cut = 0;
+    edge = good ? logit_of(kept.cut) : INFINITY;
+    if (!good) kept.cut = 0;
     for (int v = tid; v < sl.nv; v += kThreadsS)
       write_kept<E>(a, row, sl.first, v, sl.at(v), aligned_out && sl.first + (v + 1) * VEC <= a.V, kept, edge, M, s);
   }
@@ -982,7 +1115,7 @@ Shape shape_of(int V, bool bf16) {
   s.nvec = (V + (bf16 ? 8 : 4) - 1) / (bf16 ? 8 : 4);
   for (s.C = 1; s.C <= kMaxCS; s.C *= 2) {
     s.nvs = (s.nvec + s.C - 1) / s.C;
-    if (s.nvs * 16ll <= kSliceBytesS) {
+    if (s.nvs * 16ll <= (s.C == kMaxCS ? kMaxSliceS : kSliceBytesS)) {
       s.staged = true;
       return s;
     }
@@ -994,7 +1127,7 @@ Shape shape_of(int V, bool bf16) {
 }
 
 constexpr size_t kTailBytes = kList * 8 + kDepth * kThreadsS * 2;
-static_assert(kDepth * kThreadsS * 2 >= 256 * 12, "the bins fit the threads' lists");
+static_assert(kDepth * kThreadsS * 2 >= static_cast<int>(sizeof(Bins)), "the bins fit the threads' lists");
 
 template <typename E, bool kStaged>
 cudaError_t launch(const SampleArgs& a, const Shape& s, cudaStream_t stream) {
@@ -1026,7 +1159,7 @@ size_t filtered_sample_workspace(int R, int V, bool bf16) {
 }
 
 cudaError_t filtered_sample_prepare() {
-  const int bytes = static_cast<int>(kSliceBytesS + kTailBytes);
+  const int bytes = static_cast<int>(kMaxSliceS + kTailBytes);
   cudaError_t e = cudaFuncSetAttribute(filtered_sample_kernel<BF16, true>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e == cudaSuccess)
