@@ -8,22 +8,29 @@
 // a threshold".  The key is (descending logit, ascending index) for the cuts
 // and the index for the draw.
 //
-// One cluster of C blocks per row, each block's slice of the row in shared
-// memory (TMA bulk copies), so the row crosses HBM once.
-//   1. As the copies land every thread keeps its largest logit.  The cluster
-//      exchanges the row's maximum and a threshold tau: a low order statistic
-//      of the threads' maxima, above which a few hundred logits lie.
-//   2. One sweep over the slice sums every weight (only when the cuts need the
-//      whole row's sum: top-p alone, or no cut at all) and lists the logits
-//      from tau up.  What a cut keeps nearly always lies in that list: the k
-//      largest, what min-p leaves, the share of the mass that top-p asks for.
-//      Whether it does is known exactly from counts and sums.
-//   3. The list goes to one block, which makes the cuts and the draw on it:
-//      a 256-bin histogram of weights over the key's range, one warp for the
-//      at most 32 candidates of the crossing bin.
-// A row without cuts draws from the sweep's sums by 32-vector group.  A row
-// whose kept set does not lie in the list (flat distributions, a large k)
-// takes the same cuts by histograms over the slices, level by level.
+// Three kernels, the last two small:
+//   row     one cluster of C blocks per row, each block's slice in shared
+//           memory (TMA bulk copies), so the row crosses HBM once.  As the
+//           copies land every thread keeps its largest logit; the cluster
+//           exchanges the row's maximum and a threshold tau, a quantile of
+//           the threads' maxima above which some hundred logits lie.  One
+//           sweep over the slice lists the logits from tau up and, when
+//           top-p asks for a share of the whole row's mass, sums
+//           approximate weights with a bound on their error.  What a cut
+//           keeps nearly always lies in the list -- the k largest, what
+//           min-p leaves, the share that top-p asks for -- and whether it
+//           does is known from counts and sums.
+//   finish  one small block per listed row makes the cuts and the draw on the
+//           list: 256 bins of weights over the key's range, one warp for the
+//           at most 32 candidates of the crossing bin.  The cut that the
+//           approximate sum gives is checked against the sum's bounds; in the
+//           rare row between them the exact sum is taken.
+//   write   the filtered rows, streaming.
+// Rows without cuts are drawn by the row kernel from exact sums by 32-vector
+// group.  A row whose kept set does not lie in the list (flat distributions,
+// a large k) takes the same cuts there by bins over the slices.  When every
+// row's cluster fits the GPU at once, the row kernel does the other two's
+// work as well: latency counts then, and there is no next row to overlap.
 #include <cooperative_groups.h>
 
 #include <cfloat>
@@ -38,18 +45,22 @@ namespace cg = cooperative_groups;
 namespace specv {
 namespace {
 
-constexpr int kThreadsS = 512;
+constexpr int kThreadsS = 256;          // row kernel
 constexpr int kWarpsS = kThreadsS / 32;
+constexpr int kThreadsB = 128;          // finish kernel
 constexpr int kMaxCS = 8;               // blocks of a cluster
-constexpr int kDepth = 12;              // listed logits a thread holds
 constexpr int kList = 1024;             // listed logits of a row
-constexpr int kPerThread = kList / kThreadsS;
 constexpr int kGroups = kList / kWarpsS;  // rounds with group sums of their own (they share the list's memory)
 constexpr long long kSliceBytesS = 65024;     // a slice, while more blocks can share the row
 constexpr long long kMaxSliceS = 128 * 1024;  // a slice of the largest cluster (65536 bf16: 16-bit places)
 constexpr int kChunkS = 1024;           // vectors per bulk copy
 constexpr int kMaxChunksS = 8;
 static_assert(kMaxSliceS / 16 <= kChunkS * kMaxChunksS, "bulk copies of a slice");
+constexpr int kVectorsS = kMaxSliceS / 16 / kThreadsS;  // vectors of a slice a thread sweeps at most
+// Blocks of the row kernel that run at once (two an SM, 152 SMs): rows in
+// clusters of no more than these are finished in it.
+constexpr int kFusedBlocks = 304;
+constexpr int kRowsAtOnce = 8192;       // rows listed in the workspace at a time
 
 // 2^f on [-1/2, 1/2] times 2^40: 1 + f (c1 + f (c2 + ...)), a minimax fit of
 // the relative error (9.2e-8; 1.9e-7 with the roundings of every operation).
@@ -260,6 +271,24 @@ __device__ __forceinline__ uint32_t at_least(const uint4& w, float from) {
   return hit;
 }
 
+// The approximate mass of a vector, sum of 2^t by ex2.approx.
+template <typename E>
+__device__ __forceinline__ float vector_mass(const uint4& w, float M, float s) {
+  constexpr int NP = Staged<E>::kVec / 2;
+  float2 x[NP];
+  unpack_pairs<E>(w, x);
+#pragma unroll
+  for (int k = 0; k < NP; ++k) {
+    const float2 d = fadd2(x[k], both(-M));
+    x[k] = make_float2(ex2(d.x * s), ex2(d.y * s));
+  }
+#pragma unroll
+  for (int h = NP / 2; h > 0; h >>= 1)
+#pragma unroll
+    for (int k = 0; k < h; ++k) x[k] = fadd2(x[k], x[k + h]);
+  return x[0].x + x[0].y;
+}
+
 // The logit of a cut key; the lowest finite one for "no cut".
 __device__ __forceinline__ float logit_of(unsigned long long cut) {
   if (cut == ~0ull) return -FLT_MAX;
@@ -270,21 +299,19 @@ __device__ __forceinline__ float logit_of(unsigned long long cut) {
 // What every rank of a cluster publishes to all.
 struct Exchange {
   float max[kMaxCS], tau[kMaxCS];  // tau: sum of the warps' order statistics, taus of them
-  int taus[kMaxCS], listed[kMaxCS];                         // listed: -1 when a thread's list overflowed
+  int taus[kMaxCS], listed[kMaxCS];
   unsigned long long sum[kMaxCS], listed_sum[kMaxCS];
   unsigned long long mass[kMaxCS], count[kMaxCS];
 };
 
+// Scratch of block-wide steps.
 struct Shared {
-  Exchange x;
-  unsigned long long part[kWarpsS], part2[kWarpsS];
-  float wmax[kWarpsS], wtau[kWarpsS];
+  unsigned long long part[16], part2[16];  // a warp each
   unsigned long long few_key[32], few_w[32];
-  unsigned long long rem, lo, cut;
-  unsigned int n_few, bin_count;
-  unsigned int list_n;
-  int scan[kWarpsS];
-  int sel[4];
+  unsigned long long rem, lo, cut, w_token;
+  unsigned int n_few, bin_count, list_n;
+  int sel[2];
+  float wmax[16], wtau[16];
 };
 
 // 256 bins of weights, kept as 32-bit parts so that shared memory adds them
@@ -316,6 +343,7 @@ __device__ __forceinline__ unsigned long long bin_value(const Bins* h, unsigned 
 struct Ctx {
   Shared* sh;
   Bins* bins;
+  Exchange* x;
   int C, rank;
   __device__ __forceinline__ void sync() const {
     if (C == 1) {
@@ -329,25 +357,20 @@ struct Ctx {
   __device__ __forceinline__ T* at(T* p, int r) const {
     return C == 1 ? p : cg::this_cluster().map_shared_rank(p, r);
   }
+  // kParts of the bins' parts and the counts to zero.
+  template <int NT, int kParts>
   __device__ __forceinline__ void clear() const {
-    unsigned int* x = &bins->part[0][0];
-    for (int i = threadIdx.x; i < 5 * 256; i += kThreadsS) x[i] = 0;
+    for (int i = threadIdx.x; i < 256; i += NT) {
+#pragma unroll
+      for (int k = 0; k < kParts; ++k) bins->part[k][i] = 0;
+      bins->count[i] = 0;
+    }
     if (threadIdx.x == 0) sh->n_few = 0;
   }
 };
 
-__device__ __forceinline__ unsigned long long block_sum(unsigned long long v, unsigned long long* part) {
-  v = warp_sum_u64(v);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-  __syncthreads();
-  unsigned long long t = 0;
-#pragma unroll
-  for (int w = 0; w < kWarpsS; ++w) t += part[w];
-  return t;
-}
-
-// Two sums at once.
+// Two block-wide sums at once.
+template <int NT>
 __device__ __forceinline__ void block_sum2(unsigned long long a, unsigned long long b, Shared& sh,
                                            unsigned long long* sa, unsigned long long* sb) {
   a = warp_sum_u64(a);
@@ -360,7 +383,7 @@ __device__ __forceinline__ void block_sum2(unsigned long long a, unsigned long l
   __syncthreads();
   *sa = *sb = 0;
 #pragma unroll
-  for (int w = 0; w < kWarpsS; ++w) {
+  for (int w = 0; w < NT / 32; ++w) {
     *sa += sh.part[w];
     *sb += sh.part2[w];
   }
@@ -420,17 +443,18 @@ __device__ __forceinline__ int bin_shift(unsigned long long span) {
 // The crossing key over the listed elements, which the block's threads hold
 // (key, and weight 0 for those outside the set).  Keys lie in [lo, hi].
 // kCount: every weight is 1.
-template <bool kCount>
-__device__ unsigned long long list_crossing(const Ctx& c, const unsigned long long (&key)[kPerThread],
-                                            const unsigned long long (&w)[kPerThread], unsigned long long lo,
+template <int NT, bool kCount>
+__device__ unsigned long long list_crossing(const Ctx& c, const unsigned long long (&key)[kList / NT],
+                                            const unsigned long long (&w)[kList / NT], unsigned long long lo,
                                             unsigned long long hi, unsigned long long rem) {
+  constexpr int kPer = kList / NT;
   int shift = bin_shift(hi - lo);
   for (;;) {
     __syncthreads();
-    c.clear();
+    c.clear<NT, kCount ? 0 : 2>();
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kPerThread; ++i) {
+    for (int i = 0; i < kPer; ++i) {
       const unsigned long long at = (key[i] - lo) >> shift;
       if (w[i] && key[i] >= lo && at < 256) {
         if (kCount) atomicAdd(&c.bins->count[at], 1u);
@@ -450,7 +474,7 @@ __device__ unsigned long long list_crossing(const Ctx& c, const unsigned long lo
     shift = shift > 8 ? shift - 8 : 0;
   }
 #pragma unroll
-  for (int i = 0; i < kPerThread; ++i)
+  for (int i = 0; i < kPer; ++i)
     if (w[i] && key[i] >= lo && (key[i] - lo) >> shift == 0) {
       const unsigned int at = atomicAdd(&c.sh->n_few, 1u);
       if (at < 32) {
@@ -495,7 +519,7 @@ __device__ unsigned long long slice_crossing(const Ctx& c, const Slice<E, kStage
   float from = -INFINITY, to = INFINITY;
   for (;;) {
     c.sync();  // what other ranks read is free
-    c.clear();
+    c.clear<kThreadsS, kCount ? 0 : 4>();
     __syncthreads();
     sweep(from, to, [&](unsigned int j, float x) {
       unsigned int at = bin_of(x);
@@ -595,16 +619,16 @@ __device__ void group_sums(const Ctx& c, const Slice<E, kStaged>& sl, unsigned l
     if (lane == 0) groups[r * kWarpsS + warp] = g;
   }
   unsigned long long t, k;
-  block_sum2(mine, n, *c.sh, &t, &k);
+  block_sum2<kThreadsS>(mine, n, *c.sh, &t, &k);
   if (threadIdx.x < c.C) {
-    *c.at(&c.sh->x.mass[c.rank], threadIdx.x) = t;
-    *c.at(&c.sh->x.count[c.rank], threadIdx.x) = k;
+    *c.at(&c.x->mass[c.rank], threadIdx.x) = t;
+    *c.at(&c.x->count[c.rank], threadIdx.x) = k;
   }
   c.sync();
   *S = *count = 0;
   for (int r = 0; r < c.C; ++r) {
-    *S += c.sh->x.mass[r];
-    *count += c.sh->x.count[r];
+    *S += c.x->mass[r];
+    *count += c.x->count[r];
   }
 }
 
@@ -618,11 +642,11 @@ __device__ int group_draw(const Ctx& c, const Slice<E, kStaged>& sl, const unsig
   int owner = c.C - 1;
   unsigned long long off = 0;
   for (int r = 0; r < c.C; ++r) {
-    if (off + c.sh->x.mass[r] > theta) {
+    if (off + c.x->mass[r] > theta) {
       owner = r;
       break;
     }
-    off += c.sh->x.mass[r];
+    off += c.x->mass[r];
   }
   if (c.rank != owner) return -1;
   if (warp == 0) {
@@ -735,26 +759,141 @@ __device__ __forceinline__ void write_kept(const SampleArgs& a, int row, int fir
   }
 }
 
+// A listed row on its way from the row kernel to the others.
+struct __align__(16) RowHead {
+  float M, from;             // largest logit, smallest listed one
+  unsigned long long Z;      // approximate mass of the row (2^-40), when top-p needs it
+  unsigned long long cut;    // kept keys go up to here (for the write kernel)
+  int listed;                // -1: the row is finished
+  int good;
+};
+
+// Bounds of the exact sum of a row's weights around the approximate one.  The
+// approximate terms are 2^t of the same t by ex2.approx (2^-22) instead of
+// the polynomial (2^-22), summed in fp32 by at most 13 additions
+// (2^-20.3), and each whole-number weight is rounded by 1/2: together
+// below 2^-19.
+__device__ __forceinline__ unsigned long long sum_slack(unsigned long long Z) { return (Z >> 19) + 1; }
+
+__device__ __forceinline__ unsigned long long share_of(float top_p, unsigned long long total) {
+  return max(1ull, draw_threshold(fminf(fmaxf(top_p, 0.f), 0.99999994f), total));
+}
+
+// Exact sum of a row's weights by one block, from global memory.
+template <typename E, int NT>
+__device__ unsigned long long row_total(const void* logits, int V, float M, float s, Shared& sh) {
+  unsigned long long t = 0, u;
+  for (int j = threadIdx.x; j < V; j += NT) t += weight(load_one<E>(logits, j), M, s);
+  block_sum2<NT>(t, 0, sh, &t, &u);
+  return t;
+}
+
+// The cuts and the draw of a covered row on its list (x, index), by one block.
+// Writes the row's outputs; returns the largest kept key.
+template <typename E, int NT>
+__device__ unsigned long long finish_row(const Ctx& c, const SampleArgs& a, const Settings& set, int row,
+                                         const uint2* list, const RowHead& head, float s, const void* logits) {
+  constexpr int kPer = kList / NT;
+  const int tid = threadIdx.x;
+  const bool has_k = set.k < a.V, has_m = set.min_p > 0.f, has_p = set.top_p < 1.f, whole = !has_k && !has_m;
+  const unsigned long long least =
+      max(1ull, __float2ull_rn(__fmul_rn(fminf(fmaxf(set.min_p, 0.f), 1.f), kScale)));
+  unsigned long long key[kPer], w[kPer], kept[kPer], id[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int e = i * NT + tid;
+    const bool in = e < head.listed;
+    const uint2 q = in ? list[e] : make_uint2(0, 0);
+    const float x = __uint_as_float(q.x);
+    key[i] = cut_key(x, q.y);
+    id[i] = q.y;
+    kept[i] = in;
+    w[i] = in ? weight(x, head.M, s) : 0ull;
+    if (w[i] < least) w[i] = 0;
+  }
+  const unsigned long long klo = cut_key(head.M, 0), khi = cut_key(head.from, 0x3fffff);
+  if (has_k && set.k < head.listed) {
+    const unsigned long long cut = list_crossing<NT, true>(c, key, kept, klo, khi, set.k - 1);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (key[i] > cut) w[i] = 0;
+  }
+  unsigned long long S, count, need = 0, least_need = 0;
+  unsigned long long total = head.Z, slack = whole ? sum_slack(total) : 0;
+  if (has_p && !whole) {
+    unsigned long long t = 0, u;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) t += w[i];
+    block_sum2<NT>(t, 0, *c.sh, &total, &u);
+  }
+  for (;;) {
+    unsigned long long cut = ~0ull;
+    if (has_p) {
+      need = share_of(set.top_p, total + slack);
+      least_need = share_of(set.top_p, total - slack);
+      cut = list_crossing<NT, false>(c, key, w, klo, khi, least_need - 1);
+    }
+    unsigned long long t = 0, n = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      kept[i] = key[i] <= cut ? w[i] : 0;
+      t += kept[i];
+      n += kept[i] > 0;
+    }
+    block_sum2<NT>(t, n, *c.sh, &S, &count);
+    // the kept mass reaches the smallest share asked for; if it reaches the
+    // largest as well, the cut is the exact sum's
+    if (!has_p || slack == 0 || S >= need) break;
+    total = row_total<E, NT>(logits, a.V, head.M, s, *c.sh);
+    slack = 0;
+  }
+  const int token = static_cast<int>(list_crossing<NT, false>(c, id, kept, 0, a.V - 1, draw_threshold(a.uniforms[row], S)));
+  unsigned long long top = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    if (kept[i] && id[i] == static_cast<unsigned long long>(token)) c.sh->w_token = kept[i];
+    if (kept[i] && key[i] > top) top = key[i];
+  }
+  if (a.filtered) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if ((tid & 31) == 0) c.sh->part[tid >> 5] = top;
+  }
+  __syncthreads();
+  if (a.filtered)
+#pragma unroll
+    for (int x = 0; x < NT / 32; ++x) top = max(top, c.sh->part[x]);
+  if (tid == 0) {
+    a.tokens[row] = token;
+    if (a.p) a.p[row] = __fdiv_rn(__ull2float_rn(c.sh->w_token), __ull2float_rn(S));
+    if (a.n_kept) a.n_kept[row] = static_cast<int>(count);
+  }
+  return top;
+}
+
 template <typename E, bool kStaged>
-__global__ void __launch_bounds__(kThreadsS, 2)
-filtered_sample_kernel(const SampleArgs a, int nvec, int nvs, bool aligned_in, bool aligned_out, float mz) {
+__global__ void __launch_bounds__(kThreadsS, 3)
+filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_in, bool aligned_out, bool split,
+                  RowHead* heads, uint2* lists, float mz) {
   constexpr int VEC = Staged<E>::kVec;
+  constexpr int kPerWord = 32 / VEC, kWords = kStaged ? kVectorsS / kPerWord : 1;
   using raw = typename E::raw;
-  extern __shared__ __align__(128) uint4 dyn[];  // slice [nvs] | list [kList] | threads' lists, later the bins
+  extern __shared__ __align__(128) uint4 dyn[];  // slice [nvs] | list, bins or group sums
   __shared__ Shared sh;
+  __shared__ Exchange ex;
   __shared__ __align__(8) unsigned long long bars[kMaxChunksS];
   cg::cluster_group cluster = cg::this_cluster();
   Ctx c;
   c.sh = &sh;
+  c.x = &ex;
   c.C = static_cast<int>(cluster.num_blocks());
   c.rank = static_cast<int>(cluster.block_rank());
   uint4* slice = dyn;
-  uint2* list = reinterpret_cast<uint2*>(dyn + (kStaged ? nvs : 0));          // (x, index)
-  unsigned long long* groups = reinterpret_cast<unsigned long long*>(list);   // shares the list's memory
-  uint16_t* deep = reinterpret_cast<uint16_t*>(list + kList);                 // [kDepth][threads]
-  c.bins = reinterpret_cast<Bins*>(list + kList);                             // shares it
+  uint2* list = reinterpret_cast<uint2*>(dyn + (kStaged ? nvs : 0));
+  unsigned long long* groups = reinterpret_cast<unsigned long long*>(list);
+  c.bins = reinterpret_cast<Bins*>(list);
   const int lgC = __ffs(c.C) - 1;
-  const int row = static_cast<int>(blockIdx.x >> lgC);
+  const int at = static_cast<int>(blockIdx.x >> lgC), row = row0 + at;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int v0 = static_cast<int>((static_cast<long long>(nvec) * c.rank) >> lgC);
   Slice<E, kStaged> sl;
@@ -762,9 +901,9 @@ filtered_sample_kernel(const SampleArgs a, int nvec, int nvs, bool aligned_in, b
   sl.first = v0 * VEC;
   sl.V = a.V;
   sl.staged = slice;
-  sl.global = static_cast<const raw*>(a.logits) + row * a.row_stride + sl.first;
-  sl.width = kStaged ? 1 : (sl.nv + kThreadsS * kGroups - 1) / (kThreadsS * kGroups);
-  if (!kStaged && sl.width < 1) sl.width = 1;
+  const raw* logits = static_cast<const raw*>(a.logits) + row * a.row_stride;
+  sl.global = logits + sl.first;
+  sl.width = kStaged ? 1 : max(1, (sl.nv + kThreadsS * kGroups - 1) / (kThreadsS * kGroups));
 
   // ---- the slice into shared memory -------------------------------------
   const int nch = (sl.nv + kChunkS - 1) / kChunkS;
@@ -784,17 +923,14 @@ filtered_sample_kernel(const SampleArgs a, int nvec, int nvs, bool aligned_in, b
     for (int j = tid; j < sl.nv * VEC; j += kThreadsS)
       dst[j] = sl.first + j < a.V ? __ldg(sl.global + j) : masked_value<E>();
   }
-  if (tid == 0) {
-    sh.list_n = 0;
-    sh.n_few = 0;
-  }
+  if (tid == 0) sh.list_n = 0;
   const Settings set = settings_of(a, row);
   const float u = a.uniforms[row];
   const float s = __fdiv_rn(1.44269502f, set.T);
   __syncthreads();
   if (c.C > 1) cluster_arrive_relaxed();  // matched before the first store to another block
 
-  // ---- 1. the row's maximum and the list's threshold ----------------------
+  // ---- the row's maximum and the list's threshold --------------------------
   bool landed = true;
   Peak<E> peak;
   if (bulk) {
@@ -804,7 +940,7 @@ filtered_sample_kernel(const SampleArgs a, int nvec, int nvs, bool aligned_in, b
         break;
       }
       const int stop = min((k + 1) * kChunkS, sl.nv);
-#pragma unroll 2
+#pragma unroll 4
       for (int v = k * kChunkS + tid; v < stop; v += kThreadsS) peak.take(slice[v]);
     }
   } else {
@@ -831,17 +967,18 @@ filtered_sample_kernel(const SampleArgs a, int nvec, int nvs, bool aligned_in, b
         ++n;
       }
     }
-    *c.at(&sh.x.max[c.rank], tid) = m;
-    *c.at(&sh.x.tau[c.rank], tid) = t;
-    *c.at(&sh.x.taus[c.rank], tid) = n;
+    *c.at(&ex.max[c.rank], tid) = m;
+    *c.at(&ex.tau[c.rank], tid) = t;
+    *c.at(&ex.taus[c.rank], tid) = n;
   }
   c.sync();
+  RowHead head;
   float M = -INFINITY, tau = 0.f;
   int taus = 0;
   for (int r = 0; r < c.C; ++r) {
-    M = fmaxf(M, sh.x.max[r]);
-    tau += sh.x.tau[r];
-    taus += sh.x.taus[r];
+    M = fmaxf(M, ex.max[r]);
+    tau += ex.tau[r];
+    taus += ex.taus[r];
   }
   tau = taus ? fminf(tau / taus, M) : -INFINITY;
   M += 0.f;
@@ -850,9 +987,10 @@ filtered_sample_kernel(const SampleArgs a, int nvec, int nvs, bool aligned_in, b
   kept.cut = ~0ull;
   kept.least = max(1ull, __float2ull_rn(__fmul_rn(fminf(fmaxf(set.min_p, 0.f), 1.f), kScale)));
   const bool has_k = set.k < a.V, has_m = set.min_p > 0.f, has_p = set.top_p < 1.f;
-  const float p_clamped = fminf(fmaxf(set.top_p, 0.f), 0.99999994f);
-  unsigned long long S = 0, count = 0;
-  int token = -1;  // on the rank that finds it
+  head.M = M;
+  head.Z = 0;
+  head.listed = -1;
+  head.good = good;
 
   float edge = -FLT_MAX;  // the cut's logit
   auto weigh = [&](unsigned int j, float x) -> unsigned long long {
@@ -863,196 +1001,127 @@ filtered_sample_kernel(const SampleArgs a, int nvec, int nvs, bool aligned_in, b
 
   if (good) {
     bool covered = false;
-    if (has_k || has_m || has_p) {
-      // ---- 2. sum and list ----
+    if (kStaged && !timeout && (has_k || has_m || has_p)) {
+      // ---- list, and approximate sum ----
       // below `floor` every weight is 0
       const float floor = M - __fdiv_rn(42.f, s);
       const bool complete = !(tau > floor);
       const float from = complete ? floor : tau;
       const bool whole = !has_k && !has_m;  // top-p of the whole row's mass
-      Sum z;
+      uint32_t hits[kWords];
+      float z = 0.f;
       int n = 0;
-      unsigned int vectors = 0;
-      auto put = [&](const uint4& w, int v) {
-        for (uint32_t hit = at_least<E>(w, from); hit; hit &= hit - 1) {
-          if (n < kDepth) deep[n * kThreadsS + tid] = static_cast<uint16_t>(v * VEC + __ffs(hit) - 1);
-          ++n;
-        }
-      };
-      const bool lists = kStaged && !timeout;
-      if (lists) {
-        if (whole) {
-          for (int v = tid; v < sl.nv; v += kThreadsS) {
-            const uint4 w = slice[v];
-            float2 x[VEC / 2];
-            unpack_pairs<E>(w, x);
 #pragma unroll
-            for (int k = 0; k < VEC / 2; ++k) add_pair(z, x[k], M, s, mz);
-            ++vectors;
-            put(w, v);
+      for (int i = 0; i < kWords; ++i) {
+        hits[i] = 0;
+        if (i * kPerWord * kThreadsS < sl.nv) {
+          float zi = 0.f;
+#pragma unroll
+          for (int k = 0; k < kPerWord; ++k) {
+            const int v = (i * kPerWord + k) * kThreadsS + tid;
+            if (v < sl.nv) {
+              const uint4 w = slice[v];
+              hits[i] |= at_least<E>(w, from) << (k * VEC);
+              if (whole) zi += vector_mass<E>(w, M, s);
+            }
           }
-        } else {
-          for (int v = tid; v < sl.nv; v += kThreadsS) put(slice[v], v);
+          z += zi;
+          n += __popc(hits[i]);
         }
       }
-      // the listed weights' sum, and the list to rank 0
+      // each thread's place in the list, and what the listed logits weigh
       int incl = n;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
         const int o = __shfl_up_sync(0xffffffffu, incl, d);
         if (lane >= d) incl += o;
       }
-      if (lane == 31) sh.scan[warp] = incl;
-      const int over = __syncthreads_or(n > kDepth || !lists);
-      int before = incl - n, all = 0;
+      int place = 0;
+      if (lane == 31) place = static_cast<int>(atomicAdd(&sh.list_n, static_cast<unsigned int>(incl)));
+      place = __shfl_sync(0xffffffffu, place, 31) + incl - n;
+      // f(place, element) for each of the thread's listed elements
+      auto listed = [&](auto f) {
+        int i = 0;
 #pragma unroll
-      for (int w = 0; w < kWarpsS; ++w) {
-        if (w < warp) before += sh.scan[w];
-        all += sh.scan[w];
+        for (int k = 0; k < kWords; ++k)
+          for (uint32_t h = hits[k]; h; h &= h - 1) {
+            const int b = __ffs(h) - 1;
+            f(i++, ((k * kPerWord + b / VEC) * kThreadsS + tid) * VEC + b % VEC);
+          }
+      };
+      unsigned long long zs = 0, ls = 0;
+      if (whole) {
+        float l = 0.f;
+        listed([&](int, int e) { l += ex2(__fmul_rn(__fsub_rn(staged_elem<E>(slice, e), M), s)); });
+        block_sum2<kThreadsS>(__float2ull_rn(z * kScale), __float2ull_rn(l * kScale), sh, &zs, &ls);
+      } else {
+        __syncthreads();
       }
-      if (tid == 0) sh.sel[2] = over ? 0 : static_cast<int>(atomicAdd(c.at(&sh.list_n, 0), static_cast<unsigned int>(all)));
-      __syncthreads();
-      const int base = sh.sel[2];
-      unsigned long long lw = 0;
-      if (!over) {
-        uint2* to = c.at(list, 0);
-        for (int i = 0; i < n; ++i) {
-          const int e = deep[i * kThreadsS + tid];
-          const float x = staged_elem<E>(slice, e);
-          if (whole) lw += weight(x, M, s);  // the sum decides whether the list covers top-p
-          if (base + before + i < kList)
-            to[base + before + i] = make_uint2(__float_as_uint(x), static_cast<unsigned int>(sl.first + e));
-        }
-      }
-      unsigned long long zs = 0;
-      if (whole) block_sum2(value_of(z, vectors * VEC), lw, sh, &zs, &lw);
+      const int all = static_cast<int>(sh.list_n);
       if (tid < c.C) {
-        *c.at(&sh.x.sum[c.rank], tid) = zs;
-        *c.at(&sh.x.listed_sum[c.rank], tid) = lw;
-        *c.at(&sh.x.listed[c.rank], tid) = over ? -1 : all;
+        *c.at(&ex.sum[c.rank], tid) = zs;
+        *c.at(&ex.listed_sum[c.rank], tid) = ls;
+        *c.at(&ex.listed[c.rank], tid) = all;
       }
       c.sync();
-      int listed = 0;
-      bool overflow = false;
-      unsigned long long Z = 0, L = 0;
+      int total = 0, before = 0;
+      unsigned long long L = 0;
       for (int r = 0; r < c.C; ++r) {
-        overflow |= sh.x.listed[r] < 0;
-        listed += sh.x.listed[r];
-        Z += sh.x.sum[r];
-        L += sh.x.listed_sum[r];
+        if (r < c.rank) before += ex.listed[r];
+        total += ex.listed[r];
+        head.Z += ex.sum[r];
+        L += ex.listed_sum[r];
       }
-      overflow |= listed > kList;
+      head.from = from;
       // does the list hold all that can be kept?
-      if (!overflow) {
+      if (total <= kList) {
         if (complete) {
           covered = true;
         } else if (has_k) {
-          covered = listed >= set.k;
+          covered = total >= set.k;
         } else if (has_m) {  // weights below tau are below min-p's (2^-18: the polynomial's slack)
           const unsigned long long wt = weight(tau, M, s);
           covered = wt + (wt >> 18) + 1 < kept.least;
         } else {
-          covered = L >= max(1ull, draw_threshold(p_clamped, Z));
+          // (a thread may hold the whole list: 1024 additions, 2^-14)
+          covered = L > (L >> 13) + share_of(set.top_p, head.Z + sum_slack(head.Z));
         }
       }
       if (covered) {
-        if (c.rank == 0) {
-          // ---- 3. the cuts and the draw on the list ----
-          unsigned long long key[kPerThread], w[kPerThread], one[kPerThread], id[kPerThread];
-#pragma unroll
-          for (int i = 0; i < kPerThread; ++i) {
-            const int e = i * kThreadsS + tid;
-            const bool in = e < listed;
-            const uint2 q = in ? list[e] : make_uint2(0, 0);
-            const float x = __uint_as_float(q.x);
-            key[i] = cut_key(x, q.y);
-            id[i] = q.y;
-            one[i] = in;
-            w[i] = in ? weight(x, M, s) : 0ull;
-            if (w[i] < kept.least) w[i] = 0;
-          }
-          const unsigned long long klo = cut_key(M, 0), khi = cut_key(from, 0x3fffff);
-          if (has_k && set.k < listed) {
-            kept.cut = list_crossing<true>(c, key, one, klo, khi, set.k - 1);
-#pragma unroll
-            for (int i = 0; i < kPerThread; ++i)
-              if (key[i] > kept.cut) w[i] = 0;
-          }
-          if (has_p) {
-            unsigned long long total = 0;
-#pragma unroll
-            for (int i = 0; i < kPerThread; ++i) total += w[i];
-            total = whole ? Z : block_sum(total, sh.part);
-            kept.cut = list_crossing<false>(c, key, w, klo, khi, max(1ull, draw_threshold(p_clamped, total)) - 1);
-#pragma unroll
-            for (int i = 0; i < kPerThread; ++i)
-              if (key[i] > kept.cut) w[i] = 0;
-          }
-          unsigned long long t = 0, n_kept = 0, top = 0;
-#pragma unroll
-          for (int i = 0; i < kPerThread; ++i) {
-            t += w[i];
-            n_kept += w[i] > 0;
-            if (w[i] && key[i] > top) top = key[i];
-          }
-          block_sum2(t, n_kept, sh, &S, &count);
-          if (a.filtered) {  // the largest key kept: a bound for rows cut by min-p alone
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-            __syncthreads();
-            if (lane == 0) sh.part[warp] = top;
-            __syncthreads();
-#pragma unroll
-            for (int x = 0; x < kWarpsS; ++x) top = max(top, sh.part[x]);
-            kept.cut = top;
-          }
-          token = static_cast<int>(list_crossing<false>(c, id, w, 0, a.V - 1, draw_threshold(u, S)));
-#pragma unroll
-          for (int i = 0; i < kPerThread; ++i)
-            if (w[i] && id[i] == static_cast<unsigned long long>(token)) sh.part2[0] = w[i];
-          __syncthreads();
-          if (tid == 0) {
-            a.tokens[row] = token;
-            if (a.p) a.p[row] = __fdiv_rn(__ull2float_rn(sh.part2[0]), __ull2float_rn(S));
-            if (a.n_kept) a.n_kept[row] = static_cast<int>(count);
-          }
-          if (a.filtered && tid < c.C) *c.at(&sh.cut, tid) = kept.cut;
-        }
-        if (a.filtered) {
+        head.listed = total;
+        if (split) {
+          uint2* to = lists + static_cast<size_t>(at) * kList + before + place;
+          listed([&](int i, int e) {
+            to[i] = make_uint2(__float_as_uint(staged_elem<E>(slice, e)), static_cast<unsigned int>(sl.first + e));
+          });
+        } else {
+          uint2* to = c.at(list, 0) + before + place;
+          listed([&](int i, int e) {
+            to[i] = make_uint2(__float_as_uint(staged_elem<E>(slice, e)), static_cast<unsigned int>(sl.first + e));
+          });
           c.sync();
-          kept.cut = sh.cut;
-        }
-      } else {
-        // ---- the cuts over the slices ----
-        auto cut_at = [&](unsigned long long key) {
-          kept.cut = key;
-          edge = logit_of(key);
-        };
-        if (has_k)
-          cut_at(slice_crossing<E, kStaged, true>(c, sl, M, s, set.k - 1, weigh));
-        if (has_p) {
-          unsigned long long total = Z;
-          if (!(whole && lists)) {
-            c.sync();  // the list is not read any more
-            group_sums<E, kStaged>(c, sl, groups, [&](int v, unsigned int* k) {
-              const uint4 x = sl.at(v);
-              unsigned long long t = 0;
-#pragma unroll
-              for (int i = 0; i < VEC; ++i) t += weigh(sl.first + v * VEC + i, element<E>(x, i));
-              return t;
-            }, &total, &count);
+          if (c.rank == 0) {
+            // the list is in registers before the bins take its place
+            kept.cut = finish_row<E, kThreadsS>(c, a, set, row, list, head, s, logits);
+            if (a.filtered && tid < c.C) *c.at(&sh.cut, tid) = kept.cut;
           }
-          cut_at(slice_crossing<E, kStaged, false>(c, sl, M, s, max(1ull, draw_threshold(p_clamped, total)) - 1, weigh));
+          if (a.filtered) {
+            c.sync();
+            kept.cut = sh.cut;
+          }
         }
       }
     }
     if (!covered) {
-      // ---- the draw over the slices ----
-      c.sync();  // the list is not read any more
-      const bool all = !(has_k || has_m || has_p);
-      group_sums<E, kStaged>(c, sl, groups, [&](int v, unsigned int* k) {
+      // ---- the cuts over the slices ----
+      auto cut_at = [&](unsigned long long key) {
+        kept.cut = key;
+        edge = logit_of(key);
+      };
+      // one vector's kept weights
+      auto vector_sum = [&](int v, unsigned int* k) -> unsigned long long {
         const uint4 w = sl.at(v);
-        if (all) {
+        if (kept.cut == ~0ull && !has_m) {  // all of them
           Sum z;
           float2 x[VEC / 2];
           unpack_pairs<E>(w, x);
@@ -1071,15 +1140,23 @@ filtered_sample_kernel(const SampleArgs a, int nvec, int nvs, bool aligned_in, b
           *k += e > 0;
         }
         return t;
-      }, &S, &count);
-      token = group_draw<E, kStaged>(c, sl, groups, draw_threshold(u, S), weigh);
-      if (token >= 0) {  // on the rank that holds it
-        const float x_token = kStaged ? staged_elem<E>(slice, token - sl.first) : load_one<E>(sl.global, token - sl.first);
-        if (tid == 0) {
-          a.tokens[row] = token;
-          if (a.p) a.p[row] = __fdiv_rn(__ull2float_rn(weight(x_token, M, s)), __ull2float_rn(S));
-          if (a.n_kept) a.n_kept[row] = static_cast<int>(count);
-        }
+      };
+      unsigned long long S = 0, count = 0;
+      if (has_k) cut_at(slice_crossing<E, kStaged, true>(c, sl, M, s, set.k - 1, weigh));
+      if (has_p) {
+        c.sync();
+        group_sums<E, kStaged>(c, sl, groups, vector_sum, &S, &count);
+        cut_at(slice_crossing<E, kStaged, false>(c, sl, M, s, share_of(set.top_p, S) - 1, weigh));
+      }
+      // ---- the draw over the slices ----
+      c.sync();
+      group_sums<E, kStaged>(c, sl, groups, vector_sum, &S, &count);
+      const int token = group_draw<E, kStaged>(c, sl, groups, draw_threshold(u, S), weigh);
+      if (token >= 0 && tid == 0) {  // on the rank that holds it
+        const float x = kStaged ? staged_elem<E>(slice, token - sl.first) : load_one<E>(sl.global, token - sl.first);
+        a.tokens[row] = token;
+        if (a.p) a.p[row] = __fdiv_rn(__ull2float_rn(weight(x, M, s)), __ull2float_rn(S));
+        if (a.n_kept) a.n_kept[row] = static_cast<int>(count);
       }
     }
   } else if (c.rank == 0 && tid == 0) {
@@ -1088,12 +1165,14 @@ filtered_sample_kernel(const SampleArgs a, int nvec, int nvs, bool aligned_in, b
     if (a.n_kept) a.n_kept[row] = 0;
   }
 
-  // ---- the filtered row ----
-  if (a.filtered) {
-    edge = good ? logit_of(kept.cut) : INFINITY;
-    if (!good) kept.cut = 0;
+  if (!good) kept.cut = 0;
+  if (split) {
+    head.cut = kept.cut;
+    if (c.rank == 0 && tid == 0) heads[at] = head;
+  } else if (a.filtered) {
+    const float bound = good ? logit_of(kept.cut) : INFINITY;
     for (int v = tid; v < sl.nv; v += kThreadsS)
-      write_kept<E>(a, row, sl.first, v, sl.at(v), aligned_out && sl.first + (v + 1) * VEC <= a.V, kept, edge, M, s);
+      write_kept<E>(a, row, sl.first, v, sl.at(v), aligned_out && sl.first + (v + 1) * VEC <= a.V, kept, bound, M, s);
   }
   if (tid == 0) {
     int bad = timeout ? kWaitTimeout : 0;
@@ -1105,74 +1184,157 @@ filtered_sample_kernel(const SampleArgs a, int nvec, int nvs, bool aligned_in, b
   }
 }
 
+// One block per listed row.
+template <typename E>
+__global__ void __launch_bounds__(kThreadsB) filter_finish_kernel(const SampleArgs a, int row0, RowHead* heads,
+                                                                  const uint2* lists) {
+  __shared__ Shared sh;
+  __shared__ Bins bins;
+  Ctx c;
+  c.sh = &sh;
+  c.bins = &bins;
+  c.x = nullptr;
+  c.C = 1;
+  c.rank = 0;
+  const int row = row0 + blockIdx.x;
+  const Settings set = settings_of(a, row);
+  const float s = __fdiv_rn(1.44269502f, set.T);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const RowHead head = heads[blockIdx.x];
+  if (head.listed < 0) return;
+  const void* logits = static_cast<const typename E::raw*>(a.logits) + row * a.row_stride;
+  const unsigned long long cut = finish_row<E, kThreadsB>(c, a, set, row, lists + static_cast<size_t>(blockIdx.x) * kList,
+                                                          head, s, logits);
+  if (a.filtered && threadIdx.x == 0) heads[blockIdx.x].cut = cut;
+}
+
+// The filtered rows: 256 threads, kWriteVecs vectors each, several blocks a row.
+constexpr int kWriteVecs = 8;
+template <typename E>
+__global__ void __launch_bounds__(256) filter_write_kernel(const SampleArgs a, int row0, int nvec, bool aligned_in,
+                                                           bool aligned_out, const RowHead* heads) {
+  constexpr int VEC = Staged<E>::kVec;
+  const int row = row0 + blockIdx.x;
+  const Settings set = settings_of(a, row);
+  const float s = __fdiv_rn(1.44269502f, set.T);
+  Slice<E, false> sl;
+  sl.first = 0;
+  sl.V = a.V;
+  sl.global = static_cast<const typename E::raw*>(a.logits) + row * a.row_stride;
+  uint4 w[kWriteVecs];
+#pragma unroll
+  for (int i = 0; i < kWriteVecs; ++i) {
+    const int v = (blockIdx.y * kWriteVecs + i) * 256 + threadIdx.x;
+    if (v < nvec) w[i] = aligned_in ? ld_stream_v4(sl.global + v * VEC) : sl.at(v);
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const RowHead head = heads[blockIdx.x];
+  Kept kept;
+  kept.cut = head.cut;
+  kept.least = max(1ull, __float2ull_rn(__fmul_rn(fminf(fmaxf(set.min_p, 0.f), 1.f), kScale)));
+  const float edge = head.good ? logit_of(kept.cut) : INFINITY;
+#pragma unroll
+  for (int i = 0; i < kWriteVecs; ++i) {
+    const int v = (blockIdx.y * kWriteVecs + i) * 256 + threadIdx.x;
+    if (v < nvec)
+      write_kept<E>(a, row, 0, v, w[i], aligned_out && (v + 1) * VEC <= a.V, kept, edge, head.M, s);
+  }
+}
+
 // Blocks per row: the fewest whose slices fit, or 8 that read global memory.
 struct Shape {
   int nvec, C, nvs;
-  bool staged;
+  bool staged, split;
 };
-Shape shape_of(int V, bool bf16) {
+Shape shape_of(int R, int V, bool bf16) {
   Shape s;
   s.nvec = (V + (bf16 ? 8 : 4) - 1) / (bf16 ? 8 : 4);
   for (s.C = 1; s.C <= kMaxCS; s.C *= 2) {
     s.nvs = (s.nvec + s.C - 1) / s.C;
     if (s.nvs * 16ll <= (s.C == kMaxCS ? kMaxSliceS : kSliceBytesS)) {
       s.staged = true;
+      s.split = static_cast<long long>(R) * s.C > kFusedBlocks;
       return s;
     }
   }
   s.C = kMaxCS;
   s.nvs = 0;
-  s.staged = false;
+  s.staged = s.split = false;
   return s;
 }
 
-constexpr size_t kTailBytes = kList * 8 + kDepth * kThreadsS * 2;
-static_assert(kDepth * kThreadsS * 2 >= static_cast<int>(sizeof(Bins)), "the bins fit the threads' lists");
+constexpr size_t kTailBytes = kList * 8;
+static_assert(sizeof(Bins) <= kTailBytes, "the bins take the list's place");
 
 template <typename E, bool kStaged>
-cudaError_t launch(const SampleArgs& a, const Shape& s, cudaStream_t stream) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned int>(a.R) * s.C);
-  cfg.blockDim = dim3(kThreadsS);
-  cfg.dynamicSmemBytes = static_cast<size_t>(s.nvs) * 16 + kTailBytes;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = s.C;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
+cudaError_t launch(const SampleArgs& a, const Shape& s, RowHead* heads, uint2* lists, cudaStream_t stream) {
   const bool in = reinterpret_cast<uintptr_t>(a.logits) % 16 == 0 && a.row_stride * E::kBytes % 16 == 0 &&
                   a.V % Staged<E>::kVec == 0;
   const bool out = reinterpret_cast<uintptr_t>(a.filtered) % 16 == 0 && a.V % Staged<E>::kVec == 0;
-  return cudaLaunchKernelEx(&cfg, filtered_sample_kernel<E, kStaged>, a, s.nvec, s.nvs, in, out, -0.f);
+  const int step = s.split ? kRowsAtOnce : 1 << 24;
+  for (int row0 = 0; row0 < a.R; row0 += step) {
+    const int rows = a.R - row0 < step ? a.R - row0 : step;
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned int>(rows) * s.C);
+    cfg.blockDim = dim3(kThreadsS);
+    cfg.dynamicSmemBytes = static_cast<size_t>(s.nvs) * 16 + kTailBytes;
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = s.C;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, filter_row_kernel<E, kStaged>, a, row0, s.nvec, s.nvs, in, out, s.split,
+                                       heads, lists, -0.f);
+    if (e != cudaSuccess || !s.split) {
+      if (e != cudaSuccess) return e;
+      continue;
+    }
+    // the next two start early and wait for what they read
+    attr[0] = {};
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(static_cast<unsigned int>(rows));
+    cfg.blockDim = dim3(kThreadsB);
+    cfg.dynamicSmemBytes = 0;
+    e = cudaLaunchKernelEx(&cfg, filter_finish_kernel<E>, a, row0, heads, static_cast<const uint2*>(lists));
+    if (e != cudaSuccess) return e;
+    if (a.filtered) {
+      cfg.gridDim = dim3(static_cast<unsigned int>(rows), (s.nvec + 256 * kWriteVecs - 1) / (256 * kWriteVecs));
+      cfg.blockDim = dim3(256);
+      e = cudaLaunchKernelEx(&cfg, filter_write_kernel<E>, a, row0, s.nvec, in, out, static_cast<const RowHead*>(heads));
+      if (e != cudaSuccess) return e;
+    }
+  }
+  return cudaSuccess;
 }
 
 }  // namespace
 
 size_t filtered_sample_workspace(int R, int V, bool bf16) {
-  (void)R;
-  (void)V;
-  (void)bf16;
-  return 0;
+  if (!shape_of(R, V, bf16).split) return 0;
+  const size_t rows = R < kRowsAtOnce ? R : kRowsAtOnce;
+  return (rows * (sizeof(RowHead) + kList * sizeof(uint2)) + 255) & ~static_cast<size_t>(255);
 }
 
 cudaError_t filtered_sample_prepare() {
   const int bytes = static_cast<int>(kMaxSliceS + kTailBytes);
-  cudaError_t e = cudaFuncSetAttribute(filtered_sample_kernel<BF16, true>,
+  cudaError_t e = cudaFuncSetAttribute(filter_row_kernel<BF16, true>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(filtered_sample_kernel<F32, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    e = cudaFuncSetAttribute(filter_row_kernel<F32, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   return e;
 }
 
 cudaError_t launch_filtered_sample(const SampleArgs& a, void* ws, int sm_count, cudaStream_t stream) {
-  (void)ws;
   (void)sm_count;
-  const Shape s = shape_of(a.V, a.bf16);
-  if (a.bf16) return s.staged ? launch<BF16, true>(a, s, stream) : launch<BF16, false>(a, s, stream);
-  return s.staged ? launch<F32, true>(a, s, stream) : launch<F32, false>(a, s, stream);
+  const Shape s = shape_of(a.R, a.V, a.bf16);
+  RowHead* heads = static_cast<RowHead*>(ws);
+  uint2* lists = reinterpret_cast<uint2*>(heads + (a.R < kRowsAtOnce ? a.R : kRowsAtOnce));
+  if (a.bf16) return s.staged ? launch<BF16, true>(a, s, heads, lists, stream) : launch<BF16, false>(a, s, heads, lists, stream);
+  return s.staged ? launch<F32, true>(a, s, heads, lists, stream) : launch<F32, false>(a, s, heads, lists, stream);
 }
 
 }  // namespace specv
