@@ -32,6 +32,7 @@
 // row's cluster fits the GPU at once, the row kernel does the other two's
 // work as well: latency counts then, and there is no next row to overlap.
 #include <cooperative_groups.h>
+#include <cuda_bf16.h>
 
 #include <cfloat>
 #include <climits>
@@ -47,10 +48,11 @@ namespace {
 
 constexpr int kThreadsS = 256;          // row kernel
 constexpr int kWarpsS = kThreadsS / 32;
-constexpr int kThreadsB = 128;          // finish kernel
 constexpr int kMaxCS = 8;               // blocks of a cluster
-constexpr int kList = 1024;             // listed logits of a row
-constexpr int kGroups = kList / kWarpsS;  // rounds with group sums of their own (they share the list's memory)
+constexpr int kList = 1536;             // listed logits of a row
+constexpr int kPlaces = 4096;           // of a block, as 16-bit places in its slice
+constexpr int kGroupSums = 1024;        // group sums of a block (they share the places' memory)
+constexpr int kGroups = kGroupSums / kWarpsS;  // rounds with group sums of their own 
 constexpr long long kSliceBytesS = 65024;     // a slice, while more blocks can share the row
 constexpr long long kMaxSliceS = 128 * 1024;  // a slice of the largest cluster (65536 bf16: 16-bit places)
 constexpr int kChunkS = 1024;           // vectors per bulk copy
@@ -60,7 +62,7 @@ constexpr int kVectorsS = kMaxSliceS / 16 / kThreadsS;  // vectors of a slice a 
 // Blocks of the row kernel that run at once (two an SM, 152 SMs): rows in
 // clusters of no more than these are finished in it.
 constexpr int kFusedBlocks = 304;
-constexpr int kRowsAtOnce = 8192;       // rows listed in the workspace at a time
+constexpr int kRowsAtOnce = 4096;       // rows listed in the workspace at a time
 
 // 2^f on [-1/2, 1/2] times 2^40: 1 + f (c1 + f (c2 + ...)), a minimax fit of
 // the relative error (9.2e-8; 1.9e-7 with the roundings of every operation).
@@ -262,25 +264,49 @@ struct Peak<F32> {
   __device__ __forceinline__ float value() const { return m; }
 };
 
-// Which elements of a vector are at least `from`: bit k for element k.
+// Which elements of a vector are at least a threshold, and the place of the
+// element behind a bit.  bf16 compares pairs against the smallest bf16 that
+// is no less (bits 0-3 even elements, 4-7 odd ones).
 template <typename E>
-__device__ __forceinline__ uint32_t at_least(const uint4& w, float from) {
-  uint32_t hit = 0;
+struct AtLeast;
+template <>
+struct AtLeast<F32> {
+  float from;
+  __device__ __forceinline__ explicit AtLeast(float f) : from(f) {}
+  __device__ __forceinline__ uint32_t bits(const uint4& w) const {
+    return (__uint_as_float(w.x) >= from ? 1u : 0u) | (__uint_as_float(w.y) >= from ? 2u : 0u) |
+           (__uint_as_float(w.z) >= from ? 4u : 0u) | (__uint_as_float(w.w) >= from ? 8u : 0u);
+  }
+  static __device__ __forceinline__ int place(int bit) { return bit; }
+};
+template <>
+struct AtLeast<BF16> {
+  __nv_bfloat162 from;
+  __device__ __forceinline__ explicit AtLeast(float f) { from = __bfloat162bfloat162(__float2bfloat16_ru(f)); }
+  __device__ __forceinline__ uint32_t bits(const uint4& w) const {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    uint32_t t = 0;
 #pragma unroll
-  for (int k = 0; k < Staged<E>::kVec; ++k) hit |= (element<E>(w, k) >= from ? 1u : 0u) << k;
-  return hit;
-}
+    for (int k = 0; k < 4; ++k) {
+      __nv_bfloat162 x;
+      memcpy(&x, &u[k], 4);
+      t |= __hge2_mask(x, from) & (0x00010001u << k);
+    }
+    return (t | (t >> 12)) & 0xffu;
+  }
+  static __device__ __forceinline__ int place(int bit) { return ((bit & 3) << 1) | (bit >> 2); }
+};
 
 // The approximate mass of a vector, sum of 2^t by ex2.approx.
 template <typename E>
-__device__ __forceinline__ float vector_mass(const uint4& w, float M, float s) {
+__device__ __forceinline__ float vector_mass(const uint4& w, float M, float s, float mz) {
   constexpr int NP = Staged<E>::kVec / 2;
   float2 x[NP];
   unpack_pairs<E>(w, x);
 #pragma unroll
   for (int k = 0; k < NP; ++k) {
-    const float2 d = fadd2(x[k], both(-M));
-    x[k] = make_float2(ex2(d.x * s), ex2(d.y * s));
+    const float2 t = fmul2(fadd2(x[k], both(-M)), both(s), mz);
+    x[k] = make_float2(ex2(t.x), ex2(t.y));
   }
 #pragma unroll
   for (int h = NP / 2; h > 0; h >>= 1)
@@ -309,15 +335,22 @@ struct Shared {
   unsigned long long part[16], part2[16];  // a warp each
   unsigned long long few_key[32], few_w[32];
   unsigned long long rem, lo, cut, w_token;
-  unsigned int n_few, bin_count, list_n;
+  unsigned int n_few, bin_count, list_n, taken;
   int sel[2];
   float wmax[16], wtau[16];
+  Settings set;
+  float u, s;
+  unsigned long long least;
+  int lane_of_tau;
 };
 
 // 256 bins of weights, kept as 32-bit parts so that shared memory adds them
 // without a loop, and of counts.
-struct Bins {
-  unsigned int part[4][256], count[256];
+struct ListBins {
+  unsigned int count[256], part[2][256];
+};
+struct Bins {  // begins as ListBins does
+  unsigned int count[256], part[4][256];
   unsigned long long sum[256];  // of the cluster
   unsigned int all[256];
 };
@@ -375,6 +408,11 @@ __device__ __forceinline__ void block_sum2(unsigned long long a, unsigned long l
                                            unsigned long long* sa, unsigned long long* sb) {
   a = warp_sum_u64(a);
   b = warp_sum_u64(b);
+  if (NT == 32) {
+    *sa = a;
+    *sb = b;
+    return;
+  }
   __syncthreads();
   if ((threadIdx.x & 31) == 0) {
     sh.part[threadIdx.x >> 5] = a;
@@ -392,7 +430,8 @@ __device__ __forceinline__ void block_sum2(unsigned long long a, unsigned long l
 // One warp: the first of 256 bins (by the running sum of value(bin)) to pass
 // rem.  Leaves the bin, what is left of rem inside it and its count in `sh`.
 template <typename F>
-__device__ __forceinline__ void crossing_bin(const Ctx& c, unsigned long long rem, F value) {
+__device__ __forceinline__ void crossing_bin(const Ctx& c, unsigned long long rem, F value,
+                                             const unsigned int* counts) {
   const int lane = threadIdx.x & 31;
   unsigned long long h[8], mine = 0;
 #pragma unroll
@@ -413,7 +452,7 @@ __device__ __forceinline__ void crossing_bin(const Ctx& c, unsigned long long re
       }
     c.sh->sel[0] = lane * 8 + b;
     c.sh->rem = rem >= before ? rem - before : 0;
-    c.sh->bin_count = c.bins->count[lane * 8 + b];
+    c.sh->bin_count = counts[lane * 8 + b];
   }
 }
 
@@ -440,54 +479,72 @@ __device__ __forceinline__ int bin_shift(unsigned long long span) {
   return bits > 8 ? bits - 8 : 0;
 }
 
-// The crossing key over the listed elements, which the block's threads hold
-// (key, and weight 0 for those outside the set).  Keys lie in [lo, hi].
-// kCount: every weight is 1.
-template <int NT, bool kCount>
-__device__ unsigned long long list_crossing(const Ctx& c, const unsigned long long (&key)[kList / NT],
-                                            const unsigned long long (&w)[kList / NT], unsigned long long lo,
-                                            unsigned long long hi, unsigned long long rem) {
-  constexpr int kPer = kList / NT;
+// A listed logit: its bits, its index, its weight's low 20 bits and the rest.
+__device__ __forceinline__ uint4 make_entry(float x, unsigned int j, unsigned long long w) {
+  return make_uint4(__float_as_uint(x), j, static_cast<unsigned int>(w) & 0xfffffu, static_cast<unsigned int>(w >> 20));
+}
+__device__ __forceinline__ unsigned long long weight_of(const uint4& e) {
+  return (static_cast<unsigned long long>(e.w) << 20) + e.z;
+}
+__device__ __forceinline__ unsigned long long key_of(const uint4& e) { return cut_key(__uint_as_float(e.x), e.y); }
+
+// NT threads meet: a warp or the block.
+template <int NT>
+__device__ __forceinline__ void meet() {
+  if (NT == 32) __syncwarp();
+  else __syncthreads();
+}
+
+// The crossing key over n listed elements by NT threads.  keys(entry) lie in
+// [lo, hi]; measure(entry) is an element's weight (kCount: 0 or 1).
+template <int NT, bool kCount, typename K, typename F>
+__device__ __forceinline__ unsigned long long list_crossing(const Ctx& c, const uint4* list, int n, unsigned long long lo,
+                                                            unsigned long long hi, unsigned long long rem, K keys,
+                                                            F measure) {
   int shift = bin_shift(hi - lo);
   for (;;) {
-    __syncthreads();
+    meet<NT>();
     c.clear<NT, kCount ? 0 : 2>();
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const unsigned long long at = (key[i] - lo) >> shift;
-      if (w[i] && key[i] >= lo && at < 256) {
+    meet<NT>();
+#pragma unroll 4
+    for (int i = threadIdx.x; i < n; i += NT) {
+      const uint4 e = list[i];
+      const unsigned long long at = (keys(e) - lo) >> shift, w = measure(e);
+      if (w && at < 256) {  // (a key below lo wraps to a large bin)
         if (kCount) atomicAdd(&c.bins->count[at], 1u);
-        else bin_add<2>(c.bins, static_cast<unsigned int>(at), w[i]);
+        else bin_add<2>(c.bins, static_cast<unsigned int>(at), w);
       }
     }
-    __syncthreads();
-    if (threadIdx.x < 32)
+    meet<NT>();
+    if (NT == 32 || threadIdx.x < 32)
       crossing_bin(c, rem, [&](int b) -> unsigned long long {
         return kCount ? c.bins->count[b] : bin_value<2>(c.bins, b);
-      });
-    __syncthreads();
+      }, c.bins->count);
+    meet<NT>();
     rem = c.sh->rem;
     lo += static_cast<unsigned long long>(c.sh->sel[0]) << shift;
     if (shift == 0) return lo;
     if (c.sh->bin_count <= 32) break;
     shift = shift > 8 ? shift - 8 : 0;
   }
-#pragma unroll
-  for (int i = 0; i < kPer; ++i)
-    if (w[i] && key[i] >= lo && (key[i] - lo) >> shift == 0) {
+#pragma unroll 4
+  for (int i = threadIdx.x; i < n; i += NT) {
+    const uint4 e = list[i];
+    const unsigned long long key = keys(e), w = measure(e);
+    if (w && (key - lo) >> shift == 0) {
       const unsigned int at = atomicAdd(&c.sh->n_few, 1u);
       if (at < 32) {
-        c.sh->few_key[at] = key[i];
-        c.sh->few_w[at] = w[i];
+        c.sh->few_key[at] = key;
+        c.sh->few_w[at] = w;
       }
     }
-  __syncthreads();
-  if (threadIdx.x < 32) {
+  }
+  meet<NT>();
+  if (NT == 32 || threadIdx.x < 32) {
     const unsigned long long k = crossing_of_few(c.sh->few_key, c.sh->few_w, min(32u, c.sh->n_few), rem);
     if (threadIdx.x == 0) c.sh->lo = k;
   }
-  __syncthreads();
+  meet<NT>();
   return c.sh->lo;
 }
 
@@ -548,7 +605,7 @@ __device__ unsigned long long slice_crossing(const Ctx& c, const Slice<E, kStage
       c.bins->all[threadIdx.x] = n;
     }
     __syncthreads();
-    if (threadIdx.x < 32) crossing_bin(c, rem, [&](int b) { return c.bins->sum[b]; });
+    if (threadIdx.x < 32) crossing_bin(c, rem, [&](int b) { return c.bins->sum[b]; }, c.bins->all);
     __syncthreads();
     rem = c.sh->rem;
     const int b = c.sh->sel[0];
@@ -726,7 +783,7 @@ __device__ __forceinline__ float warp_sort(float x, int lane) {
 // maxima.  Averaged over the row's warps it lists m within a tenth on normal
 // rows, up to 1.5 m on Zipf-shifted ones (counted).
 __device__ __forceinline__ int tau_lane(const Settings& set, int V, int C) {
-  const float m = set.k < V ? fminf(1.25f * set.k + 64.f, 700.f) : 640.f;
+  const float m = set.k < V ? fminf(1.25f * set.k + 64.f, 1000.f) : 800.f;
   const float below = ex2(-1.44269504f * m / (kThreadsS * C));
   return min(31, max(0, static_cast<int>(32.f * below)));
 }
@@ -766,14 +823,15 @@ struct __align__(16) RowHead {
   unsigned long long cut;    // kept keys go up to here (for the write kernel)
   int listed;                // -1: the row is finished
   int good;
+  unsigned int taken;        // places of the list given out
 };
 
-// Bounds of the exact sum of a row's weights around the approximate one.  The
-// approximate terms are 2^t of the same t by ex2.approx (2^-22) instead of
-// the polynomial (2^-22), summed in fp32 by at most 13 additions
-// (2^-20.3), and each whole-number weight is rounded by 1/2: together
-// below 2^-19.
-__device__ __forceinline__ unsigned long long sum_slack(unsigned long long Z) { return (Z >> 19) + 1; }
+// How far the exact sum of a row's weights can be from the approximate one.
+// The approximate terms are 2^t of the same t by ex2.approx (2^-22.5 off)
+// instead of the polynomial (2^-22.3), summed in fp32 by at most ten
+// additions (2^-20.7), and each of up to 2^19 whole-number weights is rounded
+// by 1/2 of 2^-40 (2^-22 of the sum): together below 2^-19.8.
+__device__ __forceinline__ unsigned long long sum_slack(unsigned long long Z) { return (Z >> 20) + (Z >> 22) + 2; }
 
 __device__ __forceinline__ unsigned long long share_of(float top_p, unsigned long long total) {
   return max(1ull, draw_threshold(fminf(fmaxf(top_p, 0.f), 0.99999994f), total));
@@ -781,90 +839,208 @@ __device__ __forceinline__ unsigned long long share_of(float top_p, unsigned lon
 
 // Exact sum of a row's weights by one block, from global memory.
 template <typename E, int NT>
-__device__ unsigned long long row_total(const void* logits, int V, float M, float s, Shared& sh) {
+__device__ __noinline__ unsigned long long row_total(const typename E::raw* logits, int V, float M, float s,
+                                                     float mz, Shared& sh) {
+  constexpr int VEC = Staged<E>::kVec;
+  const bool vectors = reinterpret_cast<uintptr_t>(logits) % 16 == 0;
+  Slice<E, false> sl;
+  sl.first = 0;
+  sl.V = V;
+  sl.global = logits;
+  const int nvec = (V + VEC - 1) / VEC;
   unsigned long long t = 0, u;
-  for (int j = threadIdx.x; j < V; j += NT) t += weight(load_one<E>(logits, j), M, s);
+  for (int v0 = threadIdx.x; v0 < nvec; v0 += 8 * NT) {
+    uint4 w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int v = v0 + i * NT;
+      if (v < nvec) w[i] = vectors && (v + 1) * VEC <= V ? ld_stream_v4(logits + v * VEC) : sl.at(v);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (v0 + i * NT < nvec) {
+        Sum z;
+        float2 x[VEC / 2];
+        unpack_pairs<E>(w[i], x);
+#pragma unroll
+        for (int k = 0; k < VEC / 2; ++k) add_pair(z, x[k], M, s, mz);
+        t += value_of(z, VEC);
+      }
+    }
+  }
   block_sum2<NT>(t, 0, sh, &t, &u);
   return t;
 }
 
-// The cuts and the draw of a covered row on its list (x, index), by one block.
-// Writes the row's outputs; returns the largest kept key.
+// The cuts and the draw of a covered row on its list by NT threads.  Writes
+// the row's outputs; returns the largest kept key.  Three passes over the
+// list: weights by bins of the logit's bits (top-p); sums of what lies above
+// the crossing bin, by bins of the index; the crossing bin of the draw.  A
+// bin of more than 32 candidates (ties) goes through list_crossing.
 template <typename E, int NT>
-__device__ unsigned long long finish_row(const Ctx& c, const SampleArgs& a, const Settings& set, int row,
-                                         const uint2* list, const RowHead& head, float s, const void* logits) {
-  constexpr int kPer = kList / NT;
-  const int tid = threadIdx.x;
+__device__ unsigned long long finish_row(const Ctx& c, const SampleArgs& a, const Settings& set,
+                                         unsigned long long least, float u, int row, const uint4* list,
+                                         const RowHead& head, float s, float mz) {
   const bool has_k = set.k < a.V, has_m = set.min_p > 0.f, has_p = set.top_p < 1.f, whole = !has_k && !has_m;
-  const unsigned long long least =
-      max(1ull, __float2ull_rn(__fmul_rn(fminf(fmaxf(set.min_p, 0.f), 1.f), kScale)));
-  unsigned long long key[kPer], w[kPer], kept[kPer], id[kPer];
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int e = i * NT + tid;
-    const bool in = e < head.listed;
-    const uint2 q = in ? list[e] : make_uint2(0, 0);
-    const float x = __uint_as_float(q.x);
-    key[i] = cut_key(x, q.y);
-    id[i] = q.y;
-    kept[i] = in;
-    w[i] = in ? weight(x, head.M, s) : 0ull;
-    if (w[i] < least) w[i] = 0;
-  }
+  const int n = head.listed, tid = threadIdx.x;
+  const unsigned int f0 = falling(head.M);
+  const int fshift = bin_shift(falling(head.from) - f0), jshift = bin_shift(a.V - 1);
   const unsigned long long klo = cut_key(head.M, 0), khi = cut_key(head.from, 0x3fffff);
-  if (has_k && set.k < head.listed) {
-    const unsigned long long cut = list_crossing<NT, true>(c, key, kept, klo, khi, set.k - 1);
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (key[i] > cut) w[i] = 0;
-  }
-  unsigned long long S, count, need = 0, least_need = 0;
+  ListBins* by_index = reinterpret_cast<ListBins*>(c.bins) + 1;
+  unsigned long long cut = ~0ull;
+  auto kept = [&](const uint4& e) -> unsigned long long {
+    const unsigned long long w = weight_of(e);
+    return w >= least && key_of(e) <= cut ? w : 0ull;
+  };
+  if (has_k && set.k < n)
+    cut = list_crossing<NT, true>(c, list, n, klo, khi, set.k - 1, key_of, [](const uint4&) { return 1ull; });
   unsigned long long total = head.Z, slack = whole ? sum_slack(total) : 0;
   if (has_p && !whole) {
-    unsigned long long t = 0, u;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) t += w[i];
-    block_sum2<NT>(t, 0, *c.sh, &total, &u);
+    unsigned long long t = 0, k;
+    for (int i = tid; i < n; i += NT) t += kept(list[i]);
+    block_sum2<NT>(t, 0, *c.sh, &total, &k);
   }
+  unsigned long long S, count;
+  const unsigned long long base = cut;
   for (;;) {
-    unsigned long long cut = ~0ull;
+    // ---- top-p: the crossing bin ----
+    cut = base;
+    int bin = 256;  // kept for sure: bins below
+    unsigned long long rem = 0;
     if (has_p) {
-      need = share_of(set.top_p, total + slack);
-      least_need = share_of(set.top_p, total - slack);
-      cut = list_crossing<NT, false>(c, key, w, klo, khi, least_need - 1);
+      rem = share_of(set.top_p, total - slack) - 1;
+      meet<NT>();
+      c.clear<NT, 2>();
+      meet<NT>();
+#pragma unroll 4
+      for (int i = tid; i < n; i += NT) {
+        const uint4 e = list[i];
+        if (kept(e)) {
+          const unsigned int at = min(255u, (falling(__uint_as_float(e.x)) - f0) >> fshift);
+          atomicAdd(&c.bins->part[0][at], e.z);
+          atomicAdd(&c.bins->part[1][at], e.w);
+          atomicAdd(&c.bins->count[at], 1u);
+        }
+      }
+      meet<NT>();
+      if (NT == 32 || tid < 32)
+        crossing_bin(c, rem, [&](int b) { return bin_value<2>(c.bins, b); }, c.bins->count);
+      meet<NT>();
+      bin = c.sh->sel[0];
+      rem = c.sh->rem;
+      if (c.sh->bin_count > 32) {
+        bin = 256;
+        cut = list_crossing<NT, false>(c, list, n, klo, khi, share_of(set.top_p, total - slack) - 1, key_of, kept);
+      }
     }
-    unsigned long long t = 0, n = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      kept[i] = key[i] <= cut ? w[i] : 0;
-      t += kept[i];
-      n += kept[i] > 0;
+    // ---- what is kept, by bins of the index ----
+    meet<NT>();
+    for (int i = tid; i < 256; i += NT) by_index->count[i] = by_index->part[0][i] = by_index->part[1][i] = 0;
+    if (tid == 0) c.sh->n_few = 0;
+    meet<NT>();
+    unsigned long long t = 0;
+    unsigned int k = 0;
+    auto add = [&](unsigned int j, unsigned int lo, unsigned int hi) {
+      const unsigned int at = j >> jshift;
+      atomicAdd(&by_index->part[0][at], lo);
+      atomicAdd(&by_index->part[1][at], hi);
+      atomicAdd(&by_index->count[at], 1u);
+      t += (static_cast<unsigned long long>(hi) << 20) + lo;
+      ++k;
+    };
+#pragma unroll 4
+    for (int i = tid; i < n; i += NT) {
+      const uint4 e = list[i];
+      if (!kept(e)) continue;
+      const int at = static_cast<int>(min(255u, (falling(__uint_as_float(e.x)) - f0) >> fshift));
+      if (at < bin) {
+        add(e.y, e.z, e.w);
+      } else if (at == bin) {
+        const unsigned int f = atomicAdd(&c.sh->n_few, 1u);
+        if (f < 32) {
+          c.sh->few_key[f] = key_of(e);
+          c.sh->few_w[f] = weight_of(e);
+        }
+      }
     }
-    block_sum2<NT>(t, n, *c.sh, &S, &count);
-    // the kept mass reaches the smallest share asked for; if it reaches the
-    // largest as well, the cut is the exact sum's
-    if (!has_p || slack == 0 || S >= need) break;
-    total = row_total<E, NT>(logits, a.V, head.M, s, *c.sh);
+    if (bin < 256) {
+      meet<NT>();
+      if (NT == 32 || tid < 32) {
+        const int few = min(32u, c.sh->n_few);
+        const unsigned long long key = crossing_of_few(c.sh->few_key, c.sh->few_w, few, rem);
+        if (tid < few && c.sh->few_key[tid] <= key)
+          add(static_cast<unsigned int>(c.sh->few_key[tid]) & 0x3fffffu,
+              static_cast<unsigned int>(c.sh->few_w[tid]) & 0xfffffu, static_cast<unsigned int>(c.sh->few_w[tid] >> 20));
+        if (tid == 0) c.sh->lo = key;
+      }
+      meet<NT>();
+      cut = c.sh->lo;
+    }
+    block_sum2<NT>(t, k, *c.sh, &S, &count);
+    // the kept mass reaches the smallest share that the approximate sum
+    // allows; if it reaches the largest, the cut is the exact sum's
+    if (!has_p || slack == 0 || S >= share_of(set.top_p, total + slack)) break;
+    total = row_total<E, NT>(static_cast<const typename E::raw*>(a.logits) + row * a.row_stride, a.V, head.M, s, mz,
+                             *c.sh);
     slack = 0;
   }
-  const int token = static_cast<int>(list_crossing<NT, false>(c, id, kept, 0, a.V - 1, draw_threshold(a.uniforms[row], S)));
-  unsigned long long top = 0;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    if (kept[i] && id[i] == static_cast<unsigned long long>(token)) c.sh->w_token = kept[i];
-    if (kept[i] && key[i] > top) top = key[i];
+  // ---- the draw ----
+  const unsigned long long theta = draw_threshold(u, S);
+  meet<NT>();
+  if (NT == 32 || tid < 32) {
+    crossing_bin(c, theta, [&](int b) {
+      return (static_cast<unsigned long long>(by_index->part[1][b]) << 20) + by_index->part[0][b];
+    }, by_index->count);
+    if (tid == 0) c.sh->n_few = 0;
   }
-  if (a.filtered) {
+  meet<NT>();
+  unsigned long long token;
+  if (c.sh->bin_count <= 32) {
+    const unsigned int at = static_cast<unsigned int>(c.sh->sel[0]);
+    const unsigned long long rem = c.sh->rem;
+#pragma unroll 4
+    for (int i = tid; i < n; i += NT) {
+      const uint4 e = list[i];
+      if (e.y >> jshift == at && kept(e)) {
+        const unsigned int f = atomicAdd(&c.sh->n_few, 1u);
+        if (f < 32) {
+          c.sh->few_key[f] = e.y;
+          c.sh->few_w[f] = weight_of(e);
+        }
+      }
+    }
+    meet<NT>();
+    if (NT == 32 || tid < 32) {
+      const int few = min(32u, c.sh->n_few);
+      token = crossing_of_few(c.sh->few_key, c.sh->few_w, few, rem);
+      if (tid < few && c.sh->few_key[tid] == token) c.sh->w_token = c.sh->few_w[tid];
+      if (tid == 0) c.sh->lo = token;
+    }
+    meet<NT>();
+    token = c.sh->lo;
+  } else {
+    token = list_crossing<NT, false>(c, list, n, 0, a.V - 1, theta,
+                                     [](const uint4& e) -> unsigned long long { return e.y; }, kept);
+    for (int i = tid; i < n; i += NT)
+      if (list[i].y == token) c.sh->w_token = weight_of(list[i]);
+    meet<NT>();
+  }
+  unsigned long long top = cut;
+  if (a.filtered && cut == ~0ull) {  // no cut by k or p: the largest key kept
+    top = 0;
+    for (int i = tid; i < n; i += NT)
+      if (kept(list[i])) top = max(top, key_of(list[i]));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if ((tid & 31) == 0) c.sh->part[tid >> 5] = top;
-  }
-  __syncthreads();
-  if (a.filtered)
+    if (NT > 32) {
+      if ((tid & 31) == 0) c.sh->part[tid >> 5] = top;
+      __syncthreads();
 #pragma unroll
-    for (int x = 0; x < NT / 32; ++x) top = max(top, c.sh->part[x]);
+      for (int x = 0; x < NT / 32; ++x) top = max(top, c.sh->part[x]);
+    }
+  }
   if (tid == 0) {
-    a.tokens[row] = token;
+    a.tokens[row] = static_cast<int>(token);
     if (a.p) a.p[row] = __fdiv_rn(__ull2float_rn(c.sh->w_token), __ull2float_rn(S));
     if (a.n_kept) a.n_kept[row] = static_cast<int>(count);
   }
@@ -874,11 +1050,11 @@ __device__ unsigned long long finish_row(const Ctx& c, const SampleArgs& a, cons
 template <typename E, bool kStaged>
 __global__ void __launch_bounds__(kThreadsS, 3)
 filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_in, bool aligned_out, bool split,
-                  RowHead* heads, uint2* lists, float mz) {
+                  RowHead* heads, uint4* lists, float mz) {
   constexpr int VEC = Staged<E>::kVec;
   constexpr int kPerWord = 32 / VEC, kWords = kStaged ? kVectorsS / kPerWord : 1;
   using raw = typename E::raw;
-  extern __shared__ __align__(128) uint4 dyn[];  // slice [nvs] | list, bins or group sums
+  extern __shared__ __align__(128) uint4 dyn[];  // slice [nvs] | places, group sums or bins | list (when not split)
   __shared__ Shared sh;
   __shared__ Exchange ex;
   __shared__ __align__(8) unsigned long long bars[kMaxChunksS];
@@ -889,9 +1065,10 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
   c.C = static_cast<int>(cluster.num_blocks());
   c.rank = static_cast<int>(cluster.block_rank());
   uint4* slice = dyn;
-  uint2* list = reinterpret_cast<uint2*>(dyn + (kStaged ? nvs : 0));
-  unsigned long long* groups = reinterpret_cast<unsigned long long*>(list);
-  c.bins = reinterpret_cast<Bins*>(list);
+  uint16_t* places = reinterpret_cast<uint16_t*>(dyn + (kStaged ? nvs : 0));
+  unsigned long long* groups = reinterpret_cast<unsigned long long*>(places);
+  c.bins = reinterpret_cast<Bins*>(places);
+  uint4* list = reinterpret_cast<uint4*>(places + kPlaces);
   const int lgC = __ffs(c.C) - 1;
   const int at = static_cast<int>(blockIdx.x >> lgC), row = row0 + at;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -923,11 +1100,20 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
     for (int j = tid; j < sl.nv * VEC; j += kThreadsS)
       dst[j] = sl.first + j < a.V ? __ldg(sl.global + j) : masked_value<E>();
   }
-  if (tid == 0) sh.list_n = 0;
-  const Settings set = settings_of(a, row);
-  const float u = a.uniforms[row];
-  const float s = __fdiv_rn(1.44269502f, set.T);
+  if (tid == 32) {  // the row's settings, while the copies are under way
+    sh.list_n = 0;
+    if (c.rank == 0) *(split ? &heads[at].taken : &sh.taken) = 0;
+    sh.set = settings_of(a, row);
+    sh.u = a.uniforms[row];
+    sh.s = __fdiv_rn(1.44269502f, sh.set.T);
+    sh.least = max(1ull, __float2ull_rn(__fmul_rn(fminf(fmaxf(sh.set.min_p, 0.f), 1.f), kScale)));
+    sh.lane_of_tau = tau_lane(sh.set, a.V, c.C);
+  }
   __syncthreads();
+  const Settings set = sh.set;
+  const float u = sh.u, s = sh.s;
+  // how much of the row's list is taken
+  unsigned int* count_at = split ? &heads[at].taken : c.at(&sh.taken, 0);
   if (c.C > 1) cluster_arrive_relaxed();  // matched before the first store to another block
 
   // ---- the row's maximum and the list's threshold --------------------------
@@ -949,7 +1135,7 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
   const float mine = peak.value();
   const bool odd = __any_sync(0xffffffffu, isnan(mine));
   const float sorted = warp_sort(mine, lane);
-  const float order = __shfl_sync(0xffffffffu, sorted, tau_lane(set, a.V, c.C));
+  const float order = __shfl_sync(0xffffffffu, sorted, sh.lane_of_tau);
   if (lane == 31) {
     sh.wmax[warp] = odd ? INFINITY : sorted;
     sh.wtau[warp] = order;
@@ -985,7 +1171,7 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
   const bool good = M > -INFINITY && M < INFINITY;
   Kept kept;
   kept.cut = ~0ull;
-  kept.least = max(1ull, __float2ull_rn(__fmul_rn(fminf(fmaxf(set.min_p, 0.f), 1.f), kScale)));
+  kept.least = sh.least;
   const bool has_k = set.k < a.V, has_m = set.min_p > 0.f, has_p = set.top_p < 1.f;
   head.M = M;
   head.Z = 0;
@@ -1005,11 +1191,16 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
       // ---- list, and approximate sum ----
       // below `floor` every weight is 0
       const float floor = M - __fdiv_rn(42.f, s);
-      const bool complete = !(tau > floor);
-      const float from = complete ? floor : tau;
+      // below `least_x` every weight is under min-p's share (with room for the
+      // roundings of t and of the polynomial, and for shares near 2^-40 of the weight itself)
+      const float share = has_m ? __log2f(fminf(set.min_p, 1.f)) - (set.min_p < 1e-6f ? 2.f : 1e-4f) : -42.f;
+      const float least_x = fmaxf(floor, M + __fdiv_rn(share, s) - fabsf(M) * 2.4e-7f);
+      const bool complete = !(tau > least_x);
+      const float from = complete ? least_x : tau;
       const bool whole = !has_k && !has_m;  // top-p of the whole row's mass
+      const AtLeast<E> test(from);
       uint32_t hits[kWords];
-      float z = 0.f;
+      float z = 0.f, z_low = 0.f;
       int n = 0;
 #pragma unroll
       for (int i = 0; i < kWords; ++i) {
@@ -1021,15 +1212,18 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
             const int v = (i * kPerWord + k) * kThreadsS + tid;
             if (v < sl.nv) {
               const uint4 w = slice[v];
-              hits[i] |= at_least<E>(w, from) << (k * VEC);
-              if (whole) zi += vector_mass<E>(w, M, s);
+              hits[i] |= test.bits(w) << (k * VEC);
+              if (whole) zi += vector_mass<E>(w, M, s, mz);
             }
           }
-          z += zi;
+          // z + z_low is the sum without a further rounding
+          const float t = __fadd_rn(z, zi), q = __fsub_rn(t, z);
+          z_low += __fadd_rn(__fsub_rn(z, __fsub_rn(t, q)), __fsub_rn(zi, q));
+          z = t;
           n += __popc(hits[i]);
         }
       }
-      // each thread's place in the list, and what the listed logits weigh
+      // each thread's place in the block's list, the list, what it weighs
       int incl = n;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -1039,70 +1233,59 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
       int place = 0;
       if (lane == 31) place = static_cast<int>(atomicAdd(&sh.list_n, static_cast<unsigned int>(incl)));
       place = __shfl_sync(0xffffffffu, place, 31) + incl - n;
-      // f(place, element) for each of the thread's listed elements
-      auto listed = [&](auto f) {
-        int i = 0;
 #pragma unroll
-        for (int k = 0; k < kWords; ++k)
-          for (uint32_t h = hits[k]; h; h &= h - 1) {
-            const int b = __ffs(h) - 1;
-            f(i++, ((k * kPerWord + b / VEC) * kThreadsS + tid) * VEC + b % VEC);
-          }
-      };
+      for (int i = 0; i < kWords; ++i)
+        for (uint32_t h = hits[i]; h; h &= h - 1) {
+          const int bit = __ffs(h) - 1;
+          const int e = ((i * kPerWord + bit / VEC) * kThreadsS + tid) * VEC + AtLeast<E>::place(bit % VEC);
+          if (place < kPlaces) places[place] = static_cast<uint16_t>(e);
+          ++place;
+        }
+      __syncthreads();
+      const int all = static_cast<int>(sh.list_n), fit = min(all, kPlaces);
+      if (tid == 0) sh.sel[0] = static_cast<int>(atomicAdd(count_at, static_cast<unsigned int>(all)));
+      __syncthreads();
+      const int before = sh.sel[0];
+      uint4* to = split ? lists + static_cast<size_t>(at) * kList : c.at(list, 0);
       unsigned long long zs = 0, ls = 0;
-      if (whole) {
-        float l = 0.f;
-        listed([&](int, int e) { l += ex2(__fmul_rn(__fsub_rn(staged_elem<E>(slice, e), M), s)); });
-        block_sum2<kThreadsS>(__float2ull_rn(z * kScale), __float2ull_rn(l * kScale), sh, &zs, &ls);
-      } else {
-        __syncthreads();
+      for (int i = tid; i < fit && before + i < kList; i += kThreadsS) {
+        const int e = places[i];
+        const float x = staged_elem<E>(slice, e);
+        const unsigned long long w = weight(x, M, s);
+        ls += w;
+        to[before + i] = make_entry(x, static_cast<unsigned int>(sl.first + e), w);
       }
-      const int all = static_cast<int>(sh.list_n);
+      if (whole)
+        block_sum2<kThreadsS>(__float2ull_rn(z * kScale) + static_cast<long long>(z_low * kScale), ls, sh, &zs, &ls);
       if (tid < c.C) {
         *c.at(&ex.sum[c.rank], tid) = zs;
         *c.at(&ex.listed_sum[c.rank], tid) = ls;
         *c.at(&ex.listed[c.rank], tid) = all;
       }
       c.sync();
-      int total = 0, before = 0;
+      int total = 0;
       unsigned long long L = 0;
       for (int r = 0; r < c.C; ++r) {
-        if (r < c.rank) before += ex.listed[r];
         total += ex.listed[r];
         head.Z += ex.sum[r];
         L += ex.listed_sum[r];
       }
       head.from = from;
       // does the list hold all that can be kept?
-      if (total <= kList) {
+      if (total <= kList) {  // (no block's places overflowed then either)
         if (complete) {
           covered = true;
         } else if (has_k) {
           covered = total >= set.k;
-        } else if (has_m) {  // weights below tau are below min-p's (2^-18: the polynomial's slack)
-          const unsigned long long wt = weight(tau, M, s);
-          covered = wt + (wt >> 18) + 1 < kept.least;
-        } else {
-          // (a thread may hold the whole list: 1024 additions, 2^-14)
-          covered = L > (L >> 13) + share_of(set.top_p, head.Z + sum_slack(head.Z));
+        } else if (!has_m) {
+          covered = L >= share_of(set.top_p, head.Z + sum_slack(head.Z));
         }
       }
       if (covered) {
         head.listed = total;
-        if (split) {
-          uint2* to = lists + static_cast<size_t>(at) * kList + before + place;
-          listed([&](int i, int e) {
-            to[i] = make_uint2(__float_as_uint(staged_elem<E>(slice, e)), static_cast<unsigned int>(sl.first + e));
-          });
-        } else {
-          uint2* to = c.at(list, 0) + before + place;
-          listed([&](int i, int e) {
-            to[i] = make_uint2(__float_as_uint(staged_elem<E>(slice, e)), static_cast<unsigned int>(sl.first + e));
-          });
-          c.sync();
+        if (!split) {
           if (c.rank == 0) {
-            // the list is in registers before the bins take its place
-            kept.cut = finish_row<E, kThreadsS>(c, a, set, row, list, head, s, logits);
+            kept.cut = finish_row<E, kThreadsS>(c, a, set, kept.least, u, row, list, head, s, mz);
             if (a.filtered && tid < c.C) *c.at(&sh.cut, tid) = kept.cut;
           }
           if (a.filtered) {
@@ -1184,27 +1367,29 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
   }
 }
 
-// One block per listed row.
+// One warp per listed row: a list of some hundred logits is little work, and
+// many rows at once hide its steps' latency.
 template <typename E>
-__global__ void __launch_bounds__(kThreadsB) filter_finish_kernel(const SampleArgs a, int row0, RowHead* heads,
-                                                                  const uint2* lists) {
+__global__ void __launch_bounds__(32, 32) filter_finish_kernel(const SampleArgs a, int row0, RowHead* heads,
+                                                           const uint4* lists, float mz) {
   __shared__ Shared sh;
-  __shared__ Bins bins;
+  __shared__ ListBins bins[2];
   Ctx c;
   c.sh = &sh;
-  c.bins = &bins;
+  c.bins = reinterpret_cast<Bins*>(bins);
   c.x = nullptr;
   c.C = 1;
   c.rank = 0;
   const int row = row0 + blockIdx.x;
   const Settings set = settings_of(a, row);
-  const float s = __fdiv_rn(1.44269502f, set.T);
+  const float u = a.uniforms[row], s = __fdiv_rn(1.44269502f, set.T);
+  const unsigned long long least =
+      max(1ull, __float2ull_rn(__fmul_rn(fminf(fmaxf(set.min_p, 0.f), 1.f), kScale)));
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const RowHead head = heads[blockIdx.x];
   if (head.listed < 0) return;
-  const void* logits = static_cast<const typename E::raw*>(a.logits) + row * a.row_stride;
-  const unsigned long long cut = finish_row<E, kThreadsB>(c, a, set, row, lists + static_cast<size_t>(blockIdx.x) * kList,
-                                                          head, s, logits);
+  const unsigned long long cut = finish_row<E, 32>(c, a, set, least, u, row, lists + static_cast<size_t>(blockIdx.x) * kList,
+                                                   head, s, mz);
   if (a.filtered && threadIdx.x == 0) heads[blockIdx.x].cut = cut;
 }
 
@@ -1263,11 +1448,11 @@ Shape shape_of(int R, int V, bool bf16) {
   return s;
 }
 
-constexpr size_t kTailBytes = kList * 8;
-static_assert(sizeof(Bins) <= kTailBytes, "the bins take the list's place");
+constexpr size_t kPlaceBytes = kPlaces * 2, kListBytes = kList * 16;
+static_assert(sizeof(Bins) <= kPlaceBytes && 2 * sizeof(ListBins) <= sizeof(Bins) && kGroupSums * 8 <= kPlaceBytes, "they share the places' memory");
 
 template <typename E, bool kStaged>
-cudaError_t launch(const SampleArgs& a, const Shape& s, RowHead* heads, uint2* lists, cudaStream_t stream) {
+cudaError_t launch(const SampleArgs& a, const Shape& s, RowHead* heads, uint4* lists, cudaStream_t stream) {
   const bool in = reinterpret_cast<uintptr_t>(a.logits) % 16 == 0 && a.row_stride * E::kBytes % 16 == 0 &&
                   a.V % Staged<E>::kVec == 0;
   const bool out = reinterpret_cast<uintptr_t>(a.filtered) % 16 == 0 && a.V % Staged<E>::kVec == 0;
@@ -1278,7 +1463,7 @@ cudaError_t launch(const SampleArgs& a, const Shape& s, RowHead* heads, uint2* l
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned int>(rows) * s.C);
     cfg.blockDim = dim3(kThreadsS);
-    cfg.dynamicSmemBytes = static_cast<size_t>(s.nvs) * 16 + kTailBytes;
+    cfg.dynamicSmemBytes = static_cast<size_t>(s.nvs) * 16 + kPlaceBytes + (s.split ? 0 : kListBytes);
     cfg.stream = stream;
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = s.C;
@@ -1297,9 +1482,9 @@ cudaError_t launch(const SampleArgs& a, const Shape& s, RowHead* heads, uint2* l
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.gridDim = dim3(static_cast<unsigned int>(rows));
-    cfg.blockDim = dim3(kThreadsB);
+    cfg.blockDim = dim3(32);
     cfg.dynamicSmemBytes = 0;
-    e = cudaLaunchKernelEx(&cfg, filter_finish_kernel<E>, a, row0, heads, static_cast<const uint2*>(lists));
+    e = cudaLaunchKernelEx(&cfg, filter_finish_kernel<E>, a, row0, heads, static_cast<const uint4*>(lists), -0.f);
     if (e != cudaSuccess) return e;
     if (a.filtered) {
       cfg.gridDim = dim3(static_cast<unsigned int>(rows), (s.nvec + 256 * kWriteVecs - 1) / (256 * kWriteVecs));
@@ -1316,11 +1501,11 @@ cudaError_t launch(const SampleArgs& a, const Shape& s, RowHead* heads, uint2* l
 size_t filtered_sample_workspace(int R, int V, bool bf16) {
   if (!shape_of(R, V, bf16).split) return 0;
   const size_t rows = R < kRowsAtOnce ? R : kRowsAtOnce;
-  return (rows * (sizeof(RowHead) + kList * sizeof(uint2)) + 255) & ~static_cast<size_t>(255);
+  return (rows * (sizeof(RowHead) + kList * sizeof(uint4)) + 255) & ~static_cast<size_t>(255);
 }
 
 cudaError_t filtered_sample_prepare() {
-  const int bytes = static_cast<int>(kMaxSliceS + kTailBytes);
+  const int bytes = static_cast<int>(kMaxSliceS + kPlaceBytes + kListBytes);
   cudaError_t e = cudaFuncSetAttribute(filter_row_kernel<BF16, true>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e == cudaSuccess)
@@ -1332,7 +1517,7 @@ cudaError_t launch_filtered_sample(const SampleArgs& a, void* ws, int sm_count, 
   (void)sm_count;
   const Shape s = shape_of(a.R, a.V, a.bf16);
   RowHead* heads = static_cast<RowHead*>(ws);
-  uint2* lists = reinterpret_cast<uint2*>(heads + (a.R < kRowsAtOnce ? a.R : kRowsAtOnce));
+  uint4* lists = reinterpret_cast<uint4*>(heads + (a.R < kRowsAtOnce ? a.R : kRowsAtOnce));
   if (a.bf16) return s.staged ? launch<BF16, true>(a, s, heads, lists, stream) : launch<BF16, false>(a, s, heads, lists, stream);
   return s.staged ? launch<F32, true>(a, s, heads, lists, stream) : launch<F32, false>(a, s, heads, lists, stream);
 }
