@@ -8,29 +8,30 @@
 // a threshold".  The key is (descending logit, ascending index) for the cuts
 // and the index for the draw.
 //
-// Three kernels, the last two small:
-//   row     one cluster of C blocks per row, each block's slice in shared
+// Four kernels:
+//   list    one cluster of C blocks per row, each block's slice in shared
 //           memory (TMA bulk copies), so the row crosses HBM once.  As the
 //           copies land every thread keeps its largest logit; the cluster
-//           exchanges the row's maximum and a threshold tau, a quantile of
-//           the threads' maxima above which some hundred logits lie.  One
-//           sweep over the slice lists the logits from tau up and, when
-//           top-p asks for a share of the whole row's mass, sums
-//           approximate weights with a bound on their error.  What a cut
-//           keeps nearly always lies in the list -- the k largest, what
-//           min-p leaves, the share that top-p asks for -- and whether it
-//           does is known from counts and sums.
-//   finish  one small block per listed row makes the cuts and the draw on the
-//           list: 256 bins of weights over the key's range, one warp for the
-//           at most 32 candidates of the crossing bin.  The cut that the
-//           approximate sum gives is checked against the sum's bounds; in the
-//           rare row between them the exact sum is taken.
+//           exchanges the row's maximum and a threshold, a quantile of the
+//           threads' maxima above which some hundred logits lie (or min-p's
+//           own threshold where that is higher).  One sweep over the slice
+//           lists the logits from there up and, when top-p asks for a share
+//           of the whole row's mass, sums approximate weights of the others
+//           with a bound on the error.  What a cut keeps nearly always lies in
+//           the list -- the k largest, what min-p leaves, the share that top-p
+//           asks for -- and whether it does is known from counts and sums.
+//           Rows without cuts are drawn here, from exact sums by 32-vector
+//           group.
+//   finish  one warp per listed row makes the cuts and the draw on the list.
+//           The cut that the approximate sum gives is checked against the
+//           sum's bounds.
+//   whole   a cluster does all of a row's work at once.  It takes the rows that
+//           the first two queue -- those whose kept set does not lie in the
+//           list (flat distributions), by bins over the slices, and the rare
+//           ones between the bounds, by the exact sum -- and every row of a
+//           call whose clusters all fit the GPU at once, where latency counts
+//           and there is no next row to overlap.
 //   write   the filtered rows, streaming.
-// Rows without cuts are drawn by the row kernel from exact sums by 32-vector
-// group.  A row whose kept set does not lie in the list (flat distributions,
-// a large k) takes the same cuts there by bins over the slices.  When every
-// row's cluster fits the GPU at once, the row kernel does the other two's
-// work as well: latency counts then, and there is no next row to overlap.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -264,18 +265,26 @@ struct Peak<F32> {
   __device__ __forceinline__ float value() const { return m; }
 };
 
-// Which elements of a vector are at least a threshold, and the place of the
-// element behind a bit.  bf16 compares pairs against the smallest bf16 that
-// is no less (bits 0-3 even elements, 4-7 odd ones).
+// Which elements of a vector are at least a threshold, the vector with -inf
+// in their place, and the place of the element behind a bit.  bf16 compares
+// pairs against the smallest bf16 that is no less than the threshold (bits
+// 0-3 even elements, 4-7 odd ones).
 template <typename E>
 struct AtLeast;
 template <>
 struct AtLeast<F32> {
   float from;
   __device__ __forceinline__ explicit AtLeast(float f) : from(f) {}
-  __device__ __forceinline__ uint32_t bits(const uint4& w) const {
-    return (__uint_as_float(w.x) >= from ? 1u : 0u) | (__uint_as_float(w.y) >= from ? 2u : 0u) |
-           (__uint_as_float(w.z) >= from ? 4u : 0u) | (__uint_as_float(w.w) >= from ? 8u : 0u);
+  __device__ __forceinline__ uint32_t bits(uint4& w) const {
+    uint32_t u[4] = {w.x, w.y, w.z, w.w}, t = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (__uint_as_float(u[k]) >= from) {
+        t |= 1u << k;
+        u[k] = 0xff800000u;
+      }
+    w = make_uint4(u[0], u[1], u[2], u[3]);
+    return t;
   }
   static __device__ __forceinline__ int place(int bit) { return bit; }
 };
@@ -283,15 +292,17 @@ template <>
 struct AtLeast<BF16> {
   __nv_bfloat162 from;
   __device__ __forceinline__ explicit AtLeast(float f) { from = __bfloat162bfloat162(__float2bfloat16_ru(f)); }
-  __device__ __forceinline__ uint32_t bits(const uint4& w) const {
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-    uint32_t t = 0;
+  __device__ __forceinline__ uint32_t bits(uint4& w) const {
+    uint32_t u[4] = {w.x, w.y, w.z, w.w}, t = 0;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       __nv_bfloat162 x;
       memcpy(&x, &u[k], 4);
-      t |= __hge2_mask(x, from) & (0x00010001u << k);
+      const uint32_t m = __hge2_mask(x, from);
+      t |= m & (0x00010001u << k);
+      u[k] = (u[k] & ~m) | (m & 0xff80ff80u);
     }
+    w = make_uint4(u[0], u[1], u[2], u[3]);
     return (t | (t >> 12)) & 0xffu;
   }
   static __device__ __forceinline__ int place(int bit) { return ((bit & 3) << 1) | (bit >> 2); }
@@ -816,22 +827,28 @@ __device__ __forceinline__ void write_kept(const SampleArgs& a, int row, int fir
   }
 }
 
-// A listed row on its way from the row kernel to the others.
+// A row on its way between the kernels.
 struct __align__(16) RowHead {
-  float M, from;             // largest logit, smallest listed one
-  unsigned long long Z;      // approximate mass of the row (2^-40), when top-p needs it
-  unsigned long long cut;    // kept keys go up to here (for the write kernel)
-  int listed;                // -1: the row is finished
+  float M, from;                 // largest logit, smallest listed one
+  unsigned long long Z, slack;   // mass of the row (2^-40) and how far the exact sum may be from it, for top-p
+  unsigned long long cut;        // kept keys go up to here (for the write kernel)
+  int listed;                    // -1: nothing to finish
   int good;
-  unsigned int taken;        // places of the list given out
+  unsigned int taken;            // places of the list given out
+  int written;                   // the filtered row is (being) written by the whole-row kernel
 };
 
-// How far the exact sum of a row's weights can be from the approximate one.
-// The approximate terms are 2^t of the same t by ex2.approx (2^-22.5 off)
-// instead of the polynomial (2^-22.3), summed in fp32 by at most ten
-// additions (2^-20.7), and each of up to 2^19 whole-number weights is rounded
-// by 1/2 of 2^-40 (2^-22 of the sum): together below 2^-19.8.
-__device__ __forceinline__ unsigned long long sum_slack(unsigned long long Z) { return (Z >> 20) + (Z >> 22) + 2; }
+// Rows for the whole-row kernel.  Zero at rest: its last block puts it back.
+struct __align__(16) Queue {
+  unsigned int n, readers;
+};
+
+// How far the exact sum of the unlisted weights can be from the approximate
+// one, U.  The approximate terms are 2^t of the same t by ex2.approx (2^-22.5
+// off) instead of the polynomial (2^-22.3), summed in fp32 by at most ten
+// additions (2^-20.7): together below 2^-20; and each of at most V
+// whole-number weights is rounded by 1/2.
+__device__ __forceinline__ unsigned long long sum_slack(unsigned long long U, int V) { return (U >> 20) + V; }
 
 __device__ __forceinline__ unsigned long long share_of(float top_p, unsigned long long total) {
   return max(1ull, draw_threshold(fminf(fmaxf(top_p, 0.f), 0.99999994f), total));
@@ -873,7 +890,8 @@ __device__ __noinline__ unsigned long long row_total(const typename E::raw* logi
 }
 
 // The cuts and the draw of a covered row on its list by NT threads.  Writes
-// the row's outputs; returns the largest kept key.  Three passes over the
+// the row's outputs; returns the largest kept key (a warp: ~0 when the row
+// needs its exact sum).  Three passes over the
 // list: weights by bins of the logit's bits (top-p); sums of what lies above
 // the crossing bin, by bins of the index; the crossing bin of the draw.  A
 // bin of more than 32 candidates (ties) goes through list_crossing.
@@ -894,7 +912,7 @@ __device__ unsigned long long finish_row(const Ctx& c, const SampleArgs& a, cons
   };
   if (has_k && set.k < n)
     cut = list_crossing<NT, true>(c, list, n, klo, khi, set.k - 1, key_of, [](const uint4&) { return 1ull; });
-  unsigned long long total = head.Z, slack = whole ? sum_slack(total) : 0;
+  unsigned long long total = head.Z, slack = whole ? head.slack : 0;
   if (has_p && !whole) {
     unsigned long long t = 0, k;
     for (int i = tid; i < n; i += NT) t += kept(list[i]);
@@ -980,6 +998,7 @@ __device__ unsigned long long finish_row(const Ctx& c, const SampleArgs& a, cons
     // the kept mass reaches the smallest share that the approximate sum
     // allows; if it reaches the largest, the cut is the exact sum's
     if (!has_p || slack == 0 || S >= share_of(set.top_p, total + slack)) break;
+    if (NT == 32) return ~0ull;  // between the bounds: for the whole-row kernel
     total = row_total<E, NT>(static_cast<const typename E::raw*>(a.logits) + row * a.row_stride, a.V, head.M, s, mz,
                              *c.sh);
     slack = 0;
@@ -1025,8 +1044,8 @@ __device__ unsigned long long finish_row(const Ctx& c, const SampleArgs& a, cons
       if (list[i].y == token) c.sh->w_token = weight_of(list[i]);
     meet<NT>();
   }
-  unsigned long long top = cut;
-  if (a.filtered && cut == ~0ull) {  // no cut by k or p: the largest key kept
+  unsigned long long top = a.filtered ? cut : 0;  // (only the filtered row needs it)
+  if (top == ~0ull) {  // no cut by k or p: the largest key kept
     top = 0;
     for (int i = tid; i < n; i += NT)
       if (kept(list[i])) top = max(top, key_of(list[i]));
@@ -1047,14 +1066,16 @@ __device__ unsigned long long finish_row(const Ctx& c, const SampleArgs& a, cons
   return top;
 }
 
-template <typename E, bool kStaged>
+// The list kernel (kWhole false: cluster i takes row row0 + i) and the
+// whole-row kernel (clusters take rows of the queue, or row i without one).
+template <typename E, bool kStaged, bool kWhole>
 __global__ void __launch_bounds__(kThreadsS, 3)
-filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_in, bool aligned_out, bool split,
-                  RowHead* heads, uint4* lists, float mz) {
+filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_in, bool aligned_out, RowHead* heads,
+                  uint4* lists, Queue* queue, int* queued, float mz) {
   constexpr int VEC = Staged<E>::kVec;
   constexpr int kPerWord = 32 / VEC, kWords = kStaged ? kVectorsS / kPerWord : 1;
   using raw = typename E::raw;
-  extern __shared__ __align__(128) uint4 dyn[];  // slice [nvs] | places, group sums or bins | list (when not split)
+  extern __shared__ __align__(128) uint4 dyn[];  // slice [nvs] | places, group sums or bins | list (kWhole)
   __shared__ Shared sh;
   __shared__ Exchange ex;
   __shared__ __align__(8) unsigned long long bars[kMaxChunksS];
@@ -1070,7 +1091,6 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
   c.bins = reinterpret_cast<Bins*>(places);
   uint4* list = reinterpret_cast<uint4*>(places + kPlaces);
   const int lgC = __ffs(c.C) - 1;
-  const int at = static_cast<int>(blockIdx.x >> lgC), row = row0 + at;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int v0 = static_cast<int>((static_cast<long long>(nvec) * c.rank) >> lgC);
   Slice<E, kStaged> sl;
@@ -1078,126 +1098,136 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
   sl.first = v0 * VEC;
   sl.V = a.V;
   sl.staged = slice;
-  const raw* logits = static_cast<const raw*>(a.logits) + row * a.row_stride;
-  sl.global = logits + sl.first;
   sl.width = kStaged ? 1 : max(1, (sl.nv + kThreadsS * kGroups - 1) / (kThreadsS * kGroups));
-
-  // ---- the slice into shared memory -------------------------------------
   const int nch = (sl.nv + kChunkS - 1) / kChunkS;
   const bool bulk = kStaged && aligned_in;
-  if (bulk) {
-    if (tid == 0) {
-      for (int k = 0; k < nch; ++k) mbar_init(&bars[k], 1);
-      fence_barrier_init();
+  if (bulk && tid == 0) {
+    for (int k = 0; k < nch; ++k) mbar_init(&bars[k], 1);
+    fence_barrier_init();
+  }
+  const int clusters = static_cast<int>(gridDim.x >> lgC);
+  int at = static_cast<int>(blockIdx.x >> lgC), stop_at = at + 1;
+  if (kWhole && queue) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    stop_at = static_cast<int>(queue->n);
+    __syncthreads();
+    if (tid == 0 && atomicAdd(&queue->readers, 1u) + 1u == gridDim.x) {  // everyone has read n
+      queue->n = 0;
+      queue->readers = 0;
+    }
+  }
+  for (int turn = 0; at < stop_at; at += clusters, ++turn) {
+    const int row = kWhole && queue ? queued[at] : row0 + at;
+    const raw* logits = static_cast<const raw*>(a.logits) + row * a.row_stride;
+    sl.global = logits + sl.first;
+
+    // ---- the slice into shared memory -----------------------------------
+    if (bulk) {
+      if (tid == 0) {
+        for (int k = 0; k < nch; ++k) {
+          const uint32_t bytes = min(kChunkS, sl.nv - k * kChunkS) * 16u;
+          mbar_arrive_expect_tx(&bars[k], bytes);
+          bulk_load(slice + k * kChunkS, sl.global + static_cast<size_t>(k) * kChunkS * VEC, bytes, &bars[k]);
+        }
+      }
+    } else if (kStaged) {  // rows that are not 16-byte aligned: element by element
+      raw* dst = reinterpret_cast<raw*>(slice);
+      for (int j = tid; j < sl.nv * VEC; j += kThreadsS)
+        dst[j] = sl.first + j < a.V ? __ldg(sl.global + j) : masked_value<E>();
+    }
+    // how much of the row's list is taken
+    unsigned int* taken = kWhole ? c.at(&sh.taken, 0) : &heads[at].taken;
+    if (tid == 32) {  // the row's settings, while the copies are under way
+      sh.list_n = 0;
+      if (c.rank == 0) *taken = 0;
+      sh.set = settings_of(a, row);
+      sh.u = a.uniforms[row];
+      sh.s = __fdiv_rn(1.44269502f, sh.set.T);
+      sh.least = max(1ull, __float2ull_rn(__fmul_rn(fminf(fmaxf(sh.set.min_p, 0.f), 1.f), kScale)));
+      sh.lane_of_tau = tau_lane(sh.set, a.V, c.C);
+    }
+    __syncthreads();
+    const Settings set = sh.set;
+    const float u = sh.u, s = sh.s;
+    if (c.C > 1) cluster_arrive_relaxed();  // matched before the first store to another block
+
+    // ---- the row's maximum and the list's threshold ------------------------
+    bool landed = true;
+    Peak<E> peak;
+    if (bulk) {
       for (int k = 0; k < nch; ++k) {
-        const uint32_t bytes = min(kChunkS, sl.nv - k * kChunkS) * 16u;
-        mbar_arrive_expect_tx(&bars[k], bytes);
-        bulk_load(slice + k * kChunkS, sl.global + static_cast<size_t>(k) * kChunkS * VEC, bytes, &bars[k]);
-      }
-    }
-  } else if (kStaged) {  // rows that are not 16-byte aligned: element by element
-    raw* dst = reinterpret_cast<raw*>(slice);
-    for (int j = tid; j < sl.nv * VEC; j += kThreadsS)
-      dst[j] = sl.first + j < a.V ? __ldg(sl.global + j) : masked_value<E>();
-  }
-  if (tid == 32) {  // the row's settings, while the copies are under way
-    sh.list_n = 0;
-    if (c.rank == 0) *(split ? &heads[at].taken : &sh.taken) = 0;
-    sh.set = settings_of(a, row);
-    sh.u = a.uniforms[row];
-    sh.s = __fdiv_rn(1.44269502f, sh.set.T);
-    sh.least = max(1ull, __float2ull_rn(__fmul_rn(fminf(fmaxf(sh.set.min_p, 0.f), 1.f), kScale)));
-    sh.lane_of_tau = tau_lane(sh.set, a.V, c.C);
-  }
-  __syncthreads();
-  const Settings set = sh.set;
-  const float u = sh.u, s = sh.s;
-  // how much of the row's list is taken
-  unsigned int* count_at = split ? &heads[at].taken : c.at(&sh.taken, 0);
-  if (c.C > 1) cluster_arrive_relaxed();  // matched before the first store to another block
-
-  // ---- the row's maximum and the list's threshold --------------------------
-  bool landed = true;
-  Peak<E> peak;
-  if (bulk) {
-    for (int k = 0; k < nch; ++k) {
-      if (!mbar_wait_sleep(&bars[k], 0u)) {
-        landed = false;
-        break;
-      }
-      const int stop = min((k + 1) * kChunkS, sl.nv);
+        if (!mbar_wait_sleep(&bars[k], turn & 1)) {
+          landed = false;
+          break;
+        }
+        const int stop = min((k + 1) * kChunkS, sl.nv);
 #pragma unroll 4
-      for (int v = k * kChunkS + tid; v < stop; v += kThreadsS) peak.take(slice[v]);
-    }
-  } else {
-    for (int v = tid; v < sl.nv; v += kThreadsS) peak.take(sl.at(v));
-  }
-  const float mine = peak.value();
-  const bool odd = __any_sync(0xffffffffu, isnan(mine));
-  const float sorted = warp_sort(mine, lane);
-  const float order = __shfl_sync(0xffffffffu, sorted, sh.lane_of_tau);
-  if (lane == 31) {
-    sh.wmax[warp] = odd ? INFINITY : sorted;
-    sh.wtau[warp] = order;
-  }
-  const int timeout = __syncthreads_or(!landed);
-  if (c.C > 1) cluster_wait();  // every block of the cluster has started
-  if (tid < c.C) {
-    float m = -INFINITY, t = 0.f;
-    int n = 0;
-#pragma unroll
-    for (int w = 0; w < kWarpsS; ++w) {
-      m = fmaxf(m, sh.wmax[w]);
-      if (sh.wtau[w] > -INFINITY) {
-        t += sh.wtau[w];
-        ++n;
+        for (int v = k * kChunkS + tid; v < stop; v += kThreadsS) peak.take(slice[v]);
       }
+    } else {
+      for (int v = tid; v < sl.nv; v += kThreadsS) peak.take(sl.at(v));
     }
-    *c.at(&ex.max[c.rank], tid) = m;
-    *c.at(&ex.tau[c.rank], tid) = t;
-    *c.at(&ex.taus[c.rank], tid) = n;
-  }
-  c.sync();
-  RowHead head;
-  float M = -INFINITY, tau = 0.f;
-  int taus = 0;
-  for (int r = 0; r < c.C; ++r) {
-    M = fmaxf(M, ex.max[r]);
-    tau += ex.tau[r];
-    taus += ex.taus[r];
-  }
-  tau = taus ? fminf(tau / taus, M) : -INFINITY;
-  M += 0.f;
-  const bool good = M > -INFINITY && M < INFINITY;
-  Kept kept;
-  kept.cut = ~0ull;
-  kept.least = sh.least;
-  const bool has_k = set.k < a.V, has_m = set.min_p > 0.f, has_p = set.top_p < 1.f;
-  head.M = M;
-  head.Z = 0;
-  head.listed = -1;
-  head.good = good;
+    const float mine = peak.value();
+    const bool odd = __any_sync(0xffffffffu, isnan(mine));
+    const float sorted = warp_sort(mine, lane);
+    const float order = __shfl_sync(0xffffffffu, sorted, sh.lane_of_tau);
+    if (lane == 31) {
+      sh.wmax[warp] = odd ? INFINITY : sorted;
+      sh.wtau[warp] = order;
+    }
+    const int timeout = __syncthreads_or(!landed);
+    if (c.C > 1) cluster_wait();  // every block of the cluster has started
+    if (tid < c.C) {
+      float m = -INFINITY, t = 0.f;
+      int n = 0;
+#pragma unroll
+      for (int w = 0; w < kWarpsS; ++w) {
+        m = fmaxf(m, sh.wmax[w]);
+        if (sh.wtau[w] > -INFINITY) {
+          t += sh.wtau[w];
+          ++n;
+        }
+      }
+      *c.at(&ex.max[c.rank], tid) = m;
+      *c.at(&ex.tau[c.rank], tid) = t;
+      *c.at(&ex.taus[c.rank], tid) = n;
+    }
+    c.sync();
+    float M = -INFINITY, tau = 0.f;
+    int taus = 0;
+    for (int r = 0; r < c.C; ++r) {
+      M = fmaxf(M, ex.max[r]);
+      tau += ex.tau[r];
+      taus += ex.taus[r];
+    }
+    tau = taus ? fminf(tau / taus, M) : -INFINITY;
+    M += 0.f;
+    const bool good = M > -INFINITY && M < INFINITY;
+    Kept kept;
+    kept.cut = ~0ull;
+    kept.least = sh.least;
+    const bool has_k = set.k < a.V, has_m = set.min_p > 0.f, has_p = set.top_p < 1.f;
+    const bool cuts = has_k || has_m || has_p, whole = !has_k && !has_m;  // whole: top-p of the whole row's mass
+    RowHead head;
+    head.M = M;
+    head.from = M;
+    head.Z = head.slack = 0;
+    head.listed = -1;
+    head.good = good;
+    head.taken = 0;
+    head.written = 0;
+    bool later = false;  // for the whole-row kernel
 
-  float edge = -FLT_MAX;  // the cut's logit
-  auto weigh = [&](unsigned int j, float x) -> unsigned long long {
-    if (!(x >= edge) || cut_key(x, j) > kept.cut) return 0ull;
-    const unsigned long long w = weight(x, M, s);
-    return w >= kept.least ? w : 0ull;
-  };
-
-  if (good) {
-    bool covered = false;
-    if (kStaged && !timeout && (has_k || has_m || has_p)) {
-      // ---- list, and approximate sum ----
-      // below `floor` every weight is 0
+    if (good && cuts && kStaged && !timeout) {
+      // ---- list, and approximate sum of the rest ----
+      // below `floor` every weight is 0, below `least_x` under min-p's share
+      // (with room for the roundings of t and of the polynomial, and for
+      // shares near 2^-40 of the weight itself)
       const float floor = M - __fdiv_rn(42.f, s);
-      // below `least_x` every weight is under min-p's share (with room for the
-      // roundings of t and of the polynomial, and for shares near 2^-40 of the weight itself)
       const float share = has_m ? __log2f(fminf(set.min_p, 1.f)) - (set.min_p < 1e-6f ? 2.f : 1e-4f) : -42.f;
       const float least_x = fmaxf(floor, M + __fdiv_rn(share, s) - fabsf(M) * 2.4e-7f);
       const bool complete = !(tau > least_x);
       const float from = complete ? least_x : tau;
-      const bool whole = !has_k && !has_m;  // top-p of the whole row's mass
       const AtLeast<E> test(from);
       uint32_t hits[kWords];
       float z = 0.f, z_low = 0.f;
@@ -1211,7 +1241,7 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
           for (int k = 0; k < kPerWord; ++k) {
             const int v = (i * kPerWord + k) * kThreadsS + tid;
             if (v < sl.nv) {
-              const uint4 w = slice[v];
+              uint4 w = slice[v];
               hits[i] |= test.bits(w) << (k * VEC);
               if (whole) zi += vector_mass<E>(w, M, s, mz);
             }
@@ -1223,7 +1253,7 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
           n += __popc(hits[i]);
         }
       }
-      // each thread's place in the block's list, the list, what it weighs
+      // each thread's place in the block's list, the block's in the row's
       int incl = n;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -1243,10 +1273,10 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
         }
       __syncthreads();
       const int all = static_cast<int>(sh.list_n), fit = min(all, kPlaces);
-      if (tid == 0) sh.sel[0] = static_cast<int>(atomicAdd(count_at, static_cast<unsigned int>(all)));
+      if (tid == 0) sh.sel[0] = static_cast<int>(atomicAdd(taken, static_cast<unsigned int>(all)));
       __syncthreads();
       const int before = sh.sel[0];
-      uint4* to = split ? lists + static_cast<size_t>(at) * kList : c.at(list, 0);
+      uint4* to = kWhole ? c.at(list, 0) : lists + static_cast<size_t>(at) * kList;
       unsigned long long zs = 0, ls = 0;
       for (int i = tid; i < fit && before + i < kList; i += kThreadsS) {
         const int e = places[i];
@@ -1264,47 +1294,44 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
       }
       c.sync();
       int total = 0;
-      unsigned long long L = 0;
+      unsigned long long L = 0, U = 0;
       for (int r = 0; r < c.C; ++r) {
         total += ex.listed[r];
-        head.Z += ex.sum[r];
+        U += ex.sum[r];
         L += ex.listed_sum[r];
       }
+      // does the list hold all that can be kept?  (a list of more than kList
+      // did not fit; the exact sums below then mean nothing)
       head.from = from;
-      // does the list hold all that can be kept?
-      if (total <= kList) {  // (no block's places overflowed then either)
-        if (complete) {
-          covered = true;
-        } else if (has_k) {
-          covered = total >= set.k;
-        } else if (!has_m) {
-          covered = L >= share_of(set.top_p, head.Z + sum_slack(head.Z));
-        }
-      }
-      if (covered) {
+      head.slack = sum_slack(U, a.V);
+      head.Z = L + U;
+      if (total <= kList &&
+          (complete || (has_k ? total >= set.k : !has_m && L >= share_of(set.top_p, head.Z + head.slack))))
         head.listed = total;
-        if (!split) {
-          if (c.rank == 0) {
-            kept.cut = finish_row<E, kThreadsS>(c, a, set, kept.least, u, row, list, head, s, mz);
-            if (a.filtered && tid < c.C) *c.at(&sh.cut, tid) = kept.cut;
-          }
-          if (a.filtered) {
-            c.sync();
-            kept.cut = sh.cut;
-          }
-        }
+      later = !kWhole && head.listed < 0;
+    }
+    if (kWhole && head.listed >= 0) {
+      if (c.rank == 0) {
+        kept.cut = finish_row<E, kThreadsS>(c, a, set, kept.least, u, row, list, head, s, mz);
+        if (a.filtered && tid < c.C) *c.at(&sh.cut, tid) = kept.cut;
+      }
+      if (a.filtered) {
+        c.sync();
+        kept.cut = sh.cut;
       }
     }
-    if (!covered) {
-      // ---- the cuts over the slices ----
-      auto cut_at = [&](unsigned long long key) {
-        kept.cut = key;
-        edge = logit_of(key);
+    if (good && head.listed < 0 && !later) {
+      // ---- the cuts and the draw over the slices ----
+      float edge = -FLT_MAX;  // the cut's logit
+      auto weigh = [&](unsigned int j, float x) -> unsigned long long {
+        if (!(x >= edge) || (kWhole && cut_key(x, j) > kept.cut)) return 0ull;
+        const unsigned long long w = weight(x, M, s);
+        return w >= kept.least ? w : 0ull;
       };
       // one vector's kept weights
       auto vector_sum = [&](int v, unsigned int* k) -> unsigned long long {
         const uint4 w = sl.at(v);
-        if (kept.cut == ~0ull && !has_m) {  // all of them
+        if (!kWhole || (kept.cut == ~0ull && !has_m)) {  // all of them
           Sum z;
           float2 x[VEC / 2];
           unpack_pairs<E>(w, x);
@@ -1325,13 +1352,18 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
         return t;
       };
       unsigned long long S = 0, count = 0;
-      if (has_k) cut_at(slice_crossing<E, kStaged, true>(c, sl, M, s, set.k - 1, weigh));
-      if (has_p) {
-        c.sync();
-        group_sums<E, kStaged>(c, sl, groups, vector_sum, &S, &count);
-        cut_at(slice_crossing<E, kStaged, false>(c, sl, M, s, share_of(set.top_p, S) - 1, weigh));
+      if (kWhole) {
+        auto cut_at = [&](unsigned long long key) {
+          kept.cut = key;
+          edge = logit_of(key);
+        };
+        if (has_k) cut_at(slice_crossing<E, kStaged, true>(c, sl, M, s, set.k - 1, weigh));
+        if (has_p) {
+          c.sync();
+          group_sums<E, kStaged>(c, sl, groups, vector_sum, &S, &count);
+          cut_at(slice_crossing<E, kStaged, false>(c, sl, M, s, share_of(set.top_p, S) - 1, weigh));
+        }
       }
-      // ---- the draw over the slices ----
       c.sync();
       group_sums<E, kStaged>(c, sl, groups, vector_sum, &S, &count);
       const int token = group_draw<E, kStaged>(c, sl, groups, draw_threshold(u, S), weigh);
@@ -1341,29 +1373,34 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
         if (a.p) a.p[row] = __fdiv_rn(__ull2float_rn(weight(x, M, s)), __ull2float_rn(S));
         if (a.n_kept) a.n_kept[row] = static_cast<int>(count);
       }
+    } else if (!good && c.rank == 0 && tid == 0) {
+      a.tokens[row] = 0;
+      if (a.p) a.p[row] = 0.f;
+      if (a.n_kept) a.n_kept[row] = 0;
     }
-  } else if (c.rank == 0 && tid == 0) {
-    a.tokens[row] = 0;
-    if (a.p) a.p[row] = 0.f;
-    if (a.n_kept) a.n_kept[row] = 0;
-  }
 
-  if (!good) kept.cut = 0;
-  if (split) {
-    head.cut = kept.cut;
-    if (c.rank == 0 && tid == 0) heads[at] = head;
-  } else if (a.filtered) {
-    const float bound = good ? logit_of(kept.cut) : INFINITY;
-    for (int v = tid; v < sl.nv; v += kThreadsS)
-      write_kept<E>(a, row, sl.first, v, sl.at(v), aligned_out && sl.first + (v + 1) * VEC <= a.V, kept, bound, M, s);
-  }
-  if (tid == 0) {
-    int bad = timeout ? kWaitTimeout : 0;
-    if (c.rank == 0) {
-      bad |= set.bad | (good ? 0 : kDataNonfiniteLogit);
-      if (!(u >= 0.f && u < 1.f)) bad |= kDataUniformRange;
+    if (!good) kept.cut = 0;
+    if (kWhole) {
+      if (a.filtered) {
+        const float bound = good ? logit_of(kept.cut) : INFINITY;
+        for (int v = tid; v < sl.nv; v += kThreadsS)
+          write_kept<E>(a, row, sl.first, v, sl.at(v), aligned_out && sl.first + (v + 1) * VEC <= a.V, kept, bound, M, s);
+      }
+      c.sync();  // this row's memory is free
+    } else if (c.rank == 0 && tid == 0) {
+      if (later) queued[atomicAdd(&queue->n, 1u)] = row;
+      head.cut = kept.cut;
+      head.written = later;
+      heads[at] = head;
     }
-    if (bad && a.status) atomicOr(a.status, bad);
+    if (tid == 0 && !(kWhole && queue)) {  // (the list kernel has reported a queued row's)
+      int bad = timeout ? kWaitTimeout : 0;
+      if (c.rank == 0) {
+        bad |= set.bad | (good ? 0 : kDataNonfiniteLogit);
+        if (!(u >= 0.f && u < 1.f)) bad |= kDataUniformRange;
+      }
+      if (bad && a.status) atomicOr(a.status, bad);
+    }
   }
 }
 
@@ -1371,7 +1408,7 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
 // many rows at once hide its steps' latency.
 template <typename E>
 __global__ void __launch_bounds__(32, 32) filter_finish_kernel(const SampleArgs a, int row0, RowHead* heads,
-                                                           const uint4* lists, float mz) {
+                                                               const uint4* lists, Queue* queue, int* queued) {
   __shared__ Shared sh;
   __shared__ ListBins bins[2];
   Ctx c;
@@ -1389,8 +1426,15 @@ __global__ void __launch_bounds__(32, 32) filter_finish_kernel(const SampleArgs 
   const RowHead head = heads[blockIdx.x];
   if (head.listed < 0) return;
   const unsigned long long cut = finish_row<E, 32>(c, a, set, least, u, row, lists + static_cast<size_t>(blockIdx.x) * kList,
-                                                   head, s, mz);
-  if (a.filtered && threadIdx.x == 0) heads[blockIdx.x].cut = cut;
+                                                   head, s, -0.f);
+  if (threadIdx.x == 0) {
+    if (cut == ~0ull) {
+      queued[atomicAdd(&queue->n, 1u)] = row;
+      heads[blockIdx.x].written = 1;
+    } else if (a.filtered) {
+      heads[blockIdx.x].cut = cut;
+    }
+  }
 }
 
 // The filtered rows: 256 threads, kWriteVecs vectors each, several blocks a row.
@@ -1406,14 +1450,15 @@ __global__ void __launch_bounds__(256) filter_write_kernel(const SampleArgs a, i
   sl.first = 0;
   sl.V = a.V;
   sl.global = static_cast<const typename E::raw*>(a.logits) + row * a.row_stride;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const RowHead head = heads[blockIdx.x];
+  if (head.written) return;
   uint4 w[kWriteVecs];
 #pragma unroll
   for (int i = 0; i < kWriteVecs; ++i) {
     const int v = (blockIdx.y * kWriteVecs + i) * 256 + threadIdx.x;
     if (v < nvec) w[i] = aligned_in ? ld_stream_v4(sl.global + v * VEC) : sl.at(v);
   }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const RowHead head = heads[blockIdx.x];
   Kept kept;
   kept.cut = head.cut;
   kept.least = max(1ull, __float2ull_rn(__fmul_rn(fminf(fmaxf(set.min_p, 0.f), 1.f), kScale)));
@@ -1449,48 +1494,97 @@ Shape shape_of(int R, int V, bool bf16) {
 }
 
 constexpr size_t kPlaceBytes = kPlaces * 2, kListBytes = kList * 16;
-static_assert(sizeof(Bins) <= kPlaceBytes && 2 * sizeof(ListBins) <= sizeof(Bins) && kGroupSums * 8 <= kPlaceBytes, "they share the places' memory");
+static_assert(sizeof(Bins) <= kPlaceBytes && 2 * sizeof(ListBins) <= sizeof(Bins) && kGroupSums * 8 <= kPlaceBytes,
+              "they share the places' memory");
+
+// Workspace: the queue, its rows, a head and a list per row.
+struct Space {
+  Queue* queue;
+  int* queued;
+  RowHead* heads;
+  uint4* lists;
+  size_t bytes;
+};
+Space space_of(void* ws, int R) {
+  const size_t rows = R < kRowsAtOnce ? R : kRowsAtOnce;
+  Space s;
+  char* p = static_cast<char*>(ws);
+  s.queue = reinterpret_cast<Queue*>(p);
+  s.lists = reinterpret_cast<uint4*>(p + 64);
+  s.heads = reinterpret_cast<RowHead*>(p + 64 + rows * kListBytes);
+  s.queued = reinterpret_cast<int*>(p + 64 + rows * (kListBytes + sizeof(RowHead)));
+  s.bytes = (64 + rows * (kListBytes + sizeof(RowHead) + 4) + 255) & ~static_cast<size_t>(255);
+  return s;
+}
 
 template <typename E, bool kStaged>
-cudaError_t launch(const SampleArgs& a, const Shape& s, RowHead* heads, uint4* lists, cudaStream_t stream) {
+cudaError_t launch(const SampleArgs& a, const Shape& s, const Space& sp, cudaStream_t stream) {
   const bool in = reinterpret_cast<uintptr_t>(a.logits) % 16 == 0 && a.row_stride * E::kBytes % 16 == 0 &&
                   a.V % Staged<E>::kVec == 0;
   const bool out = reinterpret_cast<uintptr_t>(a.filtered) % 16 == 0 && a.V % Staged<E>::kVec == 0;
-  const int step = s.split ? kRowsAtOnce : 1 << 24;
-  for (int row0 = 0; row0 < a.R; row0 += step) {
-    const int rows = a.R - row0 < step ? a.R - row0 : step;
-    cudaLaunchAttribute attr[1];
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned int>(rows) * s.C);
+  cudaLaunchAttribute attr[2] = {};
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = s.C;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  Queue* none = nullptr;
+  if (!s.split) {
+    cfg.gridDim = dim3(static_cast<unsigned int>(a.R) * s.C);
     cfg.blockDim = dim3(kThreadsS);
-    cfg.dynamicSmemBytes = static_cast<size_t>(s.nvs) * 16 + kPlaceBytes + (s.split ? 0 : kListBytes);
-    cfg.stream = stream;
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = s.C;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
+    cfg.dynamicSmemBytes = static_cast<size_t>(s.nvs) * 16 + kPlaceBytes + kListBytes;
     cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, filter_row_kernel<E, kStaged>, a, row0, s.nvec, s.nvs, in, out, s.split,
-                                       heads, lists, -0.f);
-    if (e != cudaSuccess || !s.split) {
+    return cudaLaunchKernelEx(&cfg, filter_row_kernel<E, kStaged, true>, a, 0, s.nvec, s.nvs, in, out, sp.heads, sp.lists,
+                              none, sp.queued, -0.f);
+  }
+  if constexpr (kStaged) {
+    // blocks a row of the queue is shared by: few rows, so more than C
+    int Cq = s.C;
+    while (Cq < kMaxCS && s.nvec / Cq > 1024) Cq *= 2;
+    const int nvq = (s.nvec + Cq - 1) / Cq;
+    for (int row0 = 0; row0 < a.R; row0 += kRowsAtOnce) {
+      const int rows = a.R - row0 < kRowsAtOnce ? a.R - row0 : kRowsAtOnce;
+      cfg.gridDim = dim3(static_cast<unsigned int>(rows) * s.C);
+      cfg.blockDim = dim3(kThreadsS);
+      cfg.dynamicSmemBytes = static_cast<size_t>(s.nvs) * 16 + kPlaceBytes;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      attr[0].val.clusterDim.x = s.C;
+      cudaError_t e = cudaLaunchKernelEx(&cfg, filter_row_kernel<E, true, false>, a, row0, s.nvec, s.nvs, in, out,
+                                         sp.heads, sp.lists, sp.queue, sp.queued, -0.f);
       if (e != cudaSuccess) return e;
-      continue;
-    }
-    // the next two start early and wait for what they read
-    attr[0] = {};
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(static_cast<unsigned int>(rows));
-    cfg.blockDim = dim3(32);
-    cfg.dynamicSmemBytes = 0;
-    e = cudaLaunchKernelEx(&cfg, filter_finish_kernel<E>, a, row0, heads, static_cast<const uint4*>(lists), -0.f);
-    if (e != cudaSuccess) return e;
-    if (a.filtered) {
-      cfg.gridDim = dim3(static_cast<unsigned int>(rows), (s.nvec + 256 * kWriteVecs - 1) / (256 * kWriteVecs));
-      cfg.blockDim = dim3(256);
-      e = cudaLaunchKernelEx(&cfg, filter_write_kernel<E>, a, row0, s.nvec, in, out, static_cast<const RowHead*>(heads));
+      // the next ones start early and wait for what they read
+      cfg.gridDim = dim3(static_cast<unsigned int>(rows));
+      cfg.blockDim = dim3(32);
+      cfg.dynamicSmemBytes = 0;
+      cfg.attrs = attr + 1;
+      e = cudaLaunchKernelEx(&cfg, filter_finish_kernel<E>, a, row0, sp.heads, static_cast<const uint4*>(sp.lists),
+                             sp.queue, sp.queued);
       if (e != cudaSuccess) return e;
+      const int clusters = rows < kFusedBlocks / Cq ? rows : kFusedBlocks / Cq;
+      cfg.gridDim = dim3(static_cast<unsigned int>(clusters * Cq));
+      cfg.blockDim = dim3(kThreadsS);
+      cfg.dynamicSmemBytes = static_cast<size_t>(nvq) * 16 + kPlaceBytes + kListBytes;
+      cfg.attrs = attr;
+      cfg.numAttrs = 2;
+      attr[0].val.clusterDim.x = Cq;
+      e = cudaLaunchKernelEx(&cfg, filter_row_kernel<E, true, true>, a, row0, s.nvec, nvq, in, out, sp.heads, sp.lists,
+                             sp.queue, sp.queued, -0.f);
+      if (e != cudaSuccess) return e;
+      if (a.filtered) {
+        cfg.gridDim = dim3(static_cast<unsigned int>(rows), (s.nvec + 256 * kWriteVecs - 1) / (256 * kWriteVecs));
+        cfg.blockDim = dim3(256);
+        cfg.dynamicSmemBytes = 0;
+        cfg.attrs = attr + 1;
+        cfg.numAttrs = 1;
+        e = cudaLaunchKernelEx(&cfg, filter_write_kernel<E>, a, row0, s.nvec, in, out,
+                               static_cast<const RowHead*>(sp.heads));
+        if (e != cudaSuccess) return e;
+      }
     }
   }
   return cudaSuccess;
@@ -1499,27 +1593,27 @@ cudaError_t launch(const SampleArgs& a, const Shape& s, RowHead* heads, uint4* l
 }  // namespace
 
 size_t filtered_sample_workspace(int R, int V, bool bf16) {
-  if (!shape_of(R, V, bf16).split) return 0;
-  const size_t rows = R < kRowsAtOnce ? R : kRowsAtOnce;
-  return (rows * (sizeof(RowHead) + kList * sizeof(uint4)) + 255) & ~static_cast<size_t>(255);
+  return shape_of(R, V, bf16).split ? space_of(nullptr, R).bytes : 0;
 }
 
 cudaError_t filtered_sample_prepare() {
-  const int bytes = static_cast<int>(kMaxSliceS + kPlaceBytes + kListBytes);
-  cudaError_t e = cudaFuncSetAttribute(filter_row_kernel<BF16, true>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(filter_row_kernel<F32, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  return e;
+  const int most = static_cast<int>(kMaxSliceS + kPlaceBytes + kListBytes);
+  const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+  cudaError_t e[] = {cudaFuncSetAttribute(filter_row_kernel<BF16, true, true>, attr, most),
+                     cudaFuncSetAttribute(filter_row_kernel<F32, true, true>, attr, most),
+                     cudaFuncSetAttribute(filter_row_kernel<BF16, true, false>, attr, most),
+                     cudaFuncSetAttribute(filter_row_kernel<F32, true, false>, attr, most)};
+  for (cudaError_t x : e)
+    if (x != cudaSuccess) return x;
+  return cudaSuccess;
 }
 
 cudaError_t launch_filtered_sample(const SampleArgs& a, void* ws, int sm_count, cudaStream_t stream) {
   (void)sm_count;
   const Shape s = shape_of(a.R, a.V, a.bf16);
-  RowHead* heads = static_cast<RowHead*>(ws);
-  uint4* lists = reinterpret_cast<uint4*>(heads + (a.R < kRowsAtOnce ? a.R : kRowsAtOnce));
-  if (a.bf16) return s.staged ? launch<BF16, true>(a, s, heads, lists, stream) : launch<BF16, false>(a, s, heads, lists, stream);
-  return s.staged ? launch<F32, true>(a, s, heads, lists, stream) : launch<F32, false>(a, s, heads, lists, stream);
+  const Space sp = space_of(ws, a.R);
+  if (a.bf16) return s.staged ? launch<BF16, true>(a, s, sp, stream) : launch<BF16, false>(a, s, sp, stream);
+  return s.staged ? launch<F32, true>(a, s, sp, stream) : launch<F32, false>(a, s, sp, stream);
 }
 
 }  // namespace specv

@@ -155,8 +155,8 @@ SPEC_API spec_status_t spec_cache_compact(
  *      shortest run whose sum reaches max(1, floor(top_p * total)); >= 1: all
  *   4. the draw: with S the sum of the kept weights, the token with the
  *      lowest index j whose running sum (by index) exceeds floor(u * S).
- * T == 0 keeps the largest logit alone (lowest index among equals).  Tokens
- * of weight 0 are never kept.
+ * T == 0 (or below 2^-100) keeps the largest logit alone (lowest index among
+ * equals).  Tokens of weight 0 are never kept.
  *
  *   logits   [R, V] dtype, rows row_stride elements apart.
  *   uniforms [R] fp32 in [0, 1).
@@ -167,7 +167,9 @@ SPEC_API spec_status_t spec_cache_compact(
  *   filtered [R, V] contiguous dtype or NULL: the logits of the kept tokens,
  *            -inf elsewhere -- rows that spec_verify takes as target or draft
  *            logits, so that both sides of the ratio test are truncated.
- *   workspace: spec_filtered_sample_workspace_size(...) bytes, any content.
+ *   workspace: spec_filtered_sample_workspace_size(...) bytes (0 for small
+ *            calls: NULL), zero-filled once; every call leaves it fit for the
+ *            next.  One call at a time.
  * A row with a NaN or +inf or without a finite logit is
  * SPEC_DATA_NONFINITE_LOGIT: token 0, p 0, n_kept 0, filtered -inf.
  */
