@@ -22,7 +22,7 @@
 //           asks for -- and whether it does is known from counts and sums.
 //           Rows without cuts are drawn here, from exact sums by 32-vector
 //           group.
-//   finish  one warp per listed row makes the cuts and the draw on the list.
+//   finish  one small block per listed row makes the cuts and the draw on it.
 //           The cut that the approximate sum gives is checked against the
 //           sum's bounds.
 //   whole   a cluster does all of a row's work at once.  It takes the rows that
@@ -49,6 +49,7 @@ namespace {
 
 constexpr int kThreadsS = 256;          // row kernel
 constexpr int kWarpsS = kThreadsS / 32;
+constexpr int kThreadsB = 128;          // finish kernel
 constexpr int kMaxCS = 8;               // blocks of a cluster
 constexpr int kList = 1536;             // listed logits of a row
 constexpr int kPlaces = 4096;           // of a block, as 16-bit places in its slice
@@ -834,7 +835,6 @@ struct __align__(16) RowHead {
   unsigned long long cut;        // kept keys go up to here (for the write kernel)
   int listed;                    // -1: nothing to finish
   int good;
-  unsigned int taken;            // places of the list given out
   int written;                   // the filtered row is (being) written by the whole-row kernel
 };
 
@@ -890,12 +890,12 @@ __device__ __noinline__ unsigned long long row_total(const typename E::raw* logi
 }
 
 // The cuts and the draw of a covered row on its list by NT threads.  Writes
-// the row's outputs; returns the largest kept key (a warp: ~0 when the row
-// needs its exact sum).  Three passes over the
+// the row's outputs; returns the largest kept key (without kExact: ~0 when the
+// row needs its exact sum).  Three passes over the
 // list: weights by bins of the logit's bits (top-p); sums of what lies above
 // the crossing bin, by bins of the index; the crossing bin of the draw.  A
 // bin of more than 32 candidates (ties) goes through list_crossing.
-template <typename E, int NT>
+template <typename E, int NT, bool kExact>
 __device__ unsigned long long finish_row(const Ctx& c, const SampleArgs& a, const Settings& set,
                                          unsigned long long least, float u, int row, const uint4* list,
                                          const RowHead& head, float s, float mz) {
@@ -998,7 +998,7 @@ __device__ unsigned long long finish_row(const Ctx& c, const SampleArgs& a, cons
     // the kept mass reaches the smallest share that the approximate sum
     // allows; if it reaches the largest, the cut is the exact sum's
     if (!has_p || slack == 0 || S >= share_of(set.top_p, total + slack)) break;
-    if (NT == 32) return ~0ull;  // between the bounds: for the whole-row kernel
+    if (!kExact) return ~0ull;  // between the bounds: for the whole-row kernel
     total = row_total<E, NT>(static_cast<const typename E::raw*>(a.logits) + row * a.row_stride, a.V, head.M, s, mz,
                              *c.sh);
     slack = 0;
@@ -1136,7 +1136,7 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
         dst[j] = sl.first + j < a.V ? __ldg(sl.global + j) : masked_value<E>();
     }
     // how much of the row's list is taken
-    unsigned int* taken = kWhole ? c.at(&sh.taken, 0) : &heads[at].taken;
+    unsigned int* taken = c.at(&sh.taken, 0);
     if (tid == 32) {  // the row's settings, while the copies are under way
       sh.list_n = 0;
       if (c.rank == 0) *taken = 0;
@@ -1214,7 +1214,6 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
     head.Z = head.slack = 0;
     head.listed = -1;
     head.good = good;
-    head.taken = 0;
     head.written = 0;
     bool later = false;  // for the whole-row kernel
 
@@ -1273,9 +1272,12 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
         }
       __syncthreads();
       const int all = static_cast<int>(sh.list_n), fit = min(all, kPlaces);
-      if (tid == 0) sh.sel[0] = static_cast<int>(atomicAdd(taken, static_cast<unsigned int>(all)));
-      __syncthreads();
-      const int before = sh.sel[0];
+      int before = 0;
+      if (c.C > 1) {
+        if (tid == 0) sh.sel[0] = static_cast<int>(atomicAdd(taken, static_cast<unsigned int>(all)));
+        __syncthreads();
+        before = sh.sel[0];
+      }
       uint4* to = kWhole ? c.at(list, 0) : lists + static_cast<size_t>(at) * kList;
       unsigned long long zs = 0, ls = 0;
       for (int i = tid; i < fit && before + i < kList; i += kThreadsS) {
@@ -1312,7 +1314,7 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
     }
     if (kWhole && head.listed >= 0) {
       if (c.rank == 0) {
-        kept.cut = finish_row<E, kThreadsS>(c, a, set, kept.least, u, row, list, head, s, mz);
+        kept.cut = finish_row<E, kThreadsS, true>(c, a, set, kept.least, u, row, list, head, s, mz);
         if (a.filtered && tid < c.C) *c.at(&sh.cut, tid) = kept.cut;
       }
       if (a.filtered) {
@@ -1404,13 +1406,13 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
   }
 }
 
-// One warp per listed row: a list of some hundred logits is little work, and
-// many rows at once hide its steps' latency.
+// One block per listed row, the list in shared memory.
 template <typename E>
-__global__ void __launch_bounds__(32, 32) filter_finish_kernel(const SampleArgs a, int row0, RowHead* heads,
-                                                               const uint4* lists, Queue* queue, int* queued) {
+__global__ void __launch_bounds__(kThreadsB, 8) filter_finish_kernel(const SampleArgs a, int row0, RowHead* heads,
+                                                                     const uint4* lists, Queue* queue, int* queued) {
   __shared__ Shared sh;
   __shared__ ListBins bins[2];
+  __shared__ uint4 list[kList];
   Ctx c;
   c.sh = &sh;
   c.bins = reinterpret_cast<Bins*>(bins);
@@ -1425,8 +1427,11 @@ __global__ void __launch_bounds__(32, 32) filter_finish_kernel(const SampleArgs 
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const RowHead head = heads[blockIdx.x];
   if (head.listed < 0) return;
-  const unsigned long long cut = finish_row<E, 32>(c, a, set, least, u, row, lists + static_cast<size_t>(blockIdx.x) * kList,
-                                                   head, s, -0.f);
+  const uint4* from = lists + static_cast<size_t>(blockIdx.x) * kList;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < head.listed; i += kThreadsB) list[i] = from[i];
+  const unsigned long long cut =
+      finish_row<E, kThreadsB, false>(c, a, set, least, u, row, list, head, s, -0.f);
   if (threadIdx.x == 0) {
     if (cut == ~0ull) {
       queued[atomicAdd(&queue->n, 1u)] = row;
@@ -1559,7 +1564,7 @@ cudaError_t launch(const SampleArgs& a, const Shape& s, const Space& sp, cudaStr
       if (e != cudaSuccess) return e;
       // the next ones start early and wait for what they read
       cfg.gridDim = dim3(static_cast<unsigned int>(rows));
-      cfg.blockDim = dim3(32);
+      cfg.blockDim = dim3(kThreadsB);
       cfg.dynamicSmemBytes = 0;
       cfg.attrs = attr + 1;
       e = cudaLaunchKernelEx(&cfg, filter_finish_kernel<E>, a, row0, sp.heads, static_cast<const uint4*>(sp.lists),
