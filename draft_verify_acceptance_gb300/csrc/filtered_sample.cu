@@ -52,15 +52,16 @@ constexpr int kWarpsS = kThreadsS / 32;
 constexpr int kThreadsB = 128;          // finish kernel
 constexpr int kMaxCS = 8;               // blocks of a cluster
 constexpr int kList = 1536;             // listed logits of a row
+constexpr int kLongList = 4095;         // of a queued row (bins hold 4095 of the largest weight)
 constexpr int kPlaces = 4096;           // of a block, as 16-bit places in its slice
 constexpr int kGroupSums = 1024;        // group sums of a block (they share the places' memory)
 constexpr int kGroups = kGroupSums / kWarpsS;  // rounds with group sums of their own 
 constexpr long long kSliceBytesS = 65024;     // a slice, while more blocks can share the row
-constexpr long long kMaxSliceS = 128 * 1024;  // a slice of the largest cluster (65536 bf16: 16-bit places)
+constexpr long long kMaxSliceS = 128 * 1024;  // a slice of the largest cluster (with a long list beside it)
 constexpr int kChunkS = 1024;           // vectors per bulk copy
-constexpr int kMaxChunksS = 8;
+constexpr int kMaxChunksS = 8;         // (65536 bf16 of a slice: 16-bit places)
 static_assert(kMaxSliceS / 16 <= kChunkS * kMaxChunksS, "bulk copies of a slice");
-constexpr int kVectorsS = kMaxSliceS / 16 / kThreadsS;  // vectors of a slice a thread sweeps at most
+constexpr int kVectorsS = (kMaxSliceS / 16 + kThreadsS - 1) / kThreadsS;  // vectors of a slice a thread sweeps at most
 // Blocks of the row kernel that run at once (two an SM, 152 SMs): rows in
 // clusters of no more than these are finished in it.
 constexpr int kFusedBlocks = 304;
@@ -177,13 +178,19 @@ __device__ __forceinline__ unsigned long long value_of(const Sum& z, unsigned in
   return (static_cast<unsigned long long>(high) << 20) + static_cast<long long>(low);
 }
 
-// Which tokens are kept: key (falling(x), index) at most `cut`, weight at
+// Which tokens are kept: key (falling logit, index) at most `cut`, weight at
 // least `least` (weight 0 is never kept).
 struct Kept {
   unsigned long long cut, least;
 };
+// A bf16 has 16 bits of its own, which leaves the key's bins to them and the index.
+template <typename E>
+__device__ __forceinline__ unsigned int value_key(float x) {
+  return E::kBytes == 2 ? falling(x) >> 16 : falling(x);
+}
+template <typename E>
 __device__ __forceinline__ unsigned long long cut_key(float x, unsigned int j) {
-  return (static_cast<unsigned long long>(falling(x)) << 22) | j;
+  return (static_cast<unsigned long long>(value_key<E>(x)) << 22) | j;
 }
 
 // -inf as an element.
@@ -328,10 +335,16 @@ __device__ __forceinline__ float vector_mass(const uint4& w, float M, float s, f
 }
 
 // The logit of a cut key; the lowest finite one for "no cut".
+template <typename E>
 __device__ __forceinline__ float logit_of(unsigned long long cut) {
   if (cut == ~0ull) return -FLT_MAX;
-  const unsigned int o = ~static_cast<unsigned int>(cut >> 22);
-  return __uint_as_float((o >> 31) ? o & 0x7fffffffu : ~o);
+  if constexpr (E::kBytes == 2) {
+    const unsigned int o = ~static_cast<unsigned int>(cut >> 22) & 0xffffu;
+    return __uint_as_float(((o >> 15) ? o & 0x7fffu : ~o & 0xffffu) << 16);
+  } else {
+    const unsigned int o = ~static_cast<unsigned int>(cut >> 22);
+    return __uint_as_float((o >> 31) ? o & 0x7fffffffu : ~o);
+  }
 }
 
 // What every rank of a cluster publishes to all.
@@ -366,7 +379,7 @@ struct Bins {  // begins as ListBins does
   unsigned long long sum[256];  // of the cluster
   unsigned int all[256];
 };
-template <int kParts>  // parts of 20 bits (a list) or of 11 (a slice)
+template <int kParts>  // parts of 20 bits (a list: less than 2^12 of the largest weight) or of 11 (a slice)
 __device__ __forceinline__ void bin_add(Bins* h, unsigned int at, unsigned long long w) {
   constexpr int kBits = kParts == 2 ? 20 : 11;
 #pragma unroll
@@ -498,7 +511,8 @@ __device__ __forceinline__ uint4 make_entry(float x, unsigned int j, unsigned lo
 __device__ __forceinline__ unsigned long long weight_of(const uint4& e) {
   return (static_cast<unsigned long long>(e.w) << 20) + e.z;
 }
-__device__ __forceinline__ unsigned long long key_of(const uint4& e) { return cut_key(__uint_as_float(e.x), e.y); }
+template <typename E>
+__device__ __forceinline__ unsigned long long key_of(const uint4& e) { return cut_key<E>(__uint_as_float(e.x), e.y); }
 
 // NT threads meet: a warp or the block.
 template <int NT>
@@ -593,7 +607,7 @@ __device__ unsigned long long slice_crossing(const Ctx& c, const Slice<E, kStage
     sweep(from, to, [&](unsigned int j, float x) {
       unsigned int at = bin_of(x);
       if (shift >= 0) {
-        const unsigned long long key = cut_key(x, j), d = (key - lo) >> shift;
+        const unsigned long long key = cut_key<E>(x, j), d = (key - lo) >> shift;
         if (static_cast<int>(at) != bin || key < lo || d > 255) return;
         at = static_cast<unsigned int>(d);
       }
@@ -630,8 +644,8 @@ __device__ unsigned long long slice_crossing(const Ctx& c, const Slice<E, kStage
       to = fminf(M, to + fabsf(to) * 4.8e-7f);
       from = b == 255 ? -INFINITY : M - (b + 1.01f) * unit;
       from -= b == 255 ? 0.f : fabsf(from) * 4.8e-7f;
-      lo = cut_key(to, 0);
-      shift = bin_shift(cut_key(from, 0x3fffff) - lo);
+      lo = cut_key<E>(to, 0);
+      shift = bin_shift(cut_key<E>(from, 0x3fffff) - lo);
       if (few) {
         shift = 54;  // all keys of the bin at once
         break;
@@ -645,7 +659,7 @@ __device__ unsigned long long slice_crossing(const Ctx& c, const Slice<E, kStage
   }
   Shared* zero = c.at(c.sh, 0);
   sweep(from, to, [&](unsigned int j, float x) {
-    const unsigned long long key = cut_key(x, j);
+    const unsigned long long key = cut_key<E>(x, j);
     if (bin_of(x) == bin && key >= lo && (key - lo) >> shift == 0) {
       const unsigned long long w = kCount ? 1ull : measure(j, x);
       if (w) {
@@ -794,8 +808,9 @@ __device__ __forceinline__ float warp_sort(float x, int lane) {
 // with probability e^(-m/T), so the threshold is that quantile of the
 // maxima.  Averaged over the row's warps it lists m within a tenth on normal
 // rows, up to 1.5 m on Zipf-shifted ones (counted).
-__device__ __forceinline__ int tau_lane(const Settings& set, int V, int C) {
-  const float m = set.k < V ? fminf(1.25f * set.k + 64.f, 1000.f) : 800.f;
+__device__ __forceinline__ int tau_lane(const Settings& set, int V, int C, int most) {
+  const float share = 0.55f * most;  // room for rows that list more than meant
+  const float m = set.k < V ? fminf(1.25f * set.k + 64.f, share) : share;
   const float below = ex2(-1.44269504f * m / (kThreadsS * C));
   return min(31, max(0, static_cast<int>(32.f * below)));
 }
@@ -813,7 +828,7 @@ __device__ __forceinline__ void write_kept(const SampleArgs& a, int row, int fir
   for (int k = 0; k < VEC; ++k) {
     const float f = element<E>(w, k);
     bool in = f >= edge;
-    if (in) in = cut_key(f, first + v * VEC + k) <= kept.cut && weight(f, M, s) >= kept.least;
+    if (in) in = cut_key<E>(f, first + v * VEC + k) <= kept.cut && weight(f, M, s) >= kept.least;
     if (!in) x[k] = masked_value<E>();
   }
   raw* dst = static_cast<raw*>(a.filtered) + static_cast<size_t>(row) * a.V + first + v * VEC;
@@ -901,17 +916,17 @@ __device__ unsigned long long finish_row(const Ctx& c, const SampleArgs& a, cons
                                          const RowHead& head, float s, float mz) {
   const bool has_k = set.k < a.V, has_m = set.min_p > 0.f, has_p = set.top_p < 1.f, whole = !has_k && !has_m;
   const int n = head.listed, tid = threadIdx.x;
-  const unsigned int f0 = falling(head.M);
-  const int fshift = bin_shift(falling(head.from) - f0), jshift = bin_shift(a.V - 1);
-  const unsigned long long klo = cut_key(head.M, 0), khi = cut_key(head.from, 0x3fffff);
+  const unsigned int f0 = value_key<E>(head.M);
+  const int fshift = bin_shift(value_key<E>(head.from) - f0), jshift = bin_shift(a.V - 1);
+  const unsigned long long klo = cut_key<E>(head.M, 0), khi = cut_key<E>(head.from, 0x3fffff);
   ListBins* by_index = reinterpret_cast<ListBins*>(c.bins) + 1;
   unsigned long long cut = ~0ull;
   auto kept = [&](const uint4& e) -> unsigned long long {
     const unsigned long long w = weight_of(e);
-    return w >= least && key_of(e) <= cut ? w : 0ull;
+    return w >= least && key_of<E>(e) <= cut ? w : 0ull;
   };
   if (has_k && set.k < n)
-    cut = list_crossing<NT, true>(c, list, n, klo, khi, set.k - 1, key_of, [](const uint4&) { return 1ull; });
+    cut = list_crossing<NT, true>(c, list, n, klo, khi, set.k - 1, key_of<E>, [](const uint4&) { return 1ull; });
   unsigned long long total = head.Z, slack = whole ? head.slack : 0;
   if (has_p && !whole) {
     unsigned long long t = 0, k;
@@ -934,7 +949,7 @@ __device__ unsigned long long finish_row(const Ctx& c, const SampleArgs& a, cons
       for (int i = tid; i < n; i += NT) {
         const uint4 e = list[i];
         if (kept(e)) {
-          const unsigned int at = min(255u, (falling(__uint_as_float(e.x)) - f0) >> fshift);
+          const unsigned int at = min(255u, (value_key<E>(__uint_as_float(e.x)) - f0) >> fshift);
           atomicAdd(&c.bins->part[0][at], e.z);
           atomicAdd(&c.bins->part[1][at], e.w);
           atomicAdd(&c.bins->count[at], 1u);
@@ -947,8 +962,9 @@ __device__ unsigned long long finish_row(const Ctx& c, const SampleArgs& a, cons
       bin = c.sh->sel[0];
       rem = c.sh->rem;
       if (c.sh->bin_count > 32) {
+        const unsigned long long lo = static_cast<unsigned long long>(f0 + (static_cast<unsigned int>(bin) << fshift)) << 22;
+        cut = list_crossing<NT, false>(c, list, n, lo, lo + (1ull << (fshift + 22)) - 1, rem, key_of<E>, kept);
         bin = 256;
-        cut = list_crossing<NT, false>(c, list, n, klo, khi, share_of(set.top_p, total - slack) - 1, key_of, kept);
       }
     }
     // ---- what is kept, by bins of the index ----
@@ -970,13 +986,13 @@ __device__ unsigned long long finish_row(const Ctx& c, const SampleArgs& a, cons
     for (int i = tid; i < n; i += NT) {
       const uint4 e = list[i];
       if (!kept(e)) continue;
-      const int at = static_cast<int>(min(255u, (falling(__uint_as_float(e.x)) - f0) >> fshift));
+      const int at = static_cast<int>(min(255u, (value_key<E>(__uint_as_float(e.x)) - f0) >> fshift));
       if (at < bin) {
         add(e.y, e.z, e.w);
       } else if (at == bin) {
         const unsigned int f = atomicAdd(&c.sh->n_few, 1u);
         if (f < 32) {
-          c.sh->few_key[f] = key_of(e);
+          c.sh->few_key[f] = key_of<E>(e);
           c.sh->few_w[f] = weight_of(e);
         }
       }
@@ -1048,7 +1064,7 @@ __device__ unsigned long long finish_row(const Ctx& c, const SampleArgs& a, cons
   if (top == ~0ull) {  // no cut by k or p: the largest key kept
     top = 0;
     for (int i = tid; i < n; i += NT)
-      if (kept(list[i])) top = max(top, key_of(list[i]));
+      if (kept(list[i])) top = max(top, key_of<E>(list[i]));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
     if (NT > 32) {
@@ -1071,9 +1087,9 @@ __device__ unsigned long long finish_row(const Ctx& c, const SampleArgs& a, cons
 template <typename E, bool kStaged, bool kWhole>
 __global__ void __launch_bounds__(kThreadsS, 3)
 filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_in, bool aligned_out, RowHead* heads,
-                  uint4* lists, Queue* queue, int* queued, float mz) {
+                  uint4* lists, int most, Queue* queue, int* queued, float mz) {
   constexpr int VEC = Staged<E>::kVec;
-  constexpr int kPerWord = 32 / VEC, kWords = kStaged ? kVectorsS / kPerWord : 1;
+  constexpr int kPerWord = 32 / VEC, kWords = kStaged ? (kVectorsS + kPerWord - 1) / kPerWord : 1;
   using raw = typename E::raw;
   extern __shared__ __align__(128) uint4 dyn[];  // slice [nvs] | places, group sums or bins | list (kWhole)
   __shared__ Shared sh;
@@ -1144,7 +1160,7 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
       sh.u = a.uniforms[row];
       sh.s = __fdiv_rn(1.44269502f, sh.set.T);
       sh.least = max(1ull, __float2ull_rn(__fmul_rn(fminf(fmaxf(sh.set.min_p, 0.f), 1.f), kScale)));
-      sh.lane_of_tau = tau_lane(sh.set, a.V, c.C);
+      sh.lane_of_tau = tau_lane(sh.set, a.V, c.C, most);
     }
     __syncthreads();
     const Settings set = sh.set;
@@ -1280,7 +1296,7 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
       }
       uint4* to = kWhole ? c.at(list, 0) : lists + static_cast<size_t>(at) * kList;
       unsigned long long zs = 0, ls = 0;
-      for (int i = tid; i < fit && before + i < kList; i += kThreadsS) {
+      for (int i = tid; i < fit && before + i < most; i += kThreadsS) {
         const int e = places[i];
         const float x = staged_elem<E>(slice, e);
         const unsigned long long w = weight(x, M, s);
@@ -1296,18 +1312,20 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
       }
       c.sync();
       int total = 0;
+      bool crowded = false;
       unsigned long long L = 0, U = 0;
       for (int r = 0; r < c.C; ++r) {
+        crowded |= ex.listed[r] > kPlaces;
         total += ex.listed[r];
         U += ex.sum[r];
         L += ex.listed_sum[r];
       }
-      // does the list hold all that can be kept?  (a list of more than kList
-      // did not fit; the exact sums below then mean nothing)
+      // does the list hold all that can be kept?  (more than `most`, or a
+      // block's kPlaces, did not fit, and the sums then mean nothing)
       head.from = from;
       head.slack = sum_slack(U, a.V);
       head.Z = L + U;
-      if (total <= kList &&
+      if (total <= most && !crowded &&
           (complete || (has_k ? total >= set.k : !has_m && L >= share_of(set.top_p, head.Z + head.slack))))
         head.listed = total;
       later = !kWhole && head.listed < 0;
@@ -1326,7 +1344,7 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
       // ---- the cuts and the draw over the slices ----
       float edge = -FLT_MAX;  // the cut's logit
       auto weigh = [&](unsigned int j, float x) -> unsigned long long {
-        if (!(x >= edge) || (kWhole && cut_key(x, j) > kept.cut)) return 0ull;
+        if (!(x >= edge) || (kWhole && cut_key<E>(x, j) > kept.cut)) return 0ull;
         const unsigned long long w = weight(x, M, s);
         return w >= kept.least ? w : 0ull;
       };
@@ -1357,7 +1375,7 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
       if (kWhole) {
         auto cut_at = [&](unsigned long long key) {
           kept.cut = key;
-          edge = logit_of(key);
+          edge = logit_of<E>(key);
         };
         if (has_k) cut_at(slice_crossing<E, kStaged, true>(c, sl, M, s, set.k - 1, weigh));
         if (has_p) {
@@ -1384,7 +1402,7 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
     if (!good) kept.cut = 0;
     if (kWhole) {
       if (a.filtered) {
-        const float bound = good ? logit_of(kept.cut) : INFINITY;
+        const float bound = good ? logit_of<E>(kept.cut) : INFINITY;
         for (int v = tid; v < sl.nv; v += kThreadsS)
           write_kept<E>(a, row, sl.first, v, sl.at(v), aligned_out && sl.first + (v + 1) * VEC <= a.V, kept, bound, M, s);
       }
@@ -1467,7 +1485,7 @@ __global__ void __launch_bounds__(256) filter_write_kernel(const SampleArgs a, i
   Kept kept;
   kept.cut = head.cut;
   kept.least = max(1ull, __float2ull_rn(__fmul_rn(fminf(fmaxf(set.min_p, 0.f), 1.f), kScale)));
-  const float edge = head.good ? logit_of(kept.cut) : INFINITY;
+  const float edge = head.good ? logit_of<E>(kept.cut) : INFINITY;
 #pragma unroll
   for (int i = 0; i < kWriteVecs; ++i) {
     const int v = (blockIdx.y * kWriteVecs + i) * 256 + threadIdx.x;
@@ -1498,7 +1516,7 @@ Shape shape_of(int R, int V, bool bf16) {
   return s;
 }
 
-constexpr size_t kPlaceBytes = kPlaces * 2, kListBytes = kList * 16;
+constexpr size_t kPlaceBytes = kPlaces * 2, kListBytes = kList * 16, kLongBytes = (kLongList + 1) * 16;
 static_assert(sizeof(Bins) <= kPlaceBytes && 2 * sizeof(ListBins) <= sizeof(Bins) && kGroupSums * 8 <= kPlaceBytes,
               "they share the places' memory");
 
@@ -1544,7 +1562,7 @@ cudaError_t launch(const SampleArgs& a, const Shape& s, const Space& sp, cudaStr
     cfg.dynamicSmemBytes = static_cast<size_t>(s.nvs) * 16 + kPlaceBytes + kListBytes;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, filter_row_kernel<E, kStaged, true>, a, 0, s.nvec, s.nvs, in, out, sp.heads, sp.lists,
-                              none, sp.queued, -0.f);
+                              kList, none, sp.queued, -0.f);
   }
   if constexpr (kStaged) {
     // blocks a row of the queue is shared by: few rows, so more than C
@@ -1560,7 +1578,7 @@ cudaError_t launch(const SampleArgs& a, const Shape& s, const Space& sp, cudaStr
       cfg.numAttrs = 1;
       attr[0].val.clusterDim.x = s.C;
       cudaError_t e = cudaLaunchKernelEx(&cfg, filter_row_kernel<E, true, false>, a, row0, s.nvec, s.nvs, in, out,
-                                         sp.heads, sp.lists, sp.queue, sp.queued, -0.f);
+                                         sp.heads, sp.lists, kList, sp.queue, sp.queued, -0.f);
       if (e != cudaSuccess) return e;
       // the next ones start early and wait for what they read
       cfg.gridDim = dim3(static_cast<unsigned int>(rows));
@@ -1573,12 +1591,12 @@ cudaError_t launch(const SampleArgs& a, const Shape& s, const Space& sp, cudaStr
       const int clusters = rows < kFusedBlocks / Cq ? rows : kFusedBlocks / Cq;
       cfg.gridDim = dim3(static_cast<unsigned int>(clusters * Cq));
       cfg.blockDim = dim3(kThreadsS);
-      cfg.dynamicSmemBytes = static_cast<size_t>(nvq) * 16 + kPlaceBytes + kListBytes;
+      cfg.dynamicSmemBytes = static_cast<size_t>(nvq) * 16 + kPlaceBytes + kLongBytes;
       cfg.attrs = attr;
       cfg.numAttrs = 2;
       attr[0].val.clusterDim.x = Cq;
       e = cudaLaunchKernelEx(&cfg, filter_row_kernel<E, true, true>, a, row0, s.nvec, nvq, in, out, sp.heads, sp.lists,
-                             sp.queue, sp.queued, -0.f);
+                             kLongList, sp.queue, sp.queued, -0.f);
       if (e != cudaSuccess) return e;
       if (a.filtered) {
         cfg.gridDim = dim3(static_cast<unsigned int>(rows), (s.nvec + 256 * kWriteVecs - 1) / (256 * kWriteVecs));
@@ -1602,7 +1620,7 @@ size_t filtered_sample_workspace(int R, int V, bool bf16) {
 }
 
 cudaError_t filtered_sample_prepare() {
-  const int most = static_cast<int>(kMaxSliceS + kPlaceBytes + kListBytes);
+  const int most = static_cast<int>(kMaxSliceS + kPlaceBytes + kLongBytes);
   const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
   cudaError_t e[] = {cudaFuncSetAttribute(filter_row_kernel<BF16, true, true>, attr, most),
                      cudaFuncSetAttribute(filter_row_kernel<F32, true, true>, attr, most),
