@@ -2,6 +2,13 @@
 // (sm_103a).  Copies move 16-byte pieces; page numbers come from counts of
 // references recomputed from the tables, so there is no allocator state that
 // could drift from them.
+//
+// fork and compact first make a plan (reference counts, free pages, who gets
+// which) and then copy.  Where the counts fit one block's shared memory, both
+// happen in one cooperative launch: block 0 plans there while the others
+// wait for its flag, then all write the tables and copy.  One launch instead
+// of four, and no traffic through L2 for the counts, is most of a small
+// call's time.  Larger pools count in global memory, in a launch per step.
 #include <climits>
 
 #include "device_common.cuh"
@@ -14,6 +21,73 @@ constexpr int kPlanThreads = 1024;
 
 __device__ __forceinline__ void report(int32_t* status, int bits) {
   if (bits && status) atomicOr(status, bits);
+}
+
+// A fused launch's control words.  Zero at rest: its last block puts them back.
+struct __align__(16) Control {
+  unsigned int ready, done;
+};
+constexpr int kGroup = 128;                       // threads that share a copy
+constexpr int kGroups = kPlanThreads / kGroup;
+constexpr int kMaxShared = 200 * 1024;            // of the plan
+constexpr unsigned long long kWaitNs = 2000000000ull;
+
+// Block 0 has planned: everything it wrote is visible to who sees the flag.
+__device__ __forceinline__ void publish(Control* c) {
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    __threadfence();
+    asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(&c->ready), "r"(1u) : "memory");
+  }
+}
+// The others wait for it, 2 s at most; false: it never came.
+__device__ __forceinline__ bool await(Control* c, int* ok) {
+  if (threadIdx.x == 0) {
+    const unsigned long long t0 = global_ns();
+    *ok = 1;
+    while (!ld_acquire_gpu(&c->ready)) {
+      if (global_ns() - t0 > kWaitNs) {
+        *ok = 0;
+        break;
+      }
+      __nanosleep(100);
+    }
+  }
+  __syncthreads();
+  return *ok != 0;
+}
+__device__ __forceinline__ void leave(Control* c) {
+  __syncthreads();
+  if (threadIdx.x == 0 && atom_add_acq_rel_gpu(&c->done, 1u) + 1u == gridDim.x) {
+    c->ready = 0;
+    c->done = 0;
+  }
+}
+
+// Copies `tokens` tokens of a page by kGroup threads, eight pieces a thread
+// in flight where the tokens are contiguous.
+__device__ __forceinline__ void copy_tokens(const CacheView& cv, const char* src, char* dst, int tokens, int vecs,
+                                            int lane) {
+  const int total = tokens * vecs;
+  if (cv.token_stride == vecs * 16) {
+    const uint4* from = reinterpret_cast<const uint4*>(src) + lane;
+    uint4* to = reinterpret_cast<uint4*>(dst) + lane;
+    int left = total - lane;
+    for (; left > 7 * kGroup; left -= 8 * kGroup, from += 8 * kGroup, to += 8 * kGroup) {
+      uint4 w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = from[i * kGroup];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) to[i * kGroup] = w[i];
+    }
+    for (; left > 0; left -= kGroup, from += kGroup, to += kGroup) *to = *from;
+  } else {
+    for (int e = lane; e < total; e += kGroup) {
+      const int t = e / vecs;
+      const long long at = t * cv.token_stride + (e - t * vecs) * 16;
+      *reinterpret_cast<uint4*>(dst + at) = *reinterpret_cast<const uint4*>(src + at);
+    }
+  }
 }
 
 // ---- append ----------------------------------------------------------------
@@ -101,15 +175,17 @@ __device__ __forceinline__ int child_page(const ForkArgs& a, const Child& ch, in
   return p >= 0 && p < a.cache.pages ? p : -1;
 }
 
-// Workspace: refs[P], first[P] (cleared before the launch), order[P] the free
-// pages ascending, base[C] the first fresh rank of a sequence (sign bit: its
-// last page stays), count of free pages.
+// Workspace: control words, refs[P], first[P] (cleared before the launch that
+// counts in them), order[P] the free pages ascending, base[C] the first fresh
+// rank of a sequence (sign bit: its last page stays), count of free pages.
 struct ForkSpace {
+  Control* control;
   int *refs, *first, *order, *base, *nfree;
 };
 __host__ __device__ inline ForkSpace fork_space(void* ws, int P, int C) {
   ForkSpace s;
-  s.refs = static_cast<int*>(ws);
+  s.control = static_cast<Control*>(ws);
+  s.refs = static_cast<int*>(ws) + 16;
   s.first = s.refs + P;
   s.order = s.first + P;
   s.base = s.order + P;
@@ -160,10 +236,10 @@ __device__ __forceinline__ int block_scan(int v, int* scratch, int* total) {
   return incl;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const ForkArgs a, ForkSpace s) {
-  __shared__ int scratch[32];
+// From the counts (in shared or global memory): which last pages stay, every
+// sequence's first fresh rank, the free pages and who is left.  One block.
+__device__ void fork_plan(const ForkArgs& a, const ForkSpace& s, const int* refs, const int* first, int* scratch) {
   const int tid = threadIdx.x, P = a.cache.pages;
-  // which last pages stay, and every sequence's first fresh rank
   int fresh_total = 0;
   for (int c0 = 0; c0 < a.C; c0 += kPlanThreads) {
     const int c = c0 + tid;
@@ -172,7 +248,7 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const ForkArgs 
       const Child ch = child_of(a, c);
       if (ch.tail > 0) {
         const int p = child_page(a, ch, ch.full);
-        stays = p >= 0 && s.refs[p] == 0 && s.first[p] == a.C - c;
+        stays = p >= 0 && refs[p] == 0 && first[p] == a.C - c;
       }
       fresh = max(0, ch.need - ch.full - stays);
       a.new_lengths[c] = ch.keep;
@@ -182,20 +258,31 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const ForkArgs 
     if (c < a.C) s.base[c] = (fresh_total + incl - fresh) | (stays ? INT_MIN : 0);
     fresh_total += sum;
   }
-  // the free pages ascending; the first of them are given out
+  // the free pages ascending; the first of them are given out.  A thread takes
+  // kRun neighbours, so that a scan serves kRun * 1024 pages.
+  constexpr int kRun = 8;
   int before = 0;
-  for (int p0 = 0; p0 < P; p0 += kPlanThreads) {
-    const int p = p0 + tid;
-    const int refs = p < P ? s.refs[p] + (s.refs[p] == 0 && s.first[p] > 0) : 1;
+  for (int p0 = 0; p0 < P; p0 += kPlanThreads * kRun) {
+    const int q = p0 + tid * kRun;
+    int count[kRun], mine = 0;
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) {
+      count[i] = q + i < P ? refs[q + i] : 1;
+      if (count[i] == 0) count[i] = first[q + i] > 0;
+      mine += count[i] == 0;
+    }
     int sum;
-    const int incl = block_scan(refs == 0, scratch, &sum);
-    if (p < P) {
-      const int rank = before + incl - 1;
-      if (refs == 0) {
-        s.order[rank] = p;
-        if (rank >= fresh_total) a.free_pages[rank - fresh_total] = p;
+    int rank = before + block_scan(mine, scratch, &sum) - mine;
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) {
+      if (q + i >= P) break;
+      if (count[i] == 0) {
+        s.order[rank] = q + i;
+        if (rank >= fresh_total) a.free_pages[rank - fresh_total] = q + i;
+        else count[i] = 1;
+        ++rank;
       }
-      a.ref_counts[p] = refs + (refs == 0 && rank < fresh_total);
+      a.ref_counts[q + i] = count[i];
     }
     before += sum;
   }
@@ -208,51 +295,114 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const ForkArgs 
   }
 }
 
+__global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const ForkArgs a, ForkSpace s) {
+  __shared__ int scratch[32];
+  fork_plan(a, s, s.refs, s.first, scratch);
+}
+
 // Writes the rows of the new table and copies the kept tokens of partly
-// filled pages that did not stay: block (c, slice), a slice a layer's K or V.
-__global__ void __launch_bounds__(256) fork_write_kernel(const ForkArgs a, ForkSpace s) {
+// filled pages that did not stay: groups of threads take (sequence, table row
+// or one layer's K or V).
+__device__ void fork_write(const ForkArgs& a, const ForkSpace& s) {
   const CacheView& cv = a.cache;
   const int nfree = *s.nfree;
-  const int vecs = cv.row_bytes() / 16;
-  for (int c = blockIdx.x; c < a.C; c += gridDim.x) {
+  const int vecs = cv.row_bytes() / 16, parts = 1 + 2 * cv.layers;
+  const int lane = threadIdx.x % kGroup, groups = gridDim.x * (blockDim.x / kGroup);
+  const long long items = static_cast<long long>(a.C) * parts;
+  for (long long x = blockIdx.x * (blockDim.x / kGroup) + threadIdx.x / kGroup; x < items; x += groups) {
+    const int c = static_cast<int>(x / parts), y = static_cast<int>(x - static_cast<long long>(c) * parts) - 1;
     const Child ch = child_of(a, c);
     const int packed = s.base[c], base = packed & INT_MAX;
     const int kept = ch.full + (packed < 0);
-    if (blockIdx.y == 0) {
+    if (y < 0) {
       int32_t* row = a.new_table + static_cast<long long>(c) * a.table.max_pages;
-      for (int j = threadIdx.x; j < a.table.max_pages; j += blockDim.x) {
+      for (int j = lane; j < a.table.max_pages; j += kGroup) {
         int p = -1;
         if (j < kept) p = child_page(a, ch, j);
         else if (j < ch.need && base + j - kept < nfree) p = s.order[base + j - kept];
         row[j] = p;
       }
-    }
-    if (ch.tail > 0 && packed >= 0 && ch.full < ch.need && base < nfree) {
+    } else if (ch.tail > 0 && packed >= 0 && ch.full < ch.need && base < nfree) {
       const int from = child_page(a, ch, ch.full), to = s.order[base];
       if (from < 0) continue;
-      for (int y = blockIdx.y; y < 2 * cv.layers; y += gridDim.y) {
-        char* pool = (y & 1 ? cv.v : cv.k) + (y >> 1) * cv.layer_stride;
-        const char* src = pool + from * cv.page_stride;
-        char* dst = pool + to * cv.page_stride;
-        for (int e = threadIdx.x; e < ch.tail * vecs; e += blockDim.x) {
-          const int t = e / vecs;
-          const long long at = t * cv.token_stride + (e - t * vecs) * 16;
-          *reinterpret_cast<uint4*>(dst + at) = *reinterpret_cast<const uint4*>(src + at);
-        }
-      }
+      char* pool = (y & 1 ? cv.v : cv.k) + (y >> 1) * cv.layer_stride;
+      copy_tokens(cv, pool + from * cv.page_stride, pool + to * cv.page_stride, ch.tail, vecs, lane);
     }
   }
 }
 
+__global__ void __launch_bounds__(256) fork_write_kernel(const ForkArgs a, ForkSpace s) { fork_write(a, s); }
+
+// All of it in one cooperative launch.  The counts come by parent: ends[b][f]
+// sequences keep f full pages of parent b, so page j of b gains the sum of
+// ends[b][f] over f > j -- one addition a parent's page, however many
+// sequences share it.
+__global__ void __launch_bounds__(kPlanThreads, 1) fork_fused_kernel(const ForkArgs a, ForkSpace s) {
+  extern __shared__ int counts[];  // refs[P], first[P], ends[B][max_pages + 1]
+  __shared__ int scratch[32];
+  const int tid = threadIdx.x, lane = tid & 31, P = a.cache.pages, M = a.table.max_pages;
+  if (blockIdx.x == 0) {
+    int *refs = counts, *first = refs + P, *ends = first + P;
+    const int words = 2 * P + a.B * (M + 1);
+    for (int i = tid; i < words; i += kPlanThreads) counts[i] = 0;
+    __syncthreads();
+    int bad = 0;
+    for (int c = tid; c < a.C; c += kPlanThreads) {
+      const Child ch = child_of(a, c);
+      bad |= ch.bad;
+      if (ch.full > 0) atomicAdd(&ends[ch.parent * (M + 1) + ch.full], 1);
+      if (ch.tail > 0) {
+        const int p = child_page(a, ch, ch.full);
+        if (p < 0) bad |= kDataPageRange;
+        else atomicMax(&first[p], a.C - c);
+      }
+    }
+    __syncthreads();
+    for (int b = tid >> 5; b < a.B; b += kPlanThreads / 32) {
+      const int S = a.cache.page_size, len = min(max(a.lengths[b], 0), M * S);
+      const int most = len / S;  // full pages that anyone can keep
+      int beyond = 0;            // sequences that keep more than the pages seen so far
+      for (int j0 = (most + 31) / 32 * 32 - 32; j0 >= 0; j0 -= 32) {
+        const int j = j0 + lane;
+        int sum = j < most ? ends[b * (M + 1) + j + 1] : 0;  // ends at j + 1: keeps page j
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int o = __shfl_down_sync(0xffffffffu, sum, d);
+          if (lane + d < 32) sum += o;
+        }
+        sum += beyond;
+        if (j < most && sum > 0) {
+          const int p = a.table.ids[b * a.table.stride + j];
+          if (p >= 0 && p < P) atomicAdd(&refs[p], sum);
+          else bad |= kDataPageRange;
+        }
+        beyond = __shfl_sync(0xffffffffu, sum, 0);
+      }
+    }
+    report(a.status, bad);
+    __syncthreads();
+    fork_plan(a, s, refs, first, scratch);
+    publish(s.control);
+    __syncthreads();
+  } else if (!await(s.control, &scratch[0])) {
+    if (tid == 0) report(a.status, kWaitTimeout);
+    return;
+  }
+  fork_write(a, s);
+  leave(s.control);
+}
+
 // ---- compact -------------------------------------------------------------------
-// Workspace: refs[P] (cleared before the launch), to[P] the pages' new
-// numbers, from[P] the moved pages ascending, holes[P], moves.
+// Workspace: control words, refs[P] (cleared before the launch that counts in
+// them), to[P] the pages' new numbers, from[P] the moved pages ascending, holes[P], moves.
 struct CompactSpace {
+  Control* control;
   int *refs, *to, *from, *holes, *moves;
 };
 __host__ __device__ inline CompactSpace compact_space(void* ws, int P) {
   CompactSpace s;
-  s.refs = static_cast<int*>(ws);
+  s.control = static_cast<Control*>(ws);
+  s.refs = static_cast<int*>(ws) + 16;
   s.to = s.refs + P;
   s.from = s.to + P;
   s.holes = s.from + P;
@@ -260,44 +410,63 @@ __host__ __device__ inline CompactSpace compact_space(void* ws, int P) {
   return s;
 }
 
-__global__ void __launch_bounds__(256) compact_count_kernel(const CompactArgs a, CompactSpace s) {
-  for (int b = blockIdx.x; b < a.B; b += gridDim.x)
-    for (int j = threadIdx.x; j < a.table.max_pages; j += blockDim.x) {
-      const int p = a.table.ids[b * a.table.stride + j];
-      if (p >= a.cache.pages) report(a.status, kDataPageRange);
-      else if (p >= 0) atomicAdd(&s.refs[p], 1);
-    }
+__device__ void compact_count(const CompactArgs& a, int* refs, int first, int step) {
+  const long long entries = static_cast<long long>(a.B) * a.table.max_pages;
+  int bad = 0;
+  for (long long x = first; x < entries; x += step) {
+    const int b = static_cast<int>(x / a.table.max_pages);
+    const int p = a.table.ids[b * a.table.stride + (x - static_cast<long long>(b) * a.table.max_pages)];
+    if (p >= a.cache.pages) bad = kDataPageRange;
+    else if (p >= 0) atomicAdd(&refs[p], 1);
+  }
+  report(a.status, bad);
 }
 
-__global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const CompactArgs a, CompactSpace s) {
-  __shared__ int scratch[32];
+__global__ void __launch_bounds__(256) compact_count_kernel(const CompactArgs a, CompactSpace s) {
+  compact_count(a, s.refs, blockIdx.x * 256 + threadIdx.x, gridDim.x * 256);
+}
+
+// From the counts: how many pages are in use, which move and where to.  One block.
+__device__ void compact_plan(const CompactArgs& a, const CompactSpace& s, const int* refs, int* scratch) {
   const int tid = threadIdx.x, P = a.cache.pages;
   int mine = 0, n;
-  for (int p = tid; p < P; p += kPlanThreads) mine += s.refs[p] > 0;
+  for (int p = tid; p < P; p += kPlanThreads) mine += refs[p] > 0;
   block_scan(mine, scratch, &n);
+  // movers (in use, at or above n) and holes (free, below n) in one scan: below
+  // n only holes can occur, above it only movers
+  constexpr int kRun = 8;
   int moves = 0, holes = 0;
-  for (int p0 = 0; p0 < P; p0 += kPlanThreads) {
-    const int p = p0 + tid;
-    const bool live = p < P && s.refs[p] > 0;
-    const bool mover = live && p >= n, hole = p < n && !live;
-    int sum;
-    int incl = block_scan(mover, scratch, &sum);
-    if (mover) s.from[moves + incl - 1] = p;
-    moves += sum;
-    incl = block_scan(hole, scratch, &sum);
-    if (hole) s.holes[holes + incl - 1] = p;
-    holes += sum;
-    if (p < P && !mover) {
-      s.to[p] = p;
-      if (!hole) a.ref_counts[p] = p < n ? s.refs[p] : 0;
+  for (int p0 = 0; p0 < P; p0 += kPlanThreads * kRun) {
+    const int q = p0 + tid * kRun;
+    int count[kRun], m = 0, h = 0;
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) {
+      count[i] = q + i < P ? refs[q + i] : 0;
+      m += count[i] > 0 && q + i >= n;
+      h += q + i < min(n, P) && count[i] == 0;
     }
-    if (mover) a.ref_counts[p] = 0;
+    int sum_m = 0, sum_h = 0;
+    int at_m = 0, at_h = 0;
+    if (p0 + kPlanThreads * kRun > n) at_m = moves + block_scan(m, scratch, &sum_m) - m;
+    if (p0 < n) at_h = holes + block_scan(h, scratch, &sum_h) - h;
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) {
+      const int p = q + i;
+      if (p >= P) break;
+      const bool mover = count[i] > 0 && p >= n, hole = p < n && count[i] == 0;
+      if (mover) s.from[at_m++] = p;
+      else s.to[p] = p;
+      if (hole) s.holes[at_h++] = p;
+      else a.ref_counts[p] = p < n ? count[i] : 0;
+    }
+    moves += sum_m;
+    holes += sum_h;
   }
   __syncthreads();
   for (int i = tid; i < moves; i += kPlanThreads) {
     const int from = s.from[i], to = s.holes[i];
     s.to[from] = to;
-    a.ref_counts[to] = s.refs[from];
+    a.ref_counts[to] = refs[from];
   }
   if (tid == 0) {
     *a.n_live = n;
@@ -305,27 +474,71 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const Compac
   }
 }
 
-__global__ void __launch_bounds__(256) compact_move_kernel(const CompactArgs a, CompactSpace s) {
+__global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const CompactArgs a, CompactSpace s) {
+  __shared__ int scratch[32];
+  compact_plan(a, s, s.refs, scratch);
+}
+
+// Rewrites the table and moves the pages: groups of threads take (page, one
+// layer's K or V).
+__device__ void compact_move(const CompactArgs& a, const CompactSpace& s) {
   const CacheView& cv = a.cache;
   const int P = cv.pages;
-  for (int b = blockIdx.x; b < a.B; b += gridDim.x)
-    for (int j = threadIdx.x; j < a.table.max_pages; j += blockDim.x) {
-      const int p = a.table.ids[b * a.table.stride + j];
-      a.new_table[static_cast<long long>(b) * a.table.max_pages + j] = p >= 0 && p < P ? s.to[p] : -1;
-    }
-  const int moves = *s.moves, vecs = cv.row_bytes() / 16;
-  const long long jobs = static_cast<long long>(moves) * cv.layers * 2;
-  for (long long x = blockIdx.x; x < jobs; x += gridDim.x) {
-    const int i = static_cast<int>(x / (cv.layers * 2)), y = static_cast<int>(x - static_cast<long long>(i) * cv.layers * 2);
-    char* pool = (y & 1 ? cv.v : cv.k) + (y >> 1) * cv.layer_stride;
-    const char* src = pool + s.from[i] * cv.page_stride;
-    char* dst = pool + s.holes[i] * cv.page_stride;
-    for (int e = threadIdx.x; e < cv.page_size * vecs; e += blockDim.x) {
-      const int t = e / vecs;
-      const long long at = t * cv.token_stride + (e - t * vecs) * 16;
-      *reinterpret_cast<uint4*>(dst + at) = *reinterpret_cast<const uint4*>(src + at);
-    }
+  const long long entries = static_cast<long long>(a.B) * a.table.max_pages;
+  for (long long x = blockIdx.x * blockDim.x + threadIdx.x; x < entries; x += static_cast<long long>(gridDim.x) * blockDim.x) {
+    const int b = static_cast<int>(x / a.table.max_pages);
+    const int p = a.table.ids[b * a.table.stride + (x - static_cast<long long>(b) * a.table.max_pages)];
+    a.new_table[x] = p >= 0 && p < P ? s.to[p] : -1;
   }
+  const int moves = *s.moves, vecs = cv.row_bytes() / 16, parts = 2 * cv.layers;
+  const int lane = threadIdx.x % kGroup, groups = gridDim.x * (blockDim.x / kGroup);
+  const long long jobs = static_cast<long long>(moves) * parts;
+  for (long long x = blockIdx.x * (blockDim.x / kGroup) + threadIdx.x / kGroup; x < jobs; x += groups) {
+    const int i = static_cast<int>(x / parts), y = static_cast<int>(x - static_cast<long long>(i) * parts);
+    char* pool = (y & 1 ? cv.v : cv.k) + (y >> 1) * cv.layer_stride;
+    copy_tokens(cv, pool + s.from[i] * cv.page_stride, pool + s.holes[i] * cv.page_stride, cv.page_size, vecs, lane);
+  }
+}
+
+__global__ void __launch_bounds__(256) compact_move_kernel(const CompactArgs a, CompactSpace s) { compact_move(a, s); }
+
+__global__ void __launch_bounds__(kPlanThreads, 1) compact_fused_kernel(const CompactArgs a, CompactSpace s) {
+  extern __shared__ int counts[];  // refs[P]
+  __shared__ int scratch[32];
+  if (blockIdx.x == 0) {
+    for (int i = threadIdx.x; i < a.cache.pages; i += kPlanThreads) counts[i] = 0;
+    __syncthreads();
+    compact_count(a, counts, threadIdx.x, kPlanThreads);
+    __syncthreads();
+    compact_plan(a, s, counts, scratch);
+    publish(s.control);
+    __syncthreads();
+  } else if (!await(s.control, &scratch[0])) {
+    if (threadIdx.x == 0) report(a.status, kWaitTimeout);
+    return;
+  }
+  compact_move(a, s);
+  leave(s.control);
+}
+
+// The fused launch: every block resident at once.
+template <typename A, typename S>
+cudaError_t launch_fused(void (*kernel)(A, S), const A& a, const S& s, int grid, size_t smem, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kPlanThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1] = {};
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a, s);
+}
+int fused_grid(long long items, int sm_count) {
+  const long long want = (items + kGroups - 1) / kGroups;
+  return static_cast<int>(want < 1 ? 1 : want < sm_count ? want : sm_count);
 }
 
 size_t up(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
@@ -342,30 +555,53 @@ cudaError_t launch_append(const char* k_new, const char* v_new, long long new_st
   return cudaGetLastError();
 }
 
+cudaError_t cache_pages_prepare() {
+  cudaError_t e = cudaFuncSetAttribute(fork_fused_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(compact_fused_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared);
+  return e;
+}
+
 size_t fork_workspace(int pages, int C) {
-  return up((3 * static_cast<size_t>(pages) + static_cast<size_t>(C) + 1) * 4);
+  return up((16 + 3 * static_cast<size_t>(pages) + static_cast<size_t>(C) + 1) * 4);
 }
 
 cudaError_t launch_fork(const ForkArgs& a, void* ws, int sm_count, cudaStream_t stream) {
   const ForkSpace s = fork_space(ws, a.cache.pages, a.C);
+  const long long items = static_cast<long long>(a.C) * (1 + 2 * a.cache.layers);
+  // One block counts the parents' pages; beyond about 64 Ki table entries that
+  // takes longer than three more launches.
+  const long long entries = static_cast<long long>(a.B) * (a.table.max_pages + 1);
+  const long long words = 2ll * a.cache.pages + entries;
+  if (words * 4 <= kMaxShared)
+    return launch_fused(fork_fused_kernel, a, s, fused_grid(items, sm_count), static_cast<size_t>(words) * 4, stream);
   cudaError_t e = cudaMemsetAsync(s.refs, 0, 2 * static_cast<size_t>(a.cache.pages) * 4, stream);
   if (e != cudaSuccess) return e;
   const int blocks = a.C < sm_count * 8 ? a.C : sm_count * 8;
   if (blocks > 0) fork_count_kernel<<<blocks, 256, 0, stream>>>(a, s);
   fork_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a, s);
-  const int slices = 2 * a.cache.layers < 64 ? 2 * a.cache.layers : 64;
-  if (blocks > 0) fork_write_kernel<<<dim3(blocks, slices), 256, 0, stream>>>(a, s);
+  const long long want = (items * kGroup + 255) / 256;
+  if (items > 0)
+    fork_write_kernel<<<static_cast<int>(want < sm_count * 8 ? want : sm_count * 8), 256, 0, stream>>>(a, s);
   return cudaGetLastError();
 }
 
-size_t compact_workspace(int pages) { return up((4 * static_cast<size_t>(pages) + 1) * 4); }
+size_t compact_workspace(int pages) { return up((16 + 4 * static_cast<size_t>(pages) + 1) * 4); }
 
 cudaError_t launch_compact(const CompactArgs& a, void* ws, int sm_count, cudaStream_t stream) {
   const CompactSpace s = compact_space(ws, a.cache.pages);
-  cudaError_t e = cudaMemsetAsync(s.refs, 0, static_cast<size_t>(a.cache.pages) * 4, stream);
+  const long long entries = static_cast<long long>(a.B) * a.table.max_pages;
+  const size_t smem = static_cast<size_t>(a.cache.pages) * 4;
+  // (the same trade: one block counts the entries)
+  if (smem <= kMaxShared && entries <= (1 << 16)) {
+    const long long most = a.cache.pages / 2;  // pages that can move
+    return launch_fused(compact_fused_kernel, a, s, fused_grid(most * 2 * a.cache.layers, sm_count), smem, stream);
+  }
+  cudaError_t e = cudaMemsetAsync(s.refs, 0, smem, stream);
   if (e != cudaSuccess) return e;
-  const int blocks = a.B < sm_count * 8 ? a.B : sm_count * 8;
-  if (blocks > 0) compact_count_kernel<<<blocks, 256, 0, stream>>>(a, s);
+  const long long want = (entries + 255) / 256;
+  if (entries > 0)
+    compact_count_kernel<<<static_cast<int>(want < sm_count * 8 ? want : sm_count * 8), 256, 0, stream>>>(a, s);
   compact_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a, s);
   compact_move_kernel<<<sm_count * 8, 256, 0, stream>>>(a, s);
   return cudaGetLastError();

@@ -90,6 +90,7 @@ struct ForkArgs {
   int32_t *new_table, *new_lengths, *ref_counts, *free_pages, *n_free;
   int32_t* status;
 };
+cudaError_t cache_pages_prepare();
 size_t fork_workspace(int pages, int C);
 cudaError_t launch_fork(const ForkArgs& a, void* ws, int sm_count, cudaStream_t stream);
 

@@ -30,6 +30,7 @@ spec_status_t device_sms(int* sms) {
     cudaError_t e = cudaDeviceGetAttribute(&g_sms[dev], cudaDevAttrMultiProcessorCount, dev);
     if (e == cudaSuccess) e = specv::attention_prepare();
     if (e == cudaSuccess) e = specv::filtered_sample_prepare();
+    if (e == cudaSuccess) e = specv::cache_pages_prepare();
     g_err[dev] = e;
   });
   *sms = g_sms[dev];

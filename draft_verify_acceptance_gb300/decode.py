@@ -17,7 +17,6 @@ other strides free (a layer of a larger tensor, K and V interleaved), the same f
 and V.  A page table is int32 [B, max_pages].
 """
 import ctypes
-import math
 import threading
 from typing import NamedTuple
 
@@ -92,81 +91,95 @@ class SampleResult(NamedTuple):
     status: torch.Tensor      # int32 [1] with debug, else None
 
 
-def _workspace(kind, device, stream, nbytes, given):
-    """The caller's workspace, or one kept for this kind of call, device and stream (zero-filled
-    when made, as spec_paged_attention asks)."""
+_raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream's handle, without a Stream object
+
+
+def _workspace(kind, index, stream, nbytes, given):
+    """The caller's workspace, or one kept for this kind of call, device and stream.  It is zero-filled
+    when made; every call leaves it fit for the next."""
     if given is not None:
-        if given.device != device or not given.is_contiguous():
-            raise ValueError(f"workspace must be contiguous on {device}")
+        if given.get_device() != index or not given.is_contiguous():
+            raise ValueError(f"workspace must be contiguous on cuda:{index}")
         if given.numel() * given.element_size() < nbytes:
             raise ValueError(f"workspace holds {given.numel() * given.element_size()} bytes, {nbytes} are needed")
         return given.data_ptr(), given.numel() * given.element_size()
-    key = (kind, device.index, stream)
-    with _ws_lock:
-        ws = _ws.get(key)
-        if ws is None or ws.numel() < nbytes:
-            ws = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
-            _ws[key] = ws
-    return ws.data_ptr(), ws.numel()
+    if nbytes == 0:
+        return None, 0
+    key = (kind, index, stream)
+    kept = _ws.get(key)
+    if kept is None or kept[2] < nbytes:
+        with _ws_lock:
+            kept = _ws.get(key)
+            if kept is None or kept[2] < nbytes:
+                ws = torch.zeros(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
+                kept = _ws[key] = (ws, ws.data_ptr(), nbytes)
+    return kept[1], kept[2]
 
 
 def _on_stream(fn):
     """Runs a call with its device and, when one is given, its stream current, so that what it allocates
-    belongs to the stream that uses it."""
+    belongs to the stream that uses it; passes the device's index and the stream's handle."""
     def call(first, *args, stream=None, **kw):
         if not isinstance(first, torch.Tensor) or not first.is_cuda:
             where = first.device if isinstance(first, torch.Tensor) else type(first).__name__
             raise ValueError(f"{fn.__name__} takes CUDA tensors (got {where})")
+        index = first.get_device()
         if stream is not None:
             with torch.cuda.stream(stream):
-                return fn(first, *args, _stream=stream.cuda_stream, **kw)
-        device = first.device
-        if device.index != torch.cuda.current_device():
-            with torch.cuda.device(device):
-                return fn(first, *args, _stream=torch.cuda.current_stream(device).cuda_stream, **kw)
-        return fn(first, *args, _stream=torch.cuda.current_stream(device).cuda_stream, **kw)
+                return fn((index, stream.cuda_stream), first, *args, **kw)
+        if index != torch.cuda.current_device():
+            with torch.cuda.device(index):
+                return fn((index, _raw_stream(index)), first, *args, **kw)
+        return fn((index, _raw_stream(index)), first, *args, **kw)
     call.__name__, call.__doc__, call.__wrapped__ = fn.__name__, fn.__doc__, fn
     return call
 
 
-def _ints(t, name, shape, device):
+def _ints(t, name, shape, index):
     """The pointer of a contiguous int32 tensor of a shape."""
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32:
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32:
         raise TypeError(f"{name} must be an int32 tensor")
-    if t.shape != shape or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous {tuple(shape)} on {device}, "
+    if t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {tuple(shape)} on cuda:{index}, "
                          f"got {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
-def _table(t, B, device):
+def _table(t, B, index):
     """(pointer, row stride, max_pages) of a page table; its rows may be strided."""
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32:
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32:
         raise TypeError("page_table must be an int32 tensor")
-    if t.dim() != 2 or t.shape[0] != B or t.device != device:
-        raise ValueError(f"page_table must be [{B}, max_pages] on {device}, got {tuple(t.shape)} on {t.device}")
+    if t.dim() != 2 or t.shape[0] != B or t.get_device() != index:
+        raise ValueError(f"page_table must be [{B}, max_pages] on cuda:{index}, got {tuple(t.shape)} on {t.device}")
     M = t.shape[1]
+    if t.is_contiguous():
+        return t.data_ptr(), M, M
     if M > 1 and t.stride(1) != 1:
         raise ValueError("page_table rows must be contiguous")
     return t.data_ptr(), max(t.stride(0), M) if B > 1 else M, M
 
 
-def _cache(k, v, layered, device):
-    dt = _DTYPES.get(k.dtype)
-    if dt is None or v.dtype != k.dtype:
+def _cache(k, v, layered, index):
+    dtype = k.dtype
+    dt = _DTYPES.get(dtype)
+    if dt is None or v.dtype is not dtype:
         raise TypeError(f"k_pages and v_pages must both be float32 or bfloat16, got {k.dtype} and {v.dtype}")
-    dims = k.dim()
+    shape, stride = k.shape, k.stride()
+    dims = len(shape)
     if dims != 4 and not (layered and dims == 5):
         raise ValueError("a cache tensor is [pages, page_size, heads, head_dim]"
                          + (" or [layers, pages, page_size, heads, head_dim]" if layered else ""))
-    shape, stride = k.shape, k.stride()
-    if v.shape != shape or v.stride() != stride or k.device != device or v.device != device:
+    if v.shape != shape or v.stride() != stride or k.get_device() != index or v.get_device() != index:
         raise ValueError("k_pages and v_pages must have the same shape, strides and device")
-    P, S, H, D = shape[-4:]
-    if (D > 1 and stride[-1] != 1) or (H > 1 and stride[-2] != D):
+    if dims == 5:
+        L, P, S, H, D = shape
+        ls, ps, ts, hs, ds = stride
+    else:
+        (P, S, H, D), (ps, ts, hs, ds) = shape, stride
+        L, ls = 1, 0
+    if (D > 1 and ds != 1) or (H > 1 and hs != D):
         raise ValueError("the last two dimensions (heads, head_dim) of a cache tensor must be contiguous")
-    return _Cache(k.data_ptr(), v.data_ptr(), stride[0] if dims == 5 else 0, stride[-4],
-                  stride[-3] if S > 1 else max(stride[-3], H * D), shape[0] if dims == 5 else 1, P, S, H, D, dt)
+    return _Cache(k.data_ptr(), v.data_ptr(), ls, ps, ts if S > 1 else max(ts, H * D), L, P, S, H, D, dt)
 
 
 def _raise(rc, what):
@@ -174,11 +187,11 @@ def _raise(rc, what):
 
 
 def _status(debug, device):
-    return torch.zeros(1, dtype=torch.int32, device=device) if debug else None
-
-
-def _p(t):
-    return None if t is None else t.data_ptr()
+    """The status word (None without debug) and its pointer."""
+    if not debug:
+        return None, None
+    t = torch.zeros(1, dtype=torch.int32, device=device)
+    return t, t.data_ptr()
 
 
 def attention_workspace_size(B, Q, Hq, heads, head_dim, dtype):
@@ -188,8 +201,8 @@ def attention_workspace_size(B, Q, Hq, heads, head_dim, dtype):
 
 
 @_on_stream
-def paged_attention(q, k_pages, v_pages, page_table, lengths, scale=None, *, return_lse=False, out=None,
-                    workspace=None, debug=False, _stream=0):
+def paged_attention(at, q, k_pages, v_pages, page_table, lengths, scale=None, *, return_lse=False, out=None,
+                    workspace=None, debug=False):
     """Attention of the newest Q tokens of each sequence over its paged cache.
 
     q [B, Q, Hq, D] (strides free but the last; D 64 or 128), k_pages / v_pages
@@ -200,35 +213,38 @@ def paged_attention(q, k_pages, v_pages, page_table, lengths, scale=None, *, ret
     1 / sqrt(D).  Returns out [B, Q, Hq, D], with ``return_lse`` (out, lse float32
     [B, Q, Hq]); a query that sees nothing gets 0 and -inf.
     """
-    if q.dim() != 4:
+    index, stream = at
+    shape, st = q.shape, q.stride()
+    if len(shape) != 4:
         raise ValueError("q must be [B, Q, Hq, D]")
-    device = q.device
-    B, Q, Hq, D = q.shape
-    c = _cache(k_pages, v_pages, False, device)
-    if q.dtype != k_pages.dtype:
+    B, Q, Hq, D = shape
+    c = _cache(k_pages, v_pages, False, index)
+    if q.dtype is not k_pages.dtype:
         raise TypeError(f"q is {q.dtype}, the cache {k_pages.dtype}")
-    if D != c.head_dim or Hq % c.heads:
-        raise ValueError(f"q has {Hq} heads of {D}, the cache {c.heads} of {c.head_dim}")
-    st = q.stride()
+    heads = c.heads
+    if D != c.head_dim or Hq % heads:
+        raise ValueError(f"q has {Hq} heads of {D}, the cache {heads} of {c.head_dim}")
     if D > 1 and st[3] != 1:
         raise ValueError("q's last dimension must be contiguous")
-    table, ts, M = _table(page_table, B, device)
-    lens = _ints(lengths, "lengths", (B,), device)
+    table, ts, M = _table(page_table, B, index)
+    lens = _ints(lengths, "lengths", (B,), index)
     if out is None:
-        out = torch.empty((B, Q, Hq, D), dtype=q.dtype, device=device)
-    elif out.shape != q.shape or out.dtype != q.dtype or out.device != device or not out.is_contiguous():
+        out = torch.empty(shape, dtype=q.dtype, device=q.device)
+    elif out.shape != shape or out.dtype is not q.dtype or out.get_device() != index or not out.is_contiguous():
         raise ValueError("out must be contiguous, shaped and typed as q")
-    lse = torch.empty((B, Q, Hq), dtype=torch.float32, device=device) if return_lse else None
-    status = _status(debug, device)
-    need = _lib.spec_attention_workspace_size(B, Q, Hq, c.heads, D, c.dtype)
+    lse = lse_at = None
+    if return_lse:
+        lse = torch.empty((B, Q, Hq), dtype=torch.float32, device=q.device)
+        lse_at = lse.data_ptr()
+    status, status_at = _status(debug, q.device)
+    need = _lib.spec_attention_workspace_size(B, Q, Hq, heads, D, c.dtype)
     if need == 0:
         _raise(ERR_UNSUPPORTED, f"paged_attention with head_dim {D}")
-    ws, nbytes = _workspace("attention", device, _stream, need, workspace)
+    ws, nbytes = _workspace("attention", index, stream, need, workspace)
     # the stride of a dimension of one element is free in torch
     rc = _lib.spec_paged_attention(
-        q.data_ptr(), st[0] if B > 1 else 0, st[1] if Q > 1 else 0, st[2] if Hq > 1 else 0, ctypes.byref(c), table, ts, M,
-        lens, B, Q, Hq, 1.0 / math.sqrt(D) if scale is None else float(scale), out.data_ptr(), _p(lse), ws, nbytes,
-        _stream, _p(status))
+        q.data_ptr(), st[0] if B > 1 else 0, st[1] if Q > 1 else 0, st[2] if Hq > 1 else 0, c, table, ts, M, lens, B, Q, Hq,
+        D ** -0.5 if scale is None else scale, out.data_ptr(), lse_at, ws, nbytes, stream, status_at)
     if rc != OK:
         _raise(rc, "spec_paged_attention")
     if debug:
@@ -237,7 +253,7 @@ def paged_attention(q, k_pages, v_pages, page_table, lengths, scale=None, *, ret
 
 
 @_on_stream
-def cache_append(k_new, v_new, k_pages, v_pages, page_table, lengths, starts=None, *, debug=False, _stream=0):
+def cache_append(at, k_new, v_new, k_pages, v_pages, page_table, lengths, starts=None, *, debug=False):
     """Writes new tokens' keys and values into their pages (in place).
 
     k_new / v_new [T, heads, head_dim] with ``starts`` int32 [B + 1] (sequence b's new
@@ -246,41 +262,41 @@ def cache_append(k_new, v_new, k_pages, v_pages, page_table, lengths, starts=Non
     sequence.  Rows may be strided (a slice of a fused projection).  Returns the status
     word with ``debug``, else None.
     """
-    device = k_new.device
-    c = _cache(k_pages, v_pages, False, device)
-    if k_new.dtype != k_pages.dtype or v_new.dtype != k_pages.dtype:
+    index, stream = at
+    c = _cache(k_pages, v_pages, False, index)
+    if k_new.dtype is not k_pages.dtype or v_new.dtype is not k_pages.dtype:
         raise TypeError(f"the new tokens are {k_new.dtype}, {v_new.dtype}, the cache {k_pages.dtype}")
-    if k_new.shape != v_new.shape or k_new.stride() != v_new.stride() or v_new.device != device:
+    shape, st = k_new.shape, k_new.stride()
+    if v_new.shape != shape or v_new.stride() != st or v_new.get_device() != index:
         raise ValueError("k_new and v_new must have the same shape, strides and device")
     B = lengths.shape[0]
     H, D = c.heads, c.head_dim
-    shape, st = k_new.shape, k_new.stride()
     if starts is not None:
-        if k_new.dim() != 3 or shape[1:] != (H, D):
+        if len(shape) != 3 or shape[1] != H or shape[2] != D:
             raise ValueError(f"with starts, k_new must be [T, {H}, {D}]")
         T, row = shape[0], st[0]
+        first = _ints(starts, "starts", (B + 1,), index)
     else:
-        if k_new.dim() != 4 or shape[0] != B or shape[2:] != (H, D):
+        if len(shape) != 4 or shape[0] != B or shape[2] != H or shape[3] != D:
             raise ValueError(f"without starts, k_new must be [{B}, n, {H}, {D}]")
         T, row = B * shape[1], st[1] if shape[1] > 1 else st[0]
         if B > 1 and shape[1] > 1 and st[0] != shape[1] * st[1]:
             raise ValueError("without starts, the rows of k_new must lie at one stride")
+        first = None
     if (D > 1 and st[-1] != 1) or (H > 1 and st[-2] != D):
         raise ValueError("heads and head_dim of k_new must be contiguous")
-    table, ts, M = _table(page_table, B, device)
-    lens = _ints(lengths, "lengths", (B,), device)
-    first = None if starts is None else _ints(starts, "starts", (B + 1,), device)
-    status = _status(debug, device)
-    rc = _lib.spec_cache_append(k_new.data_ptr(), v_new.data_ptr(), row if T > 1 else H * D, T, first, ctypes.byref(c),
-                                table, ts, M, lens, B, _stream, _p(status))
+    table, ts, M = _table(page_table, B, index)
+    lens = _ints(lengths, "lengths", (B,), index)
+    status, status_at = _status(debug, k_new.device)
+    rc = _lib.spec_cache_append(k_new.data_ptr(), v_new.data_ptr(), row if T > 1 else H * D, T, first, c, table, ts, M, lens,
+                                B, stream, status_at)
     if rc != OK:
         _raise(rc, "spec_cache_append")
     return status
 
 
 @_on_stream
-def cache_fork(k_pages, v_pages, page_table, lengths, parents, keep, room=0, *, workspace=None, debug=False,
-               _stream=0):
+def cache_fork(at, k_pages, v_pages, page_table, lengths, parents, keep, room=0, *, workspace=None, debug=False):
     """The next step's sequences from the current ones.
 
     Sequence c of the next step continues sequence ``parents[c]`` (-1: a new one) with its
@@ -290,67 +306,67 @@ def cache_fork(k_pages, v_pages, page_table, lengths, parents, keep, room=0, *, 
     end, and their pages are free.  Returns a ForkResult: the new page table and lengths,
     the references to each page, and the free pages.
     """
-    device = k_pages.device
-    c = _cache(k_pages, v_pages, True, device)
+    index, stream = at
+    c = _cache(k_pages, v_pages, True, index)
     B, C = lengths.shape[0], parents.shape[0]
-    table, ts, M = _table(page_table, B, device)
-    lens = _ints(lengths, "lengths", (B,), device)
-    par, kp = _ints(parents, "parents", (C,), device), _ints(keep, "keep", (C,), device)
+    table, ts, M = _table(page_table, B, index)
+    lens = _ints(lengths, "lengths", (B,), index)
+    par, kp = _ints(parents, "parents", (C,), index), _ints(keep, "keep", (C,), index)
     P = c.pages
     # one allocation; the results are views of it
-    buf = torch.empty(C * M + C + 2 * P + 1, dtype=torch.int32, device=device)
-    new, lens_new, refs, free, n_free = buf.split_with_sizes((C * M, C, P, P, 1))
-    status = _status(debug, device)
-    ws, nbytes = _workspace("pages", device, _stream, _lib.spec_cache_fork_workspace_size(P, C), workspace)
+    n = C * M
+    buf = torch.empty(n + C + 2 * P + 1, dtype=torch.int32, device=k_pages.device)
+    new, lens_new, refs, free, n_free = buf.split_with_sizes((n, C, P, P, 1))
+    status, status_at = _status(debug, k_pages.device)
+    ws, nbytes = _workspace("fork", index, stream, _lib.spec_cache_fork_workspace_size(P, C), workspace)
     base = buf.data_ptr()
-    rc = _lib.spec_cache_fork(
-        ctypes.byref(c), table, ts, M, lens, B, par, kp, C, int(room), base, base + 4 * C * M, base + 4 * (C * M + C),
-        base + 4 * (C * M + C + P), base + 4 * (C * M + C + 2 * P), ws, nbytes, _stream, _p(status))
+    rc = _lib.spec_cache_fork(c, table, ts, M, lens, B, par, kp, C, room, base, base + 4 * n, base + 4 * (n + C),
+                              base + 4 * (n + C + P), base + 4 * (n + C + 2 * P), ws, nbytes, stream, status_at)
     if rc != OK:
         _raise(rc, "spec_cache_fork")
     return ForkResult(new.view(C, M), lens_new, refs, free, n_free, status)
 
 
 @_on_stream
-def cache_compact(k_pages, v_pages, page_table, *, workspace=None, debug=False, _stream=0):
+def cache_compact(at, k_pages, v_pages, page_table, *, workspace=None, debug=False):
     """Moves the pages in use (entries >= 0 of the page table) to the front of the pool, in place,
     all layers: with n in use, those at or above n fill the unused ones below n, in
     ascending order.  Returns a CompactResult: the rewritten page table, the references
     to each page, and n.
     """
-    device = k_pages.device
-    c = _cache(k_pages, v_pages, True, device)
+    index, stream = at
+    c = _cache(k_pages, v_pages, True, index)
     B = page_table.shape[0]
-    table, ts, M = _table(page_table, B, device)
+    table, ts, M = _table(page_table, B, index)
     P = c.pages
-    buf = torch.empty(B * M + P + 1, dtype=torch.int32, device=device)
-    new, refs, n_live = buf.split_with_sizes((B * M, P, 1))
-    status = _status(debug, device)
-    ws, nbytes = _workspace("pages", device, _stream, _lib.spec_cache_compact_workspace_size(P), workspace)
+    n = B * M
+    buf = torch.empty(n + P + 1, dtype=torch.int32, device=k_pages.device)
+    new, refs, n_live = buf.split_with_sizes((n, P, 1))
+    status, status_at = _status(debug, k_pages.device)
+    ws, nbytes = _workspace("compact", index, stream, _lib.spec_cache_compact_workspace_size(P), workspace)
     base = buf.data_ptr()
-    rc = _lib.spec_cache_compact(ctypes.byref(c), table, ts, M, B, base, base + 4 * B * M, base + 4 * (B * M + P), ws,
-                                 nbytes, _stream, _p(status))
+    rc = _lib.spec_cache_compact(c, table, ts, M, B, base, base + 4 * n, base + 4 * (n + P), ws, nbytes, stream, status_at)
     if rc != OK:
         _raise(rc, "spec_cache_compact")
     return CompactResult(new.view(B, M), refs, n_live, status)
 
 
-def _setting(v, off, kind, name, R, device):
+def _setting(v, off, kind, name, R, index):
     """(scalar, pointer) of a sampling setting: None, a number for every row, or one a row."""
     if v is None:
         return off, None
     if not isinstance(v, torch.Tensor):
         return v, None
-    if v.dtype != kind:
+    if v.dtype is not kind:
         raise TypeError(f"{name} must be {kind}, got {v.dtype}")
-    if v.numel() != R or v.device != device or not v.is_contiguous():
-        raise ValueError(f"{name} must hold one value a row on {device}")
+    if v.numel() != R or v.get_device() != index or not v.is_contiguous():
+        raise ValueError(f"{name} must hold one value a row on cuda:{index}")
     return off, v.data_ptr()
 
 
 @_on_stream
-def filtered_sample(logits, uniforms, temperature=1.0, *, top_k=None, top_p=None, min_p=None, return_filtered=False,
-                    out=None, workspace=None, debug=False, _stream=0):
+def filtered_sample(at, logits, uniforms, temperature=1.0, *, top_k=None, top_p=None, min_p=None, return_filtered=False,
+                    out=None, workspace=None, debug=False):
     """One token per row of ``logits`` [..., V] (float32 or bfloat16; rows may be strided when
     two-dimensional) from its truncated softmax, by the given uniforms [...].
 
@@ -361,11 +377,12 @@ def filtered_sample(logits, uniforms, temperature=1.0, *, top_k=None, top_p=None
     SampleResult: tokens, p (the token's probability among the kept ones), n_kept and, with
     ``return_filtered``, the logits with -inf for what was not kept -- rows for ``verify``,
     whose accept test then holds for the truncated distributions.  ``out`` may give a
-    preallocated tensor for those.
+    preallocated tensor for those (the logits themselves too).
     """
-    if logits.dim() < 1:
+    index, stream = at
+    shape, device = logits.shape, logits.device
+    if len(shape) < 1:
         raise ValueError("logits must be [..., V]")
-    device, shape = logits.device, logits.shape
     dt = _DTYPES.get(logits.dtype)
     if dt is None:
         raise TypeError(f"logits must be float32 or bfloat16, got {logits.dtype}")
@@ -378,30 +395,33 @@ def filtered_sample(logits, uniforms, temperature=1.0, *, top_k=None, top_p=None
     R = rows.numel()
     if logits.is_contiguous():
         stride = V
-    elif logits.dim() == 2 and logits.stride(1) == 1 and logits.stride(0) >= V:
+    elif len(shape) == 2 and logits.stride(1) == 1 and logits.stride(0) >= V:
         stride = logits.stride(0)
     else:
         raise ValueError("the rows of logits must be contiguous, and at one stride")
-    if uniforms.dtype != torch.float32 or uniforms.shape != rows or uniforms.device != device or not uniforms.is_contiguous():
+    if uniforms.dtype is not torch.float32 or uniforms.shape != rows or uniforms.get_device() != index or not uniforms.is_contiguous():
         raise ValueError(f"uniforms must be contiguous float32 {tuple(rows)} on {device}")
-    T, Tp = _setting(temperature, 1.0, torch.float32, "temperature", R, device)
-    k, kp = _setting(top_k, 0, torch.int32, "top_k", R, device)
-    p, pp = _setting(top_p, 1.0, torch.float32, "top_p", R, device)
-    m, mp = _setting(min_p, 0.0, torch.float32, "min_p", R, device)
+    T, Tp = _setting(temperature, 1.0, torch.float32, "temperature", R, index)
+    k, kp = _setting(top_k, 0, torch.int32, "top_k", R, index)
+    p, pp = _setting(top_p, 1.0, torch.float32, "top_p", R, index)
+    m, mp = _setting(min_p, 0.0, torch.float32, "min_p", R, index)
     tokens = torch.empty(rows, dtype=torch.int32, device=device)
     prob = torch.empty(rows, dtype=torch.float32, device=device)
     n_kept = torch.empty(rows, dtype=torch.int32, device=device)
+    out_at = None
     if out is not None:
-        if out.shape != shape or out.dtype != logits.dtype or out.device != device or not out.is_contiguous():
+        if out.shape != shape or out.dtype is not logits.dtype or out.get_device() != index or not out.is_contiguous():
             raise ValueError("out must be contiguous, shaped and typed as logits")
+        out_at = out.data_ptr()
     elif return_filtered:
         out = torch.empty(shape, dtype=logits.dtype, device=device)
-    status = _status(debug, device)
+        out_at = out.data_ptr()
+    status, status_at = _status(debug, device)
     need = _lib.spec_filtered_sample_workspace_size(R, V, dt)
-    ws, nbytes = _workspace("sample", device, _stream, need, workspace) if need else (None, 0)
+    ws, nbytes = _workspace("sample", index, stream, need, workspace)
     rc = _lib.spec_filtered_sample(
-        logits.data_ptr(), stride, uniforms.data_ptr(), R, V, dt, T, int(k), p, m, Tp, kp, pp, mp, tokens.data_ptr(),
-        prob.data_ptr(), n_kept.data_ptr(), _p(out), ws, nbytes, _stream, _p(status))
+        logits.data_ptr(), stride, uniforms.data_ptr(), R, V, dt, T, k, p, m, Tp, kp, pp, mp, tokens.data_ptr(),
+        prob.data_ptr(), n_kept.data_ptr(), out_at, ws, nbytes, stream, status_at)
     if rc != OK:
         _raise(rc, "spec_filtered_sample")
     return SampleResult(tokens, prob, n_kept, out, status)
