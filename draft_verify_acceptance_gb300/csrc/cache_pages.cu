@@ -4,11 +4,11 @@
 // could drift from them.
 //
 // fork and compact first make a plan (reference counts, free pages, who gets
-// which) and then copy.  Where the counts fit one block's shared memory, both
-// happen in one cooperative launch: block 0 plans there while the others
-// wait for its flag, then all write the tables and copy.  One launch instead
-// of four, and no traffic through L2 for the counts, is most of a small
-// call's time.  Larger pools count in global memory, in a launch per step.
+// which) and then copy.  Where the counts fit one block's shared memory, one
+// block plans there, and the kernel that writes the tables and copies is its
+// programmatic dependent: two launches instead of four (a cooperative launch
+// of both in one costs the host more than the second launch does), and no
+// traffic through L2 for the counts.  Larger pools count in global memory.
 #include <climits>
 
 #include "device_common.cuh"
@@ -23,46 +23,11 @@ __device__ __forceinline__ void report(int32_t* status, int bits) {
   if (bits && status) atomicOr(status, bits);
 }
 
-// A fused launch's control words.  Zero at rest: its last block puts them back.
-struct __align__(16) Control {
-  unsigned int ready, done;
-};
-constexpr int kGroup = 128;                       // threads that share a copy
-constexpr int kGroups = kPlanThreads / kGroup;
-constexpr int kMaxShared = 200 * 1024;            // of the plan
-constexpr unsigned long long kWaitNs = 2000000000ull;
+constexpr int kGroup = 128;            // threads that share a copy
+constexpr int kMaxShared = 200 * 1024;  // of the plan
 
-// Block 0 has planned: everything it wrote is visible to who sees the flag.
-__device__ __forceinline__ void publish(Control* c) {
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    __threadfence();
-    asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(&c->ready), "r"(1u) : "memory");
-  }
-}
-// The others wait for it, 2 s at most; false: it never came.
-__device__ __forceinline__ bool await(Control* c, int* ok) {
-  if (threadIdx.x == 0) {
-    const unsigned long long t0 = global_ns();
-    *ok = 1;
-    while (!ld_acquire_gpu(&c->ready)) {
-      if (global_ns() - t0 > kWaitNs) {
-        *ok = 0;
-        break;
-      }
-      __nanosleep(100);
-    }
-  }
-  __syncthreads();
-  return *ok != 0;
-}
-__device__ __forceinline__ void leave(Control* c) {
-  __syncthreads();
-  if (threadIdx.x == 0 && atom_add_acq_rel_gpu(&c->done, 1u) + 1u == gridDim.x) {
-    c->ready = 0;
-    c->done = 0;
-  }
-}
+// Waits for what the launch before this one wrote (a dependent launch).
+__device__ __forceinline__ void after_plan() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Copies `tokens` tokens of a page by kGroup threads, eight pieces a thread
 // in flight where the tokens are contiguous.
@@ -175,17 +140,15 @@ __device__ __forceinline__ int child_page(const ForkArgs& a, const Child& ch, in
   return p >= 0 && p < a.cache.pages ? p : -1;
 }
 
-// Workspace: control words, refs[P], first[P] (cleared before the launch that
-// counts in them), order[P] the free pages ascending, base[C] the first fresh
+// Workspace: refs[P], first[P] (cleared before the launch that counts in
+// them), order[P] the free pages ascending, base[C] the first fresh
 // rank of a sequence (sign bit: its last page stays), count of free pages.
 struct ForkSpace {
-  Control* control;
   int *refs, *first, *order, *base, *nfree;
 };
 __host__ __device__ inline ForkSpace fork_space(void* ws, int P, int C) {
   ForkSpace s;
-  s.control = static_cast<Control*>(ws);
-  s.refs = static_cast<int*>(ws) + 16;
+  s.refs = static_cast<int*>(ws);
   s.first = s.refs + P;
   s.order = s.first + P;
   s.base = s.order + P;
@@ -331,78 +294,69 @@ __device__ void fork_write(const ForkArgs& a, const ForkSpace& s) {
   }
 }
 
-__global__ void __launch_bounds__(256) fork_write_kernel(const ForkArgs a, ForkSpace s) { fork_write(a, s); }
+__global__ void __launch_bounds__(256) fork_write_kernel(const ForkArgs a, ForkSpace s) {
+  after_plan();
+  fork_write(a, s);
+}
 
-// All of it in one cooperative launch.  The counts come by parent: ends[b][f]
+// Counts and plan by one block.  The counts come by parent: ends[b][f]
 // sequences keep f full pages of parent b, so page j of b gains the sum of
 // ends[b][f] over f > j -- one addition a parent's page, however many
 // sequences share it.
-__global__ void __launch_bounds__(kPlanThreads, 1) fork_fused_kernel(const ForkArgs a, ForkSpace s) {
+__global__ void __launch_bounds__(kPlanThreads, 1) fork_block_kernel(const ForkArgs a, ForkSpace s) {
   extern __shared__ int counts[];  // refs[P], first[P], ends[B][max_pages + 1]
   __shared__ int scratch[32];
   const int tid = threadIdx.x, lane = tid & 31, P = a.cache.pages, M = a.table.max_pages;
-  if (blockIdx.x == 0) {
-    int *refs = counts, *first = refs + P, *ends = first + P;
-    const int words = 2 * P + a.B * (M + 1);
-    for (int i = tid; i < words; i += kPlanThreads) counts[i] = 0;
-    __syncthreads();
-    int bad = 0;
-    for (int c = tid; c < a.C; c += kPlanThreads) {
-      const Child ch = child_of(a, c);
-      bad |= ch.bad;
-      if (ch.full > 0) atomicAdd(&ends[ch.parent * (M + 1) + ch.full], 1);
-      if (ch.tail > 0) {
-        const int p = child_page(a, ch, ch.full);
-        if (p < 0) bad |= kDataPageRange;
-        else atomicMax(&first[p], a.C - c);
-      }
+  int *refs = counts, *first = refs + P, *ends = first + P;
+  const int words = 2 * P + a.B * (M + 1);
+  for (int i = tid; i < words; i += kPlanThreads) counts[i] = 0;
+  __syncthreads();
+  int bad = 0;
+  for (int c = tid; c < a.C; c += kPlanThreads) {
+    const Child ch = child_of(a, c);
+    bad |= ch.bad;
+    if (ch.full > 0) atomicAdd(&ends[ch.parent * (M + 1) + ch.full], 1);
+    if (ch.tail > 0) {
+      const int p = child_page(a, ch, ch.full);
+      if (p < 0) bad |= kDataPageRange;
+      else atomicMax(&first[p], a.C - c);
     }
-    __syncthreads();
-    for (int b = tid >> 5; b < a.B; b += kPlanThreads / 32) {
-      const int S = a.cache.page_size, len = min(max(a.lengths[b], 0), M * S);
-      const int most = len / S;  // full pages that anyone can keep
-      int beyond = 0;            // sequences that keep more than the pages seen so far
-      for (int j0 = (most + 31) / 32 * 32 - 32; j0 >= 0; j0 -= 32) {
-        const int j = j0 + lane;
-        int sum = j < most ? ends[b * (M + 1) + j + 1] : 0;  // ends at j + 1: keeps page j
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const int o = __shfl_down_sync(0xffffffffu, sum, d);
-          if (lane + d < 32) sum += o;
-        }
-        sum += beyond;
-        if (j < most && sum > 0) {
-          const int p = a.table.ids[b * a.table.stride + j];
-          if (p >= 0 && p < P) atomicAdd(&refs[p], sum);
-          else bad |= kDataPageRange;
-        }
-        beyond = __shfl_sync(0xffffffffu, sum, 0);
-      }
-    }
-    report(a.status, bad);
-    __syncthreads();
-    fork_plan(a, s, refs, first, scratch);
-    publish(s.control);
-    __syncthreads();
-  } else if (!await(s.control, &scratch[0])) {
-    if (tid == 0) report(a.status, kWaitTimeout);
-    return;
   }
-  fork_write(a, s);
-  leave(s.control);
+  __syncthreads();
+  for (int b = tid >> 5; b < a.B; b += kPlanThreads / 32) {
+    const int S = a.cache.page_size, len = min(max(a.lengths[b], 0), M * S);
+    const int most = len / S;  // full pages that anyone can keep
+    int beyond = 0;            // sequences that keep more than the pages seen so far
+    for (int j0 = (most + 31) / 32 * 32 - 32; j0 >= 0; j0 -= 32) {
+      const int j = j0 + lane;
+      int sum = j < most ? ends[b * (M + 1) + j + 1] : 0;  // ends at j + 1: keeps page j
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_down_sync(0xffffffffu, sum, d);
+        if (lane + d < 32) sum += o;
+      }
+      sum += beyond;
+      if (j < most && sum > 0) {
+        const int p = a.table.ids[b * a.table.stride + j];
+        if (p >= 0 && p < P) atomicAdd(&refs[p], sum);
+        else bad |= kDataPageRange;
+      }
+      beyond = __shfl_sync(0xffffffffu, sum, 0);
+    }
+  }
+  report(a.status, bad);
+  __syncthreads();
+  fork_plan(a, s, refs, first, scratch);
 }
 
 // ---- compact -------------------------------------------------------------------
-// Workspace: control words, refs[P] (cleared before the launch that counts in
-// them), to[P] the pages' new numbers, from[P] the moved pages ascending, holes[P], moves.
+// Workspace: refs[P] (cleared before the launch that counts in them), to[P] the pages' new numbers, from[P] the moved pages ascending, holes[P], moves.
 struct CompactSpace {
-  Control* control;
   int *refs, *to, *from, *holes, *moves;
 };
 __host__ __device__ inline CompactSpace compact_space(void* ws, int P) {
   CompactSpace s;
-  s.control = static_cast<Control*>(ws);
-  s.refs = static_cast<int*>(ws) + 16;
+  s.refs = static_cast<int*>(ws);
   s.to = s.refs + P;
   s.from = s.to + P;
   s.holes = s.from + P;
@@ -500,45 +454,35 @@ __device__ void compact_move(const CompactArgs& a, const CompactSpace& s) {
   }
 }
 
-__global__ void __launch_bounds__(256) compact_move_kernel(const CompactArgs a, CompactSpace s) { compact_move(a, s); }
-
-__global__ void __launch_bounds__(kPlanThreads, 1) compact_fused_kernel(const CompactArgs a, CompactSpace s) {
-  extern __shared__ int counts[];  // refs[P]
-  __shared__ int scratch[32];
-  if (blockIdx.x == 0) {
-    for (int i = threadIdx.x; i < a.cache.pages; i += kPlanThreads) counts[i] = 0;
-    __syncthreads();
-    compact_count(a, counts, threadIdx.x, kPlanThreads);
-    __syncthreads();
-    compact_plan(a, s, counts, scratch);
-    publish(s.control);
-    __syncthreads();
-  } else if (!await(s.control, &scratch[0])) {
-    if (threadIdx.x == 0) report(a.status, kWaitTimeout);
-    return;
-  }
+__global__ void __launch_bounds__(256) compact_move_kernel(const CompactArgs a, CompactSpace s) {
+  after_plan();
   compact_move(a, s);
-  leave(s.control);
 }
 
-// The fused launch: every block resident at once.
+__global__ void __launch_bounds__(kPlanThreads, 1) compact_block_kernel(const CompactArgs a, CompactSpace s) {
+  extern __shared__ int counts[];  // refs[P]
+  __shared__ int scratch[32];
+  for (int i = threadIdx.x; i < a.cache.pages; i += kPlanThreads) counts[i] = 0;
+  __syncthreads();
+  compact_count(a, counts, threadIdx.x, kPlanThreads);
+  __syncthreads();
+  compact_plan(a, s, counts, scratch);
+}
+
+// The copying kernel, as the dependent of the plan's.
 template <typename A, typename S>
-cudaError_t launch_fused(void (*kernel)(A, S), const A& a, const S& s, int grid, size_t smem, cudaStream_t stream) {
+cudaError_t launch_after(void (*kernel)(A, S), const A& a, const S& s, long long groups, int sm_count, cudaStream_t stream) {
+  const long long want = (groups * kGroup + 255) / 256;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kPlanThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.gridDim = dim3(static_cast<unsigned int>(want < 1 ? 1 : want < sm_count * 8 ? want : sm_count * 8));
+  cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1] = {};
-  attr[0].id = cudaLaunchAttributeCooperative;
-  attr[0].val.cooperative = 1;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, a, s);
-}
-int fused_grid(long long items, int sm_count) {
-  const long long want = (items + kGroups - 1) / kGroups;
-  return static_cast<int>(want < 1 ? 1 : want < sm_count ? want : sm_count);
 }
 
 size_t up(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
@@ -556,55 +500,54 @@ cudaError_t launch_append(const char* k_new, const char* v_new, long long new_st
 }
 
 cudaError_t cache_pages_prepare() {
-  cudaError_t e = cudaFuncSetAttribute(fork_fused_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared);
+  cudaError_t e = cudaFuncSetAttribute(fork_block_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared);
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(compact_fused_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared);
+    e = cudaFuncSetAttribute(compact_block_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared);
   return e;
 }
 
 size_t fork_workspace(int pages, int C) {
-  return up((16 + 3 * static_cast<size_t>(pages) + static_cast<size_t>(C) + 1) * 4);
+  return up((3 * static_cast<size_t>(pages) + static_cast<size_t>(C) + 1) * 4);
 }
 
 cudaError_t launch_fork(const ForkArgs& a, void* ws, int sm_count, cudaStream_t stream) {
   const ForkSpace s = fork_space(ws, a.cache.pages, a.C);
-  const long long items = static_cast<long long>(a.C) * (1 + 2 * a.cache.layers);
-  // One block counts the parents' pages; beyond about 64 Ki table entries that
-  // takes longer than three more launches.
-  const long long entries = static_cast<long long>(a.B) * (a.table.max_pages + 1);
-  const long long words = 2ll * a.cache.pages + entries;
-  if (words * 4 <= kMaxShared)
-    return launch_fused(fork_fused_kernel, a, s, fused_grid(items, sm_count), static_cast<size_t>(words) * 4, stream);
-  cudaError_t e = cudaMemsetAsync(s.refs, 0, 2 * static_cast<size_t>(a.cache.pages) * 4, stream);
-  if (e != cudaSuccess) return e;
-  const int blocks = a.C < sm_count * 8 ? a.C : sm_count * 8;
-  if (blocks > 0) fork_count_kernel<<<blocks, 256, 0, stream>>>(a, s);
-  fork_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a, s);
-  const long long want = (items * kGroup + 255) / 256;
-  if (items > 0)
-    fork_write_kernel<<<static_cast<int>(want < sm_count * 8 ? want : sm_count * 8), 256, 0, stream>>>(a, s);
-  return cudaGetLastError();
+  const long long words = 2ll * a.cache.pages + static_cast<long long>(a.B) * (a.table.max_pages + 1);
+  if (words * 4 <= kMaxShared) {
+    fork_block_kernel<<<1, kPlanThreads, static_cast<size_t>(words) * 4, stream>>>(a, s);
+  } else {
+    const cudaError_t e = cudaMemsetAsync(s.refs, 0, 2 * static_cast<size_t>(a.cache.pages) * 4, stream);
+    if (e != cudaSuccess) return e;
+    const int blocks = a.C < sm_count * 8 ? a.C : sm_count * 8;
+    if (blocks > 0) fork_count_kernel<<<blocks, 256, 0, stream>>>(a, s);
+    fork_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a, s);
+  }
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || a.C == 0) return e;
+  return launch_after(fork_write_kernel, a, s, static_cast<long long>(a.C) * (1 + 2 * a.cache.layers), sm_count, stream);
 }
 
-size_t compact_workspace(int pages) { return up((16 + 4 * static_cast<size_t>(pages) + 1) * 4); }
+size_t compact_workspace(int pages) { return up((4 * static_cast<size_t>(pages) + 1) * 4); }
 
 cudaError_t launch_compact(const CompactArgs& a, void* ws, int sm_count, cudaStream_t stream) {
   const CompactSpace s = compact_space(ws, a.cache.pages);
   const long long entries = static_cast<long long>(a.B) * a.table.max_pages;
   const size_t smem = static_cast<size_t>(a.cache.pages) * 4;
-  // (the same trade: one block counts the entries)
+  // (one block counts 64 Ki entries in less time than two more launches take)
   if (smem <= kMaxShared && entries <= (1 << 16)) {
-    const long long most = a.cache.pages / 2;  // pages that can move
-    return launch_fused(compact_fused_kernel, a, s, fused_grid(most * 2 * a.cache.layers, sm_count), smem, stream);
+    compact_block_kernel<<<1, kPlanThreads, smem, stream>>>(a, s);
+  } else {
+    const cudaError_t e = cudaMemsetAsync(s.refs, 0, smem, stream);
+    if (e != cudaSuccess) return e;
+    const long long want = (entries + 255) / 256;
+    if (entries > 0)
+      compact_count_kernel<<<static_cast<int>(want < sm_count * 8 ? want : sm_count * 8), 256, 0, stream>>>(a, s);
+    compact_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a, s);
   }
-  cudaError_t e = cudaMemsetAsync(s.refs, 0, smem, stream);
+  const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const long long want = (entries + 255) / 256;
-  if (entries > 0)
-    compact_count_kernel<<<static_cast<int>(want < sm_count * 8 ? want : sm_count * 8), 256, 0, stream>>>(a, s);
-  compact_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a, s);
-  compact_move_kernel<<<sm_count * 8, 256, 0, stream>>>(a, s);
-  return cudaGetLastError();
+  const long long pieces = static_cast<long long>(a.cache.pages / 2) * 2 * a.cache.layers + entries / kGroup;
+  return launch_after(compact_move_kernel, a, s, pieces, sm_count, stream);
 }
 
 }  // namespace specv

@@ -117,9 +117,7 @@ SPEC_API spec_status_t spec_cache_append(
  * page_table and lengths are not changed; the outputs must not overlap them.
  * No page that new_table shares is written, and no page is both copied from
  * and written, so the call can be repeated.
- *   workspace: spec_cache_fork_workspace_size(...) bytes, zero-filled once;
- *            every call leaves it fit for the next of either size.  One call
- *            at a time, and not one workspace for fork and compact.
+ *   workspace: spec_cache_fork_workspace_size(...) bytes, any content.
  */
 SPEC_API size_t spec_cache_fork_workspace_size(int pages, int C);
 SPEC_API spec_status_t spec_cache_fork(
@@ -137,7 +135,7 @@ SPEC_API spec_status_t spec_cache_fork(
  *   page_table [B, max_pages]: entries >= 0 are in use (shared ones once).
  *   new_table [B, max_pages], ref_counts [pages] (by the new numbers),
  *   n_live [1] = n.  Pages n.. are free afterwards.
- *   workspace: as for spec_cache_fork.
+ *   workspace: spec_cache_compact_workspace_size(...) bytes, any content.
  */
 SPEC_API size_t spec_cache_compact_workspace_size(int pages);
 SPEC_API spec_status_t spec_cache_compact(
