@@ -313,18 +313,19 @@ def cache_fork(at, k_pages, v_pages, page_table, lengths, parents, keep, room=0,
     lens = _ints(lengths, "lengths", (B,), index)
     par, kp = _ints(parents, "parents", (C,), index), _ints(keep, "keep", (C,), index)
     P = c.pages
-    # one allocation; the results are views of it
-    n = C * M
-    buf = torch.empty(n + C + 2 * P + 1, dtype=torch.int32, device=k_pages.device)
-    new, lens_new, refs, free, n_free = buf.split_with_sizes((n, C, P, P, 1))
-    status, status_at = _status(debug, k_pages.device)
+    device = k_pages.device
+    new = torch.empty((C, M), dtype=torch.int32, device=device)
+    lens_new = torch.empty(C, dtype=torch.int32, device=device)
+    refs = torch.empty(P, dtype=torch.int32, device=device)
+    free = torch.empty(P, dtype=torch.int32, device=device)
+    n_free = torch.empty(1, dtype=torch.int32, device=device)
+    status, status_at = _status(debug, device)
     ws, nbytes = _workspace("fork", index, stream, _lib.spec_cache_fork_workspace_size(P, C), workspace)
-    base = buf.data_ptr()
-    rc = _lib.spec_cache_fork(c, table, ts, M, lens, B, par, kp, C, room, base, base + 4 * n, base + 4 * (n + C),
-                              base + 4 * (n + C + P), base + 4 * (n + C + 2 * P), ws, nbytes, stream, status_at)
+    rc = _lib.spec_cache_fork(c, table, ts, M, lens, B, par, kp, C, room, new.data_ptr(), lens_new.data_ptr(),
+                              refs.data_ptr(), free.data_ptr(), n_free.data_ptr(), ws, nbytes, stream, status_at)
     if rc != OK:
         _raise(rc, "spec_cache_fork")
-    return ForkResult(new.view(C, M), lens_new, refs, free, n_free, status)
+    return ForkResult(new, lens_new, refs, free, n_free, status)
 
 
 @_on_stream
@@ -339,16 +340,17 @@ def cache_compact(at, k_pages, v_pages, page_table, *, workspace=None, debug=Fal
     B = page_table.shape[0]
     table, ts, M = _table(page_table, B, index)
     P = c.pages
-    n = B * M
-    buf = torch.empty(n + P + 1, dtype=torch.int32, device=k_pages.device)
-    new, refs, n_live = buf.split_with_sizes((n, P, 1))
-    status, status_at = _status(debug, k_pages.device)
+    device = k_pages.device
+    new = torch.empty((B, M), dtype=torch.int32, device=device)
+    refs = torch.empty(P, dtype=torch.int32, device=device)
+    n_live = torch.empty(1, dtype=torch.int32, device=device)
+    status, status_at = _status(debug, device)
     ws, nbytes = _workspace("compact", index, stream, _lib.spec_cache_compact_workspace_size(P), workspace)
-    base = buf.data_ptr()
-    rc = _lib.spec_cache_compact(c, table, ts, M, B, base, base + 4 * n, base + 4 * (n + P), ws, nbytes, stream, status_at)
+    rc = _lib.spec_cache_compact(c, table, ts, M, B, new.data_ptr(), refs.data_ptr(), n_live.data_ptr(), ws, nbytes, stream,
+                                 status_at)
     if rc != OK:
         _raise(rc, "spec_cache_compact")
-    return CompactResult(new.view(B, M), refs, n_live, status)
+    return CompactResult(new, refs, n_live, status)
 
 
 def _setting(v, off, kind, name, R, index):
