@@ -203,20 +203,22 @@ __global__ void __launch_bounds__(kThreadsF) attention_kernel(const AttnArgs a) 
 
 }  // namespace
 
-constexpr int kMaxBlocks = 4;  // blocks of 8 rows an item of the tensor-core kernel holds at most
+// Up to 8 rows a cache head go to attention_mma.cuh, more to attention_tc.cuh.
+constexpr int kMmaRows = 8;
+constexpr int kMaxMmaCtas = 304;
 
 size_t attention_workspace(int D, bool bf16) {
-  const size_t rows = bf16 ? 8 * kMaxBlocks : kRowsF;
-  return (static_cast<size_t>(kAttnMaxCtas) * 4 +
-          static_cast<size_t>(kAttnMaxCtas) * 2 * rows * (D + 2) * 4 + 255) & ~static_cast<size_t>(255);
+  const size_t rows = bf16 ? kMaxRowsTc : kRowsF;
+  const size_t ctas = bf16 ? kMaxMmaCtas : kAttnMaxCtas;
+  return (static_cast<size_t>(kAttnMaxCtas) * 4 + ctas * 2 * rows * (D + 2) * 4 + 255) & ~static_cast<size_t>(255);
 }
 
 cudaError_t attention_prepare() {
-  cudaError_t e[] = {mma::prepare<64, 1>(), mma::prepare<64, 2>(), mma::prepare<64, 3>(), mma::prepare<64, 4>(),
-                     mma::prepare<128, 1>(), mma::prepare<128, 2>(), mma::prepare<128, 3>(), mma::prepare<128, 4>()};
-  for (cudaError_t x : e)
-    if (x != cudaSuccess) return x;
-  return cudaSuccess;
+  cudaError_t e = mma::prepare<64, 1>();
+  if (e == cudaSuccess) e = mma::prepare<128, 1>();
+  if (e == cudaSuccess) e = attention_tc_prepare_64();
+  if (e == cudaSuccess) e = attention_tc_prepare_128();
+  return e;
 }
 
 cudaError_t launch_attention(const AttnArgs& a, int sm_count, cudaStream_t stream) {
@@ -227,21 +229,19 @@ cudaError_t launch_attention(const AttnArgs& a, int sm_count, cudaStream_t strea
     else attention_kernel<F32, 64><<<grid, kThreadsF, 0, stream>>>(a);
     return cudaGetLastError();
   }
-  // Rows in tiles of equal size, at most 32.
-  const int R = a.Q * (a.Hq / a.cache.heads), most = 8 * kMaxBlocks;
-  const int tiles = (R + most - 1) / most;
-  const int nb = ((R + tiles - 1) / tiles + 7) / 8;
-  const int grid = sm_count * 2 < kAttnMaxCtas ? sm_count * 2 : kAttnMaxCtas;
-  switch (nb + (wide ? 4 : 0)) {
-    case 1: mma::launch<64, 1>(a, grid, stream); break;
-    case 2: mma::launch<64, 2>(a, grid, stream); break;
-    case 3: mma::launch<64, 3>(a, grid, stream); break;
-    case 4: mma::launch<64, 4>(a, grid, stream); break;
-    case 5: mma::launch<128, 1>(a, grid, stream); break;
-    case 6: mma::launch<128, 2>(a, grid, stream); break;
-    case 7: mma::launch<128, 3>(a, grid, stream); break;
-    default: mma::launch<128, 4>(a, grid, stream); break;
+  const int R = a.Q * (a.Hq / a.cache.heads);
+  if (R <= kMmaRows) {
+    const int grid = sm_count * 2 < kMaxMmaCtas ? sm_count * 2 : kMaxMmaCtas;
+    if (wide) mma::launch<128, 1>(a, grid, stream);
+    else mma::launch<64, 1>(a, grid, stream);
+    return cudaGetLastError();
   }
+  // Rows in tiles of equal size, a multiple of 16 and at most 96.
+  const int tiles = (R + kMaxRowsTc - 1) / kMaxRowsTc;
+  const int n16 = ((R + tiles - 1) / tiles + 15) / 16;
+  const int grid = sm_count < kMaxMmaCtas ? sm_count : kMaxMmaCtas;
+  if (wide) attention_tc_launch_128(a, n16, grid, stream);
+  else attention_tc_launch_64(a, n16, grid, stream);
   return cudaGetLastError();
 }
 

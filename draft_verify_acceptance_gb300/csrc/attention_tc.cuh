@@ -1,0 +1,592 @@
+// attention_tc.cuh -- bf16 paged attention for more than a few rows a cache
+// head (several queries, or many query heads to a cache head), on tcgen05
+// (sm_103a).
+//
+// The products are transposed, as in attention_mma.cuh: tokens and D are the
+// long sides, the rows few.
+//     S^T [128 tokens x N rows] = K Q^T       A = K tile,   B = Q
+//     O^T [D x N rows]         += V^T P^T     A = V^T tile, B = P^T
+// Both accumulators live in TMEM (S^T twice, so that the next tile's product
+// runs under this tile's softmax), K and V tiles are read from shared memory
+// as they come from the cache -- V^T is V's tile read with the other side
+// major -- and a tile costs the tensor cores 4 x N x 128 x D multiply-adds
+// (P^T counts twice, below), a few hundred cycles where its 64 KB take HBM
+// three thousand.
+//
+// One block per SM.  Warps 4-7 stream tiles through a ring of slots in shared
+// memory (cp.async in 16-byte pieces, so any page size and any strides), K
+// and V in turn, across item boundaries.  Warp 8 issues the products.  Warps
+// 0-3 hold one token a thread: they read S^T, keep each row's reference
+// maximum (moved only when a score passes it by 2^8), write the weights P^T
+// as two bf16 parts (hi and lo: one bf16 weight would lose up to 2^-8 of a
+// term, as much as rounding the output does) and finish items.
+#pragma once
+
+#include "attention_common.cuh"
+#include "attention_mma.cuh"
+
+namespace specv {
+namespace tc {
+
+using mma::cp16;
+using mma::cp_commit;
+using mma::cp_wait;
+using mma::nonfinite2;
+using mma::pack2;
+
+constexpr int kTile = 128;               // tokens
+constexpr int kSoft = 128;               // softmax threads (warps 0-3)
+constexpr int kLoad = 128;               // loader threads (warps 4-7)
+constexpr int kThreadsT = kSoft + kLoad + 32;
+constexpr float kSlackT = 8.f;
+
+template <int D, int N>
+struct Lay {
+  static constexpr int kSlot = kTile * D * 2;   // K or V of a tile
+  static constexpr int kQ = N * D * 2;
+  static constexpr int kP = kTile * N * 2;      // one part of P^T
+  static constexpr int kFree = 216 * 1024 - kQ - 2 * kP;  // (about 9 KB more are static)
+  static constexpr int kSlots = kFree / kSlot < 8 ? kFree / kSlot : 8;
+  static constexpr int kLag = kSlots - 2;       // slots in flight
+  static constexpr int kBytes = kSlots * kSlot + kQ + 2 * kP + 1024;  // 1024: alignment
+  static constexpr int kCols = 3 * N <= 64 ? 64 : 3 * N <= 128 ? 128 : 3 * N <= 256 ? 256 : 512;
+  static_assert(kSlots >= 4, "two tiles");
+};
+
+// ---- tcgen05 ---------------------------------------------------------------
+__device__ __forceinline__ void tmem_alloc(uint32_t* at, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(at)), "r"(cols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free(uint32_t at, uint32_t cols) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(cols) : "memory");
+}
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// Arrives on `bar` when every product issued so far is done.
+__device__ __forceinline__ void tc_commit(unsigned long long* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+               : "memory");
+}
+__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(float (&v)[16], uint32_t at) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(at));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t at, const float (&v)[16]) {
+  const uint32_t* r = reinterpret_cast<const uint32_t*>(v);
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_done() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void async_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// Shared-memory operand: start, leading and stride byte offsets; swizzle 128
+// bytes (layout 2) or none (0).
+__device__ __forceinline__ uint64_t operand(uint32_t at, uint32_t lead, uint32_t stride, uint32_t layout) {
+  return (static_cast<uint64_t>((at & 0x3ffffu) >> 4)) | (static_cast<uint64_t>(lead >> 4) << 16) |
+         (static_cast<uint64_t>(stride >> 4) << 32) | (1ull << 46) | (static_cast<uint64_t>(layout) << 61);
+}
+// bf16 operands, fp32 accumulator, M = 128; `a_mn` / `b_mn`: that operand has
+// its M or N side contiguous instead of K.
+template <int N>
+__device__ __forceinline__ constexpr uint32_t instruction(bool a_mn, bool b_mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+         (static_cast<uint32_t>(N >> 3) << 17) | (8u << 24);
+}
+
+__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void load_sync() { asm volatile("bar.sync 2, 128;" ::: "memory"); }
+__device__ __forceinline__ bool soft_any(bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(x ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
+
+// One part of an item after the other, as every role walks them.
+template <int N>
+struct Walk {
+  const AttnArgs& a;
+  long long w, end, per, base;
+  int b, H, RT, R;
+  int n, tiles, item, tile0, tile1, rt, h, row0, rows;
+  __device__ __forceinline__ Walk(const AttnArgs& args, const AttnPlan& p) : a(args) {
+    H = a.cache.heads;
+    R = a.Q * (a.Hq / H);
+    RT = (R + N - 1) / N;
+    per = p.per;
+    w = per * blockIdx.x;
+    end = min(p.total, w + per);
+    b = p.b;
+    base = p.base;
+    tile1 = tile0 = 0;
+  }
+  __device__ __forceinline__ bool next() {
+    w += tile1 - tile0;
+    if (w >= end) return false;
+    n = attn_length(a, b);
+    tiles = attn_tiles<kTile>(n);
+    while (w >= base + static_cast<long long>(tiles) * H * RT) {
+      base += static_cast<long long>(tiles) * H * RT;
+      n = attn_length(a, ++b);
+      tiles = attn_tiles<kTile>(n);
+    }
+    item = static_cast<int>((w - base) / tiles);
+    tile0 = static_cast<int>((w - base) - static_cast<long long>(item) * tiles);
+    tile1 = static_cast<int>(min(static_cast<long long>(tiles), tile0 + (end - w)));
+    rt = item / H;
+    h = item - rt * H;
+    row0 = rt * N;
+    rows = min(N, R - row0);
+    return true;
+  }
+  __device__ __forceinline__ long long first() const { return base + static_cast<long long>(item) * tiles; }
+};
+
+template <int D, int N>
+struct SharedT {
+  unsigned long long full[Lay<D, N>::kSlots], empty[Lay<D, N>::kSlots];
+  unsigned long long s_full[2], s_free[2], p_full, p_free, q_full;
+  long long off[2][kTile];             // byte offsets of a tile's tokens, -1: none
+  uint32_t valid[8][4];                // tokens that exist, by tile
+  float m[N], corr[N], wmax[4][N], lsum[4][N];
+  int limit[N];                        // last token that a row sees
+  uint32_t odd_rows[kTile][(N + 31) / 32];
+  int odd_token[kTile];
+  int n_odd;
+  uint32_t tmem;
+  int dead;                            // a wait ran out: nothing waits any more
+  int last;
+  long long plan[2 * (kThreadsT / 32) + 4];
+};
+
+template <int D, int N>
+__global__ void __launch_bounds__(kThreadsT, 1) attention_tc_kernel(const AttnArgs a, DivU64 by_page) {
+  using L = Lay<D, N>;
+  constexpr int kSlots = L::kSlots, kLag = L::kLag, kHalves = D / 64, kHalf = kTile * 128;
+  constexpr int kChunks = D / 8;  // 16-byte pieces of a token
+  extern __shared__ char raw_smem[];
+  __shared__ SharedT<D, N> sh;
+  char* smem = raw_smem + ((1024 - (smem_addr(raw_smem) & 1023)) & 1023);
+  char* q_s = smem + kSlots * L::kSlot;  // [halves][N][128 bytes]
+  char* p_s = q_s + L::kQ;               // [hi, lo][N / 8][128 tokens][16 bytes]
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  auto wait = [&](unsigned long long* bar, uint32_t parity) {
+    if (*reinterpret_cast<volatile int*>(&sh.dead)) return;
+    if (!mbar_wait_sleep(bar, parity)) {
+      *reinterpret_cast<volatile int*>(&sh.dead) = 1;
+      if (a.status) atomicOr(a.status, kWaitTimeout);
+    }
+  };
+
+  const AttnPlan plan = attn_plan<kTile, kThreadsT>(
+      a, a.cache.heads * ((a.Q * (a.Hq / a.cache.heads) + N - 1) / N), 2, sh.plan);
+  if (tid == 0) {
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&sh.full[i], kLoad);
+      mbar_init(&sh.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.s_free[i], kSoft);
+    }
+    mbar_init(&sh.p_full, kSoft);
+    mbar_init(&sh.p_free, 1);
+    mbar_init(&sh.q_full, kSoft);
+    sh.dead = 0;
+    fence_barrier_init();
+  }
+  if (warp == 8) tmem_alloc(&sh.tmem, L::kCols);
+  tc_before();
+  __syncthreads();
+  tc_after();
+  const uint32_t tmem = sh.tmem;
+  Walk<N> at(a, plan);
+
+  if (warp >= 4 && warp < 8) {
+    // ---- loaders: K and V of each tile, in turn ---------------------------
+    const int lt = tid - kSoft, S = a.cache.page_size;
+    const int chunk = lt % kChunks, r0 = lt / kChunks;
+    constexpr int kStep = kLoad / kChunks, kRows = kTile / kStep;
+    int slot = 0, seen = 0, sent = 0;  // the slot to fill; slots filled, announced
+    uint32_t turn = 0;                 // times the ring went round
+    auto announce = [&]() {
+      async_fence();
+      mbar_arrive(&sh.full[sent % kSlots]);
+      ++sent;
+    };
+    int tile_no = 0;
+    while (at.next()) {
+      const int32_t* table = a.table.ids + at.b * a.table.stride;
+      for (int tile = at.tile0; tile < at.tile1; ++tile, ++tile_no) {
+        const int t = tile * kTile + lt;
+        long long o = -1;
+        if (t < at.n) {
+          const int entry = static_cast<int>(by_page(static_cast<unsigned long long>(t)));
+          const int page = table[entry];
+          if (page >= 0 && page < a.cache.pages)
+            o = page * a.cache.page_stride + (t - entry * S) * a.cache.token_stride + at.h * (D * 2);
+          else if (a.status)
+            atomicOr(a.status, kDataPageRange);
+        }
+        const uint32_t valid = __ballot_sync(0xffffffffu, o >= 0);
+        if (lane == 0) sh.valid[tile_no & 7][warp - 4] = valid;
+        sh.off[tile_no & 1][lt] = o;
+        load_sync();
+        const long long* off = sh.off[tile_no & 1];
+#pragma unroll 1
+        for (int x = 0; x < 2; ++x) {
+          if (seen >= kSlots) wait(&sh.empty[slot], (turn + 1) & 1);
+          const char* pool = (x ? a.cache.v : a.cache.k) + chunk * 16;
+          const uint32_t dst = smem_addr(smem) + slot * L::kSlot + (chunk >> 3) * kHalf;
+#pragma unroll
+          for (int i = 0; i < kRows; ++i) {
+            const int r = r0 + i * kStep;
+            const long long from = off[r];
+            cp16(dst + r * 128 + (((chunk & 7) ^ (r & 7)) << 4), pool + (from < 0 ? 0 : from), from < 0 ? 0 : 16);
+          }
+          cp_commit();
+          ++seen;
+          if (++slot == kSlots) {
+            slot = 0;
+            ++turn;
+          }
+          if (seen > kLag) {
+            cp_wait<kLag>();
+            announce();
+          }
+        }
+      }
+    }
+    cp_wait<0>();
+    while (sent < seen) announce();
+  } else if (warp == 8) {
+    // ---- the products ------------------------------------------------------
+    if (lane == 0) {
+      const uint32_t ring = smem_addr(smem), q_at = smem_addr(q_s), p_at = smem_addr(p_s);
+      const uint32_t s_col[2] = {tmem, tmem + N}, o_col = tmem + 2 * N;
+      int k_idx = 0, items = 0;
+      Walk<N> ahead(a, plan);  // the tile whose scores are issued next
+      bool more = ahead.next();
+      int ahead_tile = more ? ahead.tile0 : 0;
+      auto scores = [&]() {  // S^T of the tile `ahead`
+        if (ahead_tile == ahead.tile0) wait(&sh.q_full, items++ & 1);
+        const int buf = k_idx & 1, slot = (2 * k_idx) % kSlots;
+        wait(&sh.full[slot], ((2 * k_idx) / kSlots) & 1);
+        if (k_idx >= 2) wait(&sh.s_free[buf], ((k_idx >> 1) - 1) & 1);
+        tc_after();
+        const uint32_t k_at = ring + slot * L::kSlot;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint32_t in = (ks & 3) * 32, half = ks >> 2;
+          tc_mma(s_col[buf], operand(k_at + half * kHalf + in, 16, 1024, 2),
+                 operand(q_at + half * (N * 128) + in, 16, 1024, 2), instruction<N>(false, false), ks > 0);
+        }
+        tc_commit(&sh.s_full[buf]);
+        tc_commit(&sh.empty[slot]);
+        ++k_idx;
+        if (++ahead_tile == ahead.tile1) {
+          more = ahead.next();
+          if (more) ahead_tile = ahead.tile0;
+        }
+      };
+      if (more) scores();
+      int v_idx = 0;
+      while (at.next()) {
+        for (int tile = at.tile0; tile < at.tile1; ++tile, ++v_idx) {
+          if (more) scores();
+          const int slot = (2 * v_idx + 1) % kSlots;
+          wait(&sh.full[slot], ((2 * v_idx + 1) / kSlots) & 1);
+          wait(&sh.p_full, v_idx & 1);
+          tc_after();
+          const uint32_t v_at = ring + slot * L::kSlot;
+#pragma unroll
+          for (int part = 0; part < 2; ++part)
+#pragma unroll
+            for (int ks = 0; ks < kTile / 16; ++ks)
+              tc_mma(o_col, operand(v_at + ks * 2048, kHalves == 2 ? kHalf : 0, 1024, 2),
+                     operand(p_at + part * L::kP + ks * 256, 128, 2048, 0), instruction<N>(true, true),
+                     tile > at.tile0 || part > 0 || ks > 0);
+          tc_commit(&sh.empty[slot]);
+          tc_commit(&sh.p_free);
+        }
+      }
+    }
+    __syncwarp();
+  } else {
+    // ---- softmax, one token a thread ------------------------------------------
+    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;  // this warp's TMEM lanes
+    const uint32_t s_col[2] = {tmem + lanes, tmem + N + lanes}, o_col = tmem + 2 * N + lanes;
+    const int G = a.Hq / a.cache.heads;
+    auto load_q = [&](const Walk<N>& x) {
+      for (int e = tid; e < N * kChunks; e += kSoft) {
+        const int r = e / kChunks, c = e - r * kChunks;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (r < x.rows) {
+          const AttnRow ar = attn_row(a, x.row0 + r, x.h);
+          v = __ldg(reinterpret_cast<const uint4*>(a.q + x.b * a.q_batch + ar.i * a.q_token + ar.hq * a.q_head + c * 16));
+        }
+        *reinterpret_cast<uint4*>(q_s + (c >> 3) * (N * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
+      }
+      async_fence();
+      mbar_arrive(&sh.q_full);
+    };
+    Walk<N> ahead(a, plan);  // the item whose queries are loaded next
+    if (ahead.next()) load_q(ahead);
+    int tile_no = 0;
+    while (at.next()) {
+      // (the last item's readers of these are done: soft_sync in its finish)
+      for (int r = tid; r < N; r += kSoft) {
+        sh.m[r] = -INFINITY;
+        sh.limit[r] = at.n - a.Q + min(at.row0 + r, at.R - 1) / G;
+      }
+      if (tid == 0) sh.n_odd = 0;
+      float l[N];
+#pragma unroll
+      for (int r = 0; r < N; ++r) l[r] = 0.f;
+      soft_sync();
+      for (int tile = at.tile0; tile < at.tile1; ++tile, ++tile_no) {
+        const int buf = tile_no & 1, t = tile * kTile + tid;
+        wait(&sh.s_full[buf], (tile_no >> 1) & 1);
+        tc_after();
+        const uint32_t valid = sh.valid[tile_no & 7][warp];
+        const bool exists = (valid >> lane) & 1;
+        // a tile whose tokens all exist and are seen by every row needs no mask
+        const bool masked = tile * kTile + kTile - 1 > at.n - a.Q || soft_any(valid != 0xffffffffu);
+        auto score = [&](float x, int r) {
+          x *= a.scale_log2;
+          return masked && (!exists || t > sh.limit[r]) ? -INFINITY : x;
+        };
+        bool grow = false;
+#pragma unroll
+        for (int c = 0; c < N; c += 16) {
+          float s[16];
+          tmem_ld16(s, s_col[buf] + c);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) grow |= score(s[i], c + i) > sh.m[c + i] + kSlackT;
+        }
+        if (soft_any(grow)) {
+          // new reference maxima, and what has been summed so far by them
+#pragma unroll
+          for (int c = 0; c < N; c += 16) {
+            float s[16];
+            tmem_ld16(s, s_col[buf] + c);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              float x = score(s[i], c + i);
+#pragma unroll
+              for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+              if (lane == i) sh.wmax[warp][c + i] = x;
+            }
+          }
+          soft_sync();
+          for (int r = tid; r < N; r += kSoft) {
+            const float old = sh.m[r];
+            float m = old;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) m = fmaxf(m, sh.wmax[w][r]);
+            sh.m[r] = m;
+            sh.corr[r] = old == -INFINITY ? 0.f : ex2(old - m);
+          }
+          soft_sync();
+#pragma unroll
+          for (int r = 0; r < N; ++r) l[r] *= sh.corr[r];
+          if (tile > at.tile0) {
+            wait(&sh.p_free, (tile_no - 1) & 1);  // O^T is complete
+            tc_after();
+#pragma unroll
+            for (int c = 0; c < N; c += 16) {
+              float o[16];
+              tmem_ld16(o, o_col + c);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] *= sh.corr[c + i];
+              tmem_st16(o_col + c, o);
+            }
+            tmem_st_done();
+          }
+        }
+        if (tile_no > 0) wait(&sh.p_free, (tile_no - 1) & 1);  // P^T has been read
+        // A value that is not finite would reach rows that do not see its token
+        // as 0 * inf: such values are zero in the product, and added to the
+        // rows that see them at the end.
+        uint32_t odd = 0;
+        if (masked) {
+          const int slot = (2 * tile_no + 1) % kSlots;
+          wait(&sh.full[slot], ((2 * tile_no + 1) / kSlots) & 1);
+          uint4* v = reinterpret_cast<uint4*>(smem + slot * L::kSlot + tid * 128);
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c) {
+            uint4* piece = v + (c >> 3) * (kHalf / 16) + (c & 7);
+            uint4 x = *piece;
+            uint32_t u[4] = {x.x, x.y, x.z, x.w}, bad = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (nonfinite2(u[i])) {
+                bad = 1;
+                if ((u[i] & 0x7f80u) == 0x7f80u) u[i] &= 0xffff0000u;
+                if ((u[i] & 0x7f800000u) == 0x7f800000u) u[i] &= 0xffffu;
+              }
+            if (bad) *piece = make_uint4(u[0], u[1], u[2], u[3]);
+            odd |= bad;
+          }
+        }
+        uint32_t seen[(N + 31) / 32];
+#pragma unroll
+        for (int i = 0; i < (N + 31) / 32; ++i) seen[i] = 0;
+#pragma unroll
+        for (int c = 0; c < N; c += 16) {
+          float s[16];
+          tmem_ld16(s, s_col[buf] + c);
+          uint32_t hi[8], lo[8];
+#pragma unroll
+          for (int i = 0; i < 16; i += 2) {
+            float p[2];
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const float m = sh.m[c + i + y];
+              p[y] = ex2(score(s[i + y], c + i + y) - (m == -INFINITY ? 0.f : m));
+              l[c + i + y] += p[y];
+              if (p[y] != 0.f) seen[(c + i + y) >> 5] |= 1u << ((c + i + y) & 31);
+            }
+            hi[i / 2] = pack2(p[0], p[1]);
+            lo[i / 2] = pack2(p[0] - bf16_lo(hi[i / 2]), p[1] - bf16_hi(hi[i / 2]));
+          }
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            char* to = p_s + (c / 8 + g) * (kTile * 16) + tid * 16;
+            *reinterpret_cast<uint4*>(to) = make_uint4(hi[4 * g], hi[4 * g + 1], hi[4 * g + 2], hi[4 * g + 3]);
+            *reinterpret_cast<uint4*>(to + L::kP) = make_uint4(lo[4 * g], lo[4 * g + 1], lo[4 * g + 2], lo[4 * g + 3]);
+          }
+        }
+        if (odd) {
+          const int i = atomicAdd(&sh.n_odd, 1);
+          if (i < kTile) {
+            sh.odd_token[i] = t;
+#pragma unroll
+            for (int x = 0; x < (N + 31) / 32; ++x) sh.odd_rows[i][x] = seen[x];
+          }
+        }
+        async_fence();
+        tc_before();
+        mbar_arrive(&sh.s_free[buf]);
+        mbar_arrive(&sh.p_full);
+      }
+      // ---- the item, or this block's part of it ---------------------------------
+      if (ahead.next()) load_q(ahead);  // its last scores are done: s_full has come
+      // sums over the tokens: a butterfly that halves the rows with the lanes
+#pragma unroll
+      for (int c = 0; c < N; c += 32) {
+        float v[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = c + i < N ? l[c + i < N ? c + i : 0] : 0.f;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+          for (int i = 0; i < o; ++i) {
+            const float give = (lane & o) ? v[i] : v[i + o], keep = (lane & o) ? v[i + o] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+          }
+        if (c + lane < N) sh.lsum[warp][c + lane] = v[0];
+      }
+      wait(&sh.p_free, (tile_no - 1) & 1);
+      tc_after();
+      soft_sync();
+      const bool whole = at.tile0 == 0 && at.tile1 == at.tiles;
+      float* slot = attn_slot<N, D>(a, blockIdx.x, at.tile0 == 0);
+      const int d = tid;  // D 64: lanes 64.. hold the same again
+      const int n_odd = min(sh.n_odd, kTile);
+#pragma unroll
+      for (int c = 0; c < N; c += 16) {
+        float o[16];
+        tmem_ld16(o, o_col + c);
+        if (n_odd > 0 && d < D) {
+          for (int k = 0; k < n_odd; ++k) {
+            const int t = sh.odd_token[k];
+            const int entry = static_cast<int>(by_page(static_cast<unsigned long long>(t)));
+            const int page = a.table.ids[at.b * a.table.stride + entry];
+            const float v = load_one<BF16>(a.cache.v + page * a.cache.page_stride +
+                                               (t - entry * a.cache.page_size) * a.cache.token_stride + at.h * (D * 2), d);
+            if (!isfinite(v))
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                if ((sh.odd_rows[k][(c + i) >> 5] >> ((c + i) & 31)) & 1) o[i] += v;
+          }
+        }
+        if (d < D) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int r = c + i;
+            if (r >= at.rows) continue;
+            if (whole) {
+              const float sum = sh.lsum[0][r] + sh.lsum[1][r] + sh.lsum[2][r] + sh.lsum[3][r];
+              const AttnRow ar = attn_row(a, at.row0 + r, at.h);
+              const size_t to = (static_cast<size_t>(at.b) * a.Q + ar.i) * a.Hq + ar.hq;
+              const float x = o[i] * (sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum));
+              static_cast<uint16_t*>(a.out)[to * D + d] = static_cast<uint16_t>(pack2(x, x) & 0xffffu);
+              if (d == 0 && a.lse) a.lse[to] = sum == 0.f ? -INFINITY : (sh.m[r] + log2f(sum)) * kLn2;
+            } else {
+              slot[r * D + d] = o[i];
+            }
+          }
+        }
+      }
+      if (!whole) {
+        for (int r = tid; r < at.rows; r += kSoft) {
+          slot[N * D + r] = sh.m[r];
+          slot[N * D + N + r] = sh.lsum[0][r] + sh.lsum[1][r] + sh.lsum[2][r] + sh.lsum[3][r];
+        }
+        const long long c0 = at.first() / at.per, c1 = (at.first() + at.tiles - 1) / at.per;
+        soft_sync();
+        if (tid == 0) {
+          __threadfence();
+          const bool last = atom_add_acq_rel_gpu(&a.counters[c0], 1u) + 1u == static_cast<unsigned int>(c1 - c0 + 1);
+          if (last) a.counters[c0] = 0u;
+          sh.last = last;
+        }
+        soft_sync();
+        if (sh.last) attn_join<N, D, kSoft>(a, at.b, at.h, at.row0, at.rows, at.first(), at.tiles, at.per);
+      }
+      tc_before();  // O^T has been read
+      soft_sync();
+    }
+  }
+  tc_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_after();
+    tmem_free(tmem, L::kCols);
+  }
+}
+
+template <int D, int N>
+cudaError_t prepare() {
+  return cudaFuncSetAttribute(attention_tc_kernel<D, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D, N>::kBytes);
+}
+template <int D, int N>
+void launch(const AttnArgs& a, int grid, cudaStream_t stream) {
+  attention_tc_kernel<D, N><<<grid, kThreadsT, Lay<D, N>::kBytes, stream>>>(
+      a, DivU64::make(static_cast<unsigned long long>(a.cache.page_size)));
+}
+
+}  // namespace tc
+}  // namespace specv
