@@ -214,11 +214,11 @@ size_t attention_workspace(int D, bool bf16) {
 }
 
 cudaError_t attention_prepare() {
-  cudaError_t e = mma::prepare<64, 1>();
-  if (e == cudaSuccess) e = mma::prepare<128, 1>();
-  if (e == cudaSuccess) e = attention_tc_prepare_64();
-  if (e == cudaSuccess) e = attention_tc_prepare_128();
-  return e;
+  cudaError_t e[] = {mma::prepare<64, 1>(), mma::prepare<128, 1>(), attention_tc_prepare_64(),
+                     attention_tc_prepare_128()};
+  for (cudaError_t x : e)
+    if (x != cudaSuccess) return x;
+  return cudaSuccess;
 }
 
 cudaError_t launch_attention(const AttnArgs& a, int sm_count, cudaStream_t stream) {
@@ -236,7 +236,7 @@ cudaError_t launch_attention(const AttnArgs& a, int sm_count, cudaStream_t strea
     else mma::launch<64, 1>(a, grid, stream);
     return cudaGetLastError();
   }
-  // Rows in tiles of equal size, a multiple of 16 and at most 96.
+  // rows in tiles of equal size, a multiple of 16 and at most 96
   const int tiles = (R + kMaxRowsTc - 1) / kMaxRowsTc;
   const int n16 = ((R + tiles - 1) / tiles + 15) / 16;
   const int grid = sm_count < kMaxMmaCtas ? sm_count : kMaxMmaCtas;

@@ -13,10 +13,13 @@
 // (P^T counts twice, below), a few hundred cycles where its 64 KB take HBM
 // three thousand.
 //
-// One block per SM.  Warps 4-7 stream tiles through a ring of slots in shared
-// memory (cp.async in 16-byte pieces, so any page size and any strides), K
-// and V in turn, across item boundaries.  Warp 8 issues the products.  Warps
-// 0-3 hold one token a thread: they read S^T, keep each row's reference
+// One block per SM.  Warps 4 and 5 stream tiles through a ring of slots in
+// shared memory, K and V in turn, across item boundaries: cp.async in 16-byte
+// pieces, whose landing arrives on the slot's barrier by itself, so any page
+// size and any strides.  (TMA boxes of a page's tokens, 128 bytes a row,
+// moved 23 bytes a cycle an SM however many warps issued them, about what
+// HBM delivers and no more: 317 us where this takes SLOT.)  Warp 6 issues the
+// products.  Warps 0-3 hold one token a thread: they read S^T, keep each row's reference
 // maximum (moved only when a score passes it by 2^8), write the weights P^T
 // as two bf16 parts (hi and lo: one bf16 weight would lose up to 2^-8 of a
 // term, as much as rounding the output does) and finish items.
@@ -29,14 +32,12 @@ namespace specv {
 namespace tc {
 
 using mma::cp16;
-using mma::cp_commit;
-using mma::cp_wait;
 using mma::nonfinite2;
 using mma::pack2;
 
 constexpr int kTile = 128;               // tokens
 constexpr int kSoft = 128;               // softmax threads (warps 0-3)
-constexpr int kLoad = 128;               // loader threads (warps 4-7)
+constexpr int kLoad = 64;                // loader threads (warps 4 and 5); warp 6 issues the products
 constexpr int kThreadsT = kSoft + kLoad + 32;
 constexpr float kSlackT = 8.f;
 
@@ -47,7 +48,6 @@ struct Lay {
   static constexpr int kP = kTile * N * 2;      // one part of P^T
   static constexpr int kFree = 216 * 1024 - kQ - 2 * kP;  // (about 9 KB more are static)
   static constexpr int kSlots = kFree / kSlot < 8 ? kFree / kSlot : 8;
-  static constexpr int kLag = kSlots - 2;       // slots in flight
   static constexpr int kBytes = kSlots * kSlot + kQ + 2 * kP + 1024;  // 1024: alignment
   static constexpr int kCols = 3 * N <= 64 ? 64 : 3 * N <= 128 ? 128 : 3 * N <= 256 ? 256 : 512;
   static_assert(kSlots >= 4, "two tiles");
@@ -64,15 +64,20 @@ __device__ __forceinline__ void tmem_free(uint32_t at, uint32_t cols) {
 }
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// The whole warp runs up to these and one lane issues: control flow that the
+// warp shares keeps addresses and descriptors in uniform registers (issued
+// under `if (lane == 0)` a product took 78 cycles).
 // Arrives on `bar` when every product issued so far is done.
 __device__ __forceinline__ void tc_commit(unsigned long long* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
-               : "memory");
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar))
+      : "memory");
 }
 __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.u32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u)
       : "memory");
 }
@@ -94,6 +99,10 @@ __device__ __forceinline__ void tmem_st16(uint32_t at, const float (&v)[16]) {
       : "memory");
 }
 __device__ __forceinline__ void tmem_st_done() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// Arrives on `bar` when the thread's copies so far have landed.
+__device__ __forceinline__ void cp_arrive(unsigned long long* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
 __device__ __forceinline__ void async_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // Shared-memory operand: start, leading and stride byte offsets; swizzle 128
@@ -111,7 +120,7 @@ __device__ __forceinline__ constexpr uint32_t instruction(bool a_mn, bool b_mn) 
 }
 
 __device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
-__device__ __forceinline__ void load_sync() { asm volatile("bar.sync 2, 128;" ::: "memory"); }
+__device__ __forceinline__ void load_sync() { asm volatile("bar.sync 2, 64;" ::: "memory"); }
 __device__ __forceinline__ bool soft_any(bool x) {
   uint32_t r;
   asm volatile(
@@ -170,6 +179,9 @@ struct SharedT {
   uint32_t valid[8][4];                // tokens that exist, by tile
   float m[N], corr[N], wmax[4][N], lsum[4][N];
   int limit[N];                        // last token that a row sees
+  long long q_off[N];                  // of the next item's rows, bytes
+  long long out_at[N];                 // of the item's rows: index of [b][i][hq]
+  float inv[N];
   uint32_t odd_rows[kTile][(N + 31) / 32];
   int odd_token[kTile];
   int n_odd;
@@ -182,7 +194,7 @@ struct SharedT {
 template <int D, int N>
 __global__ void __launch_bounds__(kThreadsT, 1) attention_tc_kernel(const AttnArgs a, DivU64 by_page) {
   using L = Lay<D, N>;
-  constexpr int kSlots = L::kSlots, kLag = L::kLag, kHalves = D / 64, kHalf = kTile * 128;
+  constexpr int kSlots = L::kSlots, kHalves = D / 64, kHalf = kTile * 128;
   constexpr int kChunks = D / 8;  // 16-byte pieces of a token
   extern __shared__ char raw_smem[];
   __shared__ SharedT<D, N> sh;
@@ -216,73 +228,84 @@ __global__ void __launch_bounds__(kThreadsT, 1) attention_tc_kernel(const AttnAr
     sh.dead = 0;
     fence_barrier_init();
   }
-  if (warp == 8) tmem_alloc(&sh.tmem, L::kCols);
+  if (warp == 6) tmem_alloc(&sh.tmem, L::kCols);
   tc_before();
   __syncthreads();
   tc_after();
   const uint32_t tmem = sh.tmem;
   Walk<N> at(a, plan);
 
-  if (warp >= 4 && warp < 8) {
-    // ---- loaders: K and V of each tile, in turn ---------------------------
+  if (warp == 4 || warp == 5) {
+    // ---- K and V of each tile, in turn -----------------------------------
     const int lt = tid - kSoft, S = a.cache.page_size;
     const int chunk = lt % kChunks, r0 = lt / kChunks;
-    constexpr int kStep = kLoad / kChunks, kRows = kTile / kStep;
-    int slot = 0, seen = 0, sent = 0;  // the slot to fill; slots filled, announced
-    uint32_t turn = 0;                 // times the ring went round
-    auto announce = [&]() {
-      async_fence();
-      mbar_arrive(&sh.full[sent % kSlots]);
-      ++sent;
-    };
-    int tile_no = 0;
-    while (at.next()) {
-      const int32_t* table = a.table.ids + at.b * a.table.stride;
-      for (int tile = at.tile0; tile < at.tile1; ++tile, ++tile_no) {
-        const int t = tile * kTile + lt;
-        long long o = -1;
-        if (t < at.n) {
-          const int entry = static_cast<int>(by_page(static_cast<unsigned long long>(t)));
-          const int page = table[entry];
-          if (page >= 0 && page < a.cache.pages)
-            o = page * a.cache.page_stride + (t - entry * S) * a.cache.token_stride + at.h * (D * 2);
-          else if (a.status)
-            atomicOr(a.status, kDataPageRange);
-        }
-        const uint32_t valid = __ballot_sync(0xffffffffu, o >= 0);
-        if (lane == 0) sh.valid[tile_no & 7][warp - 4] = valid;
-        sh.off[tile_no & 1][lt] = o;
-        load_sync();
-        const long long* off = sh.off[tile_no & 1];
-#pragma unroll 1
-        for (int x = 0; x < 2; ++x) {
-          if (seen >= kSlots) wait(&sh.empty[slot], (turn + 1) & 1);
-          const char* pool = (x ? a.cache.v : a.cache.k) + chunk * 16;
-          const uint32_t dst = smem_addr(smem) + slot * L::kSlot + (chunk >> 3) * kHalf;
+    constexpr int kStep = kLoad / kChunks, kRows = kTile / kStep, kLook = kTile / kLoad;
+    // The tile whose pages are looked up, one ahead of the copies: the table's
+    // entries are on their way while the tile before is copied.
+    Walk<N> ahead(a, plan);
+    bool more = ahead.next();
+    int ahead_tile = more ? ahead.tile0 : 0;
+    int page[kLook], place[kLook], head = 0;  // place: token in the page, -1: past the end
+    auto look_up = [&]() {
+      head = ahead.h;
 #pragma unroll
-          for (int i = 0; i < kRows; ++i) {
-            const int r = r0 + i * kStep;
-            const long long from = off[r];
-            cp16(dst + r * 128 + (((chunk & 7) ^ (r & 7)) << 4), pool + (from < 0 ? 0 : from), from < 0 ? 0 : 16);
+      for (int i = 0; i < kLook; ++i) {
+        const int t = ahead_tile * kTile + i * kLoad + lt;
+        const int entry = static_cast<int>(by_page(static_cast<unsigned long long>(t)));
+        place[i] = t < ahead.n ? t - entry * S : -1;
+        page[i] = t < ahead.n ? __ldg(a.table.ids + ahead.b * a.table.stride + entry) : -1;
+      }
+      if (++ahead_tile == ahead.tile1) {
+        more = ahead.next();
+        if (more) ahead_tile = ahead.tile0;
+      }
+    };
+    if (more) look_up();
+    int slot = 0;
+    uint32_t turn = 0;  // times the ring went round
+    for (int tile_no = 0; at.w < at.end; ++tile_no) {
+#pragma unroll
+      for (int i = 0; i < kLook; ++i) {
+        const bool ok = page[i] >= 0 && page[i] < a.cache.pages;
+        if (!ok && place[i] >= 0 && a.status) atomicOr(a.status, kDataPageRange);
+        const uint32_t valid = __ballot_sync(0xffffffffu, ok);
+        if (lane == 0) sh.valid[tile_no & 7][i * (kLoad / 32) + warp - 4] = valid;
+        sh.off[tile_no & 1][i * kLoad + lt] =
+            ok ? page[i] * a.cache.page_stride + place[i] * a.cache.token_stride + head * (D * 2) : -1ll;
+      }
+      load_sync();
+      const bool last = !more;
+      if (more) look_up();
+      const long long* off = sh.off[tile_no & 1] + r0;
+#pragma unroll 1
+      for (int x = 0; x < 2; ++x) {
+        if (turn > 0) wait(&sh.empty[slot], (turn + 1) & 1);
+        const char* pool = (x ? a.cache.v : a.cache.k) + chunk * 16;
+        const uint32_t dst = smem_addr(smem) + slot * L::kSlot + (chunk >> 3) * kHalf + r0 * 128;
+#pragma unroll 1
+        for (int i0 = 0; i0 < kRows; i0 += 8) {
+          long long from[8];  // read ahead of the copies, which no load passes
+#pragma unroll
+          for (int i = 0; i < 8; ++i) from[i] = off[(i0 + i) * kStep];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r = (i0 + i) * kStep;
+            cp16(dst + r * 128 + (((chunk & 7) ^ ((r0 + r) & 7)) << 4), pool + (from[i] < 0 ? 0 : from[i]),
+                 from[i] < 0 ? 0 : 16);
           }
-          cp_commit();
-          ++seen;
-          if (++slot == kSlots) {
-            slot = 0;
-            ++turn;
-          }
-          if (seen > kLag) {
-            cp_wait<kLag>();
-            announce();
-          }
+        }
+        cp_arrive(&sh.full[slot]);
+        if (++slot == kSlots) {
+          slot = 0;
+          ++turn;
         }
       }
+      if (last) break;
     }
-    cp_wait<0>();
-    while (sent < seen) announce();
-  } else if (warp == 8) {
+    asm volatile("cp.async.wait_all;" ::: "memory");  // no copy is under way when the block leaves
+  } else if (warp == 6) {
     // ---- the products ------------------------------------------------------
-    if (lane == 0) {
+    {
       const uint32_t ring = smem_addr(smem), q_at = smem_addr(q_s), p_at = smem_addr(p_s);
       const uint32_t s_col[2] = {tmem, tmem + N}, o_col = tmem + 2 * N;
       int k_idx = 0, items = 0;
@@ -294,6 +317,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) attention_tc_kernel(const AttnAr
         const int buf = k_idx & 1, slot = (2 * k_idx) % kSlots;
         wait(&sh.full[slot], ((2 * k_idx) / kSlots) & 1);
         if (k_idx >= 2) wait(&sh.s_free[buf], ((k_idx >> 1) - 1) & 1);
+        async_fence();  // the loaders' copies, to the products
         tc_after();
         const uint32_t k_at = ring + slot * L::kSlot;
 #pragma unroll
@@ -318,6 +342,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) attention_tc_kernel(const AttnAr
           const int slot = (2 * v_idx + 1) % kSlots;
           wait(&sh.full[slot], ((2 * v_idx + 1) / kSlots) & 1);
           wait(&sh.p_full, v_idx & 1);
+          async_fence();
           tc_after();
           const uint32_t v_at = ring + slot * L::kSlot;
 #pragma unroll
@@ -339,13 +364,17 @@ __global__ void __launch_bounds__(kThreadsT, 1) attention_tc_kernel(const AttnAr
     const uint32_t s_col[2] = {tmem + lanes, tmem + N + lanes}, o_col = tmem + 2 * N + lanes;
     const int G = a.Hq / a.cache.heads;
     auto load_q = [&](const Walk<N>& x) {
-      for (int e = tid; e < N * kChunks; e += kSoft) {
-        const int r = e / kChunks, c = e - r * kChunks;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (r < x.rows) {
-          const AttnRow ar = attn_row(a, x.row0 + r, x.h);
-          v = __ldg(reinterpret_cast<const uint4*>(a.q + x.b * a.q_batch + ar.i * a.q_token + ar.hq * a.q_head + c * 16));
-        }
+      for (int r = tid; r < N; r += kSoft) {
+        const AttnRow ar = attn_row(a, x.row0 + min(r, x.rows - 1), x.h);
+        sh.q_off[r] = x.b * a.q_batch + ar.i * a.q_token + ar.hq * a.q_head;
+      }
+      soft_sync();
+      constexpr int kPieces = N * kChunks / kSoft;  // a thread's: 2 to 12
+#pragma unroll 4
+      for (int k = 0; k < kPieces; ++k) {
+        const int e = k * kSoft + tid, r = e / kChunks, c = e % kChunks;
+        uint4 v = __ldg(reinterpret_cast<const uint4*>(a.q + sh.q_off[r] + c * 16));
+        if (r >= x.rows) v = make_uint4(0, 0, 0, 0);
         *reinterpret_cast<uint4*>(q_s + (c >> 3) * (N * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
       }
       async_fence();
@@ -369,10 +398,11 @@ __global__ void __launch_bounds__(kThreadsT, 1) attention_tc_kernel(const AttnAr
         const int buf = tile_no & 1, t = tile * kTile + tid;
         wait(&sh.s_full[buf], (tile_no >> 1) & 1);
         tc_after();
-        const uint32_t valid = sh.valid[tile_no & 7][warp];
-        const bool exists = (valid >> lane) & 1;
+        const uint32_t* valid = sh.valid[tile_no & 7];
+        const bool exists = (valid[warp] >> lane) & 1;
         // a tile whose tokens all exist and are seen by every row needs no mask
-        const bool masked = tile * kTile + kTile - 1 > at.n - a.Q || soft_any(valid != 0xffffffffu);
+        const bool masked =
+            tile * kTile + kTile - 1 > at.n - a.Q || (valid[0] & valid[1] & valid[2] & valid[3]) != 0xffffffffu;
         auto score = [&](float x, int r) {
           x *= a.scale_log2;
           return masked && (!exists || t > sh.limit[r]) ? -INFINITY : x;
@@ -430,13 +460,13 @@ __global__ void __launch_bounds__(kThreadsT, 1) attention_tc_kernel(const AttnAr
         // as 0 * inf: such values are zero in the product, and added to the
         // rows that see them at the end.
         uint32_t odd = 0;
-        if (masked) {
+        if (masked && t > at.n - a.Q) {  // (tokens that do not exist are zero-filled)
           const int slot = (2 * tile_no + 1) % kSlots;
           wait(&sh.full[slot], ((2 * tile_no + 1) / kSlots) & 1);
           uint4* v = reinterpret_cast<uint4*>(smem + slot * L::kSlot + tid * 128);
-#pragma unroll
+#pragma unroll 4
           for (int c = 0; c < kChunks; ++c) {
-            uint4* piece = v + (c >> 3) * (kHalf / 16) + (c & 7);
+            uint4* piece = v + (c >> 3) * (kHalf / 16) + ((c ^ tid) & 7);  // (in an order without bank conflicts)
             uint4 x = *piece;
             uint32_t u[4] = {x.x, x.y, x.z, x.w}, bad = 0;
 #pragma unroll
@@ -513,9 +543,24 @@ __global__ void __launch_bounds__(kThreadsT, 1) attention_tc_kernel(const AttnAr
       soft_sync();
       const bool whole = at.tile0 == 0 && at.tile1 == at.tiles;
       float* slot = attn_slot<N, D>(a, blockIdx.x, at.tile0 == 0);
+      for (int r = tid; r < at.rows; r += kSoft) {
+        const float sum = sh.lsum[0][r] + sh.lsum[1][r] + sh.lsum[2][r] + sh.lsum[3][r], m = sh.m[r];
+        if (whole) {
+          const AttnRow ar = attn_row(a, at.row0 + r, at.h);
+          const size_t to = (static_cast<size_t>(at.b) * a.Q + ar.i) * a.Hq + ar.hq;
+          sh.out_at[r] = static_cast<long long>(to);
+          sh.inv[r] = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+          if (a.lse) a.lse[to] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
+        } else {
+          slot[N * D + r] = m;
+          slot[N * D + N + r] = sum;
+        }
+      }
+      // O^T through shared memory (P^T's place), a row's D values together
+      float* o_s = reinterpret_cast<float*>(p_s);
       const int d = tid;  // D 64: lanes 64.. hold the same again
       const int n_odd = min(sh.n_odd, kTile);
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < N; c += 16) {
         float o[16];
         tmem_ld16(o, o_col + c);
@@ -532,29 +577,22 @@ __global__ void __launch_bounds__(kThreadsT, 1) attention_tc_kernel(const AttnAr
                 if ((sh.odd_rows[k][(c + i) >> 5] >> ((c + i) & 31)) & 1) o[i] += v;
           }
         }
-        if (d < D) {
+        if (d < D)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int r = c + i;
-            if (r >= at.rows) continue;
-            if (whole) {
-              const float sum = sh.lsum[0][r] + sh.lsum[1][r] + sh.lsum[2][r] + sh.lsum[3][r];
-              const AttnRow ar = attn_row(a, at.row0 + r, at.h);
-              const size_t to = (static_cast<size_t>(at.b) * a.Q + ar.i) * a.Hq + ar.hq;
-              const float x = o[i] * (sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum));
-              static_cast<uint16_t*>(a.out)[to * D + d] = static_cast<uint16_t>(pack2(x, x) & 0xffffu);
-              if (d == 0 && a.lse) a.lse[to] = sum == 0.f ? -INFINITY : (sh.m[r] + log2f(sum)) * kLn2;
-            } else {
-              slot[r * D + d] = o[i];
-            }
-          }
+          for (int i = 0; i < 16; ++i) o_s[(c + i) * D + d] = o[i];
+      }
+      soft_sync();
+      for (int e = tid; e < at.rows * (D / 4); e += kSoft) {
+        const int r = e / (D / 4), x = (e % (D / 4)) * 4;
+        float4 v = *reinterpret_cast<const float4*>(o_s + r * D + x);
+        if (whole) {
+          const float inv = sh.inv[r];
+          store4(a.out, sh.out_at[r] * D + x, true, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+        } else {
+          *reinterpret_cast<float4*>(slot + r * D + x) = v;
         }
       }
       if (!whole) {
-        for (int r = tid; r < at.rows; r += kSoft) {
-          slot[N * D + r] = sh.m[r];
-          slot[N * D + N + r] = sh.lsum[0][r] + sh.lsum[1][r] + sh.lsum[2][r] + sh.lsum[3][r];
-        }
         const long long c0 = at.first() / at.per, c1 = (at.first() + at.tiles - 1) / at.per;
         soft_sync();
         if (tid == 0) {
@@ -572,7 +610,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) attention_tc_kernel(const AttnAr
   }
   tc_before();
   __syncthreads();
-  if (warp == 8) {
+  if (warp == 6) {
     tc_after();
     tmem_free(tmem, L::kCols);
   }
