@@ -203,8 +203,14 @@ __global__ void __launch_bounds__(kThreadsF) attention_kernel(const AttnArgs a) 
 
 }  // namespace
 
-// Up to 8 rows a cache head go to attention_mma.cuh, more to attention_tc.cuh.
-constexpr int kMmaRows = 8;
+// Rows a cache head (R = Q * Hq / Hkv) choose the bf16 kernel: up to 24 go to
+// attention_mma.cuh, more to attention_tc.cuh.  At 64 sequences of 400..4000
+// tokens, Hq 32, Hkv 8, D 128 (floor 94 to 96 us) the two took
+//   R = 4: 109 and 147 us;  16: 126 and 147;  24: 140 and 178;
+//   R = 32: 235 and 180;    68: 360 and 302
+// (a fourth block of 8 rows leaves mma without registers; its K and V come
+// through L2 once more a block of rows), with D 64 and R = 24: 100 and 149.
+constexpr int kMmaRows = 24;
 constexpr int kMaxMmaCtas = 304;
 
 size_t attention_workspace(int D, bool bf16) {
@@ -214,8 +220,9 @@ size_t attention_workspace(int D, bool bf16) {
 }
 
 cudaError_t attention_prepare() {
-  cudaError_t e[] = {mma::prepare<64, 1>(), mma::prepare<128, 1>(), attention_tc_prepare_64(),
-                     attention_tc_prepare_128()};
+  cudaError_t e[] = {mma::prepare<64, 1>(),  mma::prepare<64, 2>(),  mma::prepare<64, 3>(),
+                     mma::prepare<128, 1>(), mma::prepare<128, 2>(), mma::prepare<128, 3>(),
+                     attention_tc_prepare_64(), attention_tc_prepare_128()};
   for (cudaError_t x : e)
     if (x != cudaSuccess) return x;
   return cudaSuccess;
@@ -232,11 +239,17 @@ cudaError_t launch_attention(const AttnArgs& a, int sm_count, cudaStream_t strea
   const int R = a.Q * (a.Hq / a.cache.heads);
   if (R <= kMmaRows) {
     const int grid = sm_count * 2 < kMaxMmaCtas ? sm_count * 2 : kMaxMmaCtas;
-    if (wide) mma::launch<128, 1>(a, grid, stream);
-    else mma::launch<64, 1>(a, grid, stream);
+    switch ((R + 7) / 8 + (wide ? 3 : 0)) {
+      case 1: mma::launch<64, 1>(a, grid, stream); break;
+      case 2: mma::launch<64, 2>(a, grid, stream); break;
+      case 3: mma::launch<64, 3>(a, grid, stream); break;
+      case 4: mma::launch<128, 1>(a, grid, stream); break;
+      case 5: mma::launch<128, 2>(a, grid, stream); break;
+      default: mma::launch<128, 3>(a, grid, stream); break;
+    }
     return cudaGetLastError();
   }
-  // rows in tiles of equal size, a multiple of 16 and at most 96
+  // rows in tiles of equal size, a multiple of 16 and at most 96 (and so 32 at least)
   const int tiles = (R + kMaxRowsTc - 1) / kMaxRowsTc;
   const int n16 = ((R + tiles - 1) / tiles + 15) / 16;
   const int grid = sm_count < kMaxMmaCtas ? sm_count : kMaxMmaCtas;

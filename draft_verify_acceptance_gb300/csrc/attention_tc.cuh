@@ -13,16 +13,17 @@
 // (P^T counts twice, below), a few hundred cycles where its 64 KB take HBM
 // three thousand.
 //
-// One block per SM.  Warps 4 and 5 stream tiles through a ring of slots in
+// One block per SM.  Warps 8-10 stream tiles through a ring of slots in
 // shared memory, K and V in turn, across item boundaries: cp.async in 16-byte
 // pieces, whose landing arrives on the slot's barrier by itself, so any page
-// size and any strides.  (TMA boxes of a page's tokens, 128 bytes a row,
-// moved 23 bytes a cycle an SM however many warps issued them, about what
-// HBM delivers and no more: 317 us where this takes SLOT.)  Warp 6 issues the
-// products.  Warps 0-3 hold one token a thread: they read S^T, keep each row's reference
-// maximum (moved only when a score passes it by 2^8), write the weights P^T
-// as two bf16 parts (hi and lo: one bf16 weight would lose up to 2^-8 of a
-// term, as much as rounding the output does) and finish items.
+// size and any strides.  (TMA boxes of a page's tokens, 128 bytes a row, moved
+// 23 bytes a cycle an SM however many warps issued them, about what HBM
+// delivers and no more.)  Warp 11 issues the products.  Warps 0-3 hold one
+// token a thread and half of the rows, warps 4-7 the same tokens and the other
+// half: they read S^T, keep each row's reference maximum (moved only when a
+// score passes it by 2^8), write the weights P^T as two bf16 parts (hi and
+// lo: one bf16 weight would lose up to 2^-8 of a term, as much as rounding the
+// output does) and finish items.
 #pragma once
 
 #include "attention_common.cuh"
@@ -36,8 +37,8 @@ using mma::nonfinite2;
 using mma::pack2;
 
 constexpr int kTile = 128;               // tokens
-constexpr int kSoft = 128;               // softmax threads (warps 0-3)
-constexpr int kLoad = 64;                // loader threads (warps 4 and 5); warp 6 issues the products
+constexpr int kSoft = 256;               // softmax threads: two groups of four warps
+constexpr int kLoad = 96;                // loader threads
 constexpr int kThreadsT = kSoft + kLoad + 32;
 constexpr float kSlackT = 8.f;
 
@@ -81,22 +82,18 @@ __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint3
       "l"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u)
       : "memory");
 }
-__device__ __forceinline__ void tmem_ld16(float (&v)[16], uint32_t at) {
+__device__ __forceinline__ void tmem_ld8(float (&v)[8], uint32_t at) {
   uint32_t* r = reinterpret_cast<uint32_t*>(v);
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(at));
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(at));
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void tmem_st16(uint32_t at, const float (&v)[16]) {
+__device__ __forceinline__ void tmem_st8(uint32_t at, const float (&v)[8]) {
   const uint32_t* r = reinterpret_cast<const uint32_t*>(v);
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 __device__ __forceinline__ void tmem_st_done() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 // Arrives on `bar` when the thread's copies so far have landed.
@@ -119,14 +116,16 @@ __device__ __forceinline__ constexpr uint32_t instruction(bool a_mn, bool b_mn) 
          (static_cast<uint32_t>(N >> 3) << 17) | (8u << 24);
 }
 
-__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
-__device__ __forceinline__ void load_sync() { asm volatile("bar.sync 2, 64;" ::: "memory"); }
-__device__ __forceinline__ bool soft_any(bool x) {
+__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ void load_sync() { asm volatile("bar.sync 2, 96;" ::: "memory"); }
+// Group barriers (3 and 4), the second with a vote.
+__device__ __forceinline__ void group_sync(int group) { asm volatile("bar.sync %0, 128;" ::"r"(3 + group) : "memory"); }
+__device__ __forceinline__ bool group_any(int group, bool x) {
   uint32_t r;
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"(x ? 1u : 0u)
+      : "r"(x ? 1u : 0u), "r"(3 + group)
       : "memory");
   return r != 0;
 }
@@ -182,9 +181,7 @@ struct SharedT {
   long long q_off[N];                  // of the next item's rows, bytes
   long long out_at[N];                 // of the item's rows: index of [b][i][hq]
   float inv[N];
-  uint32_t odd_rows[kTile][(N + 31) / 32];
-  int odd_token[kTile];
-  int n_odd;
+  int odd;                             // the item has values that are not finite and not every row sees
   uint32_t tmem;
   int dead;                            // a wait ran out: nothing waits any more
   int last;
@@ -228,18 +225,18 @@ __global__ void __launch_bounds__(kThreadsT, 1) attention_tc_kernel(const AttnAr
     sh.dead = 0;
     fence_barrier_init();
   }
-  if (warp == 6) tmem_alloc(&sh.tmem, L::kCols);
+  if (warp == 11) tmem_alloc(&sh.tmem, L::kCols);
   tc_before();
   __syncthreads();
   tc_after();
   const uint32_t tmem = sh.tmem;
   Walk<N> at(a, plan);
 
-  if (warp == 4 || warp == 5) {
+  if (warp >= 8 && warp < 11) {
     // ---- K and V of each tile, in turn -----------------------------------
     const int lt = tid - kSoft, S = a.cache.page_size;
     const int chunk = lt % kChunks, r0 = lt / kChunks;
-    constexpr int kStep = kLoad / kChunks, kRows = kTile / kStep, kLook = kTile / kLoad;
+    constexpr int kStep = kLoad / kChunks, kRows = (kTile + kStep - 1) / kStep, kLook = (kTile + kLoad - 1) / kLoad;
     // The tile whose pages are looked up, one ahead of the copies: the table's
     // entries are on their way while the tile before is copied.
     Walk<N> ahead(a, plan);
@@ -251,9 +248,10 @@ __global__ void __launch_bounds__(kThreadsT, 1) attention_tc_kernel(const AttnAr
 #pragma unroll
       for (int i = 0; i < kLook; ++i) {
         const int t = ahead_tile * kTile + i * kLoad + lt;
+        const bool in = t < ahead.n && i * kLoad + lt < kTile;
         const int entry = static_cast<int>(by_page(static_cast<unsigned long long>(t)));
-        place[i] = t < ahead.n ? t - entry * S : -1;
-        page[i] = t < ahead.n ? __ldg(a.table.ids + ahead.b * a.table.stride + entry) : -1;
+        place[i] = in ? t - entry * S : -1;
+        page[i] = in ? __ldg(a.table.ids + ahead.b * a.table.stride + entry) : -1;
       }
       if (++ahead_tile == ahead.tile1) {
         more = ahead.next();
@@ -261,37 +259,56 @@ __global__ void __launch_bounds__(kThreadsT, 1) attention_tc_kernel(const AttnAr
       }
     };
     if (more) look_up();
+    // where the thread's piece of row r0 + i * kStep lies in the swizzled slot:
+    // the rows' low three bits go round every four (or two) steps
+    uint32_t place_of[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      place_of[i] = (chunk >> 3) * kHalf + r0 * 128 + (((chunk & 7) ^ ((r0 + i * kStep) & 7)) << 4);
+    static_assert(4 * kStep % 8 == 0, "four steps go round");
     int slot = 0;
     uint32_t turn = 0;  // times the ring went round
     for (int tile_no = 0; at.w < at.end; ++tile_no) {
+      bool all = true;
 #pragma unroll
       for (int i = 0; i < kLook; ++i) {
         const bool ok = page[i] >= 0 && page[i] < a.cache.pages;
         if (!ok && place[i] >= 0 && a.status) atomicOr(a.status, kDataPageRange);
         const uint32_t valid = __ballot_sync(0xffffffffu, ok);
-        if (lane == 0) sh.valid[tile_no & 7][i * (kLoad / 32) + warp - 4] = valid;
-        sh.off[tile_no & 1][i * kLoad + lt] =
-            ok ? page[i] * a.cache.page_stride + place[i] * a.cache.token_stride + head * (D * 2) : -1ll;
+        const int word = i * (kLoad / 32) + warp - kSoft / 32;
+        if (word < 4) {
+          if (lane == 0) sh.valid[tile_no & 7][word] = valid;
+          sh.off[tile_no & 1][i * kLoad + lt] =
+              ok ? page[i] * a.cache.page_stride + place[i] * a.cache.token_stride + head * (D * 2) : -1ll;
+        }
       }
       load_sync();
       const bool last = !more;
       if (more) look_up();
+      const uint32_t* valid = sh.valid[tile_no & 7];
+      all = (valid[0] & valid[1] & valid[2] & valid[3]) == 0xffffffffu;
       const long long* off = sh.off[tile_no & 1] + r0;
 #pragma unroll 1
       for (int x = 0; x < 2; ++x) {
         if (turn > 0) wait(&sh.empty[slot], (turn + 1) & 1);
         const char* pool = (x ? a.cache.v : a.cache.k) + chunk * 16;
-        const uint32_t dst = smem_addr(smem) + slot * L::kSlot + (chunk >> 3) * kHalf + r0 * 128;
-#pragma unroll 1
-        for (int i0 = 0; i0 < kRows; i0 += 8) {
-          long long from[8];  // read ahead of the copies, which no load passes
+        const uint32_t dst = smem_addr(smem) + slot * L::kSlot;
+        if (lt < kStep * kChunks) {
+          // (offsets are read ahead of the copies, which no load passes)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) from[i] = off[(i0 + i) * kStep];
+          for (int i0 = 0; i0 < kRows; i0 += 8) {
+            long long from[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int r = (i0 + i) * kStep;
-            cp16(dst + r * 128 + (((chunk & 7) ^ ((r0 + r) & 7)) << 4), pool + (from[i] < 0 ? 0 : from[i]),
-                 from[i] < 0 ? 0 : 16);
+            for (int i = 0; i < 8; ++i)
+              if (i0 + i < kRows && ((i0 + i + 1) * kStep <= kTile || r0 + (i0 + i) * kStep < kTile))
+                from[i] = off[(i0 + i) * kStep];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (i0 + i < kRows && ((i0 + i + 1) * kStep <= kTile || r0 + (i0 + i) * kStep < kTile)) {
+                const uint32_t to = dst + place_of[i & 3] + (i0 + i) * (kStep * 128);
+                if (all) cp16(to, pool + from[i], 16);
+                else cp16(to, pool + (from[i] < 0 ? 0 : from[i]), from[i] < 0 ? 0 : 16);
+              }
           }
         }
         cp_arrive(&sh.full[slot]);
@@ -303,7 +320,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) attention_tc_kernel(const AttnAr
       if (last) break;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");  // no copy is under way when the block leaves
-  } else if (warp == 6) {
+  } else if (warp == 11) {
     // ---- the products ------------------------------------------------------
     {
       const uint32_t ring = smem_addr(smem), q_at = smem_addr(q_s), p_at = smem_addr(p_s);
@@ -338,7 +355,9 @@ __global__ void __launch_bounds__(kThreadsT, 1) attention_tc_kernel(const AttnAr
       int v_idx = 0;
       while (at.next()) {
         for (int tile = at.tile0; tile < at.tile1; ++tile, ++v_idx) {
-          if (more) scores();
+          // the next item's queries come after this item's last weights
+          const bool next_item = ahead_tile == ahead.tile0;
+          if (more && !next_item) scores();
           const int slot = (2 * v_idx + 1) % kSlots;
           wait(&sh.full[slot], ((2 * v_idx + 1) / kSlots) & 1);
           wait(&sh.p_full, v_idx & 1);
@@ -354,13 +373,16 @@ __global__ void __launch_bounds__(kThreadsT, 1) attention_tc_kernel(const AttnAr
                      tile > at.tile0 || part > 0 || ks > 0);
           tc_commit(&sh.empty[slot]);
           tc_commit(&sh.p_free);
+          if (more && next_item) scores();
         }
       }
     }
     __syncwarp();
   } else {
-    // ---- softmax, one token a thread ------------------------------------------
-    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;  // this warp's TMEM lanes
+    // ---- softmax: one token and half of the rows a thread ----------------------
+    constexpr int kHalfN = N / 2;
+    const int group = warp >> 2, quad = warp & 3, token = tid & (kTile - 1), row_a = group * kHalfN;
+    const uint32_t lanes = (static_cast<uint32_t>(quad * 32) << 16) + row_a;  // this warp's TMEM lanes, its group's columns
     const uint32_t s_col[2] = {tmem + lanes, tmem + N + lanes}, o_col = tmem + 2 * N + lanes;
     const int G = a.Hq / a.cache.heads;
     auto load_q = [&](const Walk<N>& x) {
@@ -369,10 +391,8 @@ __global__ void __launch_bounds__(kThreadsT, 1) attention_tc_kernel(const AttnAr
         sh.q_off[r] = x.b * a.q_batch + ar.i * a.q_token + ar.hq * a.q_head;
       }
       soft_sync();
-      constexpr int kPieces = N * kChunks / kSoft;  // a thread's: 2 to 12
-#pragma unroll 4
-      for (int k = 0; k < kPieces; ++k) {
-        const int e = k * kSoft + tid, r = e / kChunks, c = e % kChunks;
+      for (int e = tid; e < N * kChunks; e += kSoft) {
+        const int r = e / kChunks, c = e % kChunks;
         uint4 v = __ldg(reinterpret_cast<const uint4*>(a.q + sh.q_off[r] + c * 16));
         if (r >= x.rows) v = make_uint4(0, 0, 0, 0);
         *reinterpret_cast<uint4*>(q_s + (c >> 3) * (N * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
@@ -389,17 +409,17 @@ __global__ void __launch_bounds__(kThreadsT, 1) attention_tc_kernel(const AttnAr
         sh.m[r] = -INFINITY;
         sh.limit[r] = at.n - a.Q + min(at.row0 + r, at.R - 1) / G;
       }
-      if (tid == 0) sh.n_odd = 0;
-      float l[N];
+      if (tid == 0) sh.odd = 0;
+      float l[kHalfN];
 #pragma unroll
-      for (int r = 0; r < N; ++r) l[r] = 0.f;
+      for (int r = 0; r < kHalfN; ++r) l[r] = 0.f;
       soft_sync();
       for (int tile = at.tile0; tile < at.tile1; ++tile, ++tile_no) {
-        const int buf = tile_no & 1, t = tile * kTile + tid;
+        const int buf = tile_no & 1, t = tile * kTile + token;
         wait(&sh.s_full[buf], (tile_no >> 1) & 1);
         tc_after();
         const uint32_t* valid = sh.valid[tile_no & 7];
-        const bool exists = (valid[warp] >> lane) & 1;
+        const bool exists = (valid[quad] >> lane) & 1;
         // a tile whose tokens all exist and are seen by every row needs no mask
         const bool masked =
             tile * kTile + kTile - 1 > at.n - a.Q || (valid[0] & valid[1] & valid[2] & valid[3]) != 0xffffffffu;
@@ -409,28 +429,29 @@ __global__ void __launch_bounds__(kThreadsT, 1) attention_tc_kernel(const AttnAr
         };
         bool grow = false;
 #pragma unroll
-        for (int c = 0; c < N; c += 16) {
-          float s[16];
-          tmem_ld16(s, s_col[buf] + c);
+        for (int c = 0; c < kHalfN; c += 8) {
+          float s[8];
+          tmem_ld8(s, s_col[buf] + c);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) grow |= score(s[i], c + i) > sh.m[c + i] + kSlackT;
+          for (int i = 0; i < 8; ++i) grow |= score(s[i], row_a + c + i) > sh.m[row_a + c + i] + kSlackT;
         }
-        if (soft_any(grow)) {
+        if (group_any(group, grow)) {
           // new reference maxima, and what has been summed so far by them
 #pragma unroll
-          for (int c = 0; c < N; c += 16) {
-            float s[16];
-            tmem_ld16(s, s_col[buf] + c);
+          for (int c = 0; c < kHalfN; c += 8) {
+            float s[8];
+            tmem_ld8(s, s_col[buf] + c);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              float x = score(s[i], c + i);
+            for (int i = 0; i < 8; ++i) {
+              float x = score(s[i], row_a + c + i);
 #pragma unroll
               for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-              if (lane == i) sh.wmax[warp][c + i] = x;
+              if (lane == i) sh.wmax[quad][row_a + c + i] = x;
             }
           }
-          soft_sync();
-          for (int r = tid; r < N; r += kSoft) {
+          group_sync(group);
+          if (token < kHalfN) {
+            const int r = row_a + token;
             const float old = sh.m[r];
             float m = old;
 #pragma unroll
@@ -438,19 +459,19 @@ __global__ void __launch_bounds__(kThreadsT, 1) attention_tc_kernel(const AttnAr
             sh.m[r] = m;
             sh.corr[r] = old == -INFINITY ? 0.f : ex2(old - m);
           }
-          soft_sync();
-#pragma unroll
-          for (int r = 0; r < N; ++r) l[r] *= sh.corr[r];
+          group_sync(group);
           if (tile > at.tile0) {
+#pragma unroll
+            for (int r = 0; r < kHalfN; ++r) l[r] *= sh.corr[row_a + r];
             wait(&sh.p_free, (tile_no - 1) & 1);  // O^T is complete
             tc_after();
 #pragma unroll
-            for (int c = 0; c < N; c += 16) {
-              float o[16];
-              tmem_ld16(o, o_col + c);
+            for (int c = 0; c < kHalfN; c += 8) {
+              float o[8];
+              tmem_ld8(o, o_col + c);
 #pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] *= sh.corr[c + i];
-              tmem_st16(o_col + c, o);
+              for (int i = 0; i < 8; ++i) o[i] *= sh.corr[row_a + c + i];
+              tmem_st8(o_col + c, o);
             }
             tmem_st_done();
           }
@@ -458,16 +479,17 @@ __global__ void __launch_bounds__(kThreadsT, 1) attention_tc_kernel(const AttnAr
         if (tile_no > 0) wait(&sh.p_free, (tile_no - 1) & 1);  // P^T has been read
         // A value that is not finite would reach rows that do not see its token
         // as 0 * inf: such values are zero in the product, and added to the
-        // rows that see them at the end.
-        uint32_t odd = 0;
-        if (masked && t > at.n - a.Q) {  // (tokens that do not exist are zero-filled)
+        // rows that see them at the end.  (Tokens that do not exist are
+        // zero-filled.)
+        if (masked && group == 0 && t > at.n - a.Q) {
           const int slot = (2 * tile_no + 1) % kSlots;
           wait(&sh.full[slot], ((2 * tile_no + 1) / kSlots) & 1);
-          uint4* v = reinterpret_cast<uint4*>(smem + slot * L::kSlot + tid * 128);
+          uint4* v = reinterpret_cast<uint4*>(smem + slot * L::kSlot + token * 128);
+          uint32_t odd = 0;
 #pragma unroll 4
           for (int c = 0; c < kChunks; ++c) {
-            uint4* piece = v + (c >> 3) * (kHalf / 16) + ((c ^ tid) & 7);  // (in an order without bank conflicts)
-            uint4 x = *piece;
+            uint4* piece = v + (c >> 3) * (kHalf / 16) + ((c ^ token) & 7);  // (in an order without bank conflicts)
+            const uint4 x = *piece;
             uint32_t u[4] = {x.x, x.y, x.z, x.w}, bad = 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -479,42 +501,28 @@ __global__ void __launch_bounds__(kThreadsT, 1) attention_tc_kernel(const AttnAr
             if (bad) *piece = make_uint4(u[0], u[1], u[2], u[3]);
             odd |= bad;
           }
+          if (odd) sh.odd = 1;
         }
-        uint32_t seen[(N + 31) / 32];
 #pragma unroll
-        for (int i = 0; i < (N + 31) / 32; ++i) seen[i] = 0;
+        for (int c = 0; c < kHalfN; c += 8) {
+          float s[8];
+          tmem_ld8(s, s_col[buf] + c);
+          uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int c = 0; c < N; c += 16) {
-          float s[16];
-          tmem_ld16(s, s_col[buf] + c);
-          uint32_t hi[8], lo[8];
-#pragma unroll
-          for (int i = 0; i < 16; i += 2) {
+          for (int i = 0; i < 8; i += 2) {
             float p[2];
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
-              const float m = sh.m[c + i + y];
-              p[y] = ex2(score(s[i + y], c + i + y) - (m == -INFINITY ? 0.f : m));
+              const float m = sh.m[row_a + c + i + y];
+              p[y] = ex2(score(s[i + y], row_a + c + i + y) - (m == -INFINITY ? 0.f : m));
               l[c + i + y] += p[y];
-              if (p[y] != 0.f) seen[(c + i + y) >> 5] |= 1u << ((c + i + y) & 31);
             }
             hi[i / 2] = pack2(p[0], p[1]);
             lo[i / 2] = pack2(p[0] - bf16_lo(hi[i / 2]), p[1] - bf16_hi(hi[i / 2]));
           }
-#pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            char* to = p_s + (c / 8 + g) * (kTile * 16) + tid * 16;
-            *reinterpret_cast<uint4*>(to) = make_uint4(hi[4 * g], hi[4 * g + 1], hi[4 * g + 2], hi[4 * g + 3]);
-            *reinterpret_cast<uint4*>(to + L::kP) = make_uint4(lo[4 * g], lo[4 * g + 1], lo[4 * g + 2], lo[4 * g + 3]);
-          }
-        }
-        if (odd) {
-          const int i = atomicAdd(&sh.n_odd, 1);
-          if (i < kTile) {
-            sh.odd_token[i] = t;
-#pragma unroll
-            for (int x = 0; x < (N + 31) / 32; ++x) sh.odd_rows[i][x] = seen[x];
-          }
+          char* to = p_s + (row_a + c) / 8 * (kTile * 16) + token * 16;
+          *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(to + L::kP) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
         async_fence();
         tc_before();
@@ -525,18 +533,24 @@ __global__ void __launch_bounds__(kThreadsT, 1) attention_tc_kernel(const AttnAr
       if (ahead.next()) load_q(ahead);  // its last scores are done: s_full has come
       // sums over the tokens: a butterfly that halves the rows with the lanes
 #pragma unroll
-      for (int c = 0; c < N; c += 32) {
-        float v[32];
+      for (int c = 0; c < kHalfN; c += 32) {
+        constexpr int kMost = kHalfN < 32 ? (kHalfN < 16 ? 8 : (kHalfN <= 16 ? 16 : 32)) : 32;
+        float v[kMost];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = c + i < N ? l[c + i < N ? c + i : 0] : 0.f;
+        for (int i = 0; i < kMost; ++i) v[i] = c + i < kHalfN ? l[c + i < kHalfN ? c + i : 0] : 0.f;
+        // lanes beyond kMost rows: plain sums first
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
+        for (int o = 16; o >= kMost; o >>= 1)
+#pragma unroll
+          for (int i = 0; i < kMost; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+#pragma unroll
+        for (int o = kMost / 2; o > 0; o >>= 1)
 #pragma unroll
           for (int i = 0; i < o; ++i) {
             const float give = (lane & o) ? v[i] : v[i + o], keep = (lane & o) ? v[i + o] : v[i];
             v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
           }
-        if (c + lane < N) sh.lsum[warp][c + lane] = v[0];
+        if (lane < kMost && c + lane < kHalfN) sh.lsum[quad][row_a + c + lane] = v[0];
       }
       wait(&sh.p_free, (tile_no - 1) & 1);
       tc_after();
@@ -558,28 +572,28 @@ __global__ void __launch_bounds__(kThreadsT, 1) attention_tc_kernel(const AttnAr
       }
       // O^T through shared memory (P^T's place), a row's D values together
       float* o_s = reinterpret_cast<float*>(p_s);
-      const int d = tid;  // D 64: lanes 64.. hold the same again
-      const int n_odd = min(sh.n_odd, kTile);
+      const int d = token;  // D 64: lanes 64.. hold the same again
+      const bool odd = sh.odd;
 #pragma unroll 1
-      for (int c = 0; c < N; c += 16) {
-        float o[16];
-        tmem_ld16(o, o_col + c);
-        if (n_odd > 0 && d < D) {
-          for (int k = 0; k < n_odd; ++k) {
-            const int t = sh.odd_token[k];
+      for (int c = 0; c < kHalfN; c += 8) {
+        float o[8];
+        tmem_ld8(o, o_col + c);
+        if (odd && d < D) {
+          for (int t = max(at.tile0 * kTile, at.n - a.Q + 1); t < min(at.tile1 * kTile, at.n); ++t) {
             const int entry = static_cast<int>(by_page(static_cast<unsigned long long>(t)));
             const int page = a.table.ids[at.b * a.table.stride + entry];
+            if (page < 0 || page >= a.cache.pages) continue;
             const float v = load_one<BF16>(a.cache.v + page * a.cache.page_stride +
                                                (t - entry * a.cache.page_size) * a.cache.token_stride + at.h * (D * 2), d);
             if (!isfinite(v))
 #pragma unroll
-              for (int i = 0; i < 16; ++i)
-                if ((sh.odd_rows[k][(c + i) >> 5] >> ((c + i) & 31)) & 1) o[i] += v;
+              for (int i = 0; i < 8; ++i)
+                if (t <= sh.limit[row_a + c + i]) o[i] += v;
           }
         }
         if (d < D)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) o_s[(c + i) * D + d] = o[i];
+          for (int i = 0; i < 8; ++i) o_s[(row_a + c + i) * D + d] = o[i];
       }
       soft_sync();
       for (int e = tid; e < at.rows * (D / 4); e += kSoft) {
@@ -610,7 +624,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) attention_tc_kernel(const AttnAr
   }
   tc_before();
   __syncthreads();
-  if (warp == 6) {
+  if (warp == 11) {
     tc_after();
     tmem_free(tmem, L::kCols);
   }

@@ -4,8 +4,8 @@
 namespace specv {
 
 cudaError_t attention_tc_prepare_64() {
-  cudaError_t e[] = {tc::prepare<64, 16>(), tc::prepare<64, 32>(), tc::prepare<64, 48>(),
-                     tc::prepare<64, 64>(), tc::prepare<64, 80>(), tc::prepare<64, 96>()};
+  cudaError_t e[] = {tc::prepare<64, 32>(), tc::prepare<64, 48>(), tc::prepare<64, 64>(), tc::prepare<64, 80>(),
+                     tc::prepare<64, 96>()};
   for (cudaError_t x : e)
     if (x != cudaSuccess) return x;
   return cudaSuccess;
@@ -13,7 +13,6 @@ cudaError_t attention_tc_prepare_64() {
 
 void attention_tc_launch_64(const AttnArgs& a, int n16, int grid, cudaStream_t stream) {
   switch (n16) {
-    case 1: tc::launch<64, 16>(a, grid, stream); break;
     case 2: tc::launch<64, 32>(a, grid, stream); break;
     case 3: tc::launch<64, 48>(a, grid, stream); break;
     case 4: tc::launch<64, 64>(a, grid, stream); break;
