@@ -9,13 +9,20 @@
 
 namespace specv {
 
-// Rows a cache head (R = Q * Hq / Hkv) choose the bf16 kernel: up to 24 go to
-// attention_mma.cuh, more to attention_tc.cuh.  At 64 sequences of 400..4000
-// tokens, Hq 32, Hkv 8, D 128 (floor 94 to 96 us) the two took
-//   R = 4: 109 and 147 us;  16: 126 and 147;  24: 140 and 178;
-//   R = 32: 235 and 180;    68: 360 and 302
-// (a fourth block of 8 rows leaves mma without registers; its K and V come
-// through L2 once more a block of rows), with D 64 and R = 24: 100 and 149.
+// bf16 items of more than 24 rows a cache head (R = Q * Hq / Hkv) over heads of
+// 128 go to attention_tc.cuh when the tables have room for kTcTokens tokens
+// times cache heads, the rest to attention_mma.cuh, in tiles of at most 24
+// rows that each read K and V again (through L2).  Measured, mma and tc:
+//   64 sequences of 400..4000 tokens, 8 cache heads, R = 24: 143 and 178 us;
+//     R = 32: 225 and 181;  R = 68: 375 and 303
+//   34 of 7406..9512 tokens, 4 cache heads, R = 72: 261 and 205
+//   19 of about 1300 tokens, 4 cache heads, R = 36: 44 and 49
+//   24 of 141..525 tokens, 1 cache head, R = 48: 27 and 39
+// (an item's start and end cost tc some 10 us, mma 4), and with heads of 64
+// mma was ahead at every size: 83 sequences of 188..808 tokens, 8 cache heads,
+// R = 48: 90 and 108; 16 of 2400 tokens, R = 85: 33 and 58.
+constexpr int64_t kTcTokens = 300000;
+
 size_t attention_workspace(int D, bool bf16) {
   const size_t rows = bf16 ? kMaxRowsTc : mma::kMmaRows;
   return (static_cast<size_t>(kAttnMaxCtas) * 4 + mma::kMaxMmaCtas * 2 * rows * (D + 2) * 4 + 255) &
@@ -23,8 +30,7 @@ size_t attention_workspace(int D, bool bf16) {
 }
 
 cudaError_t attention_prepare() {
-  cudaError_t e[] = {mma::prepare_all<BF16>(), mma::prepare_all<F32>(), attention_tc_prepare_64(),
-                     attention_tc_prepare_128()};
+  cudaError_t e[] = {mma::prepare_all<BF16>(), mma::prepare_all<F32>(), attention_tc_prepare()};
   for (cudaError_t x : e)
     if (x != cudaSuccess) return x;
   return cudaSuccess;
@@ -32,20 +38,17 @@ cudaError_t attention_prepare() {
 
 cudaError_t launch_attention(const AttnArgs& a, int sm_count, cudaStream_t stream) {
   const int R = a.Q * (a.Hq / a.cache.heads);
+  const bool tc = a.cache.bf16 && a.cache.head_dim == 128 && R > mma::kMmaRows &&
+                  static_cast<int64_t>(a.B) * a.table.max_pages * a.cache.page_size * a.cache.heads >= kTcTokens;
   // rows in tiles of equal size
-  const bool few = !a.cache.bf16 || R <= mma::kMmaRows;
-  const int most = few ? mma::kMmaRows : kMaxRowsTc;
+  const int most = tc ? kMaxRowsTc : mma::kMmaRows;
   const int tiles = (R + most - 1) / most, rows = (R + tiles - 1) / tiles;
-  if (!a.cache.bf16) {
-    mma::launch_rows<F32>(a, (rows + 7) / 8, sm_count, stream);
-  } else if (few) {
+  if (tc)  // tiles of 32 rows at least, a multiple of 16
+    attention_tc_launch(a, (rows + 15) / 16, sm_count < mma::kMaxMmaCtas ? sm_count : mma::kMaxMmaCtas, stream);
+  else if (a.cache.bf16)
     mma::launch_rows<BF16>(a, (rows + 7) / 8, sm_count, stream);
-  } else {
-    const int n16 = (rows + 15) / 16;  // 2 to 6
-    const int grid = sm_count < mma::kMaxMmaCtas ? sm_count : mma::kMaxMmaCtas;
-    if (a.cache.head_dim == 128) attention_tc_launch_128(a, n16, grid, stream);
-    else attention_tc_launch_64(a, n16, grid, stream);
-  }
+  else
+    mma::launch_rows<F32>(a, (rows + 7) / 8, sm_count, stream);
   return cudaGetLastError();
 }
 

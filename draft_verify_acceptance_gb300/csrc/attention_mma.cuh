@@ -38,21 +38,19 @@ namespace mma {
 
 constexpr int kMaxMmaCtas = 304;             // blocks of a launch
 constexpr int kMmaRows = 24;                 // rows of an item, at most
-constexpr int kWarpsM = 4;
-constexpr int kThreadsM = kWarpsM * 32;
 constexpr int kTokens = 16;                  // a warp's step
-constexpr int kStepM = kWarpsM * kTokens;    // a block's step
 constexpr float kSlack = 8.f;                // how far (log2) a score may pass the reference
 
 template <typename E, int D, int NB>
 struct Ring {
   static constexpr bool kF32 = E::kBytes == 4;
-  static constexpr int kStages = kF32 || D == 128 ? 3 : 6;
+  static constexpr int kWarps = kF32 && D == 128 ? 6 : 4;
+  static constexpr int kStages = kF32 ? (D == 128 ? 2 : 3) : (D == 128 ? 3 : 6);
   static constexpr int kCtas = kF32 && D == 128 ? 1 : 2;  // an SM holds
   static constexpr int kRow = D * E::kBytes;             // bytes of a token's K or V
   static constexpr int kHalf = kTokens * kRow;           // K of a step; V follows
   static constexpr int kStage = 2 * kHalf;
-  static constexpr int kRing = kWarpsM * kStages * kStage;
+  static constexpr int kRing = kWarps * kStages * kStage;
   // fp32 queries, split, as operand fragments: [NB][D / 16][hi, lo][32 lanes][16 bytes]
   static constexpr int kQueries = kF32 ? NB * (D / 16) * 1024 : 0;
   static constexpr int kBytes = kRing + kQueries;
@@ -169,9 +167,10 @@ __device__ __forceinline__ uint32_t even_word(uint32_t w) {
 
 // NB blocks of 8 rows an item.
 template <typename E, int D, int NB>
-__global__ void __launch_bounds__(kThreadsM, Ring<E, D, NB>::kCtas) attention_mma_kernel(const AttnArgs a, DivU64 by_page) {
+__global__ void __launch_bounds__(Ring<E, D, NB>::kWarps * 32, Ring<E, D, NB>::kCtas) attention_mma_kernel(const AttnArgs a, DivU64 by_page) {
   using L = Ring<E, D, NB>;
   constexpr bool kF32 = L::kF32;
+  constexpr int kWarpsM = L::kWarps, kThreadsM = kWarpsM * 32, kStepM = kWarpsM * kTokens;  // a block's step
   constexpr int kRows = 8 * NB, KS = D / 16, kStages = L::kStages;
   constexpr int kRow = L::kRow, kHalf = L::kHalf, kStage = L::kStage;
   constexpr int kChunks = kRow / 16;           // 16-byte pieces of a row
@@ -609,7 +608,7 @@ cudaError_t prepare() {
 template <typename E, int D, int NB>
 void launch(const AttnArgs& a, int sm_count, cudaStream_t stream) {
   const int grid = sm_count * Ring<E, D, NB>::kCtas < kMaxMmaCtas ? sm_count * Ring<E, D, NB>::kCtas : kMaxMmaCtas;
-  attention_mma_kernel<E, D, NB><<<grid, kThreadsM, Ring<E, D, NB>::kBytes, stream>>>(
+  attention_mma_kernel<E, D, NB><<<grid, Ring<E, D, NB>::kWarps * 32, Ring<E, D, NB>::kBytes, stream>>>(
       a, DivU64::make(static_cast<unsigned long long>(a.cache.page_size)));
 }
 template <typename E>

@@ -36,19 +36,20 @@ using mma::cp16;
 using mma::nonfinite2;
 using mma::pack2;
 
+constexpr int D = 128;                   // of a head
 constexpr int kTile = 128;               // tokens
 constexpr int kSoft = 256;               // softmax threads: two groups of four warps
 constexpr int kLoad = 96;                // loader threads
 constexpr int kThreadsT = kSoft + kLoad + 32;
 constexpr float kSlackT = 8.f;
 
-template <int D, int N>
+template <int N>
 struct Lay {
   static constexpr int kSlot = kTile * D * 2;   // K or V of a tile
   static constexpr int kQ = N * D * 2;
   static constexpr int kP = kTile * N * 2;      // one part of P^T
   static constexpr int kFree = 216 * 1024 - kQ - 2 * kP;  // (about 9 KB more are static)
-  static constexpr int kSlots = kFree / kSlot < 8 ? kFree / kSlot : 8;
+  static constexpr int kSlots = kFree / kSlot;
   static constexpr int kBytes = kSlots * kSlot + kQ + 2 * kP + 1024;  // 1024: alignment
   static constexpr int kCols = 3 * N <= 64 ? 64 : 3 * N <= 128 ? 128 : 3 * N <= 256 ? 256 : 512;
   static_assert(kSlots >= 4, "two tiles");
@@ -170,9 +171,9 @@ struct Walk {
   __device__ __forceinline__ long long first() const { return base + static_cast<long long>(item) * tiles; }
 };
 
-template <int D, int N>
+template <int N>
 struct SharedT {
-  unsigned long long full[Lay<D, N>::kSlots], empty[Lay<D, N>::kSlots];
+  unsigned long long full[Lay<N>::kSlots], empty[Lay<N>::kSlots];
   unsigned long long s_full[2], s_free[2], p_full, p_free, q_full;
   long long off[2][kTile];             // byte offsets of a tile's tokens, -1: none
   uint32_t valid[8][4];                // tokens that exist, by tile
@@ -188,13 +189,13 @@ struct SharedT {
   long long plan[2 * (kThreadsT / 32) + 4];
 };
 
-template <int D, int N>
+template <int N>
 __global__ void __launch_bounds__(kThreadsT, 1) attention_tc_kernel(const AttnArgs a, DivU64 by_page) {
-  using L = Lay<D, N>;
-  constexpr int kSlots = L::kSlots, kHalves = D / 64, kHalf = kTile * 128;
+  using L = Lay<N>;
+  constexpr int kSlots = L::kSlots, kHalf = kTile * 128;
   constexpr int kChunks = D / 8;  // 16-byte pieces of a token
   extern __shared__ char raw_smem[];
-  __shared__ SharedT<D, N> sh;
+  __shared__ SharedT<N> sh;
   char* smem = raw_smem + ((1024 - (smem_addr(raw_smem) & 1023)) & 1023);
   char* q_s = smem + kSlots * L::kSlot;  // [halves][N][128 bytes]
   char* p_s = q_s + L::kQ;               // [hi, lo][N / 8][128 tokens][16 bytes]
@@ -260,7 +261,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) attention_tc_kernel(const AttnAr
     };
     if (more) look_up();
     // where the thread's piece of row r0 + i * kStep lies in the swizzled slot:
-    // the rows' low three bits go round every four (or two) steps
+    // the rows' low three bits go round every four steps
     uint32_t place_of[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -368,7 +369,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) attention_tc_kernel(const AttnAr
           for (int part = 0; part < 2; ++part)
 #pragma unroll
             for (int ks = 0; ks < kTile / 16; ++ks)
-              tc_mma(o_col, operand(v_at + ks * 2048, kHalves == 2 ? kHalf : 0, 1024, 2),
+              tc_mma(o_col, operand(v_at + ks * 2048, kHalf, 1024, 2),
                      operand(p_at + part * L::kP + ks * 256, 128, 2048, 0), instruction<N>(true, true),
                      tile > at.tile0 || part > 0 || ks > 0);
           tc_commit(&sh.empty[slot]);
@@ -572,13 +573,13 @@ __global__ void __launch_bounds__(kThreadsT, 1) attention_tc_kernel(const AttnAr
       }
       // O^T through shared memory (P^T's place), a row's D values together
       float* o_s = reinterpret_cast<float*>(p_s);
-      const int d = token;  // D 64: lanes 64.. hold the same again
+      const int d = token;
       const bool odd = sh.odd;
 #pragma unroll 1
       for (int c = 0; c < kHalfN; c += 8) {
         float o[8];
         tmem_ld8(o, o_col + c);
-        if (odd && d < D) {
+        if (odd) {
           for (int t = max(at.tile0 * kTile, at.n - a.Q + 1); t < min(at.tile1 * kTile, at.n); ++t) {
             const int entry = static_cast<int>(by_page(static_cast<unsigned long long>(t)));
             const int page = a.table.ids[at.b * a.table.stride + entry];
@@ -591,7 +592,6 @@ __global__ void __launch_bounds__(kThreadsT, 1) attention_tc_kernel(const AttnAr
                 if (t <= sh.limit[row_a + c + i]) o[i] += v;
           }
         }
-        if (d < D)
 #pragma unroll
           for (int i = 0; i < 8; ++i) o_s[(row_a + c + i) * D + d] = o[i];
       }
@@ -630,13 +630,13 @@ __global__ void __launch_bounds__(kThreadsT, 1) attention_tc_kernel(const AttnAr
   }
 }
 
-template <int D, int N>
+template <int N>
 cudaError_t prepare() {
-  return cudaFuncSetAttribute(attention_tc_kernel<D, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D, N>::kBytes);
+  return cudaFuncSetAttribute(attention_tc_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<N>::kBytes);
 }
-template <int D, int N>
+template <int N>
 void launch(const AttnArgs& a, int grid, cudaStream_t stream) {
-  attention_tc_kernel<D, N><<<grid, kThreadsT, Lay<D, N>::kBytes, stream>>>(
+  attention_tc_kernel<N><<<grid, kThreadsT, Lay<N>::kBytes, stream>>>(
       a, DivU64::make(static_cast<unsigned long long>(a.cache.page_size)));
 }
 

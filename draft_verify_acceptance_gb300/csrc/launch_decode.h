@@ -74,10 +74,8 @@ size_t attention_workspace(int D, bool bf16);
 cudaError_t attention_prepare();
 // tcgen05 attention (attention_tc.cuh): tiles of 16 * n16 rows, at most kMaxRowsTc.
 constexpr int kMaxRowsTc = 96;
-cudaError_t attention_tc_prepare_64();
-cudaError_t attention_tc_prepare_128();
-void attention_tc_launch_64(const AttnArgs& a, int n16, int grid, cudaStream_t stream);
-void attention_tc_launch_128(const AttnArgs& a, int n16, int grid, cudaStream_t stream);
+cudaError_t attention_tc_prepare();
+void attention_tc_launch(const AttnArgs& a, int n16, int grid, cudaStream_t stream);
 cudaError_t launch_attention(const AttnArgs& a, int sm_count, cudaStream_t stream);
 
 cudaError_t launch_append(const char* k_new, const char* v_new, long long new_stride, int T,

@@ -9,6 +9,7 @@ within 2^-21 of the exponential each and two roundings: 2^-19 relative for p abo
 whose whole-number weights are rounded by 2^-22 at most.
 """
 import math
+import sys
 
 import numpy as np
 import pytest
@@ -147,6 +148,45 @@ def test_attention_unseen_tokens_do_not_matter(decode, dtype, Q, G, D):
     q1 = q.abs()
     o, l = decode.paged_attention(q1, k2, v, table, lengths, return_lse=True)
     assert torch.isfinite(o).all() and torch.isfinite(l[1]).all()
+
+
+@pytest.fixture
+def roomy_tables(monkeypatch):
+    """Page tables with room for many tokens, which with many rows a cache head are read by another kernel."""
+    plain = make_cache
+    monkeypatch.setattr(sys.modules[__name__], "make_cache",
+                        lambda lens, S, H, D, *args, **kw: plain(lens, S, H, D, *args, **kw,
+                                                                 extra_cols=300000 // (len(lens) * S * H) + 1))
+
+
+@pytest.mark.parametrize("B,Q,Hq,H,S,lens", [
+    (3, 13, 6, 3, 5, [3, 13, 77]),                   # 26 rows; queries before the sequence's start see nothing
+    (2, 5, 7, 1, 16, [0, 128]),                      # 35 rows, an empty sequence
+    (4, 3, 32, 2, 48, [127, 128, 129, 385]),         # 48 rows, ends around a tile's
+    (2, 9, 32, 4, 16, [2000, 31]),                   # 72 rows
+    (1, 1, 96, 1, 64, [6001]),                       # 96 rows, one sequence cut over many blocks
+    (2, 17, 16, 2, 8, [17, 513]),                    # 136 rows
+    (40, 6, 8, 1, 1, list(range(1, 41))),
+    (30, 10, 4, 1, 16, [300 * (i % 7) + 1 for i in range(30)]),
+])
+def test_attention_many_rows(decode, roomy_tables, B, Q, Hq, H, S, lens):
+    test_attention(decode, torch.bfloat16, B, Q, Hq, H, 128, S, lens)
+
+
+@pytest.mark.parametrize("Q,G", [(4, 8), (9, 8), (17, 6)])
+def test_attention_many_rows_unseen_tokens(decode, roomy_tables, Q, G):
+    test_attention_unseen_tokens_do_not_matter(decode, torch.bfloat16, Q, G, 128)
+
+
+def test_attention_many_rows_repeats(decode, roomy_tables):
+    """Repeated calls, and calls on a workspace that others have used, give the same bits."""
+    for lens, Q, Hq, H, S in (([5000, 40], 4, 32, 4, 16), ([300] * 50, 9, 8, 2, 32)):
+        k, v, table, lengths = make_cache(lens, S, H, 128, torch.bfloat16, seed=7)
+        q = torch.randn((len(lens), Q, Hq, 128), generator=gen(8), device="cuda").to(torch.bfloat16)
+        first = decode.paged_attention(q, k, v, table, lengths, return_lse=True)
+        for _ in range(20):
+            again = decode.paged_attention(q, k, v, table, lengths, return_lse=True)
+            assert all(torch.equal(x, y) for x, y in zip(again, first))
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
