@@ -66,8 +66,10 @@ typedef struct {
  *            every call leaves it fit for the next.  One call at a time.
  *
  * Scores, softmax and sums are fp32 (bf16: products of bf16 pairs summed in
- * fp32; a weight exp(...) multiplies v as the sum of two bf16 values), and
- * the output is rounded once.
+ * fp32; a weight exp(...) multiplies v as the sum of two bf16 values; fp32:
+ * operands enter products as two parts of 11 bits, which leaves out 2^-22 of
+ * a term), and the output is rounded once.  A value that is not finite in a
+ * token that a query sees makes what it reaches not finite (infinite or NaN).
  * The result does not depend on the schedule's timing: partial results are
  * joined in a fixed order.
  */
