@@ -28,10 +28,12 @@
 //   whole   a cluster does all of a row's work at once.  It takes the rows that
 //           the first two queue -- those whose kept set does not lie in the
 //           list (flat distributions), by bins over the slices, and the rare
-//           ones between the bounds, by the exact sum -- and every row of a
+//           ones between the bounds (its own sums are exact) -- and every row of a
 //           call whose clusters all fit the GPU at once, where latency counts
 //           and there is no next row to overlap.
-//   write   the filtered rows, streaming.
+//   write   filtered rows that take the logits' place, streaming.  (Others are
+//           filled with -inf by the list kernel, on its way, and finish adds
+//           what is kept.)
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -843,6 +845,27 @@ __device__ __forceinline__ void write_kept(const SampleArgs& a, int row, int fir
   }
 }
 
+// -inf over `n` elements of the filtered row from `first` on, by one warp: bulk
+// copies from a block of them in shared memory, and single elements at ends
+// that are not on 16 bytes.  They are under way when it returns.
+constexpr int kBlank = 64;  // vectors
+template <typename E>
+__device__ __forceinline__ void fill_masked(const SampleArgs& a, int row, int first, int n, const uint4* blank, int lane) {
+  using raw = typename E::raw;
+  n = min(n, a.V - first);
+  raw* to = static_cast<raw*>(a.filtered) + static_cast<size_t>(row) * a.V + first;
+  const int lead = min(n, static_cast<int>(-reinterpret_cast<uintptr_t>(to) & 15u) / E::kBytes);
+  const int bytes = (n - lead) * E::kBytes & ~15, done = lead + bytes / E::kBytes;
+  if (lane < lead) to[lane] = masked_value<E>();
+  if (lane < n - done) to[done + lane] = masked_value<E>();
+  char* at = reinterpret_cast<char*>(to + lead);
+  for (int b = lane * kBlank * 16; b < bytes; b += 32 * kBlank * 16)
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(at + b), "r"(smem_addr(blank)),
+                 "r"(min(bytes - b, kBlank * 16))
+                 : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
 // A row on its way between the kernels.
 struct __align__(16) RowHead {
   float M, from;                 // largest logit, smallest listed one
@@ -869,51 +892,15 @@ __device__ __forceinline__ unsigned long long share_of(float top_p, unsigned lon
   return max(1ull, draw_threshold(fminf(fmaxf(top_p, 0.f), 0.99999994f), total));
 }
 
-// Exact sum of a row's weights by one block, from global memory.
-template <typename E, int NT>
-__device__ __noinline__ unsigned long long row_total(const typename E::raw* logits, int V, float M, float s,
-                                                     float mz, Shared& sh) {
-  constexpr int VEC = Staged<E>::kVec;
-  const bool vectors = reinterpret_cast<uintptr_t>(logits) % 16 == 0;
-  Slice<E, false> sl;
-  sl.first = 0;
-  sl.V = V;
-  sl.global = logits;
-  const int nvec = (V + VEC - 1) / VEC;
-  unsigned long long t = 0, u;
-  for (int v0 = threadIdx.x; v0 < nvec; v0 += 8 * NT) {
-    uint4 w[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int v = v0 + i * NT;
-      if (v < nvec) w[i] = vectors && (v + 1) * VEC <= V ? ld_stream_v4(logits + v * VEC) : sl.at(v);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (v0 + i * NT < nvec) {
-        Sum z;
-        float2 x[VEC / 2];
-        unpack_pairs<E>(w[i], x);
-#pragma unroll
-        for (int k = 0; k < VEC / 2; ++k) add_pair(z, x[k], M, s, mz);
-        t += value_of(z, VEC);
-      }
-    }
-  }
-  block_sum2<NT>(t, 0, sh, &t, &u);
-  return t;
-}
-
 // The cuts and the draw of a covered row on its list by NT threads.  Writes
-// the row's outputs; returns the largest kept key (without kExact: ~0 when the
-// row needs its exact sum).  Three passes over the
-// list: weights by bins of the logit's bits (top-p); sums of what lies above
+// the row's outputs; returns the largest kept key (~0 when the row needs
+// its exact sum).  Three passes over the list: weights by bins of the logit's bits (top-p); sums of what lies above
 // the crossing bin, by bins of the index; the crossing bin of the draw.  A
 // bin of more than 32 candidates (ties) goes through list_crossing.
-template <typename E, int NT, bool kExact>
+template <typename E, int NT>
 __device__ unsigned long long finish_row(const Ctx& c, const SampleArgs& a, const Settings& set,
                                          unsigned long long least, float u, int row, const uint4* list,
-                                         const RowHead& head, float s, float mz) {
+                                         const RowHead& head, float s) {
   const bool has_k = set.k < a.V, has_m = set.min_p > 0.f, has_p = set.top_p < 1.f, whole = !has_k && !has_m;
   const int n = head.listed, tid = threadIdx.x;
   const unsigned int f0 = value_key<E>(head.M);
@@ -927,98 +914,91 @@ __device__ unsigned long long finish_row(const Ctx& c, const SampleArgs& a, cons
   };
   if (has_k && set.k < n)
     cut = list_crossing<NT, true>(c, list, n, klo, khi, set.k - 1, key_of<E>, [](const uint4&) { return 1ull; });
-  unsigned long long total = head.Z, slack = whole ? head.slack : 0;
+  const unsigned long long slack = whole ? head.slack : 0;
+  unsigned long long total = head.Z;
   if (has_p && !whole) {
     unsigned long long t = 0, k;
     for (int i = tid; i < n; i += NT) t += kept(list[i]);
     block_sum2<NT>(t, 0, *c.sh, &total, &k);
   }
   unsigned long long S, count;
-  const unsigned long long base = cut;
-  for (;;) {
-    // ---- top-p: the crossing bin ----
-    cut = base;
-    int bin = 256;  // kept for sure: bins below
-    unsigned long long rem = 0;
-    if (has_p) {
-      rem = share_of(set.top_p, total - slack) - 1;
-      meet<NT>();
-      c.clear<NT, 2>();
-      meet<NT>();
-#pragma unroll 4
-      for (int i = tid; i < n; i += NT) {
-        const uint4 e = list[i];
-        if (kept(e)) {
-          const unsigned int at = min(255u, (value_key<E>(__uint_as_float(e.x)) - f0) >> fshift);
-          atomicAdd(&c.bins->part[0][at], e.z);
-          atomicAdd(&c.bins->part[1][at], e.w);
-          atomicAdd(&c.bins->count[at], 1u);
-        }
-      }
-      meet<NT>();
-      if (NT == 32 || tid < 32)
-        crossing_bin(c, rem, [&](int b) { return bin_value<2>(c.bins, b); }, c.bins->count);
-      meet<NT>();
-      bin = c.sh->sel[0];
-      rem = c.sh->rem;
-      if (c.sh->bin_count > 32) {
-        const unsigned long long lo = static_cast<unsigned long long>(f0 + (static_cast<unsigned int>(bin) << fshift)) << 22;
-        cut = list_crossing<NT, false>(c, list, n, lo, lo + (1ull << (fshift + 22)) - 1, rem, key_of<E>, kept);
-        bin = 256;
-      }
-    }
-    // ---- what is kept, by bins of the index ----
+  // ---- top-p: the crossing bin ----
+  int bin = 256;  // kept for sure: bins below
+  unsigned long long rem = 0;
+  if (has_p) {
+    rem = share_of(set.top_p, total - slack) - 1;
     meet<NT>();
-    for (int i = tid; i < 256; i += NT) by_index->count[i] = by_index->part[0][i] = by_index->part[1][i] = 0;
-    if (tid == 0) c.sh->n_few = 0;
+    c.clear<NT, 2>();
     meet<NT>();
-    unsigned long long t = 0;
-    unsigned int k = 0;
-    auto add = [&](unsigned int j, unsigned int lo, unsigned int hi) {
-      const unsigned int at = j >> jshift;
-      atomicAdd(&by_index->part[0][at], lo);
-      atomicAdd(&by_index->part[1][at], hi);
-      atomicAdd(&by_index->count[at], 1u);
-      t += (static_cast<unsigned long long>(hi) << 20) + lo;
-      ++k;
-    };
 #pragma unroll 4
     for (int i = tid; i < n; i += NT) {
       const uint4 e = list[i];
-      if (!kept(e)) continue;
-      const int at = static_cast<int>(min(255u, (value_key<E>(__uint_as_float(e.x)) - f0) >> fshift));
-      if (at < bin) {
-        add(e.y, e.z, e.w);
-      } else if (at == bin) {
-        const unsigned int f = atomicAdd(&c.sh->n_few, 1u);
-        if (f < 32) {
-          c.sh->few_key[f] = key_of<E>(e);
-          c.sh->few_w[f] = weight_of(e);
-        }
+      if (kept(e)) {
+        const unsigned int at = min(255u, (value_key<E>(__uint_as_float(e.x)) - f0) >> fshift);
+        atomicAdd(&c.bins->part[0][at], e.z);
+        atomicAdd(&c.bins->part[1][at], e.w);
+        atomicAdd(&c.bins->count[at], 1u);
       }
     }
-    if (bin < 256) {
-      meet<NT>();
-      if (NT == 32 || tid < 32) {
-        const int few = min(32u, c.sh->n_few);
-        const unsigned long long key = crossing_of_few(c.sh->few_key, c.sh->few_w, few, rem);
-        if (tid < few && c.sh->few_key[tid] <= key)
-          add(static_cast<unsigned int>(c.sh->few_key[tid]) & 0x3fffffu,
-              static_cast<unsigned int>(c.sh->few_w[tid]) & 0xfffffu, static_cast<unsigned int>(c.sh->few_w[tid] >> 20));
-        if (tid == 0) c.sh->lo = key;
-      }
-      meet<NT>();
-      cut = c.sh->lo;
+    meet<NT>();
+    if (NT == 32 || tid < 32)
+      crossing_bin(c, rem, [&](int b) { return bin_value<2>(c.bins, b); }, c.bins->count);
+    meet<NT>();
+    bin = c.sh->sel[0];
+    rem = c.sh->rem;
+    if (c.sh->bin_count > 32) {
+      const unsigned long long lo = static_cast<unsigned long long>(f0 + (static_cast<unsigned int>(bin) << fshift)) << 22;
+      cut = list_crossing<NT, false>(c, list, n, lo, lo + (1ull << (fshift + 22)) - 1, rem, key_of<E>, kept);
+      bin = 256;
     }
-    block_sum2<NT>(t, k, *c.sh, &S, &count);
-    // the kept mass reaches the smallest share that the approximate sum
-    // allows; if it reaches the largest, the cut is the exact sum's
-    if (!has_p || slack == 0 || S >= share_of(set.top_p, total + slack)) break;
-    if (!kExact) return ~0ull;  // between the bounds: for the whole-row kernel
-    total = row_total<E, NT>(static_cast<const typename E::raw*>(a.logits) + row * a.row_stride, a.V, head.M, s, mz,
-                             *c.sh);
-    slack = 0;
   }
+  // ---- what is kept, by bins of the index ----
+  meet<NT>();
+  for (int i = tid; i < 256; i += NT) by_index->count[i] = by_index->part[0][i] = by_index->part[1][i] = 0;
+  if (tid == 0) c.sh->n_few = 0;
+  meet<NT>();
+  unsigned long long t = 0;
+  unsigned int k = 0;
+  auto add = [&](unsigned int j, unsigned int lo, unsigned int hi) {
+    const unsigned int at = j >> jshift;
+    atomicAdd(&by_index->part[0][at], lo);
+    atomicAdd(&by_index->part[1][at], hi);
+    atomicAdd(&by_index->count[at], 1u);
+    t += (static_cast<unsigned long long>(hi) << 20) + lo;
+    ++k;
+  };
+#pragma unroll 4
+  for (int i = tid; i < n; i += NT) {
+    const uint4 e = list[i];
+    if (!kept(e)) continue;
+    const int at = static_cast<int>(min(255u, (value_key<E>(__uint_as_float(e.x)) - f0) >> fshift));
+    if (at < bin) {
+      add(e.y, e.z, e.w);
+    } else if (at == bin) {
+      const unsigned int f = atomicAdd(&c.sh->n_few, 1u);
+      if (f < 32) {
+        c.sh->few_key[f] = key_of<E>(e);
+        c.sh->few_w[f] = weight_of(e);
+      }
+    }
+  }
+  if (bin < 256) {
+    meet<NT>();
+    if (NT == 32 || tid < 32) {
+      const int few = min(32u, c.sh->n_few);
+      const unsigned long long key = crossing_of_few(c.sh->few_key, c.sh->few_w, few, rem);
+      if (tid < few && c.sh->few_key[tid] <= key)
+        add(static_cast<unsigned int>(c.sh->few_key[tid]) & 0x3fffffu,
+            static_cast<unsigned int>(c.sh->few_w[tid]) & 0xfffffu, static_cast<unsigned int>(c.sh->few_w[tid] >> 20));
+      if (tid == 0) c.sh->lo = key;
+    }
+    meet<NT>();
+    cut = c.sh->lo;
+  }
+  block_sum2<NT>(t, k, *c.sh, &S, &count);
+  // the kept mass reaches the smallest share that the approximate sum
+  // allows; if it does not reach the largest, the whole-row kernel takes the row
+  if (has_p && slack != 0 && S < share_of(set.top_p, total + slack)) return ~0ull;
   // ---- the draw ----
   const unsigned long long theta = draw_threshold(u, S);
   meet<NT>();
@@ -1086,8 +1066,8 @@ __device__ unsigned long long finish_row(const Ctx& c, const SampleArgs& a, cons
 // whole-row kernel (clusters take rows of the queue, or row i without one).
 template <typename E, bool kStaged, bool kWhole>
 __global__ void __launch_bounds__(kThreadsS, 3)
-filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_in, bool aligned_out, RowHead* heads,
-                  uint4* lists, int most, Queue* queue, int* queued, float mz) {
+filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_in, bool aligned_out, bool fill,
+                  RowHead* heads, uint4* lists, int most, Queue* queue, int* queued, float mz) {
   constexpr int VEC = Staged<E>::kVec;
   constexpr int kPerWord = 32 / VEC, kWords = kStaged ? (kVectorsS + kPerWord - 1) / kPerWord : 1;
   using raw = typename E::raw;
@@ -1095,6 +1075,7 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
   __shared__ Shared sh;
   __shared__ Exchange ex;
   __shared__ __align__(8) unsigned long long bars[kMaxChunksS];
+  __shared__ uint4 blank[kWhole ? 1 : kBlank];
   cg::cluster_group cluster = cg::this_cluster();
   Ctx c;
   c.sh = &sh;
@@ -1120,6 +1101,11 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
   if (bulk && tid == 0) {
     for (int k = 0; k < nch; ++k) mbar_init(&bars[k], 1);
     fence_barrier_init();
+  }
+  if (!kWhole && tid < kBlank) {
+    const uint32_t inf = E::kBytes == 2 ? 0xff80ff80u : 0xff800000u;
+    blank[tid] = make_uint4(inf, inf, inf, inf);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // bulk copies read it
   }
   const int clusters = static_cast<int>(gridDim.x >> lgC);
   int at = static_cast<int>(blockIdx.x >> lgC), stop_at = at + 1;
@@ -1165,6 +1151,9 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
     __syncthreads();
     const Settings set = sh.set;
     const float u = sh.u, s = sh.s;
+    const bool has_k = set.k < a.V, has_m = set.min_p > 0.f, has_p = set.top_p < 1.f;
+    const bool cuts = has_k || has_m || has_p, whole = !has_k && !has_m;  // whole: top-p of the whole row's mass
+    if (!kWhole && fill && cuts && warp == 1) fill_masked<E>(a, row, sl.first, sl.nv * VEC, blank, lane);
     if (c.C > 1) cluster_arrive_relaxed();  // matched before the first store to another block
 
     // ---- the row's maximum and the list's threshold ------------------------
@@ -1222,8 +1211,6 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
     Kept kept;
     kept.cut = ~0ull;
     kept.least = sh.least;
-    const bool has_k = set.k < a.V, has_m = set.min_p > 0.f, has_p = set.top_p < 1.f;
-    const bool cuts = has_k || has_m || has_p, whole = !has_k && !has_m;  // whole: top-p of the whole row's mass
     RowHead head;
     head.M = M;
     head.from = M;
@@ -1246,6 +1233,7 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
       const AtLeast<E> test(from);
       uint32_t hits[kWords];
       float z = 0.f, z_low = 0.f;
+      unsigned long long exact = 0;  // (kWhole)
       int n = 0;
 #pragma unroll
       for (int i = 0; i < kWords; ++i) {
@@ -1257,8 +1245,16 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
             const int v = (i * kPerWord + k) * kThreadsS + tid;
             if (v < sl.nv) {
               uint4 w = slice[v];
+              if (kWhole && whole) {
+                Sum x;
+                float2 pair[VEC / 2];
+                unpack_pairs<E>(w, pair);
+#pragma unroll
+                for (int p = 0; p < VEC / 2; ++p) add_pair(x, pair[p], M, s, mz);
+                exact += value_of(x, VEC);
+              }
               hits[i] |= test.bits(w) << (k * VEC);
-              if (whole) zi += vector_mass<E>(w, M, s, mz);
+              if (!kWhole && whole) zi += vector_mass<E>(w, M, s, mz);
             }
           }
           // z + z_low is the sum without a further rounding
@@ -1304,7 +1300,8 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
         to[before + i] = make_entry(x, static_cast<unsigned int>(sl.first + e), w);
       }
       if (whole)
-        block_sum2<kThreadsS>(__float2ull_rn(z * kScale) + static_cast<long long>(z_low * kScale), ls, sh, &zs, &ls);
+        block_sum2<kThreadsS>(
+            kWhole ? exact : __float2ull_rn(z * kScale) + static_cast<long long>(z_low * kScale), ls, sh, &zs, &ls);
       if (tid < c.C) {
         *c.at(&ex.sum[c.rank], tid) = zs;
         *c.at(&ex.listed_sum[c.rank], tid) = ls;
@@ -1323,8 +1320,8 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
       // does the list hold all that can be kept?  (more than `most`, or a
       // block's kPlaces, did not fit, and the sums then mean nothing)
       head.from = from;
-      head.slack = sum_slack(U, a.V);
-      head.Z = L + U;
+      head.slack = kWhole ? 0 : sum_slack(U, a.V);
+      head.Z = kWhole ? U : L + U;  // (the exact sum has the listed ones in it)
       if (total <= most && !crowded &&
           (complete || (has_k ? total >= set.k : !has_m && L >= share_of(set.top_p, head.Z + head.slack))))
         head.listed = total;
@@ -1332,7 +1329,7 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
     }
     if (kWhole && head.listed >= 0) {
       if (c.rank == 0) {
-        kept.cut = finish_row<E, kThreadsS, true>(c, a, set, kept.least, u, row, list, head, s, mz);
+        kept.cut = finish_row<E, kThreadsS>(c, a, set, kept.least, u, row, list, head, s);
         if (a.filtered && tid < c.C) *c.at(&sh.cut, tid) = kept.cut;
       }
       if (a.filtered) {
@@ -1400,14 +1397,15 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
     }
 
     if (!good) kept.cut = 0;
-    if (kWhole) {
+    if (kWhole || (fill && !cuts)) {
       if (a.filtered) {
         const float bound = good ? logit_of<E>(kept.cut) : INFINITY;
         for (int v = tid; v < sl.nv; v += kThreadsS)
           write_kept<E>(a, row, sl.first, v, sl.at(v), aligned_out && sl.first + (v + 1) * VEC <= a.V, kept, bound, M, s);
       }
-      c.sync();  // this row's memory is free
-    } else if (c.rank == 0 && tid == 0) {
+      if (kWhole) c.sync();  // this row's memory is free
+    }
+    if (!kWhole && c.rank == 0 && tid == 0) {
       if (later) queued[atomicAdd(&queue->n, 1u)] = row;
       head.cut = kept.cut;
       head.written = later;
@@ -1422,12 +1420,14 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
       if (bad && a.status) atomicOr(a.status, bad);
     }
   }
+  if (!kWhole && fill && warp == 1) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 // One block per listed row, the list in shared memory.
 template <typename E>
-__global__ void __launch_bounds__(kThreadsB, 8) filter_finish_kernel(const SampleArgs a, int row0, RowHead* heads,
-                                                                     const uint4* lists, Queue* queue, int* queued) {
+__global__ void __launch_bounds__(kThreadsB, 8) filter_finish_kernel(const SampleArgs a, int row0, bool fill,
+                                                                     RowHead* heads, const uint4* lists,
+                                                                     Queue* queue, int* queued) {
   __shared__ Shared sh;
   __shared__ ListBins bins[2];
   __shared__ uint4 list[kList];
@@ -1449,7 +1449,17 @@ __global__ void __launch_bounds__(kThreadsB, 8) filter_finish_kernel(const Sampl
 #pragma unroll 4
   for (int i = threadIdx.x; i < head.listed; i += kThreadsB) list[i] = from[i];
   const unsigned long long cut =
-      finish_row<E, kThreadsB, false>(c, a, set, least, u, row, list, head, s, -0.f);
+      finish_row<E, kThreadsB>(c, a, set, least, u, row, list, head, s);
+  if (fill && cut != ~0ull) {  // the row is -inf so far
+    typename E::raw* out = static_cast<typename E::raw*>(a.filtered) + static_cast<size_t>(row) * a.V;
+    for (int i = threadIdx.x; i < head.listed; i += kThreadsB) {
+      const uint4 e = list[i];
+      if (key_of<E>(e) <= cut && weight_of(e) >= least) {
+        if constexpr (E::kBytes == 2) out[e.y] = static_cast<uint16_t>(e.x >> 16);
+        else out[e.y] = __uint_as_float(e.x);
+      }
+    }
+  }
   if (threadIdx.x == 0) {
     if (cut == ~0ull) {
       queued[atomicAdd(&queue->n, 1u)] = row;
@@ -1556,12 +1566,18 @@ cudaError_t launch(const SampleArgs& a, const Shape& s, const Space& sp, cudaStr
   cfg.stream = stream;
   cfg.attrs = attr;
   Queue* none = nullptr;
+  // A filtered row apart from the logits is filled with -inf while they are
+  // read, and what is kept added by whoever cuts; one in their place is
+  // written after they have been read (filter_write_kernel).
+  const char *from = static_cast<const char*>(a.logits), *to = static_cast<const char*>(a.filtered);
+  const bool apart = a.filtered && (to + static_cast<size_t>(a.R) * a.V * E::kBytes <= from ||
+                                    from + (static_cast<size_t>(a.R - 1) * a.row_stride + a.V) * E::kBytes <= to);
   if (!s.split) {
     cfg.gridDim = dim3(static_cast<unsigned int>(a.R) * s.C);
     cfg.blockDim = dim3(kThreadsS);
     cfg.dynamicSmemBytes = static_cast<size_t>(s.nvs) * 16 + kPlaceBytes + kListBytes;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, filter_row_kernel<E, kStaged, true>, a, 0, s.nvec, s.nvs, in, out, sp.heads, sp.lists,
+    return cudaLaunchKernelEx(&cfg, filter_row_kernel<E, kStaged, true>, a, 0, s.nvec, s.nvs, in, out, false, sp.heads, sp.lists,
                               kList, none, sp.queued, -0.f);
   }
   if constexpr (kStaged) {
@@ -1578,14 +1594,14 @@ cudaError_t launch(const SampleArgs& a, const Shape& s, const Space& sp, cudaStr
       cfg.numAttrs = 1;
       attr[0].val.clusterDim.x = s.C;
       cudaError_t e = cudaLaunchKernelEx(&cfg, filter_row_kernel<E, true, false>, a, row0, s.nvec, s.nvs, in, out,
-                                         sp.heads, sp.lists, kList, sp.queue, sp.queued, -0.f);
+                                         apart, sp.heads, sp.lists, kList, sp.queue, sp.queued, -0.f);
       if (e != cudaSuccess) return e;
       // the next ones start early and wait for what they read
       cfg.gridDim = dim3(static_cast<unsigned int>(rows));
       cfg.blockDim = dim3(kThreadsB);
       cfg.dynamicSmemBytes = 0;
       cfg.attrs = attr + 1;
-      e = cudaLaunchKernelEx(&cfg, filter_finish_kernel<E>, a, row0, sp.heads, static_cast<const uint4*>(sp.lists),
+      e = cudaLaunchKernelEx(&cfg, filter_finish_kernel<E>, a, row0, apart, sp.heads, static_cast<const uint4*>(sp.lists),
                              sp.queue, sp.queued);
       if (e != cudaSuccess) return e;
       const int clusters = rows < kFusedBlocks / Cq ? rows : kFusedBlocks / Cq;
@@ -1595,10 +1611,10 @@ cudaError_t launch(const SampleArgs& a, const Shape& s, const Space& sp, cudaStr
       cfg.attrs = attr;
       cfg.numAttrs = 2;
       attr[0].val.clusterDim.x = Cq;
-      e = cudaLaunchKernelEx(&cfg, filter_row_kernel<E, true, true>, a, row0, s.nvec, nvq, in, out, sp.heads, sp.lists,
+      e = cudaLaunchKernelEx(&cfg, filter_row_kernel<E, true, true>, a, row0, s.nvec, nvq, in, out, false, sp.heads, sp.lists,
                              kLongList, sp.queue, sp.queued, -0.f);
       if (e != cudaSuccess) return e;
-      if (a.filtered) {
+      if (a.filtered && !apart) {
         cfg.gridDim = dim3(static_cast<unsigned int>(rows), (s.nvec + 256 * kWriteVecs - 1) / (256 * kWriteVecs));
         cfg.blockDim = dim3(256);
         cfg.dynamicSmemBytes = 0;

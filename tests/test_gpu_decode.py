@@ -537,6 +537,33 @@ def test_sample_sorted_rows_and_many_rows(decode):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [3, 701, 5000, 40009])
+def test_sample_filtered_rows_of_a_batch(decode, dtype, V):
+    """Batches that several kernels share: filtered rows apart from the logits (rows on and off 16 bytes), in their
+    place, flat rows and rows that are refused among them."""
+    R = 330
+    x = (torch.randn((R, V), generator=gen(V), device="cuda") * 3).to(dtype)
+    x[5::50] *= 0.1
+    u = torch.rand(R, generator=gen(V + 1), device="cuda")
+    settings = [MIX[i % len(MIX)] for i in range(R)]
+    want = check_sample(decode, x, u, settings)
+    x[7, V // 2], x[8, V - 1], x[9] = math.nan, math.inf, -math.inf
+    T, k, p, m = (list(c) for c in zip(*settings))
+    f = lambda c: torch.tensor(c, dtype=torch.float32, device="cuda")  # noqa: E731
+    kw = dict(temperature=f(T), top_k=i32(k), top_p=f(p), min_p=f(m), debug=True)
+    good = torch.ones(R, dtype=torch.bool, device="cuda")
+    good[7:10] = False
+    apart = decode.filtered_sample(x, u, out=torch.full_like(x, 5.0), **kw)
+    place = x.clone()
+    inside = decode.filtered_sample(place, u, out=place, **kw)
+    for r in (apart, inside):
+        assert int(r.status) == 2  # SPEC_DATA_NONFINITE_LOGIT
+        for a, b in zip(r[:4], want[:4]):
+            assert torch.equal(a[good], b[good])
+        assert (r.filtered[~good] == -math.inf).all() and (r.n_kept[~good] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("V", [1000, 32000, 40000, 128256, 500003])
 def test_sample_sums_are_the_definition_s(decode, dtype, V):
     """p is fp32(w) / fp32(S) of the whole-number weights to the bit, so a sum that is off by little shows; the
