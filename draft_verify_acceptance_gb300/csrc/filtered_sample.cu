@@ -296,6 +296,17 @@ struct AtLeast<F32> {
     w = make_uint4(u[0], u[1], u[2], u[3]);
     return t;
   }
+  // the other way round: -inf in place of the others; and the test alone
+  __device__ __forceinline__ uint32_t keep(uint4& w) const {
+    const uint32_t t = which(w);
+    w = make_uint4(t & 1 ? w.x : 0xff800000u, t & 2 ? w.y : 0xff800000u, t & 4 ? w.z : 0xff800000u,
+                   t & 8 ? w.w : 0xff800000u);
+    return t;
+  }
+  __device__ __forceinline__ uint32_t which(const uint4& w) const {
+    return (__uint_as_float(w.x) >= from ? 1u : 0u) | (__uint_as_float(w.y) >= from ? 2u : 0u) |
+           (__uint_as_float(w.z) >= from ? 4u : 0u) | (__uint_as_float(w.w) >= from ? 8u : 0u);
+  }
   static __device__ __forceinline__ int place(int bit) { return bit; }
 };
 template <>
@@ -306,14 +317,32 @@ struct AtLeast<BF16> {
     uint32_t u[4] = {w.x, w.y, w.z, w.w}, t = 0;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      __nv_bfloat162 x;
-      memcpy(&x, &u[k], 4);
-      const uint32_t m = __hge2_mask(x, from);
+      const uint32_t m = mask(u[k]);
       t |= m & (0x00010001u << k);
       u[k] = (u[k] & ~m) | (m & 0xff80ff80u);
     }
     w = make_uint4(u[0], u[1], u[2], u[3]);
     return (t | (t >> 12)) & 0xffu;
+  }
+  __device__ __forceinline__ uint32_t keep(uint4& w) const {
+    uint32_t u[4] = {w.x, w.y, w.z, w.w}, t = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t m = mask(u[k]);
+      t |= m & (0x00010001u << k);
+      u[k] = (u[k] & m) | (~m & 0xff80ff80u);
+    }
+    w = make_uint4(u[0], u[1], u[2], u[3]);
+    return t;
+  }
+  __device__ __forceinline__ uint32_t which(const uint4& w) const {
+    return (mask(w.x) & 0x00010001u) | (mask(w.y) & 0x00020002u) | (mask(w.z) & 0x00040004u) |
+           (mask(w.w) & 0x00080008u);
+  }
+  __device__ __forceinline__ uint32_t mask(uint32_t u) const {
+    __nv_bfloat162 x;
+    memcpy(&x, &u, 4);
+    return __hge2_mask(x, from);
   }
   static __device__ __forceinline__ int place(int bit) { return ((bit & 3) << 1) | (bit >> 2); }
 };
@@ -817,53 +846,64 @@ __device__ __forceinline__ int tau_lane(const Settings& set, int V, int C, int m
   return min(31, max(0, static_cast<int>(32.f * below)));
 }
 
-// A vector of the filtered row.  Most elements fail the comparison with the
-// cut's logit; the others are tested exactly.
+// Below the first logit every weight is 0, from the second up 1 or more: a
+// weight is 1 from 2^-41 of the largest up, and t, the polynomial and these
+// logits are off by less than 1e-4 and |M| 2^-22.
+__device__ __forceinline__ float zero_logit(float M, float s) { return M - __fdiv_rn(41.001f, s) - fabsf(M) * 2.4e-7f; }
+__device__ __forceinline__ float sure_logit(float M, float s) {
+  return fmaxf(M - __fdiv_rn(40.999f, s) + fabsf(M) * 2.4e-7f, -FLT_MAX);
+}
+
+// A vector of the filtered row.  Nearly every element is below `edge` and not
+// kept, or from `sure` (NaN: none) up and kept; the others are tested exactly.
 template <typename E>
 __device__ __forceinline__ void write_kept(const SampleArgs& a, int row, int first, int v, const uint4& w,
-                                           bool vectors, const Kept& kept, float edge, float M, float s) {
+                                           bool vectors, const Kept& kept, float edge, float sure, float M, float s) {
   constexpr int VEC = Staged<E>::kVec;
   using raw = typename E::raw;
-  raw x[VEC];
-  memcpy(x, &w, 16);
+  uint4 o = w;
+  AtLeast<E> above(edge), certain(sure);
+  const uint32_t some = above.keep(o);
+  if (some != certain.which(w)) {
+    raw x[VEC];
+    memcpy(x, &w, 16);
 #pragma unroll
-  for (int k = 0; k < VEC; ++k) {
-    const float f = element<E>(w, k);
-    bool in = f >= edge;
-    if (in) in = cut_key<E>(f, first + v * VEC + k) <= kept.cut && weight(f, M, s) >= kept.least;
-    if (!in) x[k] = masked_value<E>();
+    for (int k = 0; k < VEC; ++k) {
+      const float f = element<E>(w, k);
+      bool in = f >= edge;
+      if (in && !(f >= sure)) in = cut_key<E>(f, first + v * VEC + k) <= kept.cut && weight(f, M, s) >= kept.least;
+      if (!in) x[k] = masked_value<E>();
+    }
+    memcpy(&o, x, 16);
   }
   raw* dst = static_cast<raw*>(a.filtered) + static_cast<size_t>(row) * a.V + first + v * VEC;
   if (vectors) {
-    uint4 o;
-    memcpy(&o, x, 16);
     *reinterpret_cast<uint4*>(dst) = o;
   } else {
+    raw x[VEC];
+    memcpy(x, &o, 16);
 #pragma unroll
     for (int k = 0; k < VEC; ++k)
       if (first + v * VEC + k < a.V) dst[k] = x[k];
   }
 }
 
-// -inf over `n` elements of the filtered row from `first` on, by one warp: bulk
-// copies from a block of them in shared memory, and single elements at ends
-// that are not on 16 bytes.  They are under way when it returns.
-constexpr int kBlank = 64;  // vectors
+// -inf over `n` elements of the filtered row from `first` on: 16-byte stores,
+// and single elements at ends that are not on 16 bytes.
 template <typename E>
-__device__ __forceinline__ void fill_masked(const SampleArgs& a, int row, int first, int n, const uint4* blank, int lane) {
+__device__ __forceinline__ void fill_masked(const SampleArgs& a, int row, int first, int n) {
   using raw = typename E::raw;
+  const int tid = threadIdx.x;
   n = min(n, a.V - first);
   raw* to = static_cast<raw*>(a.filtered) + static_cast<size_t>(row) * a.V + first;
   const int lead = min(n, static_cast<int>(-reinterpret_cast<uintptr_t>(to) & 15u) / E::kBytes);
-  const int bytes = (n - lead) * E::kBytes & ~15, done = lead + bytes / E::kBytes;
-  if (lane < lead) to[lane] = masked_value<E>();
-  if (lane < n - done) to[done + lane] = masked_value<E>();
-  char* at = reinterpret_cast<char*>(to + lead);
-  for (int b = lane * kBlank * 16; b < bytes; b += 32 * kBlank * 16)
-    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(at + b), "r"(smem_addr(blank)),
-                 "r"(min(bytes - b, kBlank * 16))
-                 : "memory");
-  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  const int vectors = (n - lead) * E::kBytes / 16, done = lead + vectors * (16 / E::kBytes);
+  if (tid < lead) to[tid] = masked_value<E>();
+  if (tid < n - done) to[done + tid] = masked_value<E>();
+  const uint32_t inf = E::kBytes == 2 ? 0xff80ff80u : 0xff800000u;
+  uint4* at = reinterpret_cast<uint4*>(to + lead);
+#pragma unroll 4
+  for (int v = tid; v < vectors; v += kThreadsS) __stcs(at + v, make_uint4(inf, inf, inf, inf));
 }
 
 // A row on its way between the kernels.
@@ -1075,7 +1115,6 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
   __shared__ Shared sh;
   __shared__ Exchange ex;
   __shared__ __align__(8) unsigned long long bars[kMaxChunksS];
-  __shared__ uint4 blank[kWhole ? 1 : kBlank];
   cg::cluster_group cluster = cg::this_cluster();
   Ctx c;
   c.sh = &sh;
@@ -1101,11 +1140,6 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
   if (bulk && tid == 0) {
     for (int k = 0; k < nch; ++k) mbar_init(&bars[k], 1);
     fence_barrier_init();
-  }
-  if (!kWhole && tid < kBlank) {
-    const uint32_t inf = E::kBytes == 2 ? 0xff80ff80u : 0xff800000u;
-    blank[tid] = make_uint4(inf, inf, inf, inf);
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // bulk copies read it
   }
   const int clusters = static_cast<int>(gridDim.x >> lgC);
   int at = static_cast<int>(blockIdx.x >> lgC), stop_at = at + 1;
@@ -1153,7 +1187,6 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
     const float u = sh.u, s = sh.s;
     const bool has_k = set.k < a.V, has_m = set.min_p > 0.f, has_p = set.top_p < 1.f;
     const bool cuts = has_k || has_m || has_p, whole = !has_k && !has_m;  // whole: top-p of the whole row's mass
-    if (!kWhole && fill && cuts && warp == 1) fill_masked<E>(a, row, sl.first, sl.nv * VEC, blank, lane);
     if (c.C > 1) cluster_arrive_relaxed();  // matched before the first store to another block
 
     // ---- the row's maximum and the list's threshold ------------------------
@@ -1225,7 +1258,7 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
       // below `floor` every weight is 0, below `least_x` under min-p's share
       // (with room for the roundings of t and of the polynomial, and for
       // shares near 2^-40 of the weight itself)
-      const float floor = M - __fdiv_rn(42.f, s);
+      const float floor = zero_logit(M, s);
       const float share = has_m ? __log2f(fminf(set.min_p, 1.f)) - (set.min_p < 1e-6f ? 2.f : 1e-4f) : -42.f;
       const float least_x = fmaxf(floor, M + __fdiv_rn(share, s) - fabsf(M) * 2.4e-7f);
       const bool complete = !(tau > least_x);
@@ -1399,12 +1432,16 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
     if (!good) kept.cut = 0;
     if (kWhole || (fill && !cuts)) {
       if (a.filtered) {
-        const float bound = good ? logit_of<E>(kept.cut) : INFINITY;
+        const float bound = good ? fmaxf(logit_of<E>(kept.cut), zero_logit(M, s)) : INFINITY;
+        const float sure = cuts || !good ? NAN : sure_logit(M, s);
         for (int v = tid; v < sl.nv; v += kThreadsS)
-          write_kept<E>(a, row, sl.first, v, sl.at(v), aligned_out && sl.first + (v + 1) * VEC <= a.V, kept, bound, M, s);
+          write_kept<E>(a, row, sl.first, v, sl.at(v), aligned_out && sl.first + (v + 1) * VEC <= a.V, kept, bound,
+                        sure, M, s);
       }
       if (kWhole) c.sync();  // this row's memory is free
     }
+    // (here, as a cluster's barrier waits for the stores before it)
+    if (!kWhole && fill && cuts) fill_masked<E>(a, row, sl.first, sl.nv * VEC);
     if (!kWhole && c.rank == 0 && tid == 0) {
       if (later) queued[atomicAdd(&queue->n, 1u)] = row;
       head.cut = kept.cut;
@@ -1420,7 +1457,6 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
       if (bad && a.status) atomicOr(a.status, bad);
     }
   }
-  if (!kWhole && fill && warp == 1) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 // One block per listed row, the list in shared memory.
@@ -1495,12 +1531,14 @@ __global__ void __launch_bounds__(256) filter_write_kernel(const SampleArgs a, i
   Kept kept;
   kept.cut = head.cut;
   kept.least = max(1ull, __float2ull_rn(__fmul_rn(fminf(fmaxf(set.min_p, 0.f), 1.f), kScale)));
-  const float edge = head.good ? logit_of<E>(kept.cut) : INFINITY;
+  const float edge = head.good ? fmaxf(logit_of<E>(kept.cut), zero_logit(head.M, s)) : INFINITY;
+  const bool cuts = set.k < a.V || set.min_p > 0.f || set.top_p < 1.f;
+  const float sure = cuts || !head.good ? NAN : sure_logit(head.M, s);
 #pragma unroll
   for (int i = 0; i < kWriteVecs; ++i) {
     const int v = (blockIdx.y * kWriteVecs + i) * 256 + threadIdx.x;
     if (v < nvec)
-      write_kept<E>(a, row, 0, v, w[i], aligned_out && (v + 1) * VEC <= a.V, kept, edge, head.M, s);
+      write_kept<E>(a, row, 0, v, w[i], aligned_out && (v + 1) * VEC <= a.V, kept, edge, sure, head.M, s);
   }
 }
 
