@@ -159,32 +159,70 @@ __device__ __forceinline__ bool attn_arrive(const AttnArgs& a, long long first, 
   return *flag != 0;
 }
 
-// Joins the parts of an item and writes its rows: thread by thread four
-// dimensions of a row, over the parts in CTA order.
+// Joins the parts of an item and writes its rows: a thread takes four
+// dimensions of up to kE rows and adds the parts in CTA order.  The parts come
+// from L2, some 600 cycles away, so the loads of kE rows and kC parts are under
+// way together (one by one a join of two parts of 24 rows took 7 us).
 template <int kRows, int D, int kThreadsA>
 __device__ void attn_join(const AttnArgs& a, int b, int h, int row0, int rows, long long first, int tiles,
                           long long per) {
+  constexpr int kEach = kRows * (D / 4) / kThreadsA, kE = kEach < 1 ? 1 : kEach < 3 ? kEach : 3, kC = 4;
   const long long c0 = first / per, c1 = (first + tiles - 1) / per;
   __threadfence();
-  for (int e = threadIdx.x; e < rows * (D / 4); e += kThreadsA) {
-    const int r = e / (D / 4), d = (e - r * (D / 4)) * 4;
-    float m = -INFINITY;
-    for (long long c = c0; c <= c1; ++c)
-      m = fmaxf(m, __ldcg(attn_slot<kRows, D>(a, c, c == c0) + kRows * D + r));
-    float l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (long long c = c0; c <= c1; ++c) {
-      const float* s = attn_slot<kRows, D>(a, c, c == c0);
-      const float mc = __ldcg(s + kRows * D + r);
-      const float w = mc == -INFINITY ? 0.f : ex2(mc - m);
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(s + r * D + d));
-      l = fmaf(w, __ldcg(s + kRows * D + kRows + r), l);
-      o.x = fmaf(w, v.x, o.x);
-      o.y = fmaf(w, v.y, o.y);
-      o.z = fmaf(w, v.z, o.z);
-      o.w = fmaf(w, v.w, o.w);
+  for (int e0 = threadIdx.x; e0 < rows * (D / 4); e0 += kE * kThreadsA) {
+    int r[kE], d[kE];
+    float m[kE], l[kE];
+    float4 o[kE];
+#pragma unroll
+    for (int i = 0; i < kE; ++i) {
+      const int e = min(e0 + i * kThreadsA, rows * (D / 4) - 1);
+      r[i] = e / (D / 4);
+      d[i] = (e - r[i] * (D / 4)) * 4;
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+      o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    attn_write<D>(a, b, h, row0 + r, d, m, l, o);
+    for (long long c = c0; c <= c1; c += kC) {
+      float mc[kC][kE];
+#pragma unroll
+      for (int y = 0; y < kC; ++y)
+#pragma unroll
+        for (int i = 0; i < kE; ++i)
+          mc[y][i] = __ldcg(attn_slot<kRows, D>(a, min(c + y, c1), min(c + y, c1) == c0) + kRows * D + r[i]);
+#pragma unroll
+      for (int y = 0; y < kC; ++y)
+#pragma unroll
+        for (int i = 0; i < kE; ++i) m[i] = fmaxf(m[i], mc[y][i]);
+    }
+    for (long long c = c0; c <= c1; c += kC) {
+      float mc[kC][kE], lc[kC][kE];
+      float4 v[kC][kE];
+#pragma unroll
+      for (int y = 0; y < kC; ++y) {
+        const float* s = attn_slot<kRows, D>(a, min(c + y, c1), min(c + y, c1) == c0);
+#pragma unroll
+        for (int i = 0; i < kE; ++i) {
+          mc[y][i] = c + y <= c1 ? __ldcg(s + kRows * D + r[i]) : -INFINITY;
+          lc[y][i] = __ldcg(s + kRows * D + kRows + r[i]);
+          v[y][i] = __ldcg(reinterpret_cast<const float4*>(s + r[i] * D + d[i]));
+        }
+      }
+#pragma unroll
+      for (int y = 0; y < kC; ++y)
+#pragma unroll
+        for (int i = 0; i < kE; ++i) {
+          if (mc[y][i] == -INFINITY) continue;
+          const float w = ex2(mc[y][i] - m[i]);
+          l[i] = fmaf(w, lc[y][i], l[i]);
+          o[i].x = fmaf(w, v[y][i].x, o[i].x);
+          o[i].y = fmaf(w, v[y][i].y, o[i].y);
+          o[i].z = fmaf(w, v[y][i].z, o[i].z);
+          o[i].w = fmaf(w, v[y][i].w, o[i].w);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kE; ++i)
+      if (e0 + i * kThreadsA < rows * (D / 4)) attn_write<D>(a, b, h, row0 + r[i], d[i], m[i], l[i], o[i]);
   }
 }
 
