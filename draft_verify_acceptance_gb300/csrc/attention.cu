@@ -10,18 +10,20 @@
 namespace specv {
 
 // bf16 items of more than 24 rows a cache head (R = Q * Hq / Hkv) over heads of
-// 128 go to attention_tc.cuh when the tables have room for kTcTokens tokens
-// times cache heads, the rest to attention_mma.cuh, in tiles of at most 24
-// rows that each read K and V again (through L2).  Measured, mma and tc:
-//   64 sequences of 400..4000 tokens, 8 cache heads, R = 24: 143 and 178 us;
-//     R = 32: 225 and 181;  R = 68: 375 and 303
-//   34 of 7406..9512 tokens, 4 cache heads, R = 72: 261 and 205
-//   19 of about 1300 tokens, 4 cache heads, R = 36: 44 and 49
-//   24 of 141..525 tokens, 1 cache head, R = 48: 27 and 39
+// 128 go to attention_tc.cuh when the tables have room for kTcTokens tokens a
+// sequence and kTcWork tokens times cache heads in all, the rest to
+// attention_mma.cuh, in tiles of at most 24 rows that each read K and V again
+// (through L2).  Measured, mma and tc:
+//   64 sequences of 400..4000 tokens, 8 cache heads, R = 24: 114 and 178 us;
+//     R = 32: 190 and 168;  R = 36: 204 and 202;  R = 68: 295 and 261
+//   34 of 7406..9512 tokens, 4 cache heads, R = 72: 256 and 201
+//   4 of 10000..20000 tokens, 8 cache heads, R = 32: 77 and 69
+//   64 of 1000 tokens, 8 cache heads, R = 32: 97 and 99
+//   32 of 500..1500 tokens, 8 cache heads, R = 68: 88 and 98
 // (an item's start and end cost tc some 10 us, mma 4), and with heads of 64
 // mma was ahead at every size: 83 sequences of 188..808 tokens, 8 cache heads,
-// R = 48: 90 and 108; 16 of 2400 tokens, R = 85: 33 and 58.
-constexpr int64_t kTcTokens = 300000;
+// R = 48: 67 and 108; 16 of 2400 tokens, R = 85: 28 and 58.
+constexpr int64_t kTcTokens = 2048, kTcWork = 300000;
 
 size_t attention_workspace(int D, bool bf16) {
   const size_t rows = bf16 ? kMaxRowsTc : mma::kMmaRows;
@@ -38,8 +40,9 @@ cudaError_t attention_prepare() {
 
 cudaError_t launch_attention(const AttnArgs& a, int sm_count, cudaStream_t stream) {
   const int R = a.Q * (a.Hq / a.cache.heads);
+  const int64_t room = static_cast<int64_t>(a.table.max_pages) * a.cache.page_size;
   const bool tc = a.cache.bf16 && a.cache.head_dim == 128 && R > mma::kMmaRows &&
-                  static_cast<int64_t>(a.B) * a.table.max_pages * a.cache.page_size * a.cache.heads >= kTcTokens;
+                  room >= kTcTokens && room * a.B * a.cache.heads >= kTcWork;
   // rows in tiles of equal size
   const int most = tc ? kMaxRowsTc : mma::kMmaRows;
   const int tiles = (R + most - 1) / most, rows = (R + tiles - 1) / tiles;

@@ -22,13 +22,20 @@
 // without loss), so most steps need no reduction across
 // lanes and no rescaling.
 //
+// Measured, bf16, heads of 128, 32 query heads on 8: one query on 64 sequences
+// of 4000 tokens 163 us (the cache's bytes at the copy rate: 157), on 64 of
+// 400..4000 101 (94), on 3 of 60001..131072 197 (190); six queries on the
+// ragged 64 114 (94): HBM is the bound until 24 rows' 72 products a step and
+// an item's end (some 4 us: the ring drains, the warps' parts meet) show.
+//
 // fp32 takes m16n8k8 on tf32 parts: x = hi + lo with hi = x rounded to 11 bits
 // and lo the rest, and a product as hi hi + hi lo + lo hi, each exact in fp32,
 // which leaves out 2^-22 of a term.  The tensor cores' sums are not rounded to
 // nearest, so no chain of them is long: a score's hi parts make two chains of
 // D / 16 and the rest a third, and a step's part of O^T starts from zero and
-// is added by an fp32 add.  (On the fp32 units a row of 24 took 930 us where
-// this takes F32SLOT; their bound is a multiply-add per row and element.)
+// is added by an fp32 add.  (On the fp32 units, with a multiply-add per row and
+// element, 32 sequences of 400..4000 tokens took 332 us for one query and 930
+// for six, where this takes 139 and 237.)
 #pragma once
 
 #include "attention_common.cuh"
@@ -47,6 +54,7 @@ struct Ring {
   static constexpr int kWarps = kF32 && D == 128 ? 6 : 4;
   static constexpr int kStages = kF32 ? (D == 128 ? 2 : 3) : (D == 128 ? 3 : 6);
   static constexpr int kCtas = kF32 && D == 128 ? 1 : 2;  // an SM holds
+  static constexpr int kEnd = kF32 ? NB + 1 : 2 * NB + 2;  // steps that an item's start and end count as
   static constexpr int kRow = D * E::kBytes;             // bytes of a token's K or V
   static constexpr int kHalf = kTokens * kRow;           // K of a step; V follows
   static constexpr int kStage = 2 * kHalf;
@@ -191,23 +199,11 @@ __global__ void __launch_bounds__(Ring<E, D, NB>::kWarps * 32, Ring<E, D, NB>::k
   char* mine = ring + warp * (kStages * kStage);
   const uint32_t mine_at = smem_addr(mine);
 
-  AttnPlan plan = attn_plan<kStepM, kThreadsM>(a, H * RT, 4, s_plan);
-  long long w = plan.per * blockIdx.x;
-  const long long end = min(plan.total, w + plan.per);
-  int b = plan.b;
-  long long base = plan.base;
-  while (w < end) {
-    int n = attn_length(a, b), tiles = attn_tiles<kStepM>(n);
-    while (w >= base + static_cast<long long>(tiles) * H * RT) {
-      base += static_cast<long long>(tiles) * H * RT;
-      n = attn_length(a, ++b);
-      tiles = attn_tiles<kStepM>(n);
-    }
-    const int item = static_cast<int>((w - base) / tiles);
-    const int tile0 = static_cast<int>((w - base) - static_cast<long long>(item) * tiles);
-    const int tile1 = static_cast<int>(min(static_cast<long long>(tiles), tile0 + (end - w)));
-    const int rt = item / H, h = item - rt * H;
-    const int row0 = rt * kRows, rows = min(kRows, R - row0);
+  constexpr int kEnd = L::kEnd;
+  const AttnPlan plan = attn_plan<kStepM, kEnd, kThreadsM>(a, H * RT, 4, s_plan);
+  AttnWalk<kStepM, kEnd, kRows> at(a, plan);
+  while (at.next()) {
+    const int n = at.n, b = at.b, h = at.h, row0 = at.row0, rows = at.rows, tile0 = at.tile0, tile1 = at.tile1;
     const int32_t* table = a.table.ids + b * a.table.stride;
 
     // The warp's steps: tokens [kStepM * tile + 16 * warp, + 16) of each tile.
@@ -563,7 +559,7 @@ __global__ void __launch_bounds__(Ring<E, D, NB>::kWarps * 32, Ring<E, D, NB>::k
         for (int x = 0; x < 4; ++x)
           parts[(warp * kRows + nb * 8 + t4 * 2 + (x & 1)) * kPitch + dim_of<E>(mt, x >> 1, g)] = o[mt][nb][x];
     __syncthreads();
-    const bool whole = tile0 == 0 && tile1 == tiles;
+    const bool whole = at.whole();
     float* slot = attn_slot<kRows, D>(a, blockIdx.x, tile0 == 0);
     for (int e = tid; e < rows * (D / 4); e += kThreadsM) {
       const int r = e / (D / 4), d = (e - r * (D / 4)) * 4;
@@ -592,11 +588,9 @@ __global__ void __launch_bounds__(Ring<E, D, NB>::kWarps * 32, Ring<E, D, NB>::k
       }
     }
     if (!whole) {
-      const long long first_step = base + static_cast<long long>(item) * tiles;
-      if (attn_arrive(a, first_step, tiles, plan.per, &s_flag))
-        attn_join<kRows, D, kThreadsM>(a, b, h, row0, rows, first_step, tiles, plan.per);
+      if (attn_arrive(a, at.first(), at.tiles, at.per, &s_flag))
+        attn_join<kRows, D, kThreadsM>(a, b, h, row0, rows, at.first(), at.tiles, at.per);
     }
-    w += tile1 - tile0;
   }
 }
 

@@ -24,6 +24,12 @@
 // score passes it by 2^8), write the weights P^T as two bf16 parts (hi and
 // lo: one bf16 weight would lose up to 2^-8 of a term, as much as rounding the
 // output does) and finish items.
+//
+// 64 sequences of 400..4000 tokens, 8 cache heads of 128: 32 rows a head 168
+// us, 68 rows 262 (the cache's bytes at the copy rate: 95).  A tile's softmax
+// of 32 rows takes as long as its bytes take HBM, about 2500 cycles (TMEM
+// reads, exponentials, the two-part weights' stores), more with more rows; an
+// item's start and end, where the ring waits, some 10 us.
 #pragma once
 
 #include "attention_common.cuh"
@@ -131,45 +137,9 @@ __device__ __forceinline__ bool group_any(int group, bool x) {
   return r != 0;
 }
 
-// One part of an item after the other, as every role walks them.
+constexpr int kEndT = 6;                 // steps that an item's start and end count as
 template <int N>
-struct Walk {
-  const AttnArgs& a;
-  long long w, end, per, base;
-  int b, H, RT, R;
-  int n, tiles, item, tile0, tile1, rt, h, row0, rows;
-  __device__ __forceinline__ Walk(const AttnArgs& args, const AttnPlan& p) : a(args) {
-    H = a.cache.heads;
-    R = a.Q * (a.Hq / H);
-    RT = (R + N - 1) / N;
-    per = p.per;
-    w = per * blockIdx.x;
-    end = min(p.total, w + per);
-    b = p.b;
-    base = p.base;
-    tile1 = tile0 = 0;
-  }
-  __device__ __forceinline__ bool next() {
-    w += tile1 - tile0;
-    if (w >= end) return false;
-    n = attn_length(a, b);
-    tiles = attn_tiles<kTile>(n);
-    while (w >= base + static_cast<long long>(tiles) * H * RT) {
-      base += static_cast<long long>(tiles) * H * RT;
-      n = attn_length(a, ++b);
-      tiles = attn_tiles<kTile>(n);
-    }
-    item = static_cast<int>((w - base) / tiles);
-    tile0 = static_cast<int>((w - base) - static_cast<long long>(item) * tiles);
-    tile1 = static_cast<int>(min(static_cast<long long>(tiles), tile0 + (end - w)));
-    rt = item / H;
-    h = item - rt * H;
-    row0 = rt * N;
-    rows = min(N, R - row0);
-    return true;
-  }
-  __device__ __forceinline__ long long first() const { return base + static_cast<long long>(item) * tiles; }
-};
+using Walk = AttnWalk<kTile, kEndT, N>;
 
 template <int N>
 struct SharedT {
@@ -209,7 +179,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) attention_tc_kernel(const AttnAr
     }
   };
 
-  const AttnPlan plan = attn_plan<kTile, kThreadsT>(
+  const AttnPlan plan = attn_plan<kTile, kEndT, kThreadsT>(
       a, a.cache.heads * ((a.Q * (a.Hq / a.cache.heads) + N - 1) / N), 2, sh.plan);
   if (tid == 0) {
     for (int i = 0; i < kSlots; ++i) {
@@ -259,7 +229,8 @@ __global__ void __launch_bounds__(kThreadsT, 1) attention_tc_kernel(const AttnAr
         if (more) ahead_tile = ahead.tile0;
       }
     };
-    if (more) look_up();
+    const bool any = more;
+    if (any) look_up();
     // where the thread's piece of row r0 + i * kStep lies in the swizzled slot:
     // the rows' low three bits go round every four steps
     uint32_t place_of[4];
@@ -269,7 +240,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) attention_tc_kernel(const AttnAr
     static_assert(4 * kStep % 8 == 0, "four steps go round");
     int slot = 0;
     uint32_t turn = 0;  // times the ring went round
-    for (int tile_no = 0; at.w < at.end; ++tile_no) {
+    for (int tile_no = 0; any; ++tile_no) {
       bool all = true;
 #pragma unroll
       for (int i = 0; i < kLook; ++i) {
@@ -556,7 +527,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) attention_tc_kernel(const AttnAr
       wait(&sh.p_free, (tile_no - 1) & 1);
       tc_after();
       soft_sync();
-      const bool whole = at.tile0 == 0 && at.tile1 == at.tiles;
+      const bool whole = at.whole();
       float* slot = attn_slot<N, D>(a, blockIdx.x, at.tile0 == 0);
       for (int r = tid; r < at.rows; r += kSoft) {
         const float sum = sh.lsum[0][r] + sh.lsum[1][r] + sh.lsum[2][r] + sh.lsum[3][r], m = sh.m[r];
