@@ -57,53 +57,73 @@ __device__ __forceinline__ void copy_tokens(const CacheView& cv, const char* src
 
 // ---- append ----------------------------------------------------------------
 // One warp per new token: it finds the token's sequence in `starts`, its page
-// in the table, and copies the two rows.
+// in the table, and copies the two rows.  The rows' first pieces are under way
+// while it looks (four dependent loads or more): 42000 tokens of twelve
+// sequences, 8 heads of 128, in 60 us, their bytes at the copy rate 54, and a
+// verify step's 384 in 4.7, nearly all of it a launch.
+constexpr int kPieces = 4;  // of K, and of V, a lane holds
 __global__ void __launch_bounds__(256)
 append_kernel(const char* k_new, const char* v_new, long long new_stride, int T, const int32_t* starts,
               CacheView c, PageTable table, const int32_t* lengths, int B, int32_t* status) {
   const int lane = threadIdx.x & 31;
   const int vecs = c.row_bytes() / 16;
   const int per = starts ? 0 : T / B;
-  for (int row = blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5); row < T;
-       row += gridDim.x * (blockDim.x / 32)) {
-    int b, after;  // sequence, and its new tokens from this one on
-    if (starts) {
-      int lo = 0, hi = B;  // the last b with starts[b] <= row
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (starts[mid] <= row) lo = mid;
-        else hi = mid;
+  const long long warp = static_cast<long long>(blockIdx.x) * (blockDim.x / 32) + (threadIdx.x >> 5);
+  if (warp >= T) return;
+  const int row = static_cast<int>(warp);
+  const uint4* ks = reinterpret_cast<const uint4*>(k_new + row * new_stride) + lane;
+  const uint4* vs = reinterpret_cast<const uint4*>(v_new + row * new_stride) + lane;
+  uint4 kw[kPieces], vw[kPieces];
+  auto load = [&](int j0) {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i)
+      if (j0 + i * 32 + lane < vecs) {
+        kw[i] = ld_stream_v4(ks + j0 + i * 32);
+        vw[i] = ld_stream_v4(vs + j0 + i * 32);
       }
-      b = lo;
-      after = starts[b + 1] - row;
-      if (starts[b] > row || after <= 0 || starts[b + 1] > T) {  // rows that no sequence claims
-        if (lane == 0) report(status, kDataLengthRange);
-        continue;
-      }
-    } else {
-      b = row / per;
-      after = per - (row - b * per);
+  };
+  load(0);
+  int b, after;  // sequence, and its new tokens from this one on
+  if (starts) {
+    int lo = 0, hi = B;  // the last b with starts[b] <= row
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (starts[mid] <= row) lo = mid;
+      else hi = mid;
     }
-    const long long at = static_cast<long long>(lengths[b]) - after;
-    if (at < 0 || at >= static_cast<long long>(table.max_pages) * c.page_size) {
+    b = lo;
+    after = starts[b + 1] - row;
+    if (starts[b] > row || after <= 0 || starts[b + 1] > T) {  // rows that no sequence claims
       if (lane == 0) report(status, kDataLengthRange);
-      continue;
+      return;
     }
-    const int slot = static_cast<int>(at) / c.page_size;
-    const int page = table.ids[b * table.stride + slot];
-    if (page < 0 || page >= c.pages) {
-      if (lane == 0) report(status, kDataPageRange);
-      continue;
-    }
-    const long long off = page * c.page_stride + (static_cast<int>(at) - slot * c.page_size) * c.token_stride;
-    const uint4* ks = reinterpret_cast<const uint4*>(k_new + row * new_stride);
-    const uint4* vs = reinterpret_cast<const uint4*>(v_new + row * new_stride);
-    uint4* kd = reinterpret_cast<uint4*>(c.k + off);
-    uint4* vd = reinterpret_cast<uint4*>(c.v + off);
-    for (int j = lane; j < vecs; j += 32) {
-      kd[j] = __ldg(ks + j);
-      vd[j] = __ldg(vs + j);
-    }
+  } else {
+    b = row / per;
+    after = per - (row - b * per);
+  }
+  const long long at = static_cast<long long>(lengths[b]) - after;
+  if (at < 0 || at >= static_cast<long long>(table.max_pages) * c.page_size) {
+    if (lane == 0) report(status, kDataLengthRange);
+    return;
+  }
+  const int slot = static_cast<int>(at) / c.page_size;
+  const int page = table.ids[b * table.stride + slot];
+  if (page < 0 || page >= c.pages) {
+    if (lane == 0) report(status, kDataPageRange);
+    return;
+  }
+  const long long off = page * c.page_stride + (static_cast<int>(at) - slot * c.page_size) * c.token_stride;
+  uint4* kd = reinterpret_cast<uint4*>(c.k + off) + lane;
+  uint4* vd = reinterpret_cast<uint4*>(c.v + off) + lane;
+  for (int j0 = 0;;) {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i)
+      if (j0 + i * 32 + lane < vecs) {
+        kd[j0 + i * 32] = kw[i];
+        vd[j0 + i * 32] = vw[i];
+      }
+    if ((j0 += 32 * kPieces) >= vecs) break;
+    load(j0);
   }
 }
 
@@ -265,7 +285,9 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const ForkArgs 
 
 // Writes the rows of the new table and copies the kept tokens of partly
 // filled pages that did not stay: groups of threads take (sequence, table row
-// or one layer's K or V).
+// or one layer's K or V).  (Shared out by 8 tokens, what every copy looks up
+// first cost more than the evener shares gave: 28 us against 21 for 512
+// sequences with 15 tokens each in 4 layers.)
 __device__ void fork_write(const ForkArgs& a, const ForkSpace& s) {
   const CacheView& cv = a.cache;
   const int nfree = *s.nfree;
@@ -433,8 +455,21 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const Compac
   compact_plan(a, s, s.refs, scratch);
 }
 
-// Rewrites the table and moves the pages: groups of threads take (page, one
-// layer's K or V).
+// A group moves at most this many tokens of a page at a time, eight pieces a
+// thread: whole pages (32 KB with 8 heads of 128) shared the work out less
+// evenly (98 us against 97 for a pool of 4096 pages in 4 layers, half in use;
+// the move alone is 78, its bytes at the copy rate 80, the plan's block 14).
+__host__ __device__ __forceinline__ int copy_chunk(const CacheView& cv) {
+  const int vecs = static_cast<int>(cv.row_bytes() / 16);
+  return vecs < 8 * kGroup ? 8 * kGroup / vecs : 1;
+}
+__host__ __device__ __forceinline__ int copy_chunks(const CacheView& cv) {
+  const int n = copy_chunk(cv);
+  return (cv.page_size + n - 1) / n;
+}
+
+// Rewrites the table and moves the pages: groups of threads take (page, some
+// tokens of one layer's K or V).
 __device__ void compact_move(const CompactArgs& a, const CompactSpace& s) {
   const CacheView& cv = a.cache;
   const int P = cv.pages;
@@ -444,13 +479,17 @@ __device__ void compact_move(const CompactArgs& a, const CompactSpace& s) {
     const int p = a.table.ids[b * a.table.stride + (x - static_cast<long long>(b) * a.table.max_pages)];
     a.new_table[x] = p >= 0 && p < P ? s.to[p] : -1;
   }
-  const int moves = *s.moves, vecs = cv.row_bytes() / 16, parts = 2 * cv.layers;
+  const int moves = *s.moves, vecs = cv.row_bytes() / 16;
+  const int chunk = copy_chunk(cv), chunks = copy_chunks(cv), parts = 2 * cv.layers * chunks;
   const int lane = threadIdx.x % kGroup, groups = gridDim.x * (blockDim.x / kGroup);
   const long long jobs = static_cast<long long>(moves) * parts;
   for (long long x = blockIdx.x * (blockDim.x / kGroup) + threadIdx.x / kGroup; x < jobs; x += groups) {
-    const int i = static_cast<int>(x / parts), y = static_cast<int>(x - static_cast<long long>(i) * parts);
+    const int i = static_cast<int>(x / parts), z = static_cast<int>(x - static_cast<long long>(i) * parts);
+    const int y = z / chunks, t0 = (z - y * chunks) * chunk;
+    const long long at = t0 * cv.token_stride;
     char* pool = (y & 1 ? cv.v : cv.k) + (y >> 1) * cv.layer_stride;
-    copy_tokens(cv, pool + s.from[i] * cv.page_stride, pool + s.holes[i] * cv.page_stride, cv.page_size, vecs, lane);
+    copy_tokens(cv, pool + s.from[i] * cv.page_stride + at, pool + s.holes[i] * cv.page_stride + at,
+                min(chunk, cv.page_size - t0), vecs, lane);
   }
 }
 
@@ -491,11 +530,8 @@ size_t up(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
 cudaError_t launch_append(const char* k_new, const char* v_new, long long new_stride, int T,
                           const int32_t* starts, const CacheView& c, const PageTable& t,
-                          const int32_t* lengths, int B, int32_t* status, int sm_count,
-                          cudaStream_t stream) {
-  const int blocks = (T + 7) / 8, most = sm_count * 8;
-  append_kernel<<<blocks < most ? blocks : most, 256, 0, stream>>>(k_new, v_new, new_stride, T, starts, c, t,
-                                                                   lengths, B, status);
+                          const int32_t* lengths, int B, int32_t* status, cudaStream_t stream) {
+  append_kernel<<<(T - 1) / 8 + 1, 256, 0, stream>>>(k_new, v_new, new_stride, T, starts, c, t, lengths, B, status);
   return cudaGetLastError();
 }
 
@@ -546,7 +582,7 @@ cudaError_t launch_compact(const CompactArgs& a, void* ws, int sm_count, cudaStr
   }
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const long long pieces = static_cast<long long>(a.cache.pages / 2) * 2 * a.cache.layers + entries / kGroup;
+  const long long pieces = static_cast<long long>(a.cache.pages / 2) * 2 * a.cache.layers * copy_chunks(a.cache) + entries / kGroup;
   return launch_after(compact_move_kernel, a, s, pieces, sm_count, stream);
 }
 

@@ -80,8 +80,7 @@ cudaError_t launch_attention(const AttnArgs& a, int sm_count, cudaStream_t strea
 
 cudaError_t launch_append(const char* k_new, const char* v_new, long long new_stride, int T,
                           const int32_t* starts, const CacheView& c, const PageTable& t,
-                          const int32_t* lengths, int B, int32_t* status, int sm_count,
-                          cudaStream_t stream);
+                          const int32_t* lengths, int B, int32_t* status, cudaStream_t stream);
 
 struct ForkArgs {
   CacheView cache;

@@ -169,7 +169,7 @@ spec_status_t spec_cache_append(const void* k_new, const void* v_new, int64_t ne
   st = device_sms(&sms);
   if (st != SPEC_OK) return st;
   return done(specv::launch_append(static_cast<const char*>(k_new), static_cast<const char*>(v_new),
-                                   new_stride * esz, T, starts, c, t, lengths, B, device_status, sms,
+                                   new_stride * esz, T, starts, c, t, lengths, B, device_status,
                                    reinterpret_cast<cudaStream_t>(stream)));
 }
 
