@@ -1,4 +1,5 @@
-"""Build libspecverify.so (the C-ABI CUDA library) in-tree for sm_103a.
+"""Build libspecverify.so (the C-ABI CUDA library) in-tree for sm_103a, and
+_decode_calls.so, the part of decode.py that is not Python.
 
 Each translation unit under ``csrc/`` is compiled by nvcc in parallel, then
 linked into ``draft_verify_acceptance_gb300/libspecverify.so``.  Register and
@@ -8,6 +9,7 @@ import concurrent.futures as cf
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -19,6 +21,32 @@ SOURCES = ["spec_verify.cu", "verify_greedy.cu", "verify_sample.cu", "verify_sam
            "spec_verify_static.cu", "spec_decode.cu", "attention.cu", "attention_tc.cu", "cache_pages.cu", "filtered_sample.cu"]
 
 
+CALLS = os.path.join(HERE, "_decode_calls.so")
+CALLS_SOURCE = "decode_calls.cpp"
+
+
+def build_calls(force: bool = False) -> str:
+    """Compile _decode_calls.so against the installed torch if its source is newer than it."""
+    src = os.path.join(CSRC, CALLS_SOURCE)
+    deps = [src, os.path.join(ROOT, "include", "spec_decode.h"), os.path.abspath(__file__)]
+    if not force and os.path.exists(CALLS) and all(os.path.getmtime(f) <= os.path.getmtime(CALLS) for f in deps):
+        return CALLS
+    import torch
+    home = os.path.dirname(torch.__file__)
+    lib = os.path.join(home, "lib")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
+    tmp = CALLS + ".tmp"
+    r = subprocess.run(["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden",
+                        f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                        "-I", os.path.join(ROOT, "include"), "-isystem", os.path.join(home, "include"), "-isystem", cuda,
+                        "-isystem", sysconfig.get_paths()["include"], src, "-o", tmp, "-L", lib, "-lc10", "-lc10_cuda",
+                        "-ltorch_cpu", "-ltorch_python", f"-Wl,-rpath,{lib}"], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {CALLS_SOURCE}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS)
+    return CALLS
+
+
 def _nvcc():
     exe = shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc"
     if not os.path.exists(exe):
@@ -27,7 +55,7 @@ def _nvcc():
 
 
 def _deps():
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
+    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f != CALLS_SOURCE]
     files += [os.path.join(ROOT, "include", h) for h in ("spec_verify.h", "spec_decode.h")]
     files.append(os.path.abspath(__file__))
     return files
@@ -53,8 +81,16 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False) -> st
     same optional flag SPEC_NVTX (environment variable SPEC_NVTX=1 at build
     time) wraps every entry point in an NVTX range."""
     lib, bdir = (LIB_DEBUG, BUILD_DEBUG) if debug else (LIB, BUILD)
-    if not force and not _stale(lib):
-        return lib
+    with cf.ThreadPoolExecutor(max_workers=1) as calls:
+        made = None if debug else calls.submit(build_calls, force)
+        if force or _stale(lib):
+            _build_library(lib, bdir, verbose, debug)
+        if made:
+            made.result()
+    return lib
+
+
+def _build_library(lib, bdir, verbose, debug):
     os.makedirs(bdir, exist_ok=True)
     wanted = {src.replace(".cu", ".o") for src in SOURCES}
     for f in os.listdir(bdir):  # objects of sources no longer in the library
@@ -89,7 +125,6 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False) -> st
     os.replace(tmp, lib)
     if verbose:
         print(open(os.path.join(bdir, "ptxas.log")).read())
-    return lib
 
 
 if __name__ == "__main__":

@@ -22,6 +22,7 @@ from typing import NamedTuple
 
 import torch
 
+from . import _decode_calls
 from .binding import (DTYPE_BF16, DTYPE_F32, ERR_INVALID_ARG, ERR_UNSUPPORTED, MAX_V, OK, SpecVerifyError,
                       _lib)
 
@@ -65,6 +66,7 @@ _declare()
 _DTYPES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
 _ws_lock = threading.Lock()
 _ws = {}
+_KINDS = {"attention": 0, "fork": 1, "compact": 2, "sample": 3}
 
 
 class ForkResult(NamedTuple):
@@ -91,6 +93,9 @@ class SampleResult(NamedTuple):
     status: torch.Tensor      # int32 [1] with debug, else None
 
 
+_decode_calls.bind(tuple(ctypes.cast(getattr(_lib, n), ctypes.c_void_p).value for n in EXPORTS), ForkResult, CompactResult,
+                   SampleResult)
+
 _raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream's handle, without a Stream object
 
 
@@ -113,13 +118,20 @@ def _workspace(kind, index, stream, nbytes, given):
             if kept is None or kept[2] < nbytes:
                 ws = torch.zeros(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
                 kept = _ws[key] = (ws, ws.data_ptr(), nbytes)
+                _decode_calls.register_workspace(_KINDS[kind], index, stream, kept[1], nbytes)
     return kept[1], kept[2]
 
 
 def _on_stream(fn):
     """Runs a call with its device and, when one is given, its stream current, so that what it allocates
     belongs to the stream that uses it; passes the device's index and the stream's handle."""
-    def call(first, *args, stream=None, **kw):
+    native = getattr(_decode_calls, fn.__name__)
+
+    def call(*args, **kw):
+        r = native(*args, **kw)  # the ordinary call; what it does not do comes back
+        return slow(*args, **kw) if r is NotImplemented else r
+
+    def slow(first, *args, stream=None, **kw):
         if not isinstance(first, torch.Tensor) or not first.is_cuda:
             where = first.device if isinstance(first, torch.Tensor) else type(first).__name__
             raise ValueError(f"{fn.__name__} takes CUDA tensors (got {where})")

@@ -653,3 +653,74 @@ def test_filtered_rows_feed_the_verifier(decode):
     for b in range(B):
         for i in range(n[b] + 1):
             assert float(target[b, i, out[b][i]]) > -math.inf
+
+
+# ---- the calls themselves -----------------------------------------------------------------------
+
+def test_ordinary_calls_and_others_agree(decode):
+    """The ordinary call of each operator is made without decode.py's steps; with any further argument decode.py makes
+    it.  Both give the same, and what decode.py refuses is refused."""
+    calls = decode._decode_calls
+    k, v, table, lengths = make_cache([40, 7, 300], 16, 2, 64, torch.bfloat16, seed=1, layers=2, spare=60, extra_cols=4)
+    q = torch.randn((3, 5, 8, 64), generator=gen(2), device="cuda").to(torch.bfloat16)
+    a = (q, k[0], v[0], table, lengths)
+    decode.paged_attention(*a)
+    plain = calls.paged_attention(*a, return_lse=True)
+    out, lse, status = decode.paged_attention(*a, return_lse=True, debug=True)
+    assert int(status) == 0 and torch.equal(plain[0], out) and torch.equal(plain[1], lse)
+    assert torch.equal(calls.paged_attention(*a, 0.5), decode.paged_attention(*a, 0.5, debug=True)[0])
+    new = torch.randn((3, 5, 2, 64), generator=gen(3), device="cuda").to(torch.bfloat16)
+    kk, vv = k.clone(), v.clone()
+    assert calls.cache_append(new, new * 2, k[1], v[1], table, lengths) is None
+    decode.cache_append(new, new * 2, kk[1], vv[1], table, lengths, debug=True)
+    assert torch.equal(k, kk) and torch.equal(v, vv)
+    ragged = (new.flatten(0, 1), new.flatten(0, 1), k[0], v[0], table, lengths, i32([0, 3, 3, 15]))
+    assert calls.cache_append(*ragged) is None
+    parents, keep = i32([0, 2, 2, -1]), i32([40, 299, 17, 0])
+    decode.cache_fork(kk, vv, table, lengths, parents, keep, 5)
+    got = calls.cache_fork(kk.clone(), vv.clone(), table, lengths, parents, keep, room=5)
+    want = decode.cache_fork(kk.clone(), vv.clone(), table, lengths, parents, keep, 5, debug=True)
+    assert type(got) is type(want) and got.status is None and int(want.status) == 0
+    assert all(torch.equal(x, y) for x, y in zip(got[:5], want[:5]))
+    decode.cache_compact(kk.clone(), vv.clone(), table)
+    got = calls.cache_compact(kk.clone(), vv.clone(), table)
+    want = decode.cache_compact(kk.clone(), vv.clone(), table, debug=True)
+    assert type(got) is type(want) and all(torch.equal(x, y) for x, y in zip(got[:3], want[:3]))
+    x = (torch.randn((4, 6, 3001), generator=gen(4), device="cuda") * 3).to(torch.bfloat16)
+    u = torch.rand((4, 6), generator=gen(5), device="cuda")
+    kw = dict(top_k=torch.full((4, 6), 50, dtype=torch.int32, device="cuda"), top_p=0.9, return_filtered=True)
+    got = calls.filtered_sample(x, u, 0.7, **kw)
+    want = decode.filtered_sample(x, u, 0.7, debug=True, **kw)
+    assert type(got) is type(want) and all(torch.equal(p, r) for p, r in zip(got[:4], want[:4]))
+    big = (x[0, :1].expand(700, -1).contiguous(), torch.rand(700, generator=gen(6), device="cuda"))
+    first = decode.filtered_sample(*big, top_p=0.9)  # (makes the workspace)
+    assert torch.equal(calls.filtered_sample(*big, top_p=0.9).tokens, first.tokens)
+    # everything that decode.py makes of its own, or refuses
+    side = torch.cuda.Stream()
+    cpu = lengths.cpu()
+    for call, args, kw in ((calls.paged_attention, a, dict(debug=True)), (calls.paged_attention, a, dict(out=out)),
+                           (calls.paged_attention, a, dict(stream=side)), (calls.paged_attention, a, dict(nothing=None)),
+                           (calls.paged_attention, a + (0.1, True), {}), (calls.paged_attention, a, dict(scale="x")),
+                           (calls.paged_attention, a, dict(q=q)), (calls.paged_attention, a[:4], {}),
+                           (calls.paged_attention, (q.float(),) + a[1:], {}),
+                           (calls.paged_attention, (q[:2],) + a[1:], {}),
+                           (calls.paged_attention, (q, k[0], v[0].clone()[:, :8]) + a[3:], {}),
+                           (calls.paged_attention, a[:4] + (lengths.long(),), {}),
+                           (calls.paged_attention, a[:4] + (cpu,), {}), (calls.paged_attention, a[:3] + (table.t(), lengths), {}),
+                           (calls.paged_attention, a, dict(scale=math.nan)), (calls.paged_attention, (None,) * 5, {}),
+                           (calls.cache_append, (new, new, k[1], v[1], table, lengths[:2]), {}),
+                           (calls.cache_append, (new, new.float(), k[1], v[1], table, lengths), {}),
+                           (calls.cache_append, ragged[:6] + (i32([0, 3]),), {}),
+                           (calls.cache_append, (new, new, k, v, table, lengths), {}),
+                           (calls.cache_fork, (k, v, table, lengths, parents, keep[:2], 5), {}),
+                           (calls.cache_fork, (k, v, table, lengths, parents, keep, 1 << 40), {}),
+                           (calls.cache_fork, (k, v, table, lengths, parents, keep, -1), {}),
+                           (calls.cache_fork, (k, v, table, lengths, parents, keep, 0.5), {}),
+                           (calls.cache_compact, (k, v, table[0]), {}), (calls.cache_compact, (k.half(), v.half(), table), {}),
+                           (calls.filtered_sample, (x, u[:2]), {}), (calls.filtered_sample, (x, u.double()), {}),
+                           (calls.filtered_sample, (x, u), dict(top_k=1.5)), (calls.filtered_sample, (x, u), dict(top_p="x")),
+                           (calls.filtered_sample, (x, u), dict(temperature=torch.ones(5, device="cuda"))),
+                           (calls.filtered_sample, (x, u), dict(temperature=-1.0)),
+                           (calls.filtered_sample, (x, u, 1.0, 5), {}), (calls.filtered_sample, (x[..., :0], u), {}),
+                           (calls.filtered_sample, (x[..., ::2], u), {})):
+        assert call(*args, **kw) is NotImplemented, (call, kw)
