@@ -34,6 +34,14 @@
 //   write   filtered rows that take the logits' place, streaming.  (Others are
 //           filled with -inf by the list kernel, on its way, and finish adds
 //           what is kept.)
+//
+// Measured, bf16: 4096 rows of 32000, top-p 0.9, 171 us, of which list 95 (the
+// logits at the copy rate: 39; 17 instructions a logit at two thirds of the
+// issue slots), finish 46 (lists of 845 entries in three passes), whole 29 for
+// the few rows between the bounds (one row's latency); 384 rows of 128256 with
+// eight settings and filtered rows 81 us (30); 4 rows of 1000 in the whole
+// kernel alone 12.  A flat row whose kept set is a tenth of its 32000 logits
+// takes a cluster 100 us.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
