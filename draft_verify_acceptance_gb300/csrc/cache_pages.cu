@@ -58,7 +58,7 @@ __device__ __forceinline__ void copy_tokens(const CacheView& cv, const char* src
 // ---- append ----------------------------------------------------------------
 // One warp per new token: it finds the token's sequence in `starts`, its page
 // in the table, and copies the two rows.  The rows' first pieces are under way
-// while it looks (four dependent loads or more): 42000 tokens of twelve
+// while it looks (four dependent loads or more): 53000 tokens of twelve
 // sequences, 8 heads of 128, in 60 us, their bytes at the copy rate 54, and a
 // verify step's 384 in 4.7, nearly all of it a launch.
 constexpr int kPieces = 4;  // of K, and of V, a lane holds
@@ -345,25 +345,36 @@ __global__ void __launch_bounds__(kPlanThreads, 1) fork_block_kernel(const ForkA
     }
   }
   __syncthreads();
+  // a warp a parent, its pages from the last to the first, four table entries a
+  // lane on their way at once
+  constexpr int kAhead = 4;
   for (int b = tid >> 5; b < a.B; b += kPlanThreads / 32) {
-    const int S = a.cache.page_size, len = min(max(a.lengths[b], 0), M * S);
+    const int S = a.cache.page_size, len = min(max(__ldg(a.lengths + b), 0), M * S);
     const int most = len / S;  // full pages that anyone can keep
+    const int32_t* row = a.table.ids + b * a.table.stride;
     int beyond = 0;            // sequences that keep more than the pages seen so far
-    for (int j0 = (most + 31) / 32 * 32 - 32; j0 >= 0; j0 -= 32) {
-      const int j = j0 + lane;
-      int sum = j < most ? ends[b * (M + 1) + j + 1] : 0;  // ends at j + 1: keeps page j
+    for (int j0 = (most + 32 * kAhead - 1) / (32 * kAhead) * (32 * kAhead); j0 > 0;) {
+      j0 -= 32 * kAhead;
+      int page[kAhead];
 #pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int o = __shfl_down_sync(0xffffffffu, sum, d);
-        if (lane + d < 32) sum += o;
+      for (int i = 0; i < kAhead; ++i) page[i] = j0 + i * 32 + lane < most ? __ldg(row + j0 + i * 32 + lane) : 0;
+#pragma unroll
+      for (int i = kAhead - 1; i >= 0; --i) {
+        if (j0 + i * 32 >= most) continue;
+        const int j = j0 + i * 32 + lane;
+        int sum = j < most ? ends[b * (M + 1) + j + 1] : 0;  // ends at j + 1: keeps page j
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int o = __shfl_down_sync(0xffffffffu, sum, d);
+          if (lane + d < 32) sum += o;
+        }
+        sum += beyond;
+        if (j < most && sum > 0) {
+          if (page[i] >= 0 && page[i] < P) atomicAdd(&refs[page[i]], sum);
+          else bad |= kDataPageRange;
+        }
+        beyond = __shfl_sync(0xffffffffu, sum, 0);
       }
-      sum += beyond;
-      if (j < most && sum > 0) {
-        const int p = a.table.ids[b * a.table.stride + j];
-        if (p >= 0 && p < P) atomicAdd(&refs[p], sum);
-        else bad |= kDataPageRange;
-      }
-      beyond = __shfl_sync(0xffffffffu, sum, 0);
     }
   }
   report(a.status, bad);
@@ -458,7 +469,8 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const Compac
 // A group moves at most this many tokens of a page at a time, eight pieces a
 // thread: whole pages (32 KB with 8 heads of 128) shared the work out less
 // evenly (98 us against 97 for a pool of 4096 pages in 4 layers, half in use;
-// the move alone is 78, its bytes at the copy rate 80, the plan's block 14).
+// now 95: the move alone is 78, its bytes at the copy rate 80, and the plan's
+// block 12 comes before).
 __host__ __device__ __forceinline__ int copy_chunk(const CacheView& cv) {
   const int vecs = static_cast<int>(cv.row_bytes() / 16);
   return vecs < 8 * kGroup ? 8 * kGroup / vecs : 1;
@@ -503,7 +515,24 @@ __global__ void __launch_bounds__(kPlanThreads, 1) compact_block_kernel(const Co
   __shared__ int scratch[32];
   for (int i = threadIdx.x; i < a.cache.pages; i += kPlanThreads) counts[i] = 0;
   __syncthreads();
-  compact_count(a, counts, threadIdx.x, kPlanThreads);
+  // (as compact_count, four entries on their way at once, and in 32 bits)
+  constexpr int kAhead = 4;
+  const int entries = a.B * a.table.max_pages;
+  int bad = 0;
+  for (int x0 = threadIdx.x; x0 < entries; x0 += kAhead * kPlanThreads) {
+    int page[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int x = x0 + i * kPlanThreads, b = x / a.table.max_pages;
+      page[i] = x < entries ? __ldg(a.table.ids + b * a.table.stride + (x - b * a.table.max_pages)) : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (page[i] >= a.cache.pages) bad = kDataPageRange;
+      else if (page[i] >= 0) atomicAdd(&counts[page[i]], 1);
+    }
+  }
+  report(a.status, bad);
   __syncthreads();
   compact_plan(a, s, counts, scratch);
 }
