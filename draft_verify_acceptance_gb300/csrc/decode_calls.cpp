@@ -4,7 +4,7 @@
 // A call of a server's step takes the GPU 5 to 15 us, and Python's checks,
 // allocations and argument conversions took 20 to 30.  This module does them in
 // one go for calls on the current device and stream without debug, out= or
-// workspace=.  Anything else, and any argument that decode.py would refuse,
+// workspace= that no CUDA graph captures.  Anything else, and any argument that decode.py would refuse,
 // returns NotImplemented: decode.py then makes the call itself, or says what is
 // wrong with it.  (So no check here is looser than decode.py's, and there are
 // no messages.)  Workspaces are decode.py's own, registered here as it makes
@@ -14,6 +14,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -64,6 +65,7 @@ bool workspace(long kind, const Where& w, size_t bytes, void** p, size_t* have) 
   *p = nullptr;
   *have = 0;
   if (bytes == 0) return true;
+  if (c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None) return false;
   for (const Workspace& x : workspaces)
     if (x.kind == kind && x.device == w.device && x.stream == reinterpret_cast<unsigned long long>(w.stream)) {
       *p = x.p;

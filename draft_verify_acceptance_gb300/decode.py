@@ -100,16 +100,20 @@ _raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream's handle,
 
 
 def _workspace(kind, index, stream, nbytes, given):
-    """The caller's workspace, or one kept for this kind of call, device and stream.  It is zero-filled
-    when made; every call leaves it fit for the next."""
+    """(pointer, bytes, what owns them): the caller's workspace, or one kept for this kind of call, device and
+    stream.  It is zero-filled when made; every call leaves it fit for the next.  A call that a CUDA graph captures
+    gets one of its own, zero-filled by the graph: a kept one may be replaced by a larger one before a replay."""
     if given is not None:
         if given.get_device() != index or not given.is_contiguous():
             raise ValueError(f"workspace must be contiguous on cuda:{index}")
         if given.numel() * given.element_size() < nbytes:
             raise ValueError(f"workspace holds {given.numel() * given.element_size()} bytes, {nbytes} are needed")
-        return given.data_ptr(), given.numel() * given.element_size()
+        return given.data_ptr(), given.numel() * given.element_size(), given
     if nbytes == 0:
-        return None, 0
+        return None, 0, None
+    if torch.cuda.is_current_stream_capturing():
+        ws = torch.zeros(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
+        return ws.data_ptr(), nbytes, ws
     key = (kind, index, stream)
     kept = _ws.get(key)
     if kept is None or kept[2] < nbytes:
@@ -119,7 +123,7 @@ def _workspace(kind, index, stream, nbytes, given):
                 ws = torch.zeros(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
                 kept = _ws[key] = (ws, ws.data_ptr(), nbytes)
                 _decode_calls.register_workspace(_KINDS[kind], index, stream, kept[1], nbytes)
-    return kept[1], kept[2]
+    return kept[1], kept[2], kept[0]
 
 
 def _on_stream(fn):
@@ -207,8 +211,8 @@ def _status(debug, device):
 
 
 def attention_workspace_size(B, Q, Hq, heads, head_dim, dtype):
-    """Bytes of workspace that a paged_attention call with these sizes needs (0: not supported).  A call
-    inside a CUDA graph brings its own: zero-filled once, used by one call at a time."""
+    """Bytes of workspace that a paged_attention call with these sizes needs (0: not supported): zero-filled once,
+    used by one call at a time."""
     return int(_lib.spec_attention_workspace_size(B, Q, Hq, heads, head_dim, _DTYPES[dtype]))
 
 
@@ -252,7 +256,7 @@ def paged_attention(at, q, k_pages, v_pages, page_table, lengths, scale=None, *,
     need = _lib.spec_attention_workspace_size(B, Q, Hq, heads, D, c.dtype)
     if need == 0:
         _raise(ERR_UNSUPPORTED, f"paged_attention with head_dim {D}")
-    ws, nbytes = _workspace("attention", index, stream, need, workspace)
+    ws, nbytes, held = _workspace("attention", index, stream, need, workspace)
     # the stride of a dimension of one element is free in torch
     rc = _lib.spec_paged_attention(
         q.data_ptr(), st[0] if B > 1 else 0, st[1] if Q > 1 else 0, st[2] if Hq > 1 else 0, c, table, ts, M, lens, B, Q, Hq,
@@ -332,7 +336,7 @@ def cache_fork(at, k_pages, v_pages, page_table, lengths, parents, keep, room=0,
     free = torch.empty(P, dtype=torch.int32, device=device)
     n_free = torch.empty(1, dtype=torch.int32, device=device)
     status, status_at = _status(debug, device)
-    ws, nbytes = _workspace("fork", index, stream, _lib.spec_cache_fork_workspace_size(P, C), workspace)
+    ws, nbytes, held = _workspace("fork", index, stream, _lib.spec_cache_fork_workspace_size(P, C), workspace)
     rc = _lib.spec_cache_fork(c, table, ts, M, lens, B, par, kp, C, room, new.data_ptr(), lens_new.data_ptr(),
                               refs.data_ptr(), free.data_ptr(), n_free.data_ptr(), ws, nbytes, stream, status_at)
     if rc != OK:
@@ -357,7 +361,7 @@ def cache_compact(at, k_pages, v_pages, page_table, *, workspace=None, debug=Fal
     refs = torch.empty(P, dtype=torch.int32, device=device)
     n_live = torch.empty(1, dtype=torch.int32, device=device)
     status, status_at = _status(debug, device)
-    ws, nbytes = _workspace("compact", index, stream, _lib.spec_cache_compact_workspace_size(P), workspace)
+    ws, nbytes, held = _workspace("compact", index, stream, _lib.spec_cache_compact_workspace_size(P), workspace)
     rc = _lib.spec_cache_compact(c, table, ts, M, B, new.data_ptr(), refs.data_ptr(), n_live.data_ptr(), ws, nbytes, stream,
                                  status_at)
     if rc != OK:
@@ -432,7 +436,7 @@ def filtered_sample(at, logits, uniforms, temperature=1.0, *, top_k=None, top_p=
         out_at = out.data_ptr()
     status, status_at = _status(debug, device)
     need = _lib.spec_filtered_sample_workspace_size(R, V, dt)
-    ws, nbytes = _workspace("sample", index, stream, need, workspace)
+    ws, nbytes, held = _workspace("sample", index, stream, need, workspace)
     rc = _lib.spec_filtered_sample(
         logits.data_ptr(), stride, uniforms.data_ptr(), R, V, dt, T, k, p, m, Tp, kp, pp, mp, tokens.data_ptr(),
         prob.data_ptr(), n_kept.data_ptr(), out_at, ws, nbytes, stream, status_at)

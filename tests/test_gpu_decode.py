@@ -724,3 +724,38 @@ def test_ordinary_calls_and_others_agree(decode):
                            (calls.filtered_sample, (x, u, 1.0, 5), {}), (calls.filtered_sample, (x[..., :0], u), {}),
                            (calls.filtered_sample, (x[..., ::2], u), {})):
         assert call(*args, **kw) is NotImplemented, (call, kw)
+
+
+def test_calls_in_a_graph_own_their_workspaces(decode):
+    """Captured calls without a workspace of the caller's: replays are right after eager calls that need larger
+    workspaces, and eager calls after a capture that was never replayed."""
+    k, v, table, lengths = make_cache([40, 700, 3000], 16, 2, 128, torch.bfloat16, seed=1)
+    q = torch.randn((3, 1, 8, 128), generator=gen(2), device="cuda").to(torch.bfloat16)
+    x = (torch.randn((400, 4001), generator=gen(4), device="cuda") * 3).to(torch.bfloat16)
+    u = torch.rand(400, generator=gen(5), device="cuda")
+    parents, keep = i32([2, 1, 1]), i32([77, 3, 700])
+
+    def run():
+        return (decode.paged_attention(q, k, v, table, lengths), decode.filtered_sample(x, u, top_p=0.9).tokens,
+                *decode.cache_fork(k.clone(), v.clone(), table, lengths, parents, keep, 5)[:5],
+                *decode.cache_compact(k.clone(), v.clone(), table)[:3])
+    want = run()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        run()  # (workspaces of this stream exist before the capture)
+        side.synchronize()
+        graph, never = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+        with torch.cuda.graph(never, stream=side):
+            run()
+        with torch.cuda.graph(graph, stream=side):
+            got = run()
+        big = make_cache([4000] * 40, 16, 8, 128, torch.bfloat16, seed=3)
+        for _ in range(3):
+            decode.paged_attention(torch.randn((40, 4, 32, 128), generator=gen(2), device="cuda").to(torch.bfloat16), *big)
+            decode.filtered_sample(x.repeat(4, 1), u.repeat(4), top_p=0.9)
+            assert all(torch.equal(a, b) for a, b in zip(run(), want))
+            for t in got:
+                t.fill_(-7)
+            graph.replay()
+            side.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
