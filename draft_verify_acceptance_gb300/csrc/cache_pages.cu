@@ -321,7 +321,9 @@ __global__ void __launch_bounds__(256) fork_write_kernel(const ForkArgs a, ForkS
   fork_write(a, s);
 }
 
-// Counts and plan by one block.  The counts come by parent: ends[b][f]
+// Counts and plan by one block (12 us for 64 sequences of up to 1000 tokens, 14
+// for 8 parents of up to 250 pages and 512 sequences: dependent look-ups and
+// scans).  The counts come by parent: ends[b][f]
 // sequences keep f full pages of parent b, so page j of b gains the sum of
 // ends[b][f] over f > j -- one addition a parent's page, however many
 // sequences share it.

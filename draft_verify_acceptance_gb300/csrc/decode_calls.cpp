@@ -13,9 +13,11 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/core/TensorImpl.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAStream.h>
+#include <c10/util/accumulate.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <climits>
@@ -159,6 +161,31 @@ at::Tensor make(at::IntArrayRef size, at::ScalarType type, int device) {
   return at::empty(size, at::TensorOptions().dtype(type).device(at::Device(at::kCUDA, static_cast<c10::DeviceIndex>(device))));
 }
 
+// Several 4-byte results in one allocation (one by one they took a third of a
+// call's host time): tensors that share its storage.
+class Results {
+ public:
+  Results(std::initializer_list<int64_t> sizes, int device) {
+    int64_t total = 0;
+    for (const int64_t n : sizes) total += rounded(n);
+    buffer_ = make({total}, at::kInt, device);
+  }
+  // the next part, in the order of the sizes
+  at::Tensor next(at::IntArrayRef size, at::ScalarType type) {
+    auto impl = c10::make_intrusive<c10::TensorImpl>(c10::TensorImpl::VIEW, c10::Storage(buffer_.storage()),
+                                                     buffer_.key_set(), c10::scalarTypeToTypeMeta(type));
+    impl->set_storage_offset(at_);
+    impl->set_sizes_contiguous(size);
+    at_ += rounded(c10::multiply_integers(size));
+    return at::Tensor(std::move(impl));
+  }
+
+ private:
+  static int64_t rounded(int64_t n) { return (n + 3) & ~static_cast<int64_t>(3); }
+  at::Tensor buffer_;
+  int64_t at_ = 0;
+};
+
 bool number(PyObject* o, float* f) {
   if (!PyFloat_Check(o) && !PyLong_Check(o)) return false;
   const double d = PyFloat_AsDouble(o);
@@ -292,9 +319,9 @@ PyObject* call_fork(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw
   void* ws;
   size_t bytes;
   if (!workspace(1, w, fork_workspace_size(c.pages, C), &ws, &bytes)) return not_done();
-  const at::Tensor table = make({C, t.pages}, at::kInt, w.device), lengths_new = make({C}, at::kInt, w.device),
-                   refs = make({c.pages}, at::kInt, w.device), free = make({c.pages}, at::kInt, w.device),
-                   n_free = make({1}, at::kInt, w.device);
+  Results r({C * t.pages, C, c.pages, c.pages, 1}, w.device);
+  const at::Tensor table = r.next({C, t.pages}, at::kInt), lengths_new = r.next({C}, at::kInt),
+                   refs = r.next({c.pages}, at::kInt), free = r.next({c.pages}, at::kInt), n_free = r.next({1}, at::kInt);
   if (fork_pages(&c, t.p, t.stride, t.pages, lengths, B, parents, keep, C, room, table.data_ptr<int>(),
                  lengths_new.data_ptr<int>(), refs.data_ptr<int>(), free.data_ptr<int>(), n_free.data_ptr<int>(), ws, bytes,
                  reinterpret_cast<spec_stream_t>(w.stream), nullptr) != SPEC_OK)
@@ -317,8 +344,8 @@ PyObject* call_compact(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject*
   if (!cache_of(k, tensor(a[1]), true, w.device, &c) || B > INT_MAX || !table_of(pt, B, w.device, &t) ||
       !workspace(2, w, compact_workspace_size(c.pages), &ws, &bytes))
     return not_done();
-  const at::Tensor table = make({B, t.pages}, at::kInt, w.device), refs = make({c.pages}, at::kInt, w.device),
-                   n_live = make({1}, at::kInt, w.device);
+  Results r({B * t.pages, c.pages, 1}, w.device);
+  const at::Tensor table = r.next({B, t.pages}, at::kInt), refs = r.next({c.pages}, at::kInt), n_live = r.next({1}, at::kInt);
   if (compact(&c, t.p, t.stride, t.pages, B, table.data_ptr<int>(), refs.data_ptr<int>(), n_live.data_ptr<int>(), ws, bytes,
               reinterpret_cast<spec_stream_t>(w.stream), nullptr) != SPEC_OK)
     return not_done();
@@ -375,8 +402,8 @@ PyObject* call_sample(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* 
   size_t bytes;
   if (!workspace(3, w, sample_workspace_size(R, V, dtype), &ws, &bytes)) return not_done();
   const bool filtered = a[6] == Py_True;
-  const at::Tensor tokens = make(rows, at::kInt, w.device), p = make(rows, at::kFloat, w.device),
-                   n_kept = make(rows, at::kInt, w.device);
+  Results r({R, R, R}, w.device);
+  const at::Tensor tokens = r.next(rows, at::kInt), p = r.next(rows, at::kFloat), n_kept = r.next(rows, at::kInt);
   at::Tensor out;
   if (filtered) out = make(x->sizes(), x->scalar_type(), w.device);
   if (sample(x->data_ptr(), stride, u->data_ptr<float>(), R, V, dtype, T, top_k, top_p, min_p, Ts, ks, ps, ms,
