@@ -192,31 +192,30 @@ __global__ void __launch_bounds__(256) fork_count_kernel(const ForkArgs a, ForkS
   }
 }
 
-// Inclusive scan of one int a thread over the block; `total` its sum.
-__device__ __forceinline__ int block_scan(int v, int* scratch, int* total) {
+// Sum of `mine`, one int a warp, over the warps before this one; `total` over
+// all.
+__device__ __forceinline__ int warps_before(int mine, int* scratch, int* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int incl = v;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int o = __shfl_up_sync(0xffffffffu, incl, d);
-    if (lane >= d) incl += o;
-  }
   __syncthreads();
-  if (lane == 31) scratch[warp] = incl;
+  if (lane == 0) scratch[warp] = mine;
   __syncthreads();
-  if (warp == 0) {
-    int x = lane < kPlanThreads / 32 ? scratch[lane] : 0;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int o = __shfl_up_sync(0xffffffffu, x, d);
-      if (lane >= d) x += o;
-    }
-    scratch[lane] = x;
-  }
-  __syncthreads();
-  if (warp > 0) incl += scratch[warp - 1];
-  *total = scratch[kPlanThreads / 32 - 1];
-  return incl;
+  const int x = scratch[lane];  // (32 warps)
+  *total = __reduce_add_sync(0xffffffffu, x);
+  return __reduce_add_sync(0xffffffffu, lane < warp ? x : 0);
+}
+static_assert(kPlanThreads == 32 * 32, "a lane a warp");
+
+// A plan goes through the pages in rounds of kRun * 1024, a warp through kRun
+// times 32 neighbours, a lane a page: what a lane ranks comes from ballots and
+// one scan over the warps, and reads and writes are of neighbours.  (Eight
+// neighbours a thread met bank conflicts and stores of 32 sectors: the plans'
+// kernels took 12.5 us for a fork, 11.7 for a compaction, and take 9.8 and 8.2.)
+constexpr int kRun = 8;
+__device__ __forceinline__ int page_of_run(int p0, int i) {
+  return p0 + (threadIdx.x >> 5) * (32 * kRun) + i * 32 + (threadIdx.x & 31);
+}
+__device__ __forceinline__ int lanes_before(unsigned int ballot) {
+  return __popc(ballot & ((1u << (threadIdx.x & 31)) - 1u));
 }
 
 // From the counts (in shared or global memory): which last pages stay, every
@@ -236,36 +235,42 @@ __device__ void fork_plan(const ForkArgs& a, const ForkSpace& s, const int* refs
       fresh = max(0, ch.need - ch.full - stays);
       a.new_lengths[c] = ch.keep;
     }
-    int sum;
-    const int incl = block_scan(fresh, scratch, &sum);
-    if (c < a.C) s.base[c] = (fresh_total + incl - fresh) | (stays ? INT_MIN : 0);
+    int sum, incl = fresh;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, incl, d);
+      if ((tid & 31) >= d) incl += o;
+    }
+    const int before = warps_before(__shfl_sync(0xffffffffu, incl, 31), scratch, &sum);
+    if (c < a.C) s.base[c] = (fresh_total + before + incl - fresh) | (stays ? INT_MIN : 0);
     fresh_total += sum;
   }
-  // the free pages ascending; the first of them are given out.  A thread takes
-  // kRun neighbours, so that a scan serves kRun * 1024 pages.
-  constexpr int kRun = 8;
+  // the free pages ascending; the first of them are given out
   int before = 0;
   for (int p0 = 0; p0 < P; p0 += kPlanThreads * kRun) {
-    const int q = p0 + tid * kRun;
     int count[kRun], mine = 0;
+    unsigned int free[kRun];
 #pragma unroll
     for (int i = 0; i < kRun; ++i) {
-      count[i] = q + i < P ? refs[q + i] : 1;
-      if (count[i] == 0) count[i] = first[q + i] > 0;
-      mine += count[i] == 0;
+      const int p = page_of_run(p0, i);
+      count[i] = p < P ? refs[p] : 1;
+      if (count[i] == 0) count[i] = first[p] > 0;
+      free[i] = __ballot_sync(0xffffffffu, count[i] == 0);
+      mine += __popc(free[i]);
     }
     int sum;
-    int rank = before + block_scan(mine, scratch, &sum) - mine;
+    int rank = before + warps_before(mine, scratch, &sum);
 #pragma unroll
     for (int i = 0; i < kRun; ++i) {
-      if (q + i >= P) break;
+      const int p = page_of_run(p0, i), at = rank + lanes_before(free[i]);
+      rank += __popc(free[i]);
+      if (p >= P) continue;
       if (count[i] == 0) {
-        s.order[rank] = q + i;
-        if (rank >= fresh_total) a.free_pages[rank - fresh_total] = q + i;
+        s.order[at] = p;
+        if (at >= fresh_total) a.free_pages[at - fresh_total] = p;
         else count[i] = 1;
-        ++rank;
       }
-      a.ref_counts[q + i] = count[i];
+      a.ref_counts[p] = count[i];
     }
     before += sum;
   }
@@ -321,7 +326,7 @@ __global__ void __launch_bounds__(256) fork_write_kernel(const ForkArgs a, ForkS
   fork_write(a, s);
 }
 
-// Counts and plan by one block (12 us for 64 sequences of up to 1000 tokens, 14
+// Counts and plan by one block (10 us for 64 sequences of up to 1000 tokens, and
 // for 8 parents of up to 250 pages and 512 sequences: dependent look-ups and
 // scans).  The counts come by parent: ends[b][f]
 // sequences keep f full pages of parent b, so page j of b gains the sum of
@@ -420,36 +425,40 @@ __device__ void compact_plan(const CompactArgs& a, const CompactSpace& s, const 
   const int tid = threadIdx.x, P = a.cache.pages;
   int mine = 0, n;
   for (int p = tid; p < P; p += kPlanThreads) mine += refs[p] > 0;
-  block_scan(mine, scratch, &n);
-  // movers (in use, at or above n) and holes (free, below n) in one scan: below
-  // n only holes can occur, above it only movers
-  constexpr int kRun = 8;
+  warps_before(__reduce_add_sync(0xffffffffu, mine), scratch, &n);
+  // movers (in use, at or above n) and holes (free, below n) in one scan, the
+  // holes counted in the upper half
+  static_assert(kPlanThreads * kRun < 1 << 15, "both fit");
   int moves = 0, holes = 0;
   for (int p0 = 0; p0 < P; p0 += kPlanThreads * kRun) {
-    const int q = p0 + tid * kRun;
-    int count[kRun], m = 0, h = 0;
+    int count[kRun], both = 0;
+    unsigned int mover[kRun], hole[kRun];
 #pragma unroll
     for (int i = 0; i < kRun; ++i) {
-      count[i] = q + i < P ? refs[q + i] : 0;
-      m += count[i] > 0 && q + i >= n;
-      h += q + i < min(n, P) && count[i] == 0;
+      const int p = page_of_run(p0, i);
+      count[i] = p < P ? refs[p] : 0;
+      mover[i] = __ballot_sync(0xffffffffu, count[i] > 0 && p >= n);
+      hole[i] = __ballot_sync(0xffffffffu, p < min(n, P) && count[i] == 0);
+      both += __popc(mover[i]) + (__popc(hole[i]) << 16);
     }
-    int sum_m = 0, sum_h = 0;
-    int at_m = 0, at_h = 0;
-    if (p0 + kPlanThreads * kRun > n) at_m = moves + block_scan(m, scratch, &sum_m) - m;
-    if (p0 < n) at_h = holes + block_scan(h, scratch, &sum_h) - h;
+    int sum;
+    const int start = warps_before(both, scratch, &sum);
+    int at_m = moves + (start & 0xffff), at_h = holes + (start >> 16);
 #pragma unroll
     for (int i = 0; i < kRun; ++i) {
-      const int p = q + i;
-      if (p >= P) break;
-      const bool mover = count[i] > 0 && p >= n, hole = p < n && count[i] == 0;
-      if (mover) s.from[at_m++] = p;
-      else s.to[p] = p;
-      if (hole) s.holes[at_h++] = p;
-      else a.ref_counts[p] = p < n ? count[i] : 0;
+      const int p = page_of_run(p0, i);
+      const bool moves_it = count[i] > 0 && p >= n, is_hole = p < n && count[i] == 0;
+      if (p < P) {
+        if (moves_it) s.from[at_m + lanes_before(mover[i])] = p;
+        else s.to[p] = p;
+        if (is_hole) s.holes[at_h + lanes_before(hole[i])] = p;
+        else a.ref_counts[p] = p < n ? count[i] : 0;
+      }
+      at_m += __popc(mover[i]);
+      at_h += __popc(hole[i]);
     }
-    moves += sum_m;
-    holes += sum_h;
+    moves += sum & 0xffff;
+    holes += sum >> 16;
   }
   __syncthreads();
   for (int i = tid; i < moves; i += kPlanThreads) {
@@ -471,8 +480,8 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const Compac
 // A group moves at most this many tokens of a page at a time, eight pieces a
 // thread: whole pages (32 KB with 8 heads of 128) shared the work out less
 // evenly (98 us against 97 for a pool of 4096 pages in 4 layers, half in use;
-// now 95: the move alone is 78, its bytes at the copy rate 80, and the plan's
-// block 12 comes before).
+// now 91: the move alone is 78, its bytes at the copy rate 80, and the plan's
+// block 8 comes before).
 __host__ __device__ __forceinline__ int copy_chunk(const CacheView& cv) {
   const int vecs = static_cast<int>(cv.row_bytes() / 16);
   return vecs < 8 * kGroup ? 8 * kGroup / vecs : 1;
