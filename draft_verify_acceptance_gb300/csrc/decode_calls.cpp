@@ -125,8 +125,8 @@ bool table_of(const at::Tensor* t, int64_t B, int device, Table* out) {
   if (M > INT_MAX || (!t->is_contiguous() && M > 1 && t->stride(1) != 1)) return false;
   out->p = static_cast<const int32_t*>(t->data_ptr());
   out->pages = static_cast<int>(M);
-  out->stride = t->is_contiguous() || B <= 1 ? M : std::max<int64_t>(t->stride(0), M);
-  return true;
+  out->stride = t->is_contiguous() || B <= 1 ? M : t->stride(0);
+  return out->stride == 0 || out->stride >= M;
 }
 
 bool cache_of(const at::Tensor* k, const at::Tensor* v, bool layered, int device, spec_cache_t* c) {

@@ -71,7 +71,9 @@ spec_status_t check_cache(const spec_cache_t* c, CacheView* out) {
 }
 
 spec_status_t check_table(const int32_t* ids, int64_t stride, int max_pages, int page_size, PageTable* out) {
-  if (max_pages < 0 || stride < max_pages || (max_pages > 0 && !want32(ids))) return SPEC_ERR_INVALID_ARG;
+  // rows lie apart, or one row (stride 0) holds for every sequence
+  if (max_pages < 0 || stride < 0 || (stride > 0 && stride < max_pages) || (max_pages > 0 && !want32(ids)))
+    return SPEC_ERR_INVALID_ARG;
   // positions are 32-bit
   if (static_cast<int64_t>(max_pages) * page_size > (1ll << 30)) return SPEC_ERR_UNSUPPORTED;
   out->ids = ids;

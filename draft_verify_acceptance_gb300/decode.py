@@ -14,7 +14,8 @@ fallback.  Calls are queued on ``stream`` (default: the current stream); with
 A cache tensor is [pages, page_size, heads, head_dim], or with a leading layers
 dimension for cache_fork and cache_compact; the last two dimensions are contiguous, the
 other strides free (a layer of a larger tensor, K and V interleaved), the same for K
-and V.  A page table is int32 [B, max_pages].
+and V.  A page table is int32 [B, max_pages]; its rows may be strided or one row
+expanded to all sequences, but not overlap otherwise.
 """
 import ctypes
 import threading
@@ -162,7 +163,7 @@ def _ints(t, name, shape, index):
 
 
 def _table(t, B, index):
-    """(pointer, row stride, max_pages) of a page table; its rows may be strided."""
+    """(pointer, row stride, max_pages) of a page table.  Its rows may be strided, or one row expanded to all."""
     if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32:
         raise TypeError("page_table must be an int32 tensor")
     if t.dim() != 2 or t.shape[0] != B or t.get_device() != index:
@@ -172,7 +173,10 @@ def _table(t, B, index):
         return t.data_ptr(), M, M
     if M > 1 and t.stride(1) != 1:
         raise ValueError("page_table rows must be contiguous")
-    return t.data_ptr(), max(t.stride(0), M) if B > 1 else M, M
+    stride = t.stride(0) if B > 1 else M
+    if 0 < stride < M:
+        raise ValueError("page_table rows must not overlap")
+    return t.data_ptr(), stride, M
 
 
 def _cache(k, v, layered, index):

@@ -52,7 +52,8 @@ typedef struct {
  *            contiguous, rows 16-byte aligned), cache's dtype.  Query head h
  *            reads cache head h / (Hq / heads); Hq is a multiple of heads.
  *   cache    one layer (layers == 1), head_dim D 64 or 128.
- *   page_table [B, max_pages] int32, rows table_stride apart: the page of
+ *   page_table [B, max_pages] int32, rows table_stride apart (at least
+ *            max_pages, or 0: one row holds for every sequence): the page of
  *            token t of sequence b is entry t / page_size of row b.  Entries
  *            past the sequence's length are not read.
  *   lengths  [B] int32: tokens of sequence b, the Q new ones included.

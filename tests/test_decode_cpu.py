@@ -90,6 +90,22 @@ def test_attention_refusals(decode):
         assert lib.spec_attention_workspace_size(*bad) == 0
 
 
+def test_page_tables_of_one_row_and_of_overlapping_rows(decode):
+    """One row expanded to every sequence keeps its stride of 0 (read at a stride of its length, the rows after the first
+    would be other memory); rows that overlap otherwise are refused."""
+    one = torch.arange(4, dtype=torch.int32)[None]
+    t = one.expand(3, 4)
+    assert decode._table(t, 3, -1) == (one.data_ptr(), 0, 4)
+    assert decode._table(one, 1, -1) == (one.data_ptr(), 4, 4)
+    assert decode._table(torch.zeros((3, 9), dtype=torch.int32)[:, :4], 3, -1)[1:] == (9, 4)
+    with pytest.raises(ValueError):
+        decode._table(torch.arange(9, dtype=torch.int32).as_strided((3, 4), (2, 1)), 3, -1)
+    lib, c = decode._lib, cache(decode)
+    for stride, code in ((0, decode.OK), (4, decode.OK), (3, decode.ERR_INVALID_ARG), (1, decode.ERR_INVALID_ARG),
+                         (-4, decode.ERR_INVALID_ARG)):
+        assert lib.spec_cache_append(FAKE, FAKE, 128, 0, None, ctypes.byref(c), FAKE, stride, 4, FAKE, 2, None, None) == code
+
+
 def test_append_refusals(decode):
     lib, c = decode._lib, cache(decode)
 

@@ -269,6 +269,39 @@ def test_attention_data_errors(decode, dtype):
     assert (out[2] == 0).all() and torch.isinf(lse[2]).all()
 
 
+@pytest.mark.parametrize("Q", [1, 9])
+def test_one_page_table_row_for_every_sequence(decode, Q):
+    """Continuations that share a prompt's pages: one row expanded gives what its copies give, in every call that takes
+    a table, ordinary or not; rows that overlap otherwise are refused."""
+    S, H, D, N = 16, 2, 128, 5
+    k, v, row, _ = make_cache([400], S, H, D, torch.bfloat16, seed=9, layers=2, spare=40, extra_cols=2400)
+    table, lengths = row.expand(N, -1), i32([400, 17, 90, 0, 399])
+    q = torch.randn((N, Q, 8 * H, D), generator=gen(2), device="cuda").to(torch.bfloat16)
+    for kw in ({}, {"debug": True}):
+        a = decode.paged_attention(q, k[0], v[0], table, lengths, return_lse=True, **kw)
+        b = decode.paged_attention(q, k[0], v[0], table.contiguous(), lengths, return_lse=True, **kw)
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+        new = torch.randn((N, 1, H, D), generator=gen(3), device="cuda").to(torch.bfloat16)
+        pools = [[x.clone() for x in (k[1], v[1])] for _ in range(2)]
+        for pool, t in zip(pools, (table, table.contiguous())):
+            decode.cache_append(new, new, *pool, t, lengths, **kw)
+        assert all(torch.equal(x, y) for x, y in zip(*pools)) and not torch.equal(pools[0][0], k[1])
+        parents, keep = i32([0, 0, 2, 4]), i32([400, 33, 90, 1])
+        pools = [[x.clone() for x in (k, v)] for _ in range(2)]
+        for f in (lambda c, t: decode.cache_fork(*c, t, lengths, parents, keep, 3, **kw)[:5],
+                  lambda c, t: decode.cache_compact(*c, t, **kw)[:3]):
+            a, b = f(pools[0], table), f(pools[1], table.contiguous())
+            assert all(torch.equal(x, y) for x, y in zip(a, b)) and all(torch.equal(x, y) for x, y in zip(*pools))
+    M = table.shape[1]
+    overlap = torch.zeros(M + 4 * N, dtype=torch.int32, device="cuda").as_strided((N, M), (4, 1))
+    for call, args in ((decode.paged_attention, (q, k[0], v[0], overlap, lengths)),
+                       (decode.cache_append, (new, new, k[1], v[1], overlap, lengths)),
+                       (decode.cache_fork, (k, v, overlap, lengths, parents, keep)),
+                       (decode.cache_compact, (k, v, overlap))):
+        with pytest.raises(ValueError):
+            call(*args)
+
+
 def test_attention_offsets_past_32_bits(decode):
     """Pages beyond 2^32 bytes and 2^31 elements of the pool."""
     S, H, D = 16, 8, 128
