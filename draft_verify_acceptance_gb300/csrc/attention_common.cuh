@@ -278,23 +278,25 @@ __device__ void attn_join(const AttnArgs& a, int b, int h, int row0, int rows, l
         const float* s = attn_slot<kRows, D>(a, min(c + y, c1), min(c + y, c1) == c0);
 #pragma unroll
         for (int i = 0; i < kE; ++i) {
-          mc[y][i] = c + y <= c1 ? __ldcg(s + kRows * D + r[i]) : -INFINITY;
+          mc[y][i] = __ldcg(s + kRows * D + r[i]);
           lc[y][i] = __ldcg(s + kRows * D + kRows + r[i]);
           v[y][i] = __ldcg(reinterpret_cast<const float4*>(s + r[i] * D + d[i]));
         }
       }
 #pragma unroll
-      for (int y = 0; y < kC; ++y)
+      for (int y = 0; y < kC; ++y) {
+        if (c + y > c1) break;
 #pragma unroll
         for (int i = 0; i < kE; ++i) {
-          if (mc[y][i] == -INFINITY) continue;
-          const float w = ex2(mc[y][i] - m[i]);
+          // a part without a maximum holds zeros, or NaN that it passes on
+          const float w = mc[y][i] == -INFINITY ? 1.f : ex2(mc[y][i] - m[i]);
           l[i] = fmaf(w, lc[y][i], l[i]);
           o[i].x = fmaf(w, v[y][i].x, o[i].x);
           o[i].y = fmaf(w, v[y][i].y, o[i].y);
           o[i].z = fmaf(w, v[y][i].z, o[i].z);
           o[i].w = fmaf(w, v[y][i].w, o[i].w);
         }
+      }
     }
 #pragma unroll
     for (int i = 0; i < kE; ++i)

@@ -189,6 +189,39 @@ def test_attention_many_rows_repeats(decode, roomy_tables):
             assert all(torch.equal(x, y) for x, y in zip(again, first))
 
 
+def check_nan_in_a_cut_item(decode, dtype, Q, G, D, **kw):
+    """A row of NaN scores, and one NaN key alone in the last tile: whichever part of a sequence that is cut over blocks
+    they fall into (the number of tiles moves the cuts), the rows that see them become NaN, and no others change."""
+    step = 128 if kw else 96 if dtype == torch.float32 and D == 128 else 64
+    for tiles in range(9, 25):
+        n = step * (tiles - 1) + Q
+        k, v, table, lengths = make_cache([n], 16, 2, D, dtype, seed=tiles, **kw)
+        q = torch.randn((1, Q, 2 * G, D), generator=gen(1), device="cuda").to(dtype)
+        clean = decode.paged_attention(q, k, v, table, lengths, return_lse=True)
+        q2 = q.clone()
+        q2[0, Q - 1, G - 1, 3] = math.nan
+        out, lse = decode.paged_attention(q2, k, v, table, lengths, return_lse=True)
+        assert torch.isnan(out[0, Q - 1, G - 1]).all() and torch.isnan(lse[0, Q - 1, G - 1]), tiles
+        out[0, Q - 1, G - 1], lse[0, Q - 1, G - 1] = clean[0][0, Q - 1, G - 1], clean[1][0, Q - 1, G - 1]
+        assert torch.equal(out, clean[0]) and torch.equal(lse, clean[1])
+        k2 = k.clone()
+        k2[table[0, (n - Q) // 16], (n - Q) % 16, 1, 7] = math.nan  # the last tile's first token, seen by every query
+        out, lse = decode.paged_attention(q, k2, v, table, lengths, return_lse=True)
+        assert torch.isnan(out[0, :, G:]).all() and torch.isnan(lse[0, :, G:]).all(), tiles
+        assert torch.equal(out[0, :, :G], clean[0][0, :, :G]) and torch.equal(lse[0, :, :G], clean[1][0, :, :G])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("Q,G,D", [(1, 1, 64), (1, 4, 128), (3, 4, 128), (3, 8, 64)])
+def test_attention_nan_in_a_cut_item(decode, dtype, Q, G, D):
+    check_nan_in_a_cut_item(decode, dtype, Q, G, D)
+
+
+@pytest.mark.parametrize("Q,G", [(1, 32), (9, 8)])
+def test_attention_many_rows_nan_in_a_cut_item(decode, Q, G):
+    check_nan_in_a_cut_item(decode, torch.bfloat16, Q, G, 128, extra_cols=10000)
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_attention_layouts(decode, dtype):
     """Query from a fused projection, K and V interleaved by page, a layer of a larger cache, a table of
