@@ -455,11 +455,13 @@ __global__ void __launch_bounds__(Ring<E, D, NB>::kWarps * 32, Ring<E, D, NB>::k
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
               float p[2];
+              bool sees[2];  // a weight of 0 says nothing: it may have underflowed
 #pragma unroll
               for (int x = 0; x < 2; ++x) {
                 const float lo = __shfl_sync(0xffffffffu, s[nb][x], from);
                 const float hi = __shfl_sync(0xffffffffu, s[nb][x + 2], from);
                 p[x] = t < 8 ? lo : hi;
+                sees[x] = t0 + t <= limit[nb][x];
               }
 #pragma unroll
               for (int mt = 0; mt < KS; ++mt)
@@ -468,8 +470,8 @@ __global__ void __launch_bounds__(Ring<E, D, NB>::kWarps * 32, Ring<E, D, NB>::k
                   const int d = dim_of<E>(mt, y, g), chunk = d * E::kBytes / 16;
                   const float v = shared_value<E>(vat + t * kRow + v_place<E>(chunk, t) * 16 + d * E::kBytes % 16);
                   if (!isfinite(v)) {
-                    if (p[0] != 0.f) o[mt][nb][y * 2] += p[0] * v;
-                    if (p[1] != 0.f) o[mt][nb][y * 2 + 1] += p[1] * v;
+                    if (sees[0]) o[mt][nb][y * 2] += p[0] * v;
+                    if (sees[1]) o[mt][nb][y * 2 + 1] += p[1] * v;
                   }
                 }
             }

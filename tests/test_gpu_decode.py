@@ -150,6 +150,37 @@ def test_attention_unseen_tokens_do_not_matter(decode, dtype, Q, G, D):
     assert torch.isfinite(o).all() and torch.isfinite(l[1]).all()
 
 
+def check_nonfinite_values_of_no_weight(decode, dtype, Q, G, D, **kw):
+    """A value that is not finite reaches the rows that see its token also where its weight is too small for 32 bits,
+    among the last tokens (which some rows do not see) as before them."""
+    n = 333
+    k, v, table, lengths = make_cache([n], 16, 2, D, dtype, seed=3, **kw)
+    q = torch.randn((1, Q, 2 * G, D), generator=gen(1), device="cuda").abs().to(dtype)
+    for t in (5, n - Q, n - 2, n - 1):
+        k2 = k.clone()
+        k2[table[0, t // 16], t % 16] = -1e4
+        clean = decode.paged_attention(q, k2, v, table, lengths)
+        for bad in (math.inf, -math.inf, math.nan):
+            v2 = v.clone()
+            v2[table[0, t // 16], t % 16, 1, 3] = bad
+            out = decode.paged_attention(q, k2, v2, table, lengths)
+            sees = max(0, t - (n - Q))
+            assert not torch.isfinite(out[0, sees:, G:, 3]).any(), (t, bad)
+            out[0, sees:, G:, 3] = clean[0, sees:, G:, 3]
+            assert torch.equal(out, clean), (t, bad)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("Q,G,D", [(4, 4, 64), (3, 4, 128)])
+def test_attention_nonfinite_values_of_no_weight(decode, dtype, Q, G, D):
+    check_nonfinite_values_of_no_weight(decode, dtype, Q, G, D)
+
+
+@pytest.mark.parametrize("Q,G", [(4, 8), (9, 8)])
+def test_attention_many_rows_nonfinite_values_of_no_weight(decode, Q, G):
+    check_nonfinite_values_of_no_weight(decode, torch.bfloat16, Q, G, 128, extra_cols=10000)
+
+
 @pytest.fixture
 def roomy_tables(monkeypatch):
     """Page tables with room for many tokens, which with many rows a cache head are read by another kernel."""
