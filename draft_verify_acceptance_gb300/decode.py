@@ -24,8 +24,12 @@ from typing import NamedTuple
 import torch
 
 from . import _decode_calls
-from .binding import (DTYPE_BF16, DTYPE_F32, ERR_INVALID_ARG, ERR_UNSUPPORTED, MAX_V, OK, SpecVerifyError,
-                      _lib)
+from .binding import (DTYPE_BF16, DTYPE_F32, ERR_INVALID_ARG, ERR_UNSUPPORTED, LIB_PATH, MAX_V, OK,
+                      SpecVerifyError)
+
+# Most calls are several launches on one kept workspace, and threads on one stream share it.  So a call keeps
+# the interpreter's lock from its first launch to its last (PyDLL), as the native ones do.
+_lib = ctypes.PyDLL(LIB_PATH)
 
 DATA_PAGE_RANGE = 64
 DATA_LENGTH_RANGE = 128

@@ -106,6 +106,13 @@ def test_page_tables_of_one_row_and_of_overlapping_rows(decode):
         assert lib.spec_cache_append(FAKE, FAKE, 128, 0, None, ctypes.byref(c), FAKE, stride, 4, FAKE, 2, None, None) == code
 
 
+def test_library_calls_keep_the_interpreter_s_lock(decode):
+    """A call's launches share a workspace with other threads' calls on the stream, so none may come between them."""
+    python_api = 4  # FUNCFLAG_PYTHONAPI: the lock is not released around the call
+    for n in decode.EXPORTS:
+        assert getattr(decode._lib, n)._flags_ & python_api, n
+
+
 def test_append_refusals(decode):
     lib, c = decode._lib, cache(decode)
 

@@ -10,6 +10,7 @@ whose whole-number weights are rounded by 2^-22 at most.
 """
 import math
 import sys
+import threading
 
 import numpy as np
 import pytest
@@ -821,6 +822,46 @@ def test_ordinary_calls_and_others_agree(decode):
                            (calls.filtered_sample, (x, u, 1.0, 5), {}), (calls.filtered_sample, (x[..., :0], u), {}),
                            (calls.filtered_sample, (x[..., ::2], u), {})):
         assert call(*args, **kw) is NotImplemented, (call, kw)
+
+
+def test_threads_on_one_stream(decode):
+    """Four threads make calls of several launches on the same stream and kept workspaces, ordinary ones and others: each
+    gets its own results."""
+    def job(seed):
+        rng = np.random.RandomState(seed)
+        lens = rng.randint(1, 400, 12).tolist()
+        k, v, table, lengths = make_cache(lens, 16, 1, 64, torch.float32, seed=seed, spare=90, extra_cols=3)
+        parents = rng.randint(0, 12, 30).tolist()
+        keep = [int(rng.randint(0, lens[p] + 1)) for p in parents]
+        x = (torch.randn((330, 1000 + seed), generator=gen(seed), device="cuda") * 3).to(torch.bfloat16)
+        u = torch.rand(330, generator=gen(seed), device="cuda")
+        q = torch.randn((12, 1, 4, 64), generator=gen(seed), device="cuda")
+        parents, keep = i32(parents), i32(keep)
+
+        def run(**kw):
+            k2, v2 = k.clone(), v.clone()
+            f = decode.cache_fork(k2, v2, table, lengths, parents, keep, 5, **kw)
+            c = decode.cache_compact(k2, v2, f.page_table, **kw)
+            s = decode.filtered_sample(x, u, 0.9, top_p=0.8, return_filtered=True, **kw)
+            a = decode.paged_attention(q, k, v, table, lengths, return_lse=True, **kw)
+            return [k2, v2, *f[:5], *c[:3], *s[:4], *a[:2]]
+        return run
+    jobs = [job(seed) for seed in range(4)]
+    want = [run() for run in jobs]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(run, want):
+        for i in range(60):
+            got = run(debug=True) if i % 2 else run()
+            if not all(torch.equal(a, b) for a, b in zip(got, want)):
+                wrong.append(i)
+    threads = [threading.Thread(target=work, args=a) for a in zip(jobs, want)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
 
 
 def test_calls_in_a_graph_own_their_workspaces(decode):
