@@ -389,7 +389,7 @@ __device__ __forceinline__ float logit_of(unsigned long long cut) {
 // What every rank of a cluster publishes to all.
 struct Exchange {
   float max[kMaxCS], tau[kMaxCS];  // tau: sum of the warps' order statistics, taus of them
-  int taus[kMaxCS], listed[kMaxCS];
+  int taus[kMaxCS], listed[kMaxCS], lost[kMaxCS];  // lost: a copy never landed
   unsigned long long sum[kMaxCS], listed_sum[kMaxCS];
   unsigned long long mass[kMaxCS], count[kMaxCS];
 };
@@ -788,7 +788,7 @@ __device__ int group_draw(const Ctx& c, const Slice<E, kStaged>& sl, const unsig
         rem -= __shfl_sync(0xffffffffu, incl, 31);
       }
     }
-    int token = sl.first;  // (only a timed-out load leaves no crossing)
+    int token = sl.first;
     // the vector in the group, the element in the vector
     for (int i = 0; i < sl.width && group >= 0; ++i) {
       const int v = (group * sl.width + i) * 32 + lane;
@@ -1221,6 +1221,10 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
       sh.wmax[warp] = odd ? INFINITY : sorted;
       sh.wtau[warp] = order;
     }
+#ifdef SPEC_DEBUG
+    // (a test's way to a wait that ran out: this NaN as the row's uniform)
+    if (__float_as_uint(u) == 0x7fc0d000u + c.rank) landed = false;
+#endif
     const int timeout = __syncthreads_or(!landed);
     if (c.C > 1) cluster_wait();  // every block of the cluster has started
     if (tid < c.C) {
@@ -1237,18 +1241,20 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
       *c.at(&ex.max[c.rank], tid) = m;
       *c.at(&ex.tau[c.rank], tid) = t;
       *c.at(&ex.taus[c.rank], tid) = n;
+      *c.at(&ex.lost[c.rank], tid) = timeout;
     }
     c.sync();
     float M = -INFINITY, tau = 0.f;
-    int taus = 0;
+    int taus = 0, lost = 0;  // lost: the row has no result (every block of the cluster goes the same way)
     for (int r = 0; r < c.C; ++r) {
+      lost |= ex.lost[r];
       M = fmaxf(M, ex.max[r]);
       tau += ex.tau[r];
       taus += ex.taus[r];
     }
     tau = taus ? fminf(tau / taus, M) : -INFINITY;
     M += 0.f;
-    const bool good = M > -INFINITY && M < INFINITY;
+    const bool good = !lost && M > -INFINITY && M < INFINITY;
     Kept kept;
     kept.cut = ~0ull;
     kept.least = sh.least;
@@ -1261,7 +1267,7 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
     head.written = 0;
     bool later = false;  // for the whole-row kernel
 
-    if (good && cuts && kStaged && !timeout) {
+    if (good && cuts && kStaged) {
       // ---- list, and approximate sum of the rest ----
       // below `floor` every weight is 0, below `least_x` under min-p's share
       // (with room for the roundings of t and of the polynomial, and for
@@ -1459,7 +1465,7 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
     if (tid == 0 && !(kWhole && queue)) {  // (the list kernel has reported a queued row's)
       int bad = timeout ? kWaitTimeout : 0;
       if (c.rank == 0) {
-        bad |= set.bad | (good ? 0 : kDataNonfiniteLogit);
+        bad |= set.bad | (good || lost ? 0 : kDataNonfiniteLogit);
         if (!(u >= 0.f && u < 1.f)) bad |= kDataUniformRange;
       }
       if (bad && a.status) atomicOr(a.status, bad);

@@ -176,7 +176,9 @@ SPEC_API spec_status_t spec_cache_compact(
  *            calls: NULL), zero-filled once; every call leaves it fit for the
  *            next.  One call at a time.
  * A row with a NaN or +inf or without a finite logit is
- * SPEC_DATA_NONFINITE_LOGIT: token 0, p 0, n_kept 0, filtered -inf.
+ * SPEC_DATA_NONFINITE_LOGIT: token 0, p 0, n_kept 0, filtered -inf.  A row
+ * whose copy into shared memory did not land within the kernel's limit on its
+ * waits (SPEC_DEVICE_WAIT_TIMEOUT) gets the same.
  */
 SPEC_API size_t spec_filtered_sample_workspace_size(int R, int V, int dtype);
 SPEC_API spec_status_t spec_filtered_sample(

@@ -1,0 +1,68 @@
+"""Waits of the sampler that run out, without a fault: in the -DSPEC_DEBUG variant of the library a row whose uniform is
+a certain NaN is taken for one whose copy never landed on one block of its cluster.  The row gets no result, the status word
+says so, and the other rows are right."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+WAIT_TIMEOUT, UNIFORM_RANGE = 8, 4
+
+
+@pytest.fixture(scope="module")
+def libs():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import __graft_entry__
+    __graft_entry__.build()
+    from draft_verify_acceptance_gb300 import build, decode
+    dbg = ctypes.CDLL(build.build(debug=True))
+    for name in ("spec_filtered_sample", "spec_filtered_sample_workspace_size"):
+        for attr in ("restype", "argtypes"):
+            setattr(getattr(dbg, name), attr, getattr(getattr(decode._lib, name), attr))
+    return dbg, decode
+
+
+def call(lib, x, u, T, k, p, m, ws=None):
+    R, V = x.shape
+    dt = 1 if x.dtype == torch.bfloat16 else 0
+    tokens, n_kept, status = (torch.full((n,), -5, dtype=torch.int32, device="cuda") for n in (R, R, 1))
+    status.zero_()
+    prob, out = torch.full((R,), -5.0, device="cuda"), torch.full_like(x, 5.0)
+    need = lib.spec_filtered_sample_workspace_size(R, V, dt)
+    ws = torch.zeros(max(need, 16), dtype=torch.uint8, device="cuda") if ws is None else ws
+    rc = lib.spec_filtered_sample(x.data_ptr(), V, u.data_ptr(), R, V, dt, T, k, p, m, None, None, None, None,
+                                  tokens.data_ptr(), prob.data_ptr(), n_kept.data_ptr(), out.data_ptr(),
+                                  ws.data_ptr() if need else None, need, None, status.data_ptr())
+    assert rc == 0
+    torch.cuda.synchronize()
+    return tokens, prob, n_kept, out, int(status), ws
+
+
+SETTINGS = [(1.0, 0, 1.0, 0.0), (0.8, 0, 0.9, 0.0), (1.0, 40, 0.95, 0.0), (1.0, 0, 1.0, 0.05)]
+
+
+@pytest.mark.parametrize("R,V", [(4, 128256), (200, 128256), (400, 1000)])  # the whole-row kernel; the list kernel
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_a_row_whose_copy_is_lost_on_one_block(libs, R, V, dtype):
+    lib, decode = libs
+    g = torch.Generator(device="cuda").manual_seed(R)
+    x = (torch.randn((R, V), generator=g, device="cuda") * 3).to(dtype)
+    u = torch.rand(R, generator=g, device="cuda")
+    for s in SETTINGS:
+        want = call(lib, x, u, *s)
+        plain = decode.filtered_sample(x, u, s[0], top_k=s[1], top_p=s[2], min_p=s[3], return_filtered=True)
+        assert want[4] == 0 and all(torch.equal(a, b) for a, b in zip(want, plain[:4]))
+        lost = {R - 3: 0} if V < 2000 else {1: 2, R - 1: 0}
+        u2 = u.clone()
+        for row, rank in lost.items():
+            u2.view(torch.int32)[row] = 0x7fc0d000 + rank
+        got = call(lib, x, u2, *s)
+        assert got[4] == WAIT_TIMEOUT | UNIFORM_RANGE
+        rest = [r for r in range(R) if r not in lost]
+        assert all(torch.equal(a[rest], b[rest]) for a, b in zip(got[:4], want[:4]))
+        for row in lost:
+            assert (int(got[0][row]), float(got[1][row]), int(got[2][row])) == (0, 0.0, 0)
+            assert (got[3][row] == -math.inf).all()
