@@ -1222,8 +1222,8 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
       sh.wtau[warp] = order;
     }
 #ifdef SPEC_DEBUG
-    // (a test's way to a wait that ran out: this NaN as the row's uniform)
-    if (__float_as_uint(u) == 0x7fc0d000u + c.rank) landed = false;
+    // (a test's way to a wait that ran out: one NaN as the row's uniform, another for its turn in the queue)
+    if (__float_as_uint(u) == (kWhole && queue ? 0x7fc0e000u : 0x7fc0d000u) + c.rank) landed = false;
 #endif
     const int timeout = __syncthreads_or(!landed);
     if (c.C > 1) cluster_wait();  // every block of the cluster has started
@@ -1462,9 +1462,9 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
       head.written = later;
       heads[at] = head;
     }
-    if (tid == 0 && !(kWhole && queue)) {  // (the list kernel has reported a queued row's)
+    if (tid == 0) {
       int bad = timeout ? kWaitTimeout : 0;
-      if (c.rank == 0) {
+      if (c.rank == 0 && !(kWhole && queue)) {  // (the list kernel has reported a queued row's data and settings)
         bad |= set.bad | (good || lost ? 0 : kDataNonfiniteLogit);
         if (!(u >= 0.f && u < 1.f)) bad |= kDataUniformRange;
       }

@@ -66,3 +66,29 @@ def test_a_row_whose_copy_is_lost_on_one_block(libs, R, V, dtype):
         for row in lost:
             assert (int(got[0][row]), float(got[1][row]), int(got[2][row])) == (0, 0.0, 0)
             assert (got[3][row] == -math.inf).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_a_queued_row_whose_copy_is_lost(libs, dtype):
+    """Flat rows among others go to the whole-row kernel by a queue: one lost there is reported too."""
+    lib, decode = libs
+    R, V = 400, 40000
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randn((R, V), generator=g, device="cuda") * 3
+    x[7::15] *= 0.1
+    x = x.to(dtype)
+    u = torch.rand(R, generator=g, device="cuda")
+    want = call(lib, x, u, 1.0, 0, 0.9, 0.0)
+    plain = decode.filtered_sample(x, u, 1.0, top_p=0.9, return_filtered=True)
+    assert want[4] == 0 and all(torch.equal(a, b) for a, b in zip(want, plain[:4]))
+    row = 7 + 15 * 9
+    u.view(torch.int32)[row] = 0x7fc0e000 + 1
+    got = call(lib, x, u, 1.0, 0, 0.9, 0.0)
+    assert got[4] == WAIT_TIMEOUT | UNIFORM_RANGE
+    rest = [r for r in range(R) if r != row]
+    assert all(torch.equal(a[rest], b[rest]) for a, b in zip(got[:4], want[:4]))
+    assert (int(got[0][row]), float(got[1][row]), int(got[2][row])) == (0, 0.0, 0)
+    assert (got[3][row] == -math.inf).all()
+    # the queue is as it was: the next call on this workspace is right
+    u.view(torch.int32)[row] = 0
+    assert call(lib, x, u, 1.0, 0, 0.9, 0.0, got[5])[4] == 0
