@@ -406,6 +406,7 @@ struct Shared {
   float u, s;
   unsigned long long least;
   int lane_of_tau;
+  int stuck;  // copies never landed: the barriers' phases are lost, so no later row is copied
 };
 
 // 256 bins of weights, kept as 32-bit parts so that shared memory adds them
@@ -1110,6 +1111,15 @@ __device__ unsigned long long finish_row(const Ctx& c, const SampleArgs& a, cons
   return top;
 }
 
+// A block that gave up on a row's copies waits for them once more, with the
+// same limit: none may land after the block has left, or in the next row's
+// slice.  True where some did not.
+__device__ __noinline__ bool never_landed(unsigned long long* bars, int nch, uint32_t parity) {
+  for (int k = 0; k < nch; ++k)
+    if (!mbar_wait_sleep(&bars[k], parity)) return true;
+  return false;
+}
+
 // The list kernel (kWhole false: cluster i takes row row0 + i) and the
 // whole-row kernel (clusters take rows of the queue, or row i without one).
 template <typename E, bool kStaged, bool kWhole>
@@ -1145,6 +1155,7 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
   sl.width = kStaged ? 1 : max(1, (sl.nv + kThreadsS * kGroups - 1) / (kThreadsS * kGroups));
   const int nch = (sl.nv + kChunkS - 1) / kChunkS;
   const bool bulk = kStaged && aligned_in;
+  if (tid == 0) sh.stuck = 0;
   if (bulk && tid == 0) {
     for (int k = 0; k < nch; ++k) mbar_init(&bars[k], 1);
     fence_barrier_init();
@@ -1167,7 +1178,7 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
 
     // ---- the slice into shared memory -----------------------------------
     if (bulk) {
-      if (tid == 0) {
+      if (tid == 0 && !(kWhole && sh.stuck)) {
         for (int k = 0; k < nch; ++k) {
           const uint32_t bytes = min(kChunkS, sl.nv - k * kChunkS) * 16u;
           mbar_arrive_expect_tx(&bars[k], bytes);
@@ -1198,9 +1209,13 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
     if (c.C > 1) cluster_arrive_relaxed();  // matched before the first store to another block
 
     // ---- the row's maximum and the list's threshold ------------------------
-    bool landed = true;
+    bool landed = !(kWhole && sh.stuck);
+#ifdef SPEC_DEBUG
+    // (a test's way to a wait that ran out: one NaN as the row's uniform, another for its turn in the queue)
+    if (__float_as_uint(u) == (kWhole && queue ? 0x7fc0e000u : 0x7fc0d000u) + c.rank) landed = false;
+#endif
     Peak<E> peak;
-    if (bulk) {
+    if (bulk && landed) {
       for (int k = 0; k < nch; ++k) {
         if (!mbar_wait_sleep(&bars[k], turn & 1)) {
           landed = false;
@@ -1210,7 +1225,7 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
 #pragma unroll 4
         for (int v = k * kChunkS + tid; v < stop; v += kThreadsS) peak.take(slice[v]);
       }
-    } else {
+    } else if (!bulk) {
       for (int v = tid; v < sl.nv; v += kThreadsS) peak.take(sl.at(v));
     }
     const float mine = peak.value();
@@ -1221,11 +1236,8 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
       sh.wmax[warp] = odd ? INFINITY : sorted;
       sh.wtau[warp] = order;
     }
-#ifdef SPEC_DEBUG
-    // (a test's way to a wait that ran out: one NaN as the row's uniform, another for its turn in the queue)
-    if (__float_as_uint(u) == (kWhole && queue ? 0x7fc0e000u : 0x7fc0d000u) + c.rank) landed = false;
-#endif
     const int timeout = __syncthreads_or(!landed);
+    if (timeout && bulk && tid == 0 && !sh.stuck) sh.stuck = never_landed(bars, nch, turn & 1);
     if (c.C > 1) cluster_wait();  // every block of the cluster has started
     if (tid < c.C) {
       float m = -INFINITY, t = 0.f;

@@ -92,3 +92,23 @@ def test_a_queued_row_whose_copy_is_lost(libs, dtype):
     # the queue is as it was: the next call on this workspace is right
     u.view(torch.int32)[row] = 0
     assert call(lib, x, u, 1.0, 0, 0.9, 0.0, got[5])[4] == 0
+
+
+def test_rows_after_a_lost_one(libs):
+    """Clusters that take several queued rows each: a block that gave up waits for its copies before the next row's, so
+    the rows after a lost one are right."""
+    lib, decode = libs
+    R, V = 600, 40000
+    g = torch.Generator(device="cuda").manual_seed(6)
+    x = (torch.randn((R, V), generator=g, device="cuda") * 0.3).to(torch.bfloat16)
+    u = torch.rand(R, generator=g, device="cuda")
+    want = call(lib, x, u, 1.0, 0, 0.9, 0.0)
+    assert want[4] == 0
+    lost = list(range(3, R, 97))
+    for i, row in enumerate(lost):
+        u.view(torch.int32)[row] = 0x7fc0e000 + i % 4
+    got = call(lib, x, u, 1.0, 0, 0.9, 0.0)
+    assert got[4] == WAIT_TIMEOUT | UNIFORM_RANGE
+    rest = [r for r in range(R) if r not in lost]
+    assert all(torch.equal(a[rest], b[rest]) for a, b in zip(got[:4], want[:4]))
+    assert (got[2][lost] == 0).all() and (got[3][lost] == -math.inf).all()
