@@ -1,8 +1,11 @@
-"""Waits of the sampler that run out, without a fault: in the -DSPEC_DEBUG variant of the library a row whose uniform is
-a certain NaN is taken for one whose copy never landed on one block of its cluster.  The row gets no result, the status word
-says so, and the other rows are right."""
+"""Waits of the decode-side kernels that run out, without a fault, in the -DSPEC_DEBUG variant of the library.
+
+Sampling: a row whose uniform is a certain NaN is taken for one whose copy never landed on one block of its cluster.  The
+row gets no result, the status word says so, and the other rows are right.  Attention on tcgen05: a bit of the status word
+that the call passes makes the first block's first wait run out.  The call ends, says so, and the next one is right."""
 import ctypes
 import math
+import time
 
 import pytest
 import torch
@@ -19,7 +22,7 @@ def libs():
     __graft_entry__.build()
     from draft_verify_acceptance_gb300 import build, decode
     dbg = ctypes.CDLL(build.build(debug=True))
-    for name in ("spec_filtered_sample", "spec_filtered_sample_workspace_size"):
+    for name in ("spec_filtered_sample", "spec_filtered_sample_workspace_size", "spec_paged_attention"):
         for attr in ("restype", "argtypes"):
             setattr(getattr(dbg, name), attr, getattr(getattr(decode._lib, name), attr))
     return dbg, decode
@@ -112,3 +115,34 @@ def test_rows_after_a_lost_one(libs):
     rest = [r for r in range(R) if r not in lost]
     assert all(torch.equal(a[rest], b[rest]) for a, b in zip(got[:4], want[:4]))
     assert (got[2][lost] == 0).all() and (got[3][lost] == -math.inf).all()
+
+
+def test_attention_on_tcgen05_ends_after_a_wait_that_ran_out(libs):
+    lib, decode = libs
+    B, Q, Hq, H, D, S, n = 3, 9, 32, 4, 128, 16, 3000
+    g = torch.Generator(device="cuda").manual_seed(7)
+    pages = -(-n // S)
+    k, v = (torch.randn((B * pages, S, H, D), generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    table = torch.randperm(B * pages, generator=g, device="cuda").to(torch.int32).view(B, pages)
+    table = torch.cat([table, torch.full((B, 2000), -1, dtype=torch.int32, device="cuda")], 1)
+    lengths = torch.tensor([n, 1, n - 7], dtype=torch.int32, device="cuda")
+    q = torch.randn((B, Q, Hq, D), generator=g, device="cuda").to(torch.bfloat16)
+    want = decode.paged_attention(q, k, v, table, lengths)
+    c = decode._Cache(k.data_ptr(), v.data_ptr(), 0, S * H * D, H * D, 1, B * pages, S, H, D, 1)
+    need = decode.attention_workspace_size(B, Q, Hq, H, D, q.dtype)
+
+    def run(bit):
+        out, ws = torch.empty_like(q), torch.zeros(need, dtype=torch.uint8, device="cuda")
+        status = torch.tensor([bit], dtype=torch.int32, device="cuda")
+        torch.cuda.synchronize()
+        t0 = time.perf_counter()
+        rc = lib.spec_paged_attention(q.data_ptr(), Q * Hq * D, Hq * D, D, ctypes.byref(c), table.data_ptr(), table.shape[1],
+                                      table.shape[1], lengths.data_ptr(), B, Q, Hq, D ** -0.5, out.data_ptr(), None,
+                                      ws.data_ptr(), need, None, status.data_ptr())
+        torch.cuda.synchronize()
+        assert rc == 0 and time.perf_counter() - t0 < 5.0
+        return out, int(status)
+    for _ in range(3):
+        assert run(1 << 30)[1] == 1 << 30 | WAIT_TIMEOUT
+        out, status = run(0)
+        assert status == 0 and torch.equal(out, want)
