@@ -25,11 +25,30 @@ CALLS = os.path.join(HERE, "_decode_calls.so")
 CALLS_SOURCE = "decode_calls.cpp"
 
 
-def build_calls(force: bool = False) -> str:
-    """Compile _decode_calls.so against the installed torch if its source is newer than it."""
-    src = os.path.join(CSRC, CALLS_SOURCE)
+CALLS_FOR = os.path.join(BUILD, "decode_calls.txt")  # what _decode_calls.so was compiled against
+
+
+def _calls_abi():
+    """The torch and the interpreter whose layouts _decode_calls.so has in it."""
+    import torch
+    return f"torch {torch.__version__}, {sysconfig.get_config_var('SOABI')}"
+
+
+def _calls_fresh(src):
     deps = [src, os.path.join(ROOT, "include", "spec_decode.h"), os.path.abspath(__file__)]
-    if not force and os.path.exists(CALLS) and all(os.path.getmtime(f) <= os.path.getmtime(CALLS) for f in deps):
+    if not os.path.exists(CALLS) or any(os.path.getmtime(f) > os.path.getmtime(CALLS) for f in deps):
+        return False
+    if not os.path.exists(CALLS_FOR):
+        return False
+    with open(CALLS_FOR) as f:
+        return f.read() == _calls_abi()
+
+
+def build_calls(force: bool = False) -> str:
+    """Compile _decode_calls.so against the installed torch if its source is newer than it, or it is for another torch
+    or interpreter."""
+    src = os.path.join(CSRC, CALLS_SOURCE)
+    if not force and _calls_fresh(src):
         return CALLS
     import torch
     home = os.path.dirname(torch.__file__)
@@ -43,7 +62,12 @@ def build_calls(force: bool = False) -> str:
                         "-ltorch_cpu", "-ltorch_python", f"-Wl,-rpath,{lib}"], capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {CALLS_SOURCE}:\n{r.stdout}\n{r.stderr}")
+    os.makedirs(BUILD, exist_ok=True)
+    if os.path.exists(CALLS_FOR):
+        os.remove(CALLS_FOR)  # (until the new file is there it holds for neither)
     os.replace(tmp, CALLS)
+    with open(CALLS_FOR, "w") as f:
+        f.write(_calls_abi())
     return CALLS
 
 

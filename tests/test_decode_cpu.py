@@ -36,6 +36,24 @@ def test_exports_and_constants(decode):
     assert not set(taken) & set(defs.values())
 
 
+def test_native_calls_are_rebuilt_for_another_torch(decode, monkeypatch):
+    """_decode_calls.so has torch's and the interpreter's layouts in it: one made for others is not kept."""
+    from draft_verify_acceptance_gb300 import build
+    runs = []
+
+    def run(cmd, **kw):
+        runs.append(cmd)
+        return subprocess.CompletedProcess(cmd, 1, "", "not now")
+    monkeypatch.setattr(build.subprocess, "run", run)
+    assert build.build_calls() == build.CALLS and not runs
+    for name, value in (("CALLS_FOR", build.CALLS_FOR + ".none"), ("_calls_abi", lambda: "torch 1.0, cpython-39")):
+        with monkeypatch.context() as m:
+            m.setattr(build, name, value, raising=False)
+            with pytest.raises(RuntimeError):
+                build.build_calls()
+    assert len(runs) == 2 and os.path.exists(build.CALLS)
+
+
 def test_header_is_plain_c(tmp_path):
     f = tmp_path / "h.c"
     f.write_text('#include "spec_decode.h"\nint main(void) { spec_cache_t c; (void)c; return 0; }\n')
