@@ -1595,6 +1595,7 @@ static_assert(sizeof(Bins) <= kPlaceBytes && 2 * sizeof(ListBins) <= sizeof(Bins
               "they share the places' memory");
 
 // Workspace: the queue, its rows, a head and a list per row.
+static_assert(sizeof(Queue) <= kQueueBytes, "the queue's place");
 struct Space {
   Queue* queue;
   int* queued;
@@ -1607,10 +1608,10 @@ Space space_of(void* ws, int R) {
   Space s;
   char* p = static_cast<char*>(ws);
   s.queue = reinterpret_cast<Queue*>(p);
-  s.lists = reinterpret_cast<uint4*>(p + 64);
-  s.heads = reinterpret_cast<RowHead*>(p + 64 + rows * kListBytes);
-  s.queued = reinterpret_cast<int*>(p + 64 + rows * (kListBytes + sizeof(RowHead)));
-  s.bytes = (64 + rows * (kListBytes + sizeof(RowHead) + 4) + 255) & ~static_cast<size_t>(255);
+  s.lists = reinterpret_cast<uint4*>(p + kQueueBytes);
+  s.heads = reinterpret_cast<RowHead*>(p + kQueueBytes + rows * kListBytes);
+  s.queued = reinterpret_cast<int*>(p + kQueueBytes + rows * (kListBytes + sizeof(RowHead)));
+  s.bytes = (kQueueBytes + rows * (kListBytes + sizeof(RowHead) + 4) + 255) & ~static_cast<size_t>(255);
   return s;
 }
 

@@ -13,6 +13,9 @@ namespace {
 using specv::CacheView;
 using specv::PageTable;
 
+static_assert(specv::kAttnMaxCtas * 4 == SPEC_ATTENTION_ZERO_BYTES, "the arrival counters");
+static_assert(specv::kQueueBytes == SPEC_SAMPLE_ZERO_BYTES, "the queue");
+
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 bool want32(const void* p) { return p && aligned(p, 4); }  // a required array of 32-bit values
 bool may32(const void* p) { return aligned(p, 4); }        // an optional one

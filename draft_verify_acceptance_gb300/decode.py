@@ -71,7 +71,8 @@ _declare()
 _DTYPES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
 _ws_lock = threading.Lock()
 _ws = {}
-_KINDS = {"attention": 0, "fork": 1, "compact": 2, "sample": 3}
+# the native calls' number of a kind of workspace, and how many of its first bytes are zero between calls
+_KINDS = {"attention": (0, 2048), "fork": (1, 0), "compact": (2, 0), "sample": (3, 64)}
 
 
 class ForkResult(NamedTuple):
@@ -104,10 +105,20 @@ _decode_calls.bind(tuple(ctypes.cast(getattr(_lib, n), ctypes.c_void_p).value fo
 _raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream's handle, without a Stream object
 
 
+def _fit_workspace(kind, nbytes, index):
+    """A workspace whose first bytes are zero as far as its kind needs it (filled whole, a captured call's tens of
+    megabytes took longer than the call)."""
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
+    zero = _KINDS[kind][1]
+    if zero:
+        ws[:zero].zero_()
+    return ws
+
+
 def _workspace(kind, index, stream, nbytes, given):
     """(pointer, bytes, what owns them): the caller's workspace, or one kept for this kind of call, device and
-    stream.  It is zero-filled when made; every call leaves it fit for the next.  A call that a CUDA graph captures
-    gets one of its own, zero-filled by the graph: a kept one may be replaced by a larger one before a replay."""
+    stream; every call leaves it fit for the next.  A call that a CUDA graph captures gets one of its own, made fit
+    by the graph: a kept one may be replaced by a larger one before a replay."""
     if given is not None:
         if given.get_device() != index or not given.is_contiguous():
             raise ValueError(f"workspace must be contiguous on cuda:{index}")
@@ -117,7 +128,7 @@ def _workspace(kind, index, stream, nbytes, given):
     if nbytes == 0:
         return None, 0, None
     if torch.cuda.is_current_stream_capturing():
-        ws = torch.zeros(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
+        ws = _fit_workspace(kind, nbytes, index)
         return ws.data_ptr(), nbytes, ws
     key = (kind, index, stream)
     kept = _ws.get(key)
@@ -125,9 +136,9 @@ def _workspace(kind, index, stream, nbytes, given):
         with _ws_lock:
             kept = _ws.get(key)
             if kept is None or kept[2] < nbytes:
-                ws = torch.zeros(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
+                ws = _fit_workspace(kind, nbytes, index)
                 kept = _ws[key] = (ws, ws.data_ptr(), nbytes)
-                _decode_calls.register_workspace(_KINDS[kind], index, stream, kept[1], nbytes)
+                _decode_calls.register_workspace(_KINDS[kind][0], index, stream, kept[1], nbytes)
     return kept[1], kept[2], kept[0]
 
 

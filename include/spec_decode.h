@@ -63,8 +63,9 @@ typedef struct {
  *   gets out = 0, lse = -inf.  Tokens that a query does not see never reach
  *   its result, whatever they hold.
  *   out      [B, Q, Hq, D] contiguous, cache's dtype; lse [B, Q, Hq] fp32 or NULL.
- *   workspace: spec_attention_workspace_size(...) bytes, zero-filled once;
- *            every call leaves it fit for the next.  One call at a time.
+ *   workspace: spec_attention_workspace_size(...) bytes, the first
+ *            SPEC_ATTENTION_ZERO_BYTES of them zero-filled once; every call
+ *            leaves it fit for the next.  One call at a time.
  *
  * Scores, softmax and sums are fp32 (bf16: products of bf16 pairs summed in
  * fp32; a weight exp(...) multiplies v as the sum of two bf16 values; fp32:
@@ -74,6 +75,7 @@ typedef struct {
  * The result does not depend on the schedule's timing: partial results are
  * joined in a fixed order.
  */
+#define SPEC_ATTENTION_ZERO_BYTES 2048
 SPEC_API size_t spec_attention_workspace_size(int B, int Q, int Hq, int heads, int head_dim, int dtype);
 SPEC_API spec_status_t spec_paged_attention(
     const void* q, int64_t q_batch_stride, int64_t q_token_stride, int64_t q_head_stride,
@@ -173,13 +175,14 @@ SPEC_API spec_status_t spec_cache_compact(
  *            -inf elsewhere -- rows that spec_verify takes as target or draft
  *            logits, so that both sides of the ratio test are truncated.
  *   workspace: spec_filtered_sample_workspace_size(...) bytes (0 for small
- *            calls: NULL), zero-filled once; every call leaves it fit for the
- *            next.  One call at a time.
+ *            calls: NULL), the first SPEC_SAMPLE_ZERO_BYTES of them zero-filled
+ *            once; every call leaves it fit for the next.  One call at a time.
  * A row with a NaN or +inf or without a finite logit is
  * SPEC_DATA_NONFINITE_LOGIT: token 0, p 0, n_kept 0, filtered -inf.  A row
  * whose copy into shared memory did not land within the kernel's limit on its
  * waits (SPEC_DEVICE_WAIT_TIMEOUT) gets the same.
  */
+#define SPEC_SAMPLE_ZERO_BYTES 64
 SPEC_API size_t spec_filtered_sample_workspace_size(int R, int V, int dtype);
 SPEC_API spec_status_t spec_filtered_sample(
     const void* logits, int64_t row_stride, const float* uniforms, int R, int V, int dtype,

@@ -36,6 +36,13 @@ def test_exports_and_constants(decode):
     assert not set(taken) & set(defs.values())
 
 
+def test_workspaces_zero_bytes(decode):
+    src = open(HEADER).read()
+    zero = {k: int(v) for k, v in re.findall(r"#define\s+SPEC_(\w+)_ZERO_BYTES\s+(\d+)", src)}
+    assert zero == {"ATTENTION": decode._KINDS["attention"][1], "SAMPLE": decode._KINDS["sample"][1]}
+    assert decode._KINDS["fork"][1] == decode._KINDS["compact"][1] == 0
+
+
 def test_native_calls_are_rebuilt_for_another_torch(decode, monkeypatch):
     """_decode_calls.so has torch's and the interpreter's layouts in it: one made for others is not kept."""
     from draft_verify_acceptance_gb300 import build

@@ -864,6 +864,46 @@ def test_threads_on_one_stream(decode):
     assert not wrong
 
 
+def test_workspaces_are_zero_filled_no_further_than_needed(decode, monkeypatch):
+    """Beyond its first bytes a workspace may hold anything, and a captured call, whose workspace is made fit at every
+    replay, fills no more than those."""
+    k, v, table, lengths = make_cache([40, 700, 9000], 16, 2, 128, torch.bfloat16, seed=1, spare=90)
+    few, many = (torch.randn((3, n, 16, 128), generator=gen(2), device="cuda").to(torch.bfloat16) for n in (1, 9))
+    wide = torch.cat([table, torch.full((3, 9000), -1, dtype=torch.int32, device="cuda")], 1)
+    x = (torch.randn((400, 4001), generator=gen(4), device="cuda") * 3).to(torch.bfloat16)
+    x[::9] *= 0.1
+    u = torch.rand(400, generator=gen(5), device="cuda")
+    parents, keep = i32([2, 1, 1]), i32([77, 3, 700])
+    lib = decode._lib
+    calls = [("attention", decode.attention_workspace_size(3, 9, 16, 2, 128, few.dtype),
+              lambda **kw: [decode.paged_attention(few, k, v, table, lengths, **kw)]),
+             ("attention", decode.attention_workspace_size(3, 9, 16, 2, 128, few.dtype),
+              lambda **kw: [decode.paged_attention(many, k, v, wide, lengths, **kw)]),
+             ("sample", lib.spec_filtered_sample_workspace_size(400, 4001, 1),
+              lambda **kw: decode.filtered_sample(x, u, top_p=0.9, return_filtered=True, **kw)[:4]),
+             ("fork", lib.spec_cache_fork_workspace_size(k.shape[0], 3),
+              lambda **kw: decode.cache_fork(k.clone(), v.clone(), table, lengths, parents, keep, 5, **kw)[:5]),
+             ("compact", lib.spec_cache_compact_workspace_size(k.shape[0]),
+              lambda **kw: decode.cache_compact(k.clone(), v.clone(), table, **kw)[:3])]
+    for kind, nbytes, call in calls:
+        want = call()
+        for fill in (0xff, 0x01):
+            ws = torch.full((nbytes,), fill, dtype=torch.uint8, device="cuda")
+            ws[:decode._KINDS[kind][1]] = 0
+            for _ in range(2):
+                assert all(torch.equal(a, b) for a, b in zip(call(workspace=ws), want)), kind
+    filled = []
+    zeros, zero_ = torch.zeros, torch.Tensor.zero_
+    monkeypatch.setattr(torch, "zeros", lambda n, *a, **kw: filled.append(n) or zeros(n, *a, **kw))
+    monkeypatch.setattr(torch.Tensor, "zero_", lambda t: filled.append(t.numel()) or zero_(t))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(torch.cuda.CUDAGraph(), stream=side):
+        for _, _, call in calls:
+            call()
+    assert filled == [2048, 2048, 64]
+
+
 def test_calls_in_a_graph_own_their_workspaces(decode):
     """Captured calls without a workspace of the caller's: replays are right after eager calls that need larger
     workspaces, and eager calls after a capture that was never replayed."""
