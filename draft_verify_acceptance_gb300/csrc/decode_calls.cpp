@@ -157,6 +157,12 @@ bool cache_of(const at::Tensor* k, const at::Tensor* v, bool layered, int device
   return true;
 }
 
+// Tells autograd that a cache was changed in place.
+void written(const at::Tensor* k, PyObject* v) {
+  for (const at::Tensor* t : {k, tensor(v)})
+    if (!t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
+}
+
 at::Tensor make(at::IntArrayRef size, at::ScalarType type, int device) {
   return at::empty(size, at::TensorOptions().dtype(type).device(at::Device(at::kCUDA, static_cast<c10::DeviceIndex>(device))));
 }
@@ -297,6 +303,7 @@ PyObject* call_append(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* 
   if (append(kn->data_ptr(), vn->data_ptr(), T > 1 ? row : H * D, T, starts, &c, t.p, t.stride, t.pages, lengths, B,
              reinterpret_cast<spec_stream_t>(w.stream), nullptr) != SPEC_OK)
     return not_done();
+  written(k, a[3]);
   Py_RETURN_NONE;
 }
 
@@ -326,6 +333,7 @@ PyObject* call_fork(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw
                  lengths_new.data_ptr<int>(), refs.data_ptr<int>(), free.data_ptr<int>(), n_free.data_ptr<int>(), ws, bytes,
                  reinterpret_cast<spec_stream_t>(w.stream), nullptr) != SPEC_OK)
     return not_done();
+  written(k, a[1]);
   return result(fork_result, {&table, &lengths_new, &refs, &free, &n_free, nullptr});
 }
 
@@ -349,6 +357,7 @@ PyObject* call_compact(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject*
   if (compact(&c, t.p, t.stride, t.pages, B, table.data_ptr<int>(), refs.data_ptr<int>(), n_live.data_ptr<int>(), ws, bytes,
               reinterpret_cast<spec_stream_t>(w.stream), nullptr) != SPEC_OK)
     return not_done();
+  written(k, a[1]);
   return result(compact_result, {&table, &refs, &n_live, nullptr});
 }
 

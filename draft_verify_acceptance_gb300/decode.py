@@ -14,7 +14,13 @@ fallback.  Calls are queued on ``stream`` (default: the current stream); with
 A cache tensor is [pages, page_size, heads, head_dim], or with a leading layers
 dimension for cache_fork and cache_compact; the last two dimensions are contiguous, the
 other strides free (a layer of a larger tensor, K and V interleaved), the same for K
-and V.  A page table is int32 [B, max_pages]; its rows may be strided or one row
+and V.
+
+These are operators of inference: their results carry no gradient, also where an input requires
+one, and grad mode makes no difference.  What they write in place (a cache's tensors, ``out``) counts
+as changed for autograd, so a backward pass that needs the earlier values raises.
+
+A page table is int32 [B, max_pages]; its rows may be strided or one row
 expanded to all sequences, but not overlap otherwise.
 """
 import ctypes
@@ -217,6 +223,13 @@ def _cache(k, v, layered, index):
     return _Cache(k.data_ptr(), v.data_ptr(), ls, ps, ts if S > 1 else max(ts, H * D), L, P, S, H, D, dt)
 
 
+def _written(*tensors):
+    """Tells autograd that tensors were changed in place."""
+    for t in tensors:
+        if not t.is_inference():
+            torch.autograd.graph.increment_version(t)
+
+
 def _raise(rc, what):
     raise SpecVerifyError(rc, what)
 
@@ -267,6 +280,8 @@ def paged_attention(at, q, k_pages, v_pages, page_table, lengths, scale=None, *,
         out = torch.empty(shape, dtype=q.dtype, device=q.device)
     elif out.shape != shape or out.dtype is not q.dtype or out.get_device() != index or not out.is_contiguous():
         raise ValueError("out must be contiguous, shaped and typed as q")
+    else:
+        _written(out)
     lse = lse_at = None
     if return_lse:
         lse = torch.empty((B, Q, Hq), dtype=torch.float32, device=q.device)
@@ -327,6 +342,7 @@ def cache_append(at, k_new, v_new, k_pages, v_pages, page_table, lengths, starts
                                 B, stream, status_at)
     if rc != OK:
         _raise(rc, "spec_cache_append")
+    _written(k_pages, v_pages)
     return status
 
 
@@ -360,6 +376,7 @@ def cache_fork(at, k_pages, v_pages, page_table, lengths, parents, keep, room=0,
                               refs.data_ptr(), free.data_ptr(), n_free.data_ptr(), ws, nbytes, stream, status_at)
     if rc != OK:
         _raise(rc, "spec_cache_fork")
+    _written(k_pages, v_pages)
     return ForkResult(new, lens_new, refs, free, n_free, status)
 
 
@@ -385,6 +402,7 @@ def cache_compact(at, k_pages, v_pages, page_table, *, workspace=None, debug=Fal
                                  status_at)
     if rc != OK:
         _raise(rc, "spec_cache_compact")
+    _written(k_pages, v_pages)
     return CompactResult(new, refs, n_live, status)
 
 
@@ -450,6 +468,7 @@ def filtered_sample(at, logits, uniforms, temperature=1.0, *, top_k=None, top_p=
         if out.shape != shape or out.dtype is not logits.dtype or out.get_device() != index or not out.is_contiguous():
             raise ValueError("out must be contiguous, shaped and typed as logits")
         out_at = out.data_ptr()
+        _written(out)
     elif return_filtered:
         out = torch.empty(shape, dtype=logits.dtype, device=device)
         out_at = out.data_ptr()

@@ -824,6 +824,37 @@ def test_ordinary_calls_and_others_agree(decode):
         assert call(*args, **kw) is NotImplemented, (call, kw)
 
 
+@pytest.mark.parametrize("kw", [{}, {"debug": True}])
+def test_autograd_sees_what_is_written_in_place(decode, kw):
+    """Results carry no gradient; a backward pass that needs what a call has overwritten raises, and does not use what
+    is there now.  Inference tensors, which keep no versions, are taken too."""
+    k, v, table, lengths = make_cache([20, 33], 16, 2, 64, torch.float32, seed=1, spare=9)
+    new = torch.randn((2, 1, 2, 64), generator=gen(2), device="cuda")
+    x, u = torch.randn((2, 500), generator=gen(3), device="cuda"), torch.rand(2, generator=gen(4), device="cuda")
+    q = torch.randn((2, 1, 4, 64), generator=gen(3), device="cuda", requires_grad=True)
+    out = decode.paged_attention(q, k, v, table, lengths, **kw)
+    assert not (out[0] if kw else out).requires_grad
+    place = torch.empty_like(q, requires_grad=False)
+    calls = [(k, lambda: decode.cache_append(new, new, k, v, table, lengths, **kw)),
+             (v, lambda: decode.cache_append(new, new, k, v, table, lengths, **kw)),
+             (k, lambda: decode.cache_fork(k, v, table, lengths, i32([0, 0]), i32([20, 19]), 1, **kw)),
+             (v, lambda: decode.cache_compact(k, v, table, **kw)),
+             (place, lambda: decode.paged_attention(q, k, v, table, lengths, out=place, **kw)),
+             (x, lambda: decode.filtered_sample(x, u, out=x, **kw))]
+    for t, call in calls:
+        for _ in range(2):  # (the first makes a workspace)
+            w = torch.ones((), device="cuda", requires_grad=True)
+            y = (t * w).sum()
+            call()
+            with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+                y.backward()
+    with torch.inference_mode():
+        ki, vi = k.clone(), v.clone()
+    decode.cache_append(new, new, ki, vi, table, lengths, **kw)
+    decode.cache_append(new, new, k, v, table, lengths, **kw)
+    assert torch.equal(ki, k) and torch.equal(vi, v)
+
+
 def test_threads_on_one_stream(decode):
     """Four threads make calls of several launches on the same stream and kept workspaces, ordinary ones and others: each
     gets its own results."""
