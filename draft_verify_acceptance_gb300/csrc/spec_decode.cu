@@ -20,6 +20,11 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 bool want32(const void* p) { return p && aligned(p, 4); }  // a required array of 32-bit values
 bool may32(const void* p) { return aligned(p, 4); }        // an optional one
 
+bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
+  const auto p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+  return p < q + static_cast<uintptr_t>(nb) && q < p + static_cast<uintptr_t>(na);
+}
+
 constexpr int kMaxDevices = 64;
 std::once_flag g_once[kMaxDevices];
 int g_sms[kMaxDevices];
@@ -273,6 +278,10 @@ spec_status_t spec_filtered_sample(const void* logits, int64_t row_stride, const
   if (!logits || !aligned(logits, esz) || row_stride < V || !want32(uniforms) || !want32(tokens) ||
       !may32(p) || !may32(n_kept) || !may32(temperatures) || !may32(top_ks) || !may32(top_ps) ||
       !may32(min_ps) || !may32(device_status) || !aligned(filtered, esz))
+    return SPEC_ERR_INVALID_ARG;
+  // filtered rows may take the logits' place, but a row must not be written over another's logits
+  if (filtered && !(filtered == logits && (row_stride == V || R == 1)) &&
+      overlap(logits, ((R - 1) * row_stride + V) * esz, filtered, static_cast<int64_t>(R) * V * esz))
     return SPEC_ERR_INVALID_ARG;
   if (!workspace_ok(workspace, workspace_bytes, specv::filtered_sample_workspace(R, V, esz == 2)))
     return SPEC_ERR_INVALID_ARG;

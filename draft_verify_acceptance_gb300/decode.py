@@ -432,7 +432,7 @@ def filtered_sample(at, logits, uniforms, temperature=1.0, *, top_k=None, top_p=
     SampleResult: tokens, p (the token's probability among the kept ones), n_kept and, with
     ``return_filtered``, the logits with -inf for what was not kept -- rows for ``verify``,
     whose accept test then holds for the truncated distributions.  ``out`` may give a
-    preallocated tensor for those (the logits themselves too).
+    preallocated tensor for those: the logits themselves, or one that does not overlap them.
     """
     index, stream = at
     shape, device = logits.shape, logits.device

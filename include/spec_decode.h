@@ -174,6 +174,8 @@ SPEC_API spec_status_t spec_cache_compact(
  *   filtered [R, V] contiguous dtype or NULL: the logits of the kept tokens,
  *            -inf elsewhere -- rows that spec_verify takes as target or draft
  *            logits, so that both sides of the ratio test are truncated.
+ *            They may be the logits themselves (row_stride V), and must not
+ *            overlap them otherwise.
  *   workspace: spec_filtered_sample_workspace_size(...) bytes (0 for small
  *            calls: NULL), the first SPEC_SAMPLE_ZERO_BYTES of them zero-filled
  *            once; every call leaves it fit for the next.  One call at a time.

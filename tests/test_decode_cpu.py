@@ -190,6 +190,24 @@ def test_sample_refusals(decode):
     assert call(R=0, x=0, u=0, tok=0) == decode.OK
 
 
+def test_filtered_rows_apart_from_the_logits_or_in_their_place(decode):
+    lib = decode._lib
+    need = lib.spec_filtered_sample_workspace_size(4, 1000, 0)
+
+    def call(out, x=FAKE, stride=1000, R=4, V=1000, dtype=0):
+        return lib.spec_filtered_sample(x, stride, FAKE, R, V, dtype, 1.0, 0, 1.0, 0.0, None, None, None, None, FAKE, None, None,
+                                        out, FAKE, need, None, None)
+    size = 4 * 1000 * 4
+    for bad in (dict(out=FAKE + 4), dict(out=FAKE - 4), dict(out=FAKE + size - 4), dict(out=FAKE - size + 4),
+                dict(out=FAKE, stride=1008), dict(out=FAKE + 3 * 4032 + 3996, stride=1008),
+                dict(out=FAKE + 2, dtype=1), dict(out=FAKE + 4, R=1)):
+        assert call(**bad) == decode.ERR_INVALID_ARG, bad
+    for good in (dict(out=FAKE), dict(out=FAKE + size), dict(out=FAKE - size), dict(out=FAKE, stride=1008, R=1),
+                 dict(out=FAKE + 3 * 4032 + 4000, stride=1008)):
+        if not torch.cuda.is_available():  # (with a GPU it would be launched)
+            assert call(**good) == 3, good  # SPEC_ERR_CUDA: no argument error
+
+
 def test_binding_refuses_cpu_tensors(decode):
     x, pages = torch.zeros(2, 8), torch.zeros(3, 4, 1, 64)
     with pytest.raises(ValueError):

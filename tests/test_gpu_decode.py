@@ -700,6 +700,18 @@ def test_sample_scalars_strides_and_streams(decode):
         assert int(r.tokens.flatten()[j]) == ref.sample_row(x3.view(9, -1)[j].float().cpu().numpy(), float(u[j]), 0.7, 40, 0.9)[0]
 
 
+def test_sample_out_over_other_logits_is_refused(decode):
+    buf = torch.randn((5, 4008), generator=gen(1), device="cuda")
+    x, u = buf[:, :4000], torch.rand(5, generator=gen(2), device="cuda")
+    before = buf.clone()
+    for out in (buf.view(-1)[:20000].view(5, 4000), buf.view(-1)[8:20008].view(5, 4000)):
+        with pytest.raises(decode.SpecVerifyError):
+            decode.filtered_sample(x, u, top_k=9, out=out)
+    assert torch.equal(buf, before)
+    r = decode.filtered_sample(x[:1], u[:1], top_k=9, out=x[:1])  # one row: in its place whatever the stride
+    assert torch.equal(r.filtered, decode.filtered_sample(before[:1, :4000], u[:1], top_k=9, return_filtered=True).filtered)
+
+
 @pytest.mark.parametrize("V", [100, 40000, 300001])
 def test_sample_data_errors(decode, V):
     x = torch.randn((6, V), generator=gen(1), device="cuda")
