@@ -141,7 +141,7 @@ __device__ __forceinline__ Child child_of(const ForkArgs& a, int c) {
   ch.keep = a.keep[c];
   const bool none = ch.parent == -1 && ch.keep == 0;
   const bool ok = ch.parent >= 0 && ch.parent < a.B && ch.keep >= 0 &&
-                  ch.keep <= min(a.lengths[ch.parent], INT_MAX) &&
+                  ch.keep <= a.lengths[ch.parent] &&
                   ch.keep <= static_cast<long long>(a.table.max_pages) * S;
   if (!ok) {
     ch.parent = -1;

@@ -73,7 +73,9 @@ constexpr int kMaxChunksS = 8;         // (65536 bf16 of a slice: 16-bit places)
 static_assert(kMaxSliceS / 16 <= kChunkS * kMaxChunksS, "bulk copies of a slice");
 constexpr int kVectorsS = (kMaxSliceS / 16 + kThreadsS - 1) / kThreadsS;  // vectors of a slice a thread sweeps at most
 // Blocks of the row kernel that run at once (two an SM, 152 SMs): rows in
-// clusters of no more than these are finished in it.
+// clusters of no more than these are finished in it.  A constant, so that a
+// workspace's size does not depend on the device; nothing waits for as many to
+// run at once.
 constexpr int kFusedBlocks = 304;
 constexpr int kRowsAtOnce = 4096;       // rows listed in the workspace at a time
 
@@ -473,11 +475,6 @@ __device__ __forceinline__ void block_sum2(unsigned long long a, unsigned long l
                                            unsigned long long* sa, unsigned long long* sb) {
   a = warp_sum_u64(a);
   b = warp_sum_u64(b);
-  if (NT == 32) {
-    *sa = a;
-    *sb = b;
-    return;
-  }
   __syncthreads();
   if ((threadIdx.x & 31) == 0) {
     sh.part[threadIdx.x >> 5] = a;
@@ -554,14 +551,7 @@ __device__ __forceinline__ unsigned long long weight_of(const uint4& e) {
 template <typename E>
 __device__ __forceinline__ unsigned long long key_of(const uint4& e) { return cut_key<E>(__uint_as_float(e.x), e.y); }
 
-// NT threads meet: a warp or the block.
-template <int NT>
-__device__ __forceinline__ void meet() {
-  if (NT == 32) __syncwarp();
-  else __syncthreads();
-}
-
-// The crossing key over n listed elements by NT threads.  keys(entry) lie in
+// The crossing key over n listed elements by a block of NT threads.  keys(entry) lie in
 // [lo, hi]; measure(entry) is an element's weight (kCount: 0 or 1).
 template <int NT, bool kCount, typename K, typename F>
 __device__ __forceinline__ unsigned long long list_crossing(const Ctx& c, const uint4* list, int n, unsigned long long lo,
@@ -569,9 +559,9 @@ __device__ __forceinline__ unsigned long long list_crossing(const Ctx& c, const 
                                                             F measure) {
   int shift = bin_shift(hi - lo);
   for (;;) {
-    meet<NT>();
+    __syncthreads();
     c.clear<NT, kCount ? 0 : 2>();
-    meet<NT>();
+    __syncthreads();
 #pragma unroll 4
     for (int i = threadIdx.x; i < n; i += NT) {
       const uint4 e = list[i];
@@ -581,12 +571,12 @@ __device__ __forceinline__ unsigned long long list_crossing(const Ctx& c, const 
         else bin_add<2>(c.bins, static_cast<unsigned int>(at), w);
       }
     }
-    meet<NT>();
-    if (NT == 32 || threadIdx.x < 32)
+    __syncthreads();
+    if (threadIdx.x < 32)
       crossing_bin(c, rem, [&](int b) -> unsigned long long {
         return kCount ? c.bins->count[b] : bin_value<2>(c.bins, b);
       }, c.bins->count);
-    meet<NT>();
+    __syncthreads();
     rem = c.sh->rem;
     lo += static_cast<unsigned long long>(c.sh->sel[0]) << shift;
     if (shift == 0) return lo;
@@ -605,12 +595,12 @@ __device__ __forceinline__ unsigned long long list_crossing(const Ctx& c, const 
       }
     }
   }
-  meet<NT>();
-  if (NT == 32 || threadIdx.x < 32) {
+  __syncthreads();
+  if (threadIdx.x < 32) {
     const unsigned long long k = crossing_of_few(c.sh->few_key, c.sh->few_w, min(32u, c.sh->n_few), rem);
     if (threadIdx.x == 0) c.sh->lo = k;
   }
-  meet<NT>();
+  __syncthreads();
   return c.sh->lo;
 }
 
@@ -941,7 +931,7 @@ __device__ __forceinline__ unsigned long long share_of(float top_p, unsigned lon
   return max(1ull, draw_threshold(fminf(fmaxf(top_p, 0.f), 0.99999994f), total));
 }
 
-// The cuts and the draw of a covered row on its list by NT threads.  Writes
+// The cuts and the draw of a covered row on its list by a block of NT threads.  Writes
 // the row's outputs; returns the largest kept key (~0 when the row needs
 // its exact sum).  Three passes over the list: weights by bins of the logit's bits (top-p); sums of what lies above
 // the crossing bin, by bins of the index; the crossing bin of the draw.  A
@@ -976,9 +966,9 @@ __device__ unsigned long long finish_row(const Ctx& c, const SampleArgs& a, cons
   unsigned long long rem = 0;
   if (has_p) {
     rem = share_of(set.top_p, total - slack) - 1;
-    meet<NT>();
+    __syncthreads();
     c.clear<NT, 2>();
-    meet<NT>();
+    __syncthreads();
 #pragma unroll 4
     for (int i = tid; i < n; i += NT) {
       const uint4 e = list[i];
@@ -989,10 +979,10 @@ __device__ unsigned long long finish_row(const Ctx& c, const SampleArgs& a, cons
         atomicAdd(&c.bins->count[at], 1u);
       }
     }
-    meet<NT>();
-    if (NT == 32 || tid < 32)
+    __syncthreads();
+    if (tid < 32)
       crossing_bin(c, rem, [&](int b) { return bin_value<2>(c.bins, b); }, c.bins->count);
-    meet<NT>();
+    __syncthreads();
     bin = c.sh->sel[0];
     rem = c.sh->rem;
     if (c.sh->bin_count > 32) {
@@ -1002,10 +992,10 @@ __device__ unsigned long long finish_row(const Ctx& c, const SampleArgs& a, cons
     }
   }
   // ---- what is kept, by bins of the index ----
-  meet<NT>();
+  __syncthreads();
   for (int i = tid; i < 256; i += NT) by_index->count[i] = by_index->part[0][i] = by_index->part[1][i] = 0;
   if (tid == 0) c.sh->n_few = 0;
-  meet<NT>();
+  __syncthreads();
   unsigned long long t = 0;
   unsigned int k = 0;
   auto add = [&](unsigned int j, unsigned int lo, unsigned int hi) {
@@ -1032,8 +1022,8 @@ __device__ unsigned long long finish_row(const Ctx& c, const SampleArgs& a, cons
     }
   }
   if (bin < 256) {
-    meet<NT>();
-    if (NT == 32 || tid < 32) {
+    __syncthreads();
+    if (tid < 32) {
       const int few = min(32u, c.sh->n_few);
       const unsigned long long key = crossing_of_few(c.sh->few_key, c.sh->few_w, few, rem);
       if (tid < few && c.sh->few_key[tid] <= key)
@@ -1041,7 +1031,7 @@ __device__ unsigned long long finish_row(const Ctx& c, const SampleArgs& a, cons
             static_cast<unsigned int>(c.sh->few_w[tid]) & 0xfffffu, static_cast<unsigned int>(c.sh->few_w[tid] >> 20));
       if (tid == 0) c.sh->lo = key;
     }
-    meet<NT>();
+    __syncthreads();
     cut = c.sh->lo;
   }
   block_sum2<NT>(t, k, *c.sh, &S, &count);
@@ -1050,14 +1040,14 @@ __device__ unsigned long long finish_row(const Ctx& c, const SampleArgs& a, cons
   if (has_p && slack != 0 && S < share_of(set.top_p, total + slack)) return ~0ull;
   // ---- the draw ----
   const unsigned long long theta = draw_threshold(u, S);
-  meet<NT>();
-  if (NT == 32 || tid < 32) {
+  __syncthreads();
+  if (tid < 32) {
     crossing_bin(c, theta, [&](int b) {
       return (static_cast<unsigned long long>(by_index->part[1][b]) << 20) + by_index->part[0][b];
     }, by_index->count);
     if (tid == 0) c.sh->n_few = 0;
   }
-  meet<NT>();
+  __syncthreads();
   unsigned long long token;
   if (c.sh->bin_count <= 32) {
     const unsigned int at = static_cast<unsigned int>(c.sh->sel[0]);
@@ -1073,21 +1063,21 @@ __device__ unsigned long long finish_row(const Ctx& c, const SampleArgs& a, cons
         }
       }
     }
-    meet<NT>();
-    if (NT == 32 || tid < 32) {
+    __syncthreads();
+    if (tid < 32) {
       const int few = min(32u, c.sh->n_few);
       token = crossing_of_few(c.sh->few_key, c.sh->few_w, few, rem);
       if (tid < few && c.sh->few_key[tid] == token) c.sh->w_token = c.sh->few_w[tid];
       if (tid == 0) c.sh->lo = token;
     }
-    meet<NT>();
+    __syncthreads();
     token = c.sh->lo;
   } else {
     token = list_crossing<NT, false>(c, list, n, 0, a.V - 1, theta,
                                      [](const uint4& e) -> unsigned long long { return e.y; }, kept);
     for (int i = tid; i < n; i += NT)
       if (list[i].y == token) c.sh->w_token = weight_of(list[i]);
-    meet<NT>();
+    __syncthreads();
   }
   unsigned long long top = a.filtered ? cut : 0;  // (only the filtered row needs it)
   if (top == ~0ull) {  // no cut by k or p: the largest key kept
@@ -1096,12 +1086,10 @@ __device__ unsigned long long finish_row(const Ctx& c, const SampleArgs& a, cons
       if (kept(list[i])) top = max(top, key_of<E>(list[i]));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (NT > 32) {
-      if ((tid & 31) == 0) c.sh->part[tid >> 5] = top;
-      __syncthreads();
+    if ((tid & 31) == 0) c.sh->part[tid >> 5] = top;
+    __syncthreads();
 #pragma unroll
-      for (int x = 0; x < NT / 32; ++x) top = max(top, c.sh->part[x]);
-    }
+    for (int x = 0; x < NT / 32; ++x) top = max(top, c.sh->part[x]);
   }
   if (tid == 0) {
     a.tokens[row] = static_cast<int>(token);
@@ -1712,8 +1700,7 @@ cudaError_t filtered_sample_prepare() {
   return cudaSuccess;
 }
 
-cudaError_t launch_filtered_sample(const SampleArgs& a, void* ws, int sm_count, cudaStream_t stream) {
-  (void)sm_count;
+cudaError_t launch_filtered_sample(const SampleArgs& a, void* ws, cudaStream_t stream) {
   const Shape s = shape_of(a.R, a.V, a.bf16);
   const Space sp = space_of(ws, a.R);
   if (a.bf16) return s.staged ? launch<BF16, true>(a, s, sp, stream) : launch<BF16, false>(a, s, sp, stream);

@@ -110,6 +110,6 @@ cudaError_t launch_compact(const CompactArgs& a, void* ws, int sm_count, cudaStr
 constexpr int kQueueBytes = 64;  // at the workspace's start: zero between calls
 size_t filtered_sample_workspace(int R, int V, bool bf16);
 cudaError_t filtered_sample_prepare();
-cudaError_t launch_filtered_sample(const SampleArgs& a, void* ws, int sm_count, cudaStream_t stream);
+cudaError_t launch_filtered_sample(const SampleArgs& a, void* ws, cudaStream_t stream);
 
 }  // namespace specv

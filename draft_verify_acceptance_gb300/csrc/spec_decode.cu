@@ -286,7 +286,7 @@ spec_status_t spec_filtered_sample(const void* logits, int64_t row_stride, const
   if (!workspace_ok(workspace, workspace_bytes, specv::filtered_sample_workspace(R, V, esz == 2)))
     return SPEC_ERR_INVALID_ARG;
   int sms = 0;
-  const spec_status_t st = device_sms(&sms);
+  const spec_status_t st = device_sms(&sms);  // (sets the kernels' attributes)
   if (st != SPEC_OK) return st;
   specv::SampleArgs a;
   a.logits = logits;
@@ -308,7 +308,7 @@ spec_status_t spec_filtered_sample(const void* logits, int64_t row_stride, const
   a.n_kept = n_kept;
   a.filtered = filtered;
   a.status = device_status;
-  return done(specv::launch_filtered_sample(a, workspace, sms, reinterpret_cast<cudaStream_t>(stream)));
+  return done(specv::launch_filtered_sample(a, workspace, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"
