@@ -553,6 +553,35 @@ def test_compact(decode, P, M, B, live, layers):
             assert torch.equal(x, want)
 
 
+@pytest.mark.parametrize("P,M,B,live", [(20000, 300, 40, 9000),     # a plan of several rounds of 8192 pages
+                                        (20000, 400, 300, 11000),   # more entries than one block counts
+                                        (60000, 300, 200, 20011),   # more pages than its shared memory holds
+                                        (60000, 400, 300, 59990)])
+def test_compact_large_pools(decode, P, M, B, live):
+    g = gen(P + live)
+    k, v = (torch.randn((P, 4, 1, 8), generator=g, device="cuda") for _ in range(2))
+    table = torch.full((B * M,), -1, dtype=torch.int32, device="cuda")
+    ids = torch.randperm(P, generator=g, device="cuda")[:live].to(torch.int32)
+    at = torch.randperm(B * M, generator=g, device="cuda")
+    count = min(live, B * M)
+    table[at[:count]] = ids[:count]
+    table[at[0]] = table[at[1]]  # a shared page
+    table = table.view(B, M)
+    have = table.cpu().numpy()
+    used = np.unique(have[have >= 0])
+    n, to = len(used), np.arange(P)
+    source, dest = used[used >= n], np.setdiff1d(np.arange(n), used)
+    to[source] = dest
+    new = np.where(have >= 0, to[have], -1)
+    refs = np.bincount(new[new >= 0], minlength=P)
+    source, dest = torch.tensor(source, device="cuda"), torch.tensor(dest, device="cuda")
+    want = [x.index_copy(0, dest, x[source]) for x in (k, v)]
+    r = decode.cache_compact(k, v, table, debug=True)
+    assert int(r.status) == 0 and int(r.n_live) == n and len(source) > 0
+    assert np.array_equal(r.page_table.cpu().numpy(), new) and np.array_equal(r.ref_counts.cpu().numpy(), refs)
+    assert torch.equal(k, want[0]) and torch.equal(v, want[1])
+
+
 def test_compact_strided_and_errors(decode):
     kv = torch.randn((30, 2, 4, 2, 64), generator=gen(2), device="cuda").to(torch.bfloat16)
     k0 = kv.clone()
@@ -677,6 +706,21 @@ def test_sample_sums_are_the_definition_s(decode, dtype, V):
             w = ref.weights(row, 0.8)
             assert int(r.tokens[i]) == j and int(r.n_kept[i]) == len(kept)
             assert float(r.p[i]) == float(np.float32(w[j]) / np.float32(w[kept].sum()))
+
+
+@pytest.mark.parametrize("V", [700, 701])
+def test_sample_more_rows_than_are_listed_at_a_time(decode, V):
+    """5120 rows (a batch of 1024 sequences with 4 drafted tokens), flat ones among them; in their place too."""
+    R = 5120
+    x = (torch.randn((R, V), generator=gen(8), device="cuda") * 4).to(torch.bfloat16)
+    x[11::100] = x[11::100] * 0.02
+    u = torch.rand(R, generator=gen(9), device="cuda")
+    settings = [MIX[i % len(MIX)] for i in range(R)]
+    want = check_sample(decode, x, u, settings)
+    T, k, p, m = (list(c) for c in zip(*settings))
+    f = lambda c: torch.tensor(c, dtype=torch.float32, device="cuda")  # noqa: E731
+    got = decode.filtered_sample(x, u, f(T), top_k=i32(k), top_p=f(p), min_p=f(m), out=x)
+    assert all(torch.equal(a, b) for a, b in zip(got[:4], want[:4]))
 
 
 def test_sample_scalars_strides_and_streams(decode):
