@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(Ring<E, D, NB>::kWarps * 32, Ring<E, D, NB>::k
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-            mx = fmaxf(mx, m[nb][x]);
+            if (!(mx > m[nb][x] + kSlack)) mx = m[nb][x];  // (this row's own scores decide)
             const float c = m[nb][x] == -INFINITY ? 0.f : ex2(m[nb][x] - mx);
             m[nb][x] = mx;
             l[nb][x] *= c;

@@ -434,6 +434,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) attention_tc_kernel(const AttnAr
             float m = old;
 #pragma unroll
             for (int w = 0; w < 4; ++w) m = fmaxf(m, sh.wmax[w][r]);
+            if (!(m > old + kSlackT)) m = old;  // (this row's own scores decide)
             sh.m[r] = m;
             sh.corr[r] = old == -INFINITY ? 0.f : ex2(old - m);
           }

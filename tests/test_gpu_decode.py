@@ -182,6 +182,25 @@ def test_attention_many_rows_nonfinite_values_of_no_weight(decode, Q, G):
     check_nonfinite_values_of_no_weight(decode, torch.bfloat16, Q, G, 128, extra_cols=10000)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("Q,G,D,extra", [(4, 4, 64, 2), (3, 4, 128, 2), (6, 4, 128, 2), (9, 8, 128, 10000)])
+def test_attention_rows_do_not_depend_on_one_another(decode, dtype, Q, G, D, extra):
+    """Keys that move the maximum of the queries that see them leave the other queries' results as they were, to the
+    bit."""
+    lens, S, H = [Q, 50, 333], 16, 2
+    k, v, table, lengths = make_cache(lens, S, H, D, dtype, seed=3, extra_cols=extra)
+    q = torch.randn((3, Q, H * G, D), generator=gen(1), device="cuda").to(dtype)
+    clean = decode.paged_attention(q, k, v, table, lengths, return_lse=True)
+    for size in (30.0, 1e4, 1e30):
+        for i in range(Q - 1):
+            k2 = k.clone()
+            for b, n in enumerate(lens):
+                for t in range(max(0, n - Q + i + 1), n):
+                    k2[table[b, t // S], t % S] *= size
+            got = decode.paged_attention(q, k2, v, table, lengths, return_lse=True)
+            assert all(torch.equal(a[:, :i + 1], c[:, :i + 1]) for a, c in zip(got, clean)), (size, i)
+
+
 @pytest.fixture
 def roomy_tables(monkeypatch):
     """Page tables with room for many tokens, which with many rows a cache head are read by another kernel."""
