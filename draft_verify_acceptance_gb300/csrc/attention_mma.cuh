@@ -124,7 +124,9 @@ __device__ __forceinline__ void mma1688(float (&c)[4], const uint32_t (&a)[4], u
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// x as two tf32 parts; what is not finite stays whole in the first.
+// x as two tf32 parts; what is not finite, or rounds to infinity (from
+// kTf32Inf on), is whole in the first.
+constexpr uint32_t kTf32Inf = 0x7f7ff000u;
 __device__ __forceinline__ void split(float x, uint32_t& hi, uint32_t& lo) {
   asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(x));
   lo = (hi & 0x7f800000u) == 0x7f800000u ? 0u : __float_as_uint(x - __uint_as_float(hi));
@@ -159,11 +161,11 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 __device__ __forceinline__ bool nonfinite2(uint32_t w) {
   return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
 }
-// Is a word of the cache, one fp32 or two bf16 values, not all finite; and it
-// with zero in place of what is not.
+// Is a word of the cache, one fp32 or two bf16 values, not all finite as an
+// operand; and it with zero in place of what is not.
 template <typename E>
 __device__ __forceinline__ bool odd_word(uint32_t w) {
-  return E::kBytes == 4 ? (w & 0x7f800000u) == 0x7f800000u : nonfinite2(w);
+  return E::kBytes == 4 ? (w & 0x7fffffffu) >= kTf32Inf : nonfinite2(w);
 }
 template <typename E>
 __device__ __forceinline__ uint32_t even_word(uint32_t w) {
@@ -469,7 +471,7 @@ __global__ void __launch_bounds__(Ring<E, D, NB>::kWarps * 32, Ring<E, D, NB>::k
                 for (int y = 0; y < 2; ++y) {
                   const int d = dim_of<E>(mt, y, g), chunk = d * E::kBytes / 16;
                   const float v = shared_value<E>(vat + t * kRow + v_place<E>(chunk, t) * 16 + d * E::kBytes % 16);
-                  if (!isfinite(v)) {
+                  if (odd_word<E>(__float_as_uint(v))) {
                     if (sees[0]) o[mt][nb][y * 2] += p[0] * v;
                     if (sees[1]) o[mt][nb][y * 2 + 1] += p[1] * v;
                   }

@@ -67,10 +67,12 @@ typedef struct {
  *            SPEC_ATTENTION_ZERO_BYTES of them zero-filled once; every call
  *            leaves it fit for the next.  One call at a time.
  *
- * Scores, softmax and sums are fp32 (bf16: products of bf16 pairs summed in
- * fp32; a weight exp(...) multiplies v as the sum of two bf16 values; fp32:
- * operands enter products as two parts of 11 bits, which leaves out 2^-22 of
- * a term), and the output is rounded once.  A value that is not finite in a
+ * Scores, softmax and sums are fp32 (exponentials by ex2.approx, within 2^-22;
+ * bf16: products of bf16 pairs summed in fp32; a weight exp(...) multiplies v
+ * as the sum of two bf16 values, 2^-17; fp32: operands enter products as two
+ * parts of 11 bits, which leaves out 2^-22 of a term), and the output is
+ * rounded once.  Sums are divided at the end, of weights of up to 2^8: values
+ * from about 2^119 / tokens on may overflow in them.  A value that is not finite in a
  * token that a query sees makes what it reaches not finite (infinite or NaN).
  * The result does not depend on the schedule's timing: partial results are
  * joined in a fixed order.

@@ -201,6 +201,25 @@ def test_attention_rows_do_not_depend_on_one_another(decode, dtype, Q, G, D, ext
             assert all(torch.equal(a[:, :i + 1], c[:, :i + 1]) for a, c in zip(got, clean)), (size, i)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("Q,G,D,extra", [(4, 4, 64, 2), (3, 4, 128, 2), (9, 8, 128, 10000)])
+def test_attention_largest_values(decode, dtype, Q, G, D, extra):
+    """The type's largest values where no query looks change nothing."""
+    lens, S, H = [Q, 50, 333], 16, 2
+    k, v, table, lengths = make_cache(lens, S, H, D, dtype, seed=3, extra_cols=extra)
+    q = torch.randn((3, Q, H * G, D), generator=gen(1), device="cuda").to(dtype)
+    clean = decode.paged_attention(q, k, v, table, lengths)
+    for most in (torch.finfo(dtype).max, torch.finfo(dtype).min):
+        for i in range(Q - 1):
+            k2, v2 = k.clone(), v.clone()
+            for b, n in enumerate(lens):
+                for t in range(max(0, n - Q + i + 1), n):
+                    k2[table[b, t // S], t % S] = most
+                    v2[table[b, t // S], t % S] = most
+            got = decode.paged_attention(q, k2, v2, table, lengths)
+            assert torch.equal(got[:, :i + 1], clean[:, :i + 1]), (most, i)
+
+
 @pytest.fixture
 def roomy_tables(monkeypatch):
     """Page tables with room for many tokens, which with many rows a cache head are read by another kernel."""
