@@ -1255,6 +1255,14 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
     tau = taus ? fminf(tau / taus, M) : -INFINITY;
     M += 0.f;
     const bool good = !lost && M > -INFINITY && M < INFINITY;
+    if (tid == 0) {
+      int bad = timeout ? kWaitTimeout : 0;
+      if (c.rank == 0 && !(kWhole && queue)) {  // (the list kernel has reported a queued row's data and settings)
+        bad |= set.bad | (good || lost ? 0 : kDataNonfiniteLogit);
+        if (!(u >= 0.f && u < 1.f)) bad |= kDataUniformRange;
+      }
+      if (bad && a.status) atomicOr(a.status, bad);
+    }
     Kept kept;
     kept.cut = ~0ull;
     kept.least = sh.least;
@@ -1461,14 +1469,6 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
       head.cut = kept.cut;
       head.written = later;
       heads[at] = head;
-    }
-    if (tid == 0) {
-      int bad = timeout ? kWaitTimeout : 0;
-      if (c.rank == 0 && !(kWhole && queue)) {  // (the list kernel has reported a queued row's data and settings)
-        bad |= set.bad | (good || lost ? 0 : kDataNonfiniteLogit);
-        if (!(u >= 0.f && u < 1.f)) bad |= kDataUniformRange;
-      }
-      if (bad && a.status) atomicOr(a.status, bad);
     }
   }
 }
