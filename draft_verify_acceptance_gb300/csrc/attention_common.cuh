@@ -278,14 +278,13 @@ __device__ void attn_join(const AttnArgs& a, int b, int h, int row0, int rows, l
         const float* s = attn_slot<kRows, D>(a, min(c + y, c1), min(c + y, c1) == c0);
 #pragma unroll
         for (int i = 0; i < kE; ++i) {
-          mc[y][i] = __ldcg(s + kRows * D + r[i]);
-          lc[y][i] = __ldcg(s + kRows * D + kRows + r[i]);
-          v[y][i] = __ldcg(reinterpret_cast<const float4*>(s + r[i] * D + d[i]));
+          mc[y][i] = c + y <= c1 ? __ldcg(s + kRows * D + r[i]) : -INFINITY;
+          lc[y][i] = c + y <= c1 ? __ldcg(s + kRows * D + kRows + r[i]) : 0.f;
+          v[y][i] = c + y <= c1 ? __ldcg(reinterpret_cast<const float4*>(s + r[i] * D + d[i])) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
       }
 #pragma unroll
-      for (int y = 0; y < kC; ++y) {
-        if (c + y > c1) break;
+      for (int y = 0; y < kC; ++y)
 #pragma unroll
         for (int i = 0; i < kE; ++i) {
           // a part without a maximum holds zeros, or NaN that it passes on
@@ -296,7 +295,6 @@ __device__ void attn_join(const AttnArgs& a, int b, int h, int row0, int rows, l
           o[i].z = fmaf(w, v[y][i].z, o[i].z);
           o[i].w = fmaf(w, v[y][i].w, o[i].w);
         }
-      }
     }
 #pragma unroll
     for (int i = 0; i < kE; ++i)
