@@ -391,7 +391,7 @@ __device__ __forceinline__ float logit_of(unsigned long long cut) {
 // What every rank of a cluster publishes to all.
 struct Exchange {
   float max[kMaxCS], tau[kMaxCS];  // tau: sum of the warps' order statistics, taus of them
-  int taus[kMaxCS], listed[kMaxCS], lost[kMaxCS];  // lost: a copy never landed
+  int taus[kMaxCS], listed[kMaxCS];  // taus -1: a copy never landed
   unsigned long long sum[kMaxCS], listed_sum[kMaxCS];
   unsigned long long mass[kMaxCS], count[kMaxCS];
 };
@@ -1240,14 +1240,14 @@ filter_row_kernel(const SampleArgs a, int row0, int nvec, int nvs, bool aligned_
       }
       *c.at(&ex.max[c.rank], tid) = m;
       *c.at(&ex.tau[c.rank], tid) = t;
-      *c.at(&ex.taus[c.rank], tid) = n;
-      *c.at(&ex.lost[c.rank], tid) = timeout;
+      *c.at(&ex.taus[c.rank], tid) = timeout ? -1 : n;
     }
     c.sync();
     float M = -INFINITY, tau = 0.f;
-    int taus = 0, lost = 0;  // lost: the row has no result (every block of the cluster goes the same way)
+    int taus = 0;
+    bool lost = false;  // the row has no result (every block of the cluster goes the same way)
     for (int r = 0; r < c.C; ++r) {
-      lost |= ex.lost[r];
+      lost |= ex.taus[r] < 0;
       M = fmaxf(M, ex.max[r]);
       tau += ex.tau[r];
       taus += ex.taus[r];
