@@ -14,15 +14,16 @@ namespace specv {
 // sequence and kTcWork tokens times cache heads in all, the rest to
 // attention_mma.cuh, in tiles of at most 24 rows that each read K and V again
 // (through L2).  Measured, mma and tc:
-//   64 sequences of 400..4000 tokens, 8 cache heads, R = 24: 114 and 178 us;
-//     R = 32: 190 and 168;  R = 36: 204 and 202;  R = 68: 295 and 261
-//   34 of 7406..9512 tokens, 4 cache heads, R = 72: 256 and 201
-//   4 of 10000..20000 tokens, 8 cache heads, R = 32: 77 and 69
-//   64 of 1000 tokens, 8 cache heads, R = 32: 97 and 99
-//   32 of 500..1500 tokens, 8 cache heads, R = 68: 88 and 98
-// (an item's start and end cost tc some 10 us, mma 4), and with heads of 64
-// mma was ahead at every size: 83 sequences of 188..808 tokens, 8 cache heads,
-// R = 48: 67 and 108; 16 of 2400 tokens, R = 85: 28 and 58.
+//   64 sequences of 400..4000 tokens, 8 cache heads, R = 24: 114 and 169 us;
+//     R = 32: 185 and 172;  R = 36: 201 and 201;  R = 68: 291 and 257
+//   34 of 7406..9512 tokens, 4 cache heads, R = 72: 251 and 197
+//   4 of 10000..20000 tokens, 8 cache heads, R = 32: 75 and 71
+//   64 of 1000 tokens, 8 cache heads, R = 32: 95 and 101
+//   32 of 500..1500 tokens, 8 cache heads, R = 68: 87 and 97
+// (an item's start and end cost tc some 10 us, mma 4).  With heads of 64, for
+// which a tcgen05 kernel was tried and not kept, mma was ahead at every size:
+// 83 sequences of 188..808 tokens, 8 cache heads, R = 48: 67 and 108; 16 of
+// 2400 tokens, R = 85: 28 and 58.
 constexpr int64_t kTcTokens = 2048, kTcWork = 300000;
 
 size_t attention_workspace(int D, bool bf16) {

@@ -23,19 +23,22 @@
 // lanes and no rescaling.
 //
 // Measured, bf16, heads of 128, 32 query heads on 8: one query on 64 sequences
-// of 4000 tokens 163 us (the cache's bytes at the copy rate: 157), on 64 of
-// 400..4000 101 (94), on 3 of 60001..131072 197 (190); six queries on the
-// ragged 64 114 (94): HBM is the bound until 24 rows' 72 products a step and
-// an item's end (some 4 us: the ring drains, the warps' parts meet) show.
+// of 4000 tokens 166 us (the cache's bytes at the copy rate: 157), on 64 of
+// 400..4000 101 (94), on 3 of 60001..131072 200 to 215 (190; it differs by
+// machine); six queries on the ragged 64 107 to 116 (94): HBM is the bound
+// until 24 rows' 72 products a step and an item's end (some 4 us: the ring
+// drains, the warps' parts meet) show.
 //
 // fp32 takes m16n8k8 on tf32 parts: x = hi + lo with hi = x rounded to 11 bits
 // and lo the rest, and a product as hi hi + hi lo + lo hi, each exact in fp32,
 // which leaves out 2^-22 of a term.  The tensor cores' sums are not rounded to
 // nearest, so no chain of them is long: a score's hi parts make two chains of
 // D / 16 and the rest a third, and a step's part of O^T starts from zero and
-// is added by an fp32 add.  (On the fp32 units, with a multiply-add per row and
-// element, 32 sequences of 400..4000 tokens took 332 us for one query and 930
-// for six, where this takes 139 and 237.)
+// is added by an fp32 add.  32 sequences of 400..4000 tokens take 141 us for one
+// query and 234 for six (97): neither HBM (59 and 36 %) nor the issue slots (40
+// and 34 %) nor the tensor cores (20 and 36 %) are full, and a warp waits most
+// for results of its own (fixed latencies, then the tensor pipe): six warps an
+// SM, which is what the ring leaves room for, are too few to cover them.
 #pragma once
 
 #include "attention_common.cuh"

@@ -26,10 +26,12 @@
 // output does) and finish items.
 //
 // 64 sequences of 400..4000 tokens, 8 cache heads of 128: 32 rows a head 168
-// us, 68 rows 262 (the cache's bytes at the copy rate: 95).  A tile's softmax
+// us, 68 rows 257 (the cache's bytes at the copy rate: 95).  A tile's softmax
 // of 32 rows takes as long as its bytes take HBM, about 2500 cycles (TMEM
 // reads, exponentials, the two-part weights' stores), more with more rows; an
-// item's start and end, where the ring waits, some 10 us.
+// item's start and end, where the ring waits, some 10 us.  Its warps wait for
+// TMEM and shared memory and for instructions (each of the roles has code of
+// its own); the tensor cores are busy 8 and 14 % of the time.
 #pragma once
 
 #include "attention_common.cuh"

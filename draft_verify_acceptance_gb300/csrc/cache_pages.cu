@@ -59,8 +59,8 @@ __device__ __forceinline__ void copy_tokens(const CacheView& cv, const char* src
 // One warp per new token: it finds the token's sequence in `starts`, its page
 // in the table, and copies the two rows.  The rows' first pieces are under way
 // while it looks (four dependent loads or more): 53000 tokens of twelve
-// sequences, 8 heads of 128, in 60 us, their bytes at the copy rate 54, and a
-// verify step's 384 in 4.7, nearly all of it a launch.
+// sequences, 8 heads of 128, in 55 to 68 us by machine, their bytes at the copy
+// rate 54, and a verify step's 384 in 5.5, nearly all of it a launch.
 constexpr int kPieces = 4;  // of K, and of V, a lane holds
 __global__ void __launch_bounds__(256)
 append_kernel(const char* k_new, const char* v_new, long long new_stride, int T, const int32_t* starts,

@@ -39,9 +39,13 @@
 // logits at the copy rate: 39; 17 instructions a logit at two thirds of the
 // issue slots), finish 46 (lists of 845 entries in three passes), whole 29 for
 // the few rows between the bounds (one row's latency); 384 rows of 128256 with
-// eight settings and filtered rows 81 us (30); 4 rows of 1000 in the whole
-// kernel alone 12.  A flat row whose kept set is a tenth of its 32000 logits
-// takes a cluster 100 us.
+// eight settings and filtered rows 81 us (30; the list kernel's 58 with 40 % of
+// the issue slots and 30 % of DRAM in use: barriers and latency); 4 rows of
+// 1000 in the whole kernel alone 12.  Rows whose kept set is wider than the
+// list go one by one through the whole kernel: 4096 rows of 32000 that keep
+// 1445 each take 1.7 ms (39), and a flat row that keeps a tenth of its 32000
+// logits takes a cluster 100 us.  Rows off 16 bytes are loaded by element:
+// 4096 of 32001 320 us.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 

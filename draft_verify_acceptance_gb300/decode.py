@@ -8,7 +8,8 @@
 
 As in ``binding``, every step runs in the library's CUDA kernels; this module checks
 tensors, owns a workspace per (device, stream) and passes pointers.  There is no CPU
-fallback.  Calls are queued on ``stream`` (default: the current stream); with
+fallback.  The workspaces (spec_decode.h gives their sizes) are kept for good, or may be
+the caller's by ``workspace``.  Calls are queued on ``stream`` (default: the current stream); with
 ``debug=True`` they also return the device status word (OR of DATA_* bits).
 
 A cache tensor is [pages, page_size, heads, head_dim], or with a leading layers

@@ -65,7 +65,8 @@ typedef struct {
  *   out      [B, Q, Hq, D] contiguous, cache's dtype; lse [B, Q, Hq] fp32 or NULL.
  *   workspace: spec_attention_workspace_size(...) bytes, the first
  *            SPEC_ATTENTION_ZERO_BYTES of them zero-filled once; every call
- *            leaves it fit for the next.  One call at a time.
+ *            leaves it fit for the next.  One call at a time.  (30 MB for bf16
+ *            heads of 128, 15 for 64, 8 and 4 for fp32, whatever the batch.)
  *
  * Scores, softmax and sums are fp32 (exponentials by ex2.approx, within 2^-22;
  * bf16: products of bf16 pairs summed in fp32; a weight exp(...) multiplies v
@@ -181,6 +182,7 @@ SPEC_API spec_status_t spec_cache_compact(
  *   workspace: spec_filtered_sample_workspace_size(...) bytes (0 for small
  *            calls: NULL), the first SPEC_SAMPLE_ZERO_BYTES of them zero-filled
  *            once; every call leaves it fit for the next.  One call at a time.
+ *            (24.6 KB a row, for 4096 rows and more 101 MB.)
  * A row with a NaN or +inf or without a finite logit is
  * SPEC_DATA_NONFINITE_LOGIT: token 0, p 0, n_kept 0, filtered -inf.  A row
  * whose copy into shared memory did not land within the kernel's limit on its
