@@ -1,5 +1,5 @@
 """Build libspecverify.so (the C-ABI CUDA library) in-tree for sm_103a, and
-_decode_calls.so, the part of decode.py that is not Python.
+_decode_calls.so, the part of decode.py and tree.py that is not Python.
 
 Each translation unit under ``csrc/`` is compiled by nvcc in parallel, then
 linked into ``draft_verify_acceptance_gb300/libspecverify.so``.  Register and
@@ -18,7 +18,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libspecverify.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["spec_verify.cu", "verify_greedy.cu", "verify_sample.cu", "verify_sample_fused.cu", "verify_sample_seq.cu", "verify_sample_ee.cu", "verify_sample_2p.cu", "verify_draft_sample.cu", "verify_scd.cu", "rejection_cut.cu",
-           "spec_verify_static.cu", "spec_decode.cu", "attention.cu", "attention_tc.cu", "cache_pages.cu", "filtered_sample.cu"]
+           "spec_verify_static.cu", "spec_decode.cu", "attention.cu", "attention_tc.cu", "cache_pages.cu", "filtered_sample.cu",
+           "spec_tree.cu", "attention_tree.cu", "tree_cache.cu"]
 
 
 CALLS = os.path.join(HERE, "_decode_calls.so")
@@ -35,7 +36,8 @@ def _calls_abi():
 
 
 def _calls_fresh(src):
-    deps = [src, os.path.join(ROOT, "include", "spec_decode.h"), os.path.abspath(__file__)]
+    deps = [src, os.path.join(ROOT, "include", "spec_decode.h"), os.path.join(ROOT, "include", "spec_tree.h"),
+            os.path.abspath(__file__)]
     if not os.path.exists(CALLS) or any(os.path.getmtime(f) > os.path.getmtime(CALLS) for f in deps):
         return False
     if not os.path.exists(CALLS_FOR):
@@ -80,7 +82,7 @@ def _nvcc():
 
 def _deps():
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f != CALLS_SOURCE]
-    files += [os.path.join(ROOT, "include", h) for h in ("spec_verify.h", "spec_decode.h")]
+    files += [os.path.join(ROOT, "include", h) for h in ("spec_verify.h", "spec_decode.h", "spec_tree.h")]
     files.append(os.path.abspath(__file__))
     return files
 

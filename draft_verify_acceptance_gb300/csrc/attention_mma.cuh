@@ -42,6 +42,7 @@
 #pragma once
 
 #include "attention_common.cuh"
+#include "tree_common.cuh"
 
 namespace specv {
 namespace mma {
@@ -178,8 +179,9 @@ __device__ __forceinline__ uint32_t even_word(uint32_t w) {
   return w;
 }
 
-// NB blocks of 8 rows an item.
-template <typename E, int D, int NB>
+// NB blocks of 8 rows an item.  kTree: the queries are a tree's nodes, and see
+// its tokens by TreeSight's bits instead of up to themselves.
+template <typename E, int D, int NB, bool kTree>
 __global__ void __launch_bounds__(Ring<E, D, NB>::kWarps * 32, Ring<E, D, NB>::kCtas) attention_mma_kernel(const AttnArgs a, DivU64 by_page) {
   using L = Ring<E, D, NB>;
   constexpr bool kF32 = L::kF32;
@@ -195,6 +197,7 @@ __global__ void __launch_bounds__(Ring<E, D, NB>::kWarps * 32, Ring<E, D, NB>::k
   __shared__ float s_m[kWarpsM][kRows], s_l[kWarpsM][kRows];
   __shared__ long long s_plan[2 * kWarpsM + 4];
   __shared__ int s_flag;
+  __shared__ TreeSight<kTree ? kRows : 0> s_tree;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t4 = lane & 3;
   const int H = a.cache.heads, G = a.Hq / H, R = a.Q * G;
@@ -272,6 +275,7 @@ __global__ void __launch_bounds__(Ring<E, D, NB>::kWarps * 32, Ring<E, D, NB>::k
       cp_commit();
       page = next;
     }
+    if constexpr (kTree) tree_sight<kRows>(a, b, n - a.Q, row0, rows, tid, kThreadsM, s_tree, [] { __syncthreads(); });
 
     // Queries as operand fragments (rows past the last are zero), and the
     // last token that each of the thread's rows sees.
@@ -309,8 +313,13 @@ __global__ void __launch_bounds__(Ring<E, D, NB>::kWarps * 32, Ring<E, D, NB>::k
         }
       }
 #pragma unroll
-      for (int x = 0; x < 2; ++x) limit[nb][x] = n - a.Q + (row0 + nb * 8 + t4 * 2 + x) / G;
+      for (int x = 0; x < 2; ++x) limit[nb][x] = kTree ? n - a.Q : n - a.Q + (row0 + nb * 8 + t4 * 2 + x) / G;
     }
+    // Does the thread's row x of block nb see token t (which exists)?
+    auto sees_token = [&](int nb, int x, int t) {
+      if constexpr (kTree) return t < limit[nb][x] || s_tree.sees(nb * 8 + t4 * 2 + x, t - limit[nb][x]);
+      else return t <= limit[nb][x];
+    };
 
     float o[KS][NB][4], m[NB][2], l[NB][2];
 #pragma unroll
@@ -386,7 +395,7 @@ __global__ void __launch_bounds__(Ring<E, D, NB>::kWarps * 32, Ring<E, D, NB>::k
         }
       }
       // a step whose 16 tokens exist and are seen by every row needs no mask
-      const bool masked = valid != 0xffffu || t0 + kTokens - 1 > n - a.Q;
+      const bool masked = valid != 0xffffu || t0 + kTokens - 1 > n - a.Q - (kTree ? 1 : 0);
       bool grow = false;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
@@ -395,7 +404,7 @@ __global__ void __launch_bounds__(Ring<E, D, NB>::kWarps * 32, Ring<E, D, NB>::k
           s[nb][x] *= a.scale_log2;
           if (masked) {
             const int r = g + (x >> 1) * 8;
-            if (!((valid >> r) & 1) || t0 + r > limit[nb][x & 1]) s[nb][x] = -INFINITY;
+            if (!((valid >> r) & 1) || !sees_token(nb, x & 1, t0 + r)) s[nb][x] = -INFINITY;
           }
           grow |= s[nb][x] > m[nb][x & 1] + kSlack;
         }
@@ -466,7 +475,7 @@ __global__ void __launch_bounds__(Ring<E, D, NB>::kWarps * 32, Ring<E, D, NB>::k
                 const float lo = __shfl_sync(0xffffffffu, s[nb][x], from);
                 const float hi = __shfl_sync(0xffffffffu, s[nb][x + 2], from);
                 p[x] = t < 8 ? lo : hi;
-                sees[x] = t0 + t <= limit[nb][x];
+                sees[x] = sees_token(nb, x, t0 + t);
               }
 #pragma unroll
               for (int mt = 0; mt < KS; ++mt)
@@ -584,6 +593,13 @@ __global__ void __launch_bounds__(Ring<E, D, NB>::kWarps * 32, Ring<E, D, NB>::k
         oo.z = fmaf(c, v.z, oo.z);
         oo.w = fmaf(c, v.w, oo.w);
       }
+      if constexpr (kTree) {
+        if (s_tree.blind(r)) {  // no node: what it summed over the context is nobody's
+          mm = -INFINITY;
+          ll = 0.f;
+          oo = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+      }
       if (whole) {
         attn_write<D>(a, b, h, row0 + r, d, mm, ll, oo);
       } else {
@@ -601,35 +617,35 @@ __global__ void __launch_bounds__(Ring<E, D, NB>::kWarps * 32, Ring<E, D, NB>::k
   }
 }
 
-template <typename E, int D, int NB>
+template <typename E, int D, int NB, bool kTree>
 cudaError_t prepare() {
-  return cudaFuncSetAttribute(attention_mma_kernel<E, D, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  return cudaFuncSetAttribute(attention_mma_kernel<E, D, NB, kTree>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               Ring<E, D, NB>::kBytes);
 }
-template <typename E, int D, int NB>
+template <typename E, int D, int NB, bool kTree>
 void launch(const AttnArgs& a, int sm_count, cudaStream_t stream) {
   const int grid = sm_count * Ring<E, D, NB>::kCtas < kMaxMmaCtas ? sm_count * Ring<E, D, NB>::kCtas : kMaxMmaCtas;
-  attention_mma_kernel<E, D, NB><<<grid, Ring<E, D, NB>::kWarps * 32, Ring<E, D, NB>::kBytes, stream>>>(
+  attention_mma_kernel<E, D, NB, kTree><<<grid, Ring<E, D, NB>::kWarps * 32, Ring<E, D, NB>::kBytes, stream>>>(
       a, DivU64::make(static_cast<unsigned long long>(a.cache.page_size)));
 }
-template <typename E>
+template <typename E, bool kTree = false>
 cudaError_t prepare_all() {
-  cudaError_t e[] = {prepare<E, 64, 1>(),  prepare<E, 64, 2>(),  prepare<E, 64, 3>(),
-                     prepare<E, 128, 1>(), prepare<E, 128, 2>(), prepare<E, 128, 3>()};
+  cudaError_t e[] = {prepare<E, 64, 1, kTree>(),  prepare<E, 64, 2, kTree>(),  prepare<E, 64, 3, kTree>(),
+                     prepare<E, 128, 1, kTree>(), prepare<E, 128, 2, kTree>(), prepare<E, 128, 3, kTree>()};
   for (cudaError_t x : e)
     if (x != cudaSuccess) return x;
   return cudaSuccess;
 }
 // Items of nb blocks of 8 rows, 1 to 3.
-template <typename E>
+template <typename E, bool kTree = false>
 void launch_rows(const AttnArgs& a, int nb, int sm_count, cudaStream_t stream) {
   switch (nb + (a.cache.head_dim == 128 ? 3 : 0)) {
-    case 1: launch<E, 64, 1>(a, sm_count, stream); break;
-    case 2: launch<E, 64, 2>(a, sm_count, stream); break;
-    case 3: launch<E, 64, 3>(a, sm_count, stream); break;
-    case 4: launch<E, 128, 1>(a, sm_count, stream); break;
-    case 5: launch<E, 128, 2>(a, sm_count, stream); break;
-    default: launch<E, 128, 3>(a, sm_count, stream); break;
+    case 1: launch<E, 64, 1, kTree>(a, sm_count, stream); break;
+    case 2: launch<E, 64, 2, kTree>(a, sm_count, stream); break;
+    case 3: launch<E, 64, 3, kTree>(a, sm_count, stream); break;
+    case 4: launch<E, 128, 1, kTree>(a, sm_count, stream); break;
+    case 5: launch<E, 128, 2, kTree>(a, sm_count, stream); break;
+    default: launch<E, 128, 3, kTree>(a, sm_count, stream); break;
   }
 }
 

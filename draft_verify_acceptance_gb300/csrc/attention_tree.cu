@@ -1,0 +1,36 @@
+// attention_tree.cu -- attention of the nodes of drafted trees over their
+// sequences' paged keys and values (sm_103a).
+//
+//   s_it = scale * q_i . k_t,  out_i = sum_t e^(s_it - m_i) v_t / l_i,
+//   l_i = sum_t e^(s_it - m_i),
+// over the tokens t before the tree, and those of node i's ancestors and its own.
+#include "attention_common.cuh"
+#include "attention_mma.cuh"
+#include "launch_tree.h"
+
+namespace specv {
+
+size_t tree_attention_workspace(int rows, int D, bool bf16) {
+  (void)rows;
+  (void)bf16;
+  return (static_cast<size_t>(kAttnMaxCtas) * 4 +
+          static_cast<size_t>(mma::kMaxMmaCtas) * 2 * mma::kMmaRows * (D + 2) * 4 + 255) & ~static_cast<size_t>(255);
+}
+
+cudaError_t tree_attention_prepare() {
+  cudaError_t e[] = {mma::prepare_all<BF16, true>(), mma::prepare_all<F32, true>()};
+  for (cudaError_t x : e)
+    if (x != cudaSuccess) return x;
+  return cudaSuccess;
+}
+
+cudaError_t launch_tree_attention(const AttnArgs& a, int sm_count, cudaStream_t stream) {
+  const int R = a.Q * (a.Hq / a.cache.heads);
+  // rows in tiles of equal size
+  const int tiles = (R + mma::kMmaRows - 1) / mma::kMmaRows, rows = (R + tiles - 1) / tiles;
+  if (a.cache.bf16) mma::launch_rows<BF16, true>(a, (rows + 7) / 8, sm_count, stream);
+  else mma::launch_rows<F32, true>(a, (rows + 7) / 8, sm_count, stream);
+  return cudaGetLastError();
+}
+
+}  // namespace specv

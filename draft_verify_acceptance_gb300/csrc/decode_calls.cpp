@@ -1,11 +1,11 @@
-// decode_calls.cpp -- the ordinary calls of the decode-side operators, without
-// the interpreter between their checks.
+// decode_calls.cpp -- the ordinary calls of the decode-side and the tree
+// operators, without the interpreter between their checks.
 //
 // A call of a server's step takes the GPU 5 to 15 us, and Python's checks,
 // allocations and argument conversions took 20 to 30.  This module does them in
 // one go for calls on the current device and stream without debug, out= or
 // workspace= that no CUDA graph captures.  Anything else, and any argument that decode.py would refuse,
-// returns NotImplemented: decode.py then makes the call itself, or says what is
+// returns NotImplemented: decode.py (tree.py) then makes the call itself, or says what is
 // wrong with it.  (So no check here is looser than decode.py's, and there are
 // no messages.)  Workspaces are decode.py's own, registered here as it makes
 // them.
@@ -25,7 +25,7 @@
 #include <initializer_list>
 #include <vector>
 
-#include "spec_decode.h"
+#include "spec_tree.h"
 
 namespace {
 
@@ -38,7 +38,12 @@ decltype(&spec_cache_compact_workspace_size) compact_workspace_size;
 decltype(&spec_cache_compact) compact;
 decltype(&spec_filtered_sample_workspace_size) sample_workspace_size;
 decltype(&spec_filtered_sample) sample;
-PyObject *fork_result, *compact_result, *sample_result;
+decltype(&spec_tree_attention_workspace_size) tree_workspace_size;
+decltype(&spec_tree_attention) tree_attention;
+decltype(&spec_cache_append_rotated) append_rotated;
+decltype(&spec_tree_accept) tree_accept;
+decltype(&spec_cache_keep) cache_keep;
+PyObject *fork_result, *compact_result, *sample_result, *accept_result;
 
 struct Workspace {
   long kind, device;
@@ -422,6 +427,180 @@ PyObject* call_sample(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* 
   return result(sample_result, {&tokens, &p, &n_kept, filtered ? &out : nullptr, nullptr});
 }
 
+// A tree's parents: a row a sequence, or one for all.
+bool parents_of(const at::Tensor* t, int64_t B, int64_t N, int device, const int32_t** p, int64_t* stride) {
+  if (!t || t->scalar_type() != at::kInt || !t->is_cuda() || t->get_device() != device) return false;
+  const int64_t dims = t->dim();
+  if (dims < 1 || dims > 2 || t->size(dims - 1) != N || (dims == 2 && t->size(0) != B) || (N > 1 && t->stride(dims - 1) != 1))
+    return false;
+  *p = static_cast<const int32_t*>(t->data_ptr());
+  *stride = dims == 1 ? 0 : B > 1 ? t->stride(0) : N;
+  return *stride == 0 || *stride >= N;
+}
+
+PyObject* call_tree_attention(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kwnames) {
+  static const char* const names[] = {"q", "k_pages", "v_pages", "page_table", "lengths", "parents", "scale", "return_lse"};
+  PyObject* a[8];
+  Where w;
+  if (!arguments(args, n, kwnames, names, 7, 8, a)) return not_done();
+  const at::Tensor *q = tensor(a[0]), *k = tensor(a[1]);
+  if (!q || !k || q->dim() != 4 || !where(*q, &w)) return not_done();
+  spec_cache_t c;
+  if (!cache_of(k, tensor(a[2]), false, w.device, &c) || q->scalar_type() != k->scalar_type()) return not_done();
+  const int64_t B = q->size(0), N = q->size(1), Hq = q->size(2), D = q->size(3);
+  if (D != c.head_dim || c.heads < 1 || Hq % c.heads || (D > 1 && q->stride(3) != 1) || B > INT_MAX ||
+      N > SPEC_TREE_MAX_NODES || Hq > INT_MAX)
+    return not_done();
+  Table t;
+  const int32_t *lengths, *parents;
+  int64_t parents_stride;
+  if (!table_of(tensor(a[3]), B, w.device, &t) || !ints(tensor(a[4]), B, w.device, &lengths) ||
+      !parents_of(tensor(a[5]), B, N, w.device, &parents, &parents_stride))
+    return not_done();
+  float scale = static_cast<float>(1.0 / std::sqrt(static_cast<double>(D)));
+  if (given(a[6]) && !number(a[6], &scale)) return not_done();
+  if (a[7] && a[7] != Py_True && a[7] != Py_False) return not_done();
+  const size_t need = tree_workspace_size(B, N, Hq, c.heads, D, c.dtype);
+  void* ws;
+  size_t bytes;
+  if (need == 0 || !workspace(4, w, need, &ws, &bytes)) return not_done();
+  const at::Tensor out = make({B, N, Hq, D}, q->scalar_type(), w.device);
+  const bool with_lse = a[7] == Py_True;
+  at::Tensor lse;
+  if (with_lse) lse = make({B, N, Hq}, at::kFloat, w.device);
+  if (tree_attention(q->data_ptr(), B > 1 ? q->stride(0) : 0, N > 1 ? q->stride(1) : 0, Hq > 1 ? q->stride(2) : 0, &c, t.p,
+                     t.stride, t.pages, lengths, parents, parents_stride, B, N, Hq, scale, out.data_ptr(),
+                     with_lse ? lse.data_ptr<float>() : nullptr, ws, bytes, reinterpret_cast<spec_stream_t>(w.stream),
+                     nullptr) != SPEC_OK)
+    return not_done();
+  if (!with_lse) return THPVariable_Wrap(out);
+  PyObject *x = THPVariable_Wrap(out), *y = THPVariable_Wrap(lse);
+  PyObject* r = x && y ? PyTuple_Pack(2, x, y) : nullptr;
+  Py_XDECREF(x);
+  Py_XDECREF(y);
+  return r;
+}
+
+// New tokens' rows [lead..., heads, D] at one stride, heads contiguous.
+bool rows_of(const at::Tensor& t, at::IntArrayRef lead, int64_t heads, int64_t D, int64_t T, int64_t* row) {
+  const auto size = t.sizes(), stride = t.strides();
+  const size_t m = lead.size();
+  if (size.size() != m + 2 || size.slice(0, m) != lead || size[m] != heads || size[m + 1] != D) return false;
+  if ((D > 1 && stride[m + 1] != 1) || (heads > 1 && stride[m] != D)) return false;
+  if (T <= 1) *row = heads * D;
+  else if (m == 1) *row = stride[0];
+  else if (lead[0] > 1 && lead[1] > 1 && stride[0] != lead[1] * stride[1]) return false;
+  else *row = lead[1] > 1 ? stride[1] : stride[0];
+  return true;
+}
+
+PyObject* call_append_rotated(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kwnames) {
+  static const char* const names[] = {"k_new", "v_new", "k_pages", "v_pages", "page_table", "lengths", "inv_freq", "q",
+                                      "positions", "starts", "interleaved"};
+  PyObject* a[11];
+  Where w;
+  if (!arguments(args, n, kwnames, names, 10, 11, a)) return not_done();
+  const at::Tensor *kn = tensor(a[0]), *vn = tensor(a[1]), *k = tensor(a[2]), *lens = tensor(a[5]), *freq = tensor(a[6]);
+  if (!kn || !vn || !k || !lens || !freq || lens->dim() != 1 || !where(*kn, &w)) return not_done();
+  spec_cache_t c;
+  if (!cache_of(k, tensor(a[3]), false, w.device, &c) || kn->scalar_type() != k->scalar_type() ||
+      vn->scalar_type() != k->scalar_type() || !vn->is_cuda() || vn->get_device() != w.device || kn->sizes() != vn->sizes() ||
+      kn->strides() != vn->strides())
+    return not_done();
+  const int64_t B = lens->size(0);
+  const bool flat = given(a[9]);
+  if (kn->dim() != (flat ? 3 : 4) || (!flat && kn->size(0) != B)) return not_done();
+  const at::IntArrayRef lead = kn->sizes().slice(0, flat ? 1 : 2);
+  const int64_t T = flat ? lead[0] : lead[0] * lead[1];
+  int64_t row, q_row = 0, Hq = 0;
+  const int32_t *starts = nullptr, *lengths, *positions = nullptr;
+  if (B > INT_MAX || T > INT_MAX || !rows_of(*kn, lead, c.heads, c.head_dim, T, &row)) return not_done();
+  if (flat && !ints(tensor(a[9]), B + 1, w.device, &starts)) return not_done();
+  if (freq->scalar_type() != at::kFloat || freq->dim() != 1 || !freq->is_cuda() || freq->get_device() != w.device ||
+      !freq->is_contiguous() || freq->size(0) > 1024)
+    return not_done();
+  if (given(a[8])) {
+    const at::Tensor* p = tensor(a[8]);
+    if (!p || p->scalar_type() != at::kInt || p->sizes() != lead || !p->is_cuda() || p->get_device() != w.device ||
+        !p->is_contiguous())
+      return not_done();
+    positions = static_cast<const int32_t*>(p->data_ptr());
+  }
+  const at::Tensor* q = nullptr;
+  if (given(a[7])) {
+    q = tensor(a[7]);
+    if (!q || q->scalar_type() != k->scalar_type() || q->dim() != kn->dim() || !q->is_cuda() || q->get_device() != w.device)
+      return not_done();
+    Hq = q->size(-2);
+    if (Hq > INT_MAX || !rows_of(*q, lead, Hq, c.head_dim, T, &q_row)) return not_done();
+  }
+  if (a[10] && a[10] != Py_True && a[10] != Py_False) return not_done();
+  Table t;
+  if (!table_of(tensor(a[4]), B, w.device, &t) || !ints(lens, B, w.device, &lengths)) return not_done();
+  at::Tensor out;
+  if (q) out = make(q->sizes(), q->scalar_type(), w.device);
+  if (append_rotated(kn->data_ptr(), vn->data_ptr(), row, T, starts, q ? q->data_ptr() : nullptr, q_row, Hq,
+                     q ? out.data_ptr() : nullptr, Hq * c.head_dim, positions, freq->data_ptr<float>(), freq->size(0),
+                     a[10] == Py_True, &c, t.p, t.stride, t.pages, lengths, B, reinterpret_cast<spec_stream_t>(w.stream),
+                     nullptr) != SPEC_OK)
+    return not_done();
+  written(k, a[3]);
+  if (!q) Py_RETURN_NONE;
+  return THPVariable_Wrap(out);
+}
+
+// A contiguous int32 [B, N].
+bool ints2(const at::Tensor* t, int64_t B, int64_t N, int device, const int32_t** p) {
+  if (!t || t->scalar_type() != at::kInt || t->dim() != 2 || t->size(0) != B || t->size(1) != N || !t->is_cuda() ||
+      t->get_device() != device || !t->is_contiguous())
+    return false;
+  *p = static_cast<const int32_t*>(t->data_ptr());
+  return true;
+}
+
+PyObject* call_accept(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kwnames) {
+  static const char* const names[] = {"tokens", "parents", "drawn"};
+  PyObject* a[3];
+  Where w;
+  if (!arguments(args, n, kwnames, names, 3, 3, a)) return not_done();
+  const at::Tensor* x = tensor(a[0]);
+  if (!x || x->dim() != 2 || !where(*x, &w)) return not_done();
+  const int64_t B = x->size(0), N = x->size(1);
+  const int32_t *tokens, *parents, *drawn;
+  int64_t parents_stride;
+  if (B > INT_MAX || N > SPEC_TREE_MAX_NODES || !ints2(x, B, N, w.device, &tokens) ||
+      !parents_of(tensor(a[1]), B, N, w.device, &parents, &parents_stride) || !ints2(tensor(a[2]), B, N, w.device, &drawn))
+    return not_done();
+  Results r({B, B * N, B * N}, w.device);
+  const at::Tensor len = r.next({B}, at::kInt), out = r.next({B, N}, at::kInt), path = r.next({B, N}, at::kInt);
+  if (tree_accept(tokens, parents, parents_stride, drawn, B, N, len.data_ptr<int>(), out.data_ptr<int>(), path.data_ptr<int>(),
+                  reinterpret_cast<spec_stream_t>(w.stream), nullptr) != SPEC_OK)
+    return not_done();
+  return result(accept_result, {&len, &out, &path, nullptr});
+}
+
+PyObject* call_keep(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kwnames) {
+  static const char* const names[] = {"k_pages", "v_pages", "page_table", "lengths", "path"};
+  PyObject* a[5];
+  Where w;
+  if (!arguments(args, n, kwnames, names, 5, 5, a)) return not_done();
+  const at::Tensor *k = tensor(a[0]), *lens = tensor(a[3]), *p = tensor(a[4]);
+  if (!k || !lens || !p || lens->dim() != 1 || p->dim() != 2 || !where(*k, &w)) return not_done();
+  spec_cache_t c;
+  Table t;
+  const int32_t *lengths, *path;
+  const int64_t B = lens->size(0), N = p->size(1);
+  if (B > INT_MAX || N > INT_MAX || !cache_of(k, tensor(a[1]), true, w.device, &c) ||
+      !table_of(tensor(a[2]), B, w.device, &t) || !ints(lens, B, w.device, &lengths) || !ints2(p, B, N, w.device, &path))
+    return not_done();
+  const at::Tensor out = make({B}, at::kInt, w.device);
+  if (cache_keep(&c, t.p, t.stride, t.pages, lengths, B, path, N, out.data_ptr<int>(),
+                 reinterpret_cast<spec_stream_t>(w.stream), nullptr) != SPEC_OK)
+    return not_done();
+  written(k, a[1]);
+  return THPVariable_Wrap(out);
+}
+
 // C++ exceptions (an allocation that fails, say) are decode.py's to meet again
 // and report.
 template <PyObject* (*kCall)(PyObject*, PyObject* const*, Py_ssize_t, PyObject*)>
@@ -457,6 +636,21 @@ PyObject* bind(PyObject*, PyObject* args) {
   Py_RETURN_NONE;
 }
 
+PyObject* bind_tree(PyObject*, PyObject* args) {
+  unsigned long long f[5];
+  PyObject* r;
+  if (!PyArg_ParseTuple(args, "(KKKKK)O", f, f + 1, f + 2, f + 3, f + 4, &r)) return nullptr;
+  int i = 0;
+  auto take = [&](auto& fn) { fn = reinterpret_cast<std::decay_t<decltype(fn)>>(f[i++]); };
+  take(tree_workspace_size);
+  take(tree_attention);
+  take(append_rotated);
+  take(tree_accept);
+  take(cache_keep);
+  accept_result = Py_NewRef(r);
+  Py_RETURN_NONE;
+}
+
 PyObject* register_workspace(PyObject*, PyObject* args) {
   Workspace w;
   unsigned long long p, bytes;
@@ -473,12 +667,17 @@ PyObject* register_workspace(PyObject*, PyObject* args) {
 }
 
 PyMethodDef methods[] = {{"bind", bind, METH_VARARGS, nullptr},
+                         {"bind_tree", bind_tree, METH_VARARGS, nullptr},
                          {"register_workspace", register_workspace, METH_VARARGS, nullptr},
                          {"paged_attention", nullptr, 0, nullptr},
                          {"cache_append", nullptr, 0, nullptr},
                          {"cache_fork", nullptr, 0, nullptr},
                          {"cache_compact", nullptr, 0, nullptr},
                          {"filtered_sample", nullptr, 0, nullptr},
+                         {"tree_attention", nullptr, 0, nullptr},
+                         {"cache_append_rotated", nullptr, 0, nullptr},
+                         {"tree_accept", nullptr, 0, nullptr},
+                         {"cache_keep", nullptr, 0, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_decode_calls", nullptr, -1, methods};
 
@@ -489,10 +688,12 @@ PyMODINIT_FUNC PyInit__decode_calls() {
     return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f));
   };
   PyObject* (*calls[])(PyObject*, PyObject* const*, Py_ssize_t, PyObject*) = {
-      guarded<call_attention>, guarded<call_append>, guarded<call_fork>, guarded<call_compact>, guarded<call_sample>};
-  for (int i = 0; i < 5; ++i) {
-    methods[2 + i].ml_meth = as(calls[i]);
-    methods[2 + i].ml_flags = METH_FASTCALL | METH_KEYWORDS;
+      guarded<call_attention>, guarded<call_append>, guarded<call_fork>, guarded<call_compact>, guarded<call_sample>,
+      guarded<call_tree_attention>, guarded<call_append_rotated>, guarded<call_accept>, guarded<call_keep>};
+  constexpr int kFirst = 3;  // in `methods`
+  for (int i = 0; i < 9; ++i) {
+    methods[kFirst + i].ml_meth = as(calls[i]);
+    methods[kFirst + i].ml_flags = METH_FASTCALL | METH_KEYWORDS;
   }
   return PyModule_Create(&module);
 }

@@ -46,6 +46,9 @@ struct AttnArgs {
   unsigned int* counters;
   float* partials;
   int32_t* status;
+  // trees (attention_tree.cu): the queries are nodes
+  const int32_t* parents = nullptr;  // [B, Q]
+  long long parents_stride = 0;      // entries between rows
 };
 
 struct SampleArgs {

@@ -1,0 +1,64 @@
+// tree_common.cuh -- what a tree's nodes see of the tree (sm_103a).
+//
+// Node i sees its ancestors and itself: a bit set of up to kMaxNodes bits, made
+// by following parents, which lie at lower indexes, so a walk ends.
+#pragma once
+
+#include "device_common.cuh"
+#include "launch_tree.h"
+
+namespace specv {
+
+// The bit sets of an item's rows.
+template <int kRows>
+struct TreeSight {
+  int32_t parents[kMaxNodes];
+  uint32_t bits[kRows][kNodeWords + 1];  // (the odd pitch spreads rows over the banks)
+  uint8_t none[kRows];
+  __device__ __forceinline__ bool sees(int row, int u) const { return (bits[row][(u >> 5) & (kNodeWords - 1)] >> (u & 31)) & 1; }
+  __device__ __forceinline__ bool blind(int row) const { return none[row] != 0; }
+};
+template <>
+struct TreeSight<0> {};
+
+// The set of node i as words; false when it is no node.
+__device__ __forceinline__ bool tree_line(const int32_t* parents, int i, uint32_t (&w)[kNodeWords]) {
+#pragma unroll
+  for (int x = 0; x < kNodeWords; ++x) w[x] = 0;
+  for (;;) {
+#pragma unroll
+    for (int x = 0; x < kNodeWords; ++x) w[x] |= (i >> 5) == x ? 1u << (i & 31) : 0u;
+    const int p = parents[i];
+    if (p < 0 || p >= i) return p == -1;
+    i = p;
+  }
+}
+
+// Fills `sight` for rows [row0, row0 + rows) of a cache head (row = node * G +
+// query head of the group) of sequence b, whose tree starts at token `base`, by
+// `count` threads that `sync` holds together.
+template <int kRows, typename Sync>
+__device__ __forceinline__ void tree_sight(const AttnArgs& a, int b, int base, int row0, int rows, int tid, int count,
+                                           TreeSight<kRows>& sight, Sync sync) {
+  const int32_t* parents = a.parents + b * a.parents_stride;
+  bool bad = false;
+  for (int i = tid; i < a.Q; i += count) {
+    const int p = __ldg(parents + i);
+    bad |= p >= i;
+    sight.parents[i] = p;
+  }
+  if (bad && a.status) atomicOr(a.status, kDataTreeParent);
+  sync();
+  const int G = a.Hq / a.cache.heads;
+  for (int r = tid; r < kRows; r += count) {
+    const int i = (row0 + min(r, rows - 1)) / G;
+    uint32_t w[kNodeWords];
+    const bool node = tree_line(sight.parents, i, w) && base + i >= 0;
+#pragma unroll
+    for (int x = 0; x < kNodeWords; ++x) sight.bits[r][x] = w[x];
+    sight.none[r] = !node;
+  }
+  sync();
+}
+
+}  // namespace specv

@@ -79,7 +79,7 @@ _DTYPES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
 _ws_lock = threading.Lock()
 _ws = {}
 # the native calls' number of a kind of workspace, and how many of its first bytes are zero between calls
-_KINDS = {"attention": (0, 2048), "fork": (1, 0), "compact": (2, 0), "sample": (3, 64)}
+_KINDS = {"attention": (0, 2048), "fork": (1, 0), "compact": (2, 0), "sample": (3, 64), "tree": (4, 2048)}
 
 
 class ForkResult(NamedTuple):
