@@ -19,7 +19,7 @@ LIB = os.path.join(HERE, "libspecverify.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["spec_verify.cu", "verify_greedy.cu", "verify_sample.cu", "verify_sample_fused.cu", "verify_sample_seq.cu", "verify_sample_ee.cu", "verify_sample_2p.cu", "verify_draft_sample.cu", "verify_scd.cu", "rejection_cut.cu",
            "spec_verify_static.cu", "spec_decode.cu", "attention.cu", "attention_tc.cu", "cache_pages.cu", "filtered_sample.cu",
-           "spec_tree.cu", "attention_tree.cu", "tree_cache.cu"]
+           "spec_tree.cu", "attention_tree.cu", "attention_tree_tc.cu", "tree_cache.cu"]
 
 
 CALLS = os.path.join(HERE, "_decode_calls.so")

@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(Ring<E, D, NB>::kWarps * 32, Ring<E, D, NB>::k
       cp_commit();
       page = next;
     }
-    if constexpr (kTree) tree_sight<kRows>(a, b, n - a.Q, row0, rows, tid, kThreadsM, s_tree, [] { __syncthreads(); });
+    if constexpr (kTree) tree_sight<kRows>(a, b, n - a.Q, row0, row0 + rows - 1, tid, kThreadsM, s_tree, [] { __syncthreads(); });
 
     // Queries as operand fragments (rows past the last are zero), and the
     // last token that each of the thread's rows sees.

@@ -10,15 +10,22 @@
 
 namespace specv {
 
+// bf16 items of more than 24 rows a cache head (R = N * Hq / Hkv) go to
+// attention_tree_tc.cuh, the rest to attention_mma.cuh, in tiles of at most 24 rows
+// that each read K and V again (through L2).
+namespace {
+bool on_tc(int rows, bool bf16) { return bf16 && rows > mma::kMmaRows; }
+}  // namespace
+
 size_t tree_attention_workspace(int rows, int D, bool bf16) {
-  (void)rows;
-  (void)bf16;
-  return (static_cast<size_t>(kAttnMaxCtas) * 4 +
-          static_cast<size_t>(mma::kMaxMmaCtas) * 2 * mma::kMmaRows * (D + 2) * 4 + 255) & ~static_cast<size_t>(255);
+  const size_t bytes = on_tc(rows, bf16) ? tree_tc_workspace(rows, D)
+                                         : static_cast<size_t>(kAttnMaxCtas) * 4 + static_cast<size_t>(mma::kMaxMmaCtas) * 2 *
+                                                                                       mma::kMmaRows * (D + 2) * 4;
+  return (bytes + 255) & ~static_cast<size_t>(255);
 }
 
 cudaError_t tree_attention_prepare() {
-  cudaError_t e[] = {mma::prepare_all<BF16, true>(), mma::prepare_all<F32, true>()};
+  cudaError_t e[] = {mma::prepare_all<BF16, true>(), mma::prepare_all<F32, true>(), tree_tc_prepare()};
   for (cudaError_t x : e)
     if (x != cudaSuccess) return x;
   return cudaSuccess;
@@ -28,7 +35,8 @@ cudaError_t launch_tree_attention(const AttnArgs& a, int sm_count, cudaStream_t 
   const int R = a.Q * (a.Hq / a.cache.heads);
   // rows in tiles of equal size
   const int tiles = (R + mma::kMmaRows - 1) / mma::kMmaRows, rows = (R + tiles - 1) / tiles;
-  if (a.cache.bf16) mma::launch_rows<BF16, true>(a, (rows + 7) / 8, sm_count, stream);
+  if (on_tc(R, a.cache.bf16)) tree_tc_launch(a, R, sm_count, stream);
+  else if (a.cache.bf16) mma::launch_rows<BF16, true>(a, (rows + 7) / 8, sm_count, stream);
   else mma::launch_rows<F32, true>(a, (rows + 7) / 8, sm_count, stream);
   return cudaGetLastError();
 }

@@ -13,6 +13,10 @@ constexpr int kNodeWords = kMaxNodes / 32;
 
 size_t tree_attention_workspace(int rows, int D, bool bf16);  // rows: of a cache head
 cudaError_t tree_attention_prepare();
+// tcgen05 kernels (attention_tree_tc.cuh).
+size_t tree_tc_workspace(int rows, int D);
+cudaError_t tree_tc_prepare();
+void tree_tc_launch(const AttnArgs& a, int rows, int sm_count, cudaStream_t stream);
 cudaError_t launch_tree_attention(const AttnArgs& a, int sm_count, cudaStream_t stream);
 
 struct RotatedAppendArgs {

@@ -16,6 +16,14 @@ struct TreeSight {
   uint32_t bits[kRows][kNodeWords + 1];  // (the odd pitch spreads rows over the banks)
   uint8_t none[kRows];
   __device__ __forceinline__ bool sees(int row, int u) const { return (bits[row][(u >> 5) & (kNodeWords - 1)] >> (u & 31)) & 1; }
+  // Bit y: does the row see token u0 + y, counted from the tree's first (those before it it does).
+  __device__ __forceinline__ uint32_t window(int row, int u0) const {
+    if (u0 <= -32) return 0xffffffffu;
+    if (u0 < 0) return ((1u << -u0) - 1u) | (bits[row][0] << -u0);
+    const int w = u0 >> 5;
+    const uint32_t low = w < kNodeWords ? bits[row][w] : 0u, high = w + 1 < kNodeWords ? bits[row][w + 1] : 0u;
+    return __funnelshift_r(low, high, u0);
+  }
   __device__ __forceinline__ bool blind(int row) const { return none[row] != 0; }
 };
 template <>
@@ -34,11 +42,11 @@ __device__ __forceinline__ bool tree_line(const int32_t* parents, int i, uint32_
   }
 }
 
-// Fills `sight` for rows [row0, row0 + rows) of a cache head (row = node * G +
-// query head of the group) of sequence b, whose tree starts at token `base`, by
-// `count` threads that `sync` holds together.
+// Fills `sight` for rows row0, row0 + 1, ... of a cache head (row = node * G + query
+// head of the group; those behind row `last` are as it) of sequence b, whose
+// tree starts at token `base`, by `count` threads that `sync` holds together.
 template <int kRows, typename Sync>
-__device__ __forceinline__ void tree_sight(const AttnArgs& a, int b, int base, int row0, int rows, int tid, int count,
+__device__ __forceinline__ void tree_sight(const AttnArgs& a, int b, int base, int row0, int last, int tid, int count,
                                            TreeSight<kRows>& sight, Sync sync) {
   const int32_t* parents = a.parents + b * a.parents_stride;
   bool bad = false;
@@ -51,7 +59,7 @@ __device__ __forceinline__ void tree_sight(const AttnArgs& a, int b, int base, i
   sync();
   const int G = a.Hq / a.cache.heads;
   for (int r = tid; r < kRows; r += count) {
-    const int i = (row0 + min(r, rows - 1)) / G;
+    const int i = min(row0 + r, last) / G;
     uint32_t w[kNodeWords];
     const bool node = tree_line(sight.parents, i, w) && base + i >= 0;
 #pragma unroll
