@@ -35,8 +35,8 @@ cudaError_t launch_tree_attention(const AttnArgs& a, int sm_count, cudaStream_t 
   const int R = a.Q * (a.Hq / a.cache.heads);
   // rows in tiles of equal size
   const int tiles = (R + mma::kMmaRows - 1) / mma::kMmaRows, rows = (R + tiles - 1) / tiles;
-  if (on_tc(R, a.cache.bf16)) tree_tc_launch(a, R, sm_count, stream);
-  else if (a.cache.bf16) mma::launch_rows<BF16, true>(a, (rows + 7) / 8, sm_count, stream);
+  if (on_tc(R, a.cache.bf16)) return tree_tc_launch(a, R, sm_count, stream);
+  if (a.cache.bf16) mma::launch_rows<BF16, true>(a, (rows + 7) / 8, sm_count, stream);
   else mma::launch_rows<F32, true>(a, (rows + 7) / 8, sm_count, stream);
   return cudaGetLastError();
 }

@@ -4,7 +4,8 @@
 namespace specv {
 
 size_t tree_tc_workspace(int rows, int D) {
-  return static_cast<size_t>(kAttnMaxCtas) * 4 + static_cast<size_t>(ttc::kMaxCtas) * 2 * (rows > 128 ? 256 : 128) * (D + 2) * 4;
+  if (D == 64) return rows > 128 ? ttc::workspace<64, true>() : ttc::workspace<64, false>();
+  return rows > 128 ? ttc::workspace<128, true>() : ttc::workspace<128, false>();
 }
 
 cudaError_t tree_tc_prepare() {
@@ -14,10 +15,10 @@ cudaError_t tree_tc_prepare() {
   return cudaSuccess;
 }
 
-void tree_tc_launch(const AttnArgs& a, int rows, int sm_count, cudaStream_t stream) {
-  const bool dual = rows > 128;
-  if (a.cache.head_dim == 64) dual ? ttc::launch<64, true>(a, sm_count, stream) : ttc::launch<64, false>(a, sm_count, stream);
-  else dual ? ttc::launch<128, true>(a, sm_count, stream) : ttc::launch<128, false>(a, sm_count, stream);
+cudaError_t tree_tc_launch(const AttnArgs& a, int rows, int sm_count, cudaStream_t stream) {
+  if (a.cache.head_dim == 64)
+    return rows > 128 ? ttc::launch<64, true>(a, sm_count, stream) : ttc::launch<64, false>(a, sm_count, stream);
+  return rows > 128 ? ttc::launch<128, true>(a, sm_count, stream) : ttc::launch<128, false>(a, sm_count, stream);
 }
 
 }  // namespace specv

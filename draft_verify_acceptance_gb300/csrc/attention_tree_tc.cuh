@@ -15,16 +15,22 @@
 // both over every tile;  else one for the even tiles and one for the odd ones,
 // joined at the item's end.
 //
-// One block per SM.  Warps 0-3 and 4-7: the streams' softmax.  Warps 8 and 9 copy K
-// and V of the tiles into a ring of slots, across item boundaries, in 16-byte
-// pieces that arrive on the slot's barrier by themselves, so any page size and
-// strides.  Warp 10 issues the scores' products, warp 11 the outputs'.
+// One block per SM.  Warps 0-3 and 4-7: the streams' softmax.  Warps 8-11 copy K
+// and V of the tiles, 16 tokens each, into a ring of slots, across item boundaries,
+// in 16-byte pieces that arrive on the slot's barrier by themselves, so any page
+// size and strides.  Warp 12 issues the scores' products, warp 13 the outputs'.
+//
+// Parts of an item that blocks' ranges cut are left in the workspace and joined by
+// a dependent kernel over all SMs, in block order (one block would have to read
+// up to 133 KB a part).
 #pragma once
 
 #include "attention_common.cuh"
 #include "attention_mma.cuh"
 #include "attention_tc.cuh"
 #include "tree_common.cuh"
+
+#include <type_traits>
 
 namespace specv {
 namespace ttc {
@@ -45,8 +51,13 @@ using tc::tmem_st_done;
 
 constexpr int kTile = 64;        // tokens
 constexpr int kSoft = 256;       // softmax threads, 128 a stream
-constexpr int kLoad = 64;        // loader threads
-constexpr int kThreadsR = kSoft + kLoad + 64;
+constexpr int kLoadWarps = 4, kLoadTokens = kTile / kLoadWarps;  // loader warps, a warp's tokens of a tile
+constexpr int kThreadsR = kSoft + kLoadWarps * 32 + 128;           // (two warps of the last four are idle)
+// Registers a thread: 512 x 128 at the launch, then shared out by groups of four
+// warps, 2 x 128 x (176 + 80) = 512 x 128.
+constexpr int kSoftRegs = 176, kOtherRegs = 80;
+static_assert(kSoft * kSoftRegs + (kThreadsR - kSoft) * kOtherRegs <= 65536 && kThreadsR * 128 <= 65536, "registers");
+constexpr int kScores = 8 + kLoadWarps, kOutputs = kScores + 1;   // the warps that issue products
 constexpr float kSlackR = 8.f;   // how far (log2) a score may pass the reference
 constexpr int kEndR = 6;         // steps that an item's start and end count as
 constexpr int kMaxCtas = 160;
@@ -64,33 +75,90 @@ struct Lay {
   static_assert(kSlots >= 8 && kSlots / 2 + 4 < kAhead, "the ring");
 };
 
+// An item, or this block's part of it, as the softmax warps need it (the walk's
+// own state would take a third of their registers).
+struct Item {
+  int any;   // 0: there are no more
+  int end;   // block that has its last tile
+  int b, h, n, rt, row0, rows, tile0, tile1, tiles;
+  __device__ __forceinline__ bool whole() const { return tile0 == 0 && tile1 == tiles; }
+};
+constexpr int kItems = 4;  // kept: more than a stream can be behind
+
+// The item whose first tile a block has and whose last one another block; rows 0:
+// there is none.
+struct __align__(8) Join {
+  int b, h, row0, rows, end, pad;
+};
+
 template <int D, bool kDual>
 struct Shared {
   unsigned long long full[Lay<D, kDual>::kSlots], empty[Lay<D, kDual>::kSlots];
   unsigned long long s_full[2][2], p_full[2][2], pv_done[2][2], q_full[2] /* one for both streams of shared rows */, done[2];
-  long long off[2][kTile];    // byte offsets of a tile's tokens, -1: none
-  uint32_t valid[kAhead][2];  // tokens that exist, by tile
+  unsigned long long item_ready[kItems];
+  Item item[kItems];
+  __align__(8) uint16_t valid[kAhead][kLoadWarps];  // tokens that exist, by tile
   long long q_off[2][128];    // of the next item's rows, bytes
   TreeSight<128> sight[2];
   float m[2][128], l[2][128];
   int odd[kOdd];              // the item has values that are not finite and not every row sees
   uint32_t tmem;
   int dead;                   // a wait ran out: nothing waits any more
-  int last;
   long long plan[2 * (kThreadsR / 32) + 4];
 };
 
-// O += P V with P in TMEM.
-__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+// The products of a tile, issued by one lane in one go (a product of its own, with
+// its election and its descriptors, took ten instructions).
+// S = Q K^T: steps of 16 dimensions, 64 a half of the operands.
+template <int D>
+__device__ __forceinline__ void scores_mma(uint32_t d, uint64_t a, uint64_t b) {
+  constexpr uint32_t kKind = tc::instruction<kTile>(false, false);
+  if constexpr (D == 128)
+    asm volatile(
+        "{\n\t.reg .pred p, q, e;\n\t.reg .b64 a, b;\n\tsetp.ne.u32 p, 0, 0;\n\tsetp.eq.u32 q, 0, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+        "add.s64 a, %1, 2;\n\tadd.s64 b, %2, 2;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, q;\n\t"
+        "add.s64 a, %1, 4;\n\tadd.s64 b, %2, 4;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, q;\n\t"
+        "add.s64 a, %1, 6;\n\tadd.s64 b, %2, 6;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, q;\n\t"
+        "add.s64 a, %1, 1024;\n\tadd.s64 b, %2, 512;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, q;\n\t"
+        "add.s64 a, %1, 1026;\n\tadd.s64 b, %2, 514;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, q;\n\t"
+        "add.s64 a, %1, 1028;\n\tadd.s64 b, %2, 516;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, q;\n\t"
+        "add.s64 a, %1, 1030;\n\tadd.s64 b, %2, 518;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, q;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(kKind)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p, q, e;\n\t.reg .b64 a, b;\n\tsetp.ne.u32 p, 0, 0;\n\tsetp.eq.u32 q, 0, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+        "add.s64 a, %1, 2;\n\tadd.s64 b, %2, 2;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, q;\n\t"
+        "add.s64 a, %1, 4;\n\tadd.s64 b, %2, 4;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, q;\n\t"
+        "add.s64 a, %1, 6;\n\tadd.s64 b, %2, 6;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, q;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(kKind)
+        : "memory");
+}
+// O += P V: steps of 16 tokens; P lies as hi, lo of 32 tokens, hi, lo of the other 32.
+template <int D>
+__device__ __forceinline__ void outputs_mma(uint32_t d, uint32_t p, uint64_t v, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p, e;\n\tsetp.ne.u32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u)
+      "{\n\t.reg .pred p, q, e;\n\t.reg .b64 b;\n\t.reg .b32 a;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.eq.u32 q, 0, 0;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+      "add.s32 a, %1, 16;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], %2, %3, q;\n\t"
+      "add.s64 b, %2, 128;\n\t"
+      "add.s32 a, %1, 8;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, q;\n\t"
+      "add.s32 a, %1, 24;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, q;\n\t"
+      "add.s64 b, %2, 256;\n\t"
+      "add.s32 a, %1, 32;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, q;\n\t"
+      "add.s32 a, %1, 48;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, q;\n\t"
+      "add.s64 b, %2, 384;\n\t"
+      "add.s32 a, %1, 40;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, q;\n\t"
+      "add.s32 a, %1, 56;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, q;\n\t}" ::"r"(d),
+      "r"(p), "l"(v), "r"(tc::instruction<D>(false, true)), "r"(add ? 1u : 0u)
       : "memory");
 }
 #define SPEC_R8(x, i) "=r"(x[i]), "=r"(x[i + 1]), "=r"(x[i + 2]), "=r"(x[i + 3]), "=r"(x[i + 4]), "=r"(x[i + 5]), "=r"(x[i + 6]), "=r"(x[i + 7])
 #define SPEC_I8(x, i) "r"(x[i]), "r"(x[i + 1]), "r"(x[i + 2]), "r"(x[i + 3]), "r"(x[i + 4]), "r"(x[i + 5]), "r"(x[i + 6]), "r"(x[i + 7])
-// 32 columns of the warp's lanes (the wait in the same statement: no use comes before it).
+// Columns of the warp's lanes (the wait in the same statement: no use comes before it).
 __device__ __forceinline__ void ld32(uint32_t (&r)[32], uint32_t at) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
@@ -99,12 +167,11 @@ __device__ __forceinline__ void ld32(uint32_t (&r)[32], uint32_t at) {
       : "r"(at)
       : "memory");
 }
-__device__ __forceinline__ void ld64(uint32_t (&r)[64], uint32_t at) {
+__device__ __forceinline__ void ld16(uint32_t (&r)[16], uint32_t at) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
-      "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,"
-      "%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n\ttcgen05.wait::ld.sync.aligned;"
-      : SPEC_R8(r, 0), SPEC_R8(r, 8), SPEC_R8(r, 16), SPEC_R8(r, 24), SPEC_R8(r, 32), SPEC_R8(r, 40), SPEC_R8(r, 48), SPEC_R8(r, 56)
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : SPEC_R8(r, 0), SPEC_R8(r, 8)
       : "r"(at)
       : "memory");
 }
@@ -114,15 +181,43 @@ __device__ __forceinline__ void st32(uint32_t at, const uint32_t (&r)[32]) {
       "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::SPEC_I8(r, 0), SPEC_I8(r, 8), SPEC_I8(r, 16), SPEC_I8(r, 24), "r"(at)
       : "memory");
 }
+__device__ __forceinline__ void st16(uint32_t at, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::SPEC_I8(r, 0),
+      SPEC_I8(r, 8), "r"(at)
+      : "memory");
+}
 #undef SPEC_R8
 #undef SPEC_I8
 
+// Two fp32 operations at a time.
+__device__ __forceinline__ uint64_t pair(uint32_t x, uint32_t y) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(x), "r"(y));
+  return d;
+}
+__device__ __forceinline__ void split(uint64_t d, float& x, float& y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(d)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 __device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
-__device__ __forceinline__ void load_sync() { asm volatile("bar.sync 2, 64;" ::: "memory"); }
 __device__ __forceinline__ void stream_sync(int s) { asm volatile("bar.sync %0, 128;" ::"r"(3 + s) : "memory"); }
 
 template <int D, bool kDual>
-__global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const AttnArgs a, DivU64 by_page) {
+__global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const AttnArgs a, DivU64 by_page, Join* joins) {
   using L = Lay<D, kDual>;
   using Walk = AttnWalk<kTile, kEndR, L::kRows>;
   constexpr int kSlots = L::kSlots, kHalf = L::kHalf, kChunks = D / 8;  // 16-byte pieces of a token
@@ -133,24 +228,29 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
   char* q_s = smem + kSlots * L::kSlot;  // [128-row tiles][halves][128][128 bytes]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
+  // (short: it stands in many places, and the roles' code shares the instruction caches)
   auto wait = [&](unsigned long long* bar, uint32_t parity) {
-    if (*reinterpret_cast<volatile int*>(&sh.dead)) return;
-    bool gave_up = false;
+    int polls = 1 << 16;
 #ifdef SPEC_DEBUG
     // (a test's way to a wait that ran out: a bit of the status word that it passes)
-    gave_up = blockIdx.x == 0 && a.status && (*reinterpret_cast<volatile int32_t*>(a.status) >> 30) != 0;
+    if (blockIdx.x == 0 && a.status && (*reinterpret_cast<volatile int32_t*>(a.status) >> 30) != 0) polls = 0;
+    else
 #endif
-    if (gave_up || !mbar_wait_sleep(bar, parity)) {
-      *reinterpret_cast<volatile int*>(&sh.dead) = 1;
-      if (a.status) atomicOr(a.status, kWaitTimeout);
-    }
+    if (mbar_try_wait_sleep(bar, parity, 20000u)) return;
+#pragma unroll 1
+    while (--polls > 0 && !*reinterpret_cast<volatile int*>(&sh.dead))
+      if (mbar_try_wait_sleep(bar, parity, 20000u)) return;
+    *reinterpret_cast<volatile int*>(&sh.dead) = 1;
+    if (a.status) atomicOr(a.status, kWaitTimeout);
   };
 
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (tid == 0) joins[blockIdx.x] = {0, 0, 0, 0, 0, 0};
   const AttnPlan plan = attn_plan<kTile, kEndR, kThreadsR>(
       a, a.cache.heads * ((a.Q * (a.Hq / a.cache.heads) + L::kRows - 1) / L::kRows), 4, sh.plan);
   if (tid == 0) {
     for (int i = 0; i < kSlots; ++i) {
-      mbar_init(&sh.full[i], kLoad + 1);
+      mbar_init(&sh.full[i], kLoadWarps * 33);
       mbar_init(&sh.empty[i], 1);
     }
     for (int s = 0; s < 2; ++s) {
@@ -162,79 +262,81 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
       mbar_init(&sh.q_full[s], 128);
       mbar_init(&sh.done[s], 1);
     }
+    for (int i = 0; i < kItems; ++i) mbar_init(&sh.item_ready[i], 1);
     for (int i = 0; i < kOdd; ++i) sh.odd[i] = 0;
     sh.dead = 0;
     fence_barrier_init();
   }
-  if (warp == 11) tmem_alloc(&sh.tmem, kCols);
+  if (warp == kOutputs) tmem_alloc(&sh.tmem, kCols);
   tc_before();
   __syncthreads();
   tc_after();
   const uint32_t tmem = sh.tmem;
-  Walk at(a, plan);
 
-  if (warp == 8 || warp == 9) {
+  auto item = [&](int k) -> const Item& {
+    wait(&sh.item_ready[k % kItems], (k / kItems) & 1);
+    return sh.item[k % kItems];
+  };
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+  if (warp < kScores) {
     // ---- K and V of each tile, in turn -----------------------------------
-    const int lt = tid - kSoft, S = a.cache.page_size;
-    const int chunk = lt % kChunks, r0 = lt / kChunks;
-    constexpr int kStep = kLoad / kChunks, kPasses = kTile / kStep;
+    const int lw = warp - 8, S = a.cache.page_size;
+    const int chunk = lane % kChunks, r0 = lane / kChunks;
+    constexpr int kStep = 32 / kChunks, kPasses = kLoadTokens / kStep;
+    const bool in_page = S % kLoadTokens == 0;  // a warp's tokens of a tile lie in one page
+    Walk at(a, plan);
     // The tile whose pages are looked up, one ahead of the copies: the table's
     // entries are on their way while the tile before is copied.
-    Walk ahead(a, plan);
-    bool more = ahead.next();
-    int ahead_tile = more ? ahead.tile0 : 0;
-    int page, place, head = 0;  // place: token in the page, -1: past the end
+    bool more = at.next();
+    int tile = more ? at.tile0 : 0;
+    int page = -1, place = -1, head = 0;  // of token lane % 16; place: token in the page, -1: past the end
     auto look_up = [&]() {
-      head = ahead.h;
-      const int t = ahead_tile * kTile + lt;
+      head = at.h;
+      const int t = tile * kTile + lw * kLoadTokens + (lane & (kLoadTokens - 1));
       const int entry = static_cast<int>(by_page(static_cast<unsigned long long>(t)));
-      place = t < ahead.n ? t - entry * S : -1;
-      page = t < ahead.n ? __ldg(a.table.ids + ahead.b * a.table.stride + entry) : -1;
-      if (++ahead_tile == ahead.tile1) {
-        more = ahead.next();
-        if (more) ahead_tile = ahead.tile0;
+      place = t < at.n ? t - entry * S : -1;
+      page = t < at.n ? __ldg(a.table.ids + at.b * a.table.stride + entry) : -1;
+      if (++tile == at.tile1) {
+        more = at.next();
+        if (more) tile = at.tile0;
       }
     };
     const bool any = more;
     if (any) look_up();
-    uint32_t place_of[2];  // where the thread's piece of row r0 + i * kStep lies in the swizzled slot
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      place_of[i] = (chunk >> 3) * kHalf + r0 * 128 + (((chunk & 7) ^ ((r0 + i * kStep) & 7)) << 4);
-    static_assert(2 * kStep % 8 == 0, "two passes go round");
+    const uint32_t ring = smem_addr(smem) + (chunk >> 3) * kHalf + (lw * kLoadTokens + r0) * 128;
+    const long long stride = a.cache.token_stride;
     int slot = 0;
     uint32_t turn = 0;  // times the ring went round
     for (int tile_no = 0; any; ++tile_no) {
       const bool ok = page >= 0 && page < a.cache.pages;
       if (!ok && place >= 0 && a.status) atomicOr(a.status, kDataPageRange);
-      const uint32_t exists = __ballot_sync(0xffffffffu, ok);
-      if (lane == 0) sh.valid[tile_no % kAhead][warp - 8] = exists;
-      sh.off[tile_no & 1][lt] = ok ? page * a.cache.page_stride + place * a.cache.token_stride + head * (D * 2) : -1ll;
-      load_sync();
+      const uint32_t exist = __ballot_sync(0xffffffffu, ok) & 0xffffu;
+      const long long off = ok ? page * a.cache.page_stride + place * stride + head * (D * 2) : -1ll;
+      if (lane == 0) sh.valid[tile_no % kAhead][lw] = static_cast<uint16_t>(exist);
       const bool last = !more;
       if (more) look_up();
-      const uint32_t* valid = sh.valid[tile_no % kAhead];
-      const bool all = (valid[0] & valid[1]) == 0xffffffffu;
-      const long long* off = sh.off[tile_no & 1] + r0;
 #pragma unroll 1
       for (int x = 0; x < 2; ++x) {
         if (turn > 0) wait(&sh.empty[slot], (turn + 1) & 1);
+        const uint32_t dst = ring + slot * L::kSlot;
         const char* pool = (x ? a.cache.v : a.cache.k) + chunk * 16;
-        const uint32_t dst = smem_addr(smem) + slot * L::kSlot;
+        if (in_page && exist == 0xffffu) {
+          const char* from = pool + __shfl_sync(0xffffffffu, off, 0) + r0 * stride;
 #pragma unroll
-        for (int i0 = 0; i0 < kPasses; i0 += 8) {  // (offsets are read ahead of the copies, which no load passes)
-          long long from[8];
+          for (int i = 0; i < kPasses; ++i, from += kStep * stride)
+            cp16(dst + i * (kStep * 128) + (((chunk & 7) ^ ((r0 + i * kStep) & 7)) << 4), from, 16);
+        } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) from[i] = off[(i0 + i) * kStep];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint32_t to = dst + place_of[i & 1] + (i0 + i) * (kStep * 128);
-            if (all) cp16(to, pool + from[i], 16);
-            else cp16(to, pool + (from[i] < 0 ? 0 : from[i]), from[i] < 0 ? 0 : 16);
+          for (int i = 0; i < kPasses; ++i) {
+            const long long from = __shfl_sync(0xffffffffu, off, r0 + i * kStep);
+            cp16(dst + i * (kStep * 128) + (((chunk & 7) ^ ((r0 + i * kStep) & 7)) << 4), pool + (from < 0 ? 0 : from),
+                 from < 0 ? 0 : 16);  // 0: the piece is zero-filled
           }
         }
         cp_arrive(&sh.full[slot]);
-        if (lt == 0) mbar_arrive(&sh.full[slot]);  // (the tile's bits, stored before load_sync, come with it)
+        if (lane == 0) mbar_arrive(&sh.full[slot]);  // (the tokens' bits come with it)
         if (++slot == kSlots) {
           slot = 0;
           ++turn;
@@ -243,29 +345,54 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
       if (last) break;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");  // no copy is under way when the block leaves
-  } else if (warp == 10) {
+  } else if (warp == kScores) {
     // ---- scores ----------------------------------------------------------------
     const uint32_t ring = smem_addr(smem), q_at = smem_addr(q_s);
-    int count[2] = {0, 0}, tile_no = 0, items = 0;
-    while (at.next()) {
-      for (int tile = at.tile0; tile < at.tile1; ++tile, ++tile_no) {
+    int count0 = 0, count1 = 0, tile_no = 0, items = 0;  // tiles of the streams, where they differ; of both
+    // The other warps' items, told one ahead: the next one's queries are loaded
+    // under this one's last tile.
+    Walk ahead(a, plan);
+    int told = 0;
+    auto tell = [&]() {
+      const bool any = ahead.next();
+      if (lane == 0) {
+        Item& i = sh.item[told % kItems];
+        i.any = any;
+        if (any) {
+          i.end = ahead.whole() ? 0 : static_cast<int>((ahead.first() + ahead.tiles - 1) / ahead.per);
+          i.b = ahead.b;
+          i.h = ahead.h;
+          i.n = ahead.n;
+          i.rt = ahead.rt;
+          i.row0 = ahead.row0;
+          i.rows = ahead.rows;
+          i.tile0 = ahead.tile0;
+          i.tile1 = ahead.tile1;
+          i.tiles = ahead.tiles;
+        }
+        mbar_arrive(&sh.item_ready[told % kItems]);
+      }
+      ++told;
+      return any;
+    };
+    for (bool any = tell(); any;) {
+      const int tiles = ahead.tile1 - ahead.tile0;
+      any = tell();
+      for (int j = 0; j < tiles; ++j, ++tile_no) {
         const int slot = (2 * tile_no) % kSlots;
         wait(&sh.full[slot], ((2 * tile_no) / kSlots) & 1);
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          if (!kDual && s != ((tile - at.tile0) & 1)) continue;
-          const int c = count[s]++, buf = c & 1;
-          if (tile == at.tile0) wait(&sh.q_full[s], items & 1);
-          if (c >= 2) wait(&sh.pv_done[s][buf], ((c >> 1) - 1) & 1);
-          async_fence();  // the copies, to the products
-          tc_after();
-          const uint32_t k_at = ring + slot * L::kSlot, qs = q_at + (kDual ? s : 0) * (128 * D * 2);
-#pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {
-            const uint32_t in = (ks & 3) * 32, half = ks >> 2;
-            tc_mma(tmem + s * kStream + buf * kTile, operand(qs + half * (128 * 128) + in, 16, 1024, 2),
-                   operand(k_at + half * kHalf + in, 16, 1024, 2), tc::instruction<kTile>(false, false), ks > 0);
+        async_fence();  // the copies, to the products
+#pragma unroll 1
+        for (int s = kDual ? 0 : j & 1; s < (kDual ? 2 : (j & 1) + 1); ++s) {
+          const int c = kDual ? tile_no : s ? count1++ : count0++, buf = c & 1;
+          if (j == 0) {
+            wait(&sh.q_full[s], items & 1);
+            async_fence();
           }
+          wait(&sh.pv_done[s][buf], ((c >> 1) + 1) & 1);  // (the first of a buffer finds it free)
+          tc_after();
+          scores_mma<D>(tmem + s * kStream + buf * kTile, operand(q_at + (kDual ? s : 0) * (128 * D * 2), 16, 1024, 2),
+                        operand(ring + slot * L::kSlot, 16, 1024, 2));
           if (!kDual || s == 1) tc_commit(&sh.empty[slot]);
           tc_commit(&sh.s_full[s][buf]);
         }
@@ -277,29 +404,25 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
       mbar_wait_sleep(&sh.done[0], 0);
     }
     __syncwarp();
-  } else if (warp == 11) {
+  } else if (warp == kOutputs) {
     // ---- outputs -----------------------------------------------------------------
     const uint32_t ring = smem_addr(smem);
-    int count[2] = {0, 0}, tile_no = 0;
-    while (at.next()) {
-      for (int tile = at.tile0; tile < at.tile1; ++tile, ++tile_no) {
+    int count0 = 0, count1 = 0, tile_no = 0;
+    for (int items = 0;; ++items) {
+      const Item& at = item(items);
+      if (!at.any) break;
+      const int tiles = at.tile1 - at.tile0;
+      for (int j = 0; j < tiles; ++j, ++tile_no) {
         const int slot = (2 * tile_no + 1) % kSlots;
         wait(&sh.full[slot], ((2 * tile_no + 1) / kSlots) & 1);
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          if (!kDual && s != ((tile - at.tile0) & 1)) continue;
-          const int c = count[s]++, buf = c & 1;
+#pragma unroll 1
+        for (int s = kDual ? 0 : j & 1; s < (kDual ? 2 : (j & 1) + 1); ++s) {
+          const int c = kDual ? tile_no : s ? count1++ : count0++, buf = c & 1;
           wait(&sh.p_full[s][buf], (c >> 1) & 1);
           async_fence();
           tc_after();
-          const uint32_t v_at = ring + slot * L::kSlot, p = tmem + s * kStream + buf * kTile;
-          const bool first = kDual ? tile == at.tile0 : tile - at.tile0 < 2;
-#pragma unroll
-          for (int part = 0; part < 2; ++part)
-#pragma unroll
-            for (int ks = 0; ks < kTile / 16; ++ks)
-              tc_mma_ts(tmem + s * kStream + kO, p + part * (kTile / 2) + ks * 8, operand(v_at + ks * 2048, kHalf, 1024, 2),
-                        tc::instruction<D>(false, true), !first || part > 0 || ks > 0);
+          outputs_mma<D>(tmem + s * kStream + kO, tmem + s * kStream + buf * kTile, operand(ring + slot * L::kSlot, kHalf, 1024, 2),
+                         kDual ? j > 0 : j > 1);
           if (!kDual || s == 1) tc_commit(&sh.empty[slot]);
           tc_commit(&sh.pv_done[s][buf]);
         }
@@ -310,8 +433,10 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
       mbar_wait_sleep(&sh.done[1], 0);
     }
     __syncwarp();
+  }
   } else {
     // ---- softmax: a row a thread --------------------------------------------------
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     const int s = warp >> 2, row_in = tid & 127, quad = warp & 3;
     const int row_at = kDual ? s * 128 : 0;  // the stream's first row of an item
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
@@ -319,7 +444,7 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
     const float scale = fabsf(a.scale_log2) > 0.f ? fabsf(a.scale_log2) : 1.f;
     const bool turned = !(a.scale_log2 > 0.f), flat = a.scale_log2 == 0.f;  // scores change their sign; are all zero
     TreeSight<128>& sight = sh.sight[s];
-    auto load_q = [&](const Walk& x) {  // under way when it returns
+    auto load_q = [&](const Item& x) {  // under way when it returns
       stream_sync(s);  // (q_off is free)
       {
         const AttnRow ar = attn_row(a, x.row0 + min(row_at + row_in, x.rows - 1), x.h);
@@ -327,11 +452,11 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
       }
       stream_sync(s);
       const uint32_t to = smem_addr(q_s) + (kDual ? s : 0) * (128 * D * 2);
-#pragma unroll 4
+      const int rows = x.rows - row_at;
+#pragma unroll 2
       for (int e = row_in; e < 128 * kChunks; e += 128) {
         const int r = e / kChunks, c = e % kChunks;
-        cp16(to + (c >> 3) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4), a.q + sh.q_off[s][r] + c * 16,
-             row_at + r < x.rows ? 16 : 0);
+        cp16(to + (c >> 3) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4), a.q + sh.q_off[s][r] + c * 16, r < rows ? 16 : 0);
       }
     };
     auto q_loaded = [&]() {
@@ -339,15 +464,17 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
       async_fence();
       mbar_arrive(&sh.q_full[kDual ? s : 0]);
     };
-    Walk ahead(a, plan);  // the item whose queries are loaded next
-    bool more = ahead.next();
-    if (more && (kDual || s == 0)) {
-      load_q(ahead);
-      q_loaded();
+    if (kDual || s == 0) {
+      const Item& x = item(0);
+      if (x.any) {
+        load_q(x);
+        q_loaded();
+      }
     }
-    if (more) more = ahead.next();
-    int count = 0, tile_no = 0, items = 0, sight_b = -1, sight_rt = -1;
-    while (at.next()) {
+    int count = 0, tile_no = 0, sight_b = -1, sight_rt = -1;
+    for (int items = 0;; ++items) {
+      const Item& at = item(items);
+      if (!at.any) break;
       const int base = at.n - a.Q;
       if (at.b != sight_b || at.rt != sight_rt) {
         stream_sync(s);
@@ -357,69 +484,75 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
       }
       if (tid == 0) sh.odd[(items + kOdd / 2) % kOdd] = 0;
       float m = -INFINITY, l = 0.f;
-      const int tiles = at.tile1 - at.tile0;
+      const int tile0 = at.tile0, tiles = at.tile1 - tile0;
       const int first = kDual ? 0 : s, step = kDual ? 1 : 2;
       for (int j = first; j < tiles; j += step, ++count) {
-        const int tile = at.tile0 + j, buf = count & 1, t0 = tile * kTile, now = tile_no + j;
+        const int buf = count & 1, t0 = (tile0 + j) * kTile, now = tile_no + j;
         wait(&sh.s_full[s][buf], (count >> 1) & 1);
         tc_after();
-        const bool last = j == tiles - 1;  // the item's last scores are done, so its queries have been read
-        if (last && more) load_q(ahead);
-        uint32_t x[64];
-        ld64(x, s_col + buf * kTile);
-        if (turned) {
-#pragma unroll
-          for (int i = 0; i < 64; ++i) x[i] = flat ? 0u : x[i] ^ 0x80000000u;
+        bool loading = false;  // the item's last scores are done, so its queries have been read
+        if (j == tiles - 1) {
+          const Item& next = item(items + 1);
+          loading = next.any;
+          if (loading) load_q(next);
         }
-        const uint32_t* valid = sh.valid[now % kAhead];
-        const uint32_t v0 = valid[0], v1 = valid[1];
+        const uint32_t at_s = s_col + buf * kTile;
+        const uint2 valid = *reinterpret_cast<const uint2*>(sh.valid[now % kAhead]);
         // a tile whose tokens all exist and come before the tree needs no mask
-        if ((v0 & v1) != 0xffffffffu || t0 + kTile > base) {
-          const uint32_t see[2] = {v0 & sight.window(row_in, t0 - base), v1 & sight.window(row_in, t0 + 32 - base)};
-#pragma unroll
-          for (int i = 0; i < 64; ++i)
-            if (!((see[i >> 5] >> (i & 31)) & 1)) x[i] = 0xff800000u;  // -inf
-          // A value that is not finite would reach rows that do not see its token
-          // as 0 * inf: such values are zero in the products, and added to the
-          // rows that see them at the end.  (Tokens that do not exist are
-          // zero-filled.  The first stream does it for both: the second's
-          // products with the tile are issued after the first's.)
-          if (t0 + kTile > base && (!kDual || s == 0)) {
-            const int slot = (2 * now + 1) % kSlots;
-            wait(&sh.full[slot], ((2 * now + 1) / kSlots) & 1);
-            const int token = row_in & (kTile - 1);
-            constexpr int kPer = kChunks / 2;  // pieces a thread looks at
-            if (t0 + token >= base) {
-              uint4* v = reinterpret_cast<uint4*>(smem + slot * L::kSlot + token * 128);
-              bool odd = false;
-#pragma unroll
-              for (int i = 0; i < kPer; ++i) {
-                const int c = (row_in >> 6) * kPer + i;
-                uint4* piece = v + (c >> 3) * (kHalf / 16) + ((c ^ token) & 7);  // (in an order without bank conflicts)
-                const uint4 w = *piece;
-                uint32_t u[4] = {w.x, w.y, w.z, w.w};
-                bool bad = false;
-#pragma unroll
-                for (int y = 0; y < 4; ++y)
-                  if (nonfinite2(u[y])) {
-                    bad = true;
-                    if ((u[y] & 0x7f80u) == 0x7f80u) u[y] &= 0xffff0000u;
-                    if ((u[y] & 0x7f800000u) == 0x7f800000u) u[y] &= 0xffffu;
-                  }
-                if (bad) *piece = make_uint4(u[0], u[1], u[2], u[3]);
-                odd |= bad;
+        const bool masked = (valid.x & valid.y) != 0xffffffffu || t0 + kTile > base;
+        // A value that is not finite would reach rows that do not see its token as 0 *
+        // inf: such values are zero in the products, and added to the rows that see
+        // them at the end.  (Tokens that do not exist are zero-filled.  The first
+        // stream does it for both: the second's products with the tile are issued
+        // after the first's.)
+        if (t0 + kTile > base && (!kDual || s == 0)) {
+          const int slot = (2 * now + 1) % kSlots, token = row_in & (kTile - 1);
+          wait(&sh.full[slot], ((2 * now + 1) / kSlots) & 1);
+          if (t0 + token >= base) {
+            uint4* v = reinterpret_cast<uint4*>(smem + slot * L::kSlot + token * 128);
+            bool odd = false;
+#pragma unroll 1
+            for (int c = (row_in >> 6) * (kChunks / 2), end = c + kChunks / 2; c < end; ++c) {
+              uint4* piece = v + (c >> 3) * (kHalf / 16) + ((c ^ token) & 7);  // (in an order without bank conflicts)
+              const uint4 w = *piece;
+              if (nonfinite2(w.x) || nonfinite2(w.y) || nonfinite2(w.z) || nonfinite2(w.w)) {
+                odd = true;
+                *piece = make_uint4(mma::even_word<BF16>(w.x), mma::even_word<BF16>(w.y), mma::even_word<BF16>(w.z), mma::even_word<BF16>(w.w));
               }
-              if (odd) {
-                sh.odd[items % kOdd] = 1;
-                async_fence();
-              }
+            }
+            if (odd) {
+              sh.odd[items % kOdd] = 1;
+              async_fence();
             }
           }
         }
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        // the largest score; masked ones go back to TMEM
+        float top = -INFINITY;
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          uint32_t x[32];
+          ld32(x, at_s + h * 32);
+          if (masked || turned) {
+            if (turned) {
 #pragma unroll
-        for (int i = 0; i < 64; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(x[i]));
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
+              for (int i = 0; i < 32; ++i) x[i] = flat ? 0u : x[i] ^ 0x80000000u;
+            }
+            const uint32_t see = (h ? valid.y : valid.x) & sight.window(row_in, t0 + h * 32 - base);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (!((see >> i) & 1)) x[i] = 0xff800000u;  // -inf
+            st32(at_s + h * 32, x);
+            tmem_st_done();
+          }
+          float y = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            top = max3(top, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+            y = max3(y, __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
+          }
+          top = fmaxf(top, y);
+        }
+        top *= scale;
         const bool grow = top > m + kSlackR;
         if (__any_sync(0xffffffffu, grow)) {
           const float c = grow ? (m == -INFINITY ? 0.f : ex2(m - top)) : 1.f;
@@ -429,37 +562,50 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
             wait(&sh.pv_done[s][buf ^ 1], ((count - 1) >> 1) & 1);  // O is complete
             tc_after();
 #pragma unroll 1
-            for (int d = 0; d < D; d += 32) {
-              uint32_t o[32];
-              ld32(o, o_col + d);
+            for (int d = 0; d < D; d += 16) {
+              uint32_t o[16];
+              ld16(o, o_col + d);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * c);
-              st32(o_col + d, o);
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * c);
+              st16(o_col + d, o);
             }
           }
         }
         const float less = m == -INFINITY ? 0.f : -m;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
-        uint32_t hi[32], lo[32];
+        const uint64_t scale2 = pair(__float_as_uint(scale), __float_as_uint(scale)), less2 = pair(__float_as_uint(less), __float_as_uint(less));
+        uint64_t sum0 = 0, sum1 = 0;  // (two fp32 zeros)
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          uint32_t x[32], hi[16], lo[16];
+          ld32(x, at_s + h * 32);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const float p0 = ex2(fmaf(__uint_as_float(x[2 * i]), scale, less));
-          const float p1 = ex2(fmaf(__uint_as_float(x[2 * i + 1]), scale, less));
-          sum[(2 * i) & 3] += p0;
-          sum[(2 * i + 1) & 3] += p1;
-          hi[i] = pack2(p0, p1);
-          lo[i] = pack2(p0 - bf16_lo(hi[i]), p1 - bf16_hi(hi[i]));
+          for (int i = 0; i < 16; ++i) {
+            float p0, p1;
+            split(fma2(pair(x[2 * i], x[2 * i + 1]), scale2, less2), p0, p1);
+            p0 = ex2(p0);
+            p1 = ex2(p1);
+            const uint64_t p = pair(__float_as_uint(p0), __float_as_uint(p1));
+            if (i & 1) sum1 = add2(sum1, p);
+            else sum0 = add2(sum0, p);
+            hi[i] = pack2(p0, p1);
+            // (the sign turned with the halves' unpacking)
+            split(add2(p, pair((hi[i] << 16) ^ 0x80000000u, (hi[i] & 0xffff0000u) ^ 0x80000000u)), p0, p1);
+            lo[i] = pack2(p0, p1);
+          }
+          st16(at_s + h * 32, hi);
+          st16(at_s + h * 32 + 16, lo);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        st32(s_col + buf * kTile, hi);
-        st32(s_col + buf * kTile + 32, lo);
+        {
+          float a0, a1;
+          split(add2(sum0, sum1), a0, a1);
+          l += a0 + a1;
+        }
         tmem_st_done();
         tc_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.p_full[s][buf]);
-        if (last && more) q_loaded();
+        if (loading) q_loaded();
       }
-      if (more) more = ahead.next();
 
       // ---- the item, or this block's part of it ---------------------------------
       const bool mine = tiles > first;  // has the stream a part
@@ -493,50 +639,59 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
       const float inv = whole ? (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l)) : 1.f;
       const bool odd = *reinterpret_cast<volatile int*>(&sh.odd[items % kOdd]) != 0;
       constexpr int kPart = kDual ? D : D / 2;  // columns that the thread writes
+      if (none) c0 = c1 = 0.f;
+      c0 *= inv;
+      c1 *= inv;
 #pragma unroll 1
-      for (int d = kDual ? 0 : s * kPart; d < (kDual ? D : (s + 1) * kPart); d += 32) {
-        uint32_t u[32];
-        float o[32];
-        ld32(u, tmem + lanes + (kDual ? s * kStream : 0) + kO + d);
+      for (int d = kDual ? 0 : s * kPart, end = d + kPart; d < end; d += 16) {
+        uint32_t u[16];
+        float o[16];
+        ld16(u, tmem + lanes + (kDual ? s * kStream : 0) + kO + d);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(u[i]);
-        if constexpr (!kDual) {
+        for (int i = 0; i < 16; ++i) o[i] = __uint_as_float(u[i]) * c0;
+        if (!kDual && both) {
+          ld16(u, tmem + lanes + kStream + kO + d);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] *= c0;
-          if (both) {
-            ld32(u, tmem + lanes + kStream + kO + d);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = fmaf(c1, __uint_as_float(u[i]), o[i]);
-          }
-        }
-        if (odd) {
-          for (int t = max(at.tile0 * kTile, max(base, 0)); t < min(at.tile1 * kTile, at.n); ++t) {
-            if (!sight.sees(row_in, t - base)) continue;
-            const int entry = static_cast<int>(by_page(static_cast<unsigned long long>(t)));
-            const int page = a.table.ids[at.b * a.table.stride + entry];
-            if (page < 0 || page >= a.cache.pages) continue;
-            const char* v = a.cache.v + page * a.cache.page_stride + (t - entry * a.cache.page_size) * a.cache.token_stride +
-                            at.h * (D * 2);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const float y = load_one<BF16>(v, d + i);
-              if (!isfinite(y)) o[i] += y;
-            }
-          }
+          for (int i = 0; i < 16; ++i) o[i] = fmaf(c1, __uint_as_float(u[i]), o[i]);
         }
         if (!row) continue;
+        if (none) {  // (0 * NaN)
 #pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] = none ? 0.f : o[i] * inv;
+          for (int i = 0; i < 16; ++i) o[i] = 0.f;
+        }
         if (whole) {
           uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + to * D + d);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+          for (int i = 0; i < 2; ++i)
             out[i] = make_uint4(pack2(o[8 * i], o[8 * i + 1]), pack2(o[8 * i + 2], o[8 * i + 3]), pack2(o[8 * i + 4], o[8 * i + 5]),
                                 pack2(o[8 * i + 6], o[8 * i + 7]));
         } else {
           float4* out = reinterpret_cast<float4*>(slot + r * D + d);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) out[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          for (int i = 0; i < 4; ++i) out[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        }
+      }
+      if (odd && row && !none) {  // by the thread that wrote them
+        constexpr int kFrom = kDual ? 0 : kPart;
+#pragma unroll 1
+        for (int t = max(at.tile0 * kTile, max(base, 0)); t < min(at.tile1 * kTile, at.n); ++t) {
+          if (!sight.sees(row_in, t - base)) continue;
+          const int entry = static_cast<int>(by_page(static_cast<unsigned long long>(t)));
+          const int page = a.table.ids[at.b * a.table.stride + entry];
+          if (page < 0 || page >= a.cache.pages) continue;
+          const char* v = a.cache.v + page * a.cache.page_stride + (t - entry * a.cache.page_size) * a.cache.token_stride +
+                          at.h * (D * 2);
+#pragma unroll 1
+          for (int d = s * kFrom; d < s * kFrom + kPart; ++d) {
+            const float y = load_one<BF16>(v, d);
+            if (isfinite(y)) continue;
+            if (whole) {
+              uint16_t* out = static_cast<uint16_t*>(a.out) + to * D + d;
+              *out = static_cast<uint16_t>(pack2(__uint_as_float(static_cast<uint32_t>(*out) << 16) + y, 0.f));
+            } else {
+              slot[r * D + d] += y;
+            }
+          }
         }
       }
       if (row && (kDual || s == 0)) {
@@ -548,31 +703,74 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
         }
       }
       tc_before();  // O has been read
-      if (!whole) {
-        soft_sync();
-        if (tid == 0) {
-          const long long k0 = at.first() / at.per, k1 = (at.first() + at.tiles - 1) / at.per;
-          __threadfence();
-          const bool last = atom_add_acq_rel_gpu(&a.counters[k0], 1u) + 1u == static_cast<unsigned int>(k1 - k0 + 1);
-          if (last) a.counters[k0] = 0u;
-          sh.last = last;
-        }
-        soft_sync();
-        if (sh.last) attn_join<L::kRows, D, kSoft>(a, at.b, at.h, at.row0, at.rows, at.first(), at.tiles, at.per);
-        soft_sync();
-      } else if constexpr (!kDual) {
-        soft_sync();  // both streams' O may be written again
-      }
+      if (!whole && at.tile0 == 0 && tid == 0) joins[blockIdx.x] = {at.b, at.h, at.row0, at.rows, at.end, 0};
+      if constexpr (!kDual) soft_sync();  // both streams' O may be written again
       tile_no += tiles;
-      ++items;
     }
   }
   tc_before();
   __syncthreads();
-  if (warp == 11) {
+  if (warp == kOutputs) {
     tc_after();
     tmem_free(tmem, kCols);
   }
+}
+
+// One warp a row of a cut item: blocks [block, end] of the launch have left (m, l, O)
+// of it.  Lanes hold the parts' maxima and sums, 32 at a time, then D / 32 values
+// of O each, eight parts' loads under way together.
+constexpr int kJoinWarps = 4;
+template <int D, bool kDual>
+__global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const AttnArgs a, const Join* joins) {
+  constexpr int kRows = Lay<D, kDual>::kRows, kN = D / 32;
+  using V = typename std::conditional<kN == 4, float4, float2>::type;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Join j = joins[blockIdx.x];
+  const int lane = threadIdx.x & 31, r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
+  if (r >= j.rows) return;
+  const int first = blockIdx.x;
+  auto slot = [&](int c) { return attn_slot<kRows, D>(a, c, c == first); };
+  float m = -INFINITY;
+  for (int c0 = first; c0 <= j.end; c0 += 32)
+    if (c0 + lane <= j.end) m = fmaxf(m, slot(c0 + lane)[kRows * D + r]);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  float l = 0.f, o[kN];
+#pragma unroll
+  for (int i = 0; i < kN; ++i) o[i] = 0.f;
+  for (int c0 = first; c0 <= j.end; c0 += 32) {
+    float w = 0.f;
+    if (c0 + lane <= j.end) {
+      const float* s = slot(c0 + lane) + kRows * D + r;
+      w = s[0] == -INFINITY ? 1.f : ex2(s[0] - m);  // a part without a maximum holds zeros, or NaN that it passes on
+      l = fmaf(w, s[kRows], l);
+    }
+    const int parts = min(32, j.end - c0 + 1);
+    for (int c = 0; c < parts; c += 8) {
+      V v[8];
+#pragma unroll
+      for (int y = 0; y < 8; ++y)
+        if (c + y < parts) v[y] = *reinterpret_cast<const V*>(slot(c0 + c + y) + r * D + lane * kN);
+#pragma unroll
+      for (int y = 0; y < 8; ++y) {
+        const float wy = __shfl_sync(0xffffffffu, w, c + y);
+        if (c + y < parts) {
+          const float* x = reinterpret_cast<const float*>(&v[y]);
+#pragma unroll
+          for (int i = 0; i < kN; ++i) o[i] = fmaf(wy, x[i], o[i]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+  const AttnRow ar = attn_row(a, j.row0 + r, j.h);
+  const size_t at = (static_cast<size_t>(j.b) * a.Q + ar.i) * a.Hq + ar.hq;
+  const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+  uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + at * D + lane * kN);
+  if constexpr (kN == 4) *reinterpret_cast<uint2*>(out) = make_uint2(pack2(o[0] * inv, o[1] * inv), pack2(o[2] * inv, o[3] * inv));
+  else *out = pack2(o[0] * inv, o[1] * inv);
+  if (lane == 0 && a.lse) a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 template <int D, bool kDual>
@@ -580,9 +778,32 @@ cudaError_t prepare() {
   return cudaFuncSetAttribute(attention_tree_kernel<D, kDual>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D, kDual>::kBytes);
 }
 template <int D, bool kDual>
-void launch(const AttnArgs& a, int sm_count, cudaStream_t stream) {
-  attention_tree_kernel<D, kDual><<<sm_count < kMaxCtas ? sm_count : kMaxCtas, kThreadsR, Lay<D, kDual>::kBytes, stream>>>(
-      a, DivU64::make(static_cast<unsigned long long>(a.cache.page_size)));
+size_t workspace() {
+  return static_cast<size_t>(kAttnMaxCtas) * 4 + static_cast<size_t>(kMaxCtas) * (2 * Lay<D, kDual>::kRows * (D + 2) * 4 + sizeof(Join));
+}
+template <int D, bool kDual>
+cudaError_t launch(const AttnArgs& a, int sm_count, cudaStream_t stream) {
+  using L = Lay<D, kDual>;
+  const int grid = sm_count < kMaxCtas ? sm_count : kMaxCtas;
+  Join* joins = reinterpret_cast<Join*>(a.partials + static_cast<size_t>(kMaxCtas) * 2 * L::kRows * (D + 2));
+  attention_tree_kernel<D, kDual><<<grid, kThreadsR, L::kBytes, stream>>>(
+      a, DivU64::make(static_cast<unsigned long long>(a.cache.page_size)), joins);
+  const int R = a.Q * (a.Hq / a.cache.heads), tiles = (R + L::kRows - 1) / L::kRows;
+  // sequences that the table has no room to make long are not cut (attn_plan)
+  if (static_cast<int64_t>(a.table.max_pages) * a.cache.page_size <= kWholeTiles * kTile &&
+      static_cast<int64_t>(a.B) * a.cache.heads * tiles <= grid)
+    return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, ((R < L::kRows ? R : L::kRows) + kJoinWarps - 1) / kJoinWarps);
+  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.stream = stream;
+  cudaLaunchAttribute after[1];
+  after[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  after[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = after;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, tree_join_kernel<D, kDual>, a, static_cast<const Join*>(joins));
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace ttc

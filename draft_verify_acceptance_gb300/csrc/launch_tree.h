@@ -16,7 +16,7 @@ cudaError_t tree_attention_prepare();
 // tcgen05 kernels (attention_tree_tc.cuh).
 size_t tree_tc_workspace(int rows, int D);
 cudaError_t tree_tc_prepare();
-void tree_tc_launch(const AttnArgs& a, int rows, int sm_count, cudaStream_t stream);
+cudaError_t tree_tc_launch(const AttnArgs& a, int rows, int sm_count, cudaStream_t stream);
 cudaError_t launch_tree_attention(const AttnArgs& a, int sm_count, cudaStream_t stream);
 
 struct RotatedAppendArgs {

@@ -29,19 +29,6 @@ struct TreeSight {
 template <>
 struct TreeSight<0> {};
 
-// The set of node i as words; false when it is no node.
-__device__ __forceinline__ bool tree_line(const int32_t* parents, int i, uint32_t (&w)[kNodeWords]) {
-#pragma unroll
-  for (int x = 0; x < kNodeWords; ++x) w[x] = 0;
-  for (;;) {
-#pragma unroll
-    for (int x = 0; x < kNodeWords; ++x) w[x] |= (i >> 5) == x ? 1u << (i & 31) : 0u;
-    const int p = parents[i];
-    if (p < 0 || p >= i) return p == -1;
-    i = p;
-  }
-}
-
 // Fills `sight` for rows row0, row0 + 1, ... of a cache head (row = node * G + query
 // head of the group; those behind row `last` are as it) of sequence b, whose
 // tree starts at token `base`, by `count` threads that `sync` holds together.
@@ -50,6 +37,7 @@ __device__ __forceinline__ void tree_sight(const AttnArgs& a, int b, int base, i
                                            TreeSight<kRows>& sight, Sync sync) {
   const int32_t* parents = a.parents + b * a.parents_stride;
   bool bad = false;
+#pragma unroll 1
   for (int i = tid; i < a.Q; i += count) {
     const int p = __ldg(parents + i);
     bad |= p >= i;
@@ -58,13 +46,28 @@ __device__ __forceinline__ void tree_sight(const AttnArgs& a, int b, int base, i
   if (bad && a.status) atomicOr(a.status, kDataTreeParent);
   sync();
   const int G = a.Hq / a.cache.heads;
+#pragma unroll 1
   for (int r = tid; r < kRows; r += count) {
-    const int i = min(row0 + r, last) / G;
-    uint32_t w[kNodeWords];
-    const bool node = tree_line(sight.parents, i, w) && base + i >= 0;
+    const int node = min(row0 + r, last) / G;
+    uint32_t* bits = sight.bits[r];
 #pragma unroll
-    for (int x = 0; x < kNodeWords; ++x) sight.bits[r][x] = w[x];
-    sight.none[r] = !node;
+    for (int x = 0; x < kNodeWords; ++x) bits[x] = 0;
+    // up the line, a word's bits gathered before they are stored (parents lie lower)
+    int i = node, p;
+    uint32_t word = 0;
+#pragma unroll 1
+    for (;;) {
+      word |= 1u << (i & 31);
+      p = sight.parents[i];
+      const bool up = p >= 0 && p < i;
+      if (!up || (p >> 5) != (i >> 5)) {
+        bits[i >> 5] = word;
+        word = 0;
+      }
+      if (!up) break;
+      i = p;
+    }
+    sight.none[r] = p != -1 || base + node < 0;
   }
   sync();
 }
