@@ -16,9 +16,9 @@
 // joined at the item's end.
 //
 // One block per SM.  Warps 0-3 and 4-7: the streams' softmax.  Warps 8-11 copy K
-// and V of the tiles, 16 tokens each, into a ring of slots, across item boundaries,
-// in 16-byte pieces that arrive on the slot's barrier by themselves, so any page
-// size and strides.  Warp 12 issues the scores' products, warp 13 the outputs'.
+// and V of the tiles into a ring of slots, across item boundaries, in 16-byte
+// pieces that arrive on the slot's barrier by themselves, so any page size and
+// strides.  Warp 12 issues the scores' products, warp 13 the outputs'.
 //
 // Parts of an item that blocks' ranges cut are left in the workspace and joined by
 // a dependent kernel over all SMs, in block order (one block would have to read
@@ -51,7 +51,7 @@ using tc::tmem_st_done;
 
 constexpr int kTile = 64;        // tokens
 constexpr int kSoft = 256;       // softmax threads, 128 a stream
-constexpr int kLoadWarps = 4, kLoadTokens = kTile / kLoadWarps;  // loader warps, a warp's tokens of a tile
+constexpr int kLoadWarps = 4;    // K and V of the even and of the odd tiles
 constexpr int kThreadsR = kSoft + kLoadWarps * 32 + 128;           // (two warps of the last four are idle)
 // Registers a thread: 512 x 128 at the launch, then shared out by groups of four
 // warps, 2 x 128 x (176 + 80) = 512 x 128.
@@ -97,7 +97,7 @@ struct Shared {
   unsigned long long s_full[2][2], p_full[2][2], pv_done[2][2], q_full[2] /* one for both streams of shared rows */, done[2];
   unsigned long long item_ready[kItems];
   Item item[kItems];
-  __align__(8) uint16_t valid[kAhead][kLoadWarps];  // tokens that exist, by tile
+  uint2 valid[kAhead];  // tokens that exist, by tile
   long long q_off[2][128];    // of the next item's rows, bytes
   TreeSight<128> sight[2];
   float m[2][128], l[2][128];
@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
       a, a.cache.heads * ((a.Q * (a.Hq / a.cache.heads) + L::kRows - 1) / L::kRows), 4, sh.plan);
   if (tid == 0) {
     for (int i = 0; i < kSlots; ++i) {
-      mbar_init(&sh.full[i], kLoadWarps * 33);
+      mbar_init(&sh.full[i], 33);
       mbar_init(&sh.empty[i], 1);
     }
     for (int s = 0; s < 2; ++s) {
@@ -282,65 +282,82 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
   if (warp < kScores) {
     // ---- K and V of each tile, in turn -----------------------------------
-    const int lw = warp - 8, S = a.cache.page_size;
-    const int chunk = lane % kChunks, r0 = lane / kChunks;
-    constexpr int kStep = 32 / kChunks, kPasses = kLoadTokens / kStep;
-    const bool in_page = S % kLoadTokens == 0;  // a warp's tokens of a tile lie in one page
+    // A warp takes K or V of every other tile, so that it looks its 64 tokens up
+    // and waits once for 32 copies (with 16 tokens of every K and V a warp these
+    // took more of its time than the copies).
+    const bool is_v = warp & 1;
+    const int S = a.cache.page_size, chunk = lane % kChunks, r0 = lane / kChunks;
+    constexpr int kStep = 32 / kChunks, kPasses = 16 / kStep;
+    const bool in_page = S % 16 == 0;  // tokens 16 g .. 16 g + 15 of a tile lie in one page
     Walk at(a, plan);
-    // The tile whose pages are looked up, one ahead of the copies: the table's
-    // entries are on their way while the tile before is copied.
     bool more = at.next();
     int tile = more ? at.tile0 : 0;
-    int page = -1, place = -1, head = 0;  // of token lane % 16; place: token in the page, -1: past the end
+    auto step = [&]() {
+      if (++tile < at.tile1) return;
+      more = at.next();
+      if (more) tile = at.tile0;
+    };
+    if (more && warp >= 10) step();  // the second pair starts with the second tile
+    // The pages of tokens lane and 32 + lane, looked up a tile ahead: the table's
+    // entries are on their way while the tile before is copied.
+    int page[2], place[2], head = 0;  // place: token in the page, -1: past the end
     auto look_up = [&]() {
       head = at.h;
-      const int t = tile * kTile + lw * kLoadTokens + (lane & (kLoadTokens - 1));
-      const int entry = static_cast<int>(by_page(static_cast<unsigned long long>(t)));
-      place = t < at.n ? t - entry * S : -1;
-      page = t < at.n ? __ldg(a.table.ids + at.b * a.table.stride + entry) : -1;
-      if (++tile == at.tile1) {
-        more = at.next();
-        if (more) tile = at.tile0;
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int t = tile * kTile + y * 32 + lane;
+        const int entry = static_cast<int>(by_page(static_cast<unsigned long long>(t)));
+        place[y] = t < at.n ? t - entry * S : -1;
+        page[y] = t < at.n ? __ldg(a.table.ids + at.b * a.table.stride + entry) : -1;
       }
+      step();
+      if (more) step();
     };
     const bool any = more;
     if (any) look_up();
-    const uint32_t ring = smem_addr(smem) + (chunk >> 3) * kHalf + (lw * kLoadTokens + r0) * 128;
-    const long long stride = a.cache.token_stride;
-    int slot = 0;
-    uint32_t turn = 0;  // times the ring went round
-    for (int tile_no = 0; any; ++tile_no) {
-      const bool ok = page >= 0 && page < a.cache.pages;
-      if (!ok && place >= 0 && a.status) atomicOr(a.status, kDataPageRange);
-      const uint32_t exist = __ballot_sync(0xffffffffu, ok) & 0xffffu;
-      const long long off = ok ? page * a.cache.page_stride + place * stride + head * (D * 2) : -1ll;
-      if (lane == 0) sh.valid[tile_no % kAhead][lw] = static_cast<uint16_t>(exist);
+    const uint32_t ring = smem_addr(smem) + (chunk >> 3) * kHalf + r0 * 128;
+    const char* pool = (is_v ? a.cache.v : a.cache.k) + chunk * 16 + r0 * a.cache.token_stride;
+    const long long stride = kStep * a.cache.token_stride;
+    int slot = warp - 8;
+    uint32_t turn = 1;  // the parity of a slot that is free the first time
+    for (int tile_no = (warp - 8) >> 1; any; tile_no += 2) {
+      uint32_t exist[2];
+      long long off[2];
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const bool ok = page[y] >= 0 && page[y] < a.cache.pages;
+        if (!ok && place[y] >= 0 && a.status) atomicOr(a.status, kDataPageRange);
+        exist[y] = __ballot_sync(0xffffffffu, ok);
+        off[y] = ok ? page[y] * a.cache.page_stride + place[y] * a.cache.token_stride + head * (D * 2) : -1ll;
+      }
+      if (!is_v && lane == 0) sh.valid[tile_no % kAhead] = make_uint2(exist[0], exist[1]);
       const bool last = !more;
       if (more) look_up();
+      wait(&sh.empty[slot], turn & 1);
+      const uint32_t dst = ring + slot * L::kSlot;
+      if (in_page && (exist[0] & exist[1]) == 0xffffffffu) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const char* from = pool + __shfl_sync(0xffffffffu, off[g >> 1], (g & 1) * 16);
+#pragma unroll
+          for (int i = 0; i < kPasses; ++i, from += stride)
+            cp16(dst + (g * 16 + i * kStep) * 128 + (((chunk & 7) ^ ((r0 + i * kStep) & 7)) << 4), from, 16);
+        }
+      } else {
 #pragma unroll 1
-      for (int x = 0; x < 2; ++x) {
-        if (turn > 0) wait(&sh.empty[slot], (turn + 1) & 1);
-        const uint32_t dst = ring + slot * L::kSlot;
-        const char* pool = (x ? a.cache.v : a.cache.k) + chunk * 16;
-        if (in_page && exist == 0xffffu) {
-          const char* from = pool + __shfl_sync(0xffffffffu, off, 0) + r0 * stride;
-#pragma unroll
-          for (int i = 0; i < kPasses; ++i, from += kStep * stride)
-            cp16(dst + i * (kStep * 128) + (((chunk & 7) ^ ((r0 + i * kStep) & 7)) << 4), from, 16);
-        } else {
-#pragma unroll
-          for (int i = 0; i < kPasses; ++i) {
-            const long long from = __shfl_sync(0xffffffffu, off, r0 + i * kStep);
-            cp16(dst + i * (kStep * 128) + (((chunk & 7) ^ ((r0 + i * kStep) & 7)) << 4), pool + (from < 0 ? 0 : from),
-                 from < 0 ? 0 : 16);  // 0: the piece is zero-filled
-          }
+        for (int i = 0; i < 4 * kPasses; ++i) {
+          const int t = r0 + i * kStep;
+          const long long from = __shfl_sync(0xffffffffu, i < 2 * kPasses ? off[0] : off[1], t & 31) - r0 * a.cache.token_stride;
+          const bool some = ((i < 2 * kPasses ? exist[0] : exist[1]) >> (t & 31)) & 1;
+          cp16(dst + i * kStep * 128 + (((chunk & 7) ^ (t & 7)) << 4), some ? pool + from : a.cache.k, some ? 16 : 0);  // 0: zero-filled
         }
-        cp_arrive(&sh.full[slot]);
-        if (lane == 0) mbar_arrive(&sh.full[slot]);  // (the tokens' bits come with it)
-        if (++slot == kSlots) {
-          slot = 0;
-          ++turn;
-        }
+      }
+      cp_arrive(&sh.full[slot]);
+      if (lane == 0) mbar_arrive(&sh.full[slot]);  // (the tokens' bits come with it)
+      slot += 4;
+      if (slot >= kSlots) {
+        slot -= kSlots;
+        ++turn;
       }
       if (last) break;
     }
@@ -497,7 +514,7 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
           if (loading) load_q(next);
         }
         const uint32_t at_s = s_col + buf * kTile;
-        const uint2 valid = *reinterpret_cast<const uint2*>(sh.valid[now % kAhead]);
+        const uint2 valid = sh.valid[now % kAhead];
         // a tile whose tokens all exist and come before the tree needs no mask
         const bool masked = (valid.x & valid.y) != 0xffffffffu || t0 + kTile > base;
         // A value that is not finite would reach rows that do not see its token as 0 *
