@@ -52,12 +52,13 @@ using tc::tmem_st_done;
 constexpr int kTile = 64;        // tokens
 constexpr int kSoft = 256;       // softmax threads, 128 a stream
 constexpr int kLoadWarps = 4;    // K and V of the even and of the odd tiles
-constexpr int kThreadsR = kSoft + kLoadWarps * 32 + 128;           // (two warps of the last four are idle)
+constexpr int kThreadsR = kSoft + kLoadWarps * 32 + 128;           // (one warp of the last four is idle)
 // Registers a thread: 512 x 128 at the launch, then shared out by groups of four
 // warps, 2 x 128 x (176 + 80) = 512 x 128.
 constexpr int kSoftRegs = 176, kOtherRegs = 80;
 static_assert(kSoft * kSoftRegs + (kThreadsR - kSoft) * kOtherRegs <= 65536 && kThreadsR * 128 <= 65536, "registers");
-constexpr int kScores = 8 + kLoadWarps, kOutputs = kScores + 1;   // the warps that issue products
+constexpr int kScores = 8 + kLoadWarps, kOutputs = kScores + 1;   // the warps that issue products,
+constexpr int kWalker = kOutputs + 1;                             // and the one that finds the block's items
 constexpr float kSlackR = 8.f;   // how far (log2) a score may pass the reference
 constexpr int kEndR = 6;         // steps that an item's start and end count as
 constexpr int kMaxCtas = 160;
@@ -75,15 +76,15 @@ struct Lay {
   static_assert(kSlots >= 8 && kSlots / 2 + 4 < kAhead, "the ring");
 };
 
-// An item, or this block's part of it, as the softmax warps need it (the walk's
-// own state would take a third of their registers).
+// An item, or this block's part of it.  One warp finds them for the others (the
+// walk takes some thousand cycles an item, and a third of the softmax warps' registers).
 struct Item {
   int any;   // 0: there are no more
   int end;   // block that has its last tile
   int b, h, n, rt, row0, rows, tile0, tile1, tiles;
   __device__ __forceinline__ bool whole() const { return tile0 == 0 && tile1 == tiles; }
 };
-constexpr int kItems = 4;  // kept: more than a stream can be behind
+constexpr int kItems = 8;  // told ahead of the softmax warps' last
 
 // The item whose first tile a block has and whose last one another block; rows 0:
 // there is none.
@@ -95,7 +96,7 @@ template <int D, bool kDual>
 struct Shared {
   unsigned long long full[Lay<D, kDual>::kSlots], empty[Lay<D, kDual>::kSlots];
   unsigned long long s_full[2][2], p_full[2][2], pv_done[2][2], q_full[2] /* one for both streams of shared rows */, done[2];
-  unsigned long long item_ready[kItems];
+  unsigned long long item_ready[kItems], item_free[kItems];
   Item item[kItems];
   uint2 valid[kAhead];  // tokens that exist, by tile
   long long q_off[2][128];    // of the next item's rows, bytes
@@ -262,7 +263,10 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
       mbar_init(&sh.q_full[s], 128);
       mbar_init(&sh.done[s], 1);
     }
-    for (int i = 0; i < kItems; ++i) mbar_init(&sh.item_ready[i], 1);
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(&sh.item_ready[i], 1);
+      mbar_init(&sh.item_free[i], 2);
+    }
     for (int i = 0; i < kOdd; ++i) sh.odd[i] = 0;
     sh.dead = 0;
     fence_barrier_init();
@@ -289,50 +293,63 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
     const int S = a.cache.page_size, chunk = lane % kChunks, r0 = lane / kChunks;
     constexpr int kStep = 32 / kChunks, kPasses = 16 / kStep;
     const bool in_page = S % 16 == 0;  // tokens 16 g .. 16 g + 15 of a tile lie in one page
-    Walk at(a, plan);
-    bool more = at.next();
-    int tile = more ? at.tile0 : 0;
+    int items = -1, tile = 0, tile1 = 0, n = 0, head = 0;
+    bool more = true;  // there is a tile `tile`
+    const int32_t* ids = nullptr;
     auto step = [&]() {
-      if (++tile < at.tile1) return;
-      more = at.next();
-      if (more) tile = at.tile0;
-    };
-    if (more && warp >= 10) step();  // the second pair starts with the second tile
-    // The pages of tokens lane and 32 + lane, looked up a tile ahead: the table's
-    // entries are on their way while the tile before is copied.
-    int page[2], place[2], head = 0;  // place: token in the page, -1: past the end
-    auto look_up = [&]() {
+      if (++tile < tile1) return;
+      const Item& at = item(++items);
+      more = at.any;
+      if (!more) return;
+      tile = at.tile0;
+      tile1 = at.tile1;
+      n = at.n;
       head = at.h;
+      ids = a.table.ids + at.b * a.table.stride;
+    };
+    step();
+    if (more && warp >= 10) step();  // the second pair starts with the second tile
+    // The pages of tokens lane and 32 + lane, looked up a tile of the warp's ahead:
+    // the table's entries are on their way while the tiles before are copied.
+    struct Pages {
+      int page[2], place[2], head;  // place: token in the page, -1: past the end
+      bool any;
+    };
+    auto look_up = [&](Pages& p) {
+      p.any = more;
+      if (!more) return;
+      p.head = head;
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         const int t = tile * kTile + y * 32 + lane;
         const int entry = static_cast<int>(by_page(static_cast<unsigned long long>(t)));
-        place[y] = t < at.n ? t - entry * S : -1;
-        page[y] = t < at.n ? __ldg(a.table.ids + at.b * a.table.stride + entry) : -1;
+        p.place[y] = t < n ? t - entry * S : -1;
+        p.page[y] = t < n ? __ldg(ids + entry) : -1;
       }
       step();
       if (more) step();
     };
-    const bool any = more;
-    if (any) look_up();
+    Pages now, next;
+    look_up(now);
+    look_up(next);
     const uint32_t ring = smem_addr(smem) + (chunk >> 3) * kHalf + r0 * 128;
     const char* pool = (is_v ? a.cache.v : a.cache.k) + chunk * 16 + r0 * a.cache.token_stride;
     const long long stride = kStep * a.cache.token_stride;
     int slot = warp - 8;
     uint32_t turn = 1;  // the parity of a slot that is free the first time
-    for (int tile_no = (warp - 8) >> 1; any; tile_no += 2) {
+    for (int tile_no = (warp - 8) >> 1; now.any; tile_no += 2) {
       uint32_t exist[2];
       long long off[2];
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
-        const bool ok = page[y] >= 0 && page[y] < a.cache.pages;
-        if (!ok && place[y] >= 0 && a.status) atomicOr(a.status, kDataPageRange);
+        const bool ok = now.page[y] >= 0 && now.page[y] < a.cache.pages;
+        if (!ok && now.place[y] >= 0 && a.status) atomicOr(a.status, kDataPageRange);
         exist[y] = __ballot_sync(0xffffffffu, ok);
-        off[y] = ok ? page[y] * a.cache.page_stride + place[y] * a.cache.token_stride + head * (D * 2) : -1ll;
+        off[y] = ok ? now.page[y] * a.cache.page_stride + now.place[y] * a.cache.token_stride + now.head * (D * 2) : -1ll;
       }
       if (!is_v && lane == 0) sh.valid[tile_no % kAhead] = make_uint2(exist[0], exist[1]);
-      const bool last = !more;
-      if (more) look_up();
+      now = next;
+      look_up(next);
       wait(&sh.empty[slot], turn & 1);
       const uint32_t dst = ring + slot * L::kSlot;
       if (in_page && (exist[0] & exist[1]) == 0xffffffffu) {
@@ -359,42 +376,16 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
         slot -= kSlots;
         ++turn;
       }
-      if (last) break;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");  // no copy is under way when the block leaves
   } else if (warp == kScores) {
     // ---- scores ----------------------------------------------------------------
     const uint32_t ring = smem_addr(smem), q_at = smem_addr(q_s);
     int count0 = 0, count1 = 0, tile_no = 0, items = 0;  // tiles of the streams, where they differ; of both
-    // The other warps' items, told one ahead: the next one's queries are loaded
-    // under this one's last tile.
-    Walk ahead(a, plan);
-    int told = 0;
-    auto tell = [&]() {
-      const bool any = ahead.next();
-      if (lane == 0) {
-        Item& i = sh.item[told % kItems];
-        i.any = any;
-        if (any) {
-          i.end = ahead.whole() ? 0 : static_cast<int>((ahead.first() + ahead.tiles - 1) / ahead.per);
-          i.b = ahead.b;
-          i.h = ahead.h;
-          i.n = ahead.n;
-          i.rt = ahead.rt;
-          i.row0 = ahead.row0;
-          i.rows = ahead.rows;
-          i.tile0 = ahead.tile0;
-          i.tile1 = ahead.tile1;
-          i.tiles = ahead.tiles;
-        }
-        mbar_arrive(&sh.item_ready[told % kItems]);
-      }
-      ++told;
-      return any;
-    };
-    for (bool any = tell(); any;) {
-      const int tiles = ahead.tile1 - ahead.tile0;
-      any = tell();
+    for (;; ++items) {
+      const Item& at = item(items);
+      if (!at.any) break;
+      const int tiles = at.tile1 - at.tile0;
       for (int j = 0; j < tiles; ++j, ++tile_no) {
         const int slot = (2 * tile_no) % kSlots;
         wait(&sh.full[slot], ((2 * tile_no) / kSlots) & 1);
@@ -414,7 +405,6 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
           tc_commit(&sh.s_full[s][buf]);
         }
       }
-      ++items;
     }
     if (*reinterpret_cast<volatile int*>(&sh.dead)) {  // none of them may be under way when TMEM is freed
       tc_commit(&sh.done[0]);
@@ -450,6 +440,32 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
       mbar_wait_sleep(&sh.done[1], 0);
     }
     __syncwarp();
+  } else if (warp == kWalker) {
+    // ---- items -------------------------------------------------------------------
+    Walk at(a, plan);
+    for (int items = 0;; ++items) {
+      const bool any = at.next();
+      wait(&sh.item_free[items % kItems], (items / kItems + 1) & 1);  // (the first ones are)
+      if (lane == 0) {
+        Item& i = sh.item[items % kItems];
+        i.any = any;
+        if (any) {
+          i.end = at.whole() ? 0 : static_cast<int>((at.first() + at.tiles - 1) / at.per);
+          i.b = at.b;
+          i.h = at.h;
+          i.n = at.n;
+          i.rt = at.rt;
+          i.row0 = at.row0;
+          i.rows = at.rows;
+          i.tile0 = at.tile0;
+          i.tile1 = at.tile1;
+          i.tiles = at.tiles;
+        }
+        mbar_arrive(&sh.item_ready[items % kItems]);
+      }
+      __syncwarp();
+      if (!any) break;
+    }
   }
   } else {
     // ---- softmax: a row a thread --------------------------------------------------
@@ -723,6 +739,8 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
       if (!whole && at.tile0 == 0 && tid == 0) joins[blockIdx.x] = {at.b, at.h, at.row0, at.rows, at.end, 0};
       if constexpr (!kDual) soft_sync();  // both streams' O may be written again
       tile_no += tiles;
+      stream_sync(s);  // (the last to read the item)
+      if (row_in == 0) mbar_arrive(&sh.item_free[items % kItems]);
     }
   }
   tc_before();
