@@ -61,6 +61,7 @@ constexpr int kScores = 8 + kLoadWarps, kOutputs = kScores + 1;   // the warps t
 constexpr int kWalker = kOutputs + 1;                             // and the one that finds the block's items
 constexpr float kSlackR = 8.f;   // how far (log2) a score may pass the reference
 constexpr int kEndR = 6;         // steps that an item's start and end count as
+constexpr int kLeast = 4;        // tiles that a block gets at least, when there are more blocks than work
 constexpr int kMaxCtas = 160;
 constexpr int kAhead = 32;       // tiles whose valid bits are kept, more than the ring holds
 constexpr int kOdd = 8;          // items whose flag is kept, more than a stream can be behind
@@ -86,6 +87,115 @@ struct Item {
 };
 constexpr int kItems = 8;  // told ahead of the softmax warps' last
 
+// One warp's walk over the items of its block, after attention_common.cuh's cut:
+// an item's tiles and kEndR steps more are numbered item by item, sequence by
+// sequence, and block c takes steps [c * per, (c + 1) * per).  With a block for every
+// item and none of more than kWholeTiles tiles, nothing is cut.
+template <int kRows>
+struct Walker {
+  const AttnArgs& a;
+  long long w, end, per, base;  // step, last step and number of steps of the block; first step of sequence b
+  int lane, b, H, RT, R, n, tiles;
+  bool whole;
+  __device__ __forceinline__ static int divide(long long x, int y) {  // (64 bits take this GPU 500 cycles)
+    return x >> 32 ? static_cast<int>(x / y) : static_cast<int>(static_cast<unsigned>(x) / static_cast<unsigned>(y));
+  }
+  __device__ __forceinline__ void sequence() {
+    n = attn_length(a, b);
+    tiles = attn_tiles<kTile>(n);
+  }
+  __device__ Walker(const AttnArgs& args, int lane_) : a(args), lane(lane_) {
+    H = a.cache.heads;
+    R = a.Q * (a.Hq / H);
+    RT = (R + kRows - 1) / kRows;
+    long long total = 0;
+    int most = 0;
+    bool bad = false;
+#pragma unroll 1
+    for (int i = lane; i < a.B; i += 32) {
+      const int len = attn_length(a, i), t = attn_tiles<kTile>(len);
+      bad |= len != a.lengths[i];
+      most = max(most, t);
+      total += t + kEndR;
+    }
+    if (bad && a.status && blockIdx.x == 0) atomicOr(a.status, kDataLengthRange);
+    most = __reduce_max_sync(0xffffffffu, most);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
+    total *= H * RT;
+    const long long items = static_cast<long long>(a.B) * H * RT;
+    whole = most <= kWholeTiles && items <= gridDim.x;
+    if (whole) {
+      w = blockIdx.x;
+      end = items;
+      b = static_cast<int>(blockIdx.x / static_cast<unsigned>(H * RT));
+      base = static_cast<long long>(b) * H * RT;
+      if (w < end) sequence();
+      return;
+    }
+    per = (total >> 32 ? (total + gridDim.x - 1) / gridDim.x : (static_cast<unsigned>(total) + gridDim.x - 1) / gridDim.x);
+    if (per < kLeast + kEndR) per = kLeast + kEndR;
+    w = per * blockIdx.x;
+    end = min(total, w + per);
+    // the sequence that has step w, 32 sequences at a time
+    base = 0;
+    b = 0;
+    if (w >= end) return;
+#pragma unroll 1
+    for (int i0 = 0;; i0 += 32) {
+      const long long mine = i0 + lane < a.B ? static_cast<long long>(attn_tiles<kTile>(attn_length(a, i0 + lane)) + kEndR) * (H * RT) : 0;
+      long long upto = mine;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const long long o = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += o;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, w < base + upto);
+      if (past) {
+        const int l = __ffs(past) - 1;
+        b = i0 + l;
+        base += __shfl_sync(0xffffffffu, upto - mine, l);
+        break;
+      }
+      base += __shfl_sync(0xffffffffu, upto, 31);
+    }
+    sequence();
+  }
+  __device__ void next(Item& i) {
+    for (;;) {
+      i.any = w < end;
+      if (!i.any) return;
+      const int size = whole ? 1 : tiles + kEndR;
+      if (w >= base + static_cast<long long>(size) * H * RT) {
+        base += static_cast<long long>(size) * H * RT;
+        ++b;
+        sequence();
+        continue;
+      }
+      const long long in = w - base;
+      const int item = divide(in, size), off = static_cast<int>(in - static_cast<long long>(item) * size);
+      const int stop = whole ? 1 : static_cast<int>(min(static_cast<long long>(size), off + (end - w)));
+      i.tile0 = whole ? 0 : max(off - kEndR, 0);  // an item's first kEndR steps are nobody's
+      i.tile1 = whole ? tiles : min(stop - kEndR, tiles);
+      const long long first = base + static_cast<long long>(item) * size + kEndR;  // step of the item's first tile
+      w = whole ? end : w + (stop - off);
+      if (i.tile0 >= i.tile1) continue;
+      i.tiles = tiles;
+      i.n = n;
+      i.b = b;
+      i.rt = item / H;
+      i.h = item - i.rt * H;
+      i.row0 = i.rt * kRows;
+      i.rows = min(kRows, R - i.row0);
+      i.end = i.whole() ? 0 : first + tiles - 1 >= end ? block_of(first + tiles - 1) : static_cast<int>(blockIdx.x);
+      return;
+    }
+  }
+  __device__ __forceinline__ int block_of(long long step) const {
+    return step >> 32 || per >> 31 ? static_cast<int>(step / per) : static_cast<int>(static_cast<unsigned>(step) / static_cast<unsigned>(per));
+  }
+};
+
 // The item whose first tile a block has and whose last one another block; rows 0:
 // there is none.
 struct __align__(8) Join {
@@ -105,7 +215,6 @@ struct Shared {
   int odd[kOdd];              // the item has values that are not finite and not every row sees
   uint32_t tmem;
   int dead;                   // a wait ran out: nothing waits any more
-  long long plan[2 * (kThreadsR / 32) + 4];
 };
 
 // The products of a tile, issued by one lane in one go (a product of its own, with
@@ -220,7 +329,6 @@ __device__ __forceinline__ void stream_sync(int s) { asm volatile("bar.sync %0, 
 template <int D, bool kDual>
 __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const AttnArgs a, DivU64 by_page, Join* joins) {
   using L = Lay<D, kDual>;
-  using Walk = AttnWalk<kTile, kEndR, L::kRows>;
   constexpr int kSlots = L::kSlots, kHalf = L::kHalf, kChunks = D / 8;  // 16-byte pieces of a token
   constexpr int kCols = 512, kStream = 256, kO = 128;                   // TMEM: a stream's S / P buffers, then its O
   extern __shared__ char raw_smem[];
@@ -247,8 +355,6 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tid == 0) joins[blockIdx.x] = {0, 0, 0, 0, 0, 0};
-  const AttnPlan plan = attn_plan<kTile, kEndR, kThreadsR>(
-      a, a.cache.heads * ((a.Q * (a.Hq / a.cache.heads) + L::kRows - 1) / L::kRows), 4, sh.plan);
   if (tid == 0) {
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&sh.full[i], 33);
@@ -442,29 +548,17 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
     __syncwarp();
   } else if (warp == kWalker) {
     // ---- items -------------------------------------------------------------------
-    Walk at(a, plan);
+    Walker<L::kRows> at(a, lane);
     for (int items = 0;; ++items) {
-      const bool any = at.next();
+      Item i;
+      at.next(i);
       wait(&sh.item_free[items % kItems], (items / kItems + 1) & 1);  // (the first ones are)
       if (lane == 0) {
-        Item& i = sh.item[items % kItems];
-        i.any = any;
-        if (any) {
-          i.end = at.whole() ? 0 : static_cast<int>((at.first() + at.tiles - 1) / at.per);
-          i.b = at.b;
-          i.h = at.h;
-          i.n = at.n;
-          i.rt = at.rt;
-          i.row0 = at.row0;
-          i.rows = at.rows;
-          i.tile0 = at.tile0;
-          i.tile1 = at.tile1;
-          i.tiles = at.tiles;
-        }
+        sh.item[items % kItems] = i;
         mbar_arrive(&sh.item_ready[items % kItems]);
       }
       __syncwarp();
-      if (!any) break;
+      if (!i.any) break;
     }
   }
   } else {
@@ -497,12 +591,11 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
       async_fence();
       mbar_arrive(&sh.q_full[kDual ? s : 0]);
     };
+    bool loading = false;  // queries are under way
     if (kDual || s == 0) {
       const Item& x = item(0);
-      if (x.any) {
-        load_q(x);
-        q_loaded();
-      }
+      loading = x.any;
+      if (loading) load_q(x);
     }
     int count = 0, tile_no = 0, sight_b = -1, sight_rt = -1;
     for (int items = 0;; ++items) {
@@ -515,6 +608,8 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
         sight_b = at.b;
         sight_rt = at.rt;
       }
+      if (loading) q_loaded();
+      loading = false;
       if (tid == 0) sh.odd[(items + kOdd / 2) % kOdd] = 0;
       float m = -INFINITY, l = 0.f;
       const int tile0 = at.tile0, tiles = at.tile1 - tile0;
@@ -523,8 +618,7 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
         const int buf = count & 1, t0 = (tile0 + j) * kTile, now = tile_no + j;
         wait(&sh.s_full[s][buf], (count >> 1) & 1);
         tc_after();
-        bool loading = false;  // the item's last scores are done, so its queries have been read
-        if (j == tiles - 1) {
+        if (j == tiles - 1) {  // the item's last scores are done, so its queries have been read
           const Item& next = item(items + 1);
           loading = next.any;
           if (loading) load_q(next);
@@ -637,7 +731,10 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
         tc_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.p_full[s][buf]);
-        if (loading) q_loaded();
+        if (loading) {
+          q_loaded();
+          loading = false;
+        }
       }
 
       // ---- the item, or this block's part of it ---------------------------------
@@ -672,39 +769,55 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
       const float inv = whole ? (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l)) : 1.f;
       const bool odd = *reinterpret_cast<volatile int*>(&sh.odd[items % kOdd]) != 0;
       constexpr int kPart = kDual ? D : D / 2;  // columns that the thread writes
-      if (none) c0 = c1 = 0.f;
       c0 *= inv;
       c1 *= inv;
+      const uint32_t rows = __ballot_sync(0xffffffffu, row);
+      long long to4[4];  // the four lanes' rows
+#pragma unroll
+      for (int k = 0; k < 4; ++k) to4[k] = __shfl_sync(0xffffffffu, static_cast<long long>(to), (lane & 28) | k);
 #pragma unroll 1
-      for (int d = kDual ? 0 : s * kPart, end = d + kPart; d < end; d += 16) {
-        uint32_t u[16];
-        float o[16];
-        ld16(u, tmem + lanes + (kDual ? s * kStream : 0) + kO + d);
+      for (int d = kDual ? 0 : s * kPart, end = d + kPart; d < end; d += 32) {
+        uint32_t u[32];
+        float o[32];
+        ld32(u, tmem + lanes + (kDual ? s * kStream : 0) + kO + d);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) o[i] = __uint_as_float(u[i]) * c0;
+        for (int i = 0; i < 32; ++i) o[i] = none ? 0.f : __uint_as_float(u[i]) * c0;
         if (!kDual && both) {
-          ld16(u, tmem + lanes + kStream + kO + d);
+          ld32(u, tmem + lanes + kStream + kO + d);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] = fmaf(c1, __uint_as_float(u[i]), o[i]);
-        }
-        if (!row) continue;
-        if (none) {  // (0 * NaN)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] = 0.f;
+          for (int i = 0; i < 32; ++i) o[i] = none ? 0.f : fmaf(c1, __uint_as_float(u[i]), o[i]);
         }
         if (whole) {
-          uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + to * D + d);
+          // A row's 16-byte pieces change places with those of the three rows beside it,
+          // so that four lanes write 64 bytes of a row together.
+          uint32_t w[4][4];
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-            out[i] = make_uint4(pack2(o[8 * i], o[8 * i + 1]), pack2(o[8 * i + 2], o[8 * i + 3]), pack2(o[8 * i + 4], o[8 * i + 5]),
-                                pack2(o[8 * i + 6], o[8 * i + 7]));
-        } else {
-          float4* out = reinterpret_cast<float4*>(slot + r * D + d);
+          for (int i = 0; i < 16; ++i) w[i >> 2][i & 3] = pack2(o[2 * i], o[2 * i + 1]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) out[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          for (int bit = 1; bit < 4; bit <<= 1)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (!(k & bit))
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const bool up = lane & bit;
+                  const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? w[k][i] : w[k | bit][i], bit);
+                  if (up) w[k][i] = got;
+                  else w[k | bit][i] = got;
+                }
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if ((rows >> ((lane & 28) | k)) & 1)
+              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + to4[k] * D + d + (lane & 3) * 8) =
+                  make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
+        } else if (row) {
+          float4* out = reinterpret_cast<float4*>(slot) + d / 4 * L::kRows + r;  // (parts lie by four dimensions, then rows)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) out[i * L::kRows] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
         }
       }
-      if (odd && row && !none) {  // by the thread that wrote them
+      __syncwarp();
+      if (odd && row && !none) {
         constexpr int kFrom = kDual ? 0 : kPart;
 #pragma unroll 1
         for (int t = max(at.tile0 * kTile, max(base, 0)); t < min(at.tile1 * kTile, at.n); ++t) {
@@ -722,7 +835,7 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
               uint16_t* out = static_cast<uint16_t*>(a.out) + to * D + d;
               *out = static_cast<uint16_t>(pack2(__uint_as_float(static_cast<uint32_t>(*out) << 16) + y, 0.f));
             } else {
-              slot[r * D + d] += y;
+              slot[(d / 4 * L::kRows + r) * 4 + d % 4] += y;
             }
           }
         }
@@ -751,61 +864,52 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
   }
 }
 
-// One warp a row of a cut item: blocks [block, end] of the launch have left (m, l, O)
-// of it.  Lanes hold the parts' maxima and sums, 32 at a time, then D / 32 values
-// of O each, eight parts' loads under way together.
+// Blocks [block, end] of the launch have left (m, l, O) of a cut item.  A warp joins
+// 16 dimensions of 32 rows, a row a lane, in block order, four parts' loads under
+// way together.
 constexpr int kJoinWarps = 4;
 template <int D, bool kDual>
 __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const AttnArgs a, const Join* joins) {
-  constexpr int kRows = Lay<D, kDual>::kRows, kN = D / 32;
-  using V = typename std::conditional<kN == 4, float4, float2>::type;
+  constexpr int kRows = Lay<D, kDual>::kRows, kSplit = D / 16 / kJoinWarps;  // blocks that share 32 rows
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Join j = joins[blockIdx.x];
-  const int lane = threadIdx.x & 31, r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
-  if (r >= j.rows) return;
-  const int first = blockIdx.x;
-  auto slot = [&](int c) { return attn_slot<kRows, D>(a, c, c == first); };
+  const int first = blockIdx.x, lane = threadIdx.x & 31;
+  const int r0 = blockIdx.y / kSplit * 32, d0 = (blockIdx.y % kSplit * kJoinWarps + (threadIdx.x >> 5)) * 16;
+  if (r0 >= j.rows) return;
+  const int r = min(r0 + lane, j.rows - 1);
+  auto slot = [&](int c) { return attn_slot<kRows, D>(a, c, c == first) + 4 * r; };  // row r's first four values
   float m = -INFINITY;
-  for (int c0 = first; c0 <= j.end; c0 += 32)
-    if (c0 + lane <= j.end) m = fmaxf(m, slot(c0 + lane)[kRows * D + r]);
+#pragma unroll 4
+  for (int c = first; c <= j.end; ++c) m = fmaxf(m, slot(c)[kRows * D - 3 * r]);
+  float l = 0.f, o[16];
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-  float l = 0.f, o[kN];
+  for (int i = 0; i < 16; ++i) o[i] = 0.f;
+#pragma unroll 4
+  for (int c = first; c <= j.end; ++c) {
+    const float* s = slot(c);
+    const float mc = s[kRows * D - 3 * r], lc = s[kRows * D + kRows - 3 * r];
+    const float w = mc == -INFINITY ? 1.f : ex2(mc - m);  // a part without a maximum holds zeros, or NaN that it passes on
+    l = fmaf(w, lc, l);
 #pragma unroll
-  for (int i = 0; i < kN; ++i) o[i] = 0.f;
-  for (int c0 = first; c0 <= j.end; c0 += 32) {
-    float w = 0.f;
-    if (c0 + lane <= j.end) {
-      const float* s = slot(c0 + lane) + kRows * D + r;
-      w = s[0] == -INFINITY ? 1.f : ex2(s[0] - m);  // a part without a maximum holds zeros, or NaN that it passes on
-      l = fmaf(w, s[kRows], l);
-    }
-    const int parts = min(32, j.end - c0 + 1);
-    for (int c = 0; c < parts; c += 8) {
-      V v[8];
-#pragma unroll
-      for (int y = 0; y < 8; ++y)
-        if (c + y < parts) v[y] = *reinterpret_cast<const V*>(slot(c0 + c + y) + r * D + lane * kN);
-#pragma unroll
-      for (int y = 0; y < 8; ++y) {
-        const float wy = __shfl_sync(0xffffffffu, w, c + y);
-        if (c + y < parts) {
-          const float* x = reinterpret_cast<const float*>(&v[y]);
-#pragma unroll
-          for (int i = 0; i < kN; ++i) o[i] = fmaf(wy, x[i], o[i]);
-        }
-      }
+    for (int i = 0; i < 4; ++i) {
+      const float4 v = *reinterpret_cast<const float4*>(s + (d0 / 4 + i) * (kRows * 4));
+      o[4 * i] = fmaf(w, v.x, o[4 * i]);
+      o[4 * i + 1] = fmaf(w, v.y, o[4 * i + 1]);
+      o[4 * i + 2] = fmaf(w, v.z, o[4 * i + 2]);
+      o[4 * i + 3] = fmaf(w, v.w, o[4 * i + 3]);
     }
   }
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+  if (r0 + lane >= j.rows) return;
   const AttnRow ar = attn_row(a, j.row0 + r, j.h);
   const size_t at = (static_cast<size_t>(j.b) * a.Q + ar.i) * a.Hq + ar.hq;
   const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-  uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + at * D + lane * kN);
-  if constexpr (kN == 4) *reinterpret_cast<uint2*>(out) = make_uint2(pack2(o[0] * inv, o[1] * inv), pack2(o[2] * inv, o[3] * inv));
-  else *out = pack2(o[0] * inv, o[1] * inv);
-  if (lane == 0 && a.lse) a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+  uint32_t u[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) u[i] = pack2(o[2 * i] * inv, o[2 * i + 1] * inv);
+  uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at * D + d0);
+  out[0] = make_uint4(u[0], u[1], u[2], u[3]);
+  out[1] = make_uint4(u[4], u[5], u[6], u[7]);
+  if (d0 == 0 && a.lse) a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 template <int D, bool kDual>
@@ -829,7 +933,7 @@ cudaError_t launch(const AttnArgs& a, int sm_count, cudaStream_t stream) {
       static_cast<int64_t>(a.B) * a.cache.heads * tiles <= grid)
     return cudaGetLastError();
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, ((R < L::kRows ? R : L::kRows) + kJoinWarps - 1) / kJoinWarps);
+  cfg.gridDim = dim3(grid, ((R < L::kRows ? R : L::kRows) + 31) / 32 * (D / 16 / kJoinWarps));
   cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.stream = stream;
   cudaLaunchAttribute after[1];
