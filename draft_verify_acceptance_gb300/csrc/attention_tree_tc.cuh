@@ -52,15 +52,16 @@ using tc::tmem_st_done;
 constexpr int kTile = 64;        // tokens
 constexpr int kSoft = 256;       // softmax threads, 128 a stream
 constexpr int kLoadWarps = 4;    // K and V of the even and of the odd tiles
-constexpr int kThreadsR = kSoft + kLoadWarps * 32 + 128;           // (one warp of the last four is idle)
+constexpr int kThreadsR = kSoft + kLoadWarps * 32 + 128;
 // Registers a thread: 512 x 128 at the launch, then shared out by groups of four
 // warps, 2 x 128 x (176 + 80) = 512 x 128.
 constexpr int kSoftRegs = 176, kOtherRegs = 80;
 static_assert(kSoft * kSoftRegs + (kThreadsR - kSoft) * kOtherRegs <= 65536 && kThreadsR * 128 <= 65536, "registers");
 constexpr int kScores = 8 + kLoadWarps, kOutputs = kScores + 1;   // the warps that issue products,
-constexpr int kWalker = kOutputs + 1;                             // and the one that finds the block's items
+constexpr int kWalker = kOutputs + 1, kQueries = kWalker + 1;     // the one that finds the block's items, the one that copies queries
 constexpr float kSlackR = 8.f;   // how far (log2) a score may pass the reference
-constexpr int kEndR = 6;         // steps that an item's start and end count as
+template <bool kDual>
+constexpr int kEndR = kDual ? 5 : 8;  // steps that an item's start and end count as
 constexpr int kLeast = 4;        // tiles that a block gets at least, when there are more blocks than work
 constexpr int kMaxCtas = 160;
 constexpr int kAhead = 32;       // tiles whose valid bits are kept, more than the ring holds
@@ -87,15 +88,28 @@ struct Item {
 };
 constexpr int kItems = 8;  // told ahead of the softmax warps' last
 
+// What the host divides for the kernel (32-bit divisions take some 140 cycles, 64-bit ones 500).
+struct Shape {
+  int G, R, RT;  // query heads of a cache head, rows of one (nodes times G), items that they make
+  DivU64 by_page, by_group, by_heads, by_items;  // page_size, G, cache heads, items of a sequence
+};
+__device__ __forceinline__ AttnRow row_of(const Shape& z, int row, int h) {
+  AttnRow r;
+  r.i = static_cast<int>(z.by_group(static_cast<unsigned long long>(row)));
+  r.hq = h * z.G + (row - r.i * z.G);
+  return r;
+}
+
 // One warp's walk over the items of its block, after attention_common.cuh's cut:
-// an item's tiles and kEndR steps more are numbered item by item, sequence by
+// an item's tiles and kEnd steps more are numbered item by item, sequence by
 // sequence, and block c takes steps [c * per, (c + 1) * per).  With a block for every
 // item and none of more than kWholeTiles tiles, nothing is cut.
-template <int kRows>
+template <int kRows, int kEnd>
 struct Walker {
   const AttnArgs& a;
   long long w, end, per, base;  // step, last step and number of steps of the block; first step of sequence b
-  int lane, b, H, RT, R, n, tiles;
+  const Shape& z;
+  int lane, b, H, RT, n, tiles;
   bool whole;
   __device__ __forceinline__ static int divide(long long x, int y) {  // (64 bits take this GPU 500 cycles)
     return x >> 32 ? static_cast<int>(x / y) : static_cast<int>(static_cast<unsigned>(x) / static_cast<unsigned>(y));
@@ -104,10 +118,9 @@ struct Walker {
     n = attn_length(a, b);
     tiles = attn_tiles<kTile>(n);
   }
-  __device__ Walker(const AttnArgs& args, int lane_) : a(args), lane(lane_) {
+  __device__ Walker(const AttnArgs& args, const Shape& shape, int lane_) : a(args), z(shape), lane(lane_) {
     H = a.cache.heads;
-    R = a.Q * (a.Hq / H);
-    RT = (R + kRows - 1) / kRows;
+    RT = z.RT;
     long long total = 0;
     int most = 0;
     bool bad = false;
@@ -116,7 +129,7 @@ struct Walker {
       const int len = attn_length(a, i), t = attn_tiles<kTile>(len);
       bad |= len != a.lengths[i];
       most = max(most, t);
-      total += t + kEndR;
+      total += t + kEnd;
     }
     if (bad && a.status && blockIdx.x == 0) atomicOr(a.status, kDataLengthRange);
     most = __reduce_max_sync(0xffffffffu, most);
@@ -128,13 +141,13 @@ struct Walker {
     if (whole) {
       w = blockIdx.x;
       end = items;
-      b = static_cast<int>(blockIdx.x / static_cast<unsigned>(H * RT));
+      b = static_cast<int>(z.by_items(blockIdx.x));
       base = static_cast<long long>(b) * H * RT;
       if (w < end) sequence();
       return;
     }
     per = (total >> 32 ? (total + gridDim.x - 1) / gridDim.x : (static_cast<unsigned>(total) + gridDim.x - 1) / gridDim.x);
-    if (per < kLeast + kEndR) per = kLeast + kEndR;
+    if (per < kLeast + kEnd) per = kLeast + kEnd;
     w = per * blockIdx.x;
     end = min(total, w + per);
     // the sequence that has step w, 32 sequences at a time
@@ -143,7 +156,7 @@ struct Walker {
     if (w >= end) return;
 #pragma unroll 1
     for (int i0 = 0;; i0 += 32) {
-      const long long mine = i0 + lane < a.B ? static_cast<long long>(attn_tiles<kTile>(attn_length(a, i0 + lane)) + kEndR) * (H * RT) : 0;
+      const long long mine = i0 + lane < a.B ? static_cast<long long>(attn_tiles<kTile>(attn_length(a, i0 + lane)) + kEnd) * (H * RT) : 0;
       long long upto = mine;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -165,7 +178,7 @@ struct Walker {
     for (;;) {
       i.any = w < end;
       if (!i.any) return;
-      const int size = whole ? 1 : tiles + kEndR;
+      const int size = whole ? 1 : tiles + kEnd;
       if (w >= base + static_cast<long long>(size) * H * RT) {
         base += static_cast<long long>(size) * H * RT;
         ++b;
@@ -175,18 +188,18 @@ struct Walker {
       const long long in = w - base;
       const int item = divide(in, size), off = static_cast<int>(in - static_cast<long long>(item) * size);
       const int stop = whole ? 1 : static_cast<int>(min(static_cast<long long>(size), off + (end - w)));
-      i.tile0 = whole ? 0 : max(off - kEndR, 0);  // an item's first kEndR steps are nobody's
-      i.tile1 = whole ? tiles : min(stop - kEndR, tiles);
-      const long long first = base + static_cast<long long>(item) * size + kEndR;  // step of the item's first tile
+      i.tile0 = whole ? 0 : max(off - kEnd, 0);  // an item's first kEnd steps are nobody's
+      i.tile1 = whole ? tiles : min(stop - kEnd, tiles);
+      const long long first = base + static_cast<long long>(item) * size + kEnd;  // step of the item's first tile
       w = whole ? end : w + (stop - off);
       if (i.tile0 >= i.tile1) continue;
       i.tiles = tiles;
       i.n = n;
       i.b = b;
-      i.rt = item / H;
+      i.rt = static_cast<int>(z.by_heads(static_cast<unsigned long long>(item)));
       i.h = item - i.rt * H;
       i.row0 = i.rt * kRows;
-      i.rows = min(kRows, R - i.row0);
+      i.rows = min(kRows, z.R - i.row0);
       i.end = i.whole() ? 0 : first + tiles - 1 >= end ? block_of(first + tiles - 1) : static_cast<int>(blockIdx.x);
       return;
     }
@@ -205,11 +218,10 @@ struct __align__(8) Join {
 template <int D, bool kDual>
 struct Shared {
   unsigned long long full[Lay<D, kDual>::kSlots], empty[Lay<D, kDual>::kSlots];
-  unsigned long long s_full[2][2], p_full[2][2], pv_done[2][2], q_full[2] /* one for both streams of shared rows */, done[2];
+  unsigned long long s_full[2][2], p_full[2][2], pv_done[2][2], q_full, q_free, done[2];
   unsigned long long item_ready[kItems], item_free[kItems];
   Item item[kItems];
   uint2 valid[kAhead];  // tokens that exist, by tile
-  long long q_off[2][128];    // of the next item's rows, bytes
   TreeSight<128> sight[2];
   float m[2][128], l[2][128];
   int odd[kOdd];              // the item has values that are not finite and not every row sees
@@ -327,7 +339,7 @@ __device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 256;" ::
 __device__ __forceinline__ void stream_sync(int s) { asm volatile("bar.sync %0, 128;" ::"r"(3 + s) : "memory"); }
 
 template <int D, bool kDual>
-__global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const AttnArgs a, DivU64 by_page, Join* joins) {
+__global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const AttnArgs a, const Shape z, Join* joins) {
   using L = Lay<D, kDual>;
   constexpr int kSlots = L::kSlots, kHalf = L::kHalf, kChunks = D / 8;  // 16-byte pieces of a token
   constexpr int kCols = 512, kStream = 256, kO = 128;                   // TMEM: a stream's S / P buffers, then its O
@@ -366,13 +378,14 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
         mbar_init(&sh.p_full[s][i], 4);
         mbar_init(&sh.pv_done[s][i], 1);
       }
-      mbar_init(&sh.q_full[s], 128);
       mbar_init(&sh.done[s], 1);
     }
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&sh.item_ready[i], 1);
       mbar_init(&sh.item_free[i], 2);
     }
+    mbar_init(&sh.q_full, L::kRows);
+    mbar_init(&sh.q_free, 1);
     for (int i = 0; i < kOdd; ++i) sh.odd[i] = 0;
     sh.dead = 0;
     fence_barrier_init();
@@ -386,6 +399,20 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
   auto item = [&](int k) -> const Item& {
     wait(&sh.item_ready[k % kItems], (k / kItems) & 1);
     return sh.item[k % kItems];
+  };
+
+  // Copies 32 rows of an item's queries; behind the last row come zeros.
+  auto load_q = [&](const Item& at, int y) {
+    constexpr int kStep = 32 / kChunks;
+    const int rows = at.rows, chunk = lane % kChunks, r0 = lane / kChunks;
+    const AttnRow ar = row_of(z, at.row0 + min(y * 32 + lane, rows - 1), at.h);
+    const long long off = at.b * a.q_batch + ar.i * a.q_token + ar.hq * a.q_head;
+    const uint32_t to = smem_addr(q_s) + (y >> 2) * (128 * D * 2) + (chunk >> 3) * (128 * 128) + ((y & 3) * 32 + r0) * 128;
+#pragma unroll 4
+    for (int i = 0; i < 32; i += kStep)
+      cp16(to + i * 128 + (((chunk & 7) ^ ((i + r0) & 7)) << 4), a.q + __shfl_sync(0xffffffffu, off, i + r0) + chunk * 16,
+           y * 32 + i + r0 < rows ? 16 : 0);
+    cp_arrive(&sh.q_full);
   };
 
   if (warp >= 8) {
@@ -428,7 +455,7 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         const int t = tile * kTile + y * 32 + lane;
-        const int entry = static_cast<int>(by_page(static_cast<unsigned long long>(t)));
+        const int entry = static_cast<int>(z.by_page(static_cast<unsigned long long>(t)));
         p.place[y] = t < n ? t - entry * S : -1;
         p.page[y] = t < n ? __ldg(ids + entry) : -1;
       }
@@ -494,20 +521,20 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
       const int tiles = at.tile1 - at.tile0;
       for (int j = 0; j < tiles; ++j, ++tile_no) {
         const int slot = (2 * tile_no) % kSlots;
+        if (j == 0) wait(&sh.q_full, items & 1);
         wait(&sh.full[slot], ((2 * tile_no) / kSlots) & 1);
         async_fence();  // the copies, to the products
 #pragma unroll 1
         for (int s = kDual ? 0 : j & 1; s < (kDual ? 2 : (j & 1) + 1); ++s) {
           const int c = kDual ? tile_no : s ? count1++ : count0++, buf = c & 1;
-          if (j == 0) {
-            wait(&sh.q_full[s], items & 1);
-            async_fence();
-          }
           wait(&sh.pv_done[s][buf], ((c >> 1) + 1) & 1);  // (the first of a buffer finds it free)
           tc_after();
           scores_mma<D>(tmem + s * kStream + buf * kTile, operand(q_at + (kDual ? s : 0) * (128 * D * 2), 16, 1024, 2),
                         operand(ring + slot * L::kSlot, 16, 1024, 2));
-          if (!kDual || s == 1) tc_commit(&sh.empty[slot]);
+          if (!kDual || s == 1) {
+            tc_commit(&sh.empty[slot]);
+            if (j == tiles - 1) tc_commit(&sh.q_free);
+          }
           tc_commit(&sh.s_full[s][buf]);
         }
       }
@@ -548,7 +575,7 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
     __syncwarp();
   } else if (warp == kWalker) {
     // ---- items -------------------------------------------------------------------
-    Walker<L::kRows> at(a, lane);
+    Walker<L::kRows, kEndR<kDual>> at(a, z, lane);
     for (int items = 0;; ++items) {
       Item i;
       at.next(i);
@@ -560,6 +587,17 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
       __syncwarp();
       if (!i.any) break;
     }
+  } else {
+    // ---- queries, from the second item on --------------------------------------------
+    for (int items = 0;; ++items) {
+      const Item& at = item(items);
+      if (!at.any) break;
+      if (items == 0) continue;
+      wait(&sh.q_free, (items - 1) & 1);  // the scores of the item before are done
+#pragma unroll 1
+      for (int y = 0; y < L::kRows / 32; ++y) load_q(at, y);
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
   }
   } else {
     // ---- softmax: a row a thread --------------------------------------------------
@@ -571,31 +609,9 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
     const float scale = fabsf(a.scale_log2) > 0.f ? fabsf(a.scale_log2) : 1.f;
     const bool turned = !(a.scale_log2 > 0.f), flat = a.scale_log2 == 0.f;  // scores change their sign; are all zero
     TreeSight<128>& sight = sh.sight[s];
-    auto load_q = [&](const Item& x) {  // under way when it returns
-      stream_sync(s);  // (q_off is free)
-      {
-        const AttnRow ar = attn_row(a, x.row0 + min(row_at + row_in, x.rows - 1), x.h);
-        sh.q_off[s][row_in] = x.b * a.q_batch + ar.i * a.q_token + ar.hq * a.q_head;
-      }
-      stream_sync(s);
-      const uint32_t to = smem_addr(q_s) + (kDual ? s : 0) * (128 * D * 2);
-      const int rows = x.rows - row_at;
-#pragma unroll 2
-      for (int e = row_in; e < 128 * kChunks; e += 128) {
-        const int r = e / kChunks, c = e % kChunks;
-        cp16(to + (c >> 3) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4), a.q + sh.q_off[s][r] + c * 16, r < rows ? 16 : 0);
-      }
-    };
-    auto q_loaded = [&]() {
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      async_fence();
-      mbar_arrive(&sh.q_full[kDual ? s : 0]);
-    };
-    bool loading = false;  // queries are under way
-    if (kDual || s == 0) {
-      const Item& x = item(0);
-      loading = x.any;
-      if (loading) load_q(x);
+    if (warp < L::kRows / 32) {  // the first item's queries
+      const Item& at = item(0);
+      if (at.any) load_q(at, warp);
     }
     int count = 0, tile_no = 0, sight_b = -1, sight_rt = -1;
     for (int items = 0;; ++items) {
@@ -608,8 +624,6 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
         sight_b = at.b;
         sight_rt = at.rt;
       }
-      if (loading) q_loaded();
-      loading = false;
       if (tid == 0) sh.odd[(items + kOdd / 2) % kOdd] = 0;
       float m = -INFINITY, l = 0.f;
       const int tile0 = at.tile0, tiles = at.tile1 - tile0;
@@ -618,11 +632,6 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
         const int buf = count & 1, t0 = (tile0 + j) * kTile, now = tile_no + j;
         wait(&sh.s_full[s][buf], (count >> 1) & 1);
         tc_after();
-        if (j == tiles - 1) {  // the item's last scores are done, so its queries have been read
-          const Item& next = item(items + 1);
-          loading = next.any;
-          if (loading) load_q(next);
-        }
         const uint32_t at_s = s_col + buf * kTile;
         const uint2 valid = sh.valid[now % kAhead];
         // a tile whose tokens all exist and come before the tree needs no mask
@@ -731,10 +740,6 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
         tc_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.p_full[s][buf]);
-        if (loading) {
-          q_loaded();
-          loading = false;
-        }
       }
 
       // ---- the item, or this block's part of it ---------------------------------
@@ -763,7 +768,7 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
         m = -INFINITY;
         l = 0.f;
       }
-      const AttnRow ar = attn_row(a, at.row0 + min(r, at.rows - 1), at.h);
+      const AttnRow ar = row_of(z, at.row0 + min(r, at.rows - 1), at.h);
       const size_t to = (static_cast<size_t>(at.b) * a.Q + ar.i) * a.Hq + ar.hq;
       float* slot = attn_slot<L::kRows, D>(a, blockIdx.x, at.tile0 == 0);
       const float inv = whole ? (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l)) : 1.f;
@@ -822,7 +827,7 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
 #pragma unroll 1
         for (int t = max(at.tile0 * kTile, max(base, 0)); t < min(at.tile1 * kTile, at.n); ++t) {
           if (!sight.sees(row_in, t - base)) continue;
-          const int entry = static_cast<int>(by_page(static_cast<unsigned long long>(t)));
+          const int entry = static_cast<int>(z.by_page(static_cast<unsigned long long>(t)));
           const int page = a.table.ids[at.b * a.table.stride + entry];
           if (page < 0 || page >= a.cache.pages) continue;
           const char* v = a.cache.v + page * a.cache.page_stride + (t - entry * a.cache.page_size) * a.cache.token_stride +
@@ -869,7 +874,7 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
 // way together.
 constexpr int kJoinWarps = 4;
 template <int D, bool kDual>
-__global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const AttnArgs a, const Join* joins) {
+__global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const AttnArgs a, const Shape z, const Join* joins) {
   constexpr int kRows = Lay<D, kDual>::kRows, kSplit = D / 16 / kJoinWarps;  // blocks that share 32 rows
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Join j = joins[blockIdx.x];
@@ -878,29 +883,43 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const AttnAr
   if (r0 >= j.rows) return;
   const int r = min(r0 + lane, j.rows - 1);
   auto slot = [&](int c) { return attn_slot<kRows, D>(a, c, c == first) + 4 * r; };  // row r's first four values
-  float m = -INFINITY;
-#pragma unroll 4
-  for (int c = first; c <= j.end; ++c) m = fmaxf(m, slot(c)[kRows * D - 3 * r]);
-  float l = 0.f, o[16];
+  float m = -INFINITY, l = 0.f, o[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) o[i] = 0.f;
-#pragma unroll 4
-  for (int c = first; c <= j.end; ++c) {
-    const float* s = slot(c);
-    const float mc = s[kRows * D - 3 * r], lc = s[kRows * D + kRows - 3 * r];
-    const float w = mc == -INFINITY ? 1.f : ex2(mc - m);  // a part without a maximum holds zeros, or NaN that it passes on
-    l = fmaf(w, lc, l);
+  for (int c0 = first; c0 <= j.end; c0 += 4) {
+    float mc[4], lc[4];
+    float4 v[4][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 v = *reinterpret_cast<const float4*>(s + (d0 / 4 + i) * (kRows * 4));
-      o[4 * i] = fmaf(w, v.x, o[4 * i]);
-      o[4 * i + 1] = fmaf(w, v.y, o[4 * i + 1]);
-      o[4 * i + 2] = fmaf(w, v.z, o[4 * i + 2]);
-      o[4 * i + 3] = fmaf(w, v.w, o[4 * i + 3]);
+    for (int y = 0; y < 4; ++y) {
+      const bool part = c0 + y <= j.end;
+      const float* s = slot(min(c0 + y, j.end));
+      mc[y] = part ? s[kRows * D - 3 * r] : -INFINITY;
+      lc[y] = part ? s[kRows * D + kRows - 3 * r] : 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        v[y][i] = part ? *reinterpret_cast<const float4*>(s + (d0 / 4 + i) * (kRows * 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    const float before = m;
+    m = fmaxf(fmaxf(m, fmaxf(mc[0], mc[1])), fmaxf(mc[2], mc[3]));
+    const float keep = before == -INFINITY ? 1.f : ex2(before - m);
+    l *= keep;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[i] *= keep;
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+      const float w = mc[y] == -INFINITY ? 1.f : ex2(mc[y] - m);  // a part without a maximum holds zeros, or NaN that it passes on
+      l = fmaf(w, lc[y], l);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        o[4 * i] = fmaf(w, v[y][i].x, o[4 * i]);
+        o[4 * i + 1] = fmaf(w, v[y][i].y, o[4 * i + 1]);
+        o[4 * i + 2] = fmaf(w, v[y][i].z, o[4 * i + 2]);
+        o[4 * i + 3] = fmaf(w, v[y][i].w, o[4 * i + 3]);
+      }
     }
   }
   if (r0 + lane >= j.rows) return;
-  const AttnRow ar = attn_row(a, j.row0 + r, j.h);
+  const AttnRow ar = row_of(z, j.row0 + r, j.h);
   const size_t at = (static_cast<size_t>(j.b) * a.Q + ar.i) * a.Hq + ar.hq;
   const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
   uint32_t u[8];
@@ -925,15 +944,21 @@ cudaError_t launch(const AttnArgs& a, int sm_count, cudaStream_t stream) {
   using L = Lay<D, kDual>;
   const int grid = sm_count < kMaxCtas ? sm_count : kMaxCtas;
   Join* joins = reinterpret_cast<Join*>(a.partials + static_cast<size_t>(kMaxCtas) * 2 * L::kRows * (D + 2));
-  attention_tree_kernel<D, kDual><<<grid, kThreadsR, L::kBytes, stream>>>(
-      a, DivU64::make(static_cast<unsigned long long>(a.cache.page_size)), joins);
-  const int R = a.Q * (a.Hq / a.cache.heads), tiles = (R + L::kRows - 1) / L::kRows;
+  Shape z;
+  z.G = a.Hq / a.cache.heads;
+  z.R = a.Q * z.G;
+  z.RT = (z.R + L::kRows - 1) / L::kRows;
+  z.by_page = DivU64::make(static_cast<unsigned long long>(a.cache.page_size));
+  z.by_group = DivU64::make(static_cast<unsigned long long>(z.G));
+  z.by_heads = DivU64::make(static_cast<unsigned long long>(a.cache.heads));
+  z.by_items = DivU64::make(static_cast<unsigned long long>(a.cache.heads) * z.RT);
+  attention_tree_kernel<D, kDual><<<grid, kThreadsR, L::kBytes, stream>>>(a, z, joins);
   // sequences that the table has no room to make long are not cut (attn_plan)
   if (static_cast<int64_t>(a.table.max_pages) * a.cache.page_size <= kWholeTiles * kTile &&
-      static_cast<int64_t>(a.B) * a.cache.heads * tiles <= grid)
+      static_cast<int64_t>(a.B) * a.cache.heads * z.RT <= grid)
     return cudaGetLastError();
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, ((R < L::kRows ? R : L::kRows) + 31) / 32 * (D / 16 / kJoinWarps));
+  cfg.gridDim = dim3(grid, ((z.R < L::kRows ? z.R : L::kRows) + 31) / 32 * (D / 16 / kJoinWarps));
   cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.stream = stream;
   cudaLaunchAttribute after[1];
@@ -941,7 +966,7 @@ cudaError_t launch(const AttnArgs& a, int sm_count, cudaStream_t stream) {
   after[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = after;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, tree_join_kernel<D, kDual>, a, static_cast<const Join*>(joins));
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, tree_join_kernel<D, kDual>, a, z, static_cast<const Join*>(joins));
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
