@@ -289,18 +289,21 @@ __device__ __forceinline__ void ld32(uint32_t (&r)[32], uint32_t at) {
       : "r"(at)
       : "memory");
 }
+__device__ __forceinline__ void ld64(uint32_t (&r)[64], uint32_t at) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+      "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,"
+      "%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n\ttcgen05.wait::ld.sync.aligned;"
+      : SPEC_R8(r, 0), SPEC_R8(r, 8), SPEC_R8(r, 16), SPEC_R8(r, 24), SPEC_R8(r, 32), SPEC_R8(r, 40), SPEC_R8(r, 48), SPEC_R8(r, 56)
+      : "r"(at)
+      : "memory");
+}
 __device__ __forceinline__ void ld16(uint32_t (&r)[16], uint32_t at) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
       : SPEC_R8(r, 0), SPEC_R8(r, 8)
       : "r"(at)
-      : "memory");
-}
-__device__ __forceinline__ void st32(uint32_t at, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::SPEC_I8(r, 0), SPEC_I8(r, 8), SPEC_I8(r, 16), SPEC_I8(r, 24), "r"(at)
       : "memory");
 }
 __device__ __forceinline__ void st16(uint32_t at, const uint32_t (&r)[16]) {
@@ -662,31 +665,28 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
             }
           }
         }
-        // the largest score; masked ones go back to TMEM
+        uint32_t x[64];
+        ld64(x, at_s);
+        if (masked || turned) {
+          if (turned) {
+#pragma unroll
+            for (int i = 0; i < 64; ++i) x[i] = flat ? 0u : x[i] ^ 0x80000000u;
+          }
+          const uint32_t see[2] = {valid.x & sight.window(row_in, t0 - base), valid.y & sight.window(row_in, t0 + 32 - base)};
+#pragma unroll
+          for (int i = 0; i < 64; ++i)
+            if (!((see[i >> 5] >> (i & 31)) & 1)) x[i] = 0xff800000u;  // -inf
+        }
         float top = -INFINITY;
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          uint32_t x[32];
-          ld32(x, at_s + h * 32);
-          if (masked || turned) {
-            if (turned) {
+        {
+          float y[3] = {-INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-              for (int i = 0; i < 32; ++i) x[i] = flat ? 0u : x[i] ^ 0x80000000u;
-            }
-            const uint32_t see = (h ? valid.y : valid.x) & sight.window(row_in, t0 + h * 32 - base);
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (!((see >> i) & 1)) x[i] = 0xff800000u;  // -inf
-            st32(at_s + h * 32, x);
-            tmem_st_done();
-          }
-          float y = -INFINITY;
-#pragma unroll
-          for (int i = 0; i < 32; i += 4) {
+          for (int i = 0; i < 64; i += 8) {
             top = max3(top, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
-            y = max3(y, __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
+#pragma unroll
+            for (int k = 0; k < 3; ++k) y[k] = max3(y[k], __uint_as_float(x[i + 2 + 2 * k]), __uint_as_float(x[i + 3 + 2 * k]));
           }
-          top = fmaxf(top, y);
+          top = fmaxf(max3(top, y[0], y[1]), y[2]);
         }
         top *= scale;
         const bool grow = top > m + kSlackR;
@@ -709,23 +709,22 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
         }
         const float less = m == -INFINITY ? 0.f : -m;
         const uint64_t scale2 = pair(__float_as_uint(scale), __float_as_uint(scale)), less2 = pair(__float_as_uint(less), __float_as_uint(less));
-        uint64_t sum0 = 0, sum1 = 0;  // (two fp32 zeros)
-#pragma unroll 1
+        const uint64_t minus2 = pair(0xbf800000u, 0xbf800000u);  // -1
+        uint64_t sum0 = 0, sum1 = 0;                             // (two fp32 zeros)
+#pragma unroll
         for (int h = 0; h < 2; ++h) {
-          uint32_t x[32], hi[16], lo[16];
-          ld32(x, at_s + h * 32);
+          uint32_t hi[16], lo[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             float p0, p1;
-            split(fma2(pair(x[2 * i], x[2 * i + 1]), scale2, less2), p0, p1);
+            split(fma2(pair(x[h * 32 + 2 * i], x[h * 32 + 2 * i + 1]), scale2, less2), p0, p1);
             p0 = ex2(p0);
             p1 = ex2(p1);
             const uint64_t p = pair(__float_as_uint(p0), __float_as_uint(p1));
             if (i & 1) sum1 = add2(sum1, p);
             else sum0 = add2(sum0, p);
             hi[i] = pack2(p0, p1);
-            // (the sign turned with the halves' unpacking)
-            split(add2(p, pair((hi[i] << 16) ^ 0x80000000u, (hi[i] & 0xffff0000u) ^ 0x80000000u)), p0, p1);
+            split(fma2(pair(hi[i] << 16, hi[i] & 0xffff0000u), minus2, p), p0, p1);
             lo[i] = pack2(p0, p1);
           }
           st16(at_s + h * 32, hi);
