@@ -82,112 +82,167 @@ struct Piece {
 
 constexpr int kMaxFreq = 128;
 constexpr int kAppendWarps = 8;
+constexpr int kBatch = 4;  // units, and pieces of the values, that a lane has under way
 
-// A token's work in units: a unit of a rotated head is a piece of 16 bytes and
-// the one n_freq dimensions on (interleaved: one piece, its pairs side by side),
-// or a piece behind the rotated dimensions; then come the values' pieces.
+// Division of indexes below 2^23 by up to 2^8: one multiply-high.
+struct Div32 {
+  uint32_t m = 0;  // 0: divide by 1
+  static Div32 make(int d) {
+    Div32 r;
+    r.m = d <= 1 ? 0u : static_cast<uint32_t>((1ull << 32) / static_cast<unsigned>(d) + 1);
+    return r;
+  }
+  __device__ __forceinline__ int operator()(int n) const { return m ? static_cast<int>(__umulhi(static_cast<uint32_t>(n), m)) : n; }
+};
+
+// 16 bytes that are read once.  (Not by the read-only path: the queries may be rotated in place.)
+__device__ __forceinline__ uint4 ld_once(const uint4* p) { return __ldcs(p); }
+
+// A token's queries and keys are units: a piece of 16 bytes of a rotated head and
+// the one n_freq dimensions on (interleaved: one piece, its pairs side by side), or
+// a piece behind the rotated dimensions; its values are pieces.  `parts` warps share
+// a token.  A warp's first units and pieces are under way while it finds the
+// token's place and turns its angles, which every part does for itself.
 template <typename E, bool kInterleaved>
 __global__ void __launch_bounds__(kAppendWarps * 32)
-rotated_append_kernel(const RotatedAppendArgs a, int parts, DivU64 by_part, DivU64 by_unit) {
+rotated_append_kernel(const RotatedAppendArgs a, int parts, DivU64 by_part, Div32 by_unit) {
   constexpr int kN = Piece<E>::kN;
-  __shared__ float2 s_turn[kAppendWarps][kMaxFreq];
+  __shared__ float2 s_turn[kAppendWarps][kMaxFreq];  // of pair p of a unit's pairs, unit u: p * turned + u, so that lanes read side by side
+  constexpr int kPairs = kInterleaved ? kN / 2 : kN;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long job = static_cast<long long>(blockIdx.x) * kAppendWarps + warp;
   const int row = static_cast<int>(by_part(static_cast<unsigned long long>(job)));
   const int part = static_cast<int>(job - static_cast<long long>(row) * parts);
   if (row >= a.T) return;
   const int D = a.cache.head_dim, F = a.n_freq, H = a.cache.heads;
+  const int turned = kInterleaved ? 2 * F / kN : F / kN, per_head = turned + (D - 2 * F) / kN;
+  const int units = (a.q_heads + H) * per_head, q_units = a.q_heads * per_head, pieces = H * (D / kN), stride = parts * 32;
+  const char* q = a.q + row * a.q_stride;
+  const char* k = a.k_new + row * a.new_stride;
+  const uint4* v = reinterpret_cast<const uint4*>(a.v_new + row * a.new_stride);
+
+  uint4 x[kBatch], y[kBatch], w[kBatch];
+  auto unit_at = [&](int j, int& u) -> long long {  // byte offset in the queries' or the keys' row
+    const int jj = j < q_units ? j : j - q_units, head = by_unit(jj);
+    u = jj - head * per_head;
+    return static_cast<long long>(head) * (D * E::kBytes);
+  };
+  auto load = [&](int j0) {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int j = j0 + i * stride;
+      if (j >= units) break;
+      int u;
+      const long long in = unit_at(j, u);
+      const uint4* from = reinterpret_cast<const uint4*>((j < q_units ? q : k) + in);
+      x[i] = ld_once(from + (u < turned ? u : 2 * F / kN + u - turned));
+      if (!kInterleaved && u < turned) y[i] = ld_once(from + u + turned);
+    }
+  };
+  auto load_v = [&](int j0) {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      if (j0 + i * stride < pieces) w[i] = ld_once(v + j0 + i * stride);
+  };
+  const int j0 = part * 32 + lane;
+  load(j0);
+  load_v(j0);
 
   // the token's sequence and place
-  int b, after, bad = 0;
+  int b, after;
   bool claimed = true;
+  const int given = a.positions ? a.positions[row] : 0;
   if (a.starts) {
-    int lo = 0, hi = a.B;  // the last b with starts[b] <= row
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (a.starts[mid] <= row) lo = mid;
-      else hi = mid;
+    // the last b with starts[b] <= row, 32 entries at a time
+    int lo = 0, n = a.B;
+    while (n > 1) {
+      const int step = (n + 31) >> 5, i = lo + lane * step;
+      const uint32_t below = __ballot_sync(0xffffffffu, lane * step < n && (lane == 0 || a.starts[i] <= row));
+      const int last = 31 - __clz(below);
+      lo += last * step;
+      n = min(step, n - last * step);
     }
     b = lo;
-    after = a.starts[b + 1] - row;
-    claimed = a.starts[b] <= row && after > 0 && a.starts[b + 1] <= a.T;
+    const int from = a.starts[b], to = a.starts[b + 1];
+    after = to - row;
+    claimed = from <= row && after > 0 && to <= a.T;
   } else {
     const int per = a.T / a.B;
     b = row / per;
     after = per - (row - b * per);
   }
-  long long off = -1;
-  int at = 0;
-  if (claimed) {
-    const long long place = static_cast<long long>(a.lengths[b]) - after;
-    at = static_cast<int>(place);
-    if (place < 0 || place >= static_cast<long long>(a.table.max_pages) * a.cache.page_size) {
-      bad = kDataLengthRange;
-    } else {
-      const int slot = at / a.cache.page_size;
-      const int page = a.table.ids[b * a.table.stride + slot];
-      if (page < 0 || page >= a.cache.pages) bad = kDataPageRange;
-      else off = page * a.cache.page_stride + (at - slot * a.cache.page_size) * a.cache.token_stride;
-    }
-  } else {
-    bad = kDataLengthRange;
-  }
-  if (part == 0 && lane == 0) report(a.status, bad);
-  const char* q = a.q + row * a.q_stride;
+  const long long place = claimed ? static_cast<long long>(a.lengths[b]) - after : -1;
+  const bool in = place >= 0 && place < static_cast<long long>(a.table.max_pages) * a.cache.page_size;
+  const int at = static_cast<int>(place), slot = in ? at / a.cache.page_size : 0;
+  const int page = in ? a.table.ids[b * a.table.stride + slot] : -1;  // on its way while the angles are turned
+  const long long position = a.positions ? given : at;
+  for (int i = lane; i < F; i += 32)
+    s_turn[warp][i % kPairs * turned + i / kPairs] =
+        cos_sin(static_cast<uint32_t>((static_cast<unsigned long long>(position) * turns_of(a.inv_freq[i])) >> 32));
+  __syncwarp();
+  const bool kept = page >= 0 && page < a.cache.pages;
+  if (part == 0 && lane == 0 && !kept) report(a.status, in ? kDataPageRange : kDataLengthRange);
+  const long long off = kept ? page * a.cache.page_stride + (at - slot * a.cache.page_size) * a.cache.token_stride : -1;
   char* q_out = a.q_out + row * a.q_out_stride;
   if (!claimed) {
     if (a.q_out != a.q)
-      for (int j = part * 32 + lane; j < a.q_heads * (D / kN); j += parts * 32)
-        reinterpret_cast<uint4*>(q_out)[j] = make_uint4(0, 0, 0, 0);
+      for (int j = j0; j < a.q_heads * (D / kN); j += stride) reinterpret_cast<uint4*>(q_out)[j] = make_uint4(0, 0, 0, 0);
     return;
   }
 
-  const long long position = a.positions ? a.positions[row] : at;
-  for (int i = lane; i < F; i += 32)
-    s_turn[warp][i] = cos_sin(static_cast<uint32_t>((static_cast<unsigned long long>(position) * turns_of(a.inv_freq[i])) >> 32));
-  __syncwarp();
-
-  const int turned = kInterleaved ? 2 * F / kN : F / kN, per_head = turned + (D - 2 * F) / kN;
-  const int rotated = (a.q_heads + (off >= 0 ? H : 0)) * per_head, units = rotated + (off >= 0 ? H * (D / kN) : 0);
-  for (int j = part * 32 + lane; j < units; j += parts * 32) {
-    if (j >= rotated) {
-      const int e = j - rotated;
-      reinterpret_cast<uint4*>(a.cache.v + off)[e] = ld_stream_v4(reinterpret_cast<const uint4*>(a.v_new + row * a.new_stride) + e);
-      continue;
-    }
-    const int head = static_cast<int>(by_unit(static_cast<unsigned long long>(j))), u = j - head * per_head;
-    const bool is_q = head < a.q_heads;
-    const long long in = static_cast<long long>(is_q ? head : head - a.q_heads) * D * E::kBytes;
-    const uint4* from = reinterpret_cast<const uint4*>((is_q ? q : a.k_new + row * a.new_stride) + in);
-    uint4* to = reinterpret_cast<uint4*>((is_q ? q_out : a.cache.k + off) + in);
-    if (u >= turned) {
-      const int e = 2 * F / kN + u - turned;
-      to[e] = from[e];
-    } else if constexpr (kInterleaved) {
-      float x[kN];
-      Piece<E>::unpack(from[u], x);
+  if (off >= 0)
+    for (int j = j0; j < pieces;) {
 #pragma unroll
-      for (int i = 0; i < kN; i += 2) {
-        const float2 t = s_turn[warp][(u * kN + i) / 2];
-        const float p = x[i], r = x[i + 1];
-        x[i] = p * t.x - r * t.y;
-        x[i + 1] = r * t.x + p * t.y;
-      }
-      to[u] = Piece<E>::pack(x);
-    } else {
-      float x[kN], y[kN];
-      Piece<E>::unpack(from[u], x);
-      Piece<E>::unpack(from[u + turned], y);
-#pragma unroll
-      for (int i = 0; i < kN; ++i) {
-        const float2 t = s_turn[warp][u * kN + i];
-        const float p = x[i], r = y[i];
-        x[i] = p * t.x - r * t.y;
-        y[i] = r * t.x + p * t.y;
-      }
-      to[u] = Piece<E>::pack(x);
-      to[u + turned] = Piece<E>::pack(y);
+      for (int i = 0; i < kBatch; ++i)
+        if (j + i * stride < pieces) reinterpret_cast<uint4*>(a.cache.v + off)[j + i * stride] = w[i];
+      j += kBatch * stride;
+      load_v(j);
     }
+  float2 t[kPairs];  // of unit `have`: mostly all of a lane's
+  int have = -1;
+  for (int j1 = j0; j1 < units;) {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int j = j1 + i * stride;
+      if (j >= units) break;
+      int u;
+      const long long in = unit_at(j, u);
+      if (j >= q_units && off < 0) continue;
+      uint4* to = reinterpret_cast<uint4*>((j < q_units ? q_out : a.cache.k + off) + in);
+      if (u >= turned) {
+        to[2 * F / kN + u - turned] = x[i];
+        continue;
+      }
+      if (u != have) {
+        have = u;
+#pragma unroll
+        for (int e = 0; e < kPairs; ++e) t[e] = s_turn[warp][e * turned + u];
+      }
+      float f[kN];
+      Piece<E>::unpack(x[i], f);
+      if constexpr (kInterleaved) {
+#pragma unroll
+        for (int e = 0; e < kN; e += 2) {
+          const float p = f[e], r = f[e + 1];
+          f[e] = p * t[e / 2].x - r * t[e / 2].y;
+          f[e + 1] = r * t[e / 2].x + p * t[e / 2].y;
+        }
+        to[u] = Piece<E>::pack(f);
+      } else {
+        float g[kN];
+        Piece<E>::unpack(y[i], g);
+#pragma unroll
+        for (int e = 0; e < kN; ++e) {
+          const float p = f[e], r = g[e];
+          f[e] = p * t[e].x - r * t[e].y;
+          g[e] = r * t[e].x + p * t[e].y;
+        }
+        to[u] = Piece<E>::pack(f);
+        to[u + turned] = Piece<E>::pack(g);
+      }
+    }
+    j1 += kBatch * stride;
+    load(j1);
   }
 }
 
@@ -342,7 +397,8 @@ cudaError_t launch_rotated_append(const RotatedAppendArgs& a, int sm_count, cuda
   if (parts > (units + 31) / 32) parts = (units + 31) / 32;
   if (parts < 1) parts = 1;
   const long long blocks = (a.T * parts + kAppendWarps - 1) / kAppendWarps;
-  const DivU64 by_part = DivU64::make(parts), by_unit = DivU64::make(per_head);
+  const DivU64 by_part = DivU64::make(parts);
+  const Div32 by_unit = Div32::make(per_head);
   auto go = [&](auto kernel) {
     kernel<<<static_cast<unsigned>(blocks), kAppendWarps * 32, 0, stream>>>(a, static_cast<int>(parts), by_part, by_unit);
   };
