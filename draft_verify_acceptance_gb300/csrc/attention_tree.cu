@@ -12,7 +12,7 @@ namespace specv {
 
 // bf16 items of more than 24 rows a cache head (R = N * Hq / Hkv) go to
 // attention_tree_tc.cuh, the rest to attention_mma.cuh, in tiles of at most 24 rows
-// that each read K and V again (through L2).
+// that each read K and V again (through L2), and scales that are not above zero.
 namespace {
 bool on_tc(int rows, bool bf16) { return bf16 && rows > mma::kMmaRows; }
 }  // namespace
@@ -35,7 +35,7 @@ cudaError_t launch_tree_attention(const AttnArgs& a, int sm_count, cudaStream_t 
   const int R = a.Q * (a.Hq / a.cache.heads);
   // rows in tiles of equal size
   const int tiles = (R + mma::kMmaRows - 1) / mma::kMmaRows, rows = (R + tiles - 1) / tiles;
-  if (on_tc(R, a.cache.bf16)) return tree_tc_launch(a, R, sm_count, stream);
+  if (on_tc(R, a.cache.bf16) && a.scale_log2 > 0.f) return tree_tc_launch(a, R, sm_count, stream);
   if (a.cache.bf16) mma::launch_rows<BF16, true>(a, (rows + 7) / 8, sm_count, stream);
   else mma::launch_rows<F32, true>(a, (rows + 7) / 8, sm_count, stream);
   return cudaGetLastError();

@@ -111,8 +111,11 @@ struct Walker {
   const Shape& z;
   int lane, b, H, RT, n, tiles;
   bool whole;
-  __device__ __forceinline__ static int divide(long long x, int y) {  // (64 bits take this GPU 500 cycles)
-    return x >> 32 ? static_cast<int>(x / y) : static_cast<int>(static_cast<unsigned>(x) / static_cast<unsigned>(y));
+  // (64 bits take this GPU 500 cycles and much code)
+  __device__ __noinline__ static long long divide64(long long x, long long y) { return x / y; }
+  __device__ __forceinline__ static long long divide(long long x, long long y) {
+    if ((x | y) >> 32) return divide64(x, y);
+    return static_cast<unsigned>(x) / static_cast<unsigned>(y);
   }
   __device__ __forceinline__ void sequence() {
     n = attn_length(a, b);
@@ -146,7 +149,7 @@ struct Walker {
       if (w < end) sequence();
       return;
     }
-    per = (total >> 32 ? (total + gridDim.x - 1) / gridDim.x : (static_cast<unsigned>(total) + gridDim.x - 1) / gridDim.x);
+    per = divide(total + gridDim.x - 1, gridDim.x);
     if (per < kLeast + kEnd) per = kLeast + kEnd;
     w = per * blockIdx.x;
     end = min(total, w + per);
@@ -186,7 +189,7 @@ struct Walker {
         continue;
       }
       const long long in = w - base;
-      const int item = divide(in, size), off = static_cast<int>(in - static_cast<long long>(item) * size);
+      const int item = static_cast<int>(divide(in, size)), off = static_cast<int>(in - static_cast<long long>(item) * size);
       const int stop = whole ? 1 : static_cast<int>(min(static_cast<long long>(size), off + (end - w)));
       i.tile0 = whole ? 0 : max(off - kEnd, 0);  // an item's first kEnd steps are nobody's
       i.tile1 = whole ? tiles : min(stop - kEnd, tiles);
@@ -200,12 +203,9 @@ struct Walker {
       i.h = item - i.rt * H;
       i.row0 = i.rt * kRows;
       i.rows = min(kRows, z.R - i.row0);
-      i.end = i.whole() ? 0 : first + tiles - 1 >= end ? block_of(first + tiles - 1) : static_cast<int>(blockIdx.x);
+      i.end = i.whole() ? 0 : static_cast<int>(divide(first + tiles - 1, per));
       return;
     }
-  }
-  __device__ __forceinline__ int block_of(long long step) const {
-    return step >> 32 || per >> 31 ? static_cast<int>(step / per) : static_cast<int>(static_cast<unsigned>(step) / static_cast<unsigned>(per));
   }
 };
 
@@ -220,7 +220,7 @@ struct Shared {
   unsigned long long full[Lay<D, kDual>::kSlots], empty[Lay<D, kDual>::kSlots];
   unsigned long long s_full[2][2], p_full[2][2], pv_done[2][2], q_full, q_free, done[2];
   unsigned long long item_ready[kItems], item_free[kItems];
-  Item item[kItems];
+  Item item[kItems], none;
   uint2 valid[kAhead];  // tokens that exist, by tile
   TreeSight<128> sight[2];
   float m[2][128], l[2][128];
@@ -357,15 +357,17 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
     int polls = 1 << 16;
 #ifdef SPEC_DEBUG
     // (a test's way to a wait that ran out: a bit of the status word that it passes)
-    if (blockIdx.x == 0 && a.status && (*reinterpret_cast<volatile int32_t*>(a.status) >> 30) != 0) polls = 0;
-    else
+    if (blockIdx.x == 0 && a.status && (*reinterpret_cast<volatile int32_t*>(a.status) >> 30) != 0) {
+      *reinterpret_cast<volatile int*>(&sh.dead) = 1;
+      return;
+    }
 #endif
-    if (mbar_try_wait_sleep(bar, parity, 20000u)) return;
 #pragma unroll 1
-    while (--polls > 0 && !*reinterpret_cast<volatile int*>(&sh.dead))
-      if (mbar_try_wait_sleep(bar, parity, 20000u)) return;
-    *reinterpret_cast<volatile int*>(&sh.dead) = 1;
-    if (a.status) atomicOr(a.status, kWaitTimeout);
+    while (!mbar_try_wait_sleep(bar, parity, 20000u))
+      if (--polls == 0 || *reinterpret_cast<volatile int*>(&sh.dead)) {
+        *reinterpret_cast<volatile int*>(&sh.dead) = 1;
+        break;
+      }
   };
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -391,6 +393,7 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
     mbar_init(&sh.q_free, 1);
     for (int i = 0; i < kOdd; ++i) sh.odd[i] = 0;
     sh.dead = 0;
+    sh.none.any = 0;
     fence_barrier_init();
   }
   if (warp == kOutputs) tmem_alloc(&sh.tmem, kCols);
@@ -401,7 +404,7 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
 
   auto item = [&](int k) -> const Item& {
     wait(&sh.item_ready[k % kItems], (k / kItems) & 1);
-    return sh.item[k % kItems];
+    return *reinterpret_cast<volatile int*>(&sh.dead) ? sh.none : sh.item[k % kItems];  // (one that was not told has no end)
   };
 
   // Copies 32 rows of an item's queries; behind the last row come zeros.
@@ -429,69 +432,66 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
     const int S = a.cache.page_size, chunk = lane % kChunks, r0 = lane / kChunks;
     constexpr int kStep = 32 / kChunks, kPasses = 16 / kStep;
     const bool in_page = S % 16 == 0;  // tokens 16 g .. 16 g + 15 of a tile lie in one page
-    int items = -1, tile = 0, tile1 = 0, n = 0, head = 0;
-    bool more = true;  // there is a tile `tile`
-    const int32_t* ids = nullptr;
-    auto step = [&]() {
-      if (++tile < tile1) return;
-      const Item& at = item(++items);
-      more = at.any;
-      if (!more) return;
-      tile = at.tile0;
-      tile1 = at.tile1;
-      n = at.n;
-      head = at.h;
-      ids = a.table.ids + at.b * a.table.stride;
-    };
-    step();
-    if (more && warp >= 10) step();  // the second pair starts with the second tile
     // The pages of tokens lane and 32 + lane, looked up a tile of the warp's ahead:
     // the table's entries are on their way while the tiles before are copied.
     struct Pages {
       int page[2], place[2], head;  // place: token in the page, -1: past the end
       bool any;
-    };
-    auto look_up = [&](Pages& p) {
-      p.any = more;
+    } now = {}, next = {};
+    int items = -1, tile = 0, tile1 = 0, n = 0, head = 0;
+    int ahead = warp < 10 ? 1 : 2;  // tiles to go on by: the second pair starts with the second
+    bool more = true;
+    const int32_t* ids = nullptr;
+    auto look_up = [&]() {
+#pragma unroll 1
+      for (; more && ahead > 0; --ahead) {
+        if (++tile < tile1) continue;
+        const Item& at = item(++items);
+        more = at.any;
+        tile = at.tile0;
+        tile1 = at.tile1;
+        n = at.n;
+        head = at.h;
+        ids = a.table.ids + at.b * a.table.stride;
+      }
+      ahead = 2;
+      next.any = more;
       if (!more) return;
-      p.head = head;
+      next.head = head;
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         const int t = tile * kTile + y * 32 + lane;
         const int entry = static_cast<int>(z.by_page(static_cast<unsigned long long>(t)));
-        p.place[y] = t < n ? t - entry * S : -1;
-        p.page[y] = t < n ? __ldg(ids + entry) : -1;
+        next.place[y] = t < n ? t - entry * S : -1;
+        next.page[y] = t < n ? __ldg(ids + entry) : -1;
       }
-      step();
-      if (more) step();
     };
-    Pages now, next;
-    look_up(now);
-    look_up(next);
     const uint32_t ring = smem_addr(smem) + (chunk >> 3) * kHalf + r0 * 128;
     const char* pool = (is_v ? a.cache.v : a.cache.k) + chunk * 16 + r0 * a.cache.token_stride;
     const long long stride = kStep * a.cache.token_stride;
     int slot = warp - 8;
     uint32_t turn = 1;  // the parity of a slot that is free the first time
-    for (int tile_no = (warp - 8) >> 1; now.any; tile_no += 2) {
+#pragma unroll 1
+    for (int tile_no = ((warp - 8) >> 1) - 4; tile_no < 0 || now.any; tile_no += 2) {  // (two rounds fill `now` and `next`)
       uint32_t exist[2];
       long long off[2];
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         const bool ok = now.page[y] >= 0 && now.page[y] < a.cache.pages;
-        if (!ok && now.place[y] >= 0 && a.status) atomicOr(a.status, kDataPageRange);
+        if (!ok && now.place[y] >= 0 && tile_no >= 0 && a.status) atomicOr(a.status, kDataPageRange);
         exist[y] = __ballot_sync(0xffffffffu, ok);
         off[y] = ok ? now.page[y] * a.cache.page_stride + now.place[y] * a.cache.token_stride + now.head * (D * 2) : -1ll;
       }
-      if (!is_v && lane == 0) sh.valid[tile_no % kAhead] = make_uint2(exist[0], exist[1]);
       now = next;
-      look_up(next);
+      look_up();
+      if (tile_no < 0) continue;
+      if (!is_v && lane == 0) sh.valid[tile_no % kAhead] = make_uint2(exist[0], exist[1]);
       wait(&sh.empty[slot], turn & 1);
       const uint32_t dst = ring + slot * L::kSlot;
       if (in_page && (exist[0] & exist[1]) == 0xffffffffu) {
-#pragma unroll
+#pragma unroll 1
         for (int g = 0; g < 4; ++g) {
-          const char* from = pool + __shfl_sync(0xffffffffu, off[g >> 1], (g & 1) * 16);
+          const char* from = pool + __shfl_sync(0xffffffffu, g < 2 ? off[0] : off[1], (g & 1) * 16);
 #pragma unroll
           for (int i = 0; i < kPasses; ++i, from += stride)
             cp16(dst + (g * 16 + i * kStep) * 128 + (((chunk & 7) ^ ((r0 + i * kStep) & 7)) << 4), from, 16);
@@ -609,8 +609,7 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
     const int row_at = kDual ? s * 128 : 0;  // the stream's first row of an item
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t s_col = tmem + lanes + s * kStream, o_col = s_col + kO;
-    const float scale = fabsf(a.scale_log2) > 0.f ? fabsf(a.scale_log2) : 1.f;
-    const bool turned = !(a.scale_log2 > 0.f), flat = a.scale_log2 == 0.f;  // scores change their sign; are all zero
+    const float scale = a.scale_log2;  // above zero
     TreeSight<128>& sight = sh.sight[s];
     if (warp < L::kRows / 32) {  // the first item's queries
       const Item& at = item(0);
@@ -667,11 +666,7 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
         }
         uint32_t x[64];
         ld64(x, at_s);
-        if (masked || turned) {
-          if (turned) {
-#pragma unroll
-            for (int i = 0; i < 64; ++i) x[i] = flat ? 0u : x[i] ^ 0x80000000u;
-          }
+        if (masked) {
           const uint32_t see[2] = {valid.x & sight.window(row_in, t0 - base), valid.y & sight.window(row_in, t0 + 32 - base)};
 #pragma unroll
           for (int i = 0; i < 64; ++i)
@@ -864,52 +859,53 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
   __syncthreads();
   if (warp == kOutputs) {
     tc_after();
+    if (lane == 0 && sh.dead && a.status) atomicOr(a.status, kWaitTimeout);
     tmem_free(tmem, kCols);
   }
 }
 
 // Blocks [block, end] of the launch have left (m, l, O) of a cut item.  A warp joins
-// 16 dimensions of 32 rows, a row a lane, in block order, four parts' loads under
-// way together.
-constexpr int kJoinWarps = 4;
+// 8 dimensions of 32 rows, a row a lane, in block order, two parts' loads under way
+// together.  (Little code: more parts at a time took longer, to fetch it.)
+constexpr int kJoinWarps = 4, kJoinDims = 8;
 template <int D, bool kDual>
 __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const AttnArgs a, const Shape z, const Join* joins) {
-  constexpr int kRows = Lay<D, kDual>::kRows, kSplit = D / 16 / kJoinWarps;  // blocks that share 32 rows
+  constexpr int kRows = Lay<D, kDual>::kRows, kSplit = D / kJoinDims / kJoinWarps;  // blocks that share 32 rows
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Join j = joins[blockIdx.x];
   const int first = blockIdx.x, lane = threadIdx.x & 31;
-  const int r0 = blockIdx.y / kSplit * 32, d0 = (blockIdx.y % kSplit * kJoinWarps + (threadIdx.x >> 5)) * 16;
+  const int r0 = blockIdx.y / kSplit * 32, d0 = (blockIdx.y % kSplit * kJoinWarps + (threadIdx.x >> 5)) * kJoinDims;
   if (r0 >= j.rows) return;
   const int r = min(r0 + lane, j.rows - 1);
-  auto slot = [&](int c) { return attn_slot<kRows, D>(a, c, c == first) + 4 * r; };  // row r's first four values
-  float m = -INFINITY, l = 0.f, o[16];
+  float m = -INFINITY, l = 0.f, o[8];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) o[i] = 0.f;
-  for (int c0 = first; c0 <= j.end; c0 += 4) {
-    float mc[4], lc[4];
-    float4 v[4][4];
+  for (int i = 0; i < 8; ++i) o[i] = 0.f;
+#pragma unroll 1
+  for (int c0 = first; c0 <= j.end; c0 += 2) {
+    float mc[2], lc[2];
+    float4 v[2][2];
 #pragma unroll
-    for (int y = 0; y < 4; ++y) {
-      const bool part = c0 + y <= j.end;
-      const float* s = slot(min(c0 + y, j.end));
-      mc[y] = part ? s[kRows * D - 3 * r] : -INFINITY;
-      lc[y] = part ? s[kRows * D + kRows - 3 * r] : 0.f;
+    for (int y = 0; y < 2; ++y) {
+      const int c = min(c0 + y, j.end);
+      const float* s = attn_slot<kRows, D>(a, c, c == first);
+      mc[y] = s[kRows * D + r];
+      lc[y] = s[kRows * D + kRows + r];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        v[y][i] = part ? *reinterpret_cast<const float4*>(s + (d0 / 4 + i) * (kRows * 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int i = 0; i < 2; ++i) v[y][i] = *reinterpret_cast<const float4*>(s + ((d0 / 4 + i) * kRows + r) * 4);
     }
     const float before = m;
-    m = fmaxf(fmaxf(m, fmaxf(mc[0], mc[1])), fmaxf(mc[2], mc[3]));
+    m = fmaxf(m, fmaxf(mc[0], mc[1]));
     const float keep = before == -INFINITY ? 1.f : ex2(before - m);
     l *= keep;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) o[i] *= keep;
+    for (int i = 0; i < 8; ++i) o[i] *= keep;
 #pragma unroll
-    for (int y = 0; y < 4; ++y) {
+    for (int y = 0; y < 2; ++y) {
+      if (c0 + y > j.end) break;
       const float w = mc[y] == -INFINITY ? 1.f : ex2(mc[y] - m);  // a part without a maximum holds zeros, or NaN that it passes on
       l = fmaf(w, lc[y], l);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 2; ++i) {
         o[4 * i] = fmaf(w, v[y][i].x, o[4 * i]);
         o[4 * i + 1] = fmaf(w, v[y][i].y, o[4 * i + 1]);
         o[4 * i + 2] = fmaf(w, v[y][i].z, o[4 * i + 2]);
@@ -921,12 +917,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const AttnAr
   const AttnRow ar = row_of(z, j.row0 + r, j.h);
   const size_t at = (static_cast<size_t>(j.b) * a.Q + ar.i) * a.Hq + ar.hq;
   const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-  uint32_t u[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) u[i] = pack2(o[2 * i] * inv, o[2 * i + 1] * inv);
-  uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at * D + d0);
-  out[0] = make_uint4(u[0], u[1], u[2], u[3]);
-  out[1] = make_uint4(u[4], u[5], u[6], u[7]);
+  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at * D + d0) =
+      make_uint4(pack2(o[0] * inv, o[1] * inv), pack2(o[2] * inv, o[3] * inv), pack2(o[4] * inv, o[5] * inv), pack2(o[6] * inv, o[7] * inv));
   if (d0 == 0 && a.lse) a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
@@ -957,7 +949,7 @@ cudaError_t launch(const AttnArgs& a, int sm_count, cudaStream_t stream) {
       static_cast<int64_t>(a.B) * a.cache.heads * z.RT <= grid)
     return cudaGetLastError();
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, ((z.R < L::kRows ? z.R : L::kRows) + 31) / 32 * (D / 16 / kJoinWarps));
+  cfg.gridDim = dim3(grid, ((z.R < L::kRows ? z.R : L::kRows) + 31) / 32 * (D / kJoinDims / kJoinWarps));
   cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.stream = stream;
   cudaLaunchAttribute after[1];
