@@ -62,7 +62,11 @@ constexpr int kWalker = kOutputs + 1, kQueries = kWalker + 1;     // the one tha
 constexpr float kSlackR = 8.f;   // how far (log2) a score may pass the reference
 template <bool kDual>
 constexpr int kEndR = kDual ? 5 : 8;  // steps that an item's start and end count as
-constexpr int kLeast = 4;        // tiles that a block gets at least, when there are more blocks than work
+// Steps that a block gets at least, when there are more blocks than work: one tree of
+// 60 nodes over 2111 tokens, two streams, 4: 24.9 us, 3 and 6: 26.7, 9: 28.8;  one of
+// 30 over 4000, 4: 27.0, 6: 24.7, 9: 23.6;  over 700, 4: 18.5, 6 and 9: 20.5.
+template <bool kDual>
+constexpr int kLeast = kDual ? 4 : 6;
 constexpr int kMaxCtas = 160;
 constexpr int kAhead = 32;       // tiles whose valid bits are kept, more than the ring holds
 constexpr int kOdd = 8;          // items whose flag is kept, more than a stream can be behind
@@ -104,7 +108,7 @@ __device__ __forceinline__ AttnRow row_of(const Shape& z, int row, int h) {
 // an item's tiles and kEnd steps more are numbered item by item, sequence by
 // sequence, and block c takes steps [c * per, (c + 1) * per).  With a block for every
 // item and none of more than kWholeTiles tiles, nothing is cut.
-template <int kRows, int kEnd>
+template <int kRows, int kEnd, int kLeast>
 struct Walker {
   const AttnArgs& a;
   long long w, end, per, base;  // step, last step and number of steps of the block; first step of sequence b
@@ -150,7 +154,7 @@ struct Walker {
       return;
     }
     per = divide(total + gridDim.x - 1, gridDim.x);
-    if (per < kLeast + kEnd) per = kLeast + kEnd;
+    if (per < kLeast) per = kLeast;
     w = per * blockIdx.x;
     end = min(total, w + per);
     // the sequence that has step w, 32 sequences at a time
@@ -340,6 +344,17 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 
 __device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 __device__ __forceinline__ void stream_sync(int s) { asm volatile("bar.sync %0, 128;" ::"r"(3 + s) : "memory"); }
+
+// Is x true in one of `count` threads of barrier `id`.
+__device__ __forceinline__ bool any_of(int id, int count, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(x ? 1u : 0u), "r"(id), "r"(count)
+      : "memory");
+  return r != 0;
+}
 
 template <int D, bool kDual>
 __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const AttnArgs a, const Shape z, Join* joins) {
@@ -578,11 +593,12 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
     __syncwarp();
   } else if (warp == kWalker) {
     // ---- items -------------------------------------------------------------------
-    Walker<L::kRows, kEndR<kDual>> at(a, z, lane);
+    Walker<L::kRows, kEndR<kDual>, kLeast<kDual>> at(a, z, lane);
     for (int items = 0;; ++items) {
       Item i;
       at.next(i);
       wait(&sh.item_free[items % kItems], (items / kItems + 1) & 1);  // (the first ones are)
+      if (*reinterpret_cast<volatile int*>(&sh.dead)) break;             // (an item that is read stays)
       if (lane == 0) {
         sh.item[items % kItems] = i;
         mbar_arrive(&sh.item_ready[items % kItems]);
@@ -618,7 +634,8 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
     int count = 0, tile_no = 0, sight_b = -1, sight_rt = -1;
     for (int items = 0;; ++items) {
       const Item& at = item(items);
-      if (!at.any) break;
+      // (those that meet at barriers below stop together, also where a wait ran out)
+      if (kDual ? any_of(3 + s, 128, !at.any) : any_of(1, 256, !at.any)) break;
       const int base = at.n - a.Q;
       if (at.b != sight_b || at.rt != sight_rt) {
         stream_sync(s);
@@ -854,6 +871,7 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
       stream_sync(s);  // (the last to read the item)
       if (row_in == 0) mbar_arrive(&sh.item_free[items % kItems]);
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
   }
   tc_before();
   __syncthreads();

@@ -576,7 +576,20 @@ PyObject* call_accept(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* 
   if (tree_accept(tokens, parents, parents_stride, drawn, B, N, len.data_ptr<int>(), out.data_ptr<int>(), path.data_ptr<int>(),
                   reinterpret_cast<spec_stream_t>(w.stream), nullptr) != SPEC_OK)
     return not_done();
-  return result(accept_result, {&len, &out, &path, nullptr});
+  // (the result type is a tuple without more, and made as one: its own constructor runs Python)
+  PyTypeObject* type = reinterpret_cast<PyTypeObject*>(accept_result);
+  PyObject* result = type->tp_alloc(type, 4);
+  if (!result) return nullptr;
+  const at::Tensor* items[] = {&len, &out, &path};
+  for (int i = 0; i < 4; ++i) {
+    PyObject* item = i < 3 ? THPVariable_Wrap(*items[i]) : Py_NewRef(Py_None);
+    if (!item) {
+      Py_DECREF(result);
+      return nullptr;
+    }
+    PyTuple_SET_ITEM(result, i, item);
+  }
+  return result;
 }
 
 PyObject* call_keep(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kwnames) {

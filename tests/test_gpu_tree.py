@@ -123,6 +123,22 @@ def test_attention(tree, dtype, B, N, Hq, H, D, S, lens):
     assert torch.equal(again, out) and torch.equal(lse2, lse)
 
 
+@pytest.mark.parametrize("B,N,Hq,H,D", [(400, 7, 32, 8, 64), (350, 40, 16, 4, 64), (330, 9, 20, 5, 128)])
+def test_attention_of_many_short_sequences(tree, B, N, Hq, H, D):
+    """Blocks that take ten and more items each, of one tile or two, whole and cut, empty sequences among them."""
+    r = np.random.RandomState(B)
+    lens = [int(n) for n in r.randint(0, N + 70, B)]
+    k, v, table, lengths = make_cache(lens, 16, H, D, torch.bfloat16, seed=B)
+    q = (torch.randn((B, N, Hq, D), generator=gen(5), device="cuda") * 2).to(torch.bfloat16)
+    parents = i32(make_trees(B, N, N).tolist())
+    out, lse, status = tree.tree_attention(q, k, v, table, lengths, parents, return_lse=True, debug=True)
+    assert int(status) == 0
+    part = slice(B % 7, None, 11)
+    check_attention(out[part], lse[part], q[part], k, v, table[part], lengths[part], parents[part])
+    for _ in range(3):
+        assert torch.equal(tree.tree_attention(q, k, v, table, lengths, parents), out)
+
+
 @pytest.mark.parametrize("dtype", BOTH)
 @pytest.mark.parametrize("N,G,D", [(3, 4, 128), (13, 4, 64), (16, 8, 128), (30, 4, 128), (60, 4, 128), (33, 3, 64)])
 def test_a_chain_is_paged_attention(tree, dtype, N, G, D):
