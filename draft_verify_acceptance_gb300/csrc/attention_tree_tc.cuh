@@ -23,6 +23,18 @@
 // Parts of an item that blocks' ranges cut are left in the workspace and joined by
 // a dependent kernel over all SMs, in block order (one block would have to read
 // up to 133 KB a part).
+//
+// The code is kept short: with loops unrolled to 200 KB the roles evicted each
+// other from the instruction caches, and a tile took 4000 cycles.
+//
+// 32 query heads of 128 on 8:  64 sequences of 400..4000 tokens, 16 nodes (64 rows a
+// head) 114 us (the cache's bytes at the copy rate: 87; a block's tile 1300 cycles,
+// what HBM gives an SM 1430 for it when all take their share; an item's start and end
+// 5 us of a block's time, a third hidden behind the ring);  2 of 60001..131072,
+// 26 nodes: 156 us (134);  32 of 400..4000, 64 nodes (256 rows): 111 us (45), a tile 2300 cycles
+// of products, the scores' as long as the outputs' since each reads 4 KB of queries
+// for 64 tokens;  one of 2111, 60 nodes: 25 us, start, part and join.  32 of 400..4000
+// over heads of 64, 30 nodes: 55 us (23), by the softmax's latency.
 #pragma once
 
 #include "attention_common.cuh"
@@ -60,8 +72,10 @@ static_assert(kSoft * kSoftRegs + (kThreadsR - kSoft) * kOtherRegs <= 65536 && k
 constexpr int kScores = 8 + kLoadWarps, kOutputs = kScores + 1;   // the warps that issue products,
 constexpr int kWalker = kOutputs + 1, kQueries = kWalker + 1;     // the one that finds the block's items, the one that copies queries
 constexpr float kSlackR = 8.f;   // how far (log2) a score may pass the reference
+// Steps that an item's start and end count as: by the blocks' times, 6.6 us against
+// 1.27 a tile with two row tiles, 5.1 against 0.70 with one.
 template <bool kDual>
-constexpr int kEndR = kDual ? 5 : 8;  // steps that an item's start and end count as
+constexpr int kEndR = kDual ? 5 : 8;
 // Steps that a block gets at least, when there are more blocks than work: one tree of
 // 60 nodes over 2111 tokens, two streams, 4: 24.9 us, 3 and 6: 26.7, 9: 28.8;  one of
 // 30 over 4000, 4: 27.0, 6: 24.7, 9: 23.6;  over 700, 4: 18.5, 6 and 9: 20.5.
@@ -78,7 +92,7 @@ struct Lay {
   static constexpr int kHalf = kTile * 128;        // 64 dimensions of it
   static constexpr int kQ = kRows * D * 2;
   static constexpr int kSlots = (227 * 1024 - 17 * 1024 - kQ) / kSlot;
-  static constexpr int kBytes = kSlots * kSlot + kQ + 1024;  // 1024: alignment
+  static constexpr int kBytes = kSlots * kSlot + kQ + 1024;  // 1024: alignment (some 15 KB more are static)
   static_assert(kSlots >= 8 && kSlots / 2 + 4 < kAhead, "the ring");
 };
 
@@ -438,186 +452,186 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-  if (warp < kScores) {
-    // ---- K and V of each tile, in turn -----------------------------------
-    // A warp takes K or V of every other tile, so that it looks its 64 tokens up
-    // and waits once for 32 copies (with 16 tokens of every K and V a warp these
-    // took more of its time than the copies).
-    const bool is_v = warp & 1;
-    const int S = a.cache.page_size, chunk = lane % kChunks, r0 = lane / kChunks;
-    constexpr int kStep = 32 / kChunks, kPasses = 16 / kStep;
-    const bool in_page = S % 16 == 0;  // tokens 16 g .. 16 g + 15 of a tile lie in one page
-    // The pages of tokens lane and 32 + lane, looked up a tile of the warp's ahead:
-    // the table's entries are on their way while the tiles before are copied.
-    struct Pages {
-      int page[2], place[2], head;  // place: token in the page, -1: past the end
-      bool any;
-    } now = {}, next = {};
-    int items = -1, tile = 0, tile1 = 0, n = 0, head = 0;
-    int ahead = warp < 10 ? 1 : 2;  // tiles to go on by: the second pair starts with the second
-    bool more = true;
-    const int32_t* ids = nullptr;
-    auto look_up = [&]() {
+    if (warp < kScores) {
+      // ---- K and V of each tile, in turn -----------------------------------
+      // A warp takes K or V of every other tile, so that it looks its 64 tokens up
+      // and waits once for 32 copies (with 16 tokens of every K and V a warp these
+      // took more of its time than the copies).
+      const bool is_v = warp & 1;
+      const int S = a.cache.page_size, chunk = lane % kChunks, r0 = lane / kChunks;
+      constexpr int kStep = 32 / kChunks, kPasses = 16 / kStep;
+      const bool in_page = S % 16 == 0;  // tokens 16 g .. 16 g + 15 of a tile lie in one page
+      // The pages of tokens lane and 32 + lane, looked up a tile of the warp's ahead:
+      // the table's entries are on their way while the tiles before are copied.
+      struct Pages {
+        int page[2], place[2], head;  // place: token in the page, -1: past the end
+        bool any;
+      } now = {}, next = {};
+      int items = -1, tile = 0, tile1 = 0, n = 0, head = 0;
+      int ahead = warp < 10 ? 1 : 2;  // tiles to go on by: the second pair starts with the second
+      bool more = true;
+      const int32_t* ids = nullptr;
+      auto look_up = [&]() {
 #pragma unroll 1
-      for (; more && ahead > 0; --ahead) {
-        if (++tile < tile1) continue;
-        const Item& at = item(++items);
-        more = at.any;
-        tile = at.tile0;
-        tile1 = at.tile1;
-        n = at.n;
-        head = at.h;
-        ids = a.table.ids + at.b * a.table.stride;
-      }
-      ahead = 2;
-      next.any = more;
-      if (!more) return;
-      next.head = head;
-#pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        const int t = tile * kTile + y * 32 + lane;
-        const int entry = static_cast<int>(z.by_page(static_cast<unsigned long long>(t)));
-        next.place[y] = t < n ? t - entry * S : -1;
-        next.page[y] = t < n ? __ldg(ids + entry) : -1;
-      }
-    };
-    const uint32_t ring = smem_addr(smem) + (chunk >> 3) * kHalf + r0 * 128;
-    const char* pool = (is_v ? a.cache.v : a.cache.k) + chunk * 16 + r0 * a.cache.token_stride;
-    const long long stride = kStep * a.cache.token_stride;
-    int slot = warp - 8;
-    uint32_t turn = 1;  // the parity of a slot that is free the first time
-#pragma unroll 1
-    for (int tile_no = ((warp - 8) >> 1) - 4; tile_no < 0 || now.any; tile_no += 2) {  // (two rounds fill `now` and `next`)
-      uint32_t exist[2];
-      long long off[2];
-#pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        const bool ok = now.page[y] >= 0 && now.page[y] < a.cache.pages;
-        if (!ok && now.place[y] >= 0 && tile_no >= 0 && a.status) atomicOr(a.status, kDataPageRange);
-        exist[y] = __ballot_sync(0xffffffffu, ok);
-        off[y] = ok ? now.page[y] * a.cache.page_stride + now.place[y] * a.cache.token_stride + now.head * (D * 2) : -1ll;
-      }
-      now = next;
-      look_up();
-      if (tile_no < 0) continue;
-      if (!is_v && lane == 0) sh.valid[tile_no % kAhead] = make_uint2(exist[0], exist[1]);
-      wait(&sh.empty[slot], turn & 1);
-      const uint32_t dst = ring + slot * L::kSlot;
-      if (in_page && (exist[0] & exist[1]) == 0xffffffffu) {
-#pragma unroll 1
-        for (int g = 0; g < 4; ++g) {
-          const char* from = pool + __shfl_sync(0xffffffffu, g < 2 ? off[0] : off[1], (g & 1) * 16);
-#pragma unroll
-          for (int i = 0; i < kPasses; ++i, from += stride)
-            cp16(dst + (g * 16 + i * kStep) * 128 + (((chunk & 7) ^ ((r0 + i * kStep) & 7)) << 4), from, 16);
+        for (; more && ahead > 0; --ahead) {
+          if (++tile < tile1) continue;
+          const Item& at = item(++items);
+          more = at.any;
+          tile = at.tile0;
+          tile1 = at.tile1;
+          n = at.n;
+          head = at.h;
+          ids = a.table.ids + at.b * a.table.stride;
         }
-      } else {
-#pragma unroll 1
-        for (int i = 0; i < 4 * kPasses; ++i) {
-          const int t = r0 + i * kStep;
-          const long long from = __shfl_sync(0xffffffffu, i < 2 * kPasses ? off[0] : off[1], t & 31) - r0 * a.cache.token_stride;
-          const bool some = ((i < 2 * kPasses ? exist[0] : exist[1]) >> (t & 31)) & 1;
-          cp16(dst + i * kStep * 128 + (((chunk & 7) ^ (t & 7)) << 4), some ? pool + from : a.cache.k, some ? 16 : 0);  // 0: zero-filled
+        ahead = 2;
+        next.any = more;
+        if (!more) return;
+        next.head = head;
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const int t = tile * kTile + y * 32 + lane;
+          const int entry = static_cast<int>(z.by_page(static_cast<unsigned long long>(t)));
+          next.place[y] = t < n ? t - entry * S : -1;
+          next.page[y] = t < n ? __ldg(ids + entry) : -1;
         }
-      }
-      cp_arrive(&sh.full[slot]);
-      if (lane == 0) mbar_arrive(&sh.full[slot]);  // (the tokens' bits come with it)
-      slot += 4;
-      if (slot >= kSlots) {
-        slot -= kSlots;
-        ++turn;
-      }
-    }
-    asm volatile("cp.async.wait_all;" ::: "memory");  // no copy is under way when the block leaves
-  } else if (warp == kScores) {
-    // ---- scores ----------------------------------------------------------------
-    const uint32_t ring = smem_addr(smem), q_at = smem_addr(q_s);
-    int count0 = 0, count1 = 0, tile_no = 0, items = 0;  // tiles of the streams, where they differ; of both
-    for (;; ++items) {
-      const Item& at = item(items);
-      if (!at.any) break;
-      const int tiles = at.tile1 - at.tile0;
-      for (int j = 0; j < tiles; ++j, ++tile_no) {
-        const int slot = (2 * tile_no) % kSlots;
-        if (j == 0) wait(&sh.q_full, items & 1);
-        wait(&sh.full[slot], ((2 * tile_no) / kSlots) & 1);
-        async_fence();  // the copies, to the products
+      };
+      const uint32_t ring = smem_addr(smem) + (chunk >> 3) * kHalf + r0 * 128;
+      const char* pool = (is_v ? a.cache.v : a.cache.k) + chunk * 16 + r0 * a.cache.token_stride;
+      const long long stride = kStep * a.cache.token_stride;
+      int slot = warp - 8;
+      uint32_t turn = 1;  // the parity of a slot that is free the first time
 #pragma unroll 1
-        for (int s = kDual ? 0 : j & 1; s < (kDual ? 2 : (j & 1) + 1); ++s) {
-          const int c = kDual ? tile_no : s ? count1++ : count0++, buf = c & 1;
-          wait(&sh.pv_done[s][buf], ((c >> 1) + 1) & 1);  // (the first of a buffer finds it free)
-          tc_after();
-          scores_mma<D>(tmem + s * kStream + buf * kTile, operand(q_at + (kDual ? s : 0) * (128 * D * 2), 16, 1024, 2),
-                        operand(ring + slot * L::kSlot, 16, 1024, 2));
-          if (!kDual || s == 1) {
-            tc_commit(&sh.empty[slot]);
-            if (j == tiles - 1) tc_commit(&sh.q_free);
+      for (int tile_no = ((warp - 8) >> 1) - 4; tile_no < 0 || now.any; tile_no += 2) {  // (two rounds fill `now` and `next`)
+        uint32_t exist[2];
+        long long off[2];
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const bool ok = now.page[y] >= 0 && now.page[y] < a.cache.pages;
+          if (!ok && now.place[y] >= 0 && tile_no >= 0 && a.status) atomicOr(a.status, kDataPageRange);
+          exist[y] = __ballot_sync(0xffffffffu, ok);
+          off[y] = ok ? now.page[y] * a.cache.page_stride + now.place[y] * a.cache.token_stride + now.head * (D * 2) : -1ll;
+        }
+        now = next;
+        look_up();
+        if (tile_no < 0) continue;
+        if (!is_v && lane == 0) sh.valid[tile_no % kAhead] = make_uint2(exist[0], exist[1]);
+        wait(&sh.empty[slot], turn & 1);
+        const uint32_t dst = ring + slot * L::kSlot;
+        if (in_page && (exist[0] & exist[1]) == 0xffffffffu) {
+#pragma unroll 1
+          for (int g = 0; g < 4; ++g) {
+            const char* from = pool + __shfl_sync(0xffffffffu, g < 2 ? off[0] : off[1], (g & 1) * 16);
+#pragma unroll
+            for (int i = 0; i < kPasses; ++i, from += stride)
+              cp16(dst + (g * 16 + i * kStep) * 128 + (((chunk & 7) ^ ((r0 + i * kStep) & 7)) << 4), from, 16);
           }
-          tc_commit(&sh.s_full[s][buf]);
-        }
-      }
-    }
-    if (*reinterpret_cast<volatile int*>(&sh.dead)) {  // none of them may be under way when TMEM is freed
-      tc_commit(&sh.done[0]);
-      mbar_wait_sleep(&sh.done[0], 0);
-    }
-    __syncwarp();
-  } else if (warp == kOutputs) {
-    // ---- outputs -----------------------------------------------------------------
-    const uint32_t ring = smem_addr(smem);
-    int count0 = 0, count1 = 0, tile_no = 0;
-    for (int items = 0;; ++items) {
-      const Item& at = item(items);
-      if (!at.any) break;
-      const int tiles = at.tile1 - at.tile0;
-      for (int j = 0; j < tiles; ++j, ++tile_no) {
-        const int slot = (2 * tile_no + 1) % kSlots;
-        wait(&sh.full[slot], ((2 * tile_no + 1) / kSlots) & 1);
+        } else {
 #pragma unroll 1
-        for (int s = kDual ? 0 : j & 1; s < (kDual ? 2 : (j & 1) + 1); ++s) {
-          const int c = kDual ? tile_no : s ? count1++ : count0++, buf = c & 1;
-          wait(&sh.p_full[s][buf], (c >> 1) & 1);
-          async_fence();
-          tc_after();
-          outputs_mma<D>(tmem + s * kStream + kO, tmem + s * kStream + buf * kTile, operand(ring + slot * L::kSlot, kHalf, 1024, 2),
-                         kDual ? j > 0 : j > 1);
-          if (!kDual || s == 1) tc_commit(&sh.empty[slot]);
-          tc_commit(&sh.pv_done[s][buf]);
+          for (int i = 0; i < 4 * kPasses; ++i) {
+            const int t = r0 + i * kStep;
+            const long long from = __shfl_sync(0xffffffffu, i < 2 * kPasses ? off[0] : off[1], t & 31) - r0 * a.cache.token_stride;
+            const bool some = ((i < 2 * kPasses ? exist[0] : exist[1]) >> (t & 31)) & 1;
+            cp16(dst + i * kStep * 128 + (((chunk & 7) ^ (t & 7)) << 4), some ? pool + from : a.cache.k, some ? 16 : 0);  // 0: zero-filled
+          }
+        }
+        cp_arrive(&sh.full[slot]);
+        if (lane == 0) mbar_arrive(&sh.full[slot]);  // (the tokens' bits come with it)
+        slot += 4;
+        if (slot >= kSlots) {
+          slot -= kSlots;
+          ++turn;
         }
       }
-    }
-    if (*reinterpret_cast<volatile int*>(&sh.dead)) {
-      tc_commit(&sh.done[1]);
-      mbar_wait_sleep(&sh.done[1], 0);
-    }
-    __syncwarp();
-  } else if (warp == kWalker) {
-    // ---- items -------------------------------------------------------------------
-    Walker<L::kRows, kEndR<kDual>, kLeast<kDual>> at(a, z, lane);
-    for (int items = 0;; ++items) {
-      Item i;
-      at.next(i);
-      wait(&sh.item_free[items % kItems], (items / kItems + 1) & 1);  // (the first ones are)
-      if (*reinterpret_cast<volatile int*>(&sh.dead)) break;             // (an item that is read stays)
-      if (lane == 0) {
-        sh.item[items % kItems] = i;
-        mbar_arrive(&sh.item_ready[items % kItems]);
+      asm volatile("cp.async.wait_all;" ::: "memory");  // no copy is under way when the block leaves
+    } else if (warp == kScores) {
+      // ---- scores ----------------------------------------------------------------
+      const uint32_t ring = smem_addr(smem), q_at = smem_addr(q_s);
+      int count0 = 0, count1 = 0, tile_no = 0, items = 0;  // tiles of the streams, where they differ; of both
+      for (;; ++items) {
+        const Item& at = item(items);
+        if (!at.any) break;
+        const int tiles = at.tile1 - at.tile0;
+        for (int j = 0; j < tiles; ++j, ++tile_no) {
+          const int slot = (2 * tile_no) % kSlots;
+          if (j == 0) wait(&sh.q_full, items & 1);
+          wait(&sh.full[slot], ((2 * tile_no) / kSlots) & 1);
+          async_fence();  // the copies, to the products
+#pragma unroll 1
+          for (int s = kDual ? 0 : j & 1; s < (kDual ? 2 : (j & 1) + 1); ++s) {
+            const int c = kDual ? tile_no : s ? count1++ : count0++, buf = c & 1;
+            wait(&sh.pv_done[s][buf], ((c >> 1) + 1) & 1);  // (the first of a buffer finds it free)
+            tc_after();
+            scores_mma<D>(tmem + s * kStream + buf * kTile, operand(q_at + (kDual ? s : 0) * (128 * D * 2), 16, 1024, 2),
+                          operand(ring + slot * L::kSlot, 16, 1024, 2));
+            if (!kDual || s == 1) {
+              tc_commit(&sh.empty[slot]);
+              if (j == tiles - 1) tc_commit(&sh.q_free);
+            }
+            tc_commit(&sh.s_full[s][buf]);
+          }
+        }
+      }
+      if (*reinterpret_cast<volatile int*>(&sh.dead)) {  // none of them may be under way when TMEM is freed
+        tc_commit(&sh.done[0]);
+        mbar_wait_sleep(&sh.done[0], 0);
       }
       __syncwarp();
-      if (!i.any) break;
-    }
-  } else {
-    // ---- queries, from the second item on --------------------------------------------
-    for (int items = 0;; ++items) {
-      const Item& at = item(items);
-      if (!at.any) break;
-      if (items == 0) continue;
-      wait(&sh.q_free, (items - 1) & 1);  // the scores of the item before are done
+    } else if (warp == kOutputs) {
+      // ---- outputs -----------------------------------------------------------------
+      const uint32_t ring = smem_addr(smem);
+      int count0 = 0, count1 = 0, tile_no = 0;
+      for (int items = 0;; ++items) {
+        const Item& at = item(items);
+        if (!at.any) break;
+        const int tiles = at.tile1 - at.tile0;
+        for (int j = 0; j < tiles; ++j, ++tile_no) {
+          const int slot = (2 * tile_no + 1) % kSlots;
+          wait(&sh.full[slot], ((2 * tile_no + 1) / kSlots) & 1);
 #pragma unroll 1
-      for (int y = 0; y < L::kRows / 32; ++y) load_q(at, y);
+          for (int s = kDual ? 0 : j & 1; s < (kDual ? 2 : (j & 1) + 1); ++s) {
+            const int c = kDual ? tile_no : s ? count1++ : count0++, buf = c & 1;
+            wait(&sh.p_full[s][buf], (c >> 1) & 1);
+            async_fence();
+            tc_after();
+            outputs_mma<D>(tmem + s * kStream + kO, tmem + s * kStream + buf * kTile, operand(ring + slot * L::kSlot, kHalf, 1024, 2),
+                           kDual ? j > 0 : j > 1);
+            if (!kDual || s == 1) tc_commit(&sh.empty[slot]);
+            tc_commit(&sh.pv_done[s][buf]);
+          }
+        }
+      }
+      if (*reinterpret_cast<volatile int*>(&sh.dead)) {
+        tc_commit(&sh.done[1]);
+        mbar_wait_sleep(&sh.done[1], 0);
+      }
+      __syncwarp();
+    } else if (warp == kWalker) {
+      // ---- items -------------------------------------------------------------------
+      Walker<L::kRows, kEndR<kDual>, kLeast<kDual>> at(a, z, lane);
+      for (int items = 0;; ++items) {
+        Item i;
+        at.next(i);
+        wait(&sh.item_free[items % kItems], (items / kItems + 1) & 1);  // (the first ones are)
+        if (*reinterpret_cast<volatile int*>(&sh.dead)) break;             // (an item that is read stays)
+        if (lane == 0) {
+          sh.item[items % kItems] = i;
+          mbar_arrive(&sh.item_ready[items % kItems]);
+        }
+        __syncwarp();
+        if (!i.any) break;
+      }
+    } else {
+      // ---- queries, from the second item on --------------------------------------------
+      for (int items = 0;; ++items) {
+        const Item& at = item(items);
+        if (!at.any) break;
+        if (items == 0) continue;
+        wait(&sh.q_free, (items - 1) & 1);  // the scores of the item before are done
+#pragma unroll 1
+        for (int y = 0; y < L::kRows / 32; ++y) load_q(at, y);
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
-  }
   } else {
     // ---- softmax: a row a thread --------------------------------------------------
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
