@@ -208,7 +208,9 @@ __global__ void __launch_bounds__(Ring<E, D, NB>::kWarps * 32, Ring<E, D, NB>::k
   const uint32_t mine_at = smem_addr(mine);
 
   constexpr int kEnd = L::kEnd;
-  const AttnPlan plan = attn_plan<kStepM, kEnd, kThreadsM>(a, H * RT, 4, s_plan);
+  AttnPlan plan;
+  if (kTree && a.whole) plan = attn_plan_whole<kEnd>(a, H * RT);
+  else plan = attn_plan<kStepM, kEnd, kThreadsM>(a, H * RT, 4, s_plan);
   AttnWalk<kStepM, kEnd, kRows> at(a, plan);
   while (at.next()) {
     const int n = at.n, b = at.b, h = at.h, row0 = at.row0, rows = at.rows, tile0 = at.tile0, tile1 = at.tile1;
@@ -635,6 +637,15 @@ cudaError_t prepare_all() {
   for (cudaError_t x : e)
     if (x != cudaSuccess) return x;
   return cudaSuccess;
+}
+// Is no item of nb blocks of rows cut, by the room of the page tables alone (attn_plan's rule).
+template <typename E, int D>
+bool whole(const AttnArgs& a, int nb, int sm_count) {
+  using L = Ring<E, D, 1>;  // (the same for all nb in what counts here)
+  const int grid = sm_count * L::kCtas < kMaxMmaCtas ? sm_count * L::kCtas : kMaxMmaCtas;
+  const int R = a.Q * (a.Hq / a.cache.heads), RT = (R + 8 * nb - 1) / (8 * nb);
+  return static_cast<int64_t>(a.table.max_pages) * a.cache.page_size <= kWholeTiles * L::kWarps * kTokens &&
+         static_cast<int64_t>(a.B) * a.cache.heads * RT <= grid;
 }
 // Items of nb blocks of 8 rows, 1 to 3.
 template <typename E, bool kTree = false>

@@ -41,8 +41,15 @@ cudaError_t launch_tree_attention(const AttnArgs& a, int sm_count, cudaStream_t 
   // rows in tiles of equal size
   const int tiles = (R + mma::kMmaRows - 1) / mma::kMmaRows, rows = (R + tiles - 1) / tiles;
   if (on_tc(R, a.cache.bf16) && a.scale_log2 > 0.f) return tree_tc_launch(a, R, sm_count, stream);
-  if (a.cache.bf16) mma::launch_rows<BF16, true>(a, (rows + 7) / 8, sm_count, stream);
-  else mma::launch_rows<F32, true>(a, (rows + 7) / 8, sm_count, stream);
+  AttnArgs b = a;
+  const int nb = (rows + 7) / 8;
+  if (a.cache.bf16) {
+    b.whole = a.cache.head_dim == 64 ? mma::whole<BF16, 64>(a, nb, sm_count) : mma::whole<BF16, 128>(a, nb, sm_count);
+    mma::launch_rows<BF16, true>(b, nb, sm_count, stream);
+  } else {
+    b.whole = a.cache.head_dim == 64 ? mma::whole<F32, 64>(a, nb, sm_count) : mma::whole<F32, 128>(a, nb, sm_count);
+    mma::launch_rows<F32, true>(b, nb, sm_count, stream);
+  }
   return cudaGetLastError();
 }
 

@@ -145,20 +145,25 @@ struct Walker {
     long long total = 0;
     int most = 0;
     bool bad = false;
+    const long long items = static_cast<long long>(a.B) * H * RT;
+    if (a.whole) {  // (the lengths' scan takes 2 us)
+      const int own = static_cast<int>(z.by_items(blockIdx.x));
+      if (own < a.B) bad = attn_length(a, own) != a.lengths[own];
+      if (bad && a.status && lane == 0) atomicOr(a.status, kDataLengthRange);
+    }
 #pragma unroll 1
-    for (int i = lane; i < a.B; i += 32) {
+    for (int i = a.whole ? a.B : lane; i < a.B; i += 32) {
       const int len = attn_length(a, i), t = attn_tiles<kTile>(len);
       bad |= len != a.lengths[i];
       most = max(most, t);
       total += t + kEnd;
     }
-    if (bad && a.status && blockIdx.x == 0) atomicOr(a.status, kDataLengthRange);
+    if (!a.whole && bad && a.status && blockIdx.x == 0) atomicOr(a.status, kDataLengthRange);
     most = __reduce_max_sync(0xffffffffu, most);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
     total *= H * RT;
-    const long long items = static_cast<long long>(a.B) * H * RT;
-    whole = most <= kWholeTiles && items <= gridDim.x;
+    whole = most <= kWholeTiles && items <= gridDim.x;  // (a.whole: most is 0)
     if (whole) {
       w = blockIdx.x;
       end = items;
@@ -975,11 +980,11 @@ cudaError_t launch(const AttnArgs& a, int sm_count, cudaStream_t stream) {
   z.by_group = DivU64::make(static_cast<unsigned long long>(z.G));
   z.by_heads = DivU64::make(static_cast<unsigned long long>(a.cache.heads));
   z.by_items = DivU64::make(static_cast<unsigned long long>(a.cache.heads) * z.RT);
-  attention_tree_kernel<D, kDual><<<grid, kThreadsR, L::kBytes, stream>>>(a, z, joins);
-  // sequences that the table has no room to make long are not cut (attn_plan)
-  if (static_cast<int64_t>(a.table.max_pages) * a.cache.page_size <= kWholeTiles * kTile &&
-      static_cast<int64_t>(a.B) * a.cache.heads * z.RT <= grid)
-    return cudaGetLastError();
+  AttnArgs b = a;
+  b.whole = static_cast<int64_t>(a.table.max_pages) * a.cache.page_size <= kWholeTiles * kTile &&
+            static_cast<int64_t>(a.B) * a.cache.heads * z.RT <= grid;  // by the room of the page tables alone
+  attention_tree_kernel<D, kDual><<<grid, kThreadsR, L::kBytes, stream>>>(b, z, joins);
+  if (b.whole) return cudaGetLastError();  // nothing to join
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid, ((z.R < L::kRows ? z.R : L::kRows) + 31) / 32 * (D / kJoinDims / kJoinWarps));
   cfg.blockDim = dim3(kJoinWarps * 32);
@@ -989,7 +994,7 @@ cudaError_t launch(const AttnArgs& a, int sm_count, cudaStream_t stream) {
   after[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = after;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, tree_join_kernel<D, kDual>, a, z, static_cast<const Join*>(joins));
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, tree_join_kernel<D, kDual>, b, z, static_cast<const Join*>(joins));
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

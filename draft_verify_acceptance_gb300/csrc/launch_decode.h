@@ -49,6 +49,7 @@ struct AttnArgs {
   // trees (attention_tree.cu): the queries are nodes
   const int32_t* parents = nullptr;  // [B, Q]
   long long parents_stride = 0;      // entries between rows
+  bool whole = false;                // no item can be cut, whatever the lengths are
 };
 
 struct SampleArgs {

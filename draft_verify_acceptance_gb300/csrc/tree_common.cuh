@@ -4,10 +4,26 @@
 // by following parents, which lie at lower indexes, so a walk ends.
 #pragma once
 
+#include "attention_common.cuh"
 #include "device_common.cuh"
 #include "launch_tree.h"
 
 namespace specv {
+
+// attention_common.cuh's plan of a call whose table has no room for more than
+// kWholeTiles tiles a sequence, and whose items are no more than the blocks: the
+// cut is known without the lengths (a block's scan of them takes 2 us).
+template <int kEnd>
+__device__ __forceinline__ AttnPlan attn_plan_whole(const AttnArgs& a, int items_per_seq) {
+  AttnPlan p;
+  p.b = blockIdx.x / items_per_seq;
+  if (p.b < a.B && threadIdx.x == 0 && a.status && attn_length(a, p.b) != a.lengths[p.b]) atomicOr(a.status, kDataLengthRange);
+  p.pad = kWholeTiles + kEnd;
+  p.per = p.pad;
+  p.total = static_cast<long long>(a.B) * items_per_seq * p.per;
+  p.base = static_cast<long long>(p.b) * items_per_seq * p.per;
+  return p;
+}
 
 // The bit sets of an item's rows.
 template <int kRows>
