@@ -464,8 +464,8 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
       // took more of its time than the copies).
       const bool is_v = warp & 1;
       const int S = a.cache.page_size, chunk = lane % kChunks, r0 = lane / kChunks;
-      constexpr int kStep = 32 / kChunks, kPasses = 16 / kStep;
-      const bool in_page = S % 16 == 0;  // tokens 16 g .. 16 g + 15 of a tile lie in one page
+      constexpr int kStep = 32 / kChunks, kPasses = 8 / kStep;
+      const bool in_page = S % 8 == 0;  // tokens 8 g .. 8 g + 7 of a tile lie in one page
       // The pages of tokens lane and 32 + lane, looked up a tile of the warp's ahead:
       // the table's entries are on their way while the tiles before are copied.
       struct Pages {
@@ -522,21 +522,25 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
         if (!is_v && lane == 0) sh.valid[tile_no % kAhead] = make_uint2(exist[0], exist[1]);
         wait(&sh.empty[slot], turn & 1);
         const uint32_t dst = ring + slot * L::kSlot;
-        if (in_page && (exist[0] & exist[1]) == 0xffffffffu) {
-#pragma unroll 1
-          for (int g = 0; g < 4; ++g) {
-            const char* from = pool + __shfl_sync(0xffffffffu, g < 2 ? off[0] : off[1], (g & 1) * 16);
+        // (rows that do not exist are zero-filled)
+        if (in_page) {
+#pragma unroll 4
+          for (int g = 0; g < 8; ++g) {
+            const long long first = __shfl_sync(0xffffffffu, g < 4 ? off[0] : off[1], (g & 3) * 8);  // -1: nor do the rest
+            const uint32_t some = (g < 4 ? exist[0] : exist[1]) >> ((g & 3) * 8 + r0);
+            const char* from = first < 0 ? a.cache.k : pool + first;
+            const long long on = first < 0 ? 0 : stride;
 #pragma unroll
-            for (int i = 0; i < kPasses; ++i, from += stride)
-              cp16(dst + (g * 16 + i * kStep) * 128 + (((chunk & 7) ^ ((r0 + i * kStep) & 7)) << 4), from, 16);
+            for (int i = 0; i < kPasses; ++i, from += on)
+              cp16(dst + (g * 8 + i * kStep) * 128 + (((chunk & 7) ^ ((r0 + i * kStep) & 7)) << 4), from, ((some >> (i * kStep)) & 1) << 4);
           }
         } else {
-#pragma unroll 1
-          for (int i = 0; i < 4 * kPasses; ++i) {
+#pragma unroll 8
+          for (int i = 0; i < 8 * kPasses; ++i) {
             const int t = r0 + i * kStep;
-            const long long from = __shfl_sync(0xffffffffu, i < 2 * kPasses ? off[0] : off[1], t & 31) - r0 * a.cache.token_stride;
-            const bool some = ((i < 2 * kPasses ? exist[0] : exist[1]) >> (t & 31)) & 1;
-            cp16(dst + i * kStep * 128 + (((chunk & 7) ^ (t & 7)) << 4), some ? pool + from : a.cache.k, some ? 16 : 0);  // 0: zero-filled
+            const long long from = __shfl_sync(0xffffffffu, i < 4 * kPasses ? off[0] : off[1], t & 31) - r0 * a.cache.token_stride;
+            const bool some = ((i < 4 * kPasses ? exist[0] : exist[1]) >> (t & 31)) & 1;
+            cp16(dst + i * kStep * 128 + (((chunk & 7) ^ (t & 7)) << 4), some ? pool + from : a.cache.k, some ? 16 : 0);
           }
         }
         cp_arrive(&sh.full[slot]);
@@ -655,6 +659,7 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
       const Item& at = item(items);
       // (those that meet at barriers below stop together, also where a wait ran out)
       if (kDual ? any_of(3 + s, 128, !at.any) : any_of(1, 256, !at.any)) break;
+      if (items > 0 && row_in == 0) mbar_arrive(&sh.item_free[(items - 1) % kItems]);  // nobody reads the last one any more
       const int base = at.n - a.Q;
       if (at.b != sight_b || at.rt != sight_rt) {
         stream_sync(s);
@@ -685,8 +690,9 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
           if (t0 + token >= base) {
             uint4* v = reinterpret_cast<uint4*>(smem + slot * L::kSlot + token * 128);
             bool odd = false;
-#pragma unroll 1
-            for (int c = (row_in >> 6) * (kChunks / 2), end = c + kChunks / 2; c < end; ++c) {
+#pragma unroll 4
+            for (int i = 0; i < kChunks / 2; ++i) {
+              const int c = (row_in >> 6) * (kChunks / 2) + i;
               uint4* piece = v + (c >> 3) * (kHalf / 16) + ((c ^ token) & 7);  // (in an order without bank conflicts)
               const uint4 w = *piece;
               if (nonfinite2(w.x) || nonfinite2(w.y) || nonfinite2(w.z) || nonfinite2(w.w)) {
@@ -773,6 +779,15 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
       }
 
       // ---- the item, or this block's part of it ---------------------------------
+      const int r = row_at + row_in;  // of the item
+      const bool row = r < at.rows, none = sight.blind(row_in);
+      const AttnRow ar = row_of(z, at.row0 + min(r, at.rows - 1), at.h);
+      const size_t to = (static_cast<size_t>(at.b) * a.Q + ar.i) * a.Hq + ar.hq;
+      float* slot = attn_slot<L::kRows, D>(a, blockIdx.x, at.tile0 == 0);
+      const uint32_t rows = __ballot_sync(0xffffffffu, row);
+      long long to4[4];  // the four lanes' rows
+#pragma unroll
+      for (int k = 0; k < 4; ++k) to4[k] = __shfl_sync(0xffffffffu, static_cast<long long>(to), (lane & 28) | k);
       const bool mine = tiles > first;  // has the stream a part
       if (mine) wait(&sh.pv_done[s][(count - 1) & 1], ((count - 1) >> 1) & 1);
       const bool whole = at.whole();
@@ -792,24 +807,15 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
         if (both) l = fmaf(c1, sh.l[1][row_in], l);
       }
       tc_after();
-      const int r = row_at + row_in;  // of the item
-      const bool row = r < at.rows, none = sight.blind(row_in);
       if (none) {  // no node: what it summed over the context is nobody's
         m = -INFINITY;
         l = 0.f;
       }
-      const AttnRow ar = row_of(z, at.row0 + min(r, at.rows - 1), at.h);
-      const size_t to = (static_cast<size_t>(at.b) * a.Q + ar.i) * a.Hq + ar.hq;
-      float* slot = attn_slot<L::kRows, D>(a, blockIdx.x, at.tile0 == 0);
       const float inv = whole ? (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l)) : 1.f;
       const bool odd = *reinterpret_cast<volatile int*>(&sh.odd[items % kOdd]) != 0;
       constexpr int kPart = kDual ? D : D / 2;  // columns that the thread writes
       c0 *= inv;
       c1 *= inv;
-      const uint32_t rows = __ballot_sync(0xffffffffu, row);
-      long long to4[4];  // the four lanes' rows
-#pragma unroll
-      for (int k = 0; k < 4; ++k) to4[k] = __shfl_sync(0xffffffffu, static_cast<long long>(to), (lane & 28) | k);
 #pragma unroll 1
       for (int d = kDual ? 0 : s * kPart, end = d + kPart; d < end; d += 32) {
         uint32_t u[32];
@@ -887,8 +893,6 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
       if (!whole && at.tile0 == 0 && tid == 0) joins[blockIdx.x] = {at.b, at.h, at.row0, at.rows, at.end, 0};
       if constexpr (!kDual) soft_sync();  // both streams' O may be written again
       tile_no += tiles;
-      stream_sync(s);  // (the last to read the item)
-      if (row_in == 0) mbar_arrive(&sh.item_free[items % kItems]);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
   }
