@@ -72,10 +72,11 @@ static_assert(kSoft * kSoftRegs + (kThreadsR - kSoft) * kOtherRegs <= 65536 && k
 constexpr int kScores = 8 + kLoadWarps, kOutputs = kScores + 1;   // the warps that issue products,
 constexpr int kWalker = kOutputs + 1, kQueries = kWalker + 1;     // the one that finds the block's items, the one that copies queries
 constexpr float kSlackR = 8.f;   // how far (log2) a score may pass the reference
-// Steps that an item's start and end count as: by the blocks' times, 6.6 us against
-// 1.27 a tile with two row tiles, 5.1 against 0.70 with one.
+// Steps that an item's start and end count as (two row tiles; one).  4 and 6: 64 x 16
+// nodes over 400..4000 tokens 112.8 us, 32 x 64 110.9, 20 x 40 over 100..1500 42.9;  5 and
+// 8: 113.0, 111.3, 43.9;  6 and 10: 114.8, 112.1, 44.2.
 template <bool kDual>
-constexpr int kEndR = kDual ? 5 : 8;
+constexpr int kEndR = kDual ? 4 : 6;
 // Steps that a block gets at least, when there are more blocks than work: one tree of
 // 60 nodes over 2111 tokens, two streams, 4: 24.9 us, 3 and 6: 26.7, 9: 28.8;  one of
 // 30 over 4000, 4: 27.0, 6: 24.7, 9: 23.6;  over 700, 4: 18.5, 6 and 9: 20.5.
