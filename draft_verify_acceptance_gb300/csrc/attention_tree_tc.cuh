@@ -365,6 +365,21 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 __device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 __device__ __forceinline__ void stream_sync(int s) { asm volatile("bar.sync %0, 128;" ::"r"(3 + s) : "memory"); }
 
+// 16 bytes of the cache (0: zeros), with an L2 policy.
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, uint32_t bytes, unsigned long long policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint.L2::256B [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src), "r"(bytes),
+               "l"(policy)
+               : "memory");
+}
+// What is read once makes room first (partial results and page tables stay: 64 x 16
+// nodes 112.1 -> 108.0 us, long sequences 161 -> 155).
+__device__ __forceinline__ unsigned long long policy_of(bool once) {
+  unsigned long long p;
+  if (once) asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  else asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+
 // Is x true in one of `count` threads of barrier `id`.
 __device__ __forceinline__ bool any_of(int id, int count, bool x) {
   uint32_t r;
@@ -464,6 +479,7 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
       // and waits once for 32 copies (with 16 tokens of every K and V a warp these
       // took more of its time than the copies).
       const bool is_v = warp & 1;
+      const unsigned long long policy = policy_of(z.RT == 1);  // (more row tiles read the cache again)
       const int S = a.cache.page_size, chunk = lane % kChunks, r0 = lane / kChunks;
       constexpr int kStep = 32 / kChunks, kPasses = 8 / kStep;
       const bool in_page = S % 8 == 0;  // tokens 8 g .. 8 g + 7 of a tile lie in one page
@@ -533,7 +549,7 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
             const long long on = first < 0 ? 0 : stride;
 #pragma unroll
             for (int i = 0; i < kPasses; ++i, from += on)
-              cp16(dst + (g * 8 + i * kStep) * 128 + (((chunk & 7) ^ ((r0 + i * kStep) & 7)) << 4), from, ((some >> (i * kStep)) & 1) << 4);
+              cp16(dst + (g * 8 + i * kStep) * 128 + (((chunk & 7) ^ ((r0 + i * kStep) & 7)) << 4), from, ((some >> (i * kStep)) & 1) << 4, policy);
           }
         } else {
 #pragma unroll 8
@@ -541,7 +557,7 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
             const int t = r0 + i * kStep;
             const long long from = __shfl_sync(0xffffffffu, i < 4 * kPasses ? off[0] : off[1], t & 31) - r0 * a.cache.token_stride;
             const bool some = ((i < 4 * kPasses ? exist[0] : exist[1]) >> (t & 31)) & 1;
-            cp16(dst + i * kStep * 128 + (((chunk & 7) ^ (t & 7)) << 4), some ? pool + from : a.cache.k, some ? 16 : 0);
+            cp16(dst + i * kStep * 128 + (((chunk & 7) ^ (t & 7)) << 4), some ? pool + from : a.cache.k, some ? 16 : 0, policy);
           }
         }
         cp_arrive(&sh.full[slot]);
