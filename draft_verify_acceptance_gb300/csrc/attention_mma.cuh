@@ -52,12 +52,14 @@ constexpr int kMmaRows = 24;                 // rows of an item, at most
 constexpr int kTokens = 16;                  // a warp's step
 constexpr float kSlack = 8.f;                // how far (log2) a score may pass the reference
 
-template <typename E, int D, int NB>
+template <typename E, int D, int NB, int kTree = 0>
 struct Ring {
   static constexpr bool kF32 = E::kBytes == 4;
-  static constexpr int kWarps = kF32 && D == 128 ? 6 : 4;
+  static constexpr bool kWide = kTree == 2;  // one block of eight warps an SM
+  static_assert(!kWide || (kF32 && D == 64), "the others fill an SM with their rings");
+  static constexpr int kWarps = kF32 && D == 128 ? 6 : kWide ? 8 : 4;
   static constexpr int kStages = kF32 ? (D == 128 ? 2 : 3) : (D == 128 ? 3 : 6);
-  static constexpr int kCtas = kF32 && D == 128 ? 1 : 2;  // an SM holds
+  static constexpr int kCtas = (kF32 && D == 128) || kWide ? 1 : 2;  // an SM holds
   static constexpr int kEnd = kF32 ? NB + 1 : 2 * NB + 2;  // steps that an item's start and end count as
   static constexpr int kRow = D * E::kBytes;             // bytes of a token's K or V
   static constexpr int kHalf = kTokens * kRow;           // K of a step; V follows
@@ -179,11 +181,11 @@ __device__ __forceinline__ uint32_t even_word(uint32_t w) {
   return w;
 }
 
-// NB blocks of 8 rows an item.  kTree: the queries are a tree's nodes, and see
+// NB blocks of 8 rows an item.  kTree 1 and 2: the queries are a tree's nodes, and see
 // its tokens by TreeSight's bits instead of up to themselves.
-template <typename E, int D, int NB, bool kTree>
-__global__ void __launch_bounds__(Ring<E, D, NB>::kWarps * 32, Ring<E, D, NB>::kCtas) attention_mma_kernel(const AttnArgs a, DivU64 by_page) {
-  using L = Ring<E, D, NB>;
+template <typename E, int D, int NB, int kTree>
+__global__ void __launch_bounds__(Ring<E, D, NB, kTree>::kWarps * 32, Ring<E, D, NB, kTree>::kCtas) attention_mma_kernel(const AttnArgs a, DivU64 by_page) {
+  using L = Ring<E, D, NB, kTree>;
   constexpr bool kF32 = L::kF32;
   constexpr int kWarpsM = L::kWarps, kThreadsM = kWarpsM * 32, kStepM = kWarpsM * kTokens;  // a block's step
   constexpr int kRows = 8 * NB, KS = D / 16, kStages = L::kStages;
@@ -619,18 +621,19 @@ __global__ void __launch_bounds__(Ring<E, D, NB>::kWarps * 32, Ring<E, D, NB>::k
   }
 }
 
-template <typename E, int D, int NB, bool kTree>
+template <typename E, int D, int NB, int kTree>
 cudaError_t prepare() {
   return cudaFuncSetAttribute(attention_mma_kernel<E, D, NB, kTree>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              Ring<E, D, NB>::kBytes);
+                              Ring<E, D, NB, kTree>::kBytes);
 }
-template <typename E, int D, int NB, bool kTree>
+template <typename E, int D, int NB, int kTree>
 void launch(const AttnArgs& a, int sm_count, cudaStream_t stream) {
-  const int grid = sm_count * Ring<E, D, NB>::kCtas < kMaxMmaCtas ? sm_count * Ring<E, D, NB>::kCtas : kMaxMmaCtas;
-  attention_mma_kernel<E, D, NB, kTree><<<grid, Ring<E, D, NB>::kWarps * 32, Ring<E, D, NB>::kBytes, stream>>>(
+  using L = Ring<E, D, NB, kTree>;
+  const int grid = sm_count * L::kCtas < kMaxMmaCtas ? sm_count * L::kCtas : kMaxMmaCtas;
+  attention_mma_kernel<E, D, NB, kTree><<<grid, L::kWarps * 32, L::kBytes, stream>>>(
       a, DivU64::make(static_cast<unsigned long long>(a.cache.page_size)));
 }
-template <typename E, bool kTree = false>
+template <typename E, int kTree = 0>
 cudaError_t prepare_all() {
   cudaError_t e[] = {prepare<E, 64, 1, kTree>(),  prepare<E, 64, 2, kTree>(),  prepare<E, 64, 3, kTree>(),
                      prepare<E, 128, 1, kTree>(), prepare<E, 128, 2, kTree>(), prepare<E, 128, 3, kTree>()};
@@ -638,17 +641,29 @@ cudaError_t prepare_all() {
     if (x != cudaSuccess) return x;
   return cudaSuccess;
 }
+// fp32 heads of 64 in blocks of eight warps.
+inline void launch_wide(const AttnArgs& a, int nb, int sm_count, cudaStream_t stream) {
+  if (nb == 1) launch<F32, 64, 1, 2>(a, sm_count, stream);
+  else if (nb == 2) launch<F32, 64, 2, 2>(a, sm_count, stream);
+  else launch<F32, 64, 3, 2>(a, sm_count, stream);
+}
+inline cudaError_t prepare_wide() {
+  cudaError_t e[] = {prepare<F32, 64, 1, 2>(), prepare<F32, 64, 2, 2>(), prepare<F32, 64, 3, 2>()};
+  for (cudaError_t x : e)
+    if (x != cudaSuccess) return x;
+  return cudaSuccess;
+}
 // Is no item of nb blocks of rows cut, by the room of the page tables alone (attn_plan's rule).
-template <typename E, int D>
+template <typename E, int D, int kTree>
 bool whole(const AttnArgs& a, int nb, int sm_count) {
-  using L = Ring<E, D, 1>;  // (the same for all nb in what counts here)
+  using L = Ring<E, D, 1, kTree>;  // (the same for all nb in what counts here)
   const int grid = sm_count * L::kCtas < kMaxMmaCtas ? sm_count * L::kCtas : kMaxMmaCtas;
   const int R = a.Q * (a.Hq / a.cache.heads), RT = (R + 8 * nb - 1) / (8 * nb);
   return static_cast<int64_t>(a.table.max_pages) * a.cache.page_size <= kWholeTiles * L::kWarps * kTokens &&
          static_cast<int64_t>(a.B) * a.cache.heads * RT <= grid;
 }
 // Items of nb blocks of 8 rows, 1 to 3.
-template <typename E, bool kTree = false>
+template <typename E, int kTree = 0>
 void launch_rows(const AttnArgs& a, int nb, int sm_count, cudaStream_t stream) {
   switch (nb + (a.cache.head_dim == 128 ? 3 : 0)) {
     case 1: launch<E, 64, 1, kTree>(a, sm_count, stream); break;
