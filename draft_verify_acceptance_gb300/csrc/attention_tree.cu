@@ -14,10 +14,11 @@ namespace specv {
 // attention_tree_tc.cuh, the rest to attention_mma.cuh, in tiles of at most 24 rows
 // that each read K and V again (through L2), and scales that are not above zero.
 // Measured, mma and tc, 32 query heads on 8, heads of 128:  64 sequences of 400..4000
-// tokens, R = 24: 113 and 117 us, R = 32: 181 and 118;  64 of 200..400, R = 32: 55 and 42;
+// tokens, R = 24: 113 and 117 us, R = 32: 181 and 118;  64 of 200..400, R = 32: 55 and 44;
 // 8 of 1000, R = 52: 33 and 27;  one of 500, R = 120: 20 and 18, R = 240: 21 and 23;  one
 // of 20000, R = 52: 58 and 41.  Heads of 64:  32 of 400..4000, R = 48: 86 and 58;  64 of
-// 100..190, two query heads on each, R = 26: 19 and 21.
+// 100..190, two query heads on each, R = 26: 19 and 21.  (tc has since won 2 to 4 us at the small
+// ones, 10 at the large.)
 namespace {
 bool on_tc(int rows, bool bf16) { return bf16 && rows > mma::kMmaRows; }
 }  // namespace

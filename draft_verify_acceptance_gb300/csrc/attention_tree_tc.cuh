@@ -28,13 +28,12 @@
 // other from the instruction caches, and a tile took 4000 cycles.
 //
 // 32 query heads of 128 on 8:  64 sequences of 400..4000 tokens, 16 nodes (64 rows a
-// head) 114 us (the cache's bytes at the copy rate: 87; a block's tile 1300 cycles,
-// what HBM gives an SM 1430 for it when all take their share; an item's start and end
-// 5 us of a block's time, a third hidden behind the ring);  2 of 60001..131072,
-// 26 nodes: 156 us (134);  32 of 400..4000, 64 nodes (256 rows): 111 us (45), a tile 2300 cycles
-// of products, the scores' as long as the outputs' since each reads 4 KB of queries
-// for 64 tokens;  one of 2111, 60 nodes: 25 us, start, part and join.  32 of 400..4000
-// over heads of 64, 30 nodes: 55 us (23), by the softmax's latency.
+// head) 108 us (the cache's bytes at the copy rate: 87; a block's tile 1300 cycles, an
+// item's start and end 5 us of a block's time, part of it hidden behind the ring);  2 of
+// 60001..131072, 26 nodes: 155 us (139);  32 of 400..4000, 64 nodes (256 rows): 109 us (45), a
+// tile 2300 cycles of products, the scores' as long as the outputs' since each reads
+// 4 KB of queries for 64 tokens;  one of 2111, 60 nodes: 25 us, start, part and join.
+// 32 of 400..4000 over heads of 64, 30 nodes: 56 us (23), by the softmax's latency.
 #pragma once
 
 #include "attention_common.cuh"

@@ -105,7 +105,7 @@ __device__ __forceinline__ uint4 ld_once(const uint4* p) { return __ldcs(p); }
 // token's place and turns its angles, which every part does for itself.  HBM bounds
 // many tokens (53141 tokens of 12 prompts, 32 + 8 heads of 128, bf16: 202 us, 97 % of the
 // copy rate; one unit at a time it was 219), the dependent look-ups few (64 trees of
-// 16: 10.2 us, 25 MB).
+// 16: 8.4 us, 25 MB).
 template <typename E, bool kInterleaved>
 __global__ void __launch_bounds__(kAppendWarps * 32)
 rotated_append_kernel(const RotatedAppendArgs a, int parts, DivU64 by_part, Div32 by_unit) {
@@ -252,7 +252,7 @@ rotated_append_kernel(const RotatedAppendArgs a, int parts, DivU64 by_part, Div3
 // ---- accept --------------------------------------------------------------------
 // One warp a tree, a lane holding nodes lane, lane + 32, ...: a step compares all
 // of them with (node, drawn token) and takes the lowest match.  A launch bounds it:
-// 512 trees of 64 nodes 7.3 us, four trees 7.0.
+// 512 trees of 64 nodes 6 to 7 us, four trees the same.
 constexpr int kAcceptWarps = 4;
 __global__ void __launch_bounds__(kAcceptWarps * 32) tree_accept_kernel(const AcceptArgs a) {
   __shared__ int32_t s_drawn[kAcceptWarps][kMaxNodes], s_path[kAcceptWarps][kMaxNodes];
@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(kAcceptWarps * 32) tree_accept_kernel(const Ac
 // and makes the path's moves in order, eight loads under way: a token comes from
 // its own index or a later one, so no load of a batch, or of a later one, reads
 // what a store of it has written.  64 trees of 64 nodes in 16 layers, 8 heads of 128,
-// bf16, 6 nodes moved a tree: 15.0 us (their bytes at the copy rate 11.3).
+// bf16, 6 nodes moved a tree: 14.5 to 15.7 us (their bytes at the copy rate 11.3).
 constexpr int kKeepThreads = 128, kKeepMoves = 128;
 __global__ void __launch_bounds__(kKeepThreads) keep_kernel(const KeepArgs a, unsigned chunks) {
   __shared__ long long s_from[kKeepMoves], s_to[kKeepMoves];
@@ -397,8 +397,9 @@ cudaError_t launch_rotated_append(const RotatedAppendArgs& a, int sm_count, cuda
   const int esz = a.cache.bf16 ? 2 : 4, kN = 16 / esz, D = a.cache.head_dim;
   const int turned = a.interleaved ? 2 * a.n_freq / kN : a.n_freq / kN, per_head = turned + (D - 2 * a.n_freq) / kN;
   const long long units = static_cast<long long>(a.q_heads + a.cache.heads) * per_head + static_cast<long long>(a.cache.heads) * (D / kN);
-  // warps a token: enough to fill the GPU, with a unit a lane at least
-  long long parts = static_cast<long long>(sm_count) * 32 / a.T;
+  // Warps a token: one wave of the 16 that an SM holds, with a unit a lane at least.  64
+  // trees of 16: 16 an SM 8.4 us, 8 and 32 10.3, 64 14.4;  16 trees: 6.2, 6.4, 8.2, 8.2.
+  long long parts = static_cast<long long>(sm_count) * 16 / a.T;
   if (parts > (units + 31) / 32) parts = (units + 31) / 32;
   if (parts < 1) parts = 1;
   const long long blocks = (a.T * parts + kAppendWarps - 1) / kAppendWarps;
