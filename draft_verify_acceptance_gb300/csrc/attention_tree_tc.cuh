@@ -55,7 +55,6 @@ using tc::operand;
 using tc::tc_after;
 using tc::tc_before;
 using tc::tc_commit;
-using tc::tc_mma;
 using tc::tmem_alloc;
 using tc::tmem_free;
 using tc::tmem_st_done;
