@@ -75,11 +75,13 @@ constexpr float kSlackR = 8.f;   // how far (log2) a score may pass the referenc
 // 8: 113.0, 111.3, 43.9;  6 and 10: 114.8, 112.1, 44.2.
 template <bool kDual>
 constexpr int kEndR = kDual ? 4 : 6;
-// Steps that a block gets at least, when there are more blocks than work: one tree of
-// 60 nodes over 2111 tokens, two streams, 4: 24.9 us, 3 and 6: 26.7, 9: 28.8;  one of
-// 30 over 4000, 4: 27.0, 6: 24.7, 9: 23.6;  over 700, 4: 18.5, 6 and 9: 20.5.
+// Steps that a block gets at least, when there are more blocks than work: an item of T
+// tiles cut into parts of p takes p tiles, and T / p parts to join, so p goes with the
+// root of T.  One tree, one row tile: T = 11, 3 and 4 steps 17 us, 6 and 8 18.7, 12 20.7;
+// T = 32, 4 21.6, 6 20.6, 8 21.2, 12 22.6;  T = 125, 7 30.8, 8 29.0, 12 27.1.  Two row tiles:
+// T = 16 (two trees), 2 to 4 22.6, 6 24.7;  T = 33, 2 27.2, 4 24.7, 6 26.5.
 template <bool kDual>
-constexpr int kLeast = kDual ? 4 : 6;
+constexpr float kLeast = kDual ? 0.7f : 1.f;  // times the root of the most tiles
 constexpr int kMaxCtas = 160;
 constexpr int kAhead = 32;       // tiles whose valid bits are kept, more than the ring holds
 constexpr int kOdd = 8;          // items whose flag is kept, more than a stream can be behind
@@ -121,7 +123,7 @@ __device__ __forceinline__ AttnRow row_of(const Shape& z, int row, int h) {
 // an item's tiles and kEnd steps more are numbered item by item, sequence by
 // sequence, and block c takes steps [c * per, (c + 1) * per).  With a block for every
 // item and none of more than kWholeTiles tiles, nothing is cut.
-template <int kRows, int kEnd, int kLeast>
+template <int kRows, int kEnd>
 struct Walker {
   const AttnArgs& a;
   long long w, end, per, base;  // step, last step and number of steps of the block; first step of sequence b
@@ -172,7 +174,7 @@ struct Walker {
       return;
     }
     per = divide(total + gridDim.x - 1, gridDim.x);
-    if (per < kLeast) per = kLeast;
+    per = max(per, static_cast<long long>(fmaf(kRows == 256 ? kLeast<true> : kLeast<false>, sqrtf(static_cast<float>(most)), 0.5f)));
     w = per * blockIdx.x;
     end = min(total, w + per);
     // the sequence that has step w, 32 sequences at a time
@@ -631,7 +633,7 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
       __syncwarp();
     } else if (warp == kWalker) {
       // ---- items -------------------------------------------------------------------
-      Walker<L::kRows, kEndR<kDual>, kLeast<kDual>> at(a, z, lane);
+      Walker<L::kRows, kEndR<kDual>> at(a, z, lane);
       for (int items = 0;; ++items) {
         Item i;
         at.next(i);
