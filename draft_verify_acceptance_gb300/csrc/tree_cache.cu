@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(kKeepThreads) keep_kernel(const KeepArgs a, un
   const int base = n - a.N;
   int kept = 0;
   for (int j0 = 0; j0 < a.N; j0 += kKeepMoves) {
-    // the path's entries of this round, up to its end
+    // the path's next entries, up to its end
     if (tid == 0) s_end = min(a.N - j0, kKeepMoves);
     __syncthreads();
     const int j = j0 + tid;
