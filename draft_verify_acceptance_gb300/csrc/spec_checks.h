@@ -18,6 +18,18 @@ inline bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
   return p < q + static_cast<uintptr_t>(nb) && q < p + static_cast<uintptr_t>(na);
 }
 
+// Do T rows of na bytes at a and T of nb bytes at b share bytes?  Of one stride, the rows of
+// one may lie between those of the other (columns of a fused projection): then
+// the columns decide.
+inline bool rows_overlap(const void* a, int64_t a_stride, int64_t na, const void* b, int64_t b_stride, int64_t nb, int64_t T) {
+  if (!overlap(a, (T - 1) * a_stride + na, b, (T - 1) * b_stride + nb)) return false;
+  if (T == 1 || a_stride != b_stride) return true;
+  const auto p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+  const auto stride = static_cast<uintptr_t>(a_stride);
+  const uintptr_t column = p <= q ? (q - p) % stride : (stride - (p - q) % stride) % stride;  // of b's rows, from a's
+  return column < static_cast<uintptr_t>(na) || column + static_cast<uintptr_t>(nb) > stride;
+}
+
 inline spec_status_t done(cudaError_t e) { return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA; }
 
 inline spec_status_t check_cache(const spec_cache_t* c, CacheView* out) {

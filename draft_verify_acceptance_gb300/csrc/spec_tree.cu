@@ -133,11 +133,16 @@ spec_status_t spec_cache_append_rotated(const void* k_new, const void* v_new, in
     if (!q || !q_out || !aligned(q, 16) || !aligned(q_out, 16) || q_stride < q_row || q_stride * esz % 16 ||
         q_out_stride < q_row || q_out_stride * esz % 16)
       return SPEC_ERR_INVALID_ARG;
-    if (!(q == q_out && (q_stride == q_out_stride || T == 1)) &&
-        (overlap(q, ((T - 1) * q_stride + q_row) * esz, q_out, ((T - 1) * q_out_stride + q_row) * esz) ||
-         overlap(k_new, ((T - 1) * new_stride + row) * esz, q_out, ((T - 1) * q_out_stride + q_row) * esz) ||
-         overlap(v_new, ((T - 1) * new_stride + row) * esz, q_out, ((T - 1) * q_out_stride + q_row) * esz)))
+    const int64_t bytes = q_row * esz, span = (T - 1) * q_out_stride * esz + bytes, new_span = ((T - 1) * new_stride + row) * esz;
+    if (q == q_out && (q_stride == q_out_stride || T == 1)) {
+      // In place: warps read new keys and values while others of the token write its queries.
+      if (rows_overlap(q, q_stride * esz, bytes, k_new, new_stride * esz, row * esz, T) ||
+          rows_overlap(q, q_stride * esz, bytes, v_new, new_stride * esz, row * esz, T))
+        return SPEC_ERR_INVALID_ARG;
+    } else if (overlap(q, (T - 1) * q_stride * esz + bytes, q_out, span) || overlap(k_new, new_span, q_out, span) ||
+               overlap(v_new, new_span, q_out, span)) {
       return SPEC_ERR_INVALID_ARG;
+    }
   }
   int sms = 0;
   st = device_sms(&sms);

@@ -161,8 +161,8 @@ def cache_append_rotated(at, k_new, v_new, k_pages, v_pages, page_table, lengths
     turns by position * inv_freq[i]; pair i is dimensions i and F + i, or 2i and 2i + 1 with
     ``interleaved``; dimensions from 2 F on stay.  ``positions`` int32 [T] or [B, n] gives the tokens'
     positions (of a tree's nodes: the context's tokens and their depth), else they are their
-    places in their sequences.  Returns the rotated queries (``out`` if it is given: q itself, or a tensor that
-    overlaps none of the new rows; None without q), with ``debug`` (queries, status).
+    places in their sequences.  Returns the rotated queries (``out`` if it is given: q itself, which then shares
+    nothing with k_new and v_new, or a tensor that overlaps none of the new rows; None without q), with ``debug`` (queries, status).
     """
     index, stream = at
     c = _cache(k_pages, v_pages, False, index)

@@ -70,8 +70,10 @@ SPEC_API spec_status_t spec_tree_attention(
  *
  *   k_new, v_new, starts, cache, page_table, lengths: as spec_cache_append's.
  *   q        [T, q_heads, head_dim], rows q_stride elements apart, or NULL (q_heads 0);
- *   q_out    their rotated rows, q_out_stride apart: q itself at its stride, or
- *            memory that overlaps neither q's, k_new's nor v_new's.
+ *   q_out    their rotated rows, q_out_stride apart: q itself at its stride, whose
+ *            rows share no byte with k_new's and v_new's (of the same stride they may lie
+ *            in one another's gaps, as slices of a fused projection do), or memory
+ *            that overlaps neither q's, k_new's nor v_new's.
  *   positions [T] int32: the tokens' positions (of a tree's node: the context's
  *            tokens and its depth); NULL: their places in their sequences.
  *   inv_freq [n_freq] fp32, finite: the angle of pair i at position p is

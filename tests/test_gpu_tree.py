@@ -474,6 +474,42 @@ def test_append_refusals(tree):
             ok(**bad)
 
 
+@pytest.mark.parametrize("dtype", BOTH)
+@pytest.mark.parametrize("order", ["qkv", "kvq", "kqv"])
+@pytest.mark.parametrize("B,n", [(1, 1), (2, 1), (2, 7), (1, 300)])
+def test_append_in_place_between_the_rows_it_reads(tree, dtype, order, B, n):
+    """The queries of a fused projection rotated where they lie, keys and values in the gaps between them; where keys or values
+    are the queries' own bytes the call is refused."""
+    from draft_verify_acceptance_gb300.binding import SpecVerifyError
+    Hq, H, D, S = 8, 2, 64, 16
+    k, v, table, lengths = make_cache([n + 5] * B, S, H, D, dtype, seed=n)
+    fused = torch.randn((B, n, (Hq + 2 * H) * D), generator=gen(n), device="cuda").to(dtype)
+    heads = {"q": Hq, "k": H, "v": H}
+
+    def slices(x):
+        at, r = 0, {}
+        for c in order:
+            r[c] = x[..., at:at + heads[c] * D].unflatten(-1, (-1, D))
+            at += heads[c] * D
+        return r
+    inv = (10000.0 ** (-torch.arange(32, dtype=torch.float64) / 32)).float().cuda()
+    x = slices(fused.clone())
+    wk, wv = k.clone(), v.clone()
+    want = tree.cache_append_rotated(x["k"], x["v"], wk, wv, table, lengths, inv, x["q"])
+    whole = fused.clone()
+    x = slices(whole)
+    assert tree.cache_append_rotated(x["k"], x["v"], k, v, table, lengths, inv, x["q"], out=x["q"]) is x["q"]
+    assert torch.equal(x["q"], want) and torch.equal(k, wk) and torch.equal(v, wv)
+    assert torch.equal(x["k"], slices(fused)["k"]) and torch.equal(x["v"], slices(fused)["v"])
+    for bad in (x["q"][..., :H, :], x["q"][..., -H:, :]):
+        for kn, vn in ((bad, x["v"]), (x["k"], bad)):
+            if kn.stride() != vn.stride():
+                continue
+            with pytest.raises(SpecVerifyError):
+                tree.cache_append_rotated(kn, vn, k, v, table, lengths, inv, x["q"], out=x["q"])
+    assert torch.equal(k, wk) and torch.equal(v, wv)
+
+
 # ---- accept and keep ------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("B,N", [(1, 1), (7, 2), (40, 13), (5, 31), (5, 32), (5, 33), (300, 64), (10, 255), (10, 256), (3, 0)])

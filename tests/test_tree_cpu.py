@@ -208,3 +208,57 @@ def test_the_reference_walk():
     assert n[0] == 2 and path[0, :4].tolist() == [0, 2, 4, -1] and out[0, :4].tolist() == [5, 7, 3, -1]
     new, moves = ref.keep(np.array([[3, 1, 0]]), np.array([13]), path, 4, 5)
     assert new[0] == 7 and moves == [((1, 1), (1, 0)), ((1, 3), (1, 1))]
+
+
+def test_append_in_place_refuses_new_rows_that_share_its_queries(tree):
+    """q rotated in place (q_out is q): another warp of the token may already have written the queries that new keys or values
+    share bytes with.  Rows that lie in one another's gaps are no overlap (test_gpu_tree.py runs those)."""
+    lib, Q = tree._lib, FAKE + 65536
+    c = cache(tree)  # rows of 128 floats
+
+    def call(k=FAKE, v=FAKE, stride=128, T=4, q=Q, qs=128, hq=2, out=None, os_=None):
+        return lib.spec_cache_append_rotated(k, v, stride, T, None, q, qs, hq, q if out is None else out, qs if os_ is None else os_,
+                                             None, FAKE, 32, 0, ctypes.byref(c), FAKE, 4, 4, FAKE, 2, None, None)
+    row = 128 * 4
+    for bad in (dict(k=Q), dict(v=Q), dict(k=Q, v=Q), dict(k=Q + 16), dict(v=Q - 16), dict(k=Q + 3 * row), dict(v=Q - 3 * row),
+                # slices of a fused row of 512 floats: 256 of queries, then keys and values that begin too early or wrap
+                dict(qs=512, stride=512, hq=4, k=Q + 2 * row - 16), dict(qs=512, stride=512, hq=4, v=Q + 3 * row + 16),
+                dict(qs=512, stride=512, hq=4, k=Q - row + 16), dict(qs=512, stride=512, hq=4, v=Q + 8 * row),
+                dict(qs=512, stride=512, hq=4, k=Q - 8 * row),
+                # other strides, one row
+                dict(qs=256, hq=4, k=Q), dict(qs=256, hq=4, v=Q + 6 * row), dict(T=2, qs=256, hq=4, k=Q + 512, stride=512)):
+        assert call(**bad) == 1, bad
+    lib_one = lambda **kw: lib.spec_cache_append_rotated(  # noqa: E731
+        kw.get("k", FAKE), kw.get("v", FAKE), 128, 1, None, Q, 4096, 2, Q, 128, None, FAKE, 32, 0, ctypes.byref(c), FAKE, 4, 4, FAKE, 1,
+        None, None)
+    for bad in (dict(k=Q), dict(v=Q + row - 16), dict(k=Q - row + 16)):
+        assert lib_one(**bad) == 1, bad
+
+
+def test_the_rows_overlap_rule_against_bytes(tmp_path):
+    """spec_checks.h's rule for rows of one stride, and its range rule else, against the bytes themselves."""
+    src = tmp_path / "rows.cpp"
+    src.write_text('#include "spec_checks.h"\n'
+                   'extern "C" int rows(long a, long as, long na, long b, long bs, long nb, long T) {\n'
+                   '  return specv::rows_overlap(reinterpret_cast<void*>(a), as, na, reinterpret_cast<void*>(b), bs, nb, T); }\n')
+    out = tmp_path / "rows.so"
+    from draft_verify_acceptance_gb300 import build
+    r = subprocess.run(["g++", "-std=c++17", "-shared", "-fPIC", "-I", build.CSRC, "-I", os.path.join(os.path.dirname(os.path.dirname(build._nvcc())), "include"),
+                        str(src), "-o", str(out)], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    rows = ctypes.CDLL(str(out)).rows
+    rows.argtypes = [ctypes.c_long] * 7
+    rng = np.random.RandomState(0)
+    met = [0, 0]
+    for _ in range(20000):
+        T, s, na, nb = rng.randint(1, 6), rng.randint(4, 20), 0, 0
+        na, nb = rng.randint(1, s + 1), rng.randint(1, s + 1)
+        a, b = 1000, 1000 + rng.randint(-6 * s, 6 * s)
+        bytes_a = {a + t * s + i for t in range(T) for i in range(na)}
+        bytes_b = {b + t * s + i for t in range(T) for i in range(nb)}
+        share = bool(bytes_a & bytes_b)
+        assert rows(a, s, na, b, s, nb, T) == share, (T, s, na, nb, b - a)
+        met[share] += 1
+        if rows(a, s, na, b, s + 4, nb, T) == 0:  # of other strides: never too lax
+            assert not bytes_a & {b + t * (s + 4) + i for t in range(T) for i in range(nb)}
+    assert min(met) > 3000
