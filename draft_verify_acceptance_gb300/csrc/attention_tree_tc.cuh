@@ -105,7 +105,8 @@ struct Item {
   int b, h, n, rt, row0, rows, tile0, tile1, tiles;
   __device__ __forceinline__ bool whole() const { return tile0 == 0 && tile1 == tiles; }
 };
-constexpr int kItems = 8;  // told ahead of the softmax warps' last
+constexpr int kItems = 8;  // kept: the softmax warps' own, kHeld - 1 before it, the rest told ahead
+constexpr int kHeld = 2;   // items that the softmax warps start before the first of them is given up
 
 // What the host divides for the kernel (32-bit divisions take some 140 cycles, 64-bit ones 500).
 struct Shape {
@@ -473,6 +474,11 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+#ifdef SPEC_DEBUG
+    // (another bit: the warps that a block's first item may need nothing of are a millisecond late)
+    if ((warp == kQueries || warp == 10 || warp == 11) && a.status && (*reinterpret_cast<volatile int32_t*>(a.status) >> 29 & 1))
+      for (int i = 0; i < 1000; ++i) __nanosleep(1000);
+#endif
     if (warp < kScores) {
       // ---- K and V of each tile, in turn -----------------------------------
       // A warp takes K or V of every other tile, so that it looks its 64 tokens up
@@ -676,7 +682,11 @@ __global__ void __launch_bounds__(kThreadsR, 1) attention_tree_kernel(const Attn
       const Item& at = item(items);
       // (those that meet at barriers below stop together, also where a wait ran out)
       if (kDual ? any_of(3 + s, 128, !at.any) : any_of(1, 256, !at.any)) break;
-      if (items > 0 && row_in == 0) mbar_arrive(&sh.item_free[(items - 1) % kItems]);  // nobody reads the last one any more
+      // Nobody reads the item before the last any more: every warp has read it before it
+      // could do what the last one needed of it.  (The last one itself may still be ahead of
+      // the queries' warp, where it is the block's first, and of the loaders of odd
+      // tiles, where it is that and one tile: the softmax warps needed nothing of theirs.)
+      if (items >= kHeld && row_in == 0) mbar_arrive(&sh.item_free[(items - kHeld) % kItems]);
       const int base = at.n - a.Q;
       if (at.b != sight_b || at.rt != sight_rt) {
         stream_sync(s);

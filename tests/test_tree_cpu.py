@@ -262,3 +262,97 @@ def test_the_rows_overlap_rule_against_bytes(tmp_path):
         if rows(a, s, na, b, s + 4, nb, T) == 0:  # of other strides: never too lax
             assert not bytes_a & {b + t * (s + 4) + i for t in range(T) for i in range(nb)}
     assert min(met) > 3000
+
+
+def told_items_read_too_late(tiles, dual, items, held):
+    """The protocol of attention_tree_tc.cuh's warps over one block's items of `tiles` tiles each, as a graph of what waits for
+    what: (warp, item) pairs whose reading of an item is not ordered before the walker tells another into its place, and
+    whether the whole comes to an end.  Waits for ring slots and score buffers are left out: they only order more."""
+    n, after = len(tiles), {}
+
+    def event(e, *before):
+        after.setdefault(e, set()).update(b for b in before if b is not None)
+    of = [k for k, t in enumerate(tiles) for _ in range(t)]  # a tile's item
+    start = np.concatenate([[0], np.cumsum(tiles)]).tolist()
+    for k in range(n + 1):  # the last says that there are no more
+        event(("told", k), ("told", k - 1) if k else None)
+        if k >= items:
+            event(("told", k), *(("free", s, k - items) for s in (0, 1)))
+
+    def read(warp, k, *before):  # a warp's reads come in order
+        event((warp, k), ("told", k), (warp, k - 1) if k else None, *before)
+    for pair in (0, 1):  # loaders of the even and the odd tiles, K's and V's alike
+        seen = -1
+        for u in range(pair, len(of) + 5, 2):  # looks up tile u, then copies tile u - 4
+            last = of[u] if u < len(of) else n
+            for k in range(seen + 1, last + 1):
+                read(("load", pair), k, ("copied", u - 6) if u >= 6 else None)
+            seen = max(seen, last)
+            if 0 <= u - 4 < len(of):
+                event(("copied", u - 4), (("load", pair), seen), ("copied", u - 6) if u >= 6 else None)
+    for k in range(n + 1):
+        read("queries", k, ("queried", k - 1) if 1 < k <= n else None)
+        if 0 < k < n:
+            event(("queried", k), ("queries", k), ("scores", 1, start[k] - 1))  # the scores of the item before are done
+        for warp in ("scores", "outputs"):
+            read((warp,), k, (warp, 1, start[k] - 1) if k else None)
+        for s in (0, 1):
+            mine = [start[j + 1] - 1 for j in range(k) if dual or s == 0 or tiles[j] > 1]
+            event(("start", s, k), ("told", k), ("start", s, k - 1) if k else None,
+                  ("outputs", 1, mine[-1]) if mine else None)
+            if not dual and k:  # the streams' outputs are joined
+                event(("start", s, k), ("start", 1 - s, k - 1), ("outputs", 1, start[k] - 1))
+            if k >= held:
+                event(("free", s, k - held), ("start", s, k))
+    for t, k in enumerate(of):
+        event(("scores", 1, t), (("scores",), k), ("scores", 1, t - 1) if t else None, ("copied", t),
+              ("queried", k) if k else ("start", 0, 0))
+        for s in ((0, 1) if dual else ((t - start[k]) % 2,)):
+            event(("weights", s, t), ("scores", 1, t), ("start", s, k))
+            event(("outputs", 1, t), ("weights", s, t))
+        event(("outputs", 1, t), (("outputs",), k), ("outputs", 1, t - 1) if t else None, ("copied", t))
+
+    order, state = [], {}
+    for root in after:  # depth first; an event met again on its own line waits for itself
+        stack = [(root, iter(after.get(root, ())))]
+        if state.setdefault(root, 1) == 2:
+            continue
+        while stack:
+            e, rest = stack[-1]
+            x = next(rest, None)
+            if x is None:
+                state[e] = 2
+                order.append(e)
+                stack.pop()
+            elif state.get(x) == 1:
+                return None, False
+            elif x not in state:
+                state[x] = 1
+                stack.append((x, iter(after.get(x, ()))))
+    bit = {e: 1 << i for i, e in enumerate(order)}
+    upto = {}
+    for e in order:
+        upto[e] = bit[e]
+        for x in after.get(e, ()):
+            upto[e] |= upto[x]
+    readers = [("load", 0), ("load", 1), "queries", ("scores",), ("outputs",)]
+    late = [(w, k) for k in range(n + 1 - items) for w in readers if not upto[("told", k + items)] & bit[(w, k)]]
+    return late, True
+
+
+def test_told_items_stay_until_every_warp_has_read_them():
+    """An item's place is told again after the softmax warps give it up.  Given up as they start the next one, a block's first
+    item was held for nobody else: the queries' warp and, after one tile, the odd tiles' loaders might not have looked."""
+    src = open(os.path.join(ROOT, "draft_verify_acceptance_gb300", "csrc", "attention_tree_tc.cuh")).read()
+    items = int(re.search(r"constexpr int kItems = (\d+);", src).group(1))
+    held = re.search(r"constexpr int kHeld = (\d+);", src)
+    held = int(held.group(1)) if held else 1
+    assert f"items >= kHeld && row_in == 0) mbar_arrive(&sh.item_free[(items - kHeld) % kItems])" in src or held == 1
+    late, ends = told_items_read_too_late([1] * 20, False, items, 1)
+    assert ends and set(late) == {("queries", 0), (("load", 1), 0)}
+    rng = np.random.RandomState(0)
+    for dual in (False, True):
+        for case in range(40):
+            tiles = [1] * 20 if case == 0 else rng.randint(1, 2 + case % 5, 24).tolist()
+            late, ends = told_items_read_too_late(tiles, dual, items, held)
+            assert ends and late == [], (tiles, dual)
