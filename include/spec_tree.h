@@ -81,7 +81,7 @@ SPEC_API spec_status_t spec_tree_attention(
  *            `interleaved` 2i and 2i + 1; (x, y) becomes (x cos - y sin, y cos +
  *            x sin).  Dimensions from 2 n_freq on stay.  head_dim a multiple of 8
  *            up to 256, n_freq a multiple of 8 with 2 n_freq <= head_dim.
- * Angles are reduced in fixed point, to 2^-31 of a turn for every position;
+ * Angles are reduced in fixed point, to 2^-31 of a turn for every position and frequency;
  * sines and cosines are within 2^-23; products and sums are fp32, rounded once.
  * Rows that no sequence claims are SPEC_DATA_LENGTH_RANGE, and zero in q_out
  * unless it is q (then they stay).  A token without a place or page (the bits of

@@ -415,6 +415,28 @@ def test_append(tree, dtype, interleaved, counts, before, Hq, H, D, F, S):
         assert back is qi and torch.equal(qi, got) and torch.equal(whole[:, Hq * D:], qkv[:, Hq * D:]) and qi._version > version
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_append_at_high_frequencies(tree, interleaved):
+    """Frequencies from just above 1 to the largest, whose angles no double holds.  Sine, cosine and products as at the others."""
+    H, D, S, T = 2, 64, 16, 7
+    k, v, table, lengths = make_cache([T], S, H, D, torch.float32, seed=1)
+    kn, vn, q = (torch.randn((1, T, H, D), generator=gen(i), device="cuda") for i in (1, 2, 3))
+    r = np.random.RandomState(3)
+    inv = np.concatenate(([1.0, 1 + 2.0 ** -23, 2.5, -1e4, 2.0 ** 24, 1e9, 3.4028235e38, -3e30], r.uniform(1, 2, 24) * 2.0 ** r.randint(0, 127, 24)))
+    inv = torch.tensor(inv, dtype=torch.float32, device="cuda")
+    pos = [0, 1, 17, 131071, 2 ** 31 - 1, -2 ** 31, 123456789]
+    got = tree.cache_append_rotated(kn, vn, k, v, table, lengths, inv, q, i32([pos]), interleaved=interleaved)
+    exact = np.array([[ref.turns(p, f) for f in inv.cpu().tolist()] for p in pos]) * 2 * np.pi
+    one, two = (slice(0, D, 2), slice(1, D, 2)) if interleaved else (slice(0, 32), slice(32, 64))
+    t = torch.arange(T, device="cuda")
+    for out, x in ((got[0], q[0]), (k[table[0, t // S].long(), t % S], kn[0])):
+        u, w = f64(x)[..., one], f64(x)[..., two]
+        c, s = np.cos(exact)[:, None], np.sin(exact)[:, None]
+        tol = (np.abs(u) + np.abs(w)) * 2.0 ** -21.5
+        assert (np.abs(f64(out)[..., one] - (u * c - w * s)) <= tol).all()
+        assert (np.abs(f64(out)[..., two] - (w * c + u * s)) <= tol).all()
+
+
 def test_append_without_rotation_is_append(tree):
     from draft_verify_acceptance_gb300 import decode
     k, v, table, lengths = make_cache([40, 33], 16, 2, 128, torch.bfloat16, seed=1)

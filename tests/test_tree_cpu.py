@@ -356,3 +356,43 @@ def test_told_items_stay_until_every_warp_has_read_them():
             tiles = [1] * 20 if case == 0 else rng.randint(1, 2 + case % 5, 24).tolist()
             late, ends = told_items_read_too_late(tiles, dual, items, held)
             assert ends and late == [], (tiles, dual)
+
+
+def test_turns_of_high_frequencies_and_the_phase():
+    """tree_cache.cu's turns and the 32-bit phase that the sine takes, within 2^-31 of a turn for every finite frequency and
+    position, against the exact fraction."""
+    src = open(os.path.join(ROOT, "draft_verify_acceptance_gb300", "csrc", "tree_cache.cu")).read()
+    inv = int(re.search(r"kInv2Pi = (0x[0-9a-f]+)ull", src).group(1), 16)
+    words = re.search(r"kInv2PiWords\[7\] = \{[^\n]*\n([^}]*)\}", src)
+    words = [int(w, 16) for w in re.findall(r"0x([0-9a-f]+)u", words.group(1))] if words else None
+    low, full = (1 << 64) - 1, (1 << 32) - 1
+    if words:
+        assert len(words) == 7 and words[0] << 32 | words[1] == inv
+        bits = sum(w << 192 - 32 * i for i, w in enumerate(words))
+        assert abs(bits / 2 ** 224 - 1 / (2 * np.pi)) < 1e-16
+
+    def kernel(x):
+        u = int(np.float32(x).view(np.uint32))
+        e, m = (u >> 23) & 255, (u & 0x7fffff) | (0x800000 if (u >> 23) & 255 else 0)
+        shift = 150 - (e or 1)
+        if words and u & 0x7fffffff > 0x3f800000:
+            k = -shift
+            at, bit = (k >> 5, k & 31) if k > 0 else (0, 0)
+            w = [(words[at + i] << 32 | words[at + i + 1]) << bit >> 32 & full for i in range(3)]
+            first, rest = m * w[0], m * w[1] + (m * w[2] >> 32)
+            assert first <= low and rest <= low
+            lo = rest + (first << 32) & low
+            t = lo if k >= 0 else lo >> -k | ((first >> 32) + (lo < rest)) << 64 + k & low
+        else:
+            t = m * inv >> shift & low if shift >= 0 else (m * inv << -shift & low if shift > -64 else 0)
+        return -t & low if u >> 31 else t
+    rng = np.random.RandomState(1)
+    some = [1.0, np.nextafter(np.float32(1), np.float32(0)), np.nextafter(np.float32(1), np.float32(2)), 1.75, 2.5, -3.0, 1e4, 2.0 ** 23,
+            2.0 ** 24 - 1, 2.0 ** 24, 1e9, -1e20, 3.4028235e38, 500000.0 ** -0.3, 1e-40, 0.0]
+    some += (rng.uniform(1, 2, 300) * 2.0 ** rng.randint(-30, 127, 300)).tolist()
+    for x in some:
+        x = float(np.float32(x))
+        t = kernel(x)
+        for p in (1, 2, 131071, 2 ** 31 - 1, -2 ** 31, int(rng.randint(1, 2 ** 31 - 1))):
+            d = abs((p * t & low) >> 32) / 2 ** 32 - ref.turns(p, x)
+            assert min(abs(d), 1 - abs(d)) < 2.0 ** -31, (x, p, d)

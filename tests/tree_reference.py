@@ -50,6 +50,20 @@ def attention(q, k, v, table, lengths, parents, scale):
     return out, lse, mag, spread
 
 
+def turns(position, f):
+    """The fraction of a turn that position * f radians makes, exactly: for angles that a double loses."""
+    def arctan_inv(x):  # arctan(1 / x) * 2^400
+        term, total, n = (1 << 400) // x, 0, 1
+        while term:
+            total += term // n if n % 4 == 1 else -(term // n)
+            term //= x * x
+            n += 2
+        return total
+    one_turn = 8 * (4 * arctan_inv(5) - arctan_inv(239))  # 2 pi * 2^400 (Machin)
+    num, den = float(f).as_integer_ratio()
+    return ((position * num << 800) // (den * one_turn) % (1 << 400)) / (1 << 400)
+
+
 def rotate(x, position, inv_freq, interleaved):
     """Heads x [..., D] of one token, and the bound's ingredient |x| + |y| of each pair."""
     F = len(inv_freq)
