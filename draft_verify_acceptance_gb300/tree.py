@@ -87,8 +87,9 @@ def tree_attention(at, q, k_pages, v_pages, page_table, lengths, parents, scale=
     first), parents int32 [B, N] or [N].  Node i of a sequence of n tokens is its token n - N + i
     and sees the tokens before n - N, its ancestors and itself; query head h reads cache head
     h * heads // Hq.  ``scale`` defaults to 1 / sqrt(D).  Returns out [B, N, Hq, D], with
-    ``return_lse`` (out, lse float32 [B, N, Hq]); no node gets 0 and -inf.  ``out`` may give a
-    preallocated tensor that does not overlap q.
+    ``return_lse`` (out, lse float32 [B, N, Hq]); no node gets 0 and -inf.  What a node sees that is
+    not finite makes its result not finite (infinite or NaN); what it does not see never reaches it.
+    ``out`` may give a preallocated tensor that does not overlap q.
     """
     index, stream = at
     shape, st = q.shape, q.stride()

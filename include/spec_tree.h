@@ -52,7 +52,9 @@ extern "C" {
  *            rows; 7.6 and 3.9 MB else, whatever the batch.)
  *
  * Arithmetic as spec_paged_attention's; the result does not depend on the
- * schedule's timing.
+ * schedule's timing.  As there, a value that is not finite in a token that a node
+ * sees makes what it reaches not finite: whether infinite or NaN depends on the
+ * sizes and on where the token lies, and is not promised.
  */
 #define SPEC_TREE_ATTENTION_ZERO_BYTES 2048
 SPEC_API size_t spec_tree_attention_workspace_size(int B, int N, int Hq, int heads, int head_dim, int dtype);

@@ -210,6 +210,93 @@ def test_a_bad_context_value_reaches_every_node(tree, dtype, N, G):
     assert (out[0, -1] == 0).all()
 
 
+@pytest.mark.parametrize("dtype,N,G,D", [
+    (torch.bfloat16, 9, 4, 128), (torch.bfloat16, 30, 4, 64), (torch.bfloat16, 16, 8, 128),  # one row tile
+    (torch.bfloat16, 40, 4, 128), (torch.bfloat16, 64, 4, 64), (torch.bfloat16, 33, 8, 64),  # two, the last of eight rows of 264
+    (torch.bfloat16, 6, 4, 128), (torch.bfloat16, 11, 2, 64),                                # up to 24 rows
+    (torch.float32, 5, 4, 128), (torch.float32, 13, 4, 64), (torch.float32, 30, 2, 128)])
+def test_values_that_are_not_finite_in_a_cut_item(tree, dtype, N, G, D):
+    """One long sequence, cut over many blocks (more tiles than any kernel leaves whole; the lengths move the cuts and the
+    tree over them).  NaN queries and keys make the rows that see them NaN, values that are not finite make their
+    dimension not finite, wherever among the parts they lie; all else keeps its bits."""
+    S, H = 16, 2
+    p = make_trees(1, N, N, "random")
+    p[0, N - 1] = -2  # one that is none
+    up = [set(ref.line(p[0], i) or ()) for i in range(N)]
+    parents = i32(p.tolist())
+    for tiles in range(18, 30):
+        n = 64 * tiles + (1, N // 2, 63)[tiles % 3]
+        k, v, table, lengths = make_cache([n], S, H, D, dtype, seed=tiles)
+        q = torch.randn((1, N, H * G, D), generator=gen(1), device="cuda").to(dtype)
+        call = lambda q, k, v: tree.tree_attention(q, k, v, table, lengths, parents, return_lse=True)  # noqa: E731
+        clean, lse = call(q, k, v)
+        assert torch.isfinite(clean).all() and torch.isfinite(lse[0, :-1]).all()
+        q2 = q.clone()
+        q2[0, N - 2, G + 1, 3] = math.nan  # of cache head 1
+        out, l2 = call(q2, k, v)
+        assert torch.isnan(out[0, N - 2, G + 1]).all() and torch.isnan(l2[0, N - 2, G + 1])
+        out[0, N - 2, G + 1], l2[0, N - 2, G + 1] = clean[0, N - 2, G + 1], lse[0, N - 2, G + 1]
+        assert torch.equal(out, clean) and torch.equal(l2, lse)
+        spots = [0, 700 + 13 * tiles, n - N - 1] + [n - N + i for i in sorted({0, 1, N // 2, N - 2, N - 1})]
+        for j, t in enumerate(spots):
+            node = t - (n - N)
+            sees = [i for i in range(N - 1) if node < 0 or node in up[i]]
+            place = (table[0, t // S].long(), t % S, 1)
+            h = slice(G, 2 * G)
+
+            def others(out, l2, d=slice(None), with_lse=True):  # put back, all is as it was
+                out, l2 = out.clone(), l2.clone()
+                for i in sees:
+                    out[0, i, h, d] = clean[0, i, h, d]
+                    l2[0, i, h] = lse[0, i, h] if with_lse else l2[0, i, h]
+                assert torch.equal(out, clean) and torch.equal(l2, lse), (n, t, j)
+            k2 = k.clone()
+            k2[(*place, 7)] = math.nan
+            out, l2 = call(q, k2, v)
+            assert all(torch.isnan(out[0, i, h]).all() and torch.isnan(l2[0, i, h]).all() for i in sees), (n, t)
+            others(out, l2)
+            k2[(*place, 7)] = math.inf  # scores of +inf (NaN) or -inf (a weight of 0), by the query's sign
+            out, l2 = call(q, k2, v)
+            for i in sees:
+                over = q[0, i, h, 7] > 0
+                assert torch.isnan(out[0, i, h][over]).all() and torch.isnan(l2[0, i, h][over]).all(), (n, t, i)
+                if dtype == torch.bfloat16:  # (fp32 operands are two parts, infinity's second one NaN: all of these rows are)
+                    assert torch.isfinite(out[0, i, h][~over]).all() and torch.isfinite(l2[0, i, h][~over]).all(), (n, t, i)
+                    assert (l2[0, i, h][~over] <= lse[0, i, h][~over] + 1e-5).all()
+            others(out, l2)
+            for bad in (math.nan, math.inf, -math.inf):
+                v2 = v.clone()
+                v2[(*place, D - 3)] = bad
+                out, l2 = call(q, k, v2)
+                assert all((~torch.isfinite(out[0, i, h, D - 3])).all() for i in sees), (n, t, bad)
+                others(out, l2, D - 3, False)
+
+
+@pytest.mark.parametrize("dtype", BOTH)
+@pytest.mark.parametrize("N,G,H,D,lens", [
+    (9, 4, 2, 128, [512, 9, 100]), (30, 4, 8, 64, [30, 511, 65, 0, 300, 128] * 3), (16, 8, 1, 128, [5, 449]),
+    (40, 4, 2, 128, [512, 40, 104]), (60, 4, 8, 128, [60, 512, 333, 7, 190] * 3), (33, 8, 2, 64, [33, 97, 512]),
+    (5, 4, 2, 64, [5, 512, 77]), (13, 4, 2, 64, [13, 190, 100, 50])])
+def test_short_sequences_under_a_table_with_room_for_long_ones(tree, dtype, N, G, H, D, lens):
+    """A server's table has room for its longest context: that no item is cut is then known from the lengths alone.  The results
+    are those of a table that has no more room than these sequences need (bf16: bit for bit)."""
+    k, v, tight, lengths = make_cache(lens, 16, H, D, dtype, seed=N, extra_cols=0)
+    q = torch.randn((len(lens), N, H * G, D), generator=gen(5), device="cuda").to(dtype)
+    parents = i32(make_trees(len(lens), N, N).tolist())
+    want, wl = tree.tree_attention(q, k, v, tight, lengths, parents, return_lse=True)
+    check_attention(want, wl, q, k, v, tight, lengths, parents)
+    roomy = torch.full((len(lens), 4096 // 16), -1, dtype=torch.int32, device="cuda")
+    roomy[:, :tight.shape[1]] = tight
+    out, lse, status = tree.tree_attention(q, k, v, roomy, lengths, parents, return_lse=True, debug=True)
+    assert int(status) == 0
+    check_attention(out, lse, q, k, v, roomy, lengths, parents)
+    if dtype == torch.bfloat16:
+        assert torch.equal(out, want) and torch.equal(lse, wl)
+    for _ in range(3):
+        again, l2 = tree.tree_attention(q, k, v, roomy, lengths, parents, return_lse=True)
+        assert torch.equal(again, out) and torch.equal(l2, lse)
+
+
 @pytest.mark.parametrize("dtype", BOTH)
 @pytest.mark.parametrize("N", [4, 40])
 def test_large_scores_and_far_maxima(tree, dtype, N):
