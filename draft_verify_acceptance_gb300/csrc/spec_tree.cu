@@ -179,6 +179,19 @@ spec_status_t spec_tree_accept(const int32_t* tokens, const int32_t* parents, in
   if (N > 0 && (!want32(tokens) || !parents_ok(parents, parents_stride, N) || !want32(drawn) || !want32(out_tokens) ||
                 !want32(path)))
     return SPEC_ERR_INVALID_ARG;
+  if (N > 0) {
+    // A warp reads its tree whole before it writes: results may take the place of rows that it alone reads.
+    const int64_t rows = static_cast<int64_t>(B) * N * 4, shared = ((B - 1) * parents_stride + N) * 4;
+    const bool own = parents_stride == N || B == 1;  // no row of parents is another tree's too
+    auto clash = [&](const void* in, int64_t bytes, bool same) {
+      return overlap(in, bytes, accepted_len, 4ll * B) || (!(same && in == out_tokens) && overlap(in, bytes, out_tokens, rows)) ||
+             (!(same && in == path) && overlap(in, bytes, path, rows));
+    };
+    if (clash(tokens, rows, true) || clash(drawn, rows, true) || clash(parents, shared, own) ||
+        overlap(out_tokens, rows, path, rows) || overlap(out_tokens, rows, accepted_len, 4ll * B) ||
+        overlap(path, rows, accepted_len, 4ll * B))
+      return SPEC_ERR_INVALID_ARG;
+  }
   AcceptArgs a;
   a.tokens = tokens;
   a.parents = parents;
@@ -206,7 +219,8 @@ spec_status_t spec_cache_keep(const spec_cache_t* cache, const int32_t* page_tab
   if (N > (1 << 20) || B * keep_blocks(a.cache) > (1ll << 31) - 1) return SPEC_ERR_UNSUPPORTED;
   if (B == 0) return SPEC_OK;
   if (!want32(lengths) || !want32(new_lengths) || !may32(device_status) || (N > 0 && !want32(path)) ||
-      overlap(lengths, 4ll * B, new_lengths, 4ll * B))
+      overlap(lengths, 4ll * B, new_lengths, 4ll * B) || (N > 0 && overlap(path, 4ll * B * N, new_lengths, 4ll * B)) ||
+      (max_pages > 0 && overlap(page_table, 4 * ((B - 1) * table_stride + max_pages), new_lengths, 4ll * B)))
     return SPEC_ERR_INVALID_ARG;
   a.lengths = lengths;
   a.path = path;

@@ -110,6 +110,8 @@ SPEC_API spec_status_t spec_cache_append_rotated(
  *   out_tokens [B, N]: the tokens drawn after them (accepted_len accepted ones and
  *            the one that ends the walk), then -1.
  *   Where node 0 is no root: accepted_len -1 and nothing but -1.
+ *   The outputs overlap nothing, but path and out_tokens may each be one of the
+ *   inputs itself (not parents that trees share).
  * With tokens drawn from the target's distribution at each node, what is emitted
  * follows that distribution whatever the tree holds.
  */
@@ -125,8 +127,8 @@ SPEC_API spec_status_t spec_tree_accept(const int32_t* tokens, const int32_t* pa
  *   path     [B, N] int32: ascending indexes below N, ended by -1 (spec_tree_accept's).
  *            An entry that does not ascend, or is not below N, is
  *            SPEC_DATA_PATH_RANGE and ends the path.
- *   new_lengths [B] = lengths - N + entries (not below 0); not lengths itself.  A
- *            path in a sequence of fewer than N tokens is SPEC_DATA_LENGTH_RANGE:
+ *   new_lengths [B] = lengths - N + entries (not below 0); overlaps neither lengths,
+ *            path nor page_table.  A path in a sequence of fewer than N tokens is SPEC_DATA_LENGTH_RANGE:
  *            the sequence stays as it is.
  * The pages that hold the newest N tokens must be the sequence's own (those that
  * spec_cache_fork reserves are).  A token whose page, or the page it goes to,

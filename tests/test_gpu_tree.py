@@ -657,6 +657,23 @@ def test_accept_one_tree_for_all_and_bad_parents(tree):
     assert int(got.status) == tree.DATA_TREE_PARENT and got.path.tolist() == [[0, 3, 4, -1, -1]]
 
 
+def test_accept_in_place(tree):
+    """Through the C entry point: path and out_tokens written over the rows that they are made from."""
+    B, N = 37, 64
+    r = np.random.RandomState(2)
+    host = [r.randint(0, 4, (B, N)), make_trees(B, N, 3), r.randint(0, 4, (B, N))]
+    n, out, path = ref.accept(*host)
+    for over in ((0, 1), (1, 0), (2, 1), (1, 2), (0, 2), (2, 0), (2, None), (None, 2)):
+        ins = [i32(x.tolist()) for x in host]
+        got_n, fresh = i32([7] * B), [i32(x.tolist()) for x in host]
+        to = [ins[o] if o is not None else fresh[i] for i, o in enumerate(over)]
+        rc = tree._lib.spec_tree_accept(ins[0].data_ptr(), ins[1].data_ptr(), N, ins[2].data_ptr(), B, N, got_n.data_ptr(),
+                                        to[0].data_ptr(), to[1].data_ptr(), torch.cuda.current_stream().cuda_stream, None)
+        assert rc == 0
+        assert np.array_equal(got_n.cpu().numpy(), n)
+        assert np.array_equal(to[0].cpu().numpy(), out) and np.array_equal(to[1].cpu().numpy(), path), over
+
+
 @pytest.mark.parametrize("dtype", BOTH)
 @pytest.mark.parametrize("N,S,L,H,D,lens", [
     (1, 16, 1, 1, 64, [1, 5]), (5, 1, 2, 2, 64, [5, 9, 0]), (13, 16, 3, 2, 64, [13, 40, 100]), (64, 8, 2, 8, 128, [64, 200, 77]),

@@ -396,3 +396,23 @@ def test_turns_of_high_frequencies_and_the_phase():
         for p in (1, 2, 131071, 2 ** 31 - 1, -2 ** 31, int(rng.randint(1, 2 ** 31 - 1))):
             d = abs((p * t & low) >> 32) / 2 ** 32 - ref.turns(p, x)
             assert min(abs(d), 1 - abs(d)) < 2.0 ** -31, (x, p, d)
+
+
+def test_accept_and_keep_refuse_outputs_over_what_others_read(tree):
+    """Results over memory that another tree's warp, or another block, may still read."""
+    lib, c, B, N = tree._lib, cache(tree), 4, 8
+    far = [FAKE + (i << 12) for i in range(6)]
+
+    def accept(tok=far[0], par=far[1], ps=N, drawn=far[2], n=far[3], out=far[4], path=far[5]):
+        return lib.spec_tree_accept(tok, par, ps, drawn, B, N, n, out, path, None, None)
+    row = 4 * N
+    for bad in (dict(n=far[0]), dict(n=far[0] + B * row - 4), dict(n=far[1] + 16), dict(n=far[2] - 4), dict(n=far[4]), dict(n=far[5] + 4),
+                dict(path=far[4]), dict(path=far[4] + row), dict(out=far[0] + row), dict(out=far[2] - row), dict(path=far[1] + 4),
+                dict(path=far[1], ps=0), dict(out=far[1], ps=0), dict(path=far[1], ps=N + 2), dict(out=far[1] + row, ps=N)):
+        assert accept(**bad) == 1, bad
+
+    def keep(lens=far[0], table=far[1], path=far[2], new=far[3], ts=4):
+        return lib.spec_cache_keep(ctypes.byref(c), table, ts, 4, lens, B, path, N, new, None, None)
+    for bad in (dict(new=far[0]), dict(new=far[2]), dict(new=far[2] + B * row - 4), dict(new=far[2] - 12), dict(new=far[1]),
+                dict(new=far[1] + 60), dict(new=far[1] + 12, ts=0), dict(new=far[1] + 72, ts=5)):
+        assert keep(**bad) == 1, bad
