@@ -105,7 +105,10 @@ struct Item {
   int b, h, n, rt, row0, rows, tile0, tile1, tiles;
   __device__ __forceinline__ bool whole() const { return tile0 == 0 && tile1 == tiles; }
 };
-constexpr int kItems = 8;  // kept: the softmax warps' own, kHeld - 1 before it, the rest told ahead
+// Kept: the softmax warps' own, kHeld - 1 before it, the rest told ahead, of one tile each as
+// many as the ring and the loaders' look-ups are ahead (400 trees of 7 nodes over
+// 10..60 tokens, heads of 64: 16 83 us, 8 89; others the same).
+constexpr int kItems = 16;
 constexpr int kHeld = 2;   // items that the softmax warps start before the first of them is given up
 
 // What the host divides for the kernel (32-bit divisions take some 140 cycles, 64-bit ones 500).

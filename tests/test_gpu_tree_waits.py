@@ -51,10 +51,10 @@ def test_attention_ends_after_a_wait_that_ran_out(N, G, D):
         assert status == 0 and torch.equal(out, want)
 
 
-@pytest.mark.parametrize("B,N,Hq,H,D,most", [(400, 7, 32, 8, 64, 60), (300, 9, 32, 8, 128, 60), (300, 7, 32, 8, 64, 190),
-                                              (350, 40, 16, 4, 64, 60), (200, 60, 32, 8, 128, 190)])
+@pytest.mark.parametrize("B,N,Hq,H,D,most", [(400, 7, 32, 8, 64, 60), (600, 9, 32, 8, 128, 60), (500, 7, 32, 8, 64, 190),
+                                              (800, 40, 16, 4, 64, 60), (500, 60, 32, 8, 128, 190)])
 def test_warps_that_start_late_miss_nothing(B, N, Hq, H, D, most):
-    """Many short items a block, most of one tile, and the warps that copy the second item's queries and the odd tiles a
+    """Twenty and more short items a block (more than are kept), most of one tile, and the warps that copy the second item's queries and the odd tiles a
     millisecond behind: what they have not read yet is still there."""
     if not torch.cuda.is_available():
         pytest.skip("no CUDA device")
