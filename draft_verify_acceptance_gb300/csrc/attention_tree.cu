@@ -13,12 +13,18 @@ namespace specv {
 // bf16 items of more than 24 rows a cache head (R = N * Hq / Hkv) go to
 // attention_tree_tc.cuh, the rest to attention_mma.cuh, in tiles of at most 24 rows
 // that each read K and V again (through L2), and scales that are not above zero.
-// Measured, mma and tc, 32 query heads on 8, heads of 128:  64 sequences of 400..4000
-// tokens, R = 24: 113 and 117 us, R = 32: 181 and 118;  64 of 200..400, R = 32: 55 and 44;
-// 8 of 1000, R = 52: 33 and 27;  one of 500, R = 120: 20 and 18, R = 240: 21 and 23;  one
-// of 20000, R = 52: 58 and 41.  Heads of 64:  32 of 400..4000, R = 48: 86 and 58;  64 of
-// 100..190, two query heads on each, R = 26: 19 and 21.  (tc has since won 2 to 4 us at the small
-// ones, 10 at the large.)
+// Both measured on one machine (mma, tc in us; 32 query heads on 8, heads of 128 where not said):
+//                                           R = 8      16         24         32 and more
+//   64 sequences of 400..4000 tokens        102, 106   107, 106   112, 107   32: 181, 110   64: 288, 112
+//   64 of 200..400                           29, 39     36, 39     42, 39    32: 55, 39
+//   8 of 1000                                17, 22     23, 22     31, 22    52: 33, 23
+//   one of 500                               12, 16     16, 16     19, 16    120: 20, 17   240: 21, 25
+//   one of 20000                             33, 35     43, 35     46, 35    52: 58, 36
+//   32 of 400..4000, heads of 64             44, 53     47, 53     52, 54    48: 86, 55
+//   64 of 100..190, 16 heads of 64 on 8      16, 27     19, 28     21, 28    26: 31, 28
+// So 24, a row tile of mma's, is right for heads of 64.  For heads of 128 tc is ahead
+// from 17 to 20 rows on, by 5 % for large batches and by 10 to 30 % for small ones, which this
+// rule does not take; and behind at 240 rows of one short sequence.
 namespace {
 bool on_tc(int rows, bool bf16) { return bf16 && rows > mma::kMmaRows; }
 }  // namespace

@@ -27,13 +27,15 @@
 // The code is kept short: with loops unrolled to 200 KB the roles evicted each
 // other from the instruction caches, and a tile took 4000 cycles.
 //
-// 32 query heads of 128 on 8:  64 sequences of 400..4000 tokens, 16 nodes (64 rows a
-// head) 108 us (the cache's bytes at the copy rate: 87; a block's tile 1300 cycles, an
-// item's start and end 5 us of a block's time, part of it hidden behind the ring);  2 of
-// 60001..131072, 26 nodes: 155 us (139);  32 of 400..4000, 64 nodes (256 rows): 109 us (45), a
-// tile 2300 cycles of products, the scores' as long as the outputs' since each reads
-// 4 KB of queries for 64 tokens;  one of 2111, 60 nodes: 25 us, start, part and join.
-// 32 of 400..4000 over heads of 64, 30 nodes: 56 us (23), by the softmax's latency.
+// 32 query heads of 128 on 8 (ranges are over machines and lengths):  64 sequences of
+// 400..4000 tokens, 16 nodes (64 rows a head) 108 to 117 us (the cache's bytes at the copy
+// rate: 87; a block's tile 1300 cycles, an item's start and end 5 us of a block's time, part of it
+// hidden behind the ring);  2 of 60001..131072, 26 nodes: 153 to 187 us (124 to 148);  32 of
+// 400..4000, 64 nodes (256 rows): 102 to 113 us (45), a tile 2300 cycles of products, the
+// scores' as long as the outputs' since each reads 4 KB of queries for 64 tokens;  the same
+// with 33 nodes (132 rows) 103 and with 65 (260 rows: two items, the second nearly empty) 189;  one
+// of 2111, 60 nodes: 25 us, start, part and join.  32 of 400..4000 over heads of 64, 30 nodes:
+// 56 us (23), by the softmax's latency.
 #pragma once
 
 #include "attention_common.cuh"

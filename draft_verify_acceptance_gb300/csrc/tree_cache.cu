@@ -123,7 +123,7 @@ __device__ __forceinline__ uint4 ld_once(const uint4* p) { return __ldcs(p); }
 // a piece behind the rotated dimensions; its values are pieces.  `parts` warps share
 // a token.  A warp's first units and pieces are under way while it finds the
 // token's place and turns its angles, which every part does for itself.  HBM bounds
-// many tokens (53141 tokens of 12 prompts, 32 + 8 heads of 128, bf16: 202 us, 97 % of the
+// many tokens (53141 tokens of 12 prompts, 32 + 8 heads of 128, bf16: 201 us, 97 % of the
 // copy rate; one unit at a time it was 219), the dependent look-ups few (64 trees of
 // 16: 8.4 us, 25 MB).
 template <typename E, bool kInterleaved>
@@ -272,7 +272,7 @@ rotated_append_kernel(const RotatedAppendArgs a, int parts, DivU64 by_part, Div3
 // ---- accept --------------------------------------------------------------------
 // One warp a tree, a lane holding nodes lane, lane + 32, ...: a step compares all
 // of them with (node, drawn token) and takes the lowest match.  A launch bounds it:
-// 512 trees of 64 nodes 6 to 7 us, four trees the same.
+// 512 trees of 64 nodes 6 to 8 us, four trees the same.
 constexpr int kAcceptWarps = 4;
 __global__ void __launch_bounds__(kAcceptWarps * 32) tree_accept_kernel(const AcceptArgs a) {
   __shared__ int32_t s_drawn[kAcceptWarps][kMaxNodes], s_path[kAcceptWarps][kMaxNodes];
@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(kAcceptWarps * 32) tree_accept_kernel(const Ac
 // and makes the path's moves in order, eight loads under way: a token comes from
 // its own index or a later one, so no load of a batch, or of a later one, reads
 // what a store of it has written.  64 trees of 64 nodes in 16 layers, 8 heads of 128,
-// bf16, 6 nodes moved a tree: 14.5 to 15.7 us (their bytes at the copy rate 11.3).
+// bf16, 6 nodes moved a tree: 14.1 to 15.7 us (their bytes at the copy rate 11.3).
 constexpr int kKeepThreads = 128, kKeepMoves = 128;
 __global__ void __launch_bounds__(kKeepThreads) keep_kernel(const KeepArgs a, unsigned chunks) {
   __shared__ long long s_from[kKeepMoves], s_to[kKeepMoves];
