@@ -272,7 +272,7 @@ rotated_append_kernel(const RotatedAppendArgs a, int parts, DivU64 by_part, Div3
 // ---- accept --------------------------------------------------------------------
 // One warp a tree, a lane holding nodes lane, lane + 32, ...: a step compares all
 // of them with (node, drawn token) and takes the lowest match.  A launch bounds it:
-// 512 trees of 64 nodes 6 to 8 us, four trees the same.
+// 512 trees of 64 nodes 6 to 9 us by the host, four trees the same.
 constexpr int kAcceptWarps = 4;
 __global__ void __launch_bounds__(kAcceptWarps * 32) tree_accept_kernel(const AcceptArgs a) {
   __shared__ int32_t s_drawn[kAcceptWarps][kMaxNodes], s_path[kAcceptWarps][kMaxNodes];
